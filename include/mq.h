@@ -55,7 +55,9 @@ enum {
     MQ_ERR_ARCH = 4,    /* the current device is not a compute capability 10.3 (GB300) GPU */
     MQ_ERR_LAUNCH = 5,  /* the CUDA launch (or tensor-map encoding) failed */
     MQ_ERR_DEVICE = 6,  /* a kernel gave up on a bounded wait (reported by mq_device_status) */
-    MQ_ERR_SCRATCH = 7  /* mq_gemm_q6k_static: the call needs more than its fixed scratch array holds */
+    MQ_ERR_SCRATCH = 7, /* mq_gemm_q6k_static: the call needs more than its fixed scratch array holds;
+                           mq_attn_prefix: ws_bytes is less than mq_attn_ws_bytes gives */
+    MQ_ERR_TYPE = 8     /* an element type that the call does not take */
 };
 
 /* Most activation rows one mq_gemv_q4k / mq_gemv_q6k call takes. */
@@ -323,6 +325,131 @@ size_t mq_q4_1_row_bytes(int K);
 int mq_gemv_q5k(const mq_q8_plane* a, const void* w, int N, float* out, cudaStream_t stream);
 int mq_gemv_q4_0(const mq_q8_plane* a, const void* w, int N, float* out, cudaStream_t stream);
 int mq_gemv_q4_1(const mq_q8_plane* a, const void* w, int N, float* out, cudaStream_t stream);
+
+/*
+ * Between the attn_q|k|v products and attn_o: heads, caches and attention
+ * ------------------------------------------------------------------------
+ * The calls below share these conventions, beside those at the top of this file:
+ *  - Hq query heads share Hkv key/value heads in groups of G = Hq / Hkv (query head h
+ *    reads key head h / G); D is the width of a head.
+ *  - Strides are counted in elements. Element types: see the enum.
+ *  - An array that a call reads may be the output of work enqueued before it on `stream`.
+ */
+enum { MQ_F16 = 0, MQ_BF16 = 1, MQ_F32 = 2 };
+
+/* Keys and values of n sequences, `cap` rows each, in 16 bits (MQ_F16 or MQ_BF16): key
+ * head h of row j of sequence i is the `dim` elements at
+ *     k + i * seq_stride + j * row_stride + h * head_stride,
+ * the value the same place of v. So [n][cap][heads][dim] and [n][heads][cap][dim] are
+ * both a matter of strides. dim must be a multiple of 8, at most 256; the strides multiples
+ * of 8 that keep all rows apart (MQ_ERR_SHAPE otherwise); k and v 16-byte aligned. The
+ * struct lives in host memory. A row's place may pass 2^31 elements. */
+typedef struct mq_kv {
+    void* k;
+    void* v;
+    long long seq_stride;
+    long long row_stride;
+    long long head_stride;
+    int type;
+    int n;
+    int cap;
+    int heads;
+    int dim;
+} mq_kv;
+
+/* Projections of M tokens in f32, as the GEMMs and GEMVs leave them, and how their heads
+ * are normed and rotated. Head h of token m starts at q + m * q_stride + h * D (k and v
+ * alike; strides multiples of 4, pointers 16-byte aligned). A NULL q, k or v is left out. */
+typedef struct mq_qkv {
+    const float* q;
+    const float* k;
+    const float* v;
+    long long q_stride;
+    long long k_stride;
+    long long v_stride;
+    const float* wq;         /* [D] norm weights of the query heads; NULL: no norm */
+    const float* wk;         /* [D] of the key heads; NULL: no norm */
+    const float* inv_freq;   /* [n_pairs] radians per position */
+    const uint8_t* axis;     /* [n_pairs] the axis whose position turns the pair (values past the
+                                last axis count as the last); NULL: axis 0 for all */
+    const int32_t* pos;      /* [n_axes][M] positions (any int32) */
+    int M;
+    int Hq;
+    int n_pairs;             /* rotated pairs, 0 .. D/2; dims past 2 n_pairs are not rotated */
+    int n_axes;              /* 1 .. 8 where n_pairs > 0 */
+    int interleaved;         /* pairs (2i, 2i+1) instead of (i, i + n_pairs) */
+    float eps;
+} mq_qkv;
+
+/*
+ * mq_qk_norm_rope — per-head RMS norm of queries and keys, their rotation by position, and
+ * the write of keys and values into a cache, in one pass. For each head x of q (of k):
+ *     y = x * w / sqrt(mean(x^2) + eps)       (w NULL: y = x)
+ *     t = pos[axis[i]][m] * inv_freq[i]
+ *     (a, b) = (y[i], y[i + n_pairs])         (interleaved: (y[2i], y[2i + 1]))
+ *     a' = a cos t - b sin t,  b' = a sin t + b cos t
+ * rounded once to the cache's type. Sums and products are f32; t is reduced to one turn in
+ * 64 bits, so large positions lose nothing. Values are only rounded.
+ * q_out: [M][Hq][D]. Key and value of token m go to row slot[m] of the cache, counted over
+ * all its sequences (sequence slot / cap, row slot % cap); slot NULL: row m. A slot outside
+ * [0, n * cap) is skipped (padding tokens). Two tokens must not have the same slot. The
+ * cache's type, heads and dim say what is written; its k and v may be NULL where the input's
+ * are. MQ_ERR_SHAPE: M < 0, n_pairs outside 0 .. D/2, n_axes outside 1 .. 8 (with pairs), strides
+ * below the row's width or not a multiple of 4, M > n * cap with slot NULL. M == 0 is a no-op.
+ * A programmatic dependent launch, as the producers; wq and wk are read through the read-only path.
+ */
+int mq_qk_norm_rope(const mq_qkv* x, void* q_out, const mq_kv* cache, const int32_t* slot, cudaStream_t stream);
+
+/*
+ * mq_attn_prefix — attention of B sequences, T new queries each, over a prefix that all of
+ * them share and over each one's own cache:
+ *     out[b][t][h] = sum_j p_j v_j,   p = softmax_j(scale * q[b][t][h] . k_j)
+ * with j over every row of the prefix, then the rows j < own_len[b] - T + 1 + t of sequence b of `own`: the
+ * last T of its own_len[b] rows belong to the T queries themselves, each of which sees the
+ * keys up to its own. The prefix's keys and values are read once for the whole batch.
+ *   q       : [B * T][Hq][D] in the caches' type, row stride q_stride (a multiple of 8, at least Hq * D).
+ *   prefix  : one sequence (n == 1) whose rows 0 .. cap-1 are all seen; NULL or cap == 0: none.
+ *   own     : n == B sequences; NULL: none (own_len is then not read). own_len: int32 [B] on
+ *             the device, taken as 0 below 0 and as cap above cap. Rows at or past own_len
+ *             are never used, whatever they hold (infinities and NaN included).
+ *   out     : [B * T][Hq][D] in the caches' type or MQ_F32 (out_type).
+ *   lse     : f32 [B * T][Hq], log of the sum of exp(scale * q . k_j), or NULL.
+ *   score, score_out : f32 [B][Hkv][own->cap], both or neither (they may be the same array):
+ *             score_out[b][g][j] = score[b][g][j] + the weights p_j of own row j, summed over the
+ *             T queries and the group's heads, for j < own_len[b]; other entries are not touched.
+ * A query that sees no key gives zeros and an lse of -infinity.
+ * Rows that a query sees must be finite for that query's result to be; with T > 1 a value row that holds
+ * infinities or NaN also reaches the queries of its sequence that come before it.
+ * Arithmetic: products in f32 from 16-bit operands, softmax in f32, probabilities rounded to
+ * the caches' type for the product with the values (2^-12 or 2^-9 relative, as the output's own
+ * rounding is), sums in f32. An MQ_F32 output carries that rounding. Deterministic.
+ * D: 64, 96, 128 or 256; Hq a multiple of Hkv. scale must be finite. ws: caller-owned device
+ * memory of at least mq_attn_ws_bytes(...) bytes, 16-byte aligned, nothing kept in it between
+ * calls; calls that run at the same time need one each. B == 0 or T == 0 is a no-op.
+ */
+size_t mq_attn_ws_bytes(int B, int T, int Hq, int Hkv, int D, int prefix_cap, int own_cap, int scores);
+int mq_attn_prefix(const void* q, long long q_stride, int B, int T, int Hq, const mq_kv* prefix, const mq_kv* own,
+                   const int32_t* own_len, float scale, void* out, int out_type, float* lse, const float* score,
+                   float* score_out, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * mq_kv_evict — drops the least attended rows of each sequence's cache, per key head. With
+ * L = len[b] (clamped to 0 .. src->cap): L <= keep keeps all; else the last `recent` rows
+ * stay and, of the others, the keep - recent with the largest score (ties: the lower row; NaN is
+ * the lowest of all), in their order:
+ *     index[b][h][j] = the row of src that is now row j of head h (-1 past the kept ones),
+ *     dst k, v row j = src k, v row index[b][h][j],  score_out[b][h][j] = score[b][h][index]
+ *     (0 past the kept ones), len_out[b] = min(L, keep).
+ *   score: f32 [n][heads][src->cap]; score_out: f32 [n][heads][dst->cap] (NULL: not written);
+ *   index: int32 [n][heads][dst->cap] (required); len, len_out: int32 [n].
+ *   dst: same n, heads, dim and type as src, dst->cap >= keep. Either apart from src or
+ *   exactly src (same k, v, strides and cap: the rows move down in place); k or v ranges that
+ *   overlap otherwise give MQ_ERR_SHAPE, as does score_out overlapping score unless it is score and
+ *   the caps are equal. len_out may be len. Rows of dst past the kept ones are not written.
+ * 0 <= recent <= keep, else MQ_ERR_SHAPE. n == 0 is a no-op.
+ */
+int mq_kv_evict(const mq_kv* src, const int32_t* len, const float* score, int keep, int recent, const mq_kv* dst,
+                int32_t* len_out, float* score_out, int32_t* index, cudaStream_t stream);
 
 /*
  * mq_device_status — synchronizes `stream`, then returns MQ_OK if no kernel of

@@ -1,0 +1,27 @@
+// Attention pieces (attn.cuh) for few query rows per key head: a decode step's heads, a few drafted
+// tokens. See attn_few.cu.
+#pragma once
+
+#include "attn.cuh"
+
+namespace attn {
+
+struct FewArgs {
+    Plan plan;
+    const void* q;
+    long long q_stride;
+    const void *pk, *pv, *ok, *ov;                  // prefix and own keys and values
+    long long p_row, p_head, o_seq, o_row, o_head;  // their strides
+    const int32_t* len;
+    float scale_log2;                               // scale * log2 e
+    Pieces out;
+    float* raw;       // [B][Hkv][T group][cap] scaled products of the own keys (base 2), or nullptr
+};
+
+constexpr int kFewRows = 16;      // query rows per segment
+int few_tile_keys(int D);         // keys per tile
+// Blocks that the device holds at once, for a head width of D.
+int few_blocks(int D, int type);
+int launch_few(const FewArgs& a, int D, int type, cudaStream_t stream);
+
+}  // namespace attn

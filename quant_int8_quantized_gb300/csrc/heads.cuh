@@ -1,0 +1,68 @@
+// What the kernels between attn_q|k|v and attn_o share: cache descriptors and 16-bit types.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "mq_internal.cuh"
+
+namespace mq {
+
+// All rows of a cache apart, strides multiples of 8: of the axes that have more than one
+// step, the one with the least stride must clear a head, each further one all that the ones
+// before it span.
+inline bool kv_apart(const mq_kv* c) {
+    long long st[3] = {c->seq_stride, c->row_stride, c->head_stride};
+    long long n[3] = {c->n, c->cap, c->heads};
+    for (int i = 0; i < 3; ++i)
+        if (st[i] < 0 || st[i] % 8 != 0 || st[i] > (1LL << 40)) return false;
+    for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < 2; ++j)
+            if (st[j] > st[j + 1]) {
+                const long long a = st[j], b = n[j];
+                st[j] = st[j + 1];
+                n[j] = n[j + 1];
+                st[j + 1] = a;
+                n[j + 1] = b;
+            }
+    long long span = c->dim;
+    for (int i = 0; i < 3; ++i)
+        if (n[i] > 1) {
+            if (st[i] < span) return false;
+            span = st[i] * (n[i] - 1) + span;
+        }
+    return true;
+}
+
+// Elements from the first to one past the last of k (or v).
+inline long long kv_span(const mq_kv* c) {
+    return c->seq_stride * (c->n - 1) + c->row_stride * (c->cap - 1) + c->head_stride * (c->heads - 1) + c->dim;
+}
+
+inline int check_kv(const mq_kv* c, bool pointers) {
+    if (!c) return MQ_ERR_NULL;
+    if (c->type != MQ_F16 && c->type != MQ_BF16) return MQ_ERR_TYPE;
+    if (c->n < 0 || c->cap < 0 || c->heads < 1 || c->dim < 8 || c->dim % 8 != 0 || c->dim > 256) return MQ_ERR_SHAPE;
+    if (!kv_apart(c)) return MQ_ERR_SHAPE;
+    if (pointers && c->n > 0 && c->cap > 0) {
+        if (!c->k || !c->v) return MQ_ERR_NULL;
+        if (!aligned16(c->k) || !aligned16(c->v)) return MQ_ERR_ALIGN;
+    }
+    return MQ_OK;
+}
+
+}  // namespace mq
+
+// Two f32 rounded to a pair of 16-bit values, `lo` in the low half.
+template <typename T>
+__device__ __forceinline__ uint32_t mq_pack2(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t mq_pack2<__half>(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <>
+__device__ __forceinline__ uint32_t mq_pack2<__nv_bfloat16>(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}

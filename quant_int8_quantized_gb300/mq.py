@@ -16,7 +16,7 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "_lib", "libmq.so")
 
-MQ_OK, MQ_ERR_NULL, MQ_ERR_SHAPE, MQ_ERR_ALIGN, MQ_ERR_ARCH, MQ_ERR_LAUNCH, MQ_ERR_DEVICE, MQ_ERR_SCRATCH = range(8)
+MQ_OK, MQ_ERR_NULL, MQ_ERR_SHAPE, MQ_ERR_ALIGN, MQ_ERR_ARCH, MQ_ERR_LAUNCH, MQ_ERR_DEVICE, MQ_ERR_SCRATCH, MQ_ERR_TYPE = range(9)
 MQ_GEMV_MAX_ROWS = 8   # include/mq.h
 
 EXPORTED = ["mq_plane_bytes", "mq_q4k_row_bytes", "mq_q6k_row_bytes", "mq_q6k_packed_row_bytes", "mq_prepack_q6k",
@@ -24,6 +24,7 @@ EXPORTED = ["mq_plane_bytes", "mq_q4k_row_bytes", "mq_q6k_row_bytes", "mq_q6k_pa
             "mq_swiglu_quant", "mq_gemm_q4k", "mq_gemm_q6k", "mq_gemv_q4k", "mq_gemv_q6k",
             "mq_q5k_row_bytes", "mq_q4_0_row_bytes", "mq_q4_1_row_bytes", "mq_gemv_q5k", "mq_gemv_q4_0",
             "mq_gemv_q4_1", "mq_gemm_q4_0", "mq_gemm_q4_1", "mq_gemv_q6k_packed", "mq_gemm_q6k_static", "mq_gemm_q4k_pair",
+            "mq_qk_norm_rope", "mq_attn_ws_bytes", "mq_attn_prefix", "mq_kv_evict",
             "mq_device_status", "mq_status_str"]
 
 
@@ -37,6 +38,19 @@ class CPlane(ctypes.Structure):
     _fields_ = [("qs", ctypes.c_void_p), ("d", ctypes.c_void_p), ("s", ctypes.c_void_p),
                 ("ah", ctypes.c_void_p), ("ax", ctypes.c_void_p), ("af", ctypes.c_void_p),
                 ("M", ctypes.c_int), ("K", ctypes.c_int)]
+
+
+class CKV(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("seq_stride", ctypes.c_longlong),
+                ("row_stride", ctypes.c_longlong), ("head_stride", ctypes.c_longlong), ("type", ctypes.c_int),
+                ("n", ctypes.c_int), ("cap", ctypes.c_int), ("heads", ctypes.c_int), ("dim", ctypes.c_int)]
+
+
+class CQKV(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "k", "v")] + \
+               [(n, ctypes.c_longlong) for n in ("q_stride", "k_stride", "v_stride")] + \
+               [(n, ctypes.c_void_p) for n in ("wq", "wk", "inv_freq", "axis", "pos")] + \
+               [(n, ctypes.c_int) for n in ("M", "Hq", "n_pairs", "n_axes", "interleaved")] + [("eps", ctypes.c_float)]
 
 
 _lib = None
@@ -76,6 +90,11 @@ def lib() -> ctypes.CDLL:
             "mq_gemv_q4_1": (i, [pp, vp, i, vp, vp]),
             "mq_gemm_q4_0": (i, [pp, vp, i, vp, vp]),
             "mq_gemm_q4_1": (i, [pp, vp, i, vp, vp]),
+            "mq_qk_norm_rope": (i, [ctypes.POINTER(CQKV), vp, ctypes.POINTER(CKV), vp, vp]),
+            "mq_attn_ws_bytes": (sz, [i, i, i, i, i, i, i, i]),
+            "mq_attn_prefix": (i, [vp, ctypes.c_longlong, i, i, i, ctypes.POINTER(CKV), ctypes.POINTER(CKV), vp, f, vp, i,
+                                   vp, vp, vp, vp, sz, vp]),
+            "mq_kv_evict": (i, [ctypes.POINTER(CKV), vp, vp, i, i, ctypes.POINTER(CKV), vp, vp, vp, vp]),
             "mq_device_status": (i, [vp]),
             "mq_status_str": (ctypes.c_char_p, [i]),
         }
@@ -304,6 +323,209 @@ def mq_q4_0_row_bytes(K: int) -> int:
 
 def mq_q4_1_row_bytes(K: int) -> int:
     return int(lib().mq_q4_1_row_bytes(K))
+
+
+# ---------------------------------------------------------------- heads, caches, attention
+
+_TYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}   # include/mq.h: MQ_F16, MQ_BF16, MQ_F32
+
+
+class KV:
+    """Keys and values of n sequences (include/mq.h, mq_kv): 16-bit CUDA tensors k and v of shape
+    [n, cap, heads, dim], with the same strides and the last dim contiguous. A cache that is laid
+    out [n, heads, cap, dim] is given as its transpose(1, 2)."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor):
+        for t, name in ((k, "k"), (v, "v")):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{name} must be a torch.Tensor")
+            if t.device.type != "cuda":
+                raise ValueError(f"{name} must be a CUDA tensor")
+            if t.dtype not in (torch.float16, torch.bfloat16):
+                raise TypeError(f"{name} must be float16 or bfloat16, got {t.dtype}")
+            if t.dim() != 4 or (t.stride(3) != 1 and t.shape[3] > 1):
+                raise ValueError(f"{name} must be [n, cap, heads, dim] with contiguous dims")
+        if k.shape != v.shape or k.dtype != v.dtype or (k.stride() != v.stride() and k.numel()):
+            raise ValueError("k and v must have the same shape, type and strides")
+        self.k, self.v = k, v
+        self.n, self.cap, self.heads, self.dim = (int(x) for x in k.shape)
+        # an axis of one step has no stride that matters: torch may hold any number there
+        st = [int(k.stride(i)) if k.shape[i] > 1 else 0 for i in range(3)]
+        self._c = CKV(k.data_ptr(), v.data_ptr(), st[0], st[1], st[2], _TYPES[k.dtype], self.n, self.cap, self.heads,
+                      self.dim)
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def empty(cls, n: int, cap: int, heads: int, dim: int, dtype=torch.float16, device="cuda") -> "KV":
+        return cls(torch.empty((n, cap, heads, dim), dtype=dtype, device=device),
+                   torch.empty((n, cap, heads, dim), dtype=dtype, device=device))
+
+    @property
+    def dtype(self):
+        return self.k.dtype
+
+
+def _kv(c, name):
+    if not isinstance(c, KV):
+        raise TypeError(f"{name} must be a KV")
+    return c
+
+
+def rope_freq(n_pairs: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
+    """inv_freq for mq_qk_norm_rope: base^(-i / n_pairs), f32 [n_pairs]."""
+    i = torch.arange(n_pairs, dtype=torch.float64)
+    return (float(base) ** (-i / n_pairs)).to(torch.float32).to(device)
+
+
+def rope_axes(sections, device="cuda") -> torch.Tensor:
+    """axis for mq_qk_norm_rope: the first sections[0] pairs turn by axis 0, the next by axis 1, ..."""
+    return torch.tensor([a for a, n in enumerate(sections) for _ in range(n)], dtype=torch.uint8, device=device)
+
+
+def _heads(t, name, M, D, heads=None):
+    """f32 [M, heads, D] with each token's heads contiguous: (pointer, token stride, heads)."""
+    if t is None:
+        return None, 0, 0
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.float32:
+        raise TypeError(f"{name} must be torch.float32, got {t.dtype}")
+    s, st = t.shape, t.stride()
+    if len(s) != 3 or s[0] != M or s[2] != D or (heads is not None and s[1] != heads):
+        raise ValueError(f"{name} must be [{M}, {'heads' if heads is None else heads}, {D}], got {tuple(s)}")
+    if (st[2] != 1 and D > 1) or (st[1] != D and s[1] > 1):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return t.data_ptr(), (st[0] if M > 1 else s[1] * D), s[1]
+
+
+def mq_qk_norm_rope(q, k, v, q_out, cache: KV, slot=None, pos=None, inv_freq=None, axis=None, wq=None, wk=None,
+                    eps: float = 1e-6, interleaved: bool = False, stream=None):
+    """Head norms of q and k, rotation by position, q to 16 bits and k, v into the cache rows slot
+    (include/mq.h). q: f32 [M, Hq, D]; k, v: f32 [M, Hkv, D] (any may be None; a token's heads are
+    contiguous, tokens at any stride); q_out: [M, Hq, D] of the cache's type; slot: int32 [M];
+    pos: int32 [M] or [n_axes, M]; inv_freq: f32 [n_pairs]; axis: uint8 [n_pairs]."""
+    _kv(cache, "cache")
+    first = next((t for t in (q, k, v) if t is not None), None)
+    if first is None:
+        raise ValueError("one of q, k and v is needed")
+    M, D = int(first.shape[0]), cache.dim
+    x = CQKV()
+    x.q, x.q_stride, Hq = _heads(q, "q", M, D)
+    x.k, x.k_stride, _ = _heads(k, "k", M, D, cache.heads)
+    x.v, x.v_stride, _ = _heads(v, "v", M, D, cache.heads)
+    if q is not None:
+        _dev_tensor(q_out, cache.dtype, "q_out")
+        if q_out.numel() < M * Hq * D:
+            raise ValueError(f"q_out holds {q_out.numel()} elements, needs {M * Hq * D}")
+    for t, name in ((wq, "wq"), (wk, "wk")):
+        if t is not None and _dev_tensor(t, torch.float32, name).numel() != D:
+            raise ValueError(f"{name} must hold {D} weights")
+    n_pairs = n_axes = 0
+    if inv_freq is not None and inv_freq.numel():
+        n_pairs = _dev_tensor(inv_freq, torch.float32, "inv_freq").numel()
+        _dev_tensor(pos, torch.int32, "pos")
+        n_axes = 1 if pos.dim() == 1 else int(pos.shape[0])
+        if pos.numel() != n_axes * M:
+            raise ValueError(f"pos must be [{M}] or [n_axes, {M}], got {tuple(pos.shape)}")
+        if axis is not None and _dev_tensor(axis, torch.uint8, "axis").numel() != n_pairs:
+            raise ValueError(f"axis must hold {n_pairs} entries")
+        x.inv_freq, x.pos = inv_freq.data_ptr(), pos.data_ptr()
+        x.axis = None if axis is None else axis.data_ptr()
+    if slot is not None and _dev_tensor(slot, torch.int32, "slot").numel() != M:
+        raise ValueError(f"slot must hold {M} entries")
+    x.wq = None if wq is None else wq.data_ptr()
+    x.wk = None if wk is None else wk.data_ptr()
+    x.M, x.Hq, x.n_pairs, x.n_axes, x.interleaved, x.eps = M, Hq, n_pairs, n_axes, int(bool(interleaved)), float(eps)
+    _check(lib().mq_qk_norm_rope(ctypes.byref(x), _ptr(q_out), cache._ref, _ptr(slot), _stream(stream)),
+           "mq_qk_norm_rope")
+    return q_out
+
+
+def mq_attn_ws_bytes(B: int, T: int, Hq: int, Hkv: int, D: int, prefix_cap: int, own_cap: int,
+                     scores: bool = False) -> int:
+    return int(lib().mq_attn_ws_bytes(B, T, Hq, Hkv, D, prefix_cap, own_cap, int(bool(scores))))
+
+
+def attn_workspace(B: int, T: int, Hq: int, Hkv: int, D: int, prefix_cap: int, own_cap: int, scores: bool = False,
+                   device="cuda") -> torch.Tensor:
+    """A workspace for mq_attn_prefix calls of up to these sizes on one stream."""
+    return torch.empty((max(16, mq_attn_ws_bytes(B, T, Hq, Hkv, D, prefix_cap, own_cap, scores)),), dtype=torch.uint8,
+                       device=device)
+
+
+def mq_attn_prefix(q: torch.Tensor, prefix, own, own_len, out: torch.Tensor, scale=None, lse=None, score=None,
+                   score_out=None, ws=None, stream=None) -> torch.Tensor:
+    """Attention of q [B, T, Hq, D] over a shared prefix (KV of one sequence, or None) and each
+    sequence's own cache (KV of B sequences, or None) of own_len rows (include/mq.h). out: [B, T,
+    Hq, D] in q's type or f32; lse: f32 [B, T, Hq]; score, score_out: f32 [B, Hkv, own.cap];
+    scale: 1 / sqrt(D) if None; ws: attn_workspace(...), allocated for this call if None."""
+    any_kv = own if own is not None else prefix
+    if any_kv is None:
+        raise ValueError("a prefix, an own cache or both are needed")
+    if prefix is not None:
+        _kv(prefix, "prefix")
+    if own is not None:
+        _kv(own, "own")
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise TypeError("q must be a torch.Tensor [B, T, Hq, D]")
+    B, T, Hq, D = q.shape
+    if q.device.type != "cuda":
+        raise ValueError("q must be a CUDA tensor")
+    if q.dtype != any_kv.dtype:
+        raise TypeError(f"q must be {any_kv.dtype}, got {q.dtype}")
+    if D != any_kv.dim:
+        raise ValueError(f"q's heads are {D} wide, the cache's {any_kv.dim}")
+    st = q.stride()
+    if q.numel() and ((st[3] != 1) or (Hq > 1 and st[2] != D) or (B > 1 and T > 1 and st[0] != T * st[1])):
+        raise ValueError("q: a token's heads must be contiguous, and the tokens at one stride")
+    row = st[1] if T > 1 else st[0] if B > 1 else Hq * D
+    if out.dtype not in (q.dtype, torch.float32):
+        raise TypeError(f"out must be {q.dtype} or torch.float32, got {out.dtype}")
+    _dev_tensor(out, out.dtype, "out")
+    if out.numel() < q.numel():
+        raise ValueError(f"out holds {out.numel()} elements, needs {q.numel()}")
+    if own is not None and _dev_tensor(own_len, torch.int32, "own_len").numel() != B:
+        raise ValueError(f"own_len must hold {B} lengths")
+    if lse is not None and _dev_tensor(lse, torch.float32, "lse").numel() < B * T * Hq:
+        raise ValueError(f"lse needs {B * T * Hq} elements")
+    for t, name in ((score, "score"), (score_out, "score_out")):
+        if t is not None and (own is None or
+                              _dev_tensor(t, torch.float32, name).numel() < B * own.heads * own.cap):
+            raise ValueError(f"{name} must be [B, Hkv, own.cap]")
+    if ws is None:
+        ws = attn_workspace(B, T, Hq, any_kv.heads, D, prefix.cap if prefix else 0, own.cap if own else 0,
+                            score is not None, q.device)
+    _check(lib().mq_attn_prefix(q.data_ptr(), row, B, T, Hq, prefix._ref if prefix is not None else None,
+                                own._ref if own is not None else None, _ptr(own_len) if own is not None else None,
+                                float(D) ** -0.5 if scale is None else float(scale), out.data_ptr(),
+                                _TYPES[out.dtype], _ptr(lse), _ptr(score), _ptr(score_out), ws.data_ptr(),
+                                ws.numel() * ws.element_size(), _stream(stream)), "mq_attn_prefix")
+    return out
+
+
+def mq_kv_evict(src: KV, length: torch.Tensor, score: torch.Tensor, keep: int, recent: int, dst: KV,
+                length_out: torch.Tensor, score_out, index: torch.Tensor, stream=None) -> KV:
+    """Keep, per sequence and key head, the `recent` last rows of src and the best `keep - recent`
+    others by score (include/mq.h). length, length_out: int32 [n]; score: f32 [n, heads, src.cap];
+    score_out (or None): f32 [n, heads, dst.cap]; index: int32 [n, heads, dst.cap], the rows kept.
+    dst may be src: the rows then move in place."""
+    _kv(src, "src")
+    _kv(dst, "dst")
+    for t, name in ((length, "length"), (length_out, "length_out")):
+        if _dev_tensor(t, torch.int32, name).numel() != src.n:
+            raise ValueError(f"{name} must hold {src.n} lengths")
+    if _dev_tensor(score, torch.float32, "score").numel() < src.n * src.heads * src.cap:
+        raise ValueError("score must be [n, heads, src.cap]")
+    need = dst.n * dst.heads * dst.cap
+    if score_out is not None and _dev_tensor(score_out, torch.float32, "score_out").numel() < need:
+        raise ValueError("score_out must be [n, heads, dst.cap]")
+    if _dev_tensor(index, torch.int32, "index").numel() < need:
+        raise ValueError("index must be [n, heads, dst.cap]")
+    _check(lib().mq_kv_evict(src._ref, _ptr(length), _ptr(score), int(keep), int(recent), dst._ref, _ptr(length_out),
+                             _ptr(score_out), _ptr(index), _stream(stream)), "mq_kv_evict")
+    return dst
 
 
 def mq_device_status(stream=None) -> int:
