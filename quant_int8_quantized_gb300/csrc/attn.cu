@@ -7,6 +7,7 @@
 #include <utility>
 
 #include "attn_few.cuh"
+#include "attn_many.cuh"
 
 namespace attn {
 
@@ -159,40 +160,58 @@ __global__ void __launch_bounds__(256) attn_score_kernel(const float* raw, const
 
 size_t up16(size_t n) { return (n + 15) & ~(size_t)15; }
 
-// Where a call's workspace holds what, for at most `G` blocks.
-struct Layout {
-    size_t o, ml, info, lse2, raw, bytes;
+// Query rows per key head from which the tensor-core kernel takes a part.
+constexpr int kManyFrom = 33;
+
+// How a call is cut: the part of each kernel, and where the workspace holds what.
+struct Cut {
+    Plan few, many;
+    bool prefix_many, own_many;
+    size_t few_o, few_ml, few_info, many_o, many_ml, many_info, lse2, raw, bytes;
 };
 
-Plan plan_of(int B, int T, int Hq, int Hkv, int D, int prefix_keys, int own_cap) {
-    Plan p;
-    p.B = B;
-    p.T = T;
-    p.Hq = Hq;
-    p.Hkv = Hkv;
-    p.group = Hq / Hkv;
-    p.prefix_rows = B * T * p.group;
-    p.prefix_keys = prefix_keys;
-    p.own_cap = own_cap;
-    p.rows = kFewRows;
-    p.keys = few_tile_keys(D);
-    const long long most = (long long)prefix_segs(p) * ceil_div(prefix_keys, p.keys) +
-                           (all_segs(p) - prefix_segs(p)) * ceil_div(own_cap, p.keys);
-    const long long cap = (long long)mq::num_sms() * kMaxPerSm;
-    p.G = (int)(most < cap ? (most > 0 ? most : 1) : cap);
-    return p;
-}
-
-Layout layout_of(const Plan& p, int D, bool scores) {
-    Layout w;
-    const size_t places = (size_t)p.G + (size_t)all_segs(p), rows = (size_t)p.B * p.T * p.Hq;
-    w.o = 0;
-    w.ml = up16(places * p.rows * D * sizeof(float));
-    w.info = w.ml + up16(places * p.rows * sizeof(float2));
-    w.lse2 = w.info + up16((size_t)all_segs(p) * sizeof(int2));
-    w.raw = w.lse2 + (scores ? up16(rows * sizeof(float)) : 0);
-    w.bytes = w.raw + (scores ? up16(rows * p.own_cap * sizeof(float)) : 0);
-    return w;
+Cut cut_of(int B, int T, int Hq, int Hkv, int D, int prefix_keys, int own_cap, bool scores) {
+    Cut c;
+    const int group = Hq / Hkv;
+    c.prefix_many = prefix_keys > 0 && many_takes(D) && (long long)B * T * group >= kManyFrom;
+    // the weights' raw products come from the kernel for few rows
+    c.own_many = own_cap > 0 && many_takes(D) && !scores && (long long)T * group >= kManyFrom;
+    size_t at = 0;
+    auto plan = [&](bool many, size_t* o, size_t* ml, size_t* info) {
+        Plan p;
+        p.B = B;
+        p.T = T;
+        p.Hq = Hq;
+        p.Hkv = Hkv;
+        p.group = group;
+        p.prefix_rows = B * T * group;
+        p.prefix_keys = c.prefix_many == many ? prefix_keys : 0;
+        p.own_cap = c.own_many == many ? own_cap : 0;
+        p.rows = many ? kManyRows : kFewRows;
+        p.keys = many ? kManyKeys : few_tile_keys(D);
+        const long long segs = all_segs(p);
+        const long long most = (long long)prefix_segs(p) * ceil_div(p.prefix_keys, p.keys) +
+                               (segs - prefix_segs(p)) * ceil_div(p.own_cap, p.keys);
+        const long long held = (long long)mq::num_sms() * (many ? 1 : kMaxPerSm);
+        p.G = (int)(most < held ? most : held);
+        const size_t places = segs > 0 ? (size_t)p.G + (size_t)segs : 0;
+        *o = at;
+        at += up16(places * p.rows * D * sizeof(float));
+        *ml = at;
+        at += up16(places * p.rows * sizeof(float2));
+        *info = at;
+        at += up16((size_t)segs * sizeof(int2));
+        return p;
+    };
+    c.few = plan(false, &c.few_o, &c.few_ml, &c.few_info);
+    c.many = plan(true, &c.many_o, &c.many_ml, &c.many_info);
+    const size_t rows = (size_t)B * T * Hq;
+    c.lse2 = at;
+    at += scores ? up16(rows * sizeof(float)) : 0;
+    c.raw = at;
+    at += scores ? up16(rows * own_cap * sizeof(float)) : 0;
+    c.bytes = at;
+    return c;
 }
 
 bool valid_heads(int Hq, int Hkv, int D) {
@@ -208,7 +227,7 @@ bool valid_counts(long long B, long long T, long long Hq) { return B * T * Hq <=
 extern "C" size_t mq_attn_ws_bytes(int B, int T, int Hq, int Hkv, int D, int prefix_cap, int own_cap, int scores) {
     using namespace attn;
     if (B <= 0 || T <= 0 || prefix_cap < 0 || own_cap < 0 || !valid_heads(Hq, Hkv, D) || !valid_counts(B, T, Hq)) return 0;
-    return layout_of(plan_of(B, T, Hq, Hkv, D, prefix_cap, own_cap), D, scores != 0).bytes;
+    return cut_of(B, T, Hq, Hkv, D, prefix_cap, own_cap, scores != 0).bytes;
 }
 
 extern "C" int mq_attn_prefix(const void* q, long long q_stride, int B, int T, int Hq, const mq_kv* prefix,
@@ -237,21 +256,37 @@ extern "C" int mq_attn_prefix(const void* q, long long q_stride, int B, int T, i
         !mq::aligned16(lse) || !mq::aligned16(score) || !mq::aligned16(score_out))
         return MQ_ERR_ALIGN;
     const bool scores = score_out && cap > 0;
-    Plan p = plan_of(B, T, Hq, Hkv, D, P, cap);
-    if (all_segs(p) > 0x3fffffffLL || (long long)B * Hkv > 65535) return MQ_ERR_SHAPE;
-    const Layout w = layout_of(p, D, scores);
-    if (ws_bytes < w.bytes) return MQ_ERR_SCRATCH;
+    Cut c = cut_of(B, T, Hq, Hkv, D, P, cap, scores);
+    if (all_segs(c.few) > 0x3fffffffLL || (long long)B * Hkv > 65535) return MQ_ERR_SHAPE;
+    if (ws_bytes < c.bytes) return MQ_ERR_SCRATCH;
     rc = mq::check_arch();
     if (rc != MQ_OK) return rc;
     uint8_t* base = static_cast<uint8_t*>(ws);
-    const Pieces pieces = {reinterpret_cast<float*>(base + w.o), reinterpret_cast<float2*>(base + w.ml),
-                           reinterpret_cast<int2*>(base + w.info)};
-    float* lse2 = scores ? reinterpret_cast<float*>(base + w.lse2) : nullptr;
-    float* raw = scores ? reinterpret_cast<float*>(base + w.raw) : nullptr;
+    auto pieces = [&](size_t o, size_t ml, size_t info) {
+        return Pieces{reinterpret_cast<float*>(base + o), reinterpret_cast<float2*>(base + ml),
+                      reinterpret_cast<int2*>(base + info)};
+    };
+    const Pieces few = pieces(c.few_o, c.few_ml, c.few_info), many = pieces(c.many_o, c.many_ml, c.many_info);
+    float* lse2 = scores ? reinterpret_cast<float*>(base + c.lse2) : nullptr;
+    float* raw = scores ? reinterpret_cast<float*>(base + c.raw) : nullptr;
+    constexpr float kLog2e = 1.4426950408889634f;
 
-    if (all_segs(p) > 0) {
+    if (all_segs(c.many) > 0) {
+        ManyArgs m;
+        m.plan = c.many;
+        m.q = q;
+        m.q_stride = q_stride;
+        m.len = own_len;
+        // a scale of next to nothing keeps masked products (-infinity) masked where zero would not
+        m.scale_log2 = std::fmax(std::fabs(scale) * kLog2e, 1e-30f);
+        m.negative = scale < 0.0f;
+        m.out = many;
+        rc = launch_many(m, c.prefix_many ? prefix : nullptr, c.own_many ? own : nullptr, D, type, stream);
+        if (rc != MQ_OK) return rc;
+    }
+    if (all_segs(c.few) > 0) {
         FewArgs f;
-        f.plan = p;
+        f.plan = c.few;
         f.q = q;
         f.q_stride = q_stride;
         f.pk = P > 0 ? prefix->k : nullptr;
@@ -264,8 +299,8 @@ extern "C" int mq_attn_prefix(const void* q, long long q_stride, int B, int T, i
         f.o_row = cap > 0 ? own->row_stride : 0;
         f.o_head = cap > 0 ? own->head_stride : 0;
         f.len = own_len;
-        f.scale_log2 = scale * 1.4426950408889634f;
-        f.out = pieces;
+        f.scale_log2 = scale * kLog2e;
+        f.out = few;
         f.raw = raw;
         const int held = few_blocks(D, type);
         if (f.plan.G > held) f.plan.G = held;
@@ -273,16 +308,16 @@ extern "C" int mq_attn_prefix(const void* q, long long q_stride, int B, int T, i
         if (rc != MQ_OK) return rc;
     }
     JoinArgs j;
-    j.prefix = {pieces, P > 0 ? p.rows : 0};
-    j.own = {pieces, cap > 0 ? p.rows : 0};
+    j.prefix = {c.prefix_many ? many : few, P > 0 ? (c.prefix_many ? kManyRows : kFewRows) : 0};
+    j.own = {c.own_many ? many : few, cap > 0 ? (c.own_many ? kManyRows : kFewRows) : 0};
     j.len = own_len;
     j.B = B;
     j.T = T;
     j.Hq = Hq;
     j.Hkv = Hkv;
-    j.group = p.group;
+    j.group = Hq / Hkv;
     j.own_cap = cap;
-    j.seg0 = prefix_segs(p);
+    j.seg0 = prefix_segs(c.own_many ? c.many : c.few);
     j.out = out;
     j.lse = lse;
     j.lse2 = lse2;

@@ -68,30 +68,36 @@ __device__ __forceinline__ int unit_tiles(const Plan& p, const int32_t* len, int
 }
 
 // Finds the block's run. Segments follow one another as unit, then head. Threads share the
-// units (sequence and row tile), add up their tiles and scan the sums: THREADS threads, all of the block.
+// units (sequence and row tile) and scan the sums of their tiles: THREADS threads, all of the block.
 template <int THREADS>
 __device__ __forceinline__ Cursor find_run(const Plan& p, const int32_t* len) {
-    __shared__ long long s_sum[THREADS];
+    constexpr int kWarps = THREADS / 32;
+    __shared__ long long s_sum[kWarps];
     __shared__ long long s_at[2];   // unit, tiles before it
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     const int per_seq = own_tiles_of_rows(p), units = p.B * per_seq;
     const int share = ceil_div(units, THREADS);
     const int u0 = min(tid * share, units), u1 = min(u0 + share, units);
     long long sum = 0;
     for (int u = u0; u < u1; ++u) sum += unit_tiles(p, len, u, per_seq);
-    s_sum[tid] = sum;
+    long long upto = sum;           // tiles of this thread's units and of those before
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long t = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += t;
+    }
+    if (lane == 31) s_sum[wid] = upto;
     __syncthreads();
-#pragma unroll 1
-    for (int o = 1; o < THREADS; o <<= 1) {
-        const long long t = tid >= o ? s_sum[tid - o] : 0;
-        __syncthreads();
-        s_sum[tid] += t;
-        __syncthreads();
+    long long own = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < wid) upto += s_sum[w];
+        own += s_sum[w];
     }
     const int pt = p.prefix_keys > 0 ? ceil_div(p.prefix_keys, p.keys) : 0;
     const long long prefix = (long long)prefix_segs(p) * pt;
     Cursor c;
-    c.total = prefix + s_sum[THREADS - 1] * p.Hkv;
+    c.total = prefix + own * p.Hkv;
     // no block in between is without a tile: a segment's pieces are those of consecutive blocks
     c.blocks = c.total < p.G ? (int)c.total : p.G;
     c.tile = c.end = 0;
@@ -108,7 +114,7 @@ __device__ __forceinline__ Cursor find_run(const Plan& p, const int32_t* len) {
         return c;
     }
     const long long x = c.tile - prefix;
-    const long long mine = s_sum[tid] * p.Hkv, before = mine - sum * p.Hkv;
+    const long long mine = upto * p.Hkv, before = mine - sum * p.Hkv;
     if (x >= before && x < mine) {
         long long at = before;
         for (int u = u0; u < u1; ++u) {

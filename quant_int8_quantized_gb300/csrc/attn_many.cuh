@@ -1,0 +1,25 @@
+// Attention pieces (attn.cuh) for many query rows per key head: a batch on one prefix, a prompt. See
+// attn_many.cu.
+#pragma once
+
+#include "attn.cuh"
+
+namespace attn {
+
+struct ManyArgs {
+    Plan plan;
+    const void* q;
+    long long q_stride;
+    const int32_t* len;
+    float scale_log2;     // |scale| log2 e, not below 1e-30
+    int negative;         // scale < 0
+    Pieces out;
+};
+
+constexpr int kManyRows = 256;    // query rows per segment
+constexpr int kManyKeys = 128;    // keys per tile
+
+inline bool many_takes(int D) { return D == 64 || D == 128; }
+int launch_many(const ManyArgs& a, const mq_kv* prefix, const mq_kv* own, int D, int type, cudaStream_t stream);
+
+}  // namespace attn

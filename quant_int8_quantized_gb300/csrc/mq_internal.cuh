@@ -93,6 +93,7 @@ int launch_plain(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cud
 // Each translation unit with bounded waits owns one word; these read and clear it.
 int take_gemm_device_error(cudaStream_t stream, unsigned* code);
 int take_gemv_device_error(cudaStream_t stream, unsigned* code);
+int take_attn_device_error(cudaStream_t stream, unsigned* code);
 
 }  // namespace mq
 
