@@ -29,9 +29,8 @@ bool allow_smem(const void* kern, int bytes) {
 namespace {
 
 constexpr int kMaxPerSm = 4;   // blocks of a piece kernel per SM, at most
-constexpr float kLn2 = 0.6931471805599453f;
 
-// One part of the keys, as the joining kernel sees it.
+// One part of the keys, as the joining kernels see it.
 struct Part {
     Pieces p;
     int rows;      // per segment; 0: no such part
@@ -41,96 +40,134 @@ struct JoinArgs {
     Part prefix, own;
     const int32_t* len;
     int B, T, Hq, Hkv, group, own_cap, seg0;   // seg0: the own part's first segment
-    void* out;
-    float* lse;    // natural, or nullptr
-    float* lse2;   // base 2, or nullptr
+    Out fin;
+    float* lse2;    // base 2, or nullptr
 };
 
-__device__ __forceinline__ float exp2_acc(float x) { return exp2f(x); }
+// Pieces of a row: `count` of them, `stride` rows apart, the first at row `first` of the pieces.
+struct Run {
+    const Pieces* p;
+    long long first, stride;
+    int count;
+};
 
-// A warp per query row: the pieces' common maximum, then their outputs weighted and added in key order.
+// Pieces of row `in` of a segment whose blocks are f.x .. f.y.
+__device__ __forceinline__ Run run_of(const Part& p, int seg, int2 f, int in) {
+    return Run{&p.p, ((long long)f.x + seg) * p.rows + in, p.rows, f.y - f.x + 1};
+}
+
+// One warp adds up a row's pieces: their common maximum, then outputs weighted and added in order. Lane i
+// holds maximum and sum of piece i of 32; the outputs' loads do not depend on one another.
+template <typename O, int D, int N>
+__device__ __forceinline__ void join_row(const Run (&runs)[N], const Out& fin, float* lse2, long long row) {
+    constexpr int W = (D + 63) / 64;
+    const int lane = threadIdx.x & 31;
+    float m = -INFINITY, l = 0.0f;
+    float2 acc[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) acc[i] = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int w = 0; w < N; ++w) {
+#pragma unroll 1
+        for (int i0 = 0; i0 < runs[w].count; i0 += 32) {
+            const int n = min(32, runs[w].count - i0);
+            const long long first = runs[w].first + i0 * runs[w].stride;
+            float2 ml = make_float2(-INFINITY, 0.0f);
+            if (lane < n) ml = __ldca(runs[w].p->ml + first + lane * runs[w].stride);
+            float now = fmaxf(m, ml.x);
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, o));
+            const float safe = now == -INFINITY ? 0.0f : now;
+            const float back = exp2f(m - safe), f = exp2f(ml.x - safe);
+            m = now;
+            float sum = ml.y == 0.0f ? 0.0f : ml.y * f;
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            l = l * back + sum;
+#pragma unroll
+            for (int k = 0; k < W; ++k) acc[k].x *= back, acc[k].y *= back;
+            const float* o = runs[w].p->o + first * D;
+#pragma unroll 4
+            for (int i = 0; i < n; ++i) {
+                const float g = __shfl_sync(0xffffffffu, f, i);
+                const float2* oi = reinterpret_cast<const float2*>(o + i * runs[w].stride * D);
+#pragma unroll
+                for (int k = 0; k < W; ++k)
+                    if (k * 32 + lane < D / 2) {
+                        const float2 x = __ldca(oi + k * 32 + lane);
+                        acc[k].x = fmaf(x.x, g, acc[k].x);
+                        acc[k].y = fmaf(x.y, g, acc[k].y);
+                    }
+            }
+        }
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;   // l == 0: no key seen (a NaN or infinite l stays one)
+#pragma unroll
+    for (int k = 0; k < W; ++k)
+        if (k * 32 + lane < D / 2) {
+            const float x = acc[k].x * inv, y = acc[k].y * inv;
+            if constexpr (sizeof(O) == 4)
+                reinterpret_cast<float2*>(fin.out)[row * (D / 2) + k * 32 + lane] = make_float2(x, y);
+            else
+                reinterpret_cast<uint32_t*>(fin.out)[row * (D / 2) + k * 32 + lane] = mq_pack2<O>(x, y);
+        }
+    if (lane == 0) {
+        if (fin.lse) fin.lse[row] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
+        if (lse2) lse2[row] = l == 0.0f ? -INFINITY : m + log2f(l);
+    }
+}
+
+// Every query row, a warp each: its prefix segment's pieces, then its own segment's.
 template <typename O, int D>
 __global__ void __launch_bounds__(256) attn_join_kernel(const JoinArgs a) {
-    constexpr int N = (D + 63) / 64;
     mq_grid_release();
     mq_grid_wait();
-    const int lane = threadIdx.x & 31;
     const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);   // (b T + t) Hq + h
     if (row >= (long long)a.B * a.T * a.Hq) return;
     const int h = (int)(row % a.Hq);
     const long long bt = row / a.Hq;
     const int t = (int)(bt % a.T), b = (int)(bt / a.T);
-    const int hk = h / a.group;
+    const int hk = h / a.group, tg = a.T * a.group;
     const int r_own = t * a.group + h - hk * a.group;
-    float m = -INFINITY;
-    // the row's pieces: prefix segment, own segment; [first place, count, row in the segment]
-    long long place[2] = {0, 0};
-    int count[2] = {0, 0}, in[2] = {0, 0};
+    Run runs[2] = {};
     if (a.prefix.rows > 0) {
-        const int r = b * a.T * a.group + r_own;
-        const int seg = r / a.prefix.rows * a.Hkv + hk;
-        in[0] = r % a.prefix.rows;
-        const int2 f = __ldca(a.prefix.p.info + seg);
-        place[0] = (long long)f.x + seg;
-        count[0] = f.y - f.x + 1;
+        const int r = b * tg + r_own, rt = r / a.prefix.rows;
+        const int seg = rt * a.Hkv + hk;
+        runs[0] = run_of(a.prefix, seg, __ldca(a.prefix.p.info + seg), r - rt * a.prefix.rows);
     }
     if (a.own.rows > 0) {
-        const int rt = r_own / a.own.rows, tg = a.T * a.group;
+        const int rt = r_own / a.own.rows;
         const int last = min((rt + 1) * a.own.rows, tg) - 1;
         if (min(max(__ldca(a.len + b), 0), a.own_cap) - a.T + 1 + last / a.group > 0) {
             const int seg = a.seg0 + (b * ceil_div(tg, a.own.rows) + rt) * a.Hkv + hk;
-            in[1] = r_own % a.own.rows;
-            const int2 f = __ldca(a.own.p.info + seg);
-            place[1] = (long long)f.x + seg;
-            count[1] = f.y - f.x + 1;
+            runs[1] = run_of(a.own, seg, __ldca(a.own.p.info + seg), r_own - rt * a.own.rows);
         }
     }
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-        const Part& p = w ? a.own : a.prefix;
-        for (int i = lane; i < count[w]; i += 32) m = fmaxf(m, __ldca(&p.p.ml[(place[w] + i) * p.rows + in[w]].x));
-    }
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float safe = m == -INFINITY ? 0.0f : m;
-    float l = 0.0f;
-    float2 acc[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) acc[i] = make_float2(0.0f, 0.0f);
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-        const Part& p = w ? a.own : a.prefix;
-#pragma unroll 4
-        for (int i = 0; i < count[w]; ++i) {
-            const long long at = (place[w] + i) * p.rows + in[w];
-            const float2 ml = __ldca(p.p.ml + at);
-            const float f = exp2_acc(ml.x - safe);
-            l += ml.y * f;
-            const float2* o = reinterpret_cast<const float2*>(p.p.o + at * D);
-#pragma unroll
-            for (int k = 0; k < N; ++k)
-                if (k * 32 + lane < D / 2) {
-                    const float2 x = __ldca(o + k * 32 + lane);
-                    acc[k].x = fmaf(x.x, f, acc[k].x);
-                    acc[k].y = fmaf(x.y, f, acc[k].y);
-                }
-        }
-    }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;   // l == 0: no key seen (a NaN or infinite l stays one)
-#pragma unroll
-    for (int k = 0; k < N; ++k)
-        if (k * 32 + lane < D / 2) {
-            const float x = acc[k].x * inv, y = acc[k].y * inv;
-            if constexpr (sizeof(O) == 4)
-                reinterpret_cast<float2*>(a.out)[row * (D / 2) + k * 32 + lane] = make_float2(x, y);
-            else
-                reinterpret_cast<uint32_t*>(a.out)[row * (D / 2) + k * 32 + lane] = mq_pack2<O>(x, y);
-        }
-    if (lane == 0) {
-        const float l2 = l == 0.0f ? -INFINITY : safe + log2f(l);
-        if (a.lse) a.lse[row] = l == 0.0f ? -INFINITY : safe * kLn2 + logf(l);
-        if (a.lse2) a.lse2[row] = l2;
-    }
+    join_row<O, D>(runs, a.fin, a.lse2, row);
+}
+
+// The rows of the segments that one block of the first kernel began and another ended: grid x that block, y eight
+// rows of the segment. All other rows were finished by the block that held them.
+struct SplitArgs {
+    Part part;
+    const int4* split;
+    Plan plan;
+    Out fin;
+};
+template <typename O, int D>
+__global__ void __launch_bounds__(256) attn_join_split_kernel(const SplitArgs a) {
+    mq_grid_release();
+    mq_grid_wait();
+    const int4 s = __ldca(a.split + blockIdx.x);
+    if (s.x < 0) return;
+    const int per_seq = own_tiles_of_rows(a.plan), b = s.z / per_seq, rt = s.z - b * per_seq;
+    const int rows = rows_of(a.plan, a.plan.T * a.plan.group, rt);
+    const int in = blockIdx.y * 8 + (threadIdx.x >> 5);
+    if (in >= rows) return;
+    const int r = rt * a.plan.rows + in, t = r / a.plan.group;
+    const Run runs[1] = {run_of(a.part, s.x, make_int2(blockIdx.x, s.y), in)};
+    join_row<O, D>(runs, a.fin, nullptr,
+                   ((long long)b * a.plan.T + t) * a.plan.Hq + s.w * a.plan.group + r - t * a.plan.group);
 }
 
 // score_out = score + sum over the rows of 2^(raw - lse2), one thread a key.
@@ -160,22 +197,24 @@ __global__ void __launch_bounds__(256) attn_score_kernel(const float* raw, const
 
 size_t up16(size_t n) { return (n + 15) & ~(size_t)15; }
 
-// Query rows per key head from which the tensor-core kernel takes a part.
-constexpr int kManyFrom = 33;
+// Query rows per key head from which the tensor-core kernel takes the shared prefix, and from which it takes
+// a sequence's own rows (and with them the prefix, its keys then read once per sequence).
+constexpr int kPrefixMany = 33, kOwnMany = 128;
 
 // How a call is cut: the part of each kernel, and where the workspace holds what.
 struct Cut {
     Plan few, many;
-    bool prefix_many, own_many;
-    size_t few_o, few_ml, few_info, many_o, many_ml, many_info, lse2, raw, bytes;
+    bool prefix_many, own_many, fits;
+    size_t few_o, few_ml, few_info, many_o, many_ml, many_info, split, lse2, raw, bytes;
 };
 
 Cut cut_of(int B, int T, int Hq, int Hkv, int D, int prefix_keys, int own_cap, bool scores) {
     Cut c;
     const int group = Hq / Hkv;
-    c.prefix_many = prefix_keys > 0 && many_takes(D) && (long long)B * T * group >= kManyFrom;
     // the weights' raw products come from the kernel for few rows
-    c.own_many = own_cap > 0 && many_takes(D) && !scores && (long long)T * group >= kManyFrom;
+    c.own_many = own_cap > 0 && many_takes(D) && !scores && (long long)T * group >= kOwnMany;
+    c.prefix_many = prefix_keys > 0 && !c.own_many && many_takes(D) && (long long)B * T * group >= kPrefixMany;
+    c.fits = true;
     size_t at = 0;
     auto plan = [&](bool many, size_t* o, size_t* ml, size_t* info) {
         Plan p;
@@ -185,13 +224,19 @@ Cut cut_of(int B, int T, int Hq, int Hkv, int D, int prefix_keys, int own_cap, b
         p.Hkv = Hkv;
         p.group = group;
         p.prefix_rows = B * T * group;
-        p.prefix_keys = c.prefix_many == many ? prefix_keys : 0;
-        p.own_cap = c.own_many == many ? own_cap : 0;
+        p.prefix_keys = !c.own_many && c.prefix_many == many ? prefix_keys : 0;
+        p.lead_keys = many && c.own_many ? prefix_keys : 0;
+        p.own = c.own_many == many && own_cap > 0;
+        p.own_least = many ? 1 : 0;
+        p.own_cap = p.own ? own_cap : 0;
         p.rows = many ? kManyRows : kFewRows;
         p.keys = many ? kManyKeys : few_tile_keys(D);
+        p.wide = many ? kManyHalf : kFewRows;
+        p.extra = many ? kManyExtra : 0;
         const long long segs = all_segs(p);
         const long long most = (long long)prefix_segs(p) * ceil_div(p.prefix_keys, p.keys) +
-                               (segs - prefix_segs(p)) * ceil_div(p.own_cap, p.keys);
+                               (segs - prefix_segs(p)) * (ceil_div(p.lead_keys, p.keys) + ceil_div(p.own_cap, p.keys));
+        if (most * 2 + segs * p.extra > 0x7fffffffLL) c.fits = false;
         const long long held = (long long)mq::num_sms() * (many ? 1 : kMaxPerSm);
         p.G = (int)(most < held ? most : held);
         const size_t places = segs > 0 ? (size_t)p.G + (size_t)segs : 0;
@@ -205,6 +250,8 @@ Cut cut_of(int B, int T, int Hq, int Hkv, int D, int prefix_keys, int own_cap, b
     };
     c.few = plan(false, &c.few_o, &c.few_ml, &c.few_info);
     c.many = plan(true, &c.many_o, &c.many_ml, &c.many_info);
+    c.split = at;
+    at += c.own_many ? up16((size_t)c.many.G * sizeof(int4)) : 0;
     const size_t rows = (size_t)B * T * Hq;
     c.lse2 = at;
     at += scores ? up16(rows * sizeof(float)) : 0;
@@ -257,7 +304,7 @@ extern "C" int mq_attn_prefix(const void* q, long long q_stride, int B, int T, i
         return MQ_ERR_ALIGN;
     const bool scores = score_out && cap > 0;
     Cut c = cut_of(B, T, Hq, Hkv, D, P, cap, scores);
-    if (all_segs(c.few) > 0x3fffffffLL || (long long)B * Hkv > 65535) return MQ_ERR_SHAPE;
+    if (!c.fits || all_segs(c.few) > 0x3fffffffLL || all_segs(c.many) > 0x3fffffffLL || (long long)B * Hkv > 65535) return MQ_ERR_SHAPE;
     if (ws_bytes < c.bytes) return MQ_ERR_SCRATCH;
     rc = mq::check_arch();
     if (rc != MQ_OK) return rc;
@@ -269,6 +316,7 @@ extern "C" int mq_attn_prefix(const void* q, long long q_stride, int B, int T, i
     const Pieces few = pieces(c.few_o, c.few_ml, c.few_info), many = pieces(c.many_o, c.many_ml, c.many_info);
     float* lse2 = scores ? reinterpret_cast<float*>(base + c.lse2) : nullptr;
     float* raw = scores ? reinterpret_cast<float*>(base + c.raw) : nullptr;
+    const Out fin = {out, lse, out_type == MQ_F32};
     constexpr float kLog2e = 1.4426950408889634f;
 
     if (all_segs(c.many) > 0) {
@@ -281,8 +329,20 @@ extern "C" int mq_attn_prefix(const void* q, long long q_stride, int B, int T, i
         m.scale_log2 = std::fmax(std::fabs(scale) * kLog2e, 1e-30f);
         m.negative = scale < 0.0f;
         m.out = many;
-        rc = launch_many(m, c.prefix_many ? prefix : nullptr, c.own_many ? own : nullptr, D, type, stream);
+        m.split = c.own_many ? reinterpret_cast<int4*>(base + c.split) : nullptr;
+        m.fin = fin;
+        rc = launch_many(m, P > 0 ? prefix : nullptr, c.own_many ? own : nullptr, D, type, stream);
         if (rc != MQ_OK) return rc;
+        if (c.own_many) {
+            const SplitArgs s = {{many, kManyRows}, m.split, c.many, fin};
+            const int most = T * (Hq / Hkv) < kManyRows ? T * (Hq / Hkv) : kManyRows;
+            auto join = [&](auto o) {
+                using O = decltype(o);
+                return mq::launch_pdl(D == 64 ? attn_join_split_kernel<O, 64> : attn_join_split_kernel<O, 128>,
+                                      dim3(c.many.G, (most + 7) / 8), dim3(256), 0, stream, s);
+            };
+            return out_type == MQ_F32 ? join(float()) : out_type == MQ_F16 ? join(__half()) : join(__nv_bfloat16());
+        }
     }
     if (all_segs(c.few) > 0) {
         FewArgs f;
@@ -309,7 +369,7 @@ extern "C" int mq_attn_prefix(const void* q, long long q_stride, int B, int T, i
     }
     JoinArgs j;
     j.prefix = {c.prefix_many ? many : few, P > 0 ? (c.prefix_many ? kManyRows : kFewRows) : 0};
-    j.own = {c.own_many ? many : few, cap > 0 ? (c.own_many ? kManyRows : kFewRows) : 0};
+    j.own = {few, cap > 0 ? kFewRows : 0};
     j.len = own_len;
     j.B = B;
     j.T = T;
@@ -317,9 +377,8 @@ extern "C" int mq_attn_prefix(const void* q, long long q_stride, int B, int T, i
     j.Hkv = Hkv;
     j.group = Hq / Hkv;
     j.own_cap = cap;
-    j.seg0 = prefix_segs(c.own_many ? c.many : c.few);
-    j.out = out;
-    j.lse = lse;
+    j.seg0 = prefix_segs(c.few);
+    j.fin = fin;
     j.lse2 = lse2;
     const dim3 grid((unsigned)(((long long)B * T * Hq + 7) / 8));
     auto join = [&](auto o) {

@@ -1,13 +1,13 @@
 // What the attention kernels share: the work of a call as a row of key tiles, cut into equal shares.
 //
 // A *segment* is one tile of query rows against the keys of one head that these rows see: a
-// prefix segment (rows of all sequences) or an own segment (rows of one sequence). Its keys come
-// in tiles. All segments' tiles in a row, prefix segments first, are cut into one equal run per
-// block, whatever the lengths on the device are, so ragged batches stay balanced; a run may end inside a
-// segment and go on in the next. What a block computes of one segment is a *piece*: the
-// unnormalised output, maximum and sum of its rows over its keys, left in the workspace at place
-// block + segment (both only grow along the row of tiles, so places differ). The joining kernel adds
-// a row's pieces up in the order of their keys.
+// prefix segment (rows of all sequences), or an own segment (rows of one sequence; a prompt's own
+// segments begin with the prefix's keys). Its keys come in tiles. All segments' tiles in a row, prefix
+// segments first, are cut into runs of equal cost, one per block, whatever the lengths on the device
+// are, so ragged batches stay balanced; a run may end inside a segment and go on in the next. What a block
+// computes of one segment is a *piece*: the unnormalised output, maximum and sum of its rows over its keys, left in
+// the workspace at place block + segment (both only grow along the row of tiles, so places differ). The
+// joining kernels add a row's pieces up in the order of their keys.
 #pragma once
 
 #include "heads.cuh"
@@ -17,11 +17,15 @@ namespace attn {
 // The numbers of one schedule. G: blocks.
 struct Plan {
     int B, T, Hq, Hkv, group;       // group = Hq / Hkv
-    int prefix_rows, prefix_keys;   // rows per head of the prefix segments (B T group), or no segments
-    int own_cap;                    // 0: no own segments
+    int prefix_rows, prefix_keys;   // rows per head (B T group) and keys of the prefix segments; 0 keys: none
+    int lead_keys;                  // prefix keys at the head of each own segment
+    int own_cap;
+    int own;                        // there are own segments
+    int own_least;                  // tiles of an own segment at least (1: rows that see no key get their zeros there)
     int rows;                       // query rows per segment
     int keys;                       // keys per tile
     int G;
+    int wide, extra;                // cost of a tile with more than `wide` rows is 2, else 1; `extra` once a segment
 };
 
 __host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
@@ -31,12 +35,16 @@ __host__ __device__ inline int prefix_tiles_of_rows(const Plan& p) {
     return p.prefix_keys > 0 ? ceil_div(p.prefix_rows, p.rows) : 0;
 }
 __host__ __device__ inline int prefix_segs(const Plan& p) { return prefix_tiles_of_rows(p) * p.Hkv; }
-__host__ __device__ inline int own_tiles_of_rows(const Plan& p) {
-    return p.own_cap > 0 ? ceil_div(p.T * p.group, p.rows) : 0;
-}
+__host__ __device__ inline int own_tiles_of_rows(const Plan& p) { return p.own ? ceil_div(p.T * p.group, p.rows) : 0; }
 __host__ __device__ inline long long all_segs(const Plan& p) {
     return prefix_segs(p) + (long long)p.B * own_tiles_of_rows(p) * p.Hkv;
 }
+
+// Rows of row tile rt of `all`, and what one of its key tiles costs.
+__host__ __device__ inline int rows_of(const Plan& p, int all, int rt) {
+    return all - rt * p.rows < p.rows ? all - rt * p.rows : p.rows;
+}
+__host__ __device__ inline int tile_cost(const Plan& p, int rows) { return rows > p.wide ? 2 : 1; }
 
 // Own keys that the last query of row tile rt sees; rows r = t * group + g.
 __host__ __device__ inline int own_seen(const Plan& p, int len, int rt) {
@@ -45,117 +53,175 @@ __host__ __device__ inline int own_seen(const Plan& p, int len, int rt) {
     return n > 0 ? n : 0;
 }
 
-// The block that holds tile x of W.
-__device__ __forceinline__ int block_of(long long x, long long W, int G) { return (int)(((x + 1) * G - 1) / W); }
-
-// A place in the row of tiles, moved along segment by segment. Every thread of a block holds the same.
+// Costs are int32: mq_attn_prefix refuses calls whose total would not fit.
+// A block's run, moved along segment by segment. Every thread of a block holds the same.
 struct Cursor {
-    long long tile, end, total;   // this block's run, all tiles
-    int blocks;                   // that have a run: as many as there are tiles, at most p.G
-    int seg;                      // segment that holds `tile`
+    int at, end;                  // cost before the next tile, where the run ends
+    int per, longer;              // runs are `per` long, the first `longer` of them one more
+    int seg;                      // segment that holds the next tile
     int unit, head;               // its row tile (own segments: sequence * row tiles + row tile) and key head
-    int seg_tiles;                // tiles of the segment
-    int in;                       // tiles of it before `tile`
+    int tiles, cost;              // tiles of the segment, cost of one
+    int in;                       // tiles of it before the next
     bool prefix;
+
+    __device__ __forceinline__ bool more() const { return at < end; }
 };
 
+// The block whose run holds cost x.
+__device__ __forceinline__ int block_of(const Cursor& c, int x) {
+    const int head = c.longer * (c.per + 1);
+    return x < head ? x / (c.per + 1) : c.longer + (x - head) / c.per;
+}
+
 __device__ __forceinline__ int own_len_of(const Plan& p, const int32_t* len, int b) {
-    return min(max(__ldca(len + b), 0), p.own_cap);
+    return p.own_cap > 0 ? min(max(__ldca(len + b), 0), p.own_cap) : 0;
 }
 __device__ __forceinline__ int unit_tiles(const Plan& p, const int32_t* len, int unit, int per_seq) {
     const int b = unit / per_seq;
-    return ceil_div(own_seen(p, own_len_of(p, len, b), unit - b * per_seq), p.keys);
+    return max(p.own_least, ceil_div(p.lead_keys, p.keys) +
+                                ceil_div(own_seen(p, own_len_of(p, len, b), unit - b * per_seq), p.keys));
+}
+__device__ __forceinline__ int unit_cost(const Plan& p, int unit, int per_seq) {
+    return tile_cost(p, rows_of(p, p.T * p.group, unit % per_seq));
+}
+__device__ __forceinline__ int seg_cost(const Plan& p, int tiles, int cost) {
+    return tiles > 0 ? p.extra + tiles * cost : 0;
+}
+// Cost of a segment's tiles before tile i: the first one carries the segment's extra cost.
+__device__ __forceinline__ int cost_before(const Plan& p, int i, int cost) { return i > 0 ? p.extra + i * cost : 0; }
+// The first tile that begins at cost x of its segment or after.
+__device__ __forceinline__ int tile_at(const Plan& p, int x, int cost) {   // cost: 1 or 2
+    if (x <= 0) return 0;
+    return max(1, (x - p.extra + cost - 1) >> (cost - 1));
+}
+
+// Tiles of the segment that belong to this run, from c.in on.
+__device__ __forceinline__ int piece_tiles(const Plan& p, const Cursor& c) {
+    const int base = c.at - cost_before(p, c.in, c.cost);   // cost before the segment
+    return min(c.tiles, tile_at(p, c.end - base, c.cost)) - c.in;
+}
+// First and last block of the segment that c is at the start of.
+__device__ __forceinline__ int2 blocks_of(const Plan& p, const Cursor& c) {
+    return make_int2(blockIdx.x, block_of(c, c.at + cost_before(p, c.tiles - 1, c.cost)));
 }
 
 // Finds the block's run. Segments follow one another as unit, then head. Threads share the
-// units (sequence and row tile) and scan the sums of their tiles: THREADS threads, all of the block.
+// units (sequence and row tile) and scan the sums of their costs: THREADS threads, all of the block.
 template <int THREADS>
 __device__ __forceinline__ Cursor find_run(const Plan& p, const int32_t* len) {
     constexpr int kWarps = THREADS / 32;
-    __shared__ long long s_sum[kWarps];
-    __shared__ long long s_at[2];   // unit, tiles before it
+    __shared__ int s_sum[kWarps];
+    __shared__ int s_at[2];         // unit, cost before it
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     const int per_seq = own_tiles_of_rows(p), units = p.B * per_seq;
     const int share = ceil_div(units, THREADS);
     const int u0 = min(tid * share, units), u1 = min(u0 + share, units);
-    long long sum = 0;
-    for (int u = u0; u < u1; ++u) sum += unit_tiles(p, len, u, per_seq);
-    long long upto = sum;           // tiles of this thread's units and of those before
+    auto cost_of = [&](int u) { return seg_cost(p, unit_tiles(p, len, u, per_seq), unit_cost(p, u, per_seq)); };
+    int sum = 0;
+#pragma unroll 1
+    for (int u = u0; u < u1; ++u) sum += cost_of(u);
+    int upto = sum;                 // cost (of one head) of this thread's units and of those before
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long t = __shfl_up_sync(0xffffffffu, upto, o);
+        const int t = __shfl_up_sync(0xffffffffu, upto, o);
         if (lane >= o) upto += t;
     }
     if (lane == 31) s_sum[wid] = upto;
     __syncthreads();
-    long long own = 0;
+    int own = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
         if (w < wid) upto += s_sum[w];
         own += s_sum[w];
     }
-    const int pt = p.prefix_keys > 0 ? ceil_div(p.prefix_keys, p.keys) : 0;
-    const long long prefix = (long long)prefix_segs(p) * pt;
+    // all row tiles of the prefix are full but the last
+    const int pt = ceil_div(p.prefix_keys, p.keys), prt = prefix_tiles_of_rows(p);
+    const int last_cost = prt > 0 ? tile_cost(p, rows_of(p, p.prefix_rows, prt - 1)) : 0;
+    const int full_cost = tile_cost(p, p.rows);
+    const int full = seg_cost(p, pt, full_cost) * p.Hkv, last = prt > 0 ? seg_cost(p, pt, last_cost) * p.Hkv : 0;
+    const int prefix = prt > 0 ? full * (prt - 1) + last : 0;
     Cursor c;
-    c.total = prefix + own * p.Hkv;
-    // no block in between is without a tile: a segment's pieces are those of consecutive blocks
-    c.blocks = c.total < p.G ? (int)c.total : p.G;
-    c.tile = c.end = 0;
-    if (blockIdx.x >= c.blocks) return c;
-    c.tile = c.total * blockIdx.x / c.blocks;
-    c.end = c.total * (blockIdx.x + 1) / c.blocks;
-    if (c.tile < prefix) {
+    const int total = prefix + own * p.Hkv;
+    // every run is at least as long as the longest way between two tiles' beginnings, so none is without a
+    // tile: a segment's pieces are those of consecutive blocks
+    const int most = total / (p.extra + full_cost);
+    const int blocks = most < 1 ? (total > 0) : min(most, p.G), i = blockIdx.x;
+    c.at = c.end = 0;
+    if (i >= blocks) return c;
+    c.per = total / blocks;
+    c.longer = total - c.per * blocks;
+    const int begin = i * c.per + min(i, c.longer);
+    c.end = begin + c.per + (i < c.longer);
+    int base;                      // cost before the segment
+    if (begin < prefix) {
         c.prefix = true;
-        c.seg = (int)(c.tile / pt);
-        c.in = (int)(c.tile - (long long)c.seg * pt);
-        c.unit = c.seg / p.Hkv;
-        c.head = c.seg - c.unit * p.Hkv;
-        c.seg_tiles = pt;
-        return c;
-    }
-    const long long x = c.tile - prefix;
-    const long long mine = upto * p.Hkv, before = mine - sum * p.Hkv;
-    if (x >= before && x < mine) {
-        long long at = before;
-        for (int u = u0; u < u1; ++u) {
-            const long long n = (long long)unit_tiles(p, len, u, per_seq) * p.Hkv;
-            if (x < at + n) {
-                s_at[0] = u;
-                s_at[1] = at;
-                break;
+        c.unit = min(prt - 1, full > 0 ? begin / full : 0);
+        c.cost = c.unit < prt - 1 ? full_cost : last_cost;
+        c.tiles = pt;
+        const int one = seg_cost(p, pt, c.cost);
+        c.head = (begin - c.unit * full) / one;
+        c.seg = c.unit * p.Hkv + c.head;
+        base = c.unit * full + c.head * one;
+    } else {
+        const int x = begin - prefix;
+        const int mine = upto * p.Hkv, before = mine - sum * p.Hkv;
+        if (x >= before && x < mine) {
+            int at = before;
+#pragma unroll 1
+            for (int u = u0; u < u1; ++u) {
+                const int n = cost_of(u) * p.Hkv;
+                if (x < at + n) {
+                    s_at[0] = u;
+                    s_at[1] = at;
+                    break;
+                }
+                at += n;
             }
-            at += n;
         }
+        __syncthreads();
+        c.prefix = false;
+        c.unit = s_at[0];
+        c.tiles = unit_tiles(p, len, c.unit, per_seq);
+        c.cost = unit_cost(p, c.unit, per_seq);
+        const int one = seg_cost(p, c.tiles, c.cost);
+        c.head = (x - s_at[1]) / one;
+        c.seg = prefix_segs(p) + c.unit * p.Hkv + c.head;
+        base = prefix + s_at[1] + c.head * one;
     }
-    __syncthreads();
-    c.prefix = false;
-    c.unit = (int)s_at[0];
-    c.seg_tiles = unit_tiles(p, len, c.unit, per_seq);
-    const int rest = (int)(x - s_at[1]);
-    c.head = rest / c.seg_tiles;
-    c.in = rest - c.head * c.seg_tiles;
-    c.seg = prefix_segs(p) + c.unit * p.Hkv + c.head;
+    // the run's first tile is the first that begins in it, perhaps the next segment's
+    c.in = tile_at(p, begin - base, c.cost);
+    c.at = base + (c.in < c.tiles ? cost_before(p, c.in, c.cost) : seg_cost(p, c.tiles, c.cost));
     return c;
 }
 
-// To the next segment that has tiles, once `tile` has reached the end of this one.
-__device__ __forceinline__ void next_segment(const Plan& p, const int32_t* len, Cursor& c) {
+// Past `n` tiles; at a segment's end to the next one that has tiles, if the run goes on.
+__device__ __forceinline__ void advance(const Plan& p, const int32_t* len, Cursor& c, int n) {
+    if (n > 0) {
+        const int base = c.at - cost_before(p, c.in, c.cost);
+        c.in += n;
+        c.at = base + (c.in < c.tiles ? cost_before(p, c.in, c.cost) : seg_cost(p, c.tiles, c.cost));
+    }
+    if (c.in < c.tiles || !c.more()) return;
     c.in = 0;
     ++c.seg;
     if (++c.head < p.Hkv) return;
     c.head = 0;
     ++c.unit;
+    const int per_seq = own_tiles_of_rows(p);
     if (c.prefix) {
-        if (c.unit < prefix_tiles_of_rows(p)) return;
+        if (c.unit < prefix_tiles_of_rows(p)) {
+            c.cost = tile_cost(p, rows_of(p, p.prefix_rows, c.unit));
+            return;
+        }
         c.prefix = false;
         c.unit = 0;
     }
-    const int per_seq = own_tiles_of_rows(p);
-    // some unit further on has tiles: this block's run is not at its end
-    while ((c.seg_tiles = unit_tiles(p, len, c.unit, per_seq)) == 0) {
+    // some unit further on has tiles: the run is not at its end
+    while ((c.tiles = unit_tiles(p, len, c.unit, per_seq)) == 0) {
         ++c.unit;
         c.seg += p.Hkv;
     }
+    c.cost = unit_cost(p, c.unit, per_seq);
 }
 
 // Pieces in the workspace. info[segment] = first and last block that hold tiles of it, written by
@@ -165,6 +231,15 @@ struct Pieces {
     float2* ml;    // [place][rows]: maximum (of the scaled products, base 2) and sum
     int2* info;
 };
+
+// Where finished rows go.
+struct Out {
+    void* out;     // [B T][Hq][D]
+    float* lse;    // [B T][Hq], natural, or nullptr
+    int f32;       // out holds f32, not the caches' type
+};
+
+constexpr float kLn2 = 0.6931471805599453f;
 
 // Lets `kern` use `bytes` of dynamic shared memory (asked once per kernel and device).
 bool allow_smem(const void* kern, int bytes);

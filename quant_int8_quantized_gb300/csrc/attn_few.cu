@@ -81,8 +81,9 @@ __global__ void __launch_bounds__(kThreads) attn_few_kernel(const FewArgs a) {
     const uint32_t ring = tc::smem_u32(s_ring) + wid * (C::kStages * C::kStageBytes);
     const int g = lane >> 2, t2 = (lane & 3) * 2;   // this thread's rows g, g + 8 and columns t2, t2 + 1
 
-    while (c.tile < c.end) {
-        const int nt = (int)min((long long)(c.seg_tiles - c.in), c.end - c.tile);
+    advance(p, a.len, c, 0);
+    while (c.more()) {
+        const int nt = piece_tiles(p, c);
         const int key0 = c.in * kTile;
         // the segment's rows and keys
         const int per_seq = own_tiles_of_rows(p);
@@ -95,7 +96,7 @@ __global__ void __launch_bounds__(kThreads) attn_few_kernel(const FewArgs a) {
         const T* K = static_cast<const T*>(c.prefix ? a.pk : a.ok) + base;
         const T* V = static_cast<const T*>(c.prefix ? a.pv : a.ov) + base;
         if (tid == 0 && c.in == 0)
-            a.out.info[c.seg] = make_int2(blockIdx.x, block_of(c.tile + c.seg_tiles - 1, c.total, c.blocks));
+            a.out.info[c.seg] = blocks_of(p, c);
 
         auto copy = [&](int t) {   // tile t of the piece into its stage
             if (t < nt) {
@@ -255,8 +256,7 @@ __global__ void __launch_bounds__(kThreads) attn_few_kernel(const FewArgs a) {
             a.out.ml[place * kFewRows + tid] = make_float2(mm, ll);
         }
         __syncthreads();   // s_ml and the ring are free again
-        c.tile += nt;
-        if (c.tile < c.end) next_segment(p, a.len, c);
+        advance(p, a.len, c, nt);
     }
 }
 

@@ -9,7 +9,7 @@
 // descriptor of the transposed kind).
 //
 // The halves take turns: while one half's threads work on their tile, the tensor cores do the other half's
-// products. The maximum that the exponents are taken against is renewed only when a row passes it by 2^8
+// products. A segment of at most 128 rows gives both halves the same rows and every other tile. The maximum that the exponents are taken against is renewed only when a row passes it by 2^8
 // (the sums are the same in any scale, and 2^8 does not bring a 16-bit value near its end), so O in
 // tensor memory is hardly ever scaled again.
 //
@@ -41,7 +41,7 @@ constexpr uint64_t kWaitLimitNs = MQ_WAIT_LIMIT_NS;
 constexpr int kThreads = 384;
 // Registers a thread: what the launch gives to 384 threads, and after sharing out again (2 x 208 + 88 = 3 x 168).
 constexpr int kLaunchRegs = 168, kRowRegs = 208, kOtherRegs = 88;
-constexpr int kHalf = 128;
+constexpr int kHalf = kManyHalf;
 constexpr int kKeys = kManyKeys;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kGrow = 8.0f;           // powers of two by which a row may pass its maximum
@@ -58,7 +58,9 @@ struct Cfg {
 struct Bars {
     uint64_t full[10], empty[10];
     uint64_t q_ready[2], s_full[2], p_ready[2], pv_done[2];
+    uint64_t twin_full[4], twin_free[4];   // per quarter: half 1's rows of a twin segment are there / were taken
     uint64_t drained;
+    float2 twin_ml[kHalf];
     uint32_t tmem;
     int abort;
 };
@@ -95,30 +97,49 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const void* map, int x, i
         : "memory");
 }
 
-// 128-byte swizzle, the other axis contiguous: rows of 64 elements (128 bytes) are steps of the product's K axis;
-// 8 rows are an atom of 1024 bytes, `lbo` bytes lie between chunks of 64 elements.
-__device__ __forceinline__ uint64_t smem_desc_sw128_mn(uint32_t saddr, uint32_t lbo) {
-    uint64_t d = 0;
-    d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
-    d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
-    d |= (uint64_t)(1024 >> 4) << 32;
-    d |= (uint64_t)1 << 46;
-    d |= (uint64_t)2 << 61;
-    return d;
+// Matrix descriptors of 128-byte-swizzled tiles: the low word holds the address and the distance of 64-element
+// chunks, the high word is the same for all of them (atoms of 8 rows, 1024 bytes apart).
+//   K-major (Q, K): rows of 64 elements of the product's K axis; chunks are stepped through by address.
+//   the other axis contiguous (V): rows are steps of the product's K axis, `lbo` bytes between chunks of its N axis.
+constexpr uint32_t kDescHigh = (1024u >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t desc_low(uint32_t saddr, uint32_t lbo) { return saddr >> 4 | (lbo >> 4) << 16; }
+
+// A product whose operands are all in uniform registers costs its issue slot and no more; 64-bit descriptors
+// computed for each took longer to issue than the tensor cores to multiply.
+template <bool ACC>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_low, uint32_t b_low, uint32_t idesc) {
+    asm volatile(
+        "{ .reg .pred p; .reg .b64 da, db; mov.b64 da, {%1, %4}; mov.b64 db, {%2, %4}; setp.ne.b32 p, %5, 0;"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p; }" ::"r"(d),
+        "r"(a_low), "r"(b_low), "r"(idesc), "r"(kDescHigh), "n"(ACC ? 1 : 0)
+        : "memory");
 }
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_low, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{ .reg .pred p; .reg .b64 db; mov.b64 db, {%2, %4}; setp.ne.b32 p, %5, 0;"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p; }" ::"r"(d),
+        "r"(a_tmem), "r"(b_low), "r"(idesc), "r"(kDescHigh), "r"(acc)
+        : "memory");
+}
+// The same in every lane, and known to be.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 // What a role keeps of the segment that its cursor is in.
 struct Seg {
-    int b, r0, rows, len, halves;
+    int b, r0, rows, len;
+    int lead;        // tiles of the shared prefix at its head (own segments)
+    bool twin;       // both halves hold the same rows, half h the tiles of its parity
 };
 __device__ __forceinline__ Seg segment_of(const Plan& p, const int32_t* len, const Cursor& c) {
     Seg s;
     const int per_seq = own_tiles_of_rows(p);
     s.b = c.prefix ? 0 : c.unit / per_seq;
-    s.r0 = (c.prefix ? c.unit : c.unit - s.b * per_seq) * kManyRows;
-    s.rows = min(kManyRows, (c.prefix ? p.prefix_rows : p.T * p.group) - s.r0);
+    const int rt = c.prefix ? c.unit : c.unit - s.b * per_seq;
+    s.r0 = rt * kManyRows;
+    s.rows = rows_of(p, c.prefix ? p.prefix_rows : p.T * p.group, rt);
     s.len = c.prefix ? p.prefix_keys : own_len_of(p, len, s.b);
-    s.halves = s.rows > kHalf ? 2 : 1;
+    s.lead = c.prefix ? 0 : ceil_div(p.lead_keys, kKeys);
+    s.twin = s.rows <= kHalf;
     return s;
 }
 
@@ -143,10 +164,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::mbar_init(&bars.empty[i], 1);
         }
         for (int h = 0; h < 2; ++h) {
-            tc::mbar_init(&bars.q_ready[h], kHalf);
+            tc::mbar_init(&bars.q_ready[h], 4);    // a warp each
             tc::mbar_init(&bars.s_full[h], 1);
-            tc::mbar_init(&bars.p_ready[h], kHalf);
+            tc::mbar_init(&bars.p_ready[h], 4);
             tc::mbar_init(&bars.pv_done[h], 1);
+        }
+        for (int i = 0; i < 4; ++i) {
+            tc::mbar_init(&bars.twin_full[i], 1);
+            tc::mbar_init(&bars.twin_free[i], 1);
         }
         tc::mbar_init(&bars.drained, 1);
         bars.abort = 0;
@@ -166,253 +191,368 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::tc_fence_after();
     const uint32_t tmem = bars.tmem;
 
+    advance(p, a.len, c, 0);
+
     if (wid < 8) {
         tc::setmaxnreg_inc<kRowRegs>();
         // ---------------------------------------------------------------- rows: a thread each
-        const int h = wid >> 2, row = (wid & 3) * 32 + lane;
-        const uint32_t lane_base = tmem + ((uint32_t)(wid & 3) * 32 << 16);
+        const int h = wid >> 2, quarter = wid & 3, row = quarter * 32 + lane;
+        const uint32_t lane_base = tmem + ((uint32_t)quarter * 32 << 16);
         const uint32_t s_col = lane_base + h * 128, o_col = lane_base + 256 + h * 128;
-        uint32_t s_phase = 0, pv_phase = 0;
+        // The warp's rows of its half of Q; at a segment's end the same memory turns outputs into whole rows.
+        // A row is 128 bytes in each chunk, its 16-byte units at unit ^ (row % 8), as TMA would lay it.
+        uint8_t* s_rows = s_q + h * C::kTileBytes + quarter * 32 * 128;
+        auto unit_of = [&](int r, int u) {   // unit u of row r of the warp
+            return reinterpret_cast<uint4*>(s_rows + (u / 8) * C::kChunkBytes + r * 128 + (((u & 7) ^ (r & 7)) << 4));
+        };
+        constexpr int kUnits = D / 8, kRowsAtOnce = 32 / kUnits;   // lanes side by side take a row
+        const int my_unit = lane % kUnits, my_row = lane / kUnits;
+        uint32_t s_phase = 0, pv_phase = 0, twin_phase = 0;
         bool alive = true;
-        while (alive && c.tile < c.end) {
-            const int nt = (int)min((long long)(c.seg_tiles - c.in), c.end - c.tile);
+        int4 split = make_int4(-1, 0, 0, 0);
+        while (alive && c.more()) {
+            const int nt = piece_tiles(p, c);
             const Seg g = segment_of(p, a.len, c);
-            if (tid == 0 && c.in == 0)
-                a.out.info[c.seg] = make_int2(blockIdx.x, block_of(c.tile + c.seg_tiles - 1, c.total, c.blocks));
-            const bool mine = h < g.halves;
-            const int r = g.r0 + h * kHalf + row;            // row of the segment's row space
-            const bool live = h * kHalf + row < g.rows;
-            // the row of Q into shared memory, as TMA would lay it (16-byte units xor row % 8)
-            if (mine) {
-                const int q_row = r / p.group, q_in = r - q_row * p.group;   // b T + t (own: t), head in the group
-                const uint4* q = reinterpret_cast<const uint4*>(
-                    static_cast<const T*>(a.q) +
-                    (live ? ((long long)q_row + (c.prefix ? 0 : (long long)g.b * p.T)) * a.q_stride +
-                                (long long)(c.head * p.group + q_in) * D
-                          : 0));
-                uint8_t* dst = s_q + h * C::kTileBytes + row * 128;
+            const bool first = c.in == 0, whole = first && nt == c.tiles;
+            if (first && tid == 0) {
+                const int2 f = blocks_of(p, c);
+                a.out.info[c.seg] = f;
+                if (!whole) split = make_int4(c.seg, f.y, c.unit, c.head);
+            }
+            const int half0 = g.twin ? 0 : h * kHalf;            // rows of the segment before this half's
+            const int r_base = g.r0 + half0 + quarter * 32;      // the warp's first row, in the row space of its part
+            const int bt0 = c.prefix ? 0 : g.b * p.T;
+            const int n_rows = g.rows - half0 - quarter * 32;    // rows of the warp (others are zeros)
+            const int r = r_base + lane;                         // this thread's row; its query and head
+            const int q_in = r / p.group;
+            const long long q_row = bt0 + q_in;
+            const int q_head = c.head * p.group + r - q_in * p.group;
+            {
+                const long long off = q_row * a.q_stride + q_head * D;
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
-                    const uint4 x = live ? __ldca(q + i) : make_uint4(0, 0, 0, 0);
-                    *reinterpret_cast<uint4*>(dst + (i / 8) * C::kChunkBytes + (((i & 7) ^ (row & 7)) << 4)) = x;
+                for (int i0 = 0; i0 < kUnits; i0 += 8) {
+                    uint4 x[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int rr = (i0 + i) * kRowsAtOnce + my_row;
+                        const long long from = __shfl_sync(0xffffffffu, off, rr);
+                        x[i] = make_uint4(0, 0, 0, 0);
+                        if (rr < n_rows) x[i] = __ldca(reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + from) + my_unit);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) *unit_of((i0 + i) * kRowsAtOnce + my_row, my_unit) = x[i];
                 }
                 tc::fence_proxy_async_smem();
-                tc::mbar_arrive(&bars.q_ready[h]);
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&bars.q_ready[h]);
             }
-            const int seen = c.prefix ? g.len : g.len - p.T + 1 + r / p.group;
+            const int own_sees = c.prefix ? g.len : g.len - p.T + 1 + q_in;
             float m = -INFINITY, l = 0.0f;                    // base 2, scaled
-            if (mine) {
-                for (int j = 0; j < nt; ++j) {
-                    if (!(alive = wwait(bars, &bars.s_full[h], s_phase))) break;
-                    s_phase ^= 1;
-                    tc::tc_fence_after();
-                    uint32_t s[4][32];
+            const int step = g.twin ? 2 : 1, j0 = g.twin ? h : 0;
+            for (int j = j0; j < nt; j += step) {
+                if (!(alive = wwait(bars, &bars.s_full[h], s_phase))) break;
+                s_phase ^= 1;
+                tc::tc_fence_after();
+                uint32_t s[4][32];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) tc::tmem_ld32(s_col + k * 32, s[k]);
-                    tc::tmem_ld_wait();
-                    const int k0 = (c.in + j) * kKeys;
-                    if (__any_sync(0xffffffffu, k0 + kKeys > seen)) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (k0 + k * 32 + i >= seen) s[k][i] = 0xff800000u;   // -infinity
-                    }
-                    float mx = -INFINITY;
+                for (int k = 0; k < 4; ++k) tc::tmem_ld32(s_col + k * 32, s[k]);
+                tc::tmem_ld_wait();
+                const int tile = c.in + j;
+                const bool lead = tile < g.lead;
+                const int k0 = (lead ? tile : tile - g.lead) * kKeys;
+                const int seen = lead ? p.lead_keys : own_sees;
+                if (__any_sync(0xffffffffu, k0 + kKeys > seen)) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(s[k][i]));
-                    mx *= a.scale_log2;
-                    const bool grew = mx > m + kGrow;          // true for the first key that a row sees
-                    if (j == 0) {
-                        m = mx;
-                    } else if (__any_sync(0xffffffffu, grew)) {
-                        const float now = fmaxf(m, mx);
-                        const float f = now == -INFINITY ? 1.0f : exp2_fast(m - now);
-                        m = now;
-                        l *= f;
-                        // the product before this one must be done with O
-                        if (!(alive = wwait(bars, &bars.pv_done[h], pv_phase ^ 1))) break;
-                        tc::tc_fence_after();
-#pragma unroll
-                        for (int k = 0; k < D / 32; ++k) {
-                            uint32_t o[32];
-                            tc::tmem_ld32(o_col + k * 32, o);
-                            tc::tmem_ld_wait();
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                            tc::tmem_st32(o_col + k * 32, o);
-                        }
-                    }
-                    const float base = m == -INFINITY ? 0.0f : m;
-                    float sum[2] = {0.0f, 0.0f};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        uint32_t pr[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float2 x = f2_fma(make_float2(__uint_as_float(s[k][2 * i]), __uint_as_float(s[k][2 * i + 1])),
-                                                    f2_dup(a.scale_log2), f2_dup(-base));
-                            const float e0 = exp2_fast(x.x), e1 = exp2_fast(x.y);
-                            sum[0] += e0;
-                            sum[1] += e1;
-                            pr[i] = mq_pack2<T>(e0, e1);
-                        }
-                        tc::tmem_st16(s_col + k * 16, pr);
-                    }
-                    l += sum[0] + sum[1];
-                    tc::tmem_st_wait();
-                    tc::tc_fence_before();
-                    tc::mbar_arrive(&bars.p_ready[h]);
-                    pv_phase ^= 1;
+                        for (int i = 0; i < 32; ++i)
+                            if (k0 + k * 32 + i >= seen) s[k][i] = 0xff800000u;   // -infinity
                 }
-                if (alive) alive = wwait(bars, &bars.pv_done[h], pv_phase ^ 1);
-                if (alive) {
+                float mx4[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    mx4[k] = __uint_as_float(s[k][0]);
+#pragma unroll
+                    for (int i = 1; i < 32; ++i) mx4[k] = fmaxf(mx4[k], __uint_as_float(s[k][i]));
+                }
+                const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * a.scale_log2;
+                const bool grew = mx > m + kGrow;          // true for the first key that a row sees
+                if (j == j0) {
+                    m = mx;
+                } else if (__any_sync(0xffffffffu, grew)) {
+                    const float now = fmaxf(m, mx);
+                    const float f = now == -INFINITY ? 1.0f : exp2_fast(m - now);
+                    m = now;
+                    l *= f;
+                    // the product before this one must be done with O
+                    if (!(alive = wwait(bars, &bars.pv_done[h], pv_phase ^ 1))) break;
                     tc::tc_fence_after();
-                    const long long place = (long long)blockIdx.x + c.seg;
-                    const long long at = place * kManyRows + h * kHalf + row;
 #pragma unroll
-                    for (int k = 0; k < D / 32; ++k) {
-                        uint32_t o[32];
-                        tc::tmem_ld32(o_col + k * 32, o);
+                    for (int k = 0; k < D / 16; ++k) {
+                        uint32_t o[16];
+                        tc::tmem_ld16(o_col + k * 16, o);
                         tc::tmem_ld_wait();
-                        if (live) {
-                            float4* to = reinterpret_cast<float4*>(a.out.o + at * D + k * 32);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                to[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
-                                                    __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+                        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                        tc::tmem_st16(o_col + k * 16, o);
+                    }
+                }
+                const float base = m == -INFINITY ? 0.0f : m;
+                float2 sum[2] = {};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t pr[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float2 x = f2_fma(make_float2(__uint_as_float(s[k][2 * i]), __uint_as_float(s[k][2 * i + 1])),
+                                                f2_dup(a.scale_log2), f2_dup(-base));
+                        const float2 e = make_float2(exp2_fast(x.x), exp2_fast(x.y));
+                        sum[i & 1] = f2_add(sum[i & 1], e);
+                        pr[i] = mq_pack2<T>(e.x, e.y);
+                    }
+                    tc::tmem_st16(s_col + k * 16, pr);
+                }
+                sum[0] = f2_add(sum[0], sum[1]);
+                l += sum[0].x + sum[0].y;
+                tc::tmem_st_wait();
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&bars.p_ready[h]);
+                pv_phase ^= 1;
+            }
+            const bool any = j0 < nt;                         // a twin may have no tile
+            if (alive && any) alive = wwait(bars, &bars.pv_done[h], pv_phase ^ 1);
+            // A twin segment's rows are joined by half 0's threads, which reach the other half's output in the same
+            // lanes of tensor memory: f scales the own one, f1 the other.
+            float f = 1.0f, f1 = 0.0f;
+            const bool both = g.twin && nt > 1;
+            if (both && alive) {
+                if (h == 1) {
+                    bars.twin_ml[row] = make_float2(m, l);
+                    tc::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&bars.twin_full[quarter]);
+                    alive = wwait(bars, &bars.twin_free[quarter], twin_phase);
+                } else if ((alive = wwait(bars, &bars.twin_full[quarter], twin_phase))) {
+                    tc::tc_fence_after();
+                    const float2 o = bars.twin_ml[row];
+                    const float mm = fmaxf(m, o.x), mb = mm == -INFINITY ? 0.0f : mm;
+                    f = exp2_fast(m - mb);
+                    f1 = exp2_fast(o.x - mb);
+                    l = l * f + o.y * f1;
+                    m = mm;
+                }
+                twin_phase ^= 1;
+            }
+            if (alive && !(g.twin && h == 1)) {
+                tc::tc_fence_after();
+                const bool finish = a.split && whole;
+                const long long at = ((long long)blockIdx.x + c.seg) * kManyRows + half0 + quarter * 32;
+                if (finish) {
+                    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                    f *= inv;
+                    f1 *= inv;
+                }
+                const long long fin_row = q_row * p.Hq + q_head;
+                auto load = [&](int col, uint32_t (&o)[32]) {   // 32 columns of the rows' outputs, scaled
+                    tc::tmem_ld32(o_col + col, o);
+                    tc::tmem_ld_wait();
+                    if (both) {
+                        uint32_t x[32];
+                        tc::tmem_ld32(o_col + 128 + col, x);
+                        tc::tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            o[i] = __float_as_uint(__uint_as_float(o[i]) * f + __uint_as_float(x[i]) * f1);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                    }
+                };
+                // through shared memory, so that rows go out whole: 16 bits at once, f32 by halves (finished, or as
+                // they are to the piece's place)
+                const bool narrow = finish && !a.fin.f32;
+#pragma unroll 1
+                for (int k = 0; k < (narrow ? 1 : 2); ++k) {
+                    if (narrow) {
+#pragma unroll 1
+                        for (int q = 0; q < D / 32; ++q) {
+                            uint32_t o[32];
+                            load(q * 32, o);
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) {
+                                uint32_t y[4];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    y[i] = mq_pack2<T>(__uint_as_float(o[u * 8 + 2 * i]), __uint_as_float(o[u * 8 + 2 * i + 1]));
+                                *unit_of(lane, q * 4 + u) = make_uint4(y[0], y[1], y[2], y[3]);
+                            }
+                        }
+                    } else {
+#pragma unroll 1
+                        for (int q = 0; q < D / 64; ++q) {
+                            uint32_t o[32];
+                            load(k * (D / 2) + q * 32, o);
+#pragma unroll
+                            for (int u = 0; u < 8; ++u)
+                                *unit_of(lane, q * 8 + u) = make_uint4(o[u * 4], o[u * 4 + 1], o[u * 4 + 2], o[u * 4 + 3]);
                         }
                     }
-                    tc::tc_fence_before();
-                    if (live) a.out.ml[at] = make_float2(m, l);
+                    __syncwarp();
+#pragma unroll 4
+                    for (int i = 0; i < kUnits; ++i) {
+                        const int rr = i * kRowsAtOnce + my_row;
+                        const long long to = __shfl_sync(0xffffffffu, fin_row, rr);
+                        uint4* y = reinterpret_cast<uint4*>(finish ? a.fin.out : a.out.o);
+                        const long long unit = narrow ? to * kUnits : (finish ? to : at + rr) * (2 * kUnits) + k * kUnits;
+                        if (rr < n_rows) y[unit + my_unit] = *unit_of(rr, my_unit);
+                    }
+                    __syncwarp();
+                }
+                tc::tc_fence_before();
+                if (lane < n_rows) {
+                    if (!finish) {
+                        a.out.ml[at + lane] = make_float2(m, l);
+                    } else if (a.fin.lse) {
+                        a.fin.lse[fin_row] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
+                    }
+                }
+                if (both) {
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&bars.twin_free[quarter]);
                 }
             }
-            c.tile += nt;
-            if (c.tile < c.end) next_segment(p, a.len, c);
+            advance(p, a.len, c, nt);
         }
+        if (tid == 0 && a.split) a.split[blockIdx.x] = split;
     } else {
         tc::setmaxnreg_dec<kOtherRegs>();
         if (wid == 8) {
-        // ---------------------------------------------------------------- TMA
-        int slot = 0, issued = 0;
-        uint32_t phase = 0;
-        bool alive = true;
-        while (alive && c.tile < c.end) {
-            const int nt = (int)min((long long)(c.seg_tiles - c.in), c.end - c.tile);
-            const Seg g = segment_of(p, a.len, c);
-            for (int j = 0; alive && j < nt; ++j)
-                for (int kv = 0; kv < 2; ++kv) {
-                    if (!(alive = wwait(bars, &bars.empty[slot], phase ^ 1))) break;
-                    if (tc::elect_one()) {
-                        const CUtensorMap* map = c.prefix ? (kv ? &pv : &pk) : (kv ? &ov : &ok);
-                        tc::mbar_arrive_expect_tx(&bars.full[slot], C::kTileBytes);
+            // ------------------------------------------------------------ TMA: K and V of each tile
+            int slot = 0, issued = 0;
+            uint32_t phase = 0;
+            bool alive = true;
+            while (alive && c.more()) {
+                const int nt = piece_tiles(p, c);
+                const Seg g = segment_of(p, a.len, c);
+                for (int j = 0; alive && j < nt; ++j) {
+                    const int tile = c.in + j;
+                    const bool shared = c.prefix || tile < g.lead;
+                    const int k0 = (c.prefix || shared ? tile : tile - g.lead) * kKeys;
+                    for (int kv = 0; kv < 2; ++kv) {
+                        if (!(alive = wwait(bars, &bars.empty[slot], phase ^ 1))) break;
+                        if (tc::elect_one()) {
+                            const CUtensorMap* map = shared ? (kv ? &pv : &pk) : (kv ? &ov : &ok);
+                            tc::mbar_arrive_expect_tx(&bars.full[slot], C::kTileBytes);
 #pragma unroll
-                        for (int k = 0; k < C::kChunks; ++k)
-                            tma_load_4d(s_ring + slot * C::kTileBytes + k * C::kChunkBytes, map, k * 64, c.head,
-                                        (c.in + j) * kKeys, g.b, &bars.full[slot]);
+                            for (int k = 0; k < C::kChunks; ++k)
+                                tma_load_4d(s_ring + slot * C::kTileBytes + k * C::kChunkBytes, map, k * 64, c.head, k0,
+                                            shared ? 0 : g.b, &bars.full[slot]);
+                        }
+                        __syncwarp();
+                        ++issued;
+                        if (++slot == C::kRing) {
+                            slot = 0;
+                            phase ^= 1;
+                        }
                     }
-                    __syncwarp();
-                    ++issued;
-                    if (++slot == C::kRing) {
-                        slot = 0;
+                }
+                advance(p, a.len, c, nt);
+            }
+            if (!alive) {   // copies in flight must land before the block leaves
+                for (int i = 0; i < C::kRing && i < issued; ++i) {
+                    if (--slot < 0) {
+                        slot = C::kRing - 1;
                         phase ^= 1;
                     }
+                    tc::mbar_wait(&bars.full[slot], phase, kWaitLimitNs);
                 }
-            c.tile += nt;
-            if (c.tile < c.end) next_segment(p, a.len, c);
-        }
-        if (!alive) {   // copies in flight must land before the block leaves
-            for (int i = 0; i < C::kRing && i < issued; ++i) {
-                if (--slot < 0) {
-                    slot = C::kRing - 1;
-                    phase ^= 1;
-                }
-                tc::mbar_wait(&bars.full[slot], phase, kWaitLimitNs);
             }
-        }
         } else if (wid == 9) {
-        // ---------------------------------------------------------------- products
-        constexpr uint32_t fmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
-        const uint32_t idesc_qk = tc::instr_desc(kHalf, kKeys, fmt) | (a.negative ? 1u << 13 : 0u);
-        const uint32_t idesc_pv = tc::instr_desc(kHalf, D, fmt) | 1u << 16;   // V: the N axis contiguous
-        const uint32_t q_addr = tc::smem_u32(s_q), ring = tc::smem_u32(s_ring);
-        int slot = 0;
-        uint32_t phase = 0, q_phase = 0, p_phase = 0;   // q, p: a bit per half
-        bool alive = true;
-        auto next_slot = [&] {
-            if (++slot == C::kRing) {
-                slot = 0;
-                phase ^= 1;
-            }
-        };
-        while (alive && c.tile < c.end) {
-            const int nt = (int)min((long long)(c.seg_tiles - c.in), c.end - c.tile);
-            const Seg g = segment_of(p, a.len, c);
-            for (int h = 0; alive && h < g.halves; ++h) alive = wwait(bars, &bars.q_ready[h], q_phase >> h & 1);
-            if (!alive) break;
-            const uint32_t both = g.halves == 2 ? 3 : 1;
-            q_phase ^= both;
-            auto qk = [&](int h, int k_slot) {
-                if (tc::elect_one()) {
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t off = (k / 4) * C::kChunkBytes + (k % 4) * 32;
-                        tc::mma_f16(tmem + h * 128, tc::smem_desc_sw128(q_addr + h * C::kTileBytes + off),
-                                    tc::smem_desc_sw128(ring + k_slot * C::kTileBytes + off), idesc_qk, k > 0);
-                    }
-                    tc::mma_commit(&bars.s_full[h]);
-                    if (h == g.halves - 1) tc::mma_commit(&bars.empty[k_slot]);
-                }
-                __syncwarp();
+            // ------------------------------------------------------------ products
+            constexpr uint32_t fmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+            const uint32_t idesc_qk = tc::instr_desc(kHalf, kKeys, fmt) | (a.negative ? 1u << 13 : 0u);
+            const uint32_t idesc_pv = tc::instr_desc(kHalf, D, fmt) | 1u << 16;   // V: the N axis contiguous
+            const uint32_t q_addr = tc::smem_u32(s_q), ring = tc::smem_u32(s_ring);
+            int base = 0;                        // ring slot of the piece's first K tile, and the ring's turn
+            uint32_t turn = 0;
+            uint32_t q_phase = 0, p_phase = 0;   // p: a bit per half
+            bool alive = true;
+            // K (or V) of tile t of the piece: its slot, and its phase there
+            auto slot_of = [&](int t, int kv, uint32_t& ph) {
+                const int n = base + 2 * t + kv;
+                ph = (turn + n / C::kRing) & 1;
+                return n % C::kRing;
             };
-            if (!(alive = wwait(bars, &bars.full[slot], phase))) break;
-            tc::tc_fence_after();
-            for (int h = 0; h < g.halves; ++h) qk(h, slot);
-            next_slot();
-            for (int j = 0; alive && j < nt; ++j) {
-                if (!(alive = wwait(bars, &bars.full[slot], phase))) break;
-                const int v_slot = slot;
-                next_slot();
-                const int k0 = (c.in + j) * kKeys;
-                if (k0 + kKeys > g.len && !c.prefix) {
-                    // rows past the length may hold anything: zeros times a probability of zero
-                    for (int i = lane; i < (k0 + kKeys - g.len) * 8; i += 32)
-#pragma unroll
-                        for (int k = 0; k < C::kChunks; ++k)
-                            *reinterpret_cast<uint4*>(s_ring + v_slot * C::kTileBytes + k * C::kChunkBytes +
-                                                      (g.len - k0) * 128 + i * 16) = make_uint4(0, 0, 0, 0);
-                    tc::fence_proxy_async_smem();
-                    __syncwarp();
-                }
-                for (int h = 0; h < g.halves; ++h) {
-                    if (!(alive = wwait(bars, &bars.p_ready[h], p_phase >> h & 1))) break;
+            while (alive && c.more()) {
+                const int nt = piece_tiles(p, c);
+                const Seg g = segment_of(p, a.len, c);
+                // items: a half's next tile, halves in turn
+                const int items = g.twin ? nt : 2 * nt;
+                for (int h = 0; alive && h < 2; ++h) alive = wwait(bars, &bars.q_ready[h], q_phase);
+                if (!alive) break;
+                q_phase ^= 1;
+                auto qk = [&](int i) {
+                    const int h = i & 1;
+                    uint32_t ph;
+                    const int slot = slot_of(g.twin ? i : i >> 1, 0, ph);
+                    if (!(alive = wwait(bars, &bars.full[slot], ph))) return;
                     tc::tc_fence_after();
+                    const uint32_t d = uniform(tmem + h * 128), qa = uniform(desc_low(q_addr + h * C::kTileBytes, 16));
+                    const uint32_t ka = uniform(desc_low(ring + slot * C::kTileBytes, 16));
                     if (tc::elect_one()) {
+                        mma_ss<false>(d, qa, ka, idesc_qk);
 #pragma unroll
-                        for (int k = 0; k < kKeys / 16; ++k)
-                            tc::mma_f16_ts(tmem + 256 + h * 128, tmem + h * 128 + k * 8,
-                                           smem_desc_sw128_mn(ring + v_slot * C::kTileBytes + k * 2048, C::kChunkBytes),
-                                           idesc_pv, j > 0 || k > 0);
-                        tc::mma_commit(&bars.pv_done[h]);
-                        if (h == g.halves - 1) tc::mma_commit(&bars.empty[v_slot]);
+                        for (int k = 1; k < D / 16; ++k) {
+                            const uint32_t off = ((k / 4) * C::kChunkBytes + (k % 4) * 32) >> 4;
+                            mma_ss<true>(d, qa + off, ka + off, idesc_qk);
+                        }
+                        tc::mma_commit(&bars.s_full[h]);
+                        if (g.twin || h == 1) tc::mma_commit(&bars.empty[slot]);
                     }
                     __syncwarp();
-                    if (j + 1 < nt) {
-                        if (h == 0 && !(alive = wwait(bars, &bars.full[slot], phase))) break;
-                        qk(h, slot);
-                        if (h == g.halves - 1) next_slot();
+                };
+                qk(0);
+                if (alive && items > 1) qk(1);
+                for (int i = 0; alive && i < items; ++i) {
+                    const int h = i & 1, t = g.twin ? i : i >> 1;
+                    uint32_t ph;
+                    const int slot = slot_of(t, 1, ph);
+                    if (!(alive = wwait(bars, &bars.full[slot], ph))) break;
+                    const int tile = c.in + t, k0 = (tile - g.lead) * kKeys;
+                    if (!c.prefix && k0 + kKeys > g.len && tile >= g.lead && (g.twin || h == 0)) {
+                        // rows past the length may hold anything: zeros times a probability of zero
+                        for (int u = lane; u < (k0 + kKeys - g.len) * 8; u += 32)
+#pragma unroll
+                            for (int k = 0; k < C::kChunks; ++k)
+                                *reinterpret_cast<uint4*>(s_ring + slot * C::kTileBytes + k * C::kChunkBytes +
+                                                          (g.len - k0) * 128 + u * 16) = make_uint4(0, 0, 0, 0);
+                        tc::fence_proxy_async_smem();
+                        __syncwarp();
                     }
+                    if (!(alive = wwait(bars, &bars.p_ready[h], p_phase >> h & 1))) break;
+                    p_phase ^= 1u << h;
+                    tc::tc_fence_after();
+                    const uint32_t d = uniform(tmem + 256 + h * 128), pa = uniform(tmem + h * 128);
+                    const uint32_t va = uniform(desc_low(ring + slot * C::kTileBytes, C::kChunkBytes));
+                    if (tc::elect_one()) {
+                        mma_ts(d, pa, va, idesc_pv, i > 1);
+#pragma unroll
+                        for (int k = 1; k < kKeys / 16; ++k) mma_ts(d, pa + k * 8, va + (k * 2048 >> 4), idesc_pv, 1);
+                        tc::mma_commit(&bars.pv_done[h]);
+                        if (g.twin || h == 1) tc::mma_commit(&bars.empty[slot]);
+                    }
+                    __syncwarp();
+                    if (i + 2 < items) qk(i + 2);
                 }
-                p_phase ^= both;
+                base += 2 * nt;
+                turn += base / C::kRing;
+                base %= C::kRing;
+                advance(p, a.len, c, nt);
             }
-            c.tile += nt;
-            if (c.tile < c.end) next_segment(p, a.len, c);
-        }
-        if (tc::elect_one()) tc::mma_commit(&bars.drained);
-        __syncwarp();
-        tc::mbar_wait(&bars.drained, 0, kWaitLimitNs);
+            if (tc::elect_one()) tc::mma_commit(&bars.drained);
+            __syncwarp();
+            tc::mbar_wait(&bars.drained, 0, kWaitLimitNs);
         }
     }
     tc::tc_fence_before();

@@ -14,11 +14,16 @@ struct ManyArgs {
     float scale_log2;     // |scale| log2 e, not below 1e-30
     int negative;         // scale < 0
     Pieces out;
+    int4* split;          // [G]: segment that begins in the block and goes on in others (or -1), its last block,
+                          // its row tile (sequence and tile) and key head; nullptr: the call joins by row
+    Out fin;              // with `split`: segments that one block holds are finished here
 };
 
 constexpr int kManyRows = 256;    // query rows per segment
+constexpr int kManyHalf = 128;    // rows of one half
 constexpr int kManyKeys = 128;    // keys per tile
 
+constexpr int kManyExtra = 1;     // what beginning and ending a segment costs, in tiles of one half
 inline bool many_takes(int D) { return D == 64 || D == 128; }
 int launch_many(const ManyArgs& a, const mq_kv* prefix, const mq_kv* own, int D, int type, cudaStream_t stream);
 
