@@ -13,8 +13,8 @@
 // (the sums are the same in any scale, and 2^8 does not bring a 16-bit value near its end), so O in
 // tensor memory is hardly ever scaled again.
 //
-// 384 threads, one block per SM: warps 0-3 and 4-7 the rows of the halves, warp 8 TMA, warp 9 the
-// products; the register file is shared out again to give a row's thread its 128 products. Shared memory: Q (64 KB at D = 128) and a ring of K and V tiles (32 KB each).
+// 384 threads, one block per SM: warps 0-3 and 4-7 the rows of the halves, warp 8 TMA, warps 9
+// and 10 a half's products; the register file is shared out again to give a row's thread its 128 products. Shared memory: Q (64 KB at D = 128) and a ring of K and V tiles (32 KB each).
 // Waits are bounded; a wait that runs out is recorded (mq_device_status), the block drains its own copies
 // and products, frees tensor memory and returns.
 
@@ -59,15 +59,23 @@ struct Bars {
     uint64_t full[10], empty[10];
     uint64_t q_ready[2], s_full[2], p_ready[2], pv_done[2];
     uint64_t twin_full[4], twin_free[4];   // per quarter: half 1's rows of a twin segment are there / were taken
-    uint64_t drained;
+    uint64_t drained[2];
     float2 twin_ml[kHalf];
     uint32_t tmem;
     int abort;
 };
 
+// Non-suspending test of a phase.
+__device__ __forceinline__ bool ready(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                 : "=r"(ok)
+                 : "r"(tc::smem_u32(bar)), "r"(parity)
+                 : "memory");
+    return ok != 0;
+}
 // Whole warp, or any set of threads of one whose outcome need not be uniform with the others.
-__device__ bool wait(Bars& b, uint64_t* bar, uint32_t parity) {
-    if (tc::mbar_try_wait(bar, parity)) return true;
+__device__ bool wait_long(Bars& b, uint64_t* bar, uint32_t parity) {
     const uint64_t t0 = tc::globaltimer();
     for (;;) {
         if (tc::mbar_try_wait(bar, parity)) return true;
@@ -80,7 +88,7 @@ __device__ bool wait(Bars& b, uint64_t* bar, uint32_t parity) {
     }
 }
 __device__ __forceinline__ bool wwait(Bars& b, uint64_t* bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, wait(b, bar, parity));
+    return __all_sync(0xffffffffu, ready(bar, parity) || wait_long(b, bar, parity));
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -161,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < C::kRing; ++i) {
             tc::mbar_init(&bars.full[i], 1);
-            tc::mbar_init(&bars.empty[i], 1);
+            tc::mbar_init(&bars.empty[i], 2);   // a half each
         }
         for (int h = 0; h < 2; ++h) {
             tc::mbar_init(&bars.q_ready[h], 4);    // a warp each
@@ -173,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::mbar_init(&bars.twin_full[i], 1);
             tc::mbar_init(&bars.twin_free[i], 1);
         }
-        tc::mbar_init(&bars.drained, 1);
+        for (int h = 0; h < 2; ++h) tc::mbar_init(&bars.drained[h], 1);
         bars.abort = 0;
         tc::fence_mbar_init();
     }
@@ -468,91 +476,100 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc::mbar_wait(&bars.full[slot], phase, kWaitLimitNs);
                 }
             }
-        } else if (wid == 9) {
-            // ------------------------------------------------------------ products
+        } else if (wid < 11) {
+            // ------------------------------------------------------------ products of half h
+            const int h = wid - 9;
             constexpr uint32_t fmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
             const uint32_t idesc_qk = tc::instr_desc(kHalf, kKeys, fmt) | (a.negative ? 1u << 13 : 0u);
             const uint32_t idesc_pv = tc::instr_desc(kHalf, D, fmt) | 1u << 16;   // V: the N axis contiguous
-            const uint32_t q_addr = tc::smem_u32(s_q), ring = tc::smem_u32(s_ring);
-            int base = 0;                        // ring slot of the piece's first K tile, and the ring's turn
-            uint32_t turn = 0;
-            uint32_t q_phase = 0, p_phase = 0;   // p: a bit per half
+            constexpr uint32_t kTileLow = C::kTileBytes >> 4;
+            const uint32_t ring = tc::smem_u32(s_ring);
+            const uint32_t s_tm = uniform(tmem + h * 128), o_tm = uniform(tmem + 256 + h * 128);
+            const uint32_t q_low = uniform(desc_low(tc::smem_u32(s_q) + h * C::kTileBytes, 16));
+            const uint32_t k_low = uniform(desc_low(ring, 16)), v_low = uniform(desc_low(ring, C::kChunkBytes));
+            int slot = 0;                        // ring slot of the piece's first K tile, and the phase there
+            uint32_t phase = 0, q_phase = 0, p_phase = 0;
             bool alive = true;
-            // K (or V) of tile t of the piece: its slot, and its phase there
-            auto slot_of = [&](int t, int kv, uint32_t& ph) {
-                const int n = base + 2 * t + kv;
-                ph = (turn + n / C::kRing) & 1;
-                return n % C::kRing;
+            auto step_slots = [&](int n) {       // n < kRing slots on
+                slot += n;
+                if (slot >= C::kRing) {
+                    slot -= C::kRing;
+                    phase ^= 1;
+                }
+            };
+            auto qk = [&](bool twice) {          // S = Q K^T with the K tile in `slot`; one lane
+                const uint32_t kl = k_low + slot * kTileLow;
+                mma_ss<false>(s_tm, q_low, kl, idesc_qk);
+#pragma unroll
+                for (int k = 1; k < D / 16; ++k) {
+                    const uint32_t off = ((k / 4) * C::kChunkBytes + (k % 4) * 32) >> 4;
+                    mma_ss<true>(s_tm, q_low + off, kl + off, idesc_qk);
+                }
+                tc::mma_commit(&bars.s_full[h]);
+                tc::mma_commit(&bars.empty[slot]);
+                if (twice) tc::mma_commit(&bars.empty[slot]);   // the other half does not use the tile
             };
             while (alive && c.more()) {
                 const int nt = piece_tiles(p, c);
                 const Seg g = segment_of(p, a.len, c);
-                // items: a half's next tile, halves in turn
-                const int items = g.twin ? nt : 2 * nt;
-                for (int h = 0; alive && h < 2; ++h) alive = wwait(bars, &bars.q_ready[h], q_phase);
-                if (!alive) break;
+                const int step = g.twin ? 2 : 1;
+                int t = g.twin ? h : 0;
+                if (!(alive = wwait(bars, &bars.q_ready[h], q_phase))) break;
                 q_phase ^= 1;
-                auto qk = [&](int i) {
-                    const int h = i & 1;
-                    uint32_t ph;
-                    const int slot = slot_of(g.twin ? i : i >> 1, 0, ph);
-                    if (!(alive = wwait(bars, &bars.full[slot], ph))) return;
+                if (t > 0) step_slots(2);
+                if (t < nt) {
+                    if (!(alive = wwait(bars, &bars.full[slot], phase))) break;
                     tc::tc_fence_after();
-                    const uint32_t d = uniform(tmem + h * 128), qa = uniform(desc_low(q_addr + h * C::kTileBytes, 16));
-                    const uint32_t ka = uniform(desc_low(ring + slot * C::kTileBytes, 16));
-                    if (tc::elect_one()) {
-                        mma_ss<false>(d, qa, ka, idesc_qk);
-#pragma unroll
-                        for (int k = 1; k < D / 16; ++k) {
-                            const uint32_t off = ((k / 4) * C::kChunkBytes + (k % 4) * 32) >> 4;
-                            mma_ss<true>(d, qa + off, ka + off, idesc_qk);
-                        }
-                        tc::mma_commit(&bars.s_full[h]);
-                        if (g.twin || h == 1) tc::mma_commit(&bars.empty[slot]);
-                    }
+                    if (tc::elect_one()) qk(g.twin);
                     __syncwarp();
-                };
-                qk(0);
-                if (alive && items > 1) qk(1);
-                for (int i = 0; alive && i < items; ++i) {
-                    const int h = i & 1, t = g.twin ? i : i >> 1;
-                    uint32_t ph;
-                    const int slot = slot_of(t, 1, ph);
-                    if (!(alive = wwait(bars, &bars.full[slot], ph))) break;
-                    const int tile = c.in + t, k0 = (tile - g.lead) * kKeys;
-                    if (!c.prefix && k0 + kKeys > g.len && tile >= g.lead && (g.twin || h == 0)) {
+                }
+                bool first = true;
+                for (; t < nt; t += step) {
+                    step_slots(1);               // this tile's V
+                    const int v_slot = slot;
+                    if (!(alive = wwait(bars, &bars.full[slot], phase))) break;
+                    const int tile = c.in + t, past = (tile - g.lead + 1) * kKeys - g.len;
+                    if (past > 0 && !c.prefix && tile >= g.lead) {
                         // rows past the length may hold anything: zeros times a probability of zero
-                        for (int u = lane; u < (k0 + kKeys - g.len) * 8; u += 32)
+                        for (int u = lane; u < past * 8; u += 32)
 #pragma unroll
                             for (int k = 0; k < C::kChunks; ++k)
                                 *reinterpret_cast<uint4*>(s_ring + slot * C::kTileBytes + k * C::kChunkBytes +
-                                                          (g.len - k0) * 128 + u * 16) = make_uint4(0, 0, 0, 0);
+                                                          (kKeys - past) * 128 + u * 16) = make_uint4(0, 0, 0, 0);
                         tc::fence_proxy_async_smem();
                         __syncwarp();
                     }
-                    if (!(alive = wwait(bars, &bars.p_ready[h], p_phase >> h & 1))) break;
-                    p_phase ^= 1u << h;
+                    step_slots(g.twin ? 3 : 1);  // the half's next K
+                    const bool more = t + step < nt;
+                    if (more && !(alive = wwait(bars, &bars.full[slot], phase))) break;
+                    if (!(alive = wwait(bars, &bars.p_ready[h], p_phase))) break;
+                    p_phase ^= 1;
                     tc::tc_fence_after();
-                    const uint32_t d = uniform(tmem + 256 + h * 128), pa = uniform(tmem + h * 128);
-                    const uint32_t va = uniform(desc_low(ring + slot * C::kTileBytes, C::kChunkBytes));
                     if (tc::elect_one()) {
-                        mma_ts(d, pa, va, idesc_pv, i > 1);
+                        const uint32_t vl = v_low + v_slot * kTileLow;
+                        mma_ts(o_tm, s_tm, vl, idesc_pv, !first);
 #pragma unroll
-                        for (int k = 1; k < kKeys / 16; ++k) mma_ts(d, pa + k * 8, va + (k * 2048 >> 4), idesc_pv, 1);
+                        for (int k = 1; k < kKeys / 16; ++k) mma_ts(o_tm, s_tm + k * 8, vl + (k * 2048 >> 4), idesc_pv, 1);
                         tc::mma_commit(&bars.pv_done[h]);
-                        if (g.twin || h == 1) tc::mma_commit(&bars.empty[slot]);
+                        tc::mma_commit(&bars.empty[v_slot]);
+                        if (g.twin) tc::mma_commit(&bars.empty[v_slot]);
+                        if (more) qk(g.twin);
                     }
                     __syncwarp();
-                    if (i + 2 < items) qk(i + 2);
+                    first = false;
                 }
-                base += 2 * nt;
-                turn += base / C::kRing;
-                base %= C::kRing;
+                if (!alive) break;
+                // t stands at the half's first tile past the piece, `slot` at that tile's K: back to the piece's end
+                for (int n = 2 * (t - nt); n > 0; --n)
+                    if (--slot < 0) {
+                        slot = C::kRing - 1;
+                        phase ^= 1;
+                    }
                 advance(p, a.len, c, nt);
             }
-            if (tc::elect_one()) tc::mma_commit(&bars.drained);
+            if (tc::elect_one()) tc::mma_commit(&bars.drained[h]);
             __syncwarp();
-            tc::mbar_wait(&bars.drained, 0, kWaitLimitNs);
+            tc::mbar_wait(&bars.drained[h], 0, kWaitLimitNs);
         }
     }
     tc::tc_fence_before();
