@@ -160,11 +160,11 @@ __global__ void __launch_bounds__(256) attn_join_split_kernel(const SplitArgs a)
     mq_grid_wait();
     const int4 s = __ldca(a.split + blockIdx.x);
     if (s.x < 0) return;
-    const int per_seq = own_tiles_of_rows(a.plan), b = s.z / per_seq, rt = s.z - b * per_seq;
+    const int per_seq = own_tiles_of_rows(a.plan), b = a.plan.by_per_seq.of(s.z), rt = s.z - b * per_seq;
     const int rows = rows_of(a.plan, a.plan.T * a.plan.group, rt);
     const int in = blockIdx.y * 8 + (threadIdx.x >> 5);
     if (in >= rows) return;
-    const int r = rt * a.plan.rows + in, t = r / a.plan.group;
+    const int r = rt * a.plan.rows + in, t = a.plan.by_group.of(r);
     const Run runs[1] = {run_of(a.part, s.x, make_int2(blockIdx.x, s.y), in)};
     join_row<O, D>(runs, a.fin, nullptr,
                    ((long long)b * a.plan.T + t) * a.plan.Hq + s.w * a.plan.group + r - t * a.plan.group);
@@ -212,8 +212,8 @@ Cut cut_of(int B, int T, int Hq, int Hkv, int D, int prefix_keys, int own_cap, b
     Cut c;
     const int group = Hq / Hkv;
     // the weights' raw products come from the kernel for few rows
-    c.own_many = own_cap > 0 && many_takes(D) && !scores && (long long)T * group >= kOwnMany;
-    c.prefix_many = prefix_keys > 0 && !c.own_many && many_takes(D) && (long long)B * T * group >= kPrefixMany;
+    c.own_many = own_cap > 0 && many_takes(D, group) && !scores && (long long)T * group >= kOwnMany;
+    c.prefix_many = prefix_keys > 0 && !c.own_many && many_takes(D, group) && (long long)B * T * group >= kPrefixMany;
     c.fits = true;
     size_t at = 0;
     auto plan = [&](bool many, size_t* o, size_t* ml, size_t* info) {
@@ -229,10 +229,12 @@ Cut cut_of(int B, int T, int Hq, int Hkv, int D, int prefix_keys, int own_cap, b
         p.own = c.own_many == many && own_cap > 0;
         p.own_least = many ? 1 : 0;
         p.own_cap = p.own ? own_cap : 0;
-        p.rows = many ? kManyRows : kFewRows;
+        p.rows = many ? many_rows(group) : kFewRows;
         p.keys = many ? kManyKeys : few_tile_keys(D);
         p.wide = many ? kManyHalf : kFewRows;
         p.extra = many ? kManyExtra : 0;
+        p.by_group = div_by(group);
+        p.by_per_seq = div_by(p.own ? own_tiles_of_rows(p) : 1);
         const long long segs = all_segs(p);
         const long long most = (long long)prefix_segs(p) * ceil_div(p.prefix_keys, p.keys) +
                                (segs - prefix_segs(p)) * (ceil_div(p.lead_keys, p.keys) + ceil_div(p.own_cap, p.keys));
@@ -334,8 +336,8 @@ extern "C" int mq_attn_prefix(const void* q, long long q_stride, int B, int T, i
         rc = launch_many(m, P > 0 ? prefix : nullptr, c.own_many ? own : nullptr, D, type, stream);
         if (rc != MQ_OK) return rc;
         if (c.own_many) {
-            const SplitArgs s = {{many, kManyRows}, m.split, c.many, fin};
-            const int most = T * (Hq / Hkv) < kManyRows ? T * (Hq / Hkv) : kManyRows;
+            const SplitArgs s = {{many, c.many.rows}, m.split, c.many, fin};
+            const int most = T * (Hq / Hkv) < c.many.rows ? T * (Hq / Hkv) : c.many.rows;
             auto join = [&](auto o) {
                 using O = decltype(o);
                 return mq::launch_pdl(D == 64 ? attn_join_split_kernel<O, 64> : attn_join_split_kernel<O, 128>,
@@ -368,7 +370,7 @@ extern "C" int mq_attn_prefix(const void* q, long long q_stride, int B, int T, i
         if (rc != MQ_OK) return rc;
     }
     JoinArgs j;
-    j.prefix = {c.prefix_many ? many : few, P > 0 ? (c.prefix_many ? kManyRows : kFewRows) : 0};
+    j.prefix = {c.prefix_many ? many : few, P > 0 ? (c.prefix_many ? c.many.rows : kFewRows) : 0};
     j.own = {few, cap > 0 ? kFewRows : 0};
     j.len = own_len;
     j.B = B;

@@ -14,6 +14,19 @@
 
 namespace attn {
 
+// n / d for 0 <= n < 2^31 by a multiplication: l = ceil(log2 d), mul = floor(2^(31 + l) / d) + 1 < 2^32 + 1,
+// n / d = n mul >> (31 + l), since mul d exceeds 2^(31 + l) by at most d <= 2^l.
+struct Div {
+    uint32_t mul;
+    int shift, d;
+    __device__ __forceinline__ int of(int n) const { return (int)(((unsigned long long)(uint32_t)n * mul) >> shift); }
+};
+inline Div div_by(int d) {
+    int l = 0;
+    while ((1LL << l) < d) ++l;
+    return Div{(uint32_t)(((1ULL << (31 + l)) / (uint32_t)d) + 1), 31 + l, d};
+}
+
 // The numbers of one schedule. G: blocks.
 struct Plan {
     int B, T, Hq, Hkv, group;       // group = Hq / Hkv
@@ -25,6 +38,7 @@ struct Plan {
     int rows;                       // query rows per segment
     int keys;                       // keys per tile
     int G;
+    Div by_group, by_per_seq;       // by group; by the row tiles of a sequence (1 where there are none)
     int wide, extra;                // cost of a tile with more than `wide` rows is 2, else 1; `extra` once a segment
 };
 
@@ -47,10 +61,9 @@ __host__ __device__ inline int rows_of(const Plan& p, int all, int rt) {
 __host__ __device__ inline int tile_cost(const Plan& p, int rows) { return rows > p.wide ? 2 : 1; }
 
 // Own keys that the last query of row tile rt sees; rows r = t * group + g.
-__host__ __device__ inline int own_seen(const Plan& p, int len, int rt) {
-    const int last = (rt + 1) * p.rows < p.T * p.group ? (rt + 1) * p.rows - 1 : p.T * p.group - 1;
-    const int n = len - p.T + 1 + last / p.group;
-    return n > 0 ? n : 0;
+__device__ __forceinline__ int own_seen(const Plan& p, int len, int rt) {
+    const int last = min((rt + 1) * p.rows, p.T * p.group) - 1;
+    return max(0, len - p.T + 1 + p.by_group.of(last));
 }
 
 // Costs are int32: mq_attn_prefix refuses calls whose total would not fit.
@@ -77,12 +90,12 @@ __device__ __forceinline__ int own_len_of(const Plan& p, const int32_t* len, int
     return p.own_cap > 0 ? min(max(__ldca(len + b), 0), p.own_cap) : 0;
 }
 __device__ __forceinline__ int unit_tiles(const Plan& p, const int32_t* len, int unit, int per_seq) {
-    const int b = unit / per_seq;
+    const int b = p.by_per_seq.of(unit);
     return max(p.own_least, ceil_div(p.lead_keys, p.keys) +
                                 ceil_div(own_seen(p, own_len_of(p, len, b), unit - b * per_seq), p.keys));
 }
 __device__ __forceinline__ int unit_cost(const Plan& p, int unit, int per_seq) {
-    return tile_cost(p, rows_of(p, p.T * p.group, unit % per_seq));
+    return tile_cost(p, rows_of(p, p.T * p.group, unit - p.by_per_seq.of(unit) * per_seq));
 }
 __device__ __forceinline__ int seg_cost(const Plan& p, int tiles, int cost) {
     return tiles > 0 ? p.extra + tiles * cost : 0;
@@ -111,7 +124,7 @@ template <int THREADS>
 __device__ __forceinline__ Cursor find_run(const Plan& p, const int32_t* len) {
     constexpr int kWarps = THREADS / 32;
     __shared__ int s_sum[kWarps];
-    __shared__ int s_at[2];         // unit, cost before it
+    __shared__ int s_at[3];         // unit, cost before it, its tiles
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     const int per_seq = own_tiles_of_rows(p), units = p.B * per_seq;
     const int share = ceil_div(units, THREADS);
@@ -173,6 +186,7 @@ __device__ __forceinline__ Cursor find_run(const Plan& p, const int32_t* len) {
                 if (x < at + n) {
                     s_at[0] = u;
                     s_at[1] = at;
+                    s_at[2] = unit_tiles(p, len, u, per_seq);
                     break;
                 }
                 at += n;
@@ -181,7 +195,7 @@ __device__ __forceinline__ Cursor find_run(const Plan& p, const int32_t* len) {
         __syncthreads();
         c.prefix = false;
         c.unit = s_at[0];
-        c.tiles = unit_tiles(p, len, c.unit, per_seq);
+        c.tiles = s_at[2];
         c.cost = unit_cost(p, c.unit, per_seq);
         const int one = seg_cost(p, c.tiles, c.cost);
         c.head = (x - s_at[1]) / one;

@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(kThreads) attn_few_kernel(const FewArgs a) {
         const int key0 = c.in * kTile;
         // the segment's rows and keys
         const int per_seq = own_tiles_of_rows(p);
-        const int b = c.prefix ? 0 : c.unit / per_seq;
+        const int b = c.prefix ? 0 : p.by_per_seq.of(c.unit);
         const int r0 = (c.prefix ? c.unit : c.unit - b * per_seq) * kFewRows;
         const int nrows = min(kFewRows, (c.prefix ? p.prefix_rows : tg) - r0);
         const int len = c.prefix ? p.prefix_keys : own_len_of(p, a.len, b);
@@ -123,11 +123,10 @@ __global__ void __launch_bounds__(kThreads) attn_few_kernel(const FewArgs a) {
         for (int u = 0; u < 2; ++u) {
             const int r = r0 + g + 8 * u;
             const bool live = g + 8 * u < nrows;
-            const int rb = c.prefix ? r / tg : b, rr = c.prefix ? r - rb * tg : r;
-            const int t = rr / p.group, h = c.head * p.group + rr - t * p.group;
+            const int t = p.by_group.of(r), h = c.head * p.group + r - t * p.group;   // prefix: t is b T + t
             seen[u] = c.prefix ? len : len - p.T + 1 + t;
             const uint32_t* q = reinterpret_cast<const uint32_t*>(static_cast<const T*>(a.q) +
-                                                                  (live ? ((long long)rb * p.T + t) * a.q_stride + h * D : 0));
+                                                                  (live ? ((long long)b * p.T + t) * a.q_stride + h * D : 0));
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
                 qf[k][u] = live ? __ldca(q + (k * 16 + t2) / 2) : 0u;

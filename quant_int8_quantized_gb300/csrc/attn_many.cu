@@ -13,8 +13,12 @@
 // (the sums are the same in any scale, and 2^8 does not bring a 16-bit value near its end), so O in
 // tensor memory is hardly ever scaled again.
 //
-// 384 threads, one block per SM: warps 0-3 and 4-7 the rows of the halves, warp 8 TMA, warps 9
-// and 10 a half's products; the register file is shared out again to give a row's thread its 128 products. Shared memory: Q (64 KB at D = 128) and a ring of K and V tiles (32 KB each).
+// 384 threads, one block per SM: warps 0-3 and 4-7 the rows of the halves, warp 8 copies (TMA), warps 9 and 10 a
+// half's products each (one warp for both issued too slowly), warp 11 walks the block's run and hands its pieces
+// to the others through a small ring, so that nobody else divides or reads lengths on the way. The register file is shared
+// out again to give a row's thread its 128 products. Shared memory at D = 128: Q (64 KB), a ring of four K and
+// V tiles (32 KB each), and 32 KB through which the rows' outputs go out whole. The next piece's Q is on its
+// way as soon as the last product with this one's is done, and its first products run beside the output.
 // Waits are bounded; a wait that runs out is recorded (mq_device_status), the block drains its own copies
 // and products, frees tensor memory and returns.
 
@@ -51,16 +55,35 @@ struct Cfg {
     static constexpr int kChunks = D / 64;                       // 128-byte columns of a row
     static constexpr int kChunkBytes = 128 * 128;                // 128 rows of one
     static constexpr int kTileBytes = kChunks * kChunkBytes;     // a K or V tile, a half of Q
-    static constexpr int kRing = D == 128 ? 5 : 10;
-    static constexpr int kSmem = 1024 + (2 + kRing) * kTileBytes;
+    static constexpr int kQChunk = 2 * kChunkBytes;              // 256 rows of one column of Q
+    static constexpr int kRing = D == 128 ? 4 : 8;
+    static constexpr int kStageBytes = 4096;                     // a warp's part of the way out: 32 rows of 128 bytes
+    static constexpr int kSmem = 1024 + (2 + kRing) * kTileBytes + 8 * kStageBytes;
 };
 
+// A piece of the block's run, as warp 11 hands it out. n == 0: the run is over.
+struct Piece {
+    int n, in;           // tiles, and those of the segment before them
+    int lead;            // tiles of the shared prefix at the segment's head (own segments)
+    int seg, head;
+    int b, bt;           // sequence; first query, counted over the batch
+    int rows, len;       // query rows; keys of the part
+    int see;             // keys that the segment's first query sees (prefix: all)
+    int prefix, twin;    // twin: both halves hold the same rows, half h the tiles of its parity
+    int whole;           // all of the segment's tiles
+};
+constexpr int kPieces = 4;
+constexpr int kReaders = 11;             // warps that read one
+
 struct Bars {
-    uint64_t full[10], empty[10];
-    uint64_t q_ready[2], s_full[2], p_ready[2], pv_done[2];
+    uint64_t full[8], empty[8];
+    uint64_t q_full, q_free;
+    uint64_t s_full[2], p_ready[2], pv_done[2];
     uint64_t twin_full[4], twin_free[4];   // per quarter: half 1's rows of a twin segment are there / were taken
+    uint64_t piece_full[kPieces], piece_free[kPieces];
     uint64_t drained[2];
     float2 twin_ml[kHalf];
+    Piece piece[kPieces];
     uint32_t tmem;
     int abort;
 };
@@ -97,6 +120,13 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
+__device__ __forceinline__ void tma_load_3d(void* dst, const void* map, int x, int y, int z, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            tc::smem_u32(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(tc::smem_u32(bar))
+        : "memory");
+}
 __device__ __forceinline__ void tma_load_4d(void* dst, const void* map, int x, int y, int z, int w, uint64_t* bar) {
     asm volatile(
         "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::
@@ -132,36 +162,38 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_l
 // The same in every lane, and known to be.
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 
-// What a role keeps of the segment that its cursor is in.
-struct Seg {
-    int b, r0, rows, len;
-    int lead;        // tiles of the shared prefix at its head (own segments)
-    bool twin;       // both halves hold the same rows, half h the tiles of its parity
+// The pieces of a run, as a reader steps through them.
+struct Reader {
+    int slot = 0;
+    uint32_t phase = 0;
+    // The next piece, or false (the run is over, or a wait ran out: alive says which).
+    __device__ __forceinline__ bool next(Bars& b, Piece& p, bool& alive) {
+        if (!(alive = wwait(b, &b.piece_full[slot], phase))) return false;
+        p = b.piece[slot];
+        return p.n > 0;
+    }
+    __device__ __forceinline__ void done(Bars& b) {
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) tc::mbar_arrive(&b.piece_free[slot]);
+        if (++slot == kPieces) {
+            slot = 0;
+            phase ^= 1;
+        }
+    }
 };
-__device__ __forceinline__ Seg segment_of(const Plan& p, const int32_t* len, const Cursor& c) {
-    Seg s;
-    const int per_seq = own_tiles_of_rows(p);
-    s.b = c.prefix ? 0 : c.unit / per_seq;
-    const int rt = c.prefix ? c.unit : c.unit - s.b * per_seq;
-    s.r0 = rt * kManyRows;
-    s.rows = rows_of(p, c.prefix ? p.prefix_rows : p.T * p.group, rt);
-    s.len = c.prefix ? p.prefix_keys : own_len_of(p, len, s.b);
-    s.lead = c.prefix ? 0 : ceil_div(p.lead_keys, kKeys);
-    s.twin = s.rows <= kHalf;
-    return s;
-}
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    attn_many_kernel(const ManyArgs a, const __grid_constant__ CUtensorMap pk, const __grid_constant__ CUtensorMap pv,
-                     const __grid_constant__ CUtensorMap ok, const __grid_constant__ CUtensorMap ov) {
+    attn_many_kernel(const ManyArgs a, const __grid_constant__ CUtensorMap qm, const __grid_constant__ CUtensorMap pk,
+                     const __grid_constant__ CUtensorMap pv, const __grid_constant__ CUtensorMap ok,
+                     const __grid_constant__ CUtensorMap ov) {
     using C = Cfg<D>;
     extern __shared__ uint8_t s_raw[];
     __shared__ Bars s_bars;
     Bars& bars = s_bars;
-    uint8_t* smem = s_raw + ((1024 - (tc::smem_u32(s_raw) & 1023)) & 1023);
-    uint8_t* s_q = smem;                            // two halves
-    uint8_t* s_ring = smem + 2 * C::kTileBytes;
+    uint8_t* s_q = s_raw + ((1024 - (tc::smem_u32(s_raw) & 1023)) & 1023);   // [column][256 rows]
+    uint8_t* s_ring = s_q + 2 * C::kTileBytes;
+    uint8_t* s_stage = s_ring + C::kRing * C::kTileBytes;
     const Plan& p = a.plan;
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
 
@@ -169,24 +201,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < C::kRing; ++i) {
             tc::mbar_init(&bars.full[i], 1);
-            tc::mbar_init(&bars.empty[i], 2);   // a half each
+            tc::mbar_init(&bars.empty[i], 2);      // a half each
         }
+        tc::mbar_init(&bars.q_full, 1);
+        tc::mbar_init(&bars.q_free, 2);
         for (int h = 0; h < 2; ++h) {
-            tc::mbar_init(&bars.q_ready[h], 4);    // a warp each
             tc::mbar_init(&bars.s_full[h], 1);
-            tc::mbar_init(&bars.p_ready[h], 4);
+            tc::mbar_init(&bars.p_ready[h], 4);    // a warp each
             tc::mbar_init(&bars.pv_done[h], 1);
+            tc::mbar_init(&bars.drained[h], 1);
         }
         for (int i = 0; i < 4; ++i) {
             tc::mbar_init(&bars.twin_full[i], 1);
             tc::mbar_init(&bars.twin_free[i], 1);
         }
-        for (int h = 0; h < 2; ++h) tc::mbar_init(&bars.drained[h], 1);
+        for (int i = 0; i < kPieces; ++i) {
+            tc::mbar_init(&bars.piece_full[i], 1);
+            tc::mbar_init(&bars.piece_free[i], kReaders);
+        }
         bars.abort = 0;
         tc::fence_mbar_init();
     }
     if (wid == 9) tc::tmem_alloc(&bars.tmem, kTmemCols);
     if (wid == 8 && lane == 0) {
+        tc::prefetch_tensormap(&qm);
         tc::prefetch_tensormap(&pk);
         tc::prefetch_tensormap(&pv);
         tc::prefetch_tensormap(&ok);
@@ -199,65 +237,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::tc_fence_after();
     const uint32_t tmem = bars.tmem;
 
-    advance(p, a.len, c, 0);
-
     if (wid < 8) {
         tc::setmaxnreg_inc<kRowRegs>();
         // ---------------------------------------------------------------- rows: a thread each
         const int h = wid >> 2, quarter = wid & 3, row = quarter * 32 + lane;
         const uint32_t lane_base = tmem + ((uint32_t)quarter * 32 << 16);
         const uint32_t s_col = lane_base + h * 128, o_col = lane_base + 256 + h * 128;
-        // The warp's rows of its half of Q; at a segment's end the same memory turns outputs into whole rows.
-        // A row is 128 bytes in each chunk, its 16-byte units at unit ^ (row % 8), as TMA would lay it.
-        uint8_t* s_rows = s_q + h * C::kTileBytes + quarter * 32 * 128;
-        auto unit_of = [&](int r, int u) {   // unit u of row r of the warp
-            return reinterpret_cast<uint4*>(s_rows + (u / 8) * C::kChunkBytes + r * 128 + (((u & 7) ^ (r & 7)) << 4));
-        };
-        constexpr int kUnits = D / 8, kRowsAtOnce = 32 / kUnits;   // lanes side by side take a row
-        const int my_unit = lane % kUnits, my_row = lane / kUnits;
+        // unit u (16 bytes) of row r of the warp's stage: 128 bytes a row, units xor row % 8
+        uint8_t* stage = s_stage + wid * C::kStageBytes;
+        auto unit_of = [&](int r, int u) { return reinterpret_cast<uint4*>(stage + r * 128 + ((u ^ (r & 7)) << 4)); };
+        const int my_unit = lane & 7, my_row = lane >> 3;         // on the way out 8 lanes take a row's 128 bytes
         uint32_t s_phase = 0, pv_phase = 0, twin_phase = 0;
         bool alive = true;
-        int4 split = make_int4(-1, 0, 0, 0);
-        while (alive && c.more()) {
-            const int nt = piece_tiles(p, c);
-            const Seg g = segment_of(p, a.len, c);
-            const bool first = c.in == 0, whole = first && nt == c.tiles;
-            if (first && tid == 0) {
-                const int2 f = blocks_of(p, c);
-                a.out.info[c.seg] = f;
-                if (!whole) split = make_int4(c.seg, f.y, c.unit, c.head);
-            }
-            const int half0 = g.twin ? 0 : h * kHalf;            // rows of the segment before this half's
-            const int r_base = g.r0 + half0 + quarter * 32;      // the warp's first row, in the row space of its part
-            const int bt0 = c.prefix ? 0 : g.b * p.T;
-            const int n_rows = g.rows - half0 - quarter * 32;    // rows of the warp (others are zeros)
-            const int r = r_base + lane;                         // this thread's row; its query and head
-            const int q_in = r / p.group;
-            const long long q_row = bt0 + q_in;
-            const int q_head = c.head * p.group + r - q_in * p.group;
-            {
-                const long long off = q_row * a.q_stride + q_head * D;
-#pragma unroll
-                for (int i0 = 0; i0 < kUnits; i0 += 8) {
-                    uint4 x[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int rr = (i0 + i) * kRowsAtOnce + my_row;
-                        const long long from = __shfl_sync(0xffffffffu, off, rr);
-                        x[i] = make_uint4(0, 0, 0, 0);
-                        if (rr < n_rows) x[i] = __ldca(reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + from) + my_unit);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) *unit_of((i0 + i) * kRowsAtOnce + my_row, my_unit) = x[i];
-                }
-                tc::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&bars.q_ready[h]);
-            }
-            const int own_sees = c.prefix ? g.len : g.len - p.T + 1 + q_in;
+        Reader reader;
+        Piece g;
+        while (reader.next(bars, g, alive)) {
+            const int half0 = g.twin ? 0 : h * kHalf;             // rows of the segment before this half's
+            const int r = half0 + row, q_in = p.by_group.of(r);   // this thread's row; its query in the segment
+            const int n_rows = g.rows - half0 - quarter * 32;     // rows of the warp that count
+            const int own_sees = g.prefix ? g.see : g.see + q_in;
             float m = -INFINITY, l = 0.0f;                    // base 2, scaled
             const int step = g.twin ? 2 : 1, j0 = g.twin ? h : 0;
-            for (int j = j0; j < nt; j += step) {
+            for (int j = j0; j < g.n; j += step) {
                 if (!(alive = wwait(bars, &bars.s_full[h], s_phase))) break;
                 s_phase ^= 1;
                 tc::tc_fence_after();
@@ -265,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) tc::tmem_ld32(s_col + k * 32, s[k]);
                 tc::tmem_ld_wait();
-                const int tile = c.in + j;
+                const int tile = g.in + j;
                 const bool lead = tile < g.lead;
                 const int k0 = (lead ? tile : tile - g.lead) * kKeys;
                 const int seen = lead ? p.lead_keys : own_sees;
@@ -328,13 +329,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) tc::mbar_arrive(&bars.p_ready[h]);
                 pv_phase ^= 1;
             }
-            const bool any = j0 < nt;                         // a twin may have no tile
-            if (alive && any) alive = wwait(bars, &bars.pv_done[h], pv_phase ^ 1);
+            if (!alive) break;
+            if (j0 < g.n && !(alive = wwait(bars, &bars.pv_done[h], pv_phase ^ 1))) break;
             // A twin segment's rows are joined by half 0's threads, which reach the other half's output in the same
             // lanes of tensor memory: f scales the own one, f1 the other.
             float f = 1.0f, f1 = 0.0f;
-            const bool both = g.twin && nt > 1;
-            if (both && alive) {
+            const bool both = g.twin && g.n > 1;
+            if (both) {
                 if (h == 1) {
                     bars.twin_ml[row] = make_float2(m, l);
                     tc::tc_fence_before();
@@ -342,7 +343,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0) tc::mbar_arrive(&bars.twin_full[quarter]);
                     alive = wwait(bars, &bars.twin_free[quarter], twin_phase);
                 } else if ((alive = wwait(bars, &bars.twin_full[quarter], twin_phase))) {
-                    tc::tc_fence_after();
                     const float2 o = bars.twin_ml[row];
                     const float mm = fmaxf(m, o.x), mb = mm == -INFINITY ? 0.0f : mm;
                     f = exp2_fast(m - mb);
@@ -350,18 +350,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                     l = l * f + o.y * f1;
                     m = mm;
                 }
+                if (!alive) break;
                 twin_phase ^= 1;
             }
-            if (alive && !(g.twin && h == 1)) {
+            if (!(g.twin && h == 1)) {
                 tc::tc_fence_after();
-                const bool finish = a.split && whole;
-                const long long at = ((long long)blockIdx.x + c.seg) * kManyRows + half0 + quarter * 32;
+                // Rows go out whole, 128 bytes at a time through the stage: in 16 bits or f32 where they are finished,
+                // as they are (f32) to the piece's place otherwise.
+                const bool finish = a.split && g.whole;
+                const long long place = ((long long)blockIdx.x + g.seg) * p.rows + half0 + quarter * 32;
+                const long long out_row = finish ? ((long long)g.bt + q_in) * p.Hq + g.head * p.group + r - q_in * p.group
+                                                 : place + lane;
+                const bool narrow = finish && !a.fin.f32;
+                const int row_bytes = D * (narrow ? 2 : 4);
+                uint8_t* to = static_cast<uint8_t*>(finish ? a.fin.out : a.out.o) + out_row * row_bytes;
                 if (finish) {
                     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
                     f *= inv;
                     f1 *= inv;
+                    if (a.fin.lse && lane < n_rows) a.fin.lse[out_row] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
+                } else if (lane < n_rows) {
+                    a.out.ml[out_row] = make_float2(m, l);
                 }
-                const long long fin_row = q_row * p.Hq + q_head;
+                uint8_t* row_to[8];                      // rows my_row + 4 i, this lane's unit
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    row_to[i] = reinterpret_cast<uint8_t*>(
+                                    __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(to), my_row + 4 * i)) + my_unit * 16;
                 auto load = [&](int col, uint32_t (&o)[32]) {   // 32 columns of the rows' outputs, scaled
                     tc::tmem_ld32(o_col + col, o);
                     tc::tmem_ld_wait();
@@ -377,76 +392,70 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
                     }
                 };
-                // through shared memory, so that rows go out whole: 16 bits at once, f32 by halves (finished, or as
-                // they are to the piece's place)
-                const bool narrow = finish && !a.fin.f32;
 #pragma unroll 1
-                for (int k = 0; k < (narrow ? 1 : 2); ++k) {
+                for (int col = 0, off = 0; col < D; off += 128) {
+                    uint32_t o[32];
+                    load(col, o);
                     if (narrow) {
 #pragma unroll 1
-                        for (int q = 0; q < D / 32; ++q) {
-                            uint32_t o[32];
-                            load(q * 32, o);
+                        for (int part = 0;; ++part) {
 #pragma unroll
                             for (int u = 0; u < 4; ++u) {
                                 uint32_t y[4];
 #pragma unroll
                                 for (int i = 0; i < 4; ++i)
                                     y[i] = mq_pack2<T>(__uint_as_float(o[u * 8 + 2 * i]), __uint_as_float(o[u * 8 + 2 * i + 1]));
-                                *unit_of(lane, q * 4 + u) = make_uint4(y[0], y[1], y[2], y[3]);
+                                *unit_of(lane, part * 4 + u) = make_uint4(y[0], y[1], y[2], y[3]);
                             }
+                            col += 32;
+                            if (part == 1) break;
+                            load(col, o);
                         }
                     } else {
-#pragma unroll 1
-                        for (int q = 0; q < D / 64; ++q) {
-                            uint32_t o[32];
-                            load(k * (D / 2) + q * 32, o);
 #pragma unroll
-                            for (int u = 0; u < 8; ++u)
-                                *unit_of(lane, q * 8 + u) = make_uint4(o[u * 4], o[u * 4 + 1], o[u * 4 + 2], o[u * 4 + 3]);
-                        }
+                        for (int u = 0; u < 8; ++u)
+                            *unit_of(lane, u) = make_uint4(o[u * 4], o[u * 4 + 1], o[u * 4 + 2], o[u * 4 + 3]);
+                        col += 32;
                     }
                     __syncwarp();
-#pragma unroll 4
-                    for (int i = 0; i < kUnits; ++i) {
-                        const int rr = i * kRowsAtOnce + my_row;
-                        const long long to = __shfl_sync(0xffffffffu, fin_row, rr);
-                        uint4* y = reinterpret_cast<uint4*>(finish ? a.fin.out : a.out.o);
-                        const long long unit = narrow ? to * kUnits : (finish ? to : at + rr) * (2 * kUnits) + k * kUnits;
-                        if (rr < n_rows) y[unit + my_unit] = *unit_of(rr, my_unit);
-                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (my_row + 4 * i < n_rows) *reinterpret_cast<uint4*>(row_to[i] + off) = *unit_of(my_row + 4 * i, my_unit);
                     __syncwarp();
                 }
                 tc::tc_fence_before();
-                if (lane < n_rows) {
-                    if (!finish) {
-                        a.out.ml[at + lane] = make_float2(m, l);
-                    } else if (a.fin.lse) {
-                        a.fin.lse[fin_row] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
-                    }
-                }
                 if (both) {
                     __syncwarp();
                     if (lane == 0) tc::mbar_arrive(&bars.twin_free[quarter]);
                 }
             }
-            advance(p, a.len, c, nt);
+            reader.done(bars);
         }
-        if (tid == 0 && a.split) a.split[blockIdx.x] = split;
     } else {
         tc::setmaxnreg_dec<kOtherRegs>();
+        bool alive = true;
+        Reader reader;
+        Piece g;
         if (wid == 8) {
-            // ------------------------------------------------------------ TMA: K and V of each tile
+            // ------------------------------------------------------------ copies: Q of a piece, K and V of its tiles
             int slot = 0, issued = 0;
-            uint32_t phase = 0;
-            bool alive = true;
-            while (alive && c.more()) {
-                const int nt = piece_tiles(p, c);
-                const Seg g = segment_of(p, a.len, c);
-                for (int j = 0; alive && j < nt; ++j) {
-                    const int tile = c.in + j;
-                    const bool shared = c.prefix || tile < g.lead;
-                    const int k0 = (c.prefix || shared ? tile : tile - g.lead) * kKeys;
+            uint32_t phase = 0, q_phase = 0;
+            bool q_issued = false;
+            while (reader.next(bars, g, alive)) {
+                if (!(alive = wwait(bars, &bars.q_free, q_phase ^ 1))) break;
+                if (tc::elect_one()) {
+                    tc::mbar_arrive_expect_tx(&bars.q_full, C::kChunks * 128 * p.rows);
+#pragma unroll
+                    for (int k = 0; k < C::kChunks; ++k)
+                        tma_load_3d(s_q + k * C::kQChunk, &qm, k * 64, g.head * p.group, g.bt, &bars.q_full);
+                }
+                __syncwarp();
+                q_issued = true;
+                q_phase ^= 1;
+                for (int j = 0; alive && j < g.n; ++j) {
+                    const int tile = g.in + j;
+                    const bool shared = g.prefix || tile < g.lead;
+                    const int k0 = (shared ? tile : tile - g.lead) * kKeys;
                     for (int kv = 0; kv < 2; ++kv) {
                         if (!(alive = wwait(bars, &bars.empty[slot], phase ^ 1))) break;
                         if (tc::elect_one()) {
@@ -454,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tc::mbar_arrive_expect_tx(&bars.full[slot], C::kTileBytes);
 #pragma unroll
                             for (int k = 0; k < C::kChunks; ++k)
-                                tma_load_4d(s_ring + slot * C::kTileBytes + k * C::kChunkBytes, map, k * 64, c.head, k0,
+                                tma_load_4d(s_ring + slot * C::kTileBytes + k * C::kChunkBytes, map, k * 64, g.head, k0,
                                             shared ? 0 : g.b, &bars.full[slot]);
                         }
                         __syncwarp();
@@ -465,9 +474,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
-                advance(p, a.len, c, nt);
+                if (!alive) break;
+                reader.done(bars);
             }
             if (!alive) {   // copies in flight must land before the block leaves
+                if (q_issued) tc::mbar_wait(&bars.q_full, q_phase ^ 1, kWaitLimitNs);
                 for (int i = 0; i < C::kRing && i < issued; ++i) {
                     if (--slot < 0) {
                         slot = C::kRing - 1;
@@ -485,11 +496,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr uint32_t kTileLow = C::kTileBytes >> 4;
             const uint32_t ring = tc::smem_u32(s_ring);
             const uint32_t s_tm = uniform(tmem + h * 128), o_tm = uniform(tmem + 256 + h * 128);
-            const uint32_t q_low = uniform(desc_low(tc::smem_u32(s_q) + h * C::kTileBytes, 16));
+            const uint32_t q_low = uniform(desc_low(tc::smem_u32(s_q), 16));
             const uint32_t k_low = uniform(desc_low(ring, 16)), v_low = uniform(desc_low(ring, C::kChunkBytes));
             int slot = 0;                        // ring slot of the piece's first K tile, and the phase there
             uint32_t phase = 0, q_phase = 0, p_phase = 0;
-            bool alive = true;
             auto step_slots = [&](int n) {       // n < kRing slots on
                 slot += n;
                 if (slot >= C::kRing) {
@@ -497,39 +507,42 @@ __global__ void __launch_bounds__(kThreads, 1)
                     phase ^= 1;
                 }
             };
-            auto qk = [&](bool twice) {          // S = Q K^T with the K tile in `slot`; one lane
+            // S = Q K^T with the K tile in `slot`; one lane. twice: the other half does not use the tile. last: nor
+            // this half Q again.
+            auto qk = [&](uint32_t q_at, bool twice, bool last) {
                 const uint32_t kl = k_low + slot * kTileLow;
-                mma_ss<false>(s_tm, q_low, kl, idesc_qk);
+                mma_ss<false>(s_tm, q_at, kl, idesc_qk);
 #pragma unroll
-                for (int k = 1; k < D / 16; ++k) {
-                    const uint32_t off = ((k / 4) * C::kChunkBytes + (k % 4) * 32) >> 4;
-                    mma_ss<true>(s_tm, q_low + off, kl + off, idesc_qk);
-                }
+                for (int k = 1; k < D / 16; ++k)
+                    mma_ss<true>(s_tm, q_at + (((k / 4) * C::kQChunk + (k % 4) * 32) >> 4),
+                                 kl + (((k / 4) * C::kChunkBytes + (k % 4) * 32) >> 4), idesc_qk);
                 tc::mma_commit(&bars.s_full[h]);
                 tc::mma_commit(&bars.empty[slot]);
-                if (twice) tc::mma_commit(&bars.empty[slot]);   // the other half does not use the tile
+                if (twice) tc::mma_commit(&bars.empty[slot]);
+                if (last) tc::mma_commit(&bars.q_free);
             };
-            while (alive && c.more()) {
-                const int nt = piece_tiles(p, c);
-                const Seg g = segment_of(p, a.len, c);
+            while (reader.next(bars, g, alive)) {
                 const int step = g.twin ? 2 : 1;
                 int t = g.twin ? h : 0;
-                if (!(alive = wwait(bars, &bars.q_ready[h], q_phase))) break;
+                const uint32_t q_at = q_low + (g.twin ? 0 : h * (C::kChunkBytes >> 4));
+                if (!(alive = wwait(bars, &bars.q_full, q_phase))) break;
                 q_phase ^= 1;
                 if (t > 0) step_slots(2);
-                if (t < nt) {
+                if (t < g.n) {
                     if (!(alive = wwait(bars, &bars.full[slot], phase))) break;
                     tc::tc_fence_after();
-                    if (tc::elect_one()) qk(g.twin);
+                    if (tc::elect_one()) qk(q_at, g.twin, t + step >= g.n);
                     __syncwarp();
+                } else if (lane == 0) {
+                    tc::mbar_arrive(&bars.q_free);
                 }
                 bool first = true;
-                for (; t < nt; t += step) {
+                for (; t < g.n; t += step) {
                     step_slots(1);               // this tile's V
                     const int v_slot = slot;
                     if (!(alive = wwait(bars, &bars.full[slot], phase))) break;
-                    const int tile = c.in + t, past = (tile - g.lead + 1) * kKeys - g.len;
-                    if (past > 0 && !c.prefix && tile >= g.lead) {
+                    const int tile = g.in + t, past = (tile - g.lead + 1) * kKeys - g.len;
+                    if (past > 0 && !g.prefix && tile >= g.lead) {
                         // rows past the length may hold anything: zeros times a probability of zero
                         for (int u = lane; u < past * 8; u += 32)
 #pragma unroll
@@ -540,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         __syncwarp();
                     }
                     step_slots(g.twin ? 3 : 1);  // the half's next K
-                    const bool more = t + step < nt;
+                    const bool more = t + step < g.n;
                     if (more && !(alive = wwait(bars, &bars.full[slot], phase))) break;
                     if (!(alive = wwait(bars, &bars.p_ready[h], p_phase))) break;
                     p_phase ^= 1;
@@ -553,23 +566,68 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tc::mma_commit(&bars.pv_done[h]);
                         tc::mma_commit(&bars.empty[v_slot]);
                         if (g.twin) tc::mma_commit(&bars.empty[v_slot]);
-                        if (more) qk(g.twin);
+                        if (more) qk(q_at, g.twin, t + 2 * step >= g.n);
                     }
                     __syncwarp();
                     first = false;
                 }
                 if (!alive) break;
                 // t stands at the half's first tile past the piece, `slot` at that tile's K: back to the piece's end
-                for (int n = 2 * (t - nt); n > 0; --n)
+                for (int n = 2 * (t - g.n); n > 0; --n)
                     if (--slot < 0) {
                         slot = C::kRing - 1;
                         phase ^= 1;
                     }
-                advance(p, a.len, c, nt);
+                reader.done(bars);
             }
             if (tc::elect_one()) tc::mma_commit(&bars.drained[h]);
             __syncwarp();
             tc::mbar_wait(&bars.drained[h], 0, kWaitLimitNs);
+        } else {
+            // ------------------------------------------------------------ the run's pieces
+            const int per_seq = own_tiles_of_rows(p);
+            int4 split = make_int4(-1, 0, 0, 0);
+            int slot = 0;
+            uint32_t phase = 0;
+            advance(p, a.len, c, 0);
+            for (;;) {
+                g.n = 0;
+                if (c.more()) {
+                    g.n = piece_tiles(p, c);
+                    g.in = c.in;
+                    g.seg = c.seg;
+                    g.head = c.head;
+                    g.prefix = c.prefix;
+                    g.b = c.prefix ? 0 : p.by_per_seq.of(c.unit);
+                    const int rt = c.prefix ? c.unit : c.unit - g.b * per_seq;
+                    const int t0 = p.by_group.of(rt * p.rows);
+                    g.bt = g.b * p.T + t0;
+                    g.rows = rows_of(p, c.prefix ? p.prefix_rows : p.T * p.group, rt);
+                    g.len = c.prefix ? p.prefix_keys : own_len_of(p, a.len, g.b);
+                    g.see = c.prefix ? g.len : g.len - p.T + 1 + t0;
+                    g.lead = c.prefix ? 0 : ceil_div(p.lead_keys, kKeys);
+                    g.twin = g.rows <= kHalf;
+                    g.whole = c.in == 0 && g.n == c.tiles;
+                    if (c.in == 0) {
+                        const int2 f = blocks_of(p, c);
+                        if (lane == 0) a.out.info[c.seg] = f;
+                        if (!g.whole) split = make_int4(c.seg, f.y, c.unit, c.head);
+                    }
+                }
+                if (!(alive = wwait(bars, &bars.piece_free[slot], phase ^ 1))) break;
+                if (lane == 0) {
+                    bars.piece[slot] = g;
+                    tc::mbar_arrive(&bars.piece_full[slot]);
+                }
+                __syncwarp();
+                if (++slot == kPieces) {
+                    slot = 0;
+                    phase ^= 1;
+                }
+                if (g.n == 0) break;
+                advance(p, a.len, c, g.n);
+            }
+            if (lane == 0 && a.split) a.split[blockIdx.x] = split;
         }
     }
     tc::tc_fence_before();
@@ -620,18 +678,32 @@ bool kv_map(CUtensorMap* map, const mq_kv* c, const void* base) {
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The queries [B T][Hq][D] as (dim, head, query): a box is a segment's rows, group heads of each of its queries.
+bool q_map(CUtensorMap* map, const ManyArgs& a, int D, int type) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const Plan& p = a.plan;
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)p.Hq, (cuuint64_t)p.B * p.T};
+    const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)a.q_stride * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)p.group, (cuuint32_t)(p.rows / p.group)}, step[3] = {1, 1, 1};
+    return fn(map, type == MQ_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+              const_cast<void*>(a.q), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+           CUDA_SUCCESS;
+}
+
 }  // namespace
 
 int launch_many(const ManyArgs& a, const mq_kv* prefix, const mq_kv* own, int D, int type, cudaStream_t stream) {
-    CUtensorMap pk, pv, ok, ov;
+    CUtensorMap qm, pk, pv, ok, ov;
     const mq_kv* p = prefix ? prefix : own;   // a part that is not there is never read
     const mq_kv* o = own ? own : prefix;
-    if (!kv_map(&pk, p, p->k) || !kv_map(&pv, p, p->v) || !kv_map(&ok, o, o->k) || !kv_map(&ov, o, o->v))
+    if (!q_map(&qm, a, D, type) || !kv_map(&pk, p, p->k) || !kv_map(&pv, p, p->v) || !kv_map(&ok, o, o->k) || !kv_map(&ov, o, o->v))
         return MQ_ERR_LAUNCH;
     auto go = [&](auto kern, int smem) {
         if (!regs_as_planned(reinterpret_cast<const void*>(kern))) return (int)MQ_ERR_LAUNCH;
         if (!allow_smem(reinterpret_cast<const void*>(kern), smem)) return (int)MQ_ERR_LAUNCH;
-        return mq::launch_pdl(kern, dim3(a.plan.G), dim3(kThreads), smem, stream, a, pk, pv, ok, ov);
+        return mq::launch_pdl(kern, dim3(a.plan.G), dim3(kThreads), smem, stream, a, qm, pk, pv, ok, ov);
     };
     if (type == MQ_F16)
         return D == 64 ? go(attn_many_kernel<__half, 64>, Cfg<64>::kSmem) : go(attn_many_kernel<__half, 128>, Cfg<128>::kSmem);

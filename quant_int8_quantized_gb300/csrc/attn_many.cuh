@@ -19,12 +19,15 @@ struct ManyArgs {
     Out fin;              // with `split`: segments that one block holds are finished here
 };
 
-constexpr int kManyRows = 256;    // query rows per segment
+constexpr int kManyRows = 256;    // query rows per segment, at most
 constexpr int kManyHalf = 128;    // rows of one half
 constexpr int kManyKeys = 128;    // keys per tile
 
-constexpr int kManyExtra = 1;     // what beginning and ending a segment costs, in tiles of one half
-inline bool many_takes(int D) { return D == 64 || D == 128; }
+constexpr int kManyExtra = 3;     // what beginning and ending a segment costs, in tiles of one half
+// Whole queries only: a segment's rows are one box of the queries' tensor map.
+inline int many_rows(int group) { return kManyRows / group * group; }
+
+inline bool many_takes(int D, int group) { return (D == 64 || D == 128) && group <= kManyRows; }
 int launch_many(const ManyArgs& a, const mq_kv* prefix, const mq_kv* own, int D, int type, cudaStream_t stream);
 
 }  // namespace attn
