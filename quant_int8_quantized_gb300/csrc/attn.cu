@@ -28,7 +28,6 @@ bool allow_smem(const void* kern, int bytes) {
 
 namespace {
 
-constexpr int kMaxPerSm = 4;   // blocks of a piece kernel per SM, at most
 
 // One part of the keys, as the joining kernels see it.
 struct Part {
@@ -60,12 +59,11 @@ __device__ __forceinline__ Run run_of(const Part& p, int seg, int2 f, int in) {
 // holds maximum and sum of piece i of 32; the outputs' loads do not depend on one another.
 template <typename O, int D, int N>
 __device__ __forceinline__ void join_row(const Run (&runs)[N], const Out& fin, float* lse2, long long row) {
-    constexpr int W = (D + 63) / 64;
+    // lane l holds V floats at V (l + 32 k)
+    constexpr int V = D >= 128 ? 4 : 2, W = (D + 32 * V - 1) / (32 * V);
     const int lane = threadIdx.x & 31;
     float m = -INFINITY, l = 0.0f;
-    float2 acc[W];
-#pragma unroll
-    for (int i = 0; i < W; ++i) acc[i] = make_float2(0.0f, 0.0f);
+    float acc[W][V] = {};
 #pragma unroll
     for (int w = 0; w < N; ++w) {
 #pragma unroll 1
@@ -85,18 +83,28 @@ __device__ __forceinline__ void join_row(const Run (&runs)[N], const Out& fin, f
             for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
             l = l * back + sum;
 #pragma unroll
-            for (int k = 0; k < W; ++k) acc[k].x *= back, acc[k].y *= back;
+            for (int k = 0; k < W; ++k)
+#pragma unroll
+                for (int e = 0; e < V; ++e) acc[k][e] *= back;
             const float* o = runs[w].p->o + first * D;
-#pragma unroll 4
+#pragma unroll 8
             for (int i = 0; i < n; ++i) {
                 const float g = __shfl_sync(0xffffffffu, f, i);
-                const float2* oi = reinterpret_cast<const float2*>(o + i * runs[w].stride * D);
+                const float* oi = o + i * runs[w].stride * D;
 #pragma unroll
                 for (int k = 0; k < W; ++k)
-                    if (k * 32 + lane < D / 2) {
-                        const float2 x = __ldca(oi + k * 32 + lane);
-                        acc[k].x = fmaf(x.x, g, acc[k].x);
-                        acc[k].y = fmaf(x.y, g, acc[k].y);
+                    if (V * (k * 32 + lane) < D) {
+                        if constexpr (V == 4) {
+                            const float4 x = __ldca(reinterpret_cast<const float4*>(oi) + k * 32 + lane);
+                            acc[k][0] = fmaf(x.x, g, acc[k][0]);
+                            acc[k][1] = fmaf(x.y, g, acc[k][1]);
+                            acc[k][2] = fmaf(x.z, g, acc[k][2]);
+                            acc[k][3] = fmaf(x.w, g, acc[k][3]);
+                        } else {
+                            const float2 x = __ldca(reinterpret_cast<const float2*>(oi) + k * 32 + lane);
+                            acc[k][0] = fmaf(x.x, g, acc[k][0]);
+                            acc[k][1] = fmaf(x.y, g, acc[k][1]);
+                        }
                     }
             }
         }
@@ -104,12 +112,20 @@ __device__ __forceinline__ void join_row(const Run (&runs)[N], const Out& fin, f
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;   // l == 0: no key seen (a NaN or infinite l stays one)
 #pragma unroll
     for (int k = 0; k < W; ++k)
-        if (k * 32 + lane < D / 2) {
-            const float x = acc[k].x * inv, y = acc[k].y * inv;
-            if constexpr (sizeof(O) == 4)
-                reinterpret_cast<float2*>(fin.out)[row * (D / 2) + k * 32 + lane] = make_float2(x, y);
-            else
-                reinterpret_cast<uint32_t*>(fin.out)[row * (D / 2) + k * 32 + lane] = mq_pack2<O>(x, y);
+        if (V * (k * 32 + lane) < D) {
+            const long long at = row * (D / V) + k * 32 + lane;
+            float y[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e) y[e] = acc[k][e] * inv;
+            if constexpr (sizeof(O) == 4) {
+                if constexpr (V == 4) reinterpret_cast<float4*>(fin.out)[at] = make_float4(y[0], y[1], y[2], y[3]);
+                else reinterpret_cast<float2*>(fin.out)[at] = make_float2(y[0], y[1]);
+            } else {
+                if constexpr (V == 4)
+                    reinterpret_cast<uint2*>(fin.out)[at] = make_uint2(mq_pack2<O>(y[0], y[1]), mq_pack2<O>(y[2], y[3]));
+                else
+                    reinterpret_cast<uint32_t*>(fin.out)[at] = mq_pack2<O>(y[0], y[1]);
+            }
         }
     if (lane == 0) {
         if (fin.lse) fin.lse[row] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
@@ -230,16 +246,16 @@ Cut cut_of(int B, int T, int Hq, int Hkv, int D, int prefix_keys, int own_cap, b
         p.own_least = many ? 1 : 0;
         p.own_cap = p.own ? own_cap : 0;
         p.rows = many ? many_rows(group) : kFewRows;
-        p.keys = many ? kManyKeys : few_tile_keys(D);
+        p.keys = many ? kManyKeys : kFewKeys;
         p.wide = many ? kManyHalf : kFewRows;
-        p.extra = many ? kManyExtra : 0;
+        p.extra = many ? kManyExtra : kFewExtra;
         p.by_group = div_by(group);
         p.by_per_seq = div_by(p.own ? own_tiles_of_rows(p) : 1);
         const long long segs = all_segs(p);
         const long long most = (long long)prefix_segs(p) * ceil_div(p.prefix_keys, p.keys) +
                                (segs - prefix_segs(p)) * (ceil_div(p.lead_keys, p.keys) + ceil_div(p.own_cap, p.keys));
         if (most * 2 + segs * p.extra > 0x7fffffffLL) c.fits = false;
-        const long long held = (long long)mq::num_sms() * (many ? 1 : kMaxPerSm);
+        const long long held = (long long)mq::num_sms() * (many ? 1 : kFewPerSm);
         p.G = (int)(most < held ? most : held);
         const size_t places = segs > 0 ? (size_t)p.G + (size_t)segs : 0;
         *o = at;
@@ -364,8 +380,7 @@ extern "C" int mq_attn_prefix(const void* q, long long q_stride, int B, int T, i
         f.scale_log2 = scale * kLog2e;
         f.out = few;
         f.raw = raw;
-        const int held = few_blocks(D, type);
-        if (f.plan.G > held) f.plan.G = held;
+        f.beside = all_segs(c.many) > 0;
         rc = launch_few(f, D, type, stream);
         if (rc != MQ_OK) return rc;
     }

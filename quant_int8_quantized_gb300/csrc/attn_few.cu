@@ -2,13 +2,13 @@
 // read once and used for a handful of rows, so HBM bounds and the matrix products only have to keep
 // out of the way. They run as warp-wide 16 x 8 x 16 products in registers.
 //
-// Four warps share a tile of 64 keys, 16 each, and never wait for one another: a warp copies its own
-// keys and values into its own ring of stages (asynchronous 16-byte copies, rows past the end filled
-// with zeros, so nothing that lies there can reach a sum), multiplies, keeps its own running
-// maximum, sum and output, and the four are joined at the end of the piece. The products q k^T come out
-// in the layout that the second product takes as its left operand, so probabilities stay in registers.
-// Rows of a stage are padded by 16 bytes: eight rows of an 8 x 8 matrix load then fall into eight
-// different groups of banks.
+// A block is one warp with a run of its own, eight of them per SM, and nothing waits for anything else: the
+// warp copies tiles of 16 keys and values into its ring of stages (asynchronous 16-byte copies, rows past the end filled
+// with zeros, so nothing that lies there can reach a sum), keeps running maximum, sum and output in
+// registers and leaves the piece in the workspace. The copies run ahead across the ends of pieces. The
+// products q k^T come out in the layout that the second product takes as its left operand, so
+// probabilities stay in registers. Rows of a stage are padded by 16 bytes: eight rows of an 8 x 8 matrix
+// load then fall into eight different groups of banks.
 
 #include "attn_few.cuh"
 #include "tc.cuh"
@@ -16,20 +16,24 @@
 namespace attn {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
-constexpr int kKeys = 16;              // keys per warp and tile
-constexpr int kTile = kWarps * kKeys;
+constexpr int kThreads = 32;
+constexpr int kKeys = kFewKeys;
 
 template <int D>
 struct Cfg {
     static constexpr int kPitch = D * 2 + 16;                 // bytes of a row of a stage
     static constexpr int kStageBytes = 2 * kKeys * kPitch;    // keys, then values
-    static constexpr int kStages = D <= 128 ? 3 : 2;
-    static constexpr int kRing = kWarps * kStages * kStageBytes;
-    // the ring's memory takes the warps' outputs at the end of a piece
-    static constexpr int kJoin = kWarps * kFewRows * D * 4;
-    static constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
+    static constexpr int kStages = D <= 64 ? 4 : D <= 128 ? 3 : 2;
+    static constexpr int kSmem = kStages * kStageBytes;
+};
+
+// A piece as the copying side hands it to the multiplying side. n == 0: the run is over.
+struct Piece {
+    int n, key0;         // tiles, first key
+    int seg, head;
+    int b, r0;           // sequence (prefix: 0), first row
+    int rows, len;
+    int prefix;
 };
 
 __device__ __forceinline__ void ldm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -71,62 +75,95 @@ template <typename T, int D, bool RAW>
 __global__ void __launch_bounds__(kThreads) attn_few_kernel(const FewArgs a) {
     using C = Cfg<D>;
     extern __shared__ __align__(16) uint8_t s_ring[];
-    __shared__ float2 s_ml[kWarps][kFewRows];
+    __shared__ Piece s_piece[C::kStages + 1];
     mq_grid_release();
-    mq_grid_wait();
+    if (!a.beside) mq_grid_wait();
     const Plan& p = a.plan;
-    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-    const int tg = p.T * p.group;
-    Cursor c = find_run<kThreads>(p, a.len);
-    const uint32_t ring = tc::smem_u32(s_ring) + wid * (C::kStages * C::kStageBytes);
+    const int lane = threadIdx.x;
+    const int tg = p.T * p.group, per_seq = own_tiles_of_rows(p);
+    const uint32_t ring = tc::smem_u32(s_ring);
     const int g = lane >> 2, t2 = (lane & 3) * 2;   // this thread's rows g, g + 8 and columns t2, t2 + 1
 
+    // ---------------------------------------------------------------- copies, kStages - 1 tiles ahead
+    Cursor c = find_run<kThreads>(p, a.len);
     advance(p, a.len, c, 0);
-    while (c.more()) {
-        const int nt = piece_tiles(p, c);
-        const int key0 = c.in * kTile;
-        // the segment's rows and keys
-        const int per_seq = own_tiles_of_rows(p);
-        const int b = c.prefix ? 0 : p.by_per_seq.of(c.unit);
-        const int r0 = (c.prefix ? c.unit : c.unit - b * per_seq) * kFewRows;
-        const int nrows = min(kFewRows, (c.prefix ? p.prefix_rows : tg) - r0);
-        const int len = c.prefix ? p.prefix_keys : own_len_of(p, a.len, b);
-        const long long row_stride = c.prefix ? a.p_row : a.o_row;
-        const long long base = c.prefix ? c.head * a.p_head : b * a.o_seq + c.head * a.o_head;
-        const T* K = static_cast<const T*>(c.prefix ? a.pk : a.ok) + base;
-        const T* V = static_cast<const T*>(c.prefix ? a.pv : a.ov) + base;
-        if (tid == 0 && c.in == 0)
-            a.out.info[c.seg] = blocks_of(p, c);
-
-        auto copy = [&](int t) {   // tile t of the piece into its stage
-            if (t < nt) {
-                const uint32_t st = ring + (t % C::kStages) * C::kStageBytes;
-                const int k0 = key0 + t * kTile + wid * kKeys;
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i) {
-                    const int ch = i * 32 + lane, kr = ch / (D / 8), kc = ch % (D / 8);
-                    const bool in = k0 + kr < len;
-                    const long long off = (in ? k0 + kr : 0) * row_stride + kc * 8;
-                    tc::cp_async16_zfill(st + kr * C::kPitch + kc * 16, K + off, in ? 16 : 0);
-                    tc::cp_async16_zfill(st + (kKeys + kr) * C::kPitch + kc * 16, V + off, in ? 16 : 0);
-                }
+    int left = 0, handed = 0, key = 0, klen = 0, in_slot = 0;    // tiles of the copied piece left, pieces handed over
+    const T *K = nullptr, *V = nullptr;
+    long long row_stride = 0;
+    const int my_row = lane / (D / 8), my_unit = lane % (D / 8);   // of the first copies of a stage
+    auto copy = [&] {
+        if (left == 0) {
+            Piece q;
+            q.n = 0;
+            if (c.more()) {
+                q.n = piece_tiles(p, c);
+                q.key0 = c.in * kKeys;
+                q.seg = c.seg;
+                q.head = c.head;
+                q.prefix = c.prefix;
+                q.b = c.prefix ? 0 : p.by_per_seq.of(c.unit);
+                q.r0 = (c.prefix ? c.unit : c.unit - q.b * per_seq) * kFewRows;
+                q.rows = min(kFewRows, (c.prefix ? p.prefix_rows : tg) - q.r0);
+                q.len = c.prefix ? p.prefix_keys : own_len_of(p, a.len, q.b);
+                if (lane == 0 && c.in == 0) a.out.info[c.seg] = blocks_of(p, c);
+                row_stride = c.prefix ? a.p_row : a.o_row;
+                const long long base = c.prefix ? c.head * a.p_head : q.b * a.o_seq + c.head * a.o_head;
+                K = static_cast<const T*>(c.prefix ? a.pk : a.ok) + base;
+                V = static_cast<const T*>(c.prefix ? a.pv : a.ov) + base;
+                key = q.key0;
+                klen = q.len;
+                left = q.n;
+                advance(p, a.len, c, q.n);
             }
-            tc::cp_async_commit();
-        };
+            __syncwarp();
+            if (lane == 0) s_piece[handed] = q;
+            __syncwarp();
+            if (++handed == C::kStages + 1) handed = 0;
+        }
+        if (left > 0) {
+            const uint32_t st = ring + in_slot * C::kStageBytes;
 #pragma unroll
-        for (int t = 0; t < C::kStages - 1; ++t) copy(t);
+            for (int i = 0; i < D / 16; ++i) {
+                // unit i * 32 + lane of the stage's key rows (D / 8 units a row)
+                int kr, ku;
+                if constexpr (256 % D == 0) {   // a warp's units end with a row
+                    kr = i * (256 / D) + my_row;
+                    ku = my_unit;
+                } else {
+                    kr = (i * 32 + lane) / (D / 8);
+                    ku = (i * 32 + lane) % (D / 8);
+                }
+                const bool in = key + kr < klen;
+                const long long off = (in ? key + kr : 0) * row_stride + ku * 8;
+                tc::cp_async16_zfill(st + kr * C::kPitch + ku * 16, K + off, in ? 16 : 0);
+                tc::cp_async16_zfill(st + (kKeys + kr) * C::kPitch + ku * 16, V + off, in ? 16 : 0);
+            }
+            key += kKeys;
+            --left;
+            if (++in_slot == C::kStages) in_slot = 0;
+        }
+        tc::cp_async_commit();
+    };
+#pragma unroll 1
+    for (int t = 0; t < C::kStages - 1; ++t) copy();
 
+    // ---------------------------------------------------------------- products
+    int taken = 0, slot = 0;
+    for (;;) {
+        const Piece w = s_piece[taken];
+        if (w.n == 0) break;
+        if (++taken == C::kStages + 1) taken = 0;
         // query rows g and g + 8 (zeros past the last), as left operands; the keys that each sees
         uint32_t qf[D / 16][4];
         int seen[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const int r = r0 + g + 8 * u;
-            const bool live = g + 8 * u < nrows;
-            const int t = p.by_group.of(r), h = c.head * p.group + r - t * p.group;   // prefix: t is b T + t
-            seen[u] = c.prefix ? len : len - p.T + 1 + t;
+            const int r = w.r0 + g + 8 * u;
+            const bool live = g + 8 * u < w.rows;
+            const int t = p.by_group.of(r), h = w.head * p.group + r - t * p.group;   // prefix: t is b T + t
+            seen[u] = w.prefix ? w.len : w.len - p.T + 1 + t;
             const uint32_t* q = reinterpret_cast<const uint32_t*>(static_cast<const T*>(a.q) +
-                                                                  (live ? ((long long)b * p.T + t) * a.q_stride + h * D : 0));
+                                                                  (live ? ((long long)w.b * p.T + t) * a.q_stride + h * D : 0));
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
                 qf[k][u] = live ? __ldca(q + (k * 16 + t2) / 2) : 0u;
@@ -138,11 +175,13 @@ __global__ void __launch_bounds__(kThreads) attn_few_kernel(const FewArgs a) {
         for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
         float m[2] = {kNone, kNone}, l[2] = {0.0f, 0.0f};
 
-        for (int t = 0; t < nt; ++t) {
-            copy(t + C::kStages - 1);
+#pragma unroll 1
+        for (int t = 0; t < w.n; ++t) {
+            copy();
             tc::cp_async_wait<C::kStages - 1>();
             __syncwarp();
-            const uint32_t st = ring + (t % C::kStages) * C::kStageBytes;
+            const uint32_t st = ring + slot * C::kStageBytes;
+            if (++slot == C::kStages) slot = 0;
             float s[2][4] = {};
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
@@ -151,27 +190,27 @@ __global__ void __launch_bounds__(kThreads) attn_few_kernel(const FewArgs a) {
                 mma<T>(s[0], qf[k], kf[0], kf[1]);
                 mma<T>(s[1], qf[k], kf[2], kf[3]);
             }
-            const int k0 = key0 + t * kTile + wid * kKeys;
+            const int k0 = w.key0 + t * kKeys;
             float mx[2] = {m[0], m[1]};
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int key = k0 + j * 8 + t2 + (e & 1);
-                    s[j][e] = key < seen[e >> 1] ? s[j][e] * a.scale_log2 : kNone;
+                    const int key_at = k0 + j * 8 + t2 + (e & 1);
+                    s[j][e] = key_at < seen[e >> 1] ? s[j][e] * a.scale_log2 : kNone;
                     mx[e >> 1] = fmaxf(mx[e >> 1], s[j][e]);
                 }
             if constexpr (RAW) {
-                if (!c.prefix) {
+                if (!w.prefix) {
 #pragma unroll
                     for (int u = 0; u < 2; ++u)
-                        if (g + 8 * u < nrows) {
-                            float* raw = a.raw + (((long long)b * p.Hkv + c.head) * tg + r0 + g + 8 * u) * p.own_cap;
+                        if (g + 8 * u < w.rows) {
+                            float* raw = a.raw + (((long long)w.b * p.Hkv + w.head) * tg + w.r0 + g + 8 * u) * p.own_cap;
 #pragma unroll
                             for (int j = 0; j < 2; ++j)
 #pragma unroll
                                 for (int e = 0; e < 2; ++e)
-                                    if (k0 + j * 8 + t2 + e < len) raw[k0 + j * 8 + t2 + e] = s[j][2 * u + e];
+                                    if (k0 + j * 8 + t2 + e < w.len) raw[k0 + j * 8 + t2 + e] = s[j][2 * u + e];
                         }
                 }
             }
@@ -214,49 +253,23 @@ __global__ void __launch_bounds__(kThreads) attn_few_kernel(const FewArgs a) {
             }
             __syncwarp();   // the stage may be written again
         }
-        tc::cp_async_wait<0>();
-        // join the four warps
+        const long long place = ((long long)blockIdx.x + w.seg) * kFewRows;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             l[u] += __shfl_xor_sync(0xffffffffu, l[u], 1);
             l[u] += __shfl_xor_sync(0xffffffffu, l[u], 2);
-            if ((lane & 3) == 0) s_ml[wid][g + 8 * u] = make_float2(m[u], l[u]);
-        }
-        __syncthreads();
-        float* join = reinterpret_cast<float*>(s_ring);
+            const int r = g + 8 * u;
+            if (r < w.rows) {
+                if ((lane & 3) == 0) a.out.ml[place + r] = make_float2(m[u], l[u]);
+                float* to = a.out.o + (place + r) * D + t2;   // a quad writes whole 32-byte sectors
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            float mm = kNone;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, s_ml[w][g + 8 * u].x);
-            const float f = exp2_fast(m[u] - (mm == kNone ? 0.0f : mm));
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i)
-                *reinterpret_cast<float2*>(join + (wid * kFewRows + g + 8 * u) * D + i * 8 + t2) =
-                    make_float2(o[i][2 * u] * f, o[i][2 * u + 1] * f);
-        }
-        __syncthreads();
-        const long long place = (long long)blockIdx.x + c.seg;
-        for (int i = tid; i < nrows * (D / 4); i += kThreads) {
-            float4 sum = *reinterpret_cast<const float4*>(join + i * 4);
-#pragma unroll
-            for (int w = 1; w < kWarps; ++w) {
-                const float4 x = *reinterpret_cast<const float4*>(join + w * kFewRows * D + i * 4);
-                sum.x += x.x, sum.y += x.y, sum.z += x.z, sum.w += x.w;
+                for (int i = 0; i < D / 8; ++i) *reinterpret_cast<float2*>(to + i * 8) = make_float2(o[i][2 * u], o[i][2 * u + 1]);
             }
-            *reinterpret_cast<float4*>(a.out.o + place * kFewRows * D + i * 4) = sum;
         }
-        if (tid < nrows) {
-            float mm = kNone, ll = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, s_ml[w][tid].x);
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) ll += s_ml[w][tid].y * exp2_fast(s_ml[w][tid].x - (mm == kNone ? 0.0f : mm));
-            a.out.ml[place * kFewRows + tid] = make_float2(mm, ll);
-        }
-        __syncthreads();   // s_ml and the ring are free again
-        advance(p, a.len, c, nt);
     }
+    tc::cp_async_wait<0>();
+    // what follows counts on attn_many too
+    if (a.beside) mq_grid_wait();
 }
 
 template <typename T, int D, bool RAW>
@@ -279,15 +292,6 @@ int with_kernel(int D, int type, bool raw, F f) {
 }
 
 }  // namespace
-
-int few_tile_keys(int) { return kTile; }
-
-int few_blocks(int D, int type) {
-    return with_kernel(D, type, false, [](auto kern, int smem) {
-        if (!allow_smem(reinterpret_cast<const void*>(kern), smem)) return mq::num_sms();
-        return mq::num_sms() * mq::resident_blocks(reinterpret_cast<const void*>(kern), kThreads, smem);
-    });
-}
 
 int launch_few(const FewArgs& a, int D, int type, cudaStream_t stream) {
     return with_kernel(D, type, a.raw != nullptr, [&](auto kern, int smem) {

@@ -16,12 +16,13 @@ struct FewArgs {
     float scale_log2;                               // scale * log2 e
     Pieces out;
     float* raw;       // [B][Hkv][T group][cap] scaled products of the own keys (base 2), or nullptr
+    int beside;       // launched behind attn_many, whose results it does not need
 };
 
 constexpr int kFewRows = 16;      // query rows per segment
-int few_tile_keys(int D);         // keys per tile
-// Blocks that the device holds at once, for a head width of D.
-int few_blocks(int D, int type);
+constexpr int kFewKeys = 16;      // keys per tile
+constexpr int kFewExtra = 4;      // what beginning and ending a segment costs, in tiles
+constexpr int kFewPerSm = 8;      // blocks (of one warp) per SM
 int launch_few(const FewArgs& a, int D, int type, cudaStream_t stream);
 
 }  // namespace attn

@@ -197,7 +197,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Plan& p = a.plan;
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
 
-    mq_grid_release();
     if (tid == 0) {
         for (int i = 0; i < C::kRing; ++i) {
             tc::mbar_init(&bars.full[i], 1);
@@ -231,6 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::prefetch_tensormap(&ov);
     }
     mq_grid_wait();
+    mq_grid_release();   // only now: what is launched behind may run beside this kernel without waiting for it
     tc::tc_fence_before();
     Cursor c = find_run<kThreads>(p, a.len);   // holds block barriers
     __syncthreads();
