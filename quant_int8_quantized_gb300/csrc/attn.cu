@@ -33,6 +33,7 @@ namespace {
 struct Part {
     Pieces p;
     int rows;      // per segment; 0: no such part
+    Plan plan;
 };
 
 struct JoinArgs {
@@ -52,61 +53,61 @@ struct Run {
 
 // Pieces of row `in` of a segment whose blocks are f.x .. f.y.
 __device__ __forceinline__ Run run_of(const Part& p, int seg, int2 f, int in) {
-    return Run{&p.p, ((long long)f.x + seg) * p.rows + in, p.rows, f.y - f.x + 1};
+    return Run{&p.p, (long long)place_of(p.plan, f.x, seg) * p.rows + in, p.rows, f.y - f.x + 1};
 }
 
-// One warp adds up a row's pieces: their common maximum, then outputs weighted and added in order. Lane i
-// holds maximum and sum of piece i of 32; the outputs' loads do not depend on one another.
-template <typename O, int D, int N>
-__device__ __forceinline__ void join_row(const Run (&runs)[N], const Out& fin, float* lse2, long long row) {
+// One warp adds up a row's pieces, those of run 0 and then those of run 1: their common maximum, then outputs
+// weighted and added in order. Lane i holds place, maximum and sum of piece i of 32; the outputs' loads do not
+// depend on one another.
+template <typename O, int D>
+__device__ __forceinline__ void join_row(const Run& r0, const Run& r1, const Out& fin, float* lse2, long long row) {
     // lane l holds V floats at V (l + 32 k)
     constexpr int V = D >= 128 ? 4 : 2, W = (D + 32 * V - 1) / (32 * V);
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, count = r0.count + r1.count;
     float m = -INFINITY, l = 0.0f;
     float acc[W][V] = {};
-#pragma unroll
-    for (int w = 0; w < N; ++w) {
 #pragma unroll 1
-        for (int i0 = 0; i0 < runs[w].count; i0 += 32) {
-            const int n = min(32, runs[w].count - i0);
-            const long long first = runs[w].first + i0 * runs[w].stride;
-            float2 ml = make_float2(-INFINITY, 0.0f);
-            if (lane < n) ml = __ldca(runs[w].p->ml + first + lane * runs[w].stride);
-            float now = fmaxf(m, ml.x);
+    for (int i0 = 0; i0 < count; i0 += 32) {
+        const int n = min(32, count - i0), i = i0 + lane;
+        const bool second = i >= r0.count;
+        const Run& r = second ? r1 : r0;
+        const long long at = r.first + (second ? i - r0.count : i) * r.stride;
+        float2 ml = make_float2(-INFINITY, 0.0f);
+        if (lane < n) ml = __ldca(r.p->ml + at);
+        const unsigned long long from = reinterpret_cast<unsigned long long>(lane < n ? r.p->o + at * D : nullptr);
+        float now = fmaxf(m, ml.x);
 #pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, o));
-            const float safe = now == -INFINITY ? 0.0f : now;
-            const float back = exp2f(m - safe), f = exp2f(ml.x - safe);
-            m = now;
-            float sum = ml.y == 0.0f ? 0.0f : ml.y * f;
+        for (int o = 16; o >= 1; o >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, o));
+        const float safe = now == -INFINITY ? 0.0f : now;
+        const float back = exp2f(m - safe), f = exp2f(ml.x - safe);
+        m = now;
+        float sum = ml.y == 0.0f ? 0.0f : ml.y * f;
 #pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            l = l * back + sum;
+        for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        l = l * back + sum;
+#pragma unroll
+        for (int k = 0; k < W; ++k)
+#pragma unroll
+            for (int e = 0; e < V; ++e) acc[k][e] *= back;
+#pragma unroll 8
+        for (int j = 0; j < n; ++j) {
+            const float g = __shfl_sync(0xffffffffu, f, j);
+            const float* oi = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, from, j));
 #pragma unroll
             for (int k = 0; k < W; ++k)
-#pragma unroll
-                for (int e = 0; e < V; ++e) acc[k][e] *= back;
-            const float* o = runs[w].p->o + first * D;
-#pragma unroll 8
-            for (int i = 0; i < n; ++i) {
-                const float g = __shfl_sync(0xffffffffu, f, i);
-                const float* oi = o + i * runs[w].stride * D;
-#pragma unroll
-                for (int k = 0; k < W; ++k)
-                    if (V * (k * 32 + lane) < D) {
-                        if constexpr (V == 4) {
-                            const float4 x = __ldca(reinterpret_cast<const float4*>(oi) + k * 32 + lane);
-                            acc[k][0] = fmaf(x.x, g, acc[k][0]);
-                            acc[k][1] = fmaf(x.y, g, acc[k][1]);
-                            acc[k][2] = fmaf(x.z, g, acc[k][2]);
-                            acc[k][3] = fmaf(x.w, g, acc[k][3]);
-                        } else {
-                            const float2 x = __ldca(reinterpret_cast<const float2*>(oi) + k * 32 + lane);
-                            acc[k][0] = fmaf(x.x, g, acc[k][0]);
-                            acc[k][1] = fmaf(x.y, g, acc[k][1]);
-                        }
+                if (V * (k * 32 + lane) < D) {
+                    if constexpr (V == 4) {
+                        const float4 x = __ldca(reinterpret_cast<const float4*>(oi) + k * 32 + lane);
+                        acc[k][0] = fmaf(x.x, g, acc[k][0]);
+                        acc[k][1] = fmaf(x.y, g, acc[k][1]);
+                        acc[k][2] = fmaf(x.z, g, acc[k][2]);
+                        acc[k][3] = fmaf(x.w, g, acc[k][3]);
+                    } else {
+                        const float2 x = __ldca(reinterpret_cast<const float2*>(oi) + k * 32 + lane);
+                        acc[k][0] = fmaf(x.x, g, acc[k][0]);
+                        acc[k][1] = fmaf(x.y, g, acc[k][1]);
                     }
-            }
+                }
         }
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;   // l == 0: no key seen (a NaN or infinite l stays one)
@@ -134,32 +135,40 @@ __device__ __forceinline__ void join_row(const Run (&runs)[N], const Out& fin, f
 }
 
 // Every query row, a warp each: its prefix segment's pieces, then its own segment's.
+constexpr int kJoinWarps = 4;
 template <typename O, int D>
-__global__ void __launch_bounds__(256) attn_join_kernel(const JoinArgs a) {
+__global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const JoinArgs a) {
     mq_grid_release();
     mq_grid_wait();
-    const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);   // (b T + t) Hq + h
+    const long long row = (long long)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);   // (b T + t) Hq + h
     if (row >= (long long)a.B * a.T * a.Hq) return;
     const int h = (int)(row % a.Hq);
     const long long bt = row / a.Hq;
     const int t = (int)(bt % a.T), b = (int)(bt / a.T);
     const int hk = h / a.group, tg = a.T * a.group;
     const int r_own = t * a.group + h - hk * a.group;
+    // both parts' entries are read at once (an own segment without tiles has none: what lies there is not used)
     Run runs[2] = {};
+    int seg0 = 0, seg1 = 0, in0 = 0, in1 = 0, last = 0;
+    int2 f0 = make_int2(0, 0), f1 = f0;
+    int len = 0;
     if (a.prefix.rows > 0) {
         const int r = b * tg + r_own, rt = r / a.prefix.rows;
-        const int seg = rt * a.Hkv + hk;
-        runs[0] = run_of(a.prefix, seg, __ldca(a.prefix.p.info + seg), r - rt * a.prefix.rows);
+        seg0 = rt * a.Hkv + hk;
+        in0 = r - rt * a.prefix.rows;
+        f0 = __ldca(a.prefix.p.info + seg0);
     }
     if (a.own.rows > 0) {
         const int rt = r_own / a.own.rows;
-        const int last = min((rt + 1) * a.own.rows, tg) - 1;
-        if (min(max(__ldca(a.len + b), 0), a.own_cap) - a.T + 1 + last / a.group > 0) {
-            const int seg = a.seg0 + (b * ceil_div(tg, a.own.rows) + rt) * a.Hkv + hk;
-            runs[1] = run_of(a.own, seg, __ldca(a.own.p.info + seg), r_own - rt * a.own.rows);
-        }
+        last = min((rt + 1) * a.own.rows, tg) - 1;
+        seg1 = a.seg0 + (b * ceil_div(tg, a.own.rows) + rt) * a.Hkv + hk;
+        in1 = r_own - rt * a.own.rows;
+        len = __ldca(a.len + b);
+        f1 = __ldca(a.own.p.info + seg1);
     }
-    join_row<O, D>(runs, a.fin, a.lse2, row);
+    if (a.prefix.rows > 0) runs[0] = run_of(a.prefix, seg0, f0, in0);
+    if (a.own.rows > 0 && min(max(len, 0), a.own_cap) - a.T + 1 + last / a.group > 0) runs[1] = run_of(a.own, seg1, f1, in1);
+    join_row<O, D>(runs[0], runs[1], a.fin, a.lse2, row);
 }
 
 // The rows of the segments that one block of the first kernel began and another ended: grid x that block, y eight
@@ -181,8 +190,7 @@ __global__ void __launch_bounds__(256) attn_join_split_kernel(const SplitArgs a)
     const int in = blockIdx.y * 8 + (threadIdx.x >> 5);
     if (in >= rows) return;
     const int r = rt * a.plan.rows + in, t = a.plan.by_group.of(r);
-    const Run runs[1] = {run_of(a.part, s.x, make_int2(blockIdx.x, s.y), in)};
-    join_row<O, D>(runs, a.fin, nullptr,
+    join_row<O, D>(run_of(a.part, s.x, make_int2(blockIdx.x, s.y), in), Run{}, a.fin, nullptr,
                    ((long long)b * a.plan.T + t) * a.plan.Hq + s.w * a.plan.group + r - t * a.plan.group);
 }
 
@@ -216,6 +224,10 @@ size_t up16(size_t n) { return (n + 15) & ~(size_t)15; }
 // Query rows per key head from which the tensor-core kernel takes the shared prefix, and from which it takes
 // a sequence's own rows (and with them the prefix, its keys then read once per sequence).
 constexpr int kPrefixMany = 33, kOwnMany = 128;
+// Bytes of the prefix from which several row tiles of it are taken side by side, and how many at most: more of them
+// leave more of the blocks that they do not divide idle.
+constexpr long long kLanesFrom = 24 << 20;
+constexpr int kLanesMost = 8;
 
 // How a call is cut: the part of each kernel, and where the workspace holds what.
 struct Cut {
@@ -251,12 +263,23 @@ Cut cut_of(int B, int T, int Hq, int Hkv, int D, int prefix_keys, int own_cap, b
         p.extra = many ? kManyExtra : kFewExtra;
         p.by_group = div_by(group);
         p.by_per_seq = div_by(p.own ? own_tiles_of_rows(p) : 1);
+        p.lanes = 1;
+        if (many && p.prefix_keys > 0 && 2LL * prefix_keys * Hkv * D * 2 > kLanesFrom) {
+            // row tiles of one size side by side, where the keys would not stay in L2 from one to the next
+            const int n = ceil_div(p.prefix_rows, p.rows);
+            if (n > 1 && n <= kLanesMost) {
+                p.lanes = n;
+                p.rows = ceil_div(B * T, n) * group;
+                p.lanes = ceil_div(p.prefix_rows, p.rows);
+            }
+        }
         const long long segs = all_segs(p);
         const long long most = (long long)prefix_segs(p) * ceil_div(p.prefix_keys, p.keys) +
                                (segs - prefix_segs(p)) * (ceil_div(p.lead_keys, p.keys) + ceil_div(p.own_cap, p.keys));
         if (most * 2 + segs * p.extra > 0x7fffffffLL) c.fits = false;
         const long long held = (long long)mq::num_sms() * (many ? 1 : kFewPerSm);
         p.G = (int)(most < held ? most : held);
+        if (p.lanes > 1) p.G = p.G / p.lanes * p.lanes;
         const size_t places = segs > 0 ? (size_t)p.G + (size_t)segs : 0;
         *o = at;
         at += up16(places * p.rows * D * sizeof(float));
@@ -352,7 +375,7 @@ extern "C" int mq_attn_prefix(const void* q, long long q_stride, int B, int T, i
         rc = launch_many(m, P > 0 ? prefix : nullptr, c.own_many ? own : nullptr, D, type, stream);
         if (rc != MQ_OK) return rc;
         if (c.own_many) {
-            const SplitArgs s = {{many, c.many.rows}, m.split, c.many, fin};
+            const SplitArgs s = {{many, c.many.rows, c.many}, m.split, c.many, fin};
             const int most = T * (Hq / Hkv) < c.many.rows ? T * (Hq / Hkv) : c.many.rows;
             auto join = [&](auto o) {
                 using O = decltype(o);
@@ -385,8 +408,9 @@ extern "C" int mq_attn_prefix(const void* q, long long q_stride, int B, int T, i
         if (rc != MQ_OK) return rc;
     }
     JoinArgs j;
-    j.prefix = {c.prefix_many ? many : few, P > 0 ? (c.prefix_many ? c.many.rows : kFewRows) : 0};
-    j.own = {few, cap > 0 ? kFewRows : 0};
+    j.prefix = {c.prefix_many ? many : few, P > 0 ? (c.prefix_many ? c.many.rows : kFewRows) : 0,
+                c.prefix_many ? c.many : c.few};
+    j.own = {few, cap > 0 ? kFewRows : 0, c.few};
     j.len = own_len;
     j.B = B;
     j.T = T;
@@ -397,12 +421,12 @@ extern "C" int mq_attn_prefix(const void* q, long long q_stride, int B, int T, i
     j.seg0 = prefix_segs(c.few);
     j.fin = fin;
     j.lse2 = lse2;
-    const dim3 grid((unsigned)(((long long)B * T * Hq + 7) / 8));
+    const dim3 grid((unsigned)(((long long)B * T * Hq + kJoinWarps - 1) / kJoinWarps));
     auto join = [&](auto o) {
         using O = decltype(o);
         auto kern = D == 64 ? attn_join_kernel<O, 64> : D == 96 ? attn_join_kernel<O, 96>
                     : D == 128 ? attn_join_kernel<O, 128> : attn_join_kernel<O, 256>;
-        return mq::launch_pdl(kern, grid, dim3(256), 0, stream, j);
+        return mq::launch_pdl(kern, grid, dim3(32 * kJoinWarps), 0, stream, j);
     };
     rc = out_type == MQ_F32 ? join(float()) : out_type == MQ_F16 ? join(__half()) : join(__nv_bfloat16());
     if (rc != MQ_OK || !scores) return rc;

@@ -38,6 +38,7 @@ struct Plan {
     int rows;                       // query rows per segment
     int keys;                       // keys per tile
     int G;
+    int lanes;                      // prefix segments only: blocks side by side, one row tile each, over the same keys
     Div by_group, by_per_seq;       // by group; by the row tiles of a sequence (1 where there are none)
     int wide, extra;                // cost of a tile with more than `wide` rows is 2, else 1; `extra` once a segment
 };
@@ -113,15 +114,45 @@ __device__ __forceinline__ int piece_tiles(const Plan& p, const Cursor& c) {
     const int base = c.at - cost_before(p, c.in, c.cost);   // cost before the segment
     return min(c.tiles, tile_at(p, c.end - base, c.cost)) - c.in;
 }
+// This block's number in its row of tiles, and the place there of a piece of segment seg.
+__device__ __forceinline__ int block_in_lane(const Plan& p) { return p.lanes > 1 ? blockIdx.x / p.lanes : blockIdx.x; }
+__host__ __device__ inline int place_of(const Plan& p, int block, int seg) {
+    if (p.lanes == 1) return block + seg;
+    const int lane = seg / p.Hkv;
+    return lane * (p.G / p.lanes + p.Hkv) + block + seg - lane * p.Hkv;
+}
 // First and last block of the segment that c is at the start of.
 __device__ __forceinline__ int2 blocks_of(const Plan& p, const Cursor& c) {
-    return make_int2(blockIdx.x, block_of(c, c.at + cost_before(p, c.tiles - 1, c.cost)));
+    return make_int2(block_in_lane(p), block_of(c, c.at + cost_before(p, c.tiles - 1, c.cost)));
 }
 
 // Finds the block's run. Segments follow one another as unit, then head. Threads share the
 // units (sequence and row tile) and scan the sums of their costs: THREADS threads, all of the block.
 template <int THREADS>
 __device__ __forceinline__ Cursor find_run(const Plan& p, const int32_t* len) {
+    if (p.lanes > 1) {              // a row of prefix tiles of one row tile, the same for all lanes
+        Cursor c;
+        const int lane_of = blockIdx.x % p.lanes, i = blockIdx.x / p.lanes;
+        const int one = seg_cost(p, ceil_div(p.prefix_keys, p.keys), 1);
+        const int total = one * p.Hkv, most = total / (p.extra + 1);
+        const int blocks = most < 1 ? 1 : min(most, p.G / p.lanes);
+        c.at = c.end = 0;
+        if (i >= blocks) return c;
+        c.per = total / blocks;
+        c.longer = total - c.per * blocks;
+        const int begin = i * c.per + min(i, c.longer);
+        c.end = begin + c.per + (i < c.longer);
+        c.prefix = true;
+        c.unit = lane_of;
+        c.cost = 1;
+        c.tiles = ceil_div(p.prefix_keys, p.keys);
+        c.head = begin / one;
+        c.seg = lane_of * p.Hkv + c.head;
+        const int base = c.head * one;
+        c.in = tile_at(p, begin - base, 1);
+        c.at = base + (c.in < c.tiles ? cost_before(p, c.in, 1) : one);
+        return c;
+    }
     constexpr int kWarps = THREADS / 32;
     __shared__ int s_sum[kWarps];
     __shared__ int s_at[3];         // unit, cost before it, its tiles

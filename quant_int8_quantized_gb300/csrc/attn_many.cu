@@ -65,7 +65,7 @@ struct Cfg {
 struct Piece {
     int n, in;           // tiles, and those of the segment before them
     int lead;            // tiles of the shared prefix at the segment's head (own segments)
-    int seg, head;
+    int place, head;     // of the piece; key head
     int b, bt;           // sequence; first query, counted over the batch
     int rows, len;       // query rows; keys of the part
     int see;             // keys that the segment's first query sees (prefix: all)
@@ -261,6 +261,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = j0; j < g.n; j += step) {
                 if (!(alive = wwait(bars, &bars.s_full[h], s_phase))) break;
                 s_phase ^= 1;
+                if (n_rows <= 0) {                             // none of the warp's rows counts
+                    if (lane == 0) tc::mbar_arrive(&bars.p_ready[h]);
+                    pv_phase ^= 1;
+                    continue;
+                }
                 tc::tc_fence_after();
                 uint32_t s[4][32];
 #pragma unroll
@@ -358,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // Rows go out whole, 128 bytes at a time through the stage: in 16 bits or f32 where they are finished,
                 // as they are (f32) to the piece's place otherwise.
                 const bool finish = a.split && g.whole;
-                const long long place = ((long long)blockIdx.x + g.seg) * p.rows + half0 + quarter * 32;
+                const long long place = (long long)g.place * p.rows + half0 + quarter * 32;
                 const long long out_row = finish ? ((long long)g.bt + q_in) * p.Hq + g.head * p.group + r - q_in * p.group
                                                  : place + lane;
                 const bool narrow = finish && !a.fin.f32;
@@ -595,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (c.more()) {
                     g.n = piece_tiles(p, c);
                     g.in = c.in;
-                    g.seg = c.seg;
+                    g.place = place_of(p, block_in_lane(p), c.seg);
                     g.head = c.head;
                     g.prefix = c.prefix;
                     g.b = c.prefix ? 0 : p.by_per_seq.of(c.unit);
