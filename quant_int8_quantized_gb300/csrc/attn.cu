@@ -62,7 +62,7 @@ __device__ __forceinline__ Run run_of(const Part& p, int seg, int2 f, int in) {
 template <typename O, int D>
 __device__ __forceinline__ void join_row(const Run& r0, const Run& r1, const Out& fin, float* lse2, long long row) {
     // lane l holds V floats at V (l + 32 k)
-    constexpr int V = D >= 128 ? 4 : 2, W = (D + 32 * V - 1) / (32 * V);
+    constexpr int V = D >= 128 ? 4 : 2, W = (D + 32 * V - 1) / (32 * V), kAtOnce = 8;   // divides 32
     const int lane = threadIdx.x & 31, count = r0.count + r1.count;
     float m = -INFINITY, l = 0.0f;
     float acc[W][V] = {};
@@ -89,25 +89,35 @@ __device__ __forceinline__ void join_row(const Run& r0, const Run& r1, const Out
         for (int k = 0; k < W; ++k)
 #pragma unroll
             for (int e = 0; e < V; ++e) acc[k][e] *= back;
-#pragma unroll 8
-        for (int j = 0; j < n; ++j) {
-            const float g = __shfl_sync(0xffffffffu, f, j);
-            const float* oi = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, from, j));
+#pragma unroll 1
+        for (int j0 = 0; j0 < n; j0 += kAtOnce) {
+            float x[kAtOnce][W][V], g[kAtOnce];
 #pragma unroll
-            for (int k = 0; k < W; ++k)
-                if (V * (k * 32 + lane) < D) {
-                    if constexpr (V == 4) {
-                        const float4 x = __ldca(reinterpret_cast<const float4*>(oi) + k * 32 + lane);
-                        acc[k][0] = fmaf(x.x, g, acc[k][0]);
-                        acc[k][1] = fmaf(x.y, g, acc[k][1]);
-                        acc[k][2] = fmaf(x.z, g, acc[k][2]);
-                        acc[k][3] = fmaf(x.w, g, acc[k][3]);
-                    } else {
-                        const float2 x = __ldca(reinterpret_cast<const float2*>(oi) + k * 32 + lane);
-                        acc[k][0] = fmaf(x.x, g, acc[k][0]);
-                        acc[k][1] = fmaf(x.y, g, acc[k][1]);
+            for (int j = 0; j < kAtOnce; ++j) {
+                g[j] = __shfl_sync(0xffffffffu, f, j0 + j);
+                const float* oi = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, from, j0 + j));
+#pragma unroll
+                for (int k = 0; k < W; ++k) {
+#pragma unroll
+                    for (int e = 0; e < V; ++e) x[j][k][e] = 0.0f;
+                    if (j0 + j < n && V * (k * 32 + lane) < D) {
+                        if constexpr (V == 4) {
+                            const float4 v = __ldca(reinterpret_cast<const float4*>(oi) + k * 32 + lane);
+                            x[j][k][0] = v.x, x[j][k][1] = v.y, x[j][k][2] = v.z, x[j][k][3] = v.w;
+                        } else {
+                            const float2 v = __ldca(reinterpret_cast<const float2*>(oi) + k * 32 + lane);
+                            x[j][k][0] = v.x, x[j][k][1] = v.y;
+                        }
                     }
                 }
+            }
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j)
+                if (j0 + j < n)
+#pragma unroll
+                    for (int k = 0; k < W; ++k)
+#pragma unroll
+                        for (int e = 0; e < V; ++e) acc[k][e] = fmaf(x[j][k][e], g[j], acc[k][e]);
         }
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;   // l == 0: no key seen (a NaN or infinite l stays one)
@@ -194,29 +204,51 @@ __global__ void __launch_bounds__(256) attn_join_split_kernel(const SplitArgs a)
                    ((long long)b * a.plan.T + t) * a.plan.Hq + s.w * a.plan.group + r - t * a.plan.group);
 }
 
-// score_out = score + sum over the rows of 2^(raw - lse2), one thread a key.
-__global__ void __launch_bounds__(256) attn_score_kernel(const float* raw, const float* lse2, const int32_t* len,
+// score_out = score + sum over the rows of 2^(raw - lse2), four keys a thread (one where the rows of raw do not
+// begin on 16 bytes).
+template <int V>
+__global__ void __launch_bounds__(128) attn_score_kernel(const float* raw, const float* lse2, const int32_t* len,
                                                          const float* score, float* score_out, int T, int Hq, int Hkv,
                                                          int cap) {
     mq_grid_release();
     mq_grid_wait();
     const int b = blockIdx.y / Hkv, hk = blockIdx.y - b * Hkv;
     const int n = min(max(__ldca(len + b), 0), cap);
-    const int j = blockIdx.x * 256 + threadIdx.x;
+    const int j = (blockIdx.x * 128 + threadIdx.x) * V;
     if (j >= n) return;
-    const int group = Hq / Hkv, tg = T * group;
-    const float* s = raw + (long long)blockIdx.y * tg * cap + j;
-    float w = 0.0f;
-#pragma unroll 4
-    for (int r = 0; r < tg; ++r) {
-        const int t = r / group;
-        if (j >= n - T + 1 + t) continue;   // not seen; the first kernel left nothing there
-        const float l2 = __ldca(lse2 + ((long long)b * T + t) * Hq + hk * group + r - t * group);
-        const float x = __ldca(s + (long long)r * cap);
-        w += x == -INFINITY ? 0.0f : exp2f(x - l2);
-    }
+    const int group = Hq / Hkv;
+    const float* s = raw + (long long)blockIdx.y * T * group * cap + j;
     const long long at = (long long)blockIdx.y * cap + j;
-    score_out[at] = __ldca(score + at) + w;
+    float w[V] = {}, old[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) old[e] = j + e < n ? __ldca(score + at + e) : 0.0f;
+    constexpr int kAtOnce = 8;
+    const int rows = T * group;
+    for (int r0 = 0; r0 < rows; r0 += kAtOnce) {
+        float x[kAtOnce][V], l[kAtOnce];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i)
+            if (r0 + i < rows) {
+                const int t = (r0 + i) / group;
+                l[i] = __ldca(lse2 + ((long long)b * T + t) * Hq + hk * group + r0 + i - t * group);
+                if constexpr (V == 4) {
+                    const float4 v = __ldca(reinterpret_cast<const float4*>(s + (long long)(r0 + i) * cap));
+                    x[i][0] = v.x, x[i][1] = v.y, x[i][2] = v.z, x[i][3] = v.w;
+                } else {
+                    x[i][0] = __ldca(s + (long long)(r0 + i) * cap);
+                }
+            }
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i)
+            if (r0 + i < rows) {
+                const int seen = n - T + 1 + (r0 + i) / group;   // past it the first kernel left nothing
+#pragma unroll
+                for (int e = 0; e < V; ++e) w[e] += j + e < seen && x[i][e] != -INFINITY ? exp2f(x[i][e] - l[i]) : 0.0f;
+            }
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+        if (j + e < n) score_out[at + e] = old[e] + w[e];
 }
 
 size_t up16(size_t n) { return (n + 15) & ~(size_t)15; }
@@ -228,6 +260,7 @@ constexpr int kPrefixMany = 33, kOwnMany = 128;
 // leave more of the blocks that they do not divide idle.
 constexpr long long kLanesFrom = 24 << 20;
 constexpr int kLanesMost = 8;
+constexpr double kTileUs = 1.4, kDraw = 116e3;   // of a tile of two halves, measured; of an SM's eight warps with two stages in flight
 
 // How a call is cut: the part of each kernel, and where the workspace holds what.
 struct Cut {
@@ -260,7 +293,8 @@ Cut cut_of(int B, int T, int Hq, int Hkv, int D, int prefix_keys, int own_cap, b
         p.rows = many ? many_rows(group) : kFewRows;
         p.keys = many ? kManyKeys : kFewKeys;
         p.wide = many ? kManyHalf : kFewRows;
-        p.extra = many ? kManyExtra : kFewExtra;
+        p.cost = many ? kManyCost : 1;
+        p.wide_cost = many ? kManyWide : 1;
         p.by_group = div_by(group);
         p.by_per_seq = div_by(p.own ? own_tiles_of_rows(p) : 1);
         p.lanes = 1;
@@ -276,9 +310,18 @@ Cut cut_of(int B, int T, int Hq, int Hkv, int D, int prefix_keys, int own_cap, b
         const long long segs = all_segs(p);
         const long long most = (long long)prefix_segs(p) * ceil_div(p.prefix_keys, p.keys) +
                                (segs - prefix_segs(p)) * (ceil_div(p.lead_keys, p.keys) + ceil_div(p.own_cap, p.keys));
-        if (most * 2 + segs * p.extra > 0x7fffffffLL) c.fits = false;
         const long long held = (long long)mq::num_sms() * (many ? 1 : kFewPerSm);
+        p.extra = !many ? kFewExtra : p.own ? kManyExtra : kManyExtra / 2;
+        if (most * p.wide_cost + segs * p.extra > 0x7fffffffLL) c.fits = false;
         p.G = (int)(most < held ? most : held);
+        if (many && p.prefix_keys > 0 && own_cap > 0) {
+            // Beside it runs the kernel for few rows, on the SMs that this one leaves: so many that both end
+            // together if the caches are half full and each of its SMs draws kDraw bytes a us, but at most a third (they
+            // draw all that HBM gives).
+            const double own_bytes = (double)B * Hkv * own_cap * D * 2.0, work = (double)most * kTileUs;   // us of one SM
+            const int share = (int)(held / (1.0 + own_bytes / (work * kDraw)));
+            if (p.G > share) p.G = share > held - held / 3 ? share : (int)(held - held / 3 < p.G ? held - held / 3 : p.G);
+        }
         if (p.lanes > 1) p.G = p.G / p.lanes * p.lanes;
         const size_t places = segs > 0 ? (size_t)p.G + (size_t)segs : 0;
         *o = at;
@@ -430,6 +473,9 @@ extern "C" int mq_attn_prefix(const void* q, long long q_stride, int B, int T, i
     };
     rc = out_type == MQ_F32 ? join(float()) : out_type == MQ_F16 ? join(__half()) : join(__nv_bfloat16());
     if (rc != MQ_OK || !scores) return rc;
-    return mq::launch_pdl(attn_score_kernel, dim3((cap + 255) / 256, B * Hkv), dim3(256), 0, stream, raw, lse2, own_len,
-                          score, score_out, T, Hq, Hkv, cap);
+    auto score_call = [&](auto kern, int keys) {
+        return mq::launch_pdl(kern, dim3((cap + keys - 1) / keys, B * Hkv), dim3(128), 0, stream, raw, lse2, own_len,
+                              score, score_out, T, Hq, Hkv, cap);
+    };
+    return cap % 4 == 0 ? score_call(attn_score_kernel<4>, 512) : score_call(attn_score_kernel<1>, 128);
 }

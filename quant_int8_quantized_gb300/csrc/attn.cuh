@@ -40,7 +40,8 @@ struct Plan {
     int G;
     int lanes;                      // prefix segments only: blocks side by side, one row tile each, over the same keys
     Div by_group, by_per_seq;       // by group; by the row tiles of a sequence (1 where there are none)
-    int wide, extra;                // cost of a tile with more than `wide` rows is 2, else 1; `extra` once a segment
+    int wide, cost, wide_cost;      // cost of a tile with at most `wide` rows, and with more
+    int extra;                      // what a segment costs beside its tiles
 };
 
 __host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
@@ -59,7 +60,7 @@ __host__ __device__ inline long long all_segs(const Plan& p) {
 __host__ __device__ inline int rows_of(const Plan& p, int all, int rt) {
     return all - rt * p.rows < p.rows ? all - rt * p.rows : p.rows;
 }
-__host__ __device__ inline int tile_cost(const Plan& p, int rows) { return rows > p.wide ? 2 : 1; }
+__host__ __device__ inline int tile_cost(const Plan& p, int rows) { return rows > p.wide ? p.wide_cost : p.cost; }
 
 // Own keys that the last query of row tile rt sees; rows r = t * group + g.
 __device__ __forceinline__ int own_seen(const Plan& p, int len, int rt) {
@@ -104,9 +105,9 @@ __device__ __forceinline__ int seg_cost(const Plan& p, int tiles, int cost) {
 // Cost of a segment's tiles before tile i: the first one carries the segment's extra cost.
 __device__ __forceinline__ int cost_before(const Plan& p, int i, int cost) { return i > 0 ? p.extra + i * cost : 0; }
 // The first tile that begins at cost x of its segment or after.
-__device__ __forceinline__ int tile_at(const Plan& p, int x, int cost) {   // cost: 1 or 2
+__device__ __forceinline__ int tile_at(const Plan& p, int x, int cost) {
     if (x <= 0) return 0;
-    return max(1, (x - p.extra + cost - 1) >> (cost - 1));
+    return max(1, (x - p.extra + cost - 1) / cost);
 }
 
 // Tiles of the segment that belong to this run, from c.in on.
@@ -133,8 +134,8 @@ __device__ __forceinline__ Cursor find_run(const Plan& p, const int32_t* len) {
     if (p.lanes > 1) {              // a row of prefix tiles of one row tile, the same for all lanes
         Cursor c;
         const int lane_of = blockIdx.x % p.lanes, i = blockIdx.x / p.lanes;
-        const int one = seg_cost(p, ceil_div(p.prefix_keys, p.keys), 1);
-        const int total = one * p.Hkv, most = total / (p.extra + 1);
+        const int cost = p.wide_cost, one = seg_cost(p, ceil_div(p.prefix_keys, p.keys), cost);
+        const int total = one * p.Hkv, most = total / (p.extra + cost);
         const int blocks = most < 1 ? 1 : min(most, p.G / p.lanes);
         c.at = c.end = 0;
         if (i >= blocks) return c;
@@ -144,13 +145,13 @@ __device__ __forceinline__ Cursor find_run(const Plan& p, const int32_t* len) {
         c.end = begin + c.per + (i < c.longer);
         c.prefix = true;
         c.unit = lane_of;
-        c.cost = 1;
+        c.cost = cost;
         c.tiles = ceil_div(p.prefix_keys, p.keys);
         c.head = begin / one;
         c.seg = lane_of * p.Hkv + c.head;
         const int base = c.head * one;
-        c.in = tile_at(p, begin - base, 1);
-        c.at = base + (c.in < c.tiles ? cost_before(p, c.in, 1) : one);
+        c.in = tile_at(p, begin - base, cost);
+        c.at = base + (c.in < c.tiles ? cost_before(p, c.in, cost) : one);
         return c;
     }
     constexpr int kWarps = THREADS / 32;

@@ -174,6 +174,7 @@ __global__ void __launch_bounds__(kThreads) attn_few_kernel(const FewArgs a) {
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
         float m[2] = {kNone, kNone}, l[2] = {0.0f, 0.0f};
+        float* const raw_row = RAW ? a.raw + (((long long)w.b * p.Hkv + w.head) * tg + w.r0) * p.own_cap : nullptr;
 
 #pragma unroll 1
         for (int t = 0; t < w.n; ++t) {
@@ -205,12 +206,18 @@ __global__ void __launch_bounds__(kThreads) attn_few_kernel(const FewArgs a) {
 #pragma unroll
                     for (int u = 0; u < 2; ++u)
                         if (g + 8 * u < w.rows) {
-                            float* raw = a.raw + (((long long)w.b * p.Hkv + w.head) * tg + w.r0 + g + 8 * u) * p.own_cap;
+                            float* raw = raw_row + (g + 8 * u) * (long long)p.own_cap + k0 + t2;
+                            if (k0 + kKeys <= w.len && !(p.own_cap & 1)) {
 #pragma unroll
-                            for (int j = 0; j < 2; ++j)
+                                for (int j = 0; j < 2; ++j)
+                                    *reinterpret_cast<float2*>(raw + j * 8) = make_float2(s[j][2 * u], s[j][2 * u + 1]);
+                            } else {
 #pragma unroll
-                                for (int e = 0; e < 2; ++e)
-                                    if (k0 + j * 8 + t2 + e < w.len) raw[k0 + j * 8 + t2 + e] = s[j][2 * u + e];
+                                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                                    for (int e = 0; e < 2; ++e)
+                                        if (k0 + j * 8 + t2 + e < w.len) raw[j * 8 + e] = s[j][2 * u + e];
+                            }
                         }
                 }
             }

@@ -23,7 +23,10 @@ constexpr int kManyRows = 256;    // query rows per segment, at most
 constexpr int kManyHalf = 128;    // rows of one half
 constexpr int kManyKeys = 128;    // keys per tile
 
-constexpr int kManyExtra = 3;     // what beginning and ending a segment costs, in tiles of one half
+// Costs: a tile of two halves, a tile of a segment that one half would hold (its tiles alternate between the
+// halves: measured at two thirds of the former), a segment's beginning and end.
+constexpr int kManyCost = 2, kManyWide = 3, kManyExtra = 10;
+
 // Whole queries only: a segment's rows are one box of the queries' tensor map.
 inline int many_rows(int group) { return kManyRows / group * group; }
 
