@@ -253,9 +253,13 @@ __global__ void __launch_bounds__(128) attn_score_kernel(const float* raw, const
 
 size_t up16(size_t n) { return (n + 15) & ~(size_t)15; }
 
-// Query rows per key head from which the tensor-core kernel takes the shared prefix, and from which it takes
-// a sequence's own rows (and with them the prefix, its keys then read once per sequence).
-constexpr int kPrefixMany = 33, kOwnMany = 128;
+// The kernel for few rows reads a part's keys and values once for each 16 query rows of a key head, mostly out of L2.
+// Up to so many bytes that is quicker than the tensor-core kernel, which takes some 12 us whatever it does.
+#ifndef MQ_FEW_BYTES
+#define MQ_FEW_BYTES (24LL << 20)
+#endif
+constexpr long long kFewBytes = MQ_FEW_BYTES;
+constexpr int kManyFrom = 33;   // query rows per key head, at least, for the tensor-core kernel
 // Bytes of the prefix from which several row tiles of it are taken side by side, and how many at most: more of them
 // leave more of the blocks that they do not divide idle.
 constexpr long long kLanesFrom = 24 << 20;
@@ -272,9 +276,13 @@ struct Cut {
 Cut cut_of(int B, int T, int Hq, int Hkv, int D, int prefix_keys, int own_cap, bool scores) {
     Cut c;
     const int group = Hq / Hkv;
-    // the weights' raw products come from the kernel for few rows
-    c.own_many = own_cap > 0 && many_takes(D, group) && !scores && (long long)T * group >= kOwnMany;
-    c.prefix_many = prefix_keys > 0 && !c.own_many && many_takes(D, group) && (long long)B * T * group >= kPrefixMany;
+    // bytes that the kernel for few rows would read; the weights' raw products come from it
+    const long long row_tiles = ceil_div((long long)T * group, kFewRows), key_bytes = 4LL * Hkv * D;
+    const long long own_rows = (long long)T * group, prefix_rows = B * own_rows;
+    c.own_many = own_cap > 0 && many_takes(D, group) && !scores && own_rows >= kManyFrom &&
+                 B * row_tiles * (prefix_keys + (long long)own_cap) * key_bytes > kFewBytes;
+    c.prefix_many = prefix_keys > 0 && !c.own_many && many_takes(D, group) && prefix_rows >= kManyFrom &&
+                    ceil_div(prefix_rows, kFewRows) * prefix_keys * key_bytes > kFewBytes;
     c.fits = true;
     size_t at = 0;
     auto plan = [&](bool many, size_t* o, size_t* ml, size_t* info) {

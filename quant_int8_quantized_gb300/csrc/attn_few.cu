@@ -275,8 +275,9 @@ __global__ void __launch_bounds__(kThreads) attn_few_kernel(const FewArgs a) {
         }
     }
     tc::cp_async_wait<0>();
-    // what follows counts on attn_many too
-    if (a.beside) mq_grid_wait();
+    // what follows counts on attn_many too: the last block, and with it this kernel, ends after it (the others make
+    // room for more)
+    if (a.beside && blockIdx.x == gridDim.x - 1) mq_grid_wait();
 }
 
 template <typename T, int D, bool RAW>
