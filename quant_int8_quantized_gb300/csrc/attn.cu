@@ -441,21 +441,12 @@ extern "C" int mq_attn_prefix(const void* q, long long q_stride, int B, int T, i
         f.plan = c.few;
         f.q = q;
         f.q_stride = q_stride;
-        f.pk = P > 0 ? prefix->k : nullptr;
-        f.pv = P > 0 ? prefix->v : nullptr;
-        f.p_row = P > 0 ? prefix->row_stride : 0;
-        f.p_head = P > 0 ? prefix->head_stride : 0;
-        f.ok = cap > 0 ? own->k : nullptr;
-        f.ov = cap > 0 ? own->v : nullptr;
-        f.o_seq = cap > 0 ? own->seq_stride : 0;
-        f.o_row = cap > 0 ? own->row_stride : 0;
-        f.o_head = cap > 0 ? own->head_stride : 0;
         f.len = own_len;
         f.scale_log2 = scale * kLog2e;
         f.out = few;
         f.raw = raw;
         f.beside = all_segs(c.many) > 0;
-        rc = launch_few(f, D, type, stream);
+        rc = launch_few(f, P > 0 ? prefix : nullptr, cap > 0 ? own : nullptr, D, type, stream);
         if (rc != MQ_OK) return rc;
     }
     JoinArgs j;

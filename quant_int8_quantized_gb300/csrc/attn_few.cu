@@ -3,28 +3,38 @@
 // out of the way. They run as warp-wide 16 x 8 x 16 products in registers.
 //
 // A block is one warp with a run of its own, eight of them per SM, and nothing waits for anything else: the
-// warp copies tiles of 16 keys and values into its ring of stages (asynchronous 16-byte copies, rows past the end filled
-// with zeros, so nothing that lies there can reach a sum), keeps running maximum, sum and output in
-// registers and leaves the piece in the workspace. The copies run ahead across the ends of pieces. The
-// products q k^T come out in the layout that the second product takes as its left operand, so
-// probabilities stay in registers. Rows of a stage are padded by 16 bytes: eight rows of an 8 x 8 matrix
-// load then fall into eight different groups of banks.
+// warp copies tiles of 16 keys and values into its ring of stages (TMA: one lane issues a tile's few boxes, where
+// 16-byte copies of all lanes kept the warp busy and no more than some 60 bytes a ns on their way into an SM), keeps
+// running maximum, sum and output in registers and leaves the piece in the workspace. The copies run ahead
+// across the ends of pieces. The products q k^T come out in the layout that the second product takes as its
+// left operand, so probabilities stay in registers. The boxes' swizzle puts eight rows of an 8 x 8 matrix load into
+// eight different groups of banks. Value rows past a cache's length are zeroed in the stage: whatever lies there
+// must not reach a sum.
 
 #include "attn_few.cuh"
-#include "tc.cuh"
+#include "attn_maps.cuh"
 
 namespace attn {
 namespace {
+
+__device__ unsigned int g_few_error;   // bit 0: a bounded wait gave up
 
 constexpr int kThreads = 32;
 constexpr int kKeys = kFewKeys;
 
 template <int D>
 struct Cfg {
-    static constexpr int kPitch = D * 2 + 16;                 // bytes of a row of a stage
-    static constexpr int kStageBytes = 2 * kKeys * kPitch;    // keys, then values
-    static constexpr int kStages = D <= 64 ? 4 : D <= 128 ? 3 : 2;
-    static constexpr int kSmem = kStages * kStageBytes;
+    static constexpr int kDims = D % 64 == 0 ? 64 : 32;       // of a box
+    static constexpr int kRow = kDims * 2;                    // bytes of a row of it
+    static constexpr int kUnits = kDims / 8;                  // 16-byte units of that
+    static constexpr int kBoxes = D / kDims;
+    static constexpr int kBoxBytes = kKeys * kRow;
+    static constexpr int kTileBytes = kBoxes * kBoxBytes;     // of keys, or of values
+    static constexpr int kStageBytes = 2 * kTileBytes;        // keys, then values
+    static constexpr int kStages = D <= 64 ? 6 : D <= 96 ? 4 : D <= 128 ? 3 : 2;
+    static constexpr int kSmem = 1024 + kStages * kStageBytes;
+    // what the swizzle adds (xor) to the units of a row
+    __device__ static __forceinline__ int twist(int row) { return kDims == 64 ? row & 7 : (row >> 1) & 3; }
 };
 
 // A piece as the copying side hands it to the multiplying side. n == 0: the run is over.
@@ -72,25 +82,35 @@ __device__ __forceinline__ float exp2_fast(float x) {   // 2^x within 2 ulp; 2^-
 constexpr float kNone = -INFINITY;
 
 template <typename T, int D, bool RAW>
-__global__ void __launch_bounds__(kThreads) attn_few_kernel(const FewArgs a) {
+__global__ void __launch_bounds__(kThreads)
+    attn_few_kernel(const FewArgs a, const __grid_constant__ CUtensorMap pk, const __grid_constant__ CUtensorMap pv,
+                    const __grid_constant__ CUtensorMap ok, const __grid_constant__ CUtensorMap ov) {
     using C = Cfg<D>;
-    extern __shared__ __align__(16) uint8_t s_ring[];
+    extern __shared__ uint8_t s_raw[];
     __shared__ Piece s_piece[C::kStages + 1];
+    __shared__ uint64_t s_full[C::kStages];
     mq_grid_release();
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kStages; ++i) tc::mbar_init(&s_full[i], 1);
+        tc::fence_mbar_init();
+        tc::prefetch_tensormap(&pk);
+        tc::prefetch_tensormap(&pv);
+        tc::prefetch_tensormap(&ok);
+        tc::prefetch_tensormap(&ov);
+    }
     if (!a.beside) mq_grid_wait();
     const Plan& p = a.plan;
     const int lane = threadIdx.x;
     const int tg = p.T * p.group, per_seq = own_tiles_of_rows(p);
-    const uint32_t ring = tc::smem_u32(s_ring);
+    const uint32_t ring = (tc::smem_u32(s_raw) + 1023) & ~1023u;
     const int g = lane >> 2, t2 = (lane & 3) * 2;   // this thread's rows g, g + 8 and columns t2, t2 + 1
 
     // ---------------------------------------------------------------- copies, kStages - 1 tiles ahead
     Cursor c = find_run<kThreads>(p, a.len);
     advance(p, a.len, c, 0);
-    int left = 0, handed = 0, key = 0, klen = 0, in_slot = 0;    // tiles of the copied piece left, pieces handed over
-    const T *K = nullptr, *V = nullptr;
-    long long row_stride = 0;
-    const int my_row = lane / (D / 8), my_unit = lane % (D / 8);   // of the first copies of a stage
+    int left = 0, handed = 0, key = 0, in_slot = 0;    // tiles of the copied piece left, pieces handed over
+    int head = 0, seq = 0, issued = 0;
+    bool shared = false;
     auto copy = [&] {
         if (left == 0) {
             Piece q;
@@ -106,12 +126,10 @@ __global__ void __launch_bounds__(kThreads) attn_few_kernel(const FewArgs a) {
                 q.rows = min(kFewRows, (c.prefix ? p.prefix_rows : tg) - q.r0);
                 q.len = c.prefix ? p.prefix_keys : own_len_of(p, a.len, q.b);
                 if (lane == 0 && c.in == 0) a.out.info[c.seg] = blocks_of(p, c);
-                row_stride = c.prefix ? a.p_row : a.o_row;
-                const long long base = c.prefix ? c.head * a.p_head : q.b * a.o_seq + c.head * a.o_head;
-                K = static_cast<const T*>(c.prefix ? a.pk : a.ok) + base;
-                V = static_cast<const T*>(c.prefix ? a.pv : a.ov) + base;
+                head = c.head;
+                seq = q.b;
+                shared = c.prefix;
                 key = q.key0;
-                klen = q.len;
                 left = q.n;
                 advance(p, a.len, c, q.n);
             }
@@ -121,35 +139,36 @@ __global__ void __launch_bounds__(kThreads) attn_few_kernel(const FewArgs a) {
             if (++handed == C::kStages + 1) handed = 0;
         }
         if (left > 0) {
-            const uint32_t st = ring + in_slot * C::kStageBytes;
+            if (lane == 0) {
+                const uint32_t st = ring + in_slot * C::kStageBytes;
+                const CUtensorMap *km = shared ? &pk : &ok, *vm = shared ? &pv : &ov;
+                tc::mbar_arrive_expect_tx(&s_full[in_slot], C::kStageBytes);
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-                // unit i * 32 + lane of the stage's key rows (D / 8 units a row)
-                int kr, ku;
-                if constexpr (256 % D == 0) {   // a warp's units end with a row
-                    kr = i * (256 / D) + my_row;
-                    ku = my_unit;
-                } else {
-                    kr = (i * 32 + lane) / (D / 8);
-                    ku = (i * 32 + lane) % (D / 8);
+                for (int i = 0; i < C::kBoxes; ++i) {
+                    tma_load_4d(st + i * C::kBoxBytes, km, i * C::kDims, head, key, seq, &s_full[in_slot]);
+                    tma_load_4d(st + C::kTileBytes + i * C::kBoxBytes, vm, i * C::kDims, head, key, seq, &s_full[in_slot]);
                 }
-                const bool in = key + kr < klen;
-                const long long off = (in ? key + kr : 0) * row_stride + ku * 8;
-                tc::cp_async16_zfill(st + kr * C::kPitch + ku * 16, K + off, in ? 16 : 0);
-                tc::cp_async16_zfill(st + (kKeys + kr) * C::kPitch + ku * 16, V + off, in ? 16 : 0);
             }
+            ++issued;
             key += kKeys;
             --left;
             if (++in_slot == C::kStages) in_slot = 0;
         }
-        tc::cp_async_commit();
     };
 #pragma unroll 1
     for (int t = 0; t < C::kStages - 1; ++t) copy();
 
     // ---------------------------------------------------------------- products
+    // Byte of this lane's row and unit in a box, for the loads of keys (rows of eight keys, 8 dims side by side) and of
+    // values (transposed); unit 2 i of the row is this xor 32 i.
+    const int k_row = (lane >> 4) * 8 + (lane & 7), v_row = ((lane >> 3) & 1) * 8 + (lane & 7);
+    const uint32_t k_at = k_row * C::kRow + ((((lane >> 3) & 1) ^ C::twist(k_row)) << 4);
+    const uint32_t v_at = C::kTileBytes + v_row * C::kRow + (((lane >> 4) ^ C::twist(v_row)) << 4);
+    constexpr int kPairs = C::kUnits / 2;   // 16 dims each
     int taken = 0, slot = 0;
-    for (;;) {
+    uint32_t phase = 0;
+    bool alive = true;
+    while (alive) {
         const Piece w = s_piece[taken];
         if (w.n == 0) break;
         if (++taken == C::kStages + 1) taken = 0;
@@ -179,19 +198,33 @@ __global__ void __launch_bounds__(kThreads) attn_few_kernel(const FewArgs a) {
 #pragma unroll 1
         for (int t = 0; t < w.n; ++t) {
             copy();
-            tc::cp_async_wait<C::kStages - 1>();
-            __syncwarp();
+            if (!(alive = __all_sync(0xffffffffu, mbar_ready(&s_full[slot], phase) ||
+                                                      tc::mbar_wait(&s_full[slot], phase, kWaitLimitNs))))
+                break;
             const uint32_t st = ring + slot * C::kStageBytes;
-            if (++slot == C::kStages) slot = 0;
+            const int k0 = w.key0 + t * kKeys;
+            if (!w.prefix && k0 + kKeys > w.len) {   // (of the prefix what lies past the end reads as zeros)
+                for (int u = (w.len - k0) * C::kUnits + lane; u < kKeys * C::kUnits; u += 32)
+#pragma unroll
+                    for (int i = 0; i < C::kBoxes; ++i)
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(st + C::kTileBytes + i * C::kBoxBytes + u * 16),
+                                     "r"(0)
+                                     : "memory");
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+            }
+            if (++slot == C::kStages) {
+                slot = 0;
+                phase ^= 1;
+            }
             float s[2][4] = {};
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
                 uint32_t kf[4];
-                ldm4(st + ((lane >> 4) * 8 + (lane & 7)) * C::kPitch + (k * 16 + ((lane >> 3) & 1) * 8) * 2, kf);
+                ldm4(st + k / kPairs * C::kBoxBytes + (k_at ^ (k % kPairs * 32)), kf);
                 mma<T>(s[0], qf[k], kf[0], kf[1]);
                 mma<T>(s[1], qf[k], kf[2], kf[3]);
             }
-            const int k0 = w.key0 + t * kKeys;
             float mx[2] = {m[0], m[1]};
 #pragma unroll
             for (int j = 0; j < 2; ++j)
@@ -254,12 +287,13 @@ __global__ void __launch_bounds__(kThreads) attn_few_kernel(const FewArgs a) {
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
                 uint32_t vf[4];
-                ldm4t(st + (kKeys + ((lane >> 3) & 1) * 8 + (lane & 7)) * C::kPitch + (i * 16 + (lane >> 4) * 8) * 2, vf);
+                ldm4t(st + i / kPairs * C::kBoxBytes + (v_at ^ (i % kPairs * 32)), vf);
                 mma<T>(o[2 * i], pf, vf[0], vf[1]);
                 mma<T>(o[2 * i + 1], pf, vf[2], vf[3]);
             }
             __syncwarp();   // the stage may be written again
         }
+        if (!alive) break;
         const long long place = ((long long)blockIdx.x + w.seg) * kFewRows;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
@@ -274,7 +308,10 @@ __global__ void __launch_bounds__(kThreads) attn_few_kernel(const FewArgs a) {
             }
         }
     }
-    tc::cp_async_wait<0>();
+    if (!alive) {   // a copy never came: recorded; those still in flight must land before the block leaves
+        if (lane == 0) atomicOr(&g_few_error, 1u);
+        for (int i = 0; i < C::kStages && i < issued; ++i) tc::mbar_wait(&s_full[slot], phase, kWaitLimitNs);
+    }
     // what follows counts on attn_many too: the last block, and with it this kernel, ends after it (the others make
     // room for more)
     if (a.beside && blockIdx.x == gridDim.x - 1) mq_grid_wait();
@@ -301,11 +338,24 @@ int with_kernel(int D, int type, bool raw, F f) {
 
 }  // namespace
 
-int launch_few(const FewArgs& a, int D, int type, cudaStream_t stream) {
+int launch_few(const FewArgs& a, const mq_kv* prefix, const mq_kv* own, int D, int type, cudaStream_t stream) {
+    CUtensorMap pk, pv, ok, ov;
+    const mq_kv* p = prefix ? prefix : own;   // a part that is not there is never read
+    const mq_kv* o = own ? own : prefix;
+    const int dims = D % 64 == 0 ? 64 : 32;
+    if (!kv_map(&pk, p, p->k, dims, kKeys) || !kv_map(&pv, p, p->v, dims, kKeys) || !kv_map(&ok, o, o->k, dims, kKeys) ||
+        !kv_map(&ov, o, o->v, dims, kKeys))
+        return MQ_ERR_LAUNCH;
     return with_kernel(D, type, a.raw != nullptr, [&](auto kern, int smem) {
         if (!allow_smem(reinterpret_cast<const void*>(kern), smem)) return (int)MQ_ERR_LAUNCH;
-        return mq::launch_pdl(kern, dim3(a.plan.G), dim3(kThreads), smem, stream, a);
+        return mq::launch_pdl(kern, dim3(a.plan.G), dim3(kThreads), smem, stream, a, pk, pv, ok, ov);
     });
+}
+
+int take_few_error(unsigned* code) {
+    if (cudaMemcpyFromSymbol(code, g_few_error, sizeof(*code)) != cudaSuccess) return MQ_ERR_LAUNCH;
+    const unsigned zero = 0;
+    return *code && cudaMemcpyToSymbol(g_few_error, &zero, sizeof(zero)) != cudaSuccess ? MQ_ERR_LAUNCH : MQ_OK;
 }
 
 }  // namespace attn

@@ -10,8 +10,6 @@ struct FewArgs {
     Plan plan;
     const void* q;
     long long q_stride;
-    const void *pk, *pv, *ok, *ov;                  // prefix and own keys and values
-    long long p_row, p_head, o_seq, o_row, o_head;  // their strides
     const int32_t* len;
     float scale_log2;                               // scale * log2 e
     Pieces out;
@@ -23,6 +21,7 @@ constexpr int kFewRows = 16;      // query rows per segment
 constexpr int kFewKeys = 16;      // keys per tile
 constexpr int kFewExtra = 4;      // what beginning and ending a segment costs, in tiles
 constexpr int kFewPerSm = 8;      // blocks (of one warp) per SM
-int launch_few(const FewArgs& a, int D, int type, cudaStream_t stream);
+int launch_few(const FewArgs& a, const mq_kv* prefix, const mq_kv* own, int D, int type, cudaStream_t stream);
+int take_few_error(unsigned* code);   // bounded waits that gave up; cleared
 
 }  // namespace attn

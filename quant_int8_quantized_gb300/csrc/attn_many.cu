@@ -22,25 +22,18 @@
 // Waits are bounded; a wait that runs out is recorded (mq_device_status), the block drains its own copies
 // and products, frees tensor memory and returns.
 
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 #include <map>
 #include <mutex>
 #include <type_traits>
 
+#include "attn_few.cuh"
 #include "attn_many.cuh"
-#include "tc.cuh"
+#include "attn_maps.cuh"
 
 namespace attn {
 namespace {
 
 __device__ unsigned int g_attn_error;   // bit 0: a bounded wait gave up
-
-#ifndef MQ_WAIT_LIMIT_NS
-#define MQ_WAIT_LIMIT_NS 2000000000ull   // test builds may shorten it
-#endif
-constexpr uint64_t kWaitLimitNs = MQ_WAIT_LIMIT_NS;
 
 constexpr int kThreads = 384;
 // Registers a thread: what the launch gives to 384 threads, and after sharing out again (2 x 208 + 88 = 3 x 168).
@@ -88,15 +81,6 @@ struct Bars {
     int abort;
 };
 
-// Non-suspending test of a phase.
-__device__ __forceinline__ bool ready(uint64_t* bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
-                 : "=r"(ok)
-                 : "r"(tc::smem_u32(bar)), "r"(parity)
-                 : "memory");
-    return ok != 0;
-}
 // Whole warp, or any set of threads of one whose outcome need not be uniform with the others.
 __device__ bool wait_long(Bars& b, uint64_t* bar, uint32_t parity) {
     const uint64_t t0 = tc::globaltimer();
@@ -111,28 +95,13 @@ __device__ bool wait_long(Bars& b, uint64_t* bar, uint32_t parity) {
     }
 }
 __device__ __forceinline__ bool wwait(Bars& b, uint64_t* bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, ready(bar, parity) || wait_long(b, bar, parity));
+    return __all_sync(0xffffffffu, mbar_ready(bar, parity) || wait_long(b, bar, parity));
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
-}
-
-__device__ __forceinline__ void tma_load_3d(void* dst, const void* map, int x, int y, int z, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-            tc::smem_u32(dst)),
-        "l"(map), "r"(x), "r"(y), "r"(z), "r"(tc::smem_u32(bar))
-        : "memory");
-}
-__device__ __forceinline__ void tma_load_4d(void* dst, const void* map, int x, int y, int z, int w, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::
-            "r"(tc::smem_u32(dst)),
-        "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(tc::smem_u32(bar))
-        : "memory");
 }
 
 // Matrix descriptors of 128-byte-swizzled tiles: the low word holds the address and the distance of 64-element
@@ -468,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tc::mbar_arrive_expect_tx(&bars.full[slot], C::kTileBytes);
 #pragma unroll
                             for (int k = 0; k < C::kChunks; ++k)
-                                tma_load_4d(s_ring + slot * C::kTileBytes + k * C::kChunkBytes, map, k * 64, g.head, k0,
+                                tma_load_4d(tc::smem_u32(s_ring) + slot * C::kTileBytes + k * C::kChunkBytes, map, k * 64, g.head, k0,
                                             shared ? 0 : g.b, &bars.full[slot]);
                         }
                         __syncwarp();
@@ -643,19 +612,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------ host side
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    });
-    return fn;
-}
-
 // The register split assumes the launch's count (asked once per kernel).
 bool regs_as_planned(const void* kern) {
     static std::mutex mu;
@@ -669,41 +625,16 @@ bool regs_as_planned(const void* kern) {
     return ok;
 }
 
-// [n][cap][heads][dim] of k or v as (dim, head, row, sequence); rows past the cap read as zeros.
-bool kv_map(CUtensorMap* map, const mq_kv* c, const void* base) {
-    auto fn = encode_fn();
-    if (!fn) return false;
-    auto stride = [](long long s) { return (cuuint64_t)(s > 0 ? s * 2 : 16); };   // an axis of one step may have none
-    const cuuint64_t dims[4] = {(cuuint64_t)c->dim, (cuuint64_t)c->heads, (cuuint64_t)c->cap, (cuuint64_t)c->n};
-    const cuuint64_t strides[3] = {stride(c->head_stride), stride(c->row_stride), stride(c->seq_stride)};
-    const cuuint32_t box[4] = {64, 1, kManyKeys, 1}, step[4] = {1, 1, 1, 1};
-    return fn(map, c->type == MQ_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
-              const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// The queries [B T][Hq][D] as (dim, head, query): a box is a segment's rows, group heads of each of its queries.
-bool q_map(CUtensorMap* map, const ManyArgs& a, int D, int type) {
-    auto fn = encode_fn();
-    if (!fn) return false;
-    const Plan& p = a.plan;
-    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)p.Hq, (cuuint64_t)p.B * p.T};
-    const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)a.q_stride * 2};
-    const cuuint32_t box[3] = {64, (cuuint32_t)p.group, (cuuint32_t)(p.rows / p.group)}, step[3] = {1, 1, 1};
-    return fn(map, type == MQ_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
-              const_cast<void*>(a.q), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
-           CUDA_SUCCESS;
-}
-
 }  // namespace
 
 int launch_many(const ManyArgs& a, const mq_kv* prefix, const mq_kv* own, int D, int type, cudaStream_t stream) {
     CUtensorMap qm, pk, pv, ok, ov;
     const mq_kv* p = prefix ? prefix : own;   // a part that is not there is never read
     const mq_kv* o = own ? own : prefix;
-    if (!q_map(&qm, a, D, type) || !kv_map(&pk, p, p->k) || !kv_map(&pv, p, p->v) || !kv_map(&ok, o, o->k) || !kv_map(&ov, o, o->v))
+    if (!q_map(&qm, a.q, a.q_stride, (long long)a.plan.B * a.plan.T, a.plan.Hq, D, type, a.plan.group,
+               a.plan.rows / a.plan.group) ||
+        !kv_map(&pk, p, p->k, 64, kManyKeys) || !kv_map(&pv, p, p->v, 64, kManyKeys) ||
+        !kv_map(&ok, o, o->k, 64, kManyKeys) || !kv_map(&ov, o, o->v, 64, kManyKeys))
         return MQ_ERR_LAUNCH;
     auto go = [&](auto kern, int smem) {
         if (!regs_as_planned(reinterpret_cast<const void*>(kern))) return (int)MQ_ERR_LAUNCH;
@@ -723,11 +654,13 @@ int take_attn_device_error(cudaStream_t stream, unsigned* code) {
     if (cudaStreamSynchronize(stream) != cudaSuccess) return MQ_ERR_LAUNCH;
     unsigned v = 0;
     if (cudaMemcpyFromSymbol(&v, attn::g_attn_error, sizeof(v)) != cudaSuccess) return MQ_ERR_LAUNCH;
+    unsigned few = 0;
+    if (attn::take_few_error(&few) != MQ_OK) return MQ_ERR_LAUNCH;
     if (v) {
         const unsigned zero = 0;
         if (cudaMemcpyToSymbol(attn::g_attn_error, &zero, sizeof(zero)) != cudaSuccess) return MQ_ERR_LAUNCH;
     }
-    *code = v;
+    *code = v | few;
     return MQ_OK;
 }
 }  // namespace mq
