@@ -264,6 +264,7 @@ constexpr int kManyFrom = 33;   // query rows per key head, at least, for the te
 // leave more of the blocks that they do not divide idle.
 constexpr long long kLanesFrom = 24 << 20;
 constexpr int kLanesMost = 8;
+constexpr int kBeside = 2;
 constexpr double kTileUs = 1.4, kDraw = 116e3;   // of a tile of two halves, measured; of an SM's eight warps with two stages in flight
 
 // How a call is cut: the part of each kernel, and where the workspace holds what.
@@ -318,7 +319,8 @@ Cut cut_of(int B, int T, int Hq, int Hkv, int D, int prefix_keys, int own_cap, b
         const long long segs = all_segs(p);
         const long long most = (long long)prefix_segs(p) * ceil_div(p.prefix_keys, p.keys) +
                                (segs - prefix_segs(p)) * (ceil_div(p.lead_keys, p.keys) + ceil_div(p.own_cap, p.keys));
-        const long long held = (long long)mq::num_sms() * (many ? 1 : kFewPerSm);
+        // beside the tensor-core kernel the blocks come and go on a part of the SMs: shorter runs, a shorter tail
+        const long long held = (long long)mq::num_sms() * (many ? 1 : c.prefix_many ? kBeside * kFewPerSm : kFewPerSm);
         p.extra = !many ? kFewExtra : p.own ? kManyExtra : kManyExtra / 2;
         if (most * p.wide_cost + segs * p.extra > 0x7fffffffLL) c.fits = false;
         p.G = (int)(most < held ? most : held);
