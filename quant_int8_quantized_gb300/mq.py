@@ -116,8 +116,20 @@ def _ptr(t):
 
 def _stream(stream):
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return _current_stream()
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+
+
+def _current_stream():
+    """The current stream's handle, by the bindings under torch.cuda.current_stream() where they are
+    there: building a Stream object takes 3 us on a Grace core, as long as the rest of a small call."""
+    if _raw_stream is not None and torch.cuda.is_initialized():
+        return ctypes.c_void_p(_raw_stream(_device()))
+    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) if hasattr(torch._C, "_cuda_getDevice") else None
+_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
 def _check(status: int, where: str):
@@ -126,6 +138,8 @@ def _check(status: int, where: str):
 
 
 def _dev_tensor(t, dtype, name):
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous():
+        return t
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device.type != "cuda":
@@ -353,22 +367,12 @@ class KV:
         st = [int(k.stride(i)) if k.shape[i] > 1 else 0 for i in range(3)]
         self._c = CKV(k.data_ptr(), v.data_ptr(), st[0], st[1], st[2], _TYPES[k.dtype], self.n, self.cap, self.heads,
                       self.dim)
-        self._ref = ctypes.byref(self._c)
+        self._ref, self.dtype = ctypes.byref(self._c), k.dtype
 
     @classmethod
     def empty(cls, n: int, cap: int, heads: int, dim: int, dtype=torch.float16, device="cuda") -> "KV":
         return cls(torch.empty((n, cap, heads, dim), dtype=dtype, device=device),
                    torch.empty((n, cap, heads, dim), dtype=dtype, device=device))
-
-    @property
-    def dtype(self):
-        return self.k.dtype
-
-
-def _kv(c, name):
-    if not isinstance(c, KV):
-        raise TypeError(f"{name} must be a KV")
-    return c
 
 
 def rope_freq(n_pairs: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
@@ -388,9 +392,9 @@ def _heads(t, name, M, D, heads=None):
         return None, 0, 0
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.float32:
+    if t.dtype is not torch.float32:
         raise TypeError(f"{name} must be torch.float32, got {t.dtype}")
     s, st = t.shape, t.stride()
     if len(s) != 3 or s[0] != M or s[2] != D or (heads is not None and s[1] != heads):
@@ -406,39 +410,47 @@ def mq_qk_norm_rope(q, k, v, q_out, cache: KV, slot=None, pos=None, inv_freq=Non
     (include/mq.h). q: f32 [M, Hq, D]; k, v: f32 [M, Hkv, D] (any may be None; a token's heads are
     contiguous, tokens at any stride); q_out: [M, Hq, D] of the cache's type; slot: int32 [M];
     pos: int32 [M] or [n_axes, M]; inv_freq: f32 [n_pairs]; axis: uint8 [n_pairs]."""
-    _kv(cache, "cache")
-    first = next((t for t in (q, k, v) if t is not None), None)
+    if not isinstance(cache, KV):
+        raise TypeError("cache must be a KV")
+    first = q if q is not None else k if k is not None else v
     if first is None:
         raise ValueError("one of q, k and v is needed")
-    M, D = int(first.shape[0]), cache.dim
-    x = CQKV()
-    x.q, x.q_stride, Hq = _heads(q, "q", M, D)
-    x.k, x.k_stride, _ = _heads(k, "k", M, D, cache.heads)
-    x.v, x.v_stride, _ = _heads(v, "v", M, D, cache.heads)
+    M, D = first.shape[0], cache.dim
+    q_ptr, q_stride, Hq = _heads(q, "q", M, D)
+    k_ptr, k_stride, _ = _heads(k, "k", M, D, cache.heads)
+    v_ptr, v_stride, _ = _heads(v, "v", M, D, cache.heads)
+    out_ptr = slot_ptr = wq_ptr = wk_ptr = freq_ptr = axis_ptr = pos_ptr = None
     if q is not None:
-        _dev_tensor(q_out, cache.dtype, "q_out")
-        if q_out.numel() < M * Hq * D:
+        if _dev_tensor(q_out, cache.dtype, "q_out").numel() < M * Hq * D:
             raise ValueError(f"q_out holds {q_out.numel()} elements, needs {M * Hq * D}")
-    for t, name in ((wq, "wq"), (wk, "wk")):
-        if t is not None and _dev_tensor(t, torch.float32, name).numel() != D:
-            raise ValueError(f"{name} must hold {D} weights")
+        out_ptr = q_out.data_ptr()
+    if wq is not None:
+        if _dev_tensor(wq, torch.float32, "wq").numel() != D:
+            raise ValueError(f"wq must hold {D} weights")
+        wq_ptr = wq.data_ptr()
+    if wk is not None:
+        if _dev_tensor(wk, torch.float32, "wk").numel() != D:
+            raise ValueError(f"wk must hold {D} weights")
+        wk_ptr = wk.data_ptr()
     n_pairs = n_axes = 0
-    if inv_freq is not None and inv_freq.numel():
+    if inv_freq is not None:
         n_pairs = _dev_tensor(inv_freq, torch.float32, "inv_freq").numel()
-        _dev_tensor(pos, torch.int32, "pos")
-        n_axes = 1 if pos.dim() == 1 else int(pos.shape[0])
+    if n_pairs:
+        n_axes = 1 if _dev_tensor(pos, torch.int32, "pos").dim() == 1 else pos.shape[0]
         if pos.numel() != n_axes * M:
             raise ValueError(f"pos must be [{M}] or [n_axes, {M}], got {tuple(pos.shape)}")
-        if axis is not None and _dev_tensor(axis, torch.uint8, "axis").numel() != n_pairs:
-            raise ValueError(f"axis must hold {n_pairs} entries")
-        x.inv_freq, x.pos = inv_freq.data_ptr(), pos.data_ptr()
-        x.axis = None if axis is None else axis.data_ptr()
-    if slot is not None and _dev_tensor(slot, torch.int32, "slot").numel() != M:
-        raise ValueError(f"slot must hold {M} entries")
-    x.wq = None if wq is None else wq.data_ptr()
-    x.wk = None if wk is None else wk.data_ptr()
-    x.M, x.Hq, x.n_pairs, x.n_axes, x.interleaved, x.eps = M, Hq, n_pairs, n_axes, int(bool(interleaved)), float(eps)
-    _check(lib().mq_qk_norm_rope(ctypes.byref(x), _ptr(q_out), cache._ref, _ptr(slot), _stream(stream)),
+        if axis is not None:
+            if _dev_tensor(axis, torch.uint8, "axis").numel() != n_pairs:
+                raise ValueError(f"axis must hold {n_pairs} entries")
+            axis_ptr = axis.data_ptr()
+        freq_ptr, pos_ptr = inv_freq.data_ptr(), pos.data_ptr()
+    if slot is not None:
+        if _dev_tensor(slot, torch.int32, "slot").numel() != M:
+            raise ValueError(f"slot must hold {M} entries")
+        slot_ptr = slot.data_ptr()
+    x = CQKV(q_ptr, k_ptr, v_ptr, q_stride, k_stride, v_stride, wq_ptr, wk_ptr, freq_ptr, axis_ptr, pos_ptr, M, Hq,
+             n_pairs, n_axes, 1 if interleaved else 0, eps)
+    _check((_lib or lib()).mq_qk_norm_rope(ctypes.byref(x), out_ptr, cache._ref, slot_ptr, _stream(stream)),
            "mq_qk_norm_rope")
     return q_out
 
@@ -464,44 +476,53 @@ def mq_attn_prefix(q: torch.Tensor, prefix, own, own_len, out: torch.Tensor, sca
     any_kv = own if own is not None else prefix
     if any_kv is None:
         raise ValueError("a prefix, an own cache or both are needed")
-    if prefix is not None:
-        _kv(prefix, "prefix")
-    if own is not None:
-        _kv(own, "own")
+    if not isinstance(any_kv, KV) or (prefix is not None and not isinstance(prefix, KV)):
+        raise TypeError("prefix and own must be KV")
     if not isinstance(q, torch.Tensor) or q.dim() != 4:
         raise TypeError("q must be a torch.Tensor [B, T, Hq, D]")
     B, T, Hq, D = q.shape
-    if q.device.type != "cuda":
+    dtype = q.dtype
+    if not q.is_cuda:
         raise ValueError("q must be a CUDA tensor")
-    if q.dtype != any_kv.dtype:
-        raise TypeError(f"q must be {any_kv.dtype}, got {q.dtype}")
+    if dtype is not any_kv.dtype:
+        raise TypeError(f"q must be {any_kv.dtype}, got {dtype}")
     if D != any_kv.dim:
         raise ValueError(f"q's heads are {D} wide, the cache's {any_kv.dim}")
+    rows = B * T * Hq
     st = q.stride()
-    if q.numel() and ((st[3] != 1) or (Hq > 1 and st[2] != D) or (B > 1 and T > 1 and st[0] != T * st[1])):
+    if rows and (st[3] != 1 or (Hq > 1 and st[2] != D) or (B > 1 and T > 1 and st[0] != T * st[1])):
         raise ValueError("q: a token's heads must be contiguous, and the tokens at one stride")
     row = st[1] if T > 1 else st[0] if B > 1 else Hq * D
-    if out.dtype not in (q.dtype, torch.float32):
-        raise TypeError(f"out must be {q.dtype} or torch.float32, got {out.dtype}")
-    _dev_tensor(out, out.dtype, "out")
-    if out.numel() < q.numel():
-        raise ValueError(f"out holds {out.numel()} elements, needs {q.numel()}")
-    if own is not None and _dev_tensor(own_len, torch.int32, "own_len").numel() != B:
-        raise ValueError(f"own_len must hold {B} lengths")
-    if lse is not None and _dev_tensor(lse, torch.float32, "lse").numel() < B * T * Hq:
-        raise ValueError(f"lse needs {B * T * Hq} elements")
-    for t, name in ((score, "score"), (score_out, "score_out")):
-        if t is not None and (own is None or
-                              _dev_tensor(t, torch.float32, name).numel() < B * own.heads * own.cap):
-            raise ValueError(f"{name} must be [B, Hkv, own.cap]")
+    out_type = out.dtype
+    if out_type is not dtype and out_type is not torch.float32:
+        raise TypeError(f"out must be {dtype} or torch.float32, got {out_type}")
+    if _dev_tensor(out, out_type, "out").numel() < rows * D:
+        raise ValueError(f"out holds {out.numel()} elements, needs {rows * D}")
+    own_ref = len_ptr = lse_ptr = score_ptr = score_out_ptr = None
+    if own is not None:
+        if _dev_tensor(own_len, torch.int32, "own_len").numel() != B:
+            raise ValueError(f"own_len must hold {B} lengths")
+        own_ref, len_ptr = own._ref, own_len.data_ptr()
+    if lse is not None:
+        if _dev_tensor(lse, torch.float32, "lse").numel() < rows:
+            raise ValueError(f"lse needs {rows} elements")
+        lse_ptr = lse.data_ptr()
+    if score is not None:
+        if own is None or _dev_tensor(score, torch.float32, "score").numel() < B * own.heads * own.cap:
+            raise ValueError("score must be [B, Hkv, own.cap]")
+        score_ptr = score.data_ptr()
+    if score_out is not None:
+        if own is None or _dev_tensor(score_out, torch.float32, "score_out").numel() < B * own.heads * own.cap:
+            raise ValueError("score_out must be [B, Hkv, own.cap]")
+        score_out_ptr = score_out.data_ptr()
     if ws is None:
-        ws = attn_workspace(B, T, Hq, any_kv.heads, D, prefix.cap if prefix else 0, own.cap if own else 0,
-                            score is not None, q.device)
-    _check(lib().mq_attn_prefix(q.data_ptr(), row, B, T, Hq, prefix._ref if prefix is not None else None,
-                                own._ref if own is not None else None, _ptr(own_len) if own is not None else None,
-                                float(D) ** -0.5 if scale is None else float(scale), out.data_ptr(),
-                                _TYPES[out.dtype], _ptr(lse), _ptr(score), _ptr(score_out), ws.data_ptr(),
-                                ws.numel() * ws.element_size(), _stream(stream)), "mq_attn_prefix")
+        ws = attn_workspace(B, T, Hq, any_kv.heads, D, prefix.cap if prefix is not None else 0,
+                            own.cap if own is not None else 0, score is not None, q.device)
+    _check((_lib or lib()).mq_attn_prefix(q.data_ptr(), row, B, T, Hq, prefix._ref if prefix is not None else None,
+                                          own_ref, len_ptr, D ** -0.5 if scale is None else scale, out.data_ptr(),
+                                          _TYPES[out_type], lse_ptr, score_ptr, score_out_ptr,
+                                          _dev_tensor(ws, torch.uint8, "ws").data_ptr(), ws.numel(), _stream(stream)),
+           "mq_attn_prefix")
     return out
 
 
@@ -511,20 +532,25 @@ def mq_kv_evict(src: KV, length: torch.Tensor, score: torch.Tensor, keep: int, r
     others by score (include/mq.h). length, length_out: int32 [n]; score: f32 [n, heads, src.cap];
     score_out (or None): f32 [n, heads, dst.cap]; index: int32 [n, heads, dst.cap], the rows kept.
     dst may be src: the rows then move in place."""
-    _kv(src, "src")
-    _kv(dst, "dst")
-    for t, name in ((length, "length"), (length_out, "length_out")):
-        if _dev_tensor(t, torch.int32, name).numel() != src.n:
-            raise ValueError(f"{name} must hold {src.n} lengths")
+    if not isinstance(src, KV) or not isinstance(dst, KV):
+        raise TypeError("src and dst must be KV")
+    if _dev_tensor(length, torch.int32, "length").numel() != src.n:
+        raise ValueError(f"length must hold {src.n} lengths")
+    if _dev_tensor(length_out, torch.int32, "length_out").numel() != src.n:
+        raise ValueError(f"length_out must hold {src.n} lengths")
     if _dev_tensor(score, torch.float32, "score").numel() < src.n * src.heads * src.cap:
         raise ValueError("score must be [n, heads, src.cap]")
     need = dst.n * dst.heads * dst.cap
-    if score_out is not None and _dev_tensor(score_out, torch.float32, "score_out").numel() < need:
-        raise ValueError("score_out must be [n, heads, dst.cap]")
+    score_out_ptr = None
+    if score_out is not None:
+        if _dev_tensor(score_out, torch.float32, "score_out").numel() < need:
+            raise ValueError("score_out must be [n, heads, dst.cap]")
+        score_out_ptr = score_out.data_ptr()
     if _dev_tensor(index, torch.int32, "index").numel() < need:
         raise ValueError("index must be [n, heads, dst.cap]")
-    _check(lib().mq_kv_evict(src._ref, _ptr(length), _ptr(score), int(keep), int(recent), dst._ref, _ptr(length_out),
-                             _ptr(score_out), _ptr(index), _stream(stream)), "mq_kv_evict")
+    _check((_lib or lib()).mq_kv_evict(src._ref, length.data_ptr(), score.data_ptr(), keep, recent, dst._ref,
+                                       length_out.data_ptr(), score_out_ptr, index.data_ptr(), _stream(stream)),
+           "mq_kv_evict")
     return dst
 
 
