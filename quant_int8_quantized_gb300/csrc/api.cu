@@ -4,6 +4,7 @@
 #include <map>
 #include <mutex>
 #include <tuple>
+#include <utility>
 
 #include "mq_internal.cuh"
 
@@ -59,6 +60,21 @@ int resident_blocks(const void* kern, int threads, size_t smem) {
     }
     cache.emplace(key, b);
     return b;
+}
+
+bool allow_smem(const void* kern, int bytes) {
+    static std::mutex mu;
+    static std::map<std::pair<const void*, int>, bool> done;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    std::lock_guard<std::mutex> lk(mu);
+    const auto key = std::make_pair(kern, dev);
+    const auto it = done.find(key);
+    if (it != done.end()) return it->second;
+    const bool ok = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
+    if (!ok) cudaGetLastError();
+    done.emplace(key, ok);
+    return ok;
 }
 
 }  // namespace mq

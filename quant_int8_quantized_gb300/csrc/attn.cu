@@ -2,32 +2,12 @@
 // that join the pieces (attn.cuh) into outputs and add up attention weights.
 
 #include <cmath>
-#include <map>
-#include <mutex>
-#include <utility>
 
 #include "attn_few.cuh"
 #include "attn_many.cuh"
 
 namespace attn {
-
-bool allow_smem(const void* kern, int bytes) {
-    static std::mutex mu;
-    static std::map<std::pair<const void*, int>, bool> done;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return false;
-    std::lock_guard<std::mutex> lk(mu);
-    const auto key = std::make_pair(kern, dev);
-    const auto it = done.find(key);
-    if (it != done.end()) return it->second;
-    const bool ok = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
-    if (!ok) cudaGetLastError();
-    done.emplace(key, ok);
-    return ok;
-}
-
 namespace {
-
 
 // One part of the keys, as the joining kernels see it.
 struct Part {

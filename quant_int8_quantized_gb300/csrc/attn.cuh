@@ -287,7 +287,4 @@ struct Out {
 
 constexpr float kLn2 = 0.6931471805599453f;
 
-// Lets `kern` use `bytes` of dynamic shared memory (asked once per kernel and device).
-bool allow_smem(const void* kern, int bytes);
-
 }  // namespace attn

@@ -347,7 +347,7 @@ int launch_few(const FewArgs& a, const mq_kv* prefix, const mq_kv* own, int D, i
         !kv_map(&ov, o, o->v, dims, kKeys))
         return MQ_ERR_LAUNCH;
     return with_kernel(D, type, a.raw != nullptr, [&](auto kern, int smem) {
-        if (!allow_smem(reinterpret_cast<const void*>(kern), smem)) return (int)MQ_ERR_LAUNCH;
+        if (!mq::allow_smem(reinterpret_cast<const void*>(kern), smem)) return (int)MQ_ERR_LAUNCH;
         return mq::launch_pdl(kern, dim3(a.plan.G), dim3(kThreads), smem, stream, a, pk, pv, ok, ov);
     });
 }

@@ -638,7 +638,7 @@ int launch_many(const ManyArgs& a, const mq_kv* prefix, const mq_kv* own, int D,
         return MQ_ERR_LAUNCH;
     auto go = [&](auto kern, int smem) {
         if (!regs_as_planned(reinterpret_cast<const void*>(kern))) return (int)MQ_ERR_LAUNCH;
-        if (!allow_smem(reinterpret_cast<const void*>(kern), smem)) return (int)MQ_ERR_LAUNCH;
+        if (!mq::allow_smem(reinterpret_cast<const void*>(kern), smem)) return (int)MQ_ERR_LAUNCH;
         return mq::launch_pdl(kern, dim3(a.plan.G), dim3(kThreads), smem, stream, a, qm, pk, pv, ok, ov);
     };
     if (type == MQ_F16)

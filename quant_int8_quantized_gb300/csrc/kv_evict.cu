@@ -1,12 +1,15 @@
 // Eviction from a cache by accumulated attention weight: per sequence and key head the `recent`
 // last rows stay and, of the others, those with the largest score; kept rows keep their order.
 //
-// Two launches. The first finds the kept rows: scores become unsigned keys in the same order, the
-// key of the last row that is kept is found digit by digit (a histogram of 8 bits a round, counted in
-// shared memory), then every warp of the block writes the kept rows of its own stretch in order,
-// from the counts of the stretches before it. Counts are integers: the result does not depend on
-// the order of the atomics. The second moves rows, values and scores: 16 bytes a thread, every
-// kept row read once and written once.
+// Scores become unsigned keys in the same order, and the key of the last row that is kept is found digit by
+// digit: a histogram of 8 bits a round, counted in shared memory. Long rows are shared out to a cluster of
+// blocks, which add their histograms up through distributed shared memory; each block reads its stretch of the
+// scores from memory once. Then every warp writes the kept rows of its own stretch in order, from the
+// counts of the stretches before it. Counts are integers: the result does not depend on the order of the
+// atomics.
+// Then rows, values and scores move: 16 bytes a thread, every kept row read once and written once. Where there are
+// enough heads to fill the machine with blocks, each moves the rows of the head that it selected for; else a
+// second launch shares them out evenly.
 
 #include "heads.cuh"
 
@@ -14,6 +17,8 @@ namespace {
 
 constexpr int kSelThreads = 1024;
 constexpr int kWarps = kSelThreads / 32;
+constexpr int kMaxCluster = 8;
+constexpr int kMaxKeys = 40 * 1024;      // of a block's stretch that shared memory holds; longer ones are read again
 
 // Order of floats as unsigned integers; -0 equals +0, NaN is below everything.
 __device__ __forceinline__ uint32_t order_key(float f) {
@@ -22,106 +27,21 @@ __device__ __forceinline__ uint32_t order_key(float f) {
     return (b & 0x80000000u) ? ~b : b | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const float* score, const int32_t* len, int heads,
-                                                                   int cap, int keep, int recent, int dst_cap,
-                                                                   int32_t* index) {
-    __shared__ int s_hist[kWarps][256];
-    __shared__ int s_tot[256];
-    __shared__ int s_gt[kWarps], s_eq[kWarps];
-    __shared__ uint32_t s_prefix;
-    __shared__ int s_need;
-    mq_grid_release();
-    mq_grid_wait();
-    const int row = blockIdx.x;
-    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-    const int n = min(max(len[row / heads], 0), cap);
-    const float* sc = score + (long long)row * cap;
-    int32_t* out = index + (long long)row * dst_cap;
-    if (n <= keep) {
-        for (int j = tid; j < dst_cap; j += kSelThreads) out[j] = j < n ? j : -1;
-        return;
-    }
-    const int cand = n - recent;            // rows that compete for `best` places
-    const int best = keep - recent;
-    for (int j = tid; j < recent; j += kSelThreads) out[best + j] = cand + j;
-    for (int j = keep + tid; j < dst_cap; j += kSelThreads) out[j] = -1;
-    if (best == 0) return;
-    uint32_t prefix = 0;
-    int need = best;                        // rows still to be taken among those that share `prefix`
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        for (int i = lane; i < 256; i += 32) s_hist[wid][i] = 0;
-        __syncwarp();
-        const uint32_t above = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-        for (int j = tid; j < cand; j += kSelThreads) {
-            const uint32_t k = order_key(mq_ld_dep(sc + j));
-            if ((k & above) == prefix) atomicAdd(&s_hist[wid][(k >> shift) & 255u], 1);
-        }
-        __syncthreads();
-        if (tid < 256) {
-            int t = 0;
-            for (int w = 0; w < kWarps; ++w) t += s_hist[w][tid];
-            s_tot[tid] = t;
-        }
-        __syncthreads();
-        if (wid == 0) {                      // the digit at which the rows from the top reach `need`
-            int t[8], sum = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) sum += t[i] = s_tot[255 - (lane * 8 + i)];
-            int run = sum;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int u = __shfl_up_sync(0xffffffffu, run, o);
-                if (lane >= o) run += u;
-            }
-            int before = run - sum;
-            if (before < need && run >= need) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    if (before < need && before + t[i] >= need) {
-                        s_prefix = prefix | (uint32_t)(255 - (lane * 8 + i)) << shift;
-                        s_need = need - before;
-                        break;
-                    }
-                    before += t[i];
-                }
-            }
-        }
-        __syncthreads();
-        prefix = s_prefix;
-        need = s_need;
-        __syncthreads();
-    }
-    // kept: key above `prefix`, and the first `need` rows of those equal to it
-    const int per = ((cand + kWarps - 1) / kWarps + 31) / 32 * 32;
-    const int j0 = min(wid * per, cand), j1 = min(j0 + per, cand);
-    int gt = 0, eq = 0;
-    for (int j = j0 + lane; j < j1; j += 32) {
-        const uint32_t k = order_key(mq_ld_dep(sc + j));
-        gt += k > prefix;
-        eq += k == prefix;
-    }
-    gt = __reduce_add_sync(0xffffffffu, gt);
-    eq = __reduce_add_sync(0xffffffffu, eq);
-    if (lane == 0) {
-        s_gt[wid] = gt;
-        s_eq[wid] = eq;
-    }
-    __syncthreads();
-    int g0 = 0, e0 = 0;
-    for (int w = 0; w < wid; ++w) {
-        g0 += s_gt[w];
-        e0 += s_eq[w];
-    }
-    for (int j = j0; j < j1; j += 32) {
-        const uint32_t k = j + lane < j1 ? order_key(mq_ld_dep(sc + j + lane)) : 0u;
-        const bool isg = j + lane < j1 && k > prefix, ise = j + lane < j1 && k == prefix;
-        const unsigned bg = __ballot_sync(0xffffffffu, isg), be = __ballot_sync(0xffffffffu, ise);
-        const unsigned lower = (1u << lane) - 1u;
-        const int g = g0 + __popc(bg & lower), e = e0 + __popc(be & lower);
-        if (isg || (ise && e < need)) out[g + min(e, need)] = j + lane;
-        g0 += __popc(bg);
-        e0 += __popc(be);
-    }
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A shared-memory word of block `rank` of the cluster, at this block's address p.
+__device__ __forceinline__ int remote(const int* p, uint32_t rank) {
+    uint32_t at;
+    int v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
 }
 
 struct Move {
@@ -135,6 +55,189 @@ struct Move {
     long long ss, sr, sh, ds, dr, dh;   // strides in 16-byte units
     int n, heads, cap, dst_cap, keep, chunks;
 };
+
+// Selection for one head of one sequence by a cluster of C blocks. MOVE (C == 1): and the move of its rows.
+template <bool MOVE>
+__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Move a, int recent, int C, int keys_held,
+                                                                   int32_t* index) {
+    extern __shared__ uint32_t s_keys[];                  // keys of this block's stretch, if they fit
+    __shared__ int s_hist[kWarps][256];
+    __shared__ int s_tot[2][256], s_all[256];
+    __shared__ int s_gt[kWarps], s_eq[kWarps], s_cnt[2];
+    __shared__ uint32_t s_prefix;
+    __shared__ int s_need;
+    mq_grid_release();
+    mq_grid_wait();
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    const int rank = C > 1 ? (int)cluster_rank() : 0, row = blockIdx.x / C;
+    const int b = row / a.heads, h = row - b * a.heads;
+    const int n = min(max(a.len[b], 0), a.cap), keep = a.keep, dst_cap = a.dst_cap;
+    const float* sc = a.score + (long long)row * a.cap;
+    int32_t* out = index + (long long)row * dst_cap;
+    const int step = C * kSelThreads, first = rank * kSelThreads + tid;
+    if (n <= keep) {
+        for (int j = first; j < dst_cap; j += step) out[j] = j < n ? j : -1;
+    } else {
+        const int cand = n - recent;            // rows that compete for `best` places
+        const int best = keep - recent;
+        for (int j = first; j < recent; j += step) out[best + j] = cand + j;
+        for (int j = keep + first; j < dst_cap; j += step) out[j] = -1;
+        // (best is the same for all blocks of the cluster)
+        if (best > 0) {
+            const int per = ((cand + C - 1) / C + 31) / 32 * 32;
+            const int base = min(rank * per, cand), mine = min(per, cand - base);
+            const bool held = mine <= keys_held;
+            if (held)
+                for (int j = tid; j < mine; j += kSelThreads) s_keys[j] = order_key(mq_ld_dep(sc + base + j));
+            __syncthreads();
+            auto key = [&](int j) { return held ? s_keys[j] : order_key(mq_ld_dep(sc + base + j)); };
+            uint32_t prefix = 0;
+            int need = best;                    // rows still to be taken among those that share `prefix`
+#pragma unroll 1
+            for (int round = 0; round < 4; ++round) {
+                const int shift = 24 - 8 * round;
+                for (int i = lane; i < 256; i += 32) s_hist[wid][i] = 0;
+                __syncwarp();
+                const uint32_t above = round == 0 ? 0u : 0xffffffffu << (shift + 8);
+                for (int j0 = wid * 32; j0 < mine; j0 += kSelThreads) {
+                    const int j = j0 + lane;
+                    const uint32_t k = j < mine ? key(j) : 0u;
+                    const bool in = j < mine && (k & above) == prefix;
+                    const unsigned who = __ballot_sync(0xffffffffu, in);
+                    if (in) {
+                        const int digit = (int)(k >> shift) & 255;
+                        int same;               // a digit that all share is counted once: equal scores would queue
+                        __match_all_sync(who, digit, &same);
+                        if (!same) atomicAdd(&s_hist[wid][digit], 1);
+                        else if (lane == __ffs(who) - 1) atomicAdd(&s_hist[wid][digit], __popc(who));
+                    }
+                }
+                __syncthreads();
+                int* tot = s_tot[round & 1];
+                if (tid < 256) {
+                    int t = 0;
+#pragma unroll 8
+                    for (int w = 0; w < kWarps; ++w) t += s_hist[w][tid];
+                    if (C > 1) tot[tid] = t;
+                    else s_all[tid] = t;
+                }
+                if (C > 1) {
+                    cluster_sync();
+                    if (tid < 256) {
+                        int t = 0;
+                        for (int r = 0; r < C; ++r) t += remote(tot + tid, r);
+                        s_all[tid] = t;
+                    }
+                }
+                __syncthreads();
+                if (wid == 0) {                  // the digit at which the rows from the top reach `need`
+                    int t[8], sum = 0;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) sum += t[i] = s_all[255 - (lane * 8 + i)];
+                    int run = sum;
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const int u = __shfl_up_sync(0xffffffffu, run, o);
+                        if (lane >= o) run += u;
+                    }
+                    int before = run - sum;
+                    if (before < need && run >= need) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            if (before < need && before + t[i] >= need) {
+                                s_prefix = prefix | (uint32_t)(255 - (lane * 8 + i)) << shift;
+                                s_need = need - before;
+                                break;
+                            }
+                            before += t[i];
+                        }
+                    }
+                }
+                __syncthreads();
+                prefix = s_prefix;
+                need = s_need;
+            }
+            // kept: key above `prefix`, and the first `need` rows of those equal to it
+            const int stretch = ((mine + kWarps - 1) / kWarps + 31) / 32 * 32;
+            const int j0 = min(wid * stretch, mine), j1 = min(j0 + stretch, mine);
+            int gt = 0, eq = 0;
+            for (int j = j0 + lane; j < j1; j += 32) {
+                const uint32_t k = key(j);
+                gt += k > prefix;
+                eq += k == prefix;
+            }
+            gt = __reduce_add_sync(0xffffffffu, gt);
+            eq = __reduce_add_sync(0xffffffffu, eq);
+            if (lane == 0) {
+                s_gt[wid] = gt;
+                s_eq[wid] = eq;
+            }
+            __syncthreads();
+            int g0 = 0, e0 = 0;
+            if (C > 1) {
+                if (tid == 0) {
+                    int g = 0, e = 0;
+                    for (int w = 0; w < kWarps; ++w) g += s_gt[w], e += s_eq[w];
+                    s_cnt[0] = g;
+                    s_cnt[1] = e;
+                }
+                cluster_sync();
+                for (int r = 0; r < rank; ++r) {
+                    g0 += remote(&s_cnt[0], r);
+                    e0 += remote(&s_cnt[1], r);
+                }
+            }
+            for (int w = 0; w < wid; ++w) {
+                g0 += s_gt[w];
+                e0 += s_eq[w];
+            }
+            for (int j = j0; j < j1; j += 32) {
+                const uint32_t k = j + lane < j1 ? key(j + lane) : 0u;
+                const bool isg = j + lane < j1 && k > prefix, ise = j + lane < j1 && k == prefix;
+                const unsigned bg = __ballot_sync(0xffffffffu, isg), be = __ballot_sync(0xffffffffu, ise);
+                const unsigned lower = (1u << lane) - 1u;
+                const int g = g0 + __popc(bg & lower), e = e0 + __popc(be & lower);
+                if (isg || (ise && e < need)) out[g + min(e, need)] = base + j + lane;
+                g0 += __popc(bg);
+                e0 += __popc(be);
+            }
+            if (C > 1) cluster_sync();           // the others are done with this block's counts
+        }
+    }
+    if constexpr (MOVE) {
+        __syncthreads();
+        const int kept = min(n, keep);
+        if (h == 0 && tid == 0 && a.len_out) a.len_out[b] = kept;
+        if (a.score_out)
+            for (int j = tid; j < dst_cap; j += kSelThreads)
+                a.score_out[(long long)row * dst_cap + j] = j < kept ? sc[out[j]] : 0.0f;
+        const uint4 *k = a.k + (long long)b * a.ss + h * a.sh, *v = a.v + (long long)b * a.ss + h * a.sh;
+        uint4 *dk = a.dk + (long long)b * a.ds + h * a.dh, *dv = a.dv + (long long)b * a.ds + h * a.dh;
+        const int total = kept * a.chunks;
+        constexpr int kAtOnce = 4;
+        for (int i0 = tid; i0 < total; i0 += kAtOnce * kSelThreads) {
+            uint4 x[kAtOnce], y[kAtOnce];
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) {
+                const int i = i0 + u * kSelThreads, j = i / a.chunks;
+                if (i < total) {
+                    const long long from = out[j] * a.sr + i - j * a.chunks;
+                    x[u] = __ldcs(k + from);
+                    y[u] = __ldcs(v + from);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) {
+                const int i = i0 + u * kSelThreads, j = i / a.chunks;
+                if (i < total) {
+                    const long long to = j * a.dr + i - j * a.chunks;
+                    __stcs(dk + to, x[u]);
+                    __stcs(dv + to, y[u]);
+                }
+            }
+        }
+    }
+}
 
 // dst apart from src: one thread per 16 bytes of a kept row of k and of v.
 __global__ void __launch_bounds__(256) evict_move_kernel(const Move a) {
@@ -221,6 +324,28 @@ __global__ void __launch_bounds__(256) evict_len_kernel(const int32_t* len, int3
     if (i < n) len_out[i] = min(min(max(len[i], 0), cap), keep);
 }
 
+int launch_select(const Move& a, int recent, int C, int held, int32_t* index, unsigned rows, size_t smem, bool fused,
+                  cudaStream_t stream) {
+    auto kern = fused ? evict_select_kernel<true> : evict_select_kernel<false>;
+    if (!mq::allow_smem(reinterpret_cast<const void*>(kern), kMaxKeys * (int)sizeof(uint32_t))) return MQ_ERR_LAUNCH;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = C;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(rows * C);
+    cfg.blockDim = dim3(kSelThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = C > 1 ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, recent, C, held, index);
+    return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? MQ_OK : MQ_ERR_LAUNCH;
+}
+
 bool overlap(const void* a, size_t an, const void* b, size_t bn) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
     return x < y + bn && y < x + an;
@@ -259,11 +384,6 @@ extern "C" int mq_kv_evict(const mq_kv* src, const int32_t* len, const float* sc
     }
     rc = mq::check_arch();
     if (rc != MQ_OK) return rc;
-    if (dst->cap > 0) {
-        rc = mq::launch_pdl(evict_select_kernel, dim3((unsigned)rows), dim3(kSelThreads), 0, stream, score, len,
-                            src->heads, src->cap, keep, recent, dst->cap, index);
-        if (rc != MQ_OK) return rc;
-    }
     Move a;
     a.k = static_cast<const uint4*>(src->k);
     a.v = static_cast<const uint4*>(src->v);
@@ -289,6 +409,23 @@ extern "C" int mq_kv_evict(const mq_kv* src, const int32_t* len, const float* sc
     if (dst->cap > 0) {
         // Scores that move in place, or beside rows that do, go through the ordered kernel.
         const bool ordered_score = score_out && (in_place || score_out == score);
+        // a block for each 4096 scores of a head (measured: with fewer the rounds over them take longer, with more their
+        // meetings), as long as the GPU holds them all at once
+        int C = 1;
+        while (C < kMaxCluster && src->cap > 4096 * C && rows * C * 2 <= mq::num_sms()) C *= 2;
+        const int per = (src->cap + C - 1) / C + 32;
+        const int held = per < kMaxKeys ? per : kMaxKeys;
+        const size_t smem = (size_t)held * sizeof(uint32_t);
+        const bool fused = !in_place && !ordered_score && rows * 3 >= mq::num_sms() * 2 &&
+                           (long long)keep * a.chunks < (1LL << 30);
+        // other blocks may still have to read len when the first ones are done: written over it afterwards
+        const bool len_later = overlap(len, (size_t)src->n * 4, len_out, (size_t)src->n * 4);
+        if (fused && len_later) a.len_out = nullptr;
+        rc = launch_select(a, recent, C, held, index, (unsigned)rows, smem, fused, stream);
+        if (rc != MQ_OK || (fused && !len_later)) return rc;
+        if (fused)
+            return mq::launch_pdl(evict_len_kernel, dim3((a.n + 255) / 256), dim3(256), 0, stream, len, len_out, a.n, a.cap,
+                                  keep);
         if (!in_place) {
             if (ordered_score) a.score_out = nullptr;
             const long long units = (long long)a.n * keep * a.heads * a.chunks;

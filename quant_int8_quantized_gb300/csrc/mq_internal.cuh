@@ -57,6 +57,9 @@ int num_sms();      // SM count of the current device (cached)
 // launch shape, then cached. At least 1.
 int resident_blocks(const void* kern, int threads, size_t smem);
 
+// Lets `kern` use `bytes` of dynamic shared memory (asked once per kernel and device).
+bool allow_smem(const void* kern, int bytes);
+
 // Launch with programmatic stream serialization: the kernel may start while the
 // previous kernel on the stream is finishing. Kernels launched this way call
 // mq_grid_wait() before reading anything an earlier kernel writes and before

@@ -245,6 +245,26 @@ def test_evict_long(in_place):
     _evict_case(1, 1, 8, 200000, [199999], 150000, 5, in_place=in_place, kind="ties")
 
 
+@pytest.mark.parametrize("n,H,cap,keep,recent,kind", [
+    (1, 1, 4097, 100, 7, "skew"), (1, 2, 40000, 3000, 17, "equal"), (2, 2, 33000, 32999, 1, "odd"),
+    (1, 1, 700000, 5000, 100, "skew"), (130, 1, 300, 64, 9, "skew"), (20, 8, 513, 200, 31, "ties"),
+    (52, 2, 1000, 1, 0, "odd")])
+def test_evict_row_counts_and_stretches(n, H, cap, keep, recent, kind):
+    """Few long rows (clusters of blocks, stretches that do and do not fit shared memory), many short ones
+    (blocks that move their own rows), length_out the same array as length."""
+    _evict_case(n, H, 8, cap, [cap - 3 * (b % 5) for b in range(n)], keep, recent, kind=kind, seed=n)
+
+
+def test_evict_length_out_apart():
+    for n in (2, 60):
+        src, dst = mq.KV(*(_rand((n, 90, 2, 64), i).half() for i in range(2))), mq.KV.empty(n, 40, 2, 64)
+        length = torch.tensor([90 - b for b in range(n)], dtype=torch.int32, device="cuda")
+        out = torch.full((n,), -7, dtype=torch.int32, device="cuda")
+        score, index = torch.rand((n, 2, 90), device="cuda"), torch.empty((n, 2, 40), dtype=torch.int32, device="cuda")
+        mq.mq_kv_evict(src, length, score, 40, 4, dst, out, None, index)
+        assert out.tolist() == [min(90 - b, 40) for b in range(n)] and length.tolist() == [90 - b for b in range(n)]
+
+
 def test_evict_cache_past_32_bits():
     D, H, cap = 64, 2, 50
     raw = torch.empty((2, 2 ** 31 + 2 ** 22), dtype=F16, device="cuda")
