@@ -15,9 +15,8 @@
 
 namespace {
 
-constexpr int kSelThreads = 1024;
-constexpr int kWarps = kSelThreads / 32;
 constexpr int kMaxCluster = 8;
+constexpr int kBrief = 2048;             // scores of a head up to which a block has 256 threads, not 1024
 constexpr int kMaxKeys = 40 * 1024;      // of a block's stretch that shared memory holds; longer ones are read again
 
 // Order of floats as unsigned integers; -0 equals +0, NaN is below everything.
@@ -39,8 +38,8 @@ __device__ __forceinline__ void cluster_sync() {
 __device__ __forceinline__ int remote(const int* p, uint32_t rank) {
     uint32_t at;
     int v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at));
     return v;
 }
 
@@ -57,9 +56,11 @@ struct Move {
 };
 
 // Selection for one head of one sequence by a cluster of C blocks. MOVE (C == 1): and the move of its rows.
-template <bool MOVE>
+// Few warps for short rows: the rounds are then a matter of barriers and of adding the warps' histograms up.
+template <int kSelThreads, bool MOVE>
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Move a, int recent, int C, int keys_held,
                                                                    int32_t* index) {
+    constexpr int kWarps = kSelThreads / 32;
     extern __shared__ uint32_t s_keys[];                  // keys of this block's stretch, if they fit
     __shared__ int s_hist[kWarps][256];
     __shared__ int s_tot[2][256], s_all[256];
@@ -87,8 +88,18 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Move a,
             const int per = ((cand + C - 1) / C + 31) / 32 * 32;
             const int base = min(rank * per, cand), mine = min(per, cand - base);
             const bool held = mine <= keys_held;
-            if (held)
-                for (int j = tid; j < mine; j += kSelThreads) s_keys[j] = order_key(mq_ld_dep(sc + base + j));
+            if (held) {
+                constexpr int kAtOnce = 8;
+                for (int j0 = tid; j0 < mine; j0 += kAtOnce * kSelThreads) {
+                    float x[kAtOnce];
+#pragma unroll
+                    for (int u = 0; u < kAtOnce; ++u)
+                        if (j0 + u * kSelThreads < mine) x[u] = mq_ld_dep(sc + base + j0 + u * kSelThreads);
+#pragma unroll
+                    for (int u = 0; u < kAtOnce; ++u)
+                        if (j0 + u * kSelThreads < mine) s_keys[j0 + u * kSelThreads] = order_key(x[u]);
+                }
+            }
             __syncthreads();
             auto key = [&](int j) { return held ? s_keys[j] : order_key(mq_ld_dep(sc + base + j)); };
             uint32_t prefix = 0;
@@ -124,9 +135,12 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Move a,
                 if (C > 1) {
                     cluster_sync();
                     if (tid < 256) {
-                        int t = 0;
-                        for (int r = 0; r < C; ++r) t += remote(tot + tid, r);
-                        s_all[tid] = t;
+                        int t[kMaxCluster];
+#pragma unroll
+                        for (int r = 0; r < kMaxCluster; ++r) t[r] = r < C ? remote(tot + tid, r) : 0;
+#pragma unroll
+                        for (int r = 1; r < kMaxCluster; ++r) t[0] += t[r];
+                        s_all[tid] = t[0];
                     }
                 }
                 __syncthreads();
@@ -173,31 +187,28 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Move a,
                 s_eq[wid] = eq;
             }
             __syncthreads();
-            int g0 = 0, e0 = 0;
+            // counts of the warps before this one (a warp per lane), and of the blocks before this block
+            const int wg = lane < kWarps ? s_gt[lane] : 0, we = lane < kWarps ? s_eq[lane] : 0;
+            int g0 = __reduce_add_sync(0xffffffffu, lane < wid ? wg : 0), e0 = __reduce_add_sync(0xffffffffu, lane < wid ? we : 0);
             if (C > 1) {
+                const int ag = __reduce_add_sync(0xffffffffu, wg), ae = __reduce_add_sync(0xffffffffu, we);
                 if (tid == 0) {
-                    int g = 0, e = 0;
-                    for (int w = 0; w < kWarps; ++w) g += s_gt[w], e += s_eq[w];
-                    s_cnt[0] = g;
-                    s_cnt[1] = e;
+                    s_cnt[0] = ag;
+                    s_cnt[1] = ae;
                 }
                 cluster_sync();
-                for (int r = 0; r < rank; ++r) {
-                    g0 += remote(&s_cnt[0], r);
-                    e0 += remote(&s_cnt[1], r);
-                }
+                const int bg = lane < rank ? remote(&s_cnt[0], lane) : 0, be = lane < rank ? remote(&s_cnt[1], lane) : 0;
+                g0 += __reduce_add_sync(0xffffffffu, bg);
+                e0 += __reduce_add_sync(0xffffffffu, be);
             }
-            for (int w = 0; w < wid; ++w) {
-                g0 += s_gt[w];
-                e0 += s_eq[w];
-            }
-            for (int j = j0; j < j1; j += 32) {
-                const uint32_t k = j + lane < j1 ? key(j + lane) : 0u;
-                const bool isg = j + lane < j1 && k > prefix, ise = j + lane < j1 && k == prefix;
+            const unsigned lower = (1u << lane) - 1u;
+            for (int i = j0; i < j1; i += 32) {
+                const int j = i + lane;
+                const uint32_t k = j < j1 ? key(j) : 0u;
+                const bool isg = j < j1 && k > prefix, ise = j < j1 && k == prefix;
                 const unsigned bg = __ballot_sync(0xffffffffu, isg), be = __ballot_sync(0xffffffffu, ise);
-                const unsigned lower = (1u << lane) - 1u;
                 const int g = g0 + __popc(bg & lower), e = e0 + __popc(be & lower);
-                if (isg || (ise && e < need)) out[g + min(e, need)] = base + j + lane;
+                if (isg || (ise && e < need)) out[g + min(e, need)] = base + j;
                 g0 += __popc(bg);
                 e0 += __popc(be);
             }
@@ -214,7 +225,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Move a,
         const uint4 *k = a.k + (long long)b * a.ss + h * a.sh, *v = a.v + (long long)b * a.ss + h * a.sh;
         uint4 *dk = a.dk + (long long)b * a.ds + h * a.dh, *dv = a.dv + (long long)b * a.ds + h * a.dh;
         const int total = kept * a.chunks;
-        constexpr int kAtOnce = 4;
+        constexpr int kAtOnce = 4;   // twice: keys and values
         for (int i0 = tid; i0 < total; i0 += kAtOnce * kSelThreads) {
             uint4 x[kAtOnce], y[kAtOnce];
 #pragma unroll
@@ -239,7 +250,8 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Move a,
     }
 }
 
-// dst apart from src: one thread per 16 bytes of a kept row of k and of v.
+// dst apart from src: 16 bytes of a kept row of k and of v at a time.
+constexpr int kMoveUnits = 2;
 __global__ void __launch_bounds__(256) evict_move_kernel(const Move a) {
     mq_grid_release();
     mq_grid_wait();
@@ -255,19 +267,37 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const Move a) {
             a.score_out[s] = at < 0 ? 0.0f : a.score[s / a.dst_cap * a.cap + at];
         }
     if (a.keep == 0) return;
-    const int c = (int)(i % a.chunks);
-    long long r = i / a.chunks;
-    const int h = (int)(r % a.heads);
-    r /= a.heads;
-    const int j = (int)(r % a.keep);
-    const long long b = r / a.keep;
-    if (b >= a.n) return;
-    const int at = a.index[(b * a.heads + h) * a.dst_cap + j];
-    if (at < 0) return;
-    const long long from = b * a.ss + at * a.sr + h * a.sh + c, to = b * a.ds + j * a.dr + h * a.dh + c;
-    const uint4 x = __ldcs(a.k + from), y = __ldcs(a.v + from);
-    __stcs(a.dk + to, x);
-    __stcs(a.dv + to, y);
+    // kAtOnce units a thread, a grid's width apart
+    constexpr int kAtOnce = kMoveUnits;
+    const long long units = (long long)a.n * a.keep * a.heads * a.chunks, width = (long long)gridDim.x * 256;
+    uint4 x[kAtOnce], y[kAtOnce];
+    long long to[kAtOnce];
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+        const long long w = i + u * width;
+        to[u] = -1;
+        if (w < units) {
+            long long r = w / a.chunks;
+            const int c = (int)(w - r * a.chunks);
+            const long long bj = r / a.heads;
+            const int h = (int)(r - bj * a.heads);
+            const long long b = bj / a.keep;
+            const int j = (int)(bj - b * a.keep);
+            const int at = a.index[(b * a.heads + h) * a.dst_cap + j];
+            if (at >= 0) {
+                const long long from = b * a.ss + at * a.sr + h * a.sh + c;
+                to[u] = b * a.ds + j * a.dr + h * a.dh + c;
+                x[u] = __ldcs(a.k + from);
+                y[u] = __ldcs(a.v + from);
+            }
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u)
+        if (to[u] >= 0) {
+            __stcs(a.dk + to[u], x[u]);
+            __stcs(a.dv + to[u], y[u]);
+        }
 }
 
 // In place: rows only move down (index[j] >= j), so a block that takes one head's rows in order may
@@ -326,7 +356,9 @@ __global__ void __launch_bounds__(256) evict_len_kernel(const int32_t* len, int3
 
 int launch_select(const Move& a, int recent, int C, int held, int32_t* index, unsigned rows, size_t smem, bool fused,
                   cudaStream_t stream) {
-    auto kern = fused ? evict_select_kernel<true> : evict_select_kernel<false>;
+    const bool brief = a.cap <= kBrief;
+    auto kern = fused ? (brief ? evict_select_kernel<256, true> : evict_select_kernel<1024, true>)
+                      : (brief ? evict_select_kernel<256, false> : evict_select_kernel<1024, false>);
     if (!mq::allow_smem(reinterpret_cast<const void*>(kern), kMaxKeys * (int)sizeof(uint32_t))) return MQ_ERR_LAUNCH;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -337,7 +369,7 @@ int launch_select(const Move& a, int recent, int C, int held, int32_t* index, un
     attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(rows * C);
-    cfg.blockDim = dim3(kSelThreads);
+    cfg.blockDim = dim3(brief ? 256 : 1024);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = attr;
@@ -416,8 +448,8 @@ extern "C" int mq_kv_evict(const mq_kv* src, const int32_t* len, const float* sc
         const int per = (src->cap + C - 1) / C + 32;
         const int held = per < kMaxKeys ? per : kMaxKeys;
         const size_t smem = (size_t)held * sizeof(uint32_t);
-        const bool fused = !in_place && !ordered_score && rows * 3 >= mq::num_sms() * 2 &&
-                           (long long)keep * a.chunks < (1LL << 30);
+        const bool fused = !in_place && !ordered_score && C == 1 && (long long)keep * a.chunks < (1LL << 30) &&
+                           rows * 3 >= mq::num_sms() * 2;
         // other blocks may still have to read len when the first ones are done: written over it afterwards
         const bool len_later = overlap(len, (size_t)src->n * 4, len_out, (size_t)src->n * 4);
         if (fused && len_later) a.len_out = nullptr;
@@ -429,7 +461,8 @@ extern "C" int mq_kv_evict(const mq_kv* src, const int32_t* len, const float* sc
         if (!in_place) {
             if (ordered_score) a.score_out = nullptr;
             const long long units = (long long)a.n * keep * a.heads * a.chunks;
-            const long long blocks = ((units > a.n ? units : a.n) + 255) / 256;
+            const long long each = (units + kMoveUnits - 1) / kMoveUnits;
+            const long long blocks = ((each > a.n ? each : a.n) + 255) / 256;
             if (blocks > 0x7fffffffLL) return MQ_ERR_SHAPE;
             rc = mq::launch_pdl(evict_move_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, a);
             if (rc != MQ_OK) return rc;
