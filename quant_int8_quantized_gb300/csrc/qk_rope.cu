@@ -6,16 +6,17 @@
 // head is D / 8 lanes of one aligned group of 8, 16 or 32, the sum of squares a few xor shuffles,
 // and no value passes through shared memory. Values (v) and dims that are not rotated are the
 // same eight numbers a thread, turned by nothing. cos t and sin t depend on token and pair only:
-// a block computes them once for all heads of its tokens, in shared memory, while its first
+// a block computes them once for all heads of its token, in shared memory, while its first
 // heads are on their way.
 //
-// Bound: HBM, 4 bytes read and 2 written an element (M = 1: latency).
+// Bound: HBM, 4 bytes read and 2 written an element (M = 1: latency). Measured: 16384 tokens of 56 heads of 128, 110 us,
+// 6.4 TB/s; 3314 tokens of 36, 20.4 us, 4.5 TB/s; one token of 56, 2.6 us.
 
 #include "heads.cuh"
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 
 struct Args {
     const float* x[3];          // q, k, v (NULL: left out)
@@ -30,7 +31,6 @@ struct Args {
     long long seq_stride, row_stride, head_stride, slots;
     int M, D, n_pairs, n_axes, cap;
     int h0, h1, h2;             // rows of a token: [0, h0) q, [h0, h1) k, [h1, h2) v
-    int tokens;                 // tokens per block
     float eps;
 };
 
@@ -55,64 +55,69 @@ __device__ __forceinline__ float dot8(const float (&v)[8]) {
 // four pairs or eight plain numbers is placed by itself.
 template <typename T, int LG, bool INTER, bool VEC>
 __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const Args a) {
-    extern __shared__ float2 s_turn[];   // [tokens][n_pairs]
+    extern __shared__ float2 s_turn[];   // [n_pairs]
     mq_grid_release();
     mq_grid_wait();
-    const int m0 = blockIdx.x * a.tokens;
-    const int tokens = min(a.tokens, a.M - m0);
-    for (int i = threadIdx.x; i < tokens * a.n_pairs; i += kThreads) {
-        const int m = i / a.n_pairs, p = i - m * a.n_pairs;
-        const int ax = a.axis ? min((int)a.axis[p], a.n_axes - 1) : 0;
-        s_turn[i] = turn(a.pos[(long long)ax * a.M + m0 + m], a.inv_freq[p]);
-    }
-    __syncthreads();
+    const int m = blockIdx.x;            // the token
     const int lane = threadIdx.x % LG;
     const int D = a.D, n = a.n_pairs;
-    const int rows = tokens * a.h2;
-    for (int r = blockIdx.y * (kThreads / LG) + threadIdx.x / LG; r - (int)(threadIdx.x / LG) < rows;
-         r += gridDim.y * (kThreads / LG)) {
-        const bool live = r < rows && lane * 8 < D;
-        const int m = live ? r / a.h2 : 0;
-        const int hr = live ? r - m * a.h2 : 0;
-        const int what = hr < a.h0 ? 0 : hr < a.h1 ? 1 : 2;
-        const int h = hr - (what == 0 ? 0 : what == 1 ? a.h0 : a.h1);
-        const float* x = a.x[what] + (long long)(m0 + m) * a.stride[what] + (long long)h * D;
-        const int np = what == 2 ? 0 : n;             // pairs of this row
-        // this thread's numbers: e[i], i < 4 at lo + i, i >= 4 at hi + i - 4 (VEC)
-        int lo, hi;
-        bool rot = false;
-        if constexpr (VEC) {
-            if (lane * 4 < np) {
-                rot = true;
-                lo = INTER ? lane * 8 : lane * 4;
-                hi = INTER ? lo + 4 : np + lane * 4;
-            } else {
-                lo = 2 * np + (lane - np / 4) * 8;
-                hi = lo + 4;
-            }
-        }
-        // without VEC, element i of this thread is pair p's (i & 1) member for p = 4 lane + i / 2 < np, and
-        // a plain number past that
-        auto place = [&](int i) {
-            const int p = lane * 4 + i / 2;
-            if (p >= np) return lane * 8 + i;
-            return INTER ? 2 * p + (i & 1) : p + (i & 1) * np;
-        };
+    const int rows = a.h2;
+    const int r_first = blockIdx.y * (kThreads / LG) + threadIdx.x / LG, r_step = gridDim.y * (kThreads / LG);
+
+    // a row: which projection and head it is, and this thread's eight numbers of it
+    struct Row {
+        int what, h, np;
         float v[8];
-        if (live) {
-            if constexpr (VEC) {
-                const float4 u0 = __ldcs(reinterpret_cast<const float4*>(x + lo));
-                const float4 u1 = __ldcs(reinterpret_cast<const float4*>(x + hi));
-                v[0] = u0.x, v[1] = u0.y, v[2] = u0.z, v[3] = u0.w;
-                v[4] = u1.x, v[5] = u1.y, v[6] = u1.z, v[7] = u1.w;
-            } else {
+    };
+    // Without VEC, element i of this thread is pair p's (i & 1) member for p = 4 lane + i / 2 < np, and a plain number
+    // past that.
+    auto place = [&](int np, int i) {
+        const int p = lane * 4 + i / 2;
+        if (p >= np) return lane * 8 + i;
+        return INTER ? 2 * p + (i & 1) : p + (i & 1) * np;
+    };
+    // With VEC, elements 0 .. 3 lie at low(np), 4 .. 7 at high(np).
+    auto low = [&](int np) { return INTER || lane * 4 >= np ? lane * 8 : lane * 4; };
+    auto high = [&](int np) { return INTER || lane * 4 >= np ? lane * 8 + 4 : np + lane * 4; };
+    auto fetch = [&](int r, Row& x) {
+        const bool live = r < rows && lane * 8 < D;
+        const int hr = live ? r : 0;
+        x.what = hr < a.h0 ? 0 : hr < a.h1 ? 1 : 2;
+        x.h = hr - (x.what == 0 ? 0 : x.what == 1 ? a.h0 : a.h1);
+        x.np = x.what == 2 ? 0 : n;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = __ldcs(x + place(i));
-            }
+        for (int i = 0; i < 8; ++i) x.v[i] = 0.0f;
+        if (!live) return;
+        const float* p = a.x[x.what] + (long long)m * a.stride[x.what] + (long long)x.h * D;
+        if constexpr (VEC) {
+            const float4 u0 = __ldcs(reinterpret_cast<const float4*>(p + low(x.np)));
+            const float4 u1 = __ldcs(reinterpret_cast<const float4*>(p + high(x.np)));
+            x.v[0] = u0.x, x.v[1] = u0.y, x.v[2] = u0.z, x.v[3] = u0.w;
+            x.v[4] = u1.x, x.v[5] = u1.y, x.v[6] = u1.z, x.v[7] = u1.w;
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+            for (int i = 0; i < 8; ++i) x.v[i] = __ldcs(p + place(x.np, i));
         }
+    };
+    Row now;
+    fetch(r_first, now);             // on its way while the turns are computed
+
+    for (int p = threadIdx.x; p < n; p += kThreads) {
+        const int ax = a.axis ? min((int)a.axis[p], a.n_axes - 1) : 0;
+        s_turn[p] = turn(a.pos[(long long)ax * a.M + m], a.inv_freq[p]);
+    }
+    __syncthreads();
+    for (int r = r_first; r - (int)(threadIdx.x / LG) < rows; r += r_step) {
+        Row next;
+        fetch(r + r_step, next);     // (past the last row: nothing)
+        const bool live = r < rows && lane * 8 < D;
+        const int what = now.what, h = now.h, np = now.np;
+        const int lo = low(np), hi = high(np);
+        const bool rot = lane * 4 < np;
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = now.v[i];
+        now = next;
         const float* w = what == 2 ? nullptr : a.w[what];
         float ss = dot8(v);
 #pragma unroll
@@ -127,10 +132,10 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const Args a) {
                 v[4] *= sc * w1.x, v[5] *= sc * w1.y, v[6] *= sc * w1.z, v[7] *= sc * w1.w;
             } else {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] *= sc * __ldg(w + place(i));
+                for (int i = 0; i < 8; ++i) v[i] *= sc * __ldg(w + place(np, i));
             }
         }
-        const float2* tt = s_turn + m * n;
+        const float2* tt = s_turn;
         auto rotate = [](float& p, float& q, float2 t) {
             const float u = p * t.x - q * t.y;
             q = p * t.y + q * t.x;
@@ -151,9 +156,9 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const Args a) {
         }
         T* y;
         if (what == 0) {
-            y = reinterpret_cast<T*>(a.q_out) + ((long long)(m0 + m) * a.h0 + h) * D;
+            y = reinterpret_cast<T*>(a.q_out) + ((long long)m * a.h0 + h) * D;
         } else {
-            const long long s = a.slot ? (long long)a.slot[m0 + m] : (long long)(m0 + m);
+            const long long s = a.slot ? (long long)a.slot[m] : (long long)m;
             if (s < 0 || s >= a.slots) continue;
             const long long seq = s / a.cap;
             y = reinterpret_cast<T*>(a.kv[what - 1]) + seq * a.seq_stride + (s - seq * a.cap) * a.row_stride +
@@ -170,7 +175,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const Args a) {
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[place(i)] = T(v[i]);
+            for (int i = 0; i < 8; ++i) y[place(np, i)] = T(v[i]);
         }
     }
 }
@@ -243,14 +248,11 @@ extern "C" int mq_qk_norm_rope(const mq_qkv* x, void* q_out, const mq_kv* cache,
     a.eps = x->eps;
     if (a.h2 == 0) return MQ_OK;
     const int lg = D <= 64 ? 8 : D <= 128 ? 16 : 32, per = kThreads / lg;
-    // A block takes whole tokens, all heads of up to 4 of them, where that still gives every SM
-    // a few blocks; the heads of a few tokens are spread over blocks of one pass each.
-    a.tokens = x->M >= 4 * 8 * mq::num_sms() ? 4 : 1;
-    const int blocks = (x->M + a.tokens - 1) / a.tokens;
-    const int passes = (a.tokens * a.h2 + per - 1) / per;
-    const int y = blocks >= 8 * mq::num_sms() ? 1 : passes < 65535 ? passes : 65535;
-    const dim3 grid(blocks, y);
-    const size_t smem = (size_t)a.tokens * a.n_pairs * sizeof(float2);
+    // A block takes a token, all its heads (measured at 3314 tokens of 36 heads of 128: 20.4 us; 256 threads with 1, 2, 3, 4
+    // and 5 tokens: 26.2, 23.6, 23.1, 23.0 and 25.6); the heads of a few tokens are spread over blocks of one pass each.
+    const int passes = (a.h2 + per - 1) / per;
+    const dim3 grid(x->M, x->M >= 2 * mq::num_sms() ? 1 : passes < 65535 ? passes : 65535);
+    const size_t smem = (size_t)a.n_pairs * sizeof(float2);
     const bool inter = x->interleaved != 0;
     auto go = [&](auto t) {
         using T = decltype(t);
