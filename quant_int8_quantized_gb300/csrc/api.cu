@@ -71,7 +71,10 @@ bool allow_smem(const void* kern, int bytes) {
     const auto key = std::make_pair(kern, dev);
     const auto it = done.find(key);
     if (it != done.end()) return it->second;
-    const bool ok = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
+    const bool ok =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess &&
+        cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) ==
+            cudaSuccess;
     if (!ok) cudaGetLastError();
     done.emplace(key, ok);
     return ok;

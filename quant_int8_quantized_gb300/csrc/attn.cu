@@ -261,7 +261,7 @@ Cut cut_of(int B, int T, int Hq, int Hkv, int D, int prefix_keys, int own_cap, b
     const long long row_tiles = ceil_div((long long)T * group, kFewRows), key_bytes = 4LL * Hkv * D;
     const long long own_rows = (long long)T * group, prefix_rows = B * own_rows;
     c.own_many = own_cap > 0 && many_takes(D, group) && !scores && own_rows >= kManyFrom &&
-                 B * row_tiles * (prefix_keys + (long long)own_cap) * key_bytes > kFewBytes;
+                 B * row_tiles * own_cap * key_bytes > kFewBytes;
     c.prefix_many = prefix_keys > 0 && !c.own_many && many_takes(D, group) && prefix_rows >= kManyFrom &&
                     ceil_div(prefix_rows, kFewRows) * prefix_keys * key_bytes > kFewBytes;
     c.fits = true;
@@ -412,8 +412,9 @@ extern "C" int mq_attn_prefix(const void* q, long long q_stride, int B, int T, i
             const int most = T * (Hq / Hkv) < c.many.rows ? T * (Hq / Hkv) : c.many.rows;
             auto join = [&](auto o) {
                 using O = decltype(o);
-                return mq::launch_pdl(D == 64 ? attn_join_split_kernel<O, 64> : attn_join_split_kernel<O, 128>,
-                                      dim3(c.many.G, (most + 7) / 8), dim3(256), 0, stream, s);
+                auto kern = D == 64 ? attn_join_split_kernel<O, 64> : attn_join_split_kernel<O, 128>;
+                if (!mq::allow_smem(reinterpret_cast<const void*>(kern), 0)) return (int)MQ_ERR_LAUNCH;
+                return mq::launch_pdl(kern, dim3(c.many.G, (most + 7) / 8), dim3(256), 0, stream, s);
             };
             return out_type == MQ_F32 ? join(float()) : out_type == MQ_F16 ? join(__half()) : join(__nv_bfloat16());
         }
@@ -450,11 +451,13 @@ extern "C" int mq_attn_prefix(const void* q, long long q_stride, int B, int T, i
         using O = decltype(o);
         auto kern = D == 64 ? attn_join_kernel<O, 64> : D == 96 ? attn_join_kernel<O, 96>
                     : D == 128 ? attn_join_kernel<O, 128> : attn_join_kernel<O, 256>;
+        if (!mq::allow_smem(reinterpret_cast<const void*>(kern), 0)) return (int)MQ_ERR_LAUNCH;
         return mq::launch_pdl(kern, grid, dim3(32 * kJoinWarps), 0, stream, j);
     };
     rc = out_type == MQ_F32 ? join(float()) : out_type == MQ_F16 ? join(__half()) : join(__nv_bfloat16());
     if (rc != MQ_OK || !scores) return rc;
     auto score_call = [&](auto kern, int keys) {
+        if (!mq::allow_smem(reinterpret_cast<const void*>(kern), 0)) return (int)MQ_ERR_LAUNCH;
         return mq::launch_pdl(kern, dim3((cap + keys - 1) / keys, B * Hkv), dim3(128), 0, stream, raw, lse2, own_len,
                               score, score_out, T, Hq, Hkv, cap);
     };

@@ -31,7 +31,9 @@ struct Cfg {
     static constexpr int kBoxBytes = kKeys * kRow;
     static constexpr int kTileBytes = kBoxes * kBoxBytes;     // of keys, or of values
     static constexpr int kStageBytes = 2 * kTileBytes;        // keys, then values
-    static constexpr int kStages = D <= 64 ? 6 : D <= 96 ? 4 : D <= 128 ? 3 : 2;
+    // 16 KB or so of stages: with 24 (measured) an SM no longer holds eight blocks together with what each has beside
+    // them, and the last ones start when the first have ended
+    static constexpr int kStages = D <= 64 ? 4 : D <= 96 ? 3 : 2;
     static constexpr int kSmem = 1024 + kStages * kStageBytes;
     // what the swizzle adds (xor) to the units of a row
     __device__ static __forceinline__ int twist(int row) { return kDims == 64 ? row & 7 : (row >> 1) & 3; }
@@ -82,16 +84,17 @@ __device__ __forceinline__ float exp2_fast(float x) {   // 2^x within 2 ulp; 2^-
 constexpr float kNone = -INFINITY;
 
 template <typename T, int D, bool RAW>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 8)
     attn_few_kernel(const FewArgs a, const __grid_constant__ CUtensorMap pk, const __grid_constant__ CUtensorMap pv,
                     const __grid_constant__ CUtensorMap ok, const __grid_constant__ CUtensorMap ov) {
     using C = Cfg<D>;
     extern __shared__ uint8_t s_raw[];
     __shared__ Piece s_piece[C::kStages + 1];
     __shared__ uint64_t s_full[C::kStages];
+    constexpr int stages = C::kStages;
     mq_grid_release();
     if (threadIdx.x == 0) {
-        for (int i = 0; i < C::kStages; ++i) tc::mbar_init(&s_full[i], 1);
+        for (int i = 0; i < stages; ++i) tc::mbar_init(&s_full[i], 1);
         tc::fence_mbar_init();
         tc::prefetch_tensormap(&pk);
         tc::prefetch_tensormap(&pv);
@@ -105,7 +108,7 @@ __global__ void __launch_bounds__(kThreads)
     const uint32_t ring = (tc::smem_u32(s_raw) + 1023) & ~1023u;
     const int g = lane >> 2, t2 = (lane & 3) * 2;   // this thread's rows g, g + 8 and columns t2, t2 + 1
 
-    // ---------------------------------------------------------------- copies, kStages - 1 tiles ahead
+    // ---------------------------------------------------------------- copies, stages - 1 tiles ahead
     Cursor c = find_run<kThreads>(p, a.len);
     advance(p, a.len, c, 0);
     int left = 0, handed = 0, key = 0, in_slot = 0;    // tiles of the copied piece left, pieces handed over
@@ -136,7 +139,7 @@ __global__ void __launch_bounds__(kThreads)
             __syncwarp();
             if (lane == 0) s_piece[handed] = q;
             __syncwarp();
-            if (++handed == C::kStages + 1) handed = 0;
+            if (++handed == stages + 1) handed = 0;
         }
         if (left > 0) {
             if (lane == 0) {
@@ -152,11 +155,11 @@ __global__ void __launch_bounds__(kThreads)
             ++issued;
             key += kKeys;
             --left;
-            if (++in_slot == C::kStages) in_slot = 0;
+            if (++in_slot == stages) in_slot = 0;
         }
     };
 #pragma unroll 1
-    for (int t = 0; t < C::kStages - 1; ++t) copy();
+    for (int t = 0; t < stages - 1; ++t) copy();
 
     // ---------------------------------------------------------------- products
     // Byte of this lane's row and unit in a box, for the loads of keys (rows of eight keys, 8 dims side by side) and of
@@ -171,7 +174,7 @@ __global__ void __launch_bounds__(kThreads)
     while (alive) {
         const Piece w = s_piece[taken];
         if (w.n == 0) break;
-        if (++taken == C::kStages + 1) taken = 0;
+        if (++taken == stages + 1) taken = 0;
         // query rows g and g + 8 (zeros past the last), as left operands; the keys that each sees
         uint32_t qf[D / 16][4];
         int seen[2];
@@ -213,7 +216,7 @@ __global__ void __launch_bounds__(kThreads)
                 tc::fence_proxy_async_smem();
                 __syncwarp();
             }
-            if (++slot == C::kStages) {
+            if (++slot == stages) {
                 slot = 0;
                 phase ^= 1;
             }
@@ -310,7 +313,7 @@ __global__ void __launch_bounds__(kThreads)
     }
     if (!alive) {   // a copy never came: recorded; those still in flight must land before the block leaves
         if (lane == 0) atomicOr(&g_few_error, 1u);
-        for (int i = 0; i < C::kStages && i < issued; ++i) tc::mbar_wait(&s_full[slot], phase, kWaitLimitNs);
+        for (int i = 0; i < stages && i < issued; ++i) tc::mbar_wait(&s_full[slot], phase, kWaitLimitNs);
     }
     // what follows counts on attn_many too: the last block, and with it this kernel, ends after it (the others make
     // room for more)

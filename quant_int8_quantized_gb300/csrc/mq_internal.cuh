@@ -57,7 +57,9 @@ int num_sms();      // SM count of the current device (cached)
 // launch shape, then cached. At least 1.
 int resident_blocks(const void* kern, int threads, size_t smem);
 
-// Lets `kern` use `bytes` of dynamic shared memory (asked once per kernel and device).
+// Lets `kern` use `bytes` of dynamic shared memory, on SMs set up with as much of it as there is (asked once per kernel
+// and device). Kernels that run one behind the other with less ask for the same set-up: an SM has to run empty
+// before it changes over.
 bool allow_smem(const void* kern, int bytes);
 
 // Launch with programmatic stream serialization: the kernel may start while the
