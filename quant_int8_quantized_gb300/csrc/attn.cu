@@ -38,11 +38,11 @@ __device__ __forceinline__ Run run_of(const Part& p, int seg, int2 f, int in) {
 
 // One warp adds up a row's pieces, those of run 0 and then those of run 1: their common maximum, then outputs
 // weighted and added in order. Lane i holds place, maximum and sum of piece i of 32; the outputs' loads do not
-// depend on one another.
-template <typename O, int D>
+// depend on one another, kAtOnce (a divisor of 32) are asked for at once.
+template <typename O, int D, int kAtOnce>
 __device__ __forceinline__ void join_row(const Run& r0, const Run& r1, const Out& fin, float* lse2, long long row) {
     // lane l holds V floats at V (l + 32 k)
-    constexpr int V = D >= 128 ? 4 : 2, W = (D + 32 * V - 1) / (32 * V), kAtOnce = 8;   // divides 32
+    constexpr int V = D >= 128 ? 4 : 2, W = (D + 32 * V - 1) / (32 * V);
     const int lane = threadIdx.x & 31, count = r0.count + r1.count;
     float m = -INFINITY, l = 0.0f;
     float acc[W][V] = {};
@@ -125,7 +125,7 @@ __device__ __forceinline__ void join_row(const Run& r0, const Run& r1, const Out
 }
 
 // Every query row, a warp each: its prefix segment's pieces, then its own segment's.
-constexpr int kJoinWarps = 4;
+constexpr int kJoinWarps = 1;   // few rows: as many SMs as there are; many: no matter
 template <typename O, int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const JoinArgs a) {
     mq_grid_release();
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const JoinAr
     }
     if (a.prefix.rows > 0) runs[0] = run_of(a.prefix, seg0, f0, in0);
     if (a.own.rows > 0 && min(max(len, 0), a.own_cap) - a.T + 1 + last / a.group > 0) runs[1] = run_of(a.own, seg1, f1, in1);
-    join_row<O, D>(runs[0], runs[1], a.fin, a.lse2, row);
+    join_row<O, D, 16>(runs[0], runs[1], a.fin, a.lse2, row);
 }
 
 // The rows of the segments that one block of the first kernel began and another ended: grid x that block, y eight
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(256) attn_join_split_kernel(const SplitArgs a)
     const int in = blockIdx.y * 8 + (threadIdx.x >> 5);
     if (in >= rows) return;
     const int r = rt * a.plan.rows + in, t = a.plan.by_group.of(r);
-    join_row<O, D>(run_of(a.part, s.x, make_int2(blockIdx.x, s.y), in), Run{}, a.fin, nullptr,
+    join_row<O, D, 4>(run_of(a.part, s.x, make_int2(blockIdx.x, s.y), in), Run{}, a.fin, nullptr,
                    ((long long)b * a.plan.T + t) * a.plan.Hq + s.w * a.plan.group + r - t * a.plan.group);
 }
 
@@ -236,7 +236,7 @@ size_t up16(size_t n) { return (n + 15) & ~(size_t)15; }
 // The kernel for few rows reads a part's keys and values once for each 16 query rows of a key head, mostly out of L2.
 // Up to so many bytes that is quicker than the tensor-core kernel, which takes some 12 us whatever it does.
 #ifndef MQ_FEW_BYTES
-#define MQ_FEW_BYTES (24LL << 20)
+#define MQ_FEW_BYTES (64LL << 20)
 #endif
 constexpr long long kFewBytes = MQ_FEW_BYTES;
 constexpr int kManyFrom = 33;   // query rows per key head, at least, for the tensor-core kernel
