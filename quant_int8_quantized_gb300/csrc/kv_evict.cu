@@ -7,9 +7,9 @@
 // scores from memory once. Then every warp writes the kept rows of its own stretch in order, from the
 // counts of the stretches before it. Counts are integers: the result does not depend on the order of the
 // atomics.
-// Then rows, values and scores move: 16 bytes a thread, every kept row read once and written once. Where there are
-// enough heads to fill the machine with blocks, each moves the rows of the head that it selected for; else a
-// second launch shares them out evenly.
+// Then rows, values and scores move in a second launch, which shares them out evenly: 16 bytes at a time, every kept
+// row read once and written once (blocks that move what they selected themselves took longer, 69 us for 65 at 256 heads of
+// up to 4096 rows: the machine waits for the SMs that hold two of them).
 
 #include "heads.cuh"
 
@@ -55,9 +55,9 @@ struct Move {
     int n, heads, cap, dst_cap, keep, chunks;
 };
 
-// Selection for one head of one sequence by a cluster of C blocks. MOVE (C == 1): and the move of its rows.
+// Selection for one head of one sequence by a cluster of C blocks.
 // Few warps for short rows: the rounds are then a matter of barriers and of adding the warps' histograms up.
-template <int kSelThreads, bool MOVE>
+template <int kSelThreads>
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Move a, int recent, int C, int keys_held,
                                                                    int32_t* index) {
     constexpr int kWarps = kSelThreads / 32;
@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Move a,
     mq_grid_wait();
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     const int rank = C > 1 ? (int)cluster_rank() : 0, row = blockIdx.x / C;
-    const int b = row / a.heads, h = row - b * a.heads;
+    const int b = row / a.heads;
     const int n = min(max(a.len[b], 0), a.cap), keep = a.keep, dst_cap = a.dst_cap;
     const float* sc = a.score + (long long)row * a.cap;
     int32_t* out = index + (long long)row * dst_cap;
@@ -215,39 +215,6 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Move a,
             if (C > 1) cluster_sync();           // the others are done with this block's counts
         }
     }
-    if constexpr (MOVE) {
-        __syncthreads();
-        const int kept = min(n, keep);
-        if (h == 0 && tid == 0 && a.len_out) a.len_out[b] = kept;
-        if (a.score_out)
-            for (int j = tid; j < dst_cap; j += kSelThreads)
-                a.score_out[(long long)row * dst_cap + j] = j < kept ? sc[out[j]] : 0.0f;
-        const uint4 *k = a.k + (long long)b * a.ss + h * a.sh, *v = a.v + (long long)b * a.ss + h * a.sh;
-        uint4 *dk = a.dk + (long long)b * a.ds + h * a.dh, *dv = a.dv + (long long)b * a.ds + h * a.dh;
-        const int total = kept * a.chunks;
-        constexpr int kAtOnce = 4;   // twice: keys and values
-        for (int i0 = tid; i0 < total; i0 += kAtOnce * kSelThreads) {
-            uint4 x[kAtOnce], y[kAtOnce];
-#pragma unroll
-            for (int u = 0; u < kAtOnce; ++u) {
-                const int i = i0 + u * kSelThreads, j = i / a.chunks;
-                if (i < total) {
-                    const long long from = out[j] * a.sr + i - j * a.chunks;
-                    x[u] = __ldcs(k + from);
-                    y[u] = __ldcs(v + from);
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < kAtOnce; ++u) {
-                const int i = i0 + u * kSelThreads, j = i / a.chunks;
-                if (i < total) {
-                    const long long to = j * a.dr + i - j * a.chunks;
-                    __stcs(dk + to, x[u]);
-                    __stcs(dv + to, y[u]);
-                }
-            }
-        }
-    }
 }
 
 // dst apart from src: 16 bytes of a kept row of k and of v at a time.
@@ -354,11 +321,10 @@ __global__ void __launch_bounds__(256) evict_len_kernel(const int32_t* len, int3
     if (i < n) len_out[i] = min(min(max(len[i], 0), cap), keep);
 }
 
-int launch_select(const Move& a, int recent, int C, int held, int32_t* index, unsigned rows, size_t smem, bool fused,
+int launch_select(const Move& a, int recent, int C, int held, int32_t* index, unsigned rows, size_t smem,
                   cudaStream_t stream) {
     const bool brief = a.cap <= kBrief;
-    auto kern = fused ? (brief ? evict_select_kernel<256, true> : evict_select_kernel<1024, true>)
-                      : (brief ? evict_select_kernel<256, false> : evict_select_kernel<1024, false>);
+    auto kern = brief ? evict_select_kernel<256> : evict_select_kernel<1024>;
     if (!mq::allow_smem(reinterpret_cast<const void*>(kern), kMaxKeys * (int)sizeof(uint32_t))) return MQ_ERR_LAUNCH;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -448,16 +414,8 @@ extern "C" int mq_kv_evict(const mq_kv* src, const int32_t* len, const float* sc
         const int per = (src->cap + C - 1) / C + 32;
         const int held = per < kMaxKeys ? per : kMaxKeys;
         const size_t smem = (size_t)held * sizeof(uint32_t);
-        const bool fused = !in_place && !ordered_score && C == 1 && (long long)keep * a.chunks < (1LL << 30) &&
-                           rows * 3 >= mq::num_sms() * 2;
-        // other blocks may still have to read len when the first ones are done: written over it afterwards
-        const bool len_later = overlap(len, (size_t)src->n * 4, len_out, (size_t)src->n * 4);
-        if (fused && len_later) a.len_out = nullptr;
-        rc = launch_select(a, recent, C, held, index, (unsigned)rows, smem, fused, stream);
-        if (rc != MQ_OK || (fused && !len_later)) return rc;
-        if (fused)
-            return mq::launch_pdl(evict_len_kernel, dim3((a.n + 255) / 256), dim3(256), 0, stream, len, len_out, a.n, a.cap,
-                                  keep);
+        rc = launch_select(a, recent, C, held, index, (unsigned)rows, smem, stream);
+        if (rc != MQ_OK) return rc;
         if (!in_place) {
             if (ordered_score) a.score_out = nullptr;
             const long long units = (long long)a.n * keep * a.heads * a.chunks;
