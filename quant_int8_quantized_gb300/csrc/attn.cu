@@ -31,9 +31,11 @@ struct Run {
     int count;
 };
 
-// Pieces of row `in` of a segment whose blocks are f.x .. f.y.
+// Pieces of row `in` of a segment whose blocks are f.x .. f.y; none where these are no blocks (a kernel that gave up on
+// a wait leaves entries unwritten).
 __device__ __forceinline__ Run run_of(const Part& p, int seg, int2 f, int in) {
-    return Run{&p.p, (long long)place_of(p.plan, f.x, seg) * p.rows + in, p.rows, f.y - f.x + 1};
+    const bool ok = f.x >= 0 && f.y >= f.x && f.y < p.plan.G / p.plan.lanes;
+    return Run{&p.p, ok ? (long long)place_of(p.plan, f.x, seg) * p.rows + in : 0, p.rows, ok ? f.y - f.x + 1 : 0};
 }
 
 // One warp adds up a row's pieces, those of run 0 and then those of run 1: their common maximum, then outputs
@@ -235,14 +237,20 @@ size_t up16(size_t n) { return (n + 15) & ~(size_t)15; }
 
 // The kernel for few rows reads a part's keys and values once for each 16 query rows of a key head, mostly out of L2.
 // Up to so many bytes that is quicker than the tensor-core kernel, which takes some 12 us whatever it does.
-#ifndef MQ_FEW_BYTES
+#ifndef MQ_FEW_BYTES   // (these limits: test builds send small calls to the tensor-core kernel)
 #define MQ_FEW_BYTES (64LL << 20)
 #endif
 constexpr long long kFewBytes = MQ_FEW_BYTES;
-constexpr int kManyFrom = 33;   // query rows per key head, at least, for the tensor-core kernel
+#ifndef MQ_MANY_FROM
+#define MQ_MANY_FROM 33
+#endif
+constexpr int kManyFrom = MQ_MANY_FROM;   // query rows per key head, at least, for the tensor-core kernel
 // Bytes of the prefix from which several row tiles of it are taken side by side, and how many at most: more of them
 // leave more of the blocks that they do not divide idle.
-constexpr long long kLanesFrom = 24 << 20;
+#ifndef MQ_LANES_FROM
+#define MQ_LANES_FROM (24LL << 20)
+#endif
+constexpr long long kLanesFrom = MQ_LANES_FROM;
 constexpr int kLanesMost = 8;
 constexpr int kBeside = 2;
 constexpr double kTileUs = 1.4, kDraw = 116e3;   // of a tile of two halves, measured; of an SM's eight warps with two stages in flight

@@ -18,6 +18,9 @@ namespace attn {
 namespace {
 
 __device__ unsigned int g_few_error;   // bit 0: a bounded wait gave up
+#ifdef MQ_TEST_INJECT
+__device__ int g_test_skip_tile;       // test builds only: block 0 leaves out its first tile
+#endif
 
 constexpr int kThreads = 32;
 constexpr int kKeys = kFewKeys;
@@ -142,7 +145,12 @@ __global__ void __launch_bounds__(kThreads, 8)
             if (++handed == stages + 1) handed = 0;
         }
         if (left > 0) {
-            if (lane == 0) {
+#ifdef MQ_TEST_INJECT
+            const bool skip = g_test_skip_tile && blockIdx.x == 0 && issued == 0;
+#else
+            constexpr bool skip = false;
+#endif
+            if (!skip && lane == 0) {
                 const uint32_t st = ring + in_slot * C::kStageBytes;
                 const CUtensorMap *km = shared ? &pk : &ok, *vm = shared ? &pv : &ov;
                 tc::mbar_arrive_expect_tx(&s_full[in_slot], C::kStageBytes);
@@ -168,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, 8)
     const uint32_t k_at = k_row * C::kRow + ((((lane >> 3) & 1) ^ C::twist(k_row)) << 4);
     const uint32_t v_at = C::kTileBytes + v_row * C::kRow + (((lane >> 4) ^ C::twist(v_row)) << 4);
     constexpr int kPairs = C::kUnits / 2;   // 16 dims each
-    int taken = 0, slot = 0;
+    int taken = 0, slot = 0, taken_tiles = 0;
     uint32_t phase = 0;
     bool alive = true;
     while (alive) {
@@ -216,6 +224,7 @@ __global__ void __launch_bounds__(kThreads, 8)
                 tc::fence_proxy_async_smem();
                 __syncwarp();
             }
+            ++taken_tiles;
             if (++slot == stages) {
                 slot = 0;
                 phase ^= 1;
@@ -354,6 +363,10 @@ int launch_few(const FewArgs& a, const mq_kv* prefix, const mq_kv* own, int D, i
         return mq::launch_pdl(kern, dim3(a.plan.G), dim3(kThreads), smem, stream, a, pk, pv, ok, ov);
     });
 }
+
+#ifdef MQ_TEST_INJECT
+bool test_skip_few(int on) { return cudaMemcpyToSymbol(g_test_skip_tile, &on, sizeof(on)) == cudaSuccess; }
+#endif
 
 int take_few_error(unsigned* code) {
     if (cudaMemcpyFromSymbol(code, g_few_error, sizeof(*code)) != cudaSuccess) return MQ_ERR_LAUNCH;

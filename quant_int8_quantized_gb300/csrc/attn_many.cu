@@ -34,6 +34,10 @@ namespace attn {
 namespace {
 
 __device__ unsigned int g_attn_error;   // bit 0: a bounded wait gave up
+#ifdef MQ_TEST_INJECT
+// Test builds only: block 0 leaves out its first tile of keys, whose barrier then never completes.
+__device__ int g_test_skip_tile;
+#endif
 
 constexpr int kThreads = 384;
 // Registers a thread: what the launch gives to 384 threads, and after sharing out again (2 x 208 + 88 = 3 x 168).
@@ -432,7 +436,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int k0 = (shared ? tile : tile - g.lead) * kKeys;
                     for (int kv = 0; kv < 2; ++kv) {
                         if (!(alive = wwait(bars, &bars.empty[slot], phase ^ 1))) break;
-                        if (tc::elect_one()) {
+#ifdef MQ_TEST_INJECT
+                        const bool skip = g_test_skip_tile && blockIdx.x == 0 && issued == 0;
+#else
+                        constexpr bool skip = false;
+#endif
+                        if (!skip && tc::elect_one()) {
                             const CUtensorMap* map = shared ? (kv ? &pv : &pk) : (kv ? &ov : &ok);
                             tc::mbar_arrive_expect_tx(&bars.full[slot], C::kTileBytes);
 #pragma unroll
@@ -664,3 +673,13 @@ int take_attn_device_error(cudaStream_t stream, unsigned* code) {
     return MQ_OK;
 }
 }  // namespace mq
+
+#ifdef MQ_TEST_INJECT
+// Test builds only: bit 0: attn_many, bit 1: attn_few leaves out a copy.
+extern "C" int mq_test_inject_attn(int bits) {
+    const int many = bits & 1;
+    return cudaMemcpyToSymbol(attn::g_test_skip_tile, &many, sizeof(many)) == cudaSuccess && attn::test_skip_few(bits >> 1 & 1)
+               ? MQ_OK
+               : MQ_ERR_LAUNCH;
+}
+#endif

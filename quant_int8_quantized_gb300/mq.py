@@ -62,48 +62,53 @@ def lib() -> ctypes.CDLL:
     if _lib is None:
         if not os.path.exists(LIB_PATH):
             raise RuntimeError(f"{LIB_PATH} is missing: build it with __graft_entry__.build()")
-        L = ctypes.CDLL(LIB_PATH)
-        vp, i, f, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
-        pp = ctypes.POINTER(CPlane)
-        psz = ctypes.POINTER(ctypes.c_size_t)
-        sig = {
-            "mq_plane_bytes": (sz, [i, i, psz, psz, psz, psz, psz, psz]),
-            "mq_q4k_row_bytes": (sz, [i]),
-            "mq_q6k_row_bytes": (sz, [i]),
-            "mq_q6k_packed_row_bytes": (sz, [i]),
-            "mq_prepack_q6k": (i, [vp, i, i, vp, vp]),
-            "mq_quantize_q8": (i, [vp, i, i, pp, vp]),
-            "mq_rms_quant": (i, [vp, vp, i, i, f, pp, vp]),
-            "mq_swiglu_quant": (i, [vp, vp, i, i, pp, vp]),
-            "mq_gemm_q4k": (i, [pp, vp, i, vp, vp]),
-            "mq_gemm_q6k": (i, [pp, vp, i, vp, vp]),
-            "mq_gemv_q4k": (i, [pp, vp, i, vp, vp]),
-            "mq_gemv_q6k": (i, [pp, vp, i, vp, vp]),
-            "mq_gemv_q6k_packed": (i, [pp, vp, i, vp, vp]),
-            "mq_gemm_q6k_static": (i, [pp, vp, i, vp, vp]),
-            "mq_gemm_q4k_pair": (i, [pp, vp, i, vp, vp, i, vp, vp]),
-            "mq_q5k_row_bytes": (sz, [i]),
-            "mq_q4_0_row_bytes": (sz, [i]),
-            "mq_q4_1_row_bytes": (sz, [i]),
-            "mq_gemv_q5k": (i, [pp, vp, i, vp, vp]),
-            "mq_gemv_q4_0": (i, [pp, vp, i, vp, vp]),
-            "mq_gemv_q4_1": (i, [pp, vp, i, vp, vp]),
-            "mq_gemm_q4_0": (i, [pp, vp, i, vp, vp]),
-            "mq_gemm_q4_1": (i, [pp, vp, i, vp, vp]),
-            "mq_qk_norm_rope": (i, [ctypes.POINTER(CQKV), vp, ctypes.POINTER(CKV), vp, vp]),
-            "mq_attn_ws_bytes": (sz, [i, i, i, i, i, i, i, i]),
-            "mq_attn_prefix": (i, [vp, ctypes.c_longlong, i, i, i, ctypes.POINTER(CKV), ctypes.POINTER(CKV), vp, f, vp, i,
-                                   vp, vp, vp, vp, sz, vp]),
-            "mq_kv_evict": (i, [ctypes.POINTER(CKV), vp, vp, i, i, ctypes.POINTER(CKV), vp, vp, vp, vp]),
-            "mq_device_status": (i, [vp]),
-            "mq_status_str": (ctypes.c_char_p, [i]),
-        }
-        for name, (res, args) in sig.items():
-            fn = getattr(L, name)
-            fn.restype = res
-            fn.argtypes = args
-        _lib = L
+        _lib = _load(LIB_PATH)
     return _lib
+
+
+def _load(path: str) -> ctypes.CDLL:
+    """A build of the library with its entry points' signatures."""
+    L = ctypes.CDLL(path)
+    vp, i, f, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+    pp = ctypes.POINTER(CPlane)
+    psz = ctypes.POINTER(ctypes.c_size_t)
+    sig = {
+        "mq_plane_bytes": (sz, [i, i, psz, psz, psz, psz, psz, psz]),
+        "mq_q4k_row_bytes": (sz, [i]),
+        "mq_q6k_row_bytes": (sz, [i]),
+        "mq_q6k_packed_row_bytes": (sz, [i]),
+        "mq_prepack_q6k": (i, [vp, i, i, vp, vp]),
+        "mq_quantize_q8": (i, [vp, i, i, pp, vp]),
+        "mq_rms_quant": (i, [vp, vp, i, i, f, pp, vp]),
+        "mq_swiglu_quant": (i, [vp, vp, i, i, pp, vp]),
+        "mq_gemm_q4k": (i, [pp, vp, i, vp, vp]),
+        "mq_gemm_q6k": (i, [pp, vp, i, vp, vp]),
+        "mq_gemv_q4k": (i, [pp, vp, i, vp, vp]),
+        "mq_gemv_q6k": (i, [pp, vp, i, vp, vp]),
+        "mq_gemv_q6k_packed": (i, [pp, vp, i, vp, vp]),
+        "mq_gemm_q6k_static": (i, [pp, vp, i, vp, vp]),
+        "mq_gemm_q4k_pair": (i, [pp, vp, i, vp, vp, i, vp, vp]),
+        "mq_q5k_row_bytes": (sz, [i]),
+        "mq_q4_0_row_bytes": (sz, [i]),
+        "mq_q4_1_row_bytes": (sz, [i]),
+        "mq_gemv_q5k": (i, [pp, vp, i, vp, vp]),
+        "mq_gemv_q4_0": (i, [pp, vp, i, vp, vp]),
+        "mq_gemv_q4_1": (i, [pp, vp, i, vp, vp]),
+        "mq_gemm_q4_0": (i, [pp, vp, i, vp, vp]),
+        "mq_gemm_q4_1": (i, [pp, vp, i, vp, vp]),
+        "mq_qk_norm_rope": (i, [ctypes.POINTER(CQKV), vp, ctypes.POINTER(CKV), vp, vp]),
+        "mq_attn_ws_bytes": (sz, [i, i, i, i, i, i, i, i]),
+        "mq_attn_prefix": (i, [vp, ctypes.c_longlong, i, i, i, ctypes.POINTER(CKV), ctypes.POINTER(CKV), vp, f, vp, i,
+                               vp, vp, vp, vp, sz, vp]),
+        "mq_kv_evict": (i, [ctypes.POINTER(CKV), vp, vp, i, i, ctypes.POINTER(CKV), vp, vp, vp, vp]),
+        "mq_device_status": (i, [vp]),
+        "mq_status_str": (ctypes.c_char_p, [i]),
+    }
+    for name, (res, args) in sig.items():
+        fn = getattr(L, name)
+        fn.restype = res
+        fn.argtypes = args
+    return L
 
 
 def status_str(status: int) -> str:

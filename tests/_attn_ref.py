@@ -7,9 +7,10 @@ U = {torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 **
 TINY = {torch.float16: 2.0 ** -25, torch.bfloat16: 2.0 ** -134, torch.float32: 2.0 ** -150}
 
 
-def attention(q, pk, pv, k, v, lens, scale, out_dtype, score=None):
+def attention(q, pk, pv, k, v, lens, scale, out_dtype, score=None, only=None):
     """(out, lse, score_out) and their bounds, f64. q [B, T, Hq, D]; pk, pv [P, Hkv, D] or None; k, v
-    [B, cap, Hkv, D] or None; lens: list. Only visible keys are ever touched.
+    [B, cap, Hkv, D] or None; lens: list. Only visible keys are ever touched. only: the queries looked at, by
+    number (the others' entries mean nothing).
 
     Bounds: the products q.k are f32 sums of exact products, off by at most 2^-20 sum |q k| scale here
     (D <= 256 terms), the exponentials by 2^-20 relative (exp2 and the f32 rounding of its argument
@@ -28,7 +29,7 @@ def attention(q, pk, pv, k, v, lens, scale, out_dtype, score=None):
         n = 0 if k is None else min(max(int(lens[b]), 0), cap)
         for h in range(Hq):
             hk = h // G
-            for t in range(T):
+            for t in (range(T) if only is None else only):
                 own = max(0, n - T + 1 + t)
                 ks, vs = [], []
                 if pk is not None:

@@ -1,9 +1,12 @@
 """mq_attn_prefix against a plain 64-bit attention: one token and many, ragged and empty caches,
 grouped heads, every width and type, layouts and strides, rows past a cache's length that hold
-NaN, offsets past 2^31, attention weights, in graphs and on other streams."""
+NaN, offsets past 2^31, attention weights, in graphs and on other streams. Every test runs on the library
+as it is and on a test build that sends calls of any size to the tensor-core kernel (which the library
+keeps for large ones) and row tiles of any prefix side by side."""
 import pytest
 import torch
 
+from quant_int8_quantized_gb300 import build as B
 from quant_int8_quantized_gb300 import mq
 from tests import _attn_ref as R
 from tests._gpu_util import Guarded, require_gpu
@@ -12,9 +15,14 @@ pytestmark = pytest.mark.gpu
 F16, BF16, F32 = torch.float16, torch.bfloat16, torch.float32
 
 
-@pytest.fixture(scope="module", autouse=True)
-def _gpu():
+@pytest.fixture(scope="module", autouse=True, params=["as it is", "tensor cores"])
+def _library(request):
     require_gpu()
+    own = mq.lib()
+    if request.param != "as it is":
+        mq._lib = mq._load(B.build_variant("attn_many", ["MQ_FEW_BYTES=0", "MQ_MANY_FROM=1", "MQ_LANES_FROM=0"]))
+    yield
+    mq._lib = own
 
 
 def _rand(shape, dtype, seed, std=1.0):
@@ -123,7 +131,7 @@ def test_an_empty_prefix_and_an_empty_cache():
 @pytest.mark.parametrize("B", [1, 9, 33, 70])
 def test_batches_on_one_prefix(B):
     """More rows than one tile of any kind; ragged lengths with one long sequence among short ones."""
-    lens = [(b * 37) % 90 for b in range(B)]
+    lens = [(n * 37) % 90 for n in range(B)]
     lens[B // 2] = 900
     _case(B, 1, 14, 2, 128, 777, 900, lens, BF16)
 
@@ -311,3 +319,55 @@ def test_binding_refuses():
             mq.mq_attn_prefix(**a)
         if status is not None:
             assert e.value.status == status
+
+
+@pytest.mark.parametrize("T,P,cap,lens,Hq,Hkv,dtype", [(1500, 700, 1600, [1600], 28, 4, BF16), (700, 0, 700, [700, 650, 699], 32, 8, F16),
+                                                      (3314, 1000, 3314, [3314], 28, 4, BF16)])
+def test_long_prompts(T, P, cap, lens, Hq, Hkv, dtype):
+    """Prompts that the tensor-core kernel takes; sampled queries against the reference, first and last rows of
+    tiles among them."""
+    B, D = len(lens), 128
+    q = _rand((B, T, Hq, D), dtype, 1, 1.5)
+    k, v = _rand((B, cap, Hkv, D), dtype, 2), _rand((B, cap, Hkv, D), dtype, 3)
+    pk, pv = (_rand((1, P, Hkv, D), dtype, 4 + i) for i in range(2)) if P else (None, None)
+    for b, n in enumerate(lens):
+        k[b, n:], v[b, n:] = float("nan"), float("nan")
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    out, lse = torch.empty((B, T, Hq, D), dtype=dtype, device="cuda"), torch.empty((B, T, Hq), device="cuda")
+    mq.mq_attn_prefix(q, mq.KV(pk, pv) if P else None, mq.KV(k, v), n, out, lse=lse)
+    torch.cuda.synchronize()
+    assert mq.mq_device_status() == mq.MQ_OK
+    assert not out[:, max(0, T - min(lens)):].isnan().any()
+    only = [0, 35, 36, 127, 128, 255, 256, T // 2, T - 50, T - 1]
+    want, bound = R.attention(q, pk[0] if P else None, pv[0] if P else None, k, v, lens, D ** -0.5, dtype, only=only)
+    _inside(out[:, only], want[0][:, only], bound[0][:, only], "out")
+    _inside(lse[:, only], want[1][:, only], bound[1][:, only], "lse")
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,P", [(64, 40, 8, 7000), (33, 28, 4, 13001), (300, 8, 2, 25000)])
+def test_long_prefixes_of_large_batches(B, Hq, Hkv, P):
+    """Prefixes that several row tiles read side by side, with ragged own caches; sampled sequences."""
+    D, cap, dtype = 128, 100, F16
+    q, pk, pv = _rand((B, 1, Hq, D), dtype, 1, 1.5), _rand((1, P, Hkv, D), dtype, 2), _rand((1, P, Hkv, D), dtype, 3)
+    k, v = _rand((B, cap, Hkv, D), dtype, 4), _rand((B, cap, Hkv, D), dtype, 5)
+    lens = [(37 * b) % 101 for b in range(B)]
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    out, lse = torch.empty((B, 1, Hq, D), device="cuda"), torch.empty((B, 1, Hq), device="cuda")
+    mq.mq_attn_prefix(q, mq.KV(pk, pv), mq.KV(k, v), n, out, lse=lse)
+    torch.cuda.synchronize()
+    assert mq.mq_device_status() == mq.MQ_OK
+    for b in [0, 1, B // 2, B - 1]:
+        want, bound = R.attention(q[b:b + 1], pk[0], pv[0], k[b:b + 1], v[b:b + 1], lens[b:b + 1], D ** -0.5, F32)
+        _inside(out[b:b + 1], want[0], bound[0], f"out of {b}")
+        _inside(lse[b:b + 1], want[1], bound[1], f"lse of {b}")
+
+
+def test_scales_of_any_sign():
+    for scale in (0.3, -0.2, 0.0):
+        for T in (1, 40):
+            q, k, v = _rand((1, T, 4, 64), F16, 1), _rand((1, 90, 2, 64), F16, 2), _rand((1, 90, 2, 64), F16, 3)
+            n = torch.tensor([77], dtype=torch.int32, device="cuda")
+            out = torch.empty((1, T, 4, 64), dtype=F16, device="cuda")
+            mq.mq_attn_prefix(q, None, mq.KV(k, v), n, out, scale=scale)
+            want, bound = R.attention(q, None, None, k, v, [77], scale, F16)
+            _inside(out, want[0], bound[0], f"scale {scale}")
