@@ -242,7 +242,7 @@ size_t up16(size_t n) { return (n + 15) & ~(size_t)15; }
 #endif
 constexpr long long kFewBytes = MQ_FEW_BYTES;
 #ifndef MQ_MANY_FROM
-#define MQ_MANY_FROM 33
+#define MQ_MANY_FROM 17
 #endif
 constexpr int kManyFrom = MQ_MANY_FROM;   // query rows per key head, at least, for the tensor-core kernel
 // Bytes of the prefix from which several row tiles of it are taken side by side, and how many at most: more of them
@@ -252,8 +252,8 @@ constexpr int kManyFrom = MQ_MANY_FROM;   // query rows per key head, at least, 
 #endif
 constexpr long long kLanesFrom = MQ_LANES_FROM;
 constexpr int kLanesMost = 8;
-constexpr int kBeside = 2;
-constexpr double kTileUs = 1.4, kDraw = 116e3;   // of a tile of two halves, measured; of an SM's eight warps with two stages in flight
+// A tile of two halves on one SM; what an SM's eight warps draw beside the other kernel. Both measured.
+constexpr double kTileUs = 1.4, kDraw = 80e3;
 
 // How a call is cut: the part of each kernel, and where the workspace holds what.
 struct Cut {
@@ -307,18 +307,16 @@ Cut cut_of(int B, int T, int Hq, int Hkv, int D, int prefix_keys, int own_cap, b
         const long long segs = all_segs(p);
         const long long most = (long long)prefix_segs(p) * ceil_div(p.prefix_keys, p.keys) +
                                (segs - prefix_segs(p)) * (ceil_div(p.lead_keys, p.keys) + ceil_div(p.own_cap, p.keys));
-        // beside the tensor-core kernel the blocks come and go on a part of the SMs: shorter runs, a shorter tail
-        const long long held = (long long)mq::num_sms() * (many ? 1 : c.prefix_many ? kBeside * kFewPerSm : kFewPerSm);
+        const long long held = (long long)mq::num_sms() * (many ? 1 : kFewPerSm);
         p.extra = !many ? kFewExtra : p.own ? kManyExtra : kManyExtra / 2;
         if (most * p.wide_cost + segs * p.extra > 0x7fffffffLL) c.fits = false;
         p.G = (int)(most < held ? most : held);
         if (many && p.prefix_keys > 0 && own_cap > 0) {
             // Beside it runs the kernel for few rows, on the SMs that this one leaves: so many that both end
-            // together if the caches are half full and each of its SMs draws kDraw bytes a us, but at most a third (they
-            // draw all that HBM gives).
+            // together if the caches are half full and each of its SMs draws kDraw bytes a us, but at most half.
             const double own_bytes = (double)B * Hkv * own_cap * D * 2.0, work = (double)most * kTileUs;   // us of one SM
             const int share = (int)(held / (1.0 + own_bytes / (work * kDraw)));
-            if (p.G > share) p.G = share > held - held / 3 ? share : (int)(held - held / 3 < p.G ? held - held / 3 : p.G);
+            if (p.G > share) p.G = share > held / 2 ? share : (int)(held / 2 < p.G ? held / 2 : p.G);
         }
         if (p.lanes > 1) p.G = p.G / p.lanes * p.lanes;
         const size_t places = segs > 0 ? (size_t)p.G + (size_t)segs : 0;
