@@ -19,7 +19,7 @@ struct FewArgs {
 
 constexpr int kFewRows = 16;      // query rows per segment
 constexpr int kFewKeys = 16;      // keys per tile
-constexpr int kFewExtra = 4;      // what beginning and ending a segment costs, in tiles
+constexpr int kFewExtra = 2;      // what beginning and ending a segment costs, in tiles
 constexpr int kFewPerSm = 8;      // blocks (of one warp) per SM
 int launch_few(const FewArgs& a, const mq_kv* prefix, const mq_kv* own, int D, int type, cudaStream_t stream);
 #ifdef MQ_TEST_INJECT
