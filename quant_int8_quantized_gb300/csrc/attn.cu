@@ -163,27 +163,102 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const JoinAr
     join_row<O, D, 16>(runs[0], runs[1], a.fin, a.lse2, row);
 }
 
-// The rows of the segments that one block of the first kernel began and another ended: grid x that block, y eight
-// rows of the segment. All other rows were finished by the block that held them.
+// The rows of the segments that one block of the first kernel began and another ended: grid x that block, y rows
+// of the segment. All other rows were finished by the block that held them.
 struct SplitArgs {
     Part part;
     const int4* split;
     Plan plan;
     Out fin;
 };
+// A warp takes eight rows: pieces of up to four blocks (there are seldom more) have a lane each, and the loads of four
+// rows' outputs are under way at once (a row a warp: 12 us at 3314 tokens of 28 heads of 128, the latency of four
+// rounds of warps; eight: 6).
+constexpr int kSplitRows = 8, kSplitWarps = 4;
 template <typename O, int D>
-__global__ void __launch_bounds__(256) attn_join_split_kernel(const SplitArgs a) {
+__global__ void __launch_bounds__(32 * kSplitWarps) attn_join_split_kernel(const SplitArgs a) {
+    static_assert(D == 64 || D == 128, "as attn_many");
+    constexpr int V = D / 32, kAtOnce = 4;
     mq_grid_release();
     mq_grid_wait();
     const int4 s = __ldca(a.split + blockIdx.x);
     if (s.x < 0) return;
     const int per_seq = own_tiles_of_rows(a.plan), b = a.plan.by_per_seq.of(s.z), rt = s.z - b * per_seq;
-    const int rows = rows_of(a.plan, a.plan.T * a.plan.group, rt);
-    const int in = blockIdx.y * 8 + (threadIdx.x >> 5);
-    if (in >= rows) return;
-    const int r = rt * a.plan.rows + in, t = a.plan.by_group.of(r);
-    join_row<O, D, 4>(run_of(a.part, s.x, make_int2(blockIdx.x, s.y), in), Run{}, a.fin, nullptr,
-                   ((long long)b * a.plan.T + t) * a.plan.Hq + s.w * a.plan.group + r - t * a.plan.group);
+    const int rows = rows_of(a.plan, a.plan.T * a.plan.group, rt), lane = threadIdx.x & 31;
+    const int in0 = (blockIdx.y * kSplitWarps + (threadIdx.x >> 5)) * kSplitRows;
+    if (in0 >= rows) return;
+    auto out_row = [&](int in) {
+        const int r = rt * a.plan.rows + in, t = a.plan.by_group.of(r);
+        return ((long long)b * a.plan.T + t) * a.plan.Hq + s.w * a.plan.group + r - t * a.plan.group;
+    };
+    const int2 blocks = make_int2(blockIdx.x, s.y);
+    const int count = run_of(a.part, s.x, blocks, in0).count;
+    if (count > 4) {
+        for (int in = in0; in < min(rows, in0 + kSplitRows); ++in)
+            join_row<O, D, 4>(run_of(a.part, s.x, blocks, in), Run{}, a.fin, nullptr, out_row(in));
+        return;
+    }
+    const int my_row = lane >> 2, my_piece = lane & 3;
+    const Run r = run_of(a.part, s.x, blocks, in0);
+    float2 ml = make_float2(-INFINITY, 0.0f);
+    if (my_piece < count && in0 + my_row < rows) ml = __ldca(a.part.p.ml + r.first + my_row + my_piece * r.stride);
+    float x[kAtOnce][4][V];
+    auto fetch = [&](int row0) {
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i)
+#pragma unroll
+            for (int p = 0; p < 4; ++p)
+                if (p < count && in0 + row0 + i < rows) {
+                    const float* o = a.part.p.o + (r.first + row0 + i + p * r.stride) * D + lane * V;
+                    if constexpr (V == 4) {
+                        const float4 v = __ldca(reinterpret_cast<const float4*>(o));
+                        x[i][p][0] = v.x, x[i][p][1] = v.y, x[i][p][2] = v.z, x[i][p][3] = v.w;
+                    } else {
+                        const float2 v = __ldca(reinterpret_cast<const float2*>(o));
+                        x[i][p][0] = v.x, x[i][p][1] = v.y;
+                    }
+                }
+    };
+    fetch(0);
+    float m = fmaxf(ml.x, __shfl_xor_sync(0xffffffffu, ml.x, 1));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    const float f = exp2f(ml.x - (m == -INFINITY ? 0.0f : m));
+    float l = ml.y == 0.0f ? 0.0f : ml.y * f;
+    l += __shfl_xor_sync(0xffffffffu, l, 1);
+    l += __shfl_xor_sync(0xffffffffu, l, 2);
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    if (a.fin.lse && my_piece == 0 && in0 + my_row < rows)
+        a.fin.lse[out_row(in0 + my_row)] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
+#pragma unroll
+    for (int row0 = 0; row0 < kSplitRows; row0 += kAtOnce) {
+        if (row0 > 0) fetch(row0);
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            const int in = row0 + i;
+            float y[V] = {};
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const float g = __shfl_sync(0xffffffffu, f, in * 4 + p);
+                if (p < count)
+#pragma unroll
+                    for (int e = 0; e < V; ++e) y[e] = fmaf(x[i][p][e], g, y[e]);
+            }
+            const float by = __shfl_sync(0xffffffffu, inv, in * 4);
+            if (in0 + in >= rows) continue;
+#pragma unroll
+            for (int e = 0; e < V; ++e) y[e] *= by;
+            const long long at = out_row(in0 + in) * 32 + lane;
+            if constexpr (sizeof(O) == 4) {
+                if constexpr (V == 4) reinterpret_cast<float4*>(a.fin.out)[at] = make_float4(y[0], y[1], y[2], y[3]);
+                else reinterpret_cast<float2*>(a.fin.out)[at] = make_float2(y[0], y[1]);
+            } else {
+                if constexpr (V == 4)
+                    reinterpret_cast<uint2*>(a.fin.out)[at] = make_uint2(mq_pack2<O>(y[0], y[1]), mq_pack2<O>(y[2], y[3]));
+                else
+                    reinterpret_cast<uint32_t*>(a.fin.out)[at] = mq_pack2<O>(y[0], y[1]);
+            }
+        }
+    }
 }
 
 // score_out = score + sum over the rows of 2^(raw - lse2), four keys a thread (one where the rows of raw do not
@@ -420,7 +495,8 @@ extern "C" int mq_attn_prefix(const void* q, long long q_stride, int B, int T, i
                 using O = decltype(o);
                 auto kern = D == 64 ? attn_join_split_kernel<O, 64> : attn_join_split_kernel<O, 128>;
                 if (!mq::allow_smem(reinterpret_cast<const void*>(kern), 0)) return (int)MQ_ERR_LAUNCH;
-                return mq::launch_pdl(kern, dim3(c.many.G, (most + 7) / 8), dim3(256), 0, stream, s);
+                return mq::launch_pdl(kern, dim3(c.many.G, (most + kSplitRows * kSplitWarps - 1) / (kSplitRows * kSplitWarps)),
+                                      dim3(32 * kSplitWarps), 0, stream, s);
             };
             return out_type == MQ_F32 ? join(float()) : out_type == MQ_F16 ? join(__half()) : join(__nv_bfloat16());
         }
