@@ -38,39 +38,48 @@ __device__ __forceinline__ Run run_of(const Part& p, int seg, int2 f, int in) {
     return Run{&p.p, ok ? (long long)place_of(p.plan, f.x, seg) * p.rows + in : 0, p.rows, ok ? f.y - f.x + 1 : 0};
 }
 
-// One warp adds up a row's pieces, those of run 0 and then those of run 1: their common maximum, then outputs
-// weighted and added in order. Lane i holds place, maximum and sum of piece i of 32; the outputs' loads do not
-// depend on one another, kAtOnce (a divisor of 32) are asked for at once.
-template <typename O, int D, int kAtOnce>
-__device__ __forceinline__ void join_row(const Run& r0, const Run& r1, const Out& fin, float* lse2, long long row) {
-    // lane l holds V floats at V (l + 32 k)
-    constexpr int V = D >= 128 ? 4 : 2, W = (D + 32 * V - 1) / (32 * V);
-    const int lane = threadIdx.x & 31, count = r0.count + r1.count;
-    float m = -INFINITY, l = 0.0f;
-    float acc[W][V] = {};
+// A lane's part of a row of D floats: V floats at V (lane + 32 k), k < W.
+template <int D>
+struct Lane {
+    static constexpr int V = D >= 128 ? 4 : 2, W = (D + 32 * V - 1) / (32 * V);
+};
+// Maximum, sum and (this lane's part of the) output of some pieces of a row.
+template <int D>
+struct Sum {
+    float m, l, o[Lane<D>::W][Lane<D>::V];
+};
+
+// One warp adds up pieces i0 .. i1 - 1 of a row, counted over run 0 and then run 1: their common maximum, then
+// outputs weighted and added in order. Lane i holds place, maximum and sum of piece i of 32; the outputs' loads do
+// not depend on one another, kAtOnce (a divisor of 32) are asked for at once.
+template <int D, int kAtOnce>
+__device__ __forceinline__ Sum<D> add_pieces(const Run& r0, const Run& r1, int i0, int i1) {
+    constexpr int V = Lane<D>::V, W = Lane<D>::W;
+    const int lane = threadIdx.x & 31;
+    Sum<D> s = {-INFINITY, 0.0f, {}};
 #pragma unroll 1
-    for (int i0 = 0; i0 < count; i0 += 32) {
-        const int n = min(32, count - i0), i = i0 + lane;
+    for (; i0 < i1; i0 += 32) {
+        const int n = min(32, i1 - i0), i = i0 + lane;
         const bool second = i >= r0.count;
         const Run& r = second ? r1 : r0;
         const long long at = r.first + (second ? i - r0.count : i) * r.stride;
         float2 ml = make_float2(-INFINITY, 0.0f);
         if (lane < n) ml = __ldca(r.p->ml + at);
         const unsigned long long from = reinterpret_cast<unsigned long long>(lane < n ? r.p->o + at * D : nullptr);
-        float now = fmaxf(m, ml.x);
+        float now = fmaxf(s.m, ml.x);
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, o));
         const float safe = now == -INFINITY ? 0.0f : now;
-        const float back = exp2f(m - safe), f = exp2f(ml.x - safe);
-        m = now;
+        const float back = exp2f(s.m - safe), f = exp2f(ml.x - safe);
+        s.m = now;
         float sum = ml.y == 0.0f ? 0.0f : ml.y * f;
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        l = l * back + sum;
+        s.l = s.l * back + sum;
 #pragma unroll
         for (int k = 0; k < W; ++k)
 #pragma unroll
-            for (int e = 0; e < V; ++e) acc[k][e] *= back;
+            for (int e = 0; e < V; ++e) s.o[k][e] *= back;
 #pragma unroll 1
         for (int j0 = 0; j0 < n; j0 += kAtOnce) {
             float x[kAtOnce][W][V], g[kAtOnce];
@@ -99,17 +108,25 @@ __device__ __forceinline__ void join_row(const Run& r0, const Run& r1, const Out
 #pragma unroll
                     for (int k = 0; k < W; ++k)
 #pragma unroll
-                        for (int e = 0; e < V; ++e) acc[k][e] = fmaf(x[j][k][e], g[j], acc[k][e]);
+                        for (int e = 0; e < V; ++e) s.o[k][e] = fmaf(x[j][k][e], g[j], s.o[k][e]);
         }
     }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;   // l == 0: no key seen (a NaN or infinite l stays one)
+    return s;
+}
+
+// The finished row out, by one warp.
+template <typename O, int D>
+__device__ __forceinline__ void write_row(const Sum<D>& s, const Out& fin, float* lse2, long long row) {
+    constexpr int V = Lane<D>::V, W = Lane<D>::W;
+    const int lane = threadIdx.x & 31;
+    const float inv = s.l == 0.0f ? 0.0f : 1.0f / s.l;   // l == 0: no key seen (a NaN or infinite l stays one)
 #pragma unroll
     for (int k = 0; k < W; ++k)
         if (V * (k * 32 + lane) < D) {
             const long long at = row * (D / V) + k * 32 + lane;
             float y[V];
 #pragma unroll
-            for (int e = 0; e < V; ++e) y[e] = acc[k][e] * inv;
+            for (int e = 0; e < V; ++e) y[e] = s.o[k][e] * inv;
             if constexpr (sizeof(O) == 4) {
                 if constexpr (V == 4) reinterpret_cast<float4*>(fin.out)[at] = make_float4(y[0], y[1], y[2], y[3]);
                 else reinterpret_cast<float2*>(fin.out)[at] = make_float2(y[0], y[1]);
@@ -121,19 +138,22 @@ __device__ __forceinline__ void join_row(const Run& r0, const Run& r1, const Out
             }
         }
     if (lane == 0) {
-        if (fin.lse) fin.lse[row] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
-        if (lse2) lse2[row] = l == 0.0f ? -INFINITY : m + log2f(l);
+        if (fin.lse) fin.lse[row] = s.l == 0.0f ? -INFINITY : s.m * kLn2 + logf(s.l);
+        if (lse2) lse2[row] = s.l == 0.0f ? -INFINITY : s.m + log2f(s.l);
     }
 }
 
-// Every query row, a warp each: its prefix segment's pieces, then its own segment's.
-constexpr int kJoinWarps = 1;   // few rows: as many SMs as there are; many: no matter
-template <typename O, int D>
+// Every query row, a block each: its prefix segment's pieces, then its own segment's, shared out to the block's warps
+// in order.
+template <typename O, int D, int kJoinWarps>
 __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const JoinArgs a) {
+    constexpr int V = Lane<D>::V, W = Lane<D>::W;
+    __shared__ float2 s_ml[kJoinWarps];
+    __shared__ float s_o[kJoinWarps][W * V * 32];
     mq_grid_release();
     mq_grid_wait();
-    const long long row = (long long)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);   // (b T + t) Hq + h
-    if (row >= (long long)a.B * a.T * a.Hq) return;
+    const long long row = blockIdx.x;   // (b T + t) Hq + h
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     const int h = (int)(row % a.Hq);
     const long long bt = row / a.Hq;
     const int t = (int)(bt % a.T), b = (int)(bt / a.T);
@@ -160,7 +180,40 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const JoinAr
     }
     if (a.prefix.rows > 0) runs[0] = run_of(a.prefix, seg0, f0, in0);
     if (a.own.rows > 0 && min(max(len, 0), a.own_cap) - a.T + 1 + last / a.group > 0) runs[1] = run_of(a.own, seg1, f1, in1);
-    join_row<O, D, 16>(runs[0], runs[1], a.fin, a.lse2, row);
+    const int count = runs[0].count + runs[1].count, each = ceil_div(count, kJoinWarps);
+    Sum<D> sum = add_pieces<D, kJoinWarps == 1 ? 16 : 8>(runs[0], runs[1], min(wid * each, count), min((wid + 1) * each, count));
+    if constexpr (kJoinWarps == 1) {
+        write_row<O, D>(sum, a.fin, a.lse2, row);
+        return;
+    }
+    if (lane == 0) s_ml[wid] = make_float2(sum.m, sum.l);
+    if (wid > 0)
+#pragma unroll
+        for (int k = 0; k < W; ++k)
+#pragma unroll
+            for (int e = 0; e < V; ++e) s_o[wid][(k * V + e) * 32 + lane] = sum.o[k][e];
+    __syncthreads();
+    if (wid > 0) return;
+    float m = sum.m, f[kJoinWarps];
+#pragma unroll
+    for (int w = 1; w < kJoinWarps; ++w) m = fmaxf(m, s_ml[w].x);
+    sum.l = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+        f[w] = exp2f(s_ml[w].x - (m == -INFINITY ? 0.0f : m));
+        sum.l += s_ml[w].y == 0.0f ? 0.0f : s_ml[w].y * f[w];
+    }
+    sum.m = m;
+#pragma unroll
+    for (int k = 0; k < W; ++k)
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            float x = sum.o[k][e] * f[0];
+#pragma unroll
+            for (int w = 1; w < kJoinWarps; ++w) x = fmaf(s_o[w][(k * V + e) * 32 + lane], f[w], x);
+            sum.o[k][e] = x;
+        }
+    write_row<O, D>(sum, a.fin, a.lse2, row);
 }
 
 // The rows of the segments that one block of the first kernel began and another ended: grid x that block, y rows
@@ -195,7 +248,7 @@ __global__ void __launch_bounds__(32 * kSplitWarps) attn_join_split_kernel(const
     const int count = run_of(a.part, s.x, blocks, in0).count;
     if (count > 4) {
         for (int in = in0; in < min(rows, in0 + kSplitRows); ++in)
-            join_row<O, D, 4>(run_of(a.part, s.x, blocks, in), Run{}, a.fin, nullptr, out_row(in));
+            write_row<O, D>(add_pieces<D, 4>(run_of(a.part, s.x, blocks, in), Run{}, 0, count), a.fin, nullptr, out_row(in));
         return;
     }
     const int my_row = lane >> 2, my_piece = lane & 3;
@@ -528,13 +581,18 @@ extern "C" int mq_attn_prefix(const void* q, long long q_stride, int B, int T, i
     j.seg0 = prefix_segs(c.few);
     j.fin = fin;
     j.lse2 = lse2;
-    const dim3 grid((unsigned)(((long long)B * T * Hq + kJoinWarps - 1) / kJoinWarps));
+    const dim3 grid((unsigned)((long long)B * T * Hq));
     auto join = [&](auto o) {
         using O = decltype(o);
-        auto kern = D == 64 ? attn_join_kernel<O, 64> : D == 96 ? attn_join_kernel<O, 96>
-                    : D == 128 ? attn_join_kernel<O, 128> : attn_join_kernel<O, 256>;
+        // few rows: eight warps each shorten the way through a row's pieces (16 sequences of 28 heads, 40 pieces a row: 6.6 to
+        // 4 us); many: they fill the GPU by themselves (64 sequences of 40 heads: 97 us in all, 110 with eight)
+        const bool wide = (long long)B * T * Hq <= 7LL * mq::num_sms();
+        auto kern = wide ? (D == 64 ? attn_join_kernel<O, 64, 8> : D == 96 ? attn_join_kernel<O, 96, 8>
+                            : D == 128 ? attn_join_kernel<O, 128, 8> : attn_join_kernel<O, 256, 8>)
+                         : (D == 64 ? attn_join_kernel<O, 64, 1> : D == 96 ? attn_join_kernel<O, 96, 1>
+                            : D == 128 ? attn_join_kernel<O, 128, 1> : attn_join_kernel<O, 256, 1>);
         if (!mq::allow_smem(reinterpret_cast<const void*>(kern), 0)) return (int)MQ_ERR_LAUNCH;
-        return mq::launch_pdl(kern, grid, dim3(32 * kJoinWarps), 0, stream, j);
+        return mq::launch_pdl(kern, grid, dim3(wide ? 256 : 32), 0, stream, j);
     };
     rc = out_type == MQ_F32 ? join(float()) : out_type == MQ_F16 ? join(__half()) : join(__nv_bfloat16());
     if (rc != MQ_OK || !scores) return rc;
