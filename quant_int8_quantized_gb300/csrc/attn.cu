@@ -584,9 +584,10 @@ extern "C" int mq_attn_prefix(const void* q, long long q_stride, int B, int T, i
     const dim3 grid((unsigned)((long long)B * T * Hq));
     auto join = [&](auto o) {
         using O = decltype(o);
-        // few rows: eight warps each shorten the way through a row's pieces (16 sequences of 28 heads, 40 pieces a row: 6.6 to
-        // 4 us); many: they fill the GPU by themselves (64 sequences of 40 heads: 97 us in all, 110 with eight)
-        const bool wide = (long long)B * T * Hq <= 7LL * mq::num_sms();
+        // few rows: eight warps each shorten the way through a row's pieces; many: they fill the GPU by themselves, and a row's
+        // few pieces leave most of eight warps idle. Whole call, one warp a row / eight: 400 rows 20.7 / 18.2 us, 560: 27.6 /
+        // 25.4, 640: 28.0 / 26.8, 840 of D 64: 14.5 / 17.9, 1024: 33.0 / 35.6, 1600: 24.7 / 31.3
+        const bool wide = (long long)B * T * Hq <= 4LL * mq::num_sms();
         auto kern = wide ? (D == 64 ? attn_join_kernel<O, 64, 8> : D == 96 ? attn_join_kernel<O, 96, 8>
                             : D == 128 ? attn_join_kernel<O, 128, 8> : attn_join_kernel<O, 256, 8>)
                          : (D == 64 ? attn_join_kernel<O, 64, 1> : D == 96 ? attn_join_kernel<O, 96, 1>
