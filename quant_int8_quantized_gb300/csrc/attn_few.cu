@@ -322,7 +322,13 @@ __global__ void __launch_bounds__(kThreads, 8)
     }
     if (!alive) {   // a copy never came: recorded; those still in flight must land before the block leaves
         if (lane == 0) atomicOr(&g_few_error, 1u);
-        for (int i = 0; i < stages && i < issued; ++i) tc::mbar_wait(&s_full[slot], phase, kWaitLimitNs);
+        for (int i = taken_tiles; i < issued; ++i) {
+            tc::mbar_wait(&s_full[slot], phase, kWaitLimitNs);
+            if (++slot == stages) {
+                slot = 0;
+                phase ^= 1;
+            }
+        }
     }
     // what follows counts on attn_many too: the last block, and with it this kernel, ends after it (the others make
     // room for more)
