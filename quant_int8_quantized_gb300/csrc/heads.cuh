@@ -8,6 +8,19 @@
 
 namespace mq {
 
+// n / d for 0 <= n < 2^31 by a multiplication: l = ceil(log2 d), mul = floor(2^(31 + l) / d) + 1 < 2^32 + 1,
+// n / d = n mul >> (31 + l), since mul d exceeds 2^(31 + l) by at most d <= 2^l.
+struct Div {
+    uint32_t mul;
+    int shift, d;
+    __device__ __forceinline__ int of(int n) const { return (int)(((unsigned long long)(uint32_t)n * mul) >> shift); }
+};
+inline Div div_by(int d) {
+    int l = 0;
+    while ((1LL << l) < d) ++l;
+    return Div{(uint32_t)(((1ULL << (31 + l)) / (uint32_t)d) + 1), 31 + l, d};
+}
+
 // All rows of a cache apart, strides multiples of 8: of the axes that have more than one
 // step, the one with the least stride must clear a head, each further one all that the ones
 // before it span.

@@ -2,14 +2,16 @@
 // last rows stay and, of the others, those with the largest score; kept rows keep their order.
 //
 // Scores become unsigned keys in the same order, and the key of the last row that is kept is found digit by
-// digit: a histogram of 8 bits a round, counted in shared memory. Long rows are shared out to a cluster of
-// blocks, which add their histograms up through distributed shared memory; each block reads its stretch of the
-// scores from memory once. Then every warp writes the kept rows of its own stretch in order, from the
-// counts of the stretches before it. Counts are integers: the result does not depend on the order of the
-// atomics.
-// Then rows, values and scores move in a second launch, which shares them out evenly: 16 bytes at a time, every kept
-// row read once and written once (blocks that move what they selected themselves took longer, 69 us for 65 at 256 heads of
-// up to 4096 rows: the machine waits for the SMs that hold two of them).
+// digit: a histogram of 8 bits a round, counted in shared memory, until few rows share the digits and are compared with one
+// another. Long rows are shared out to a cluster of blocks, which add their histograms up through distributed shared
+// memory; each block reads its stretch of the scores from memory once. Then every warp writes the kept rows' numbers and
+// scores of its own stretch in order, from the counts of the stretches before it. Counts are integers: the result does not
+// depend on the order of the atomics. Bound: the rounds' barriers (8 heads of 512, all of the call: 6.6 us) and, on long
+// rows, the passes over the keys (8 heads of 131072: 26 us of 47).
+// Then rows and values move in a second launch, which shares them out evenly: 16 bytes at a time, every kept row read
+// once and written once. Bound: HBM (256 heads of up to 4096 rows of 128, cut to 1024: 273 MB in 61 us with the selection's
+// 13, 5.7 TB/s without; blocks that move what they selected themselves take longer: the machine waits for the SMs that hold
+// two of them).
 
 #include "heads.cuh"
 
@@ -53,6 +55,8 @@ struct Move {
     int32_t* len_out;
     long long ss, sr, sh, ds, dr, dh;   // strides in 16-byte units
     int n, heads, cap, dst_cap, keep, chunks;
+    mq::Div by_blocks, by_row, by_chunks;   // blocks of a sequence, 16-byte units of a row (of all heads), of a head
+    int rows;                               // of a sequence that a block moves
 };
 
 // Selection for one head of one sequence by a cluster of C blocks.
@@ -65,8 +69,10 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Move a,
     __shared__ int s_hist[kWarps][256];
     __shared__ int s_tot[2][256], s_all[256];
     __shared__ int s_gt[kWarps], s_eq[kWarps], s_cnt[2];
+    constexpr int kLast = kSelThreads / 2;
+    __shared__ uint32_t s_cand[kLast], s_list[kLast];
     __shared__ uint32_t s_prefix;
-    __shared__ int s_need;
+    __shared__ int s_need, s_in, s_n;
     mq_grid_release();
     mq_grid_wait();
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
@@ -75,19 +81,26 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Move a,
     const int n = min(max(a.len[b], 0), a.cap), keep = a.keep, dst_cap = a.dst_cap;
     const float* sc = a.score + (long long)row * a.cap;
     int32_t* out = index + (long long)row * dst_cap;
+    float* so = a.score_out ? a.score_out + (long long)row * dst_cap : nullptr;
+    auto take = [&](int to, int from) {          // row `from` (-1: none) is now row `to`
+        out[to] = from;
+        if (so) so[to] = from < 0 ? 0.0f : mq_ld_dep(sc + from);
+    };
     const int step = C * kSelThreads, first = rank * kSelThreads + tid;
     if (n <= keep) {
-        for (int j = first; j < dst_cap; j += step) out[j] = j < n ? j : -1;
+        for (int j = first; j < dst_cap; j += step) take(j, j < n ? j : -1);
     } else {
         const int cand = n - recent;            // rows that compete for `best` places
         const int best = keep - recent;
-        for (int j = first; j < recent; j += step) out[best + j] = cand + j;
-        for (int j = keep + first; j < dst_cap; j += step) out[j] = -1;
+        for (int j = first; j < recent; j += step) take(best + j, cand + j);
+        for (int j = keep + first; j < dst_cap; j += step) take(j, -1);
         // (best is the same for all blocks of the cluster)
         if (best > 0) {
             const int per = ((cand + C - 1) / C + 31) / 32 * 32;
             const int base = min(rank * per, cand), mine = min(per, cand - base);
             const bool held = mine <= keys_held;
+            const unsigned lower = (1u << lane) - 1u;
+            if (tid == 0) s_n = 0;
             if (held) {
                 constexpr int kAtOnce = 8;
                 for (int j0 = tid; j0 < mine; j0 += kAtOnce * kSelThreads) {
@@ -161,6 +174,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Move a,
                             if (before < need && before + t[i] >= need) {
                                 s_prefix = prefix | (uint32_t)(255 - (lane * 8 + i)) << shift;
                                 s_need = need - before;
+                                s_in = t[i];
                                 break;
                             }
                             before += t[i];
@@ -170,6 +184,59 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Move a,
                 __syncthreads();
                 prefix = s_prefix;
                 need = s_need;
+                const int in = s_in;
+                // Few share the digits so far: each is compared with all the others, by some threads next to one another. That
+                // takes in^2 steps, another round a few for each key (256 heads of 4096: up to 256 15.5 us, up to 128 13.4;
+                // blocks of 65536 keys: up to 128 135 us, up to 512 122).
+                if (round == 3 || in > kLast || (in > 128 && in * in > 8 * per)) continue;
+                const uint32_t mask = 0xffffffffu << shift;
+                for (int j0 = wid * 32; j0 < mine; j0 += kSelThreads) {
+                    const int j = j0 + lane;
+                    const uint32_t k = j < mine ? key(j) : 0u;
+                    const bool one = j < mine && (k & mask) == prefix;
+                    const unsigned who = __ballot_sync(0xffffffffu, one);
+                    if (who == 0) continue;
+                    int at = 0;
+                    if (lane == 0) at = atomicAdd(&s_n, __popc(who));
+                    at = __shfl_sync(0xffffffffu, at, 0) + __popc(who & lower);
+                    if (one) s_cand[at] = k;
+                }
+                const uint32_t* list = s_cand;
+                if (C > 1) {
+                    cluster_sync();
+                    if (tid < in) {
+                        int r = 0, at = tid;
+                        for (int c = remote(&s_n, 0); at >= c && r < C - 1; c = remote(&s_n, r)) {
+                            at -= c;
+                            ++r;
+                        }
+                        s_list[tid] = (uint32_t)remote(reinterpret_cast<const int*>(s_cand) + at, r);
+                    }
+                    list = s_list;
+                }
+                __syncthreads();
+                int side = 32;
+                while (side * in > kSelThreads) side >>= 1;
+                const int me = tid / side;
+                const uint32_t k = me < in ? list[me] : 0u;
+                int gt = 0, eq = 0;
+                if (me < in)
+                    for (int i = tid & (side - 1); i < in; i += side) {
+                        gt += list[i] > k;
+                        eq += list[i] == k;
+                    }
+                for (int o = side / 2; o >= 1; o >>= 1) {
+                    gt += __shfl_xor_sync(0xffffffffu, gt, o);
+                    eq += __shfl_xor_sync(0xffffffffu, eq, o);
+                }
+                if (me < in && gt < need && gt + eq >= need) {   // (the same value from all that are equal)
+                    s_prefix = k;
+                    s_need = need - gt;
+                }
+                __syncthreads();
+                prefix = s_prefix;
+                need = s_need;
+                break;
             }
             // kept: key above `prefix`, and the first `need` rows of those equal to it
             const int stretch = ((mine + kWarps - 1) / kWarps + 31) / 32 * 32;
@@ -201,14 +268,13 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Move a,
                 g0 += __reduce_add_sync(0xffffffffu, bg);
                 e0 += __reduce_add_sync(0xffffffffu, be);
             }
-            const unsigned lower = (1u << lane) - 1u;
             for (int i = j0; i < j1; i += 32) {
                 const int j = i + lane;
                 const uint32_t k = j < j1 ? key(j) : 0u;
                 const bool isg = j < j1 && k > prefix, ise = j < j1 && k == prefix;
                 const unsigned bg = __ballot_sync(0xffffffffu, isg), be = __ballot_sync(0xffffffffu, ise);
                 const int g = g0 + __popc(bg & lower), e = e0 + __popc(be & lower);
-                if (isg || (ise && e < need)) out[g + min(e, need)] = base + j;
+                if (isg || (ise && e < need)) take(g + min(e, need), base + j);
                 g0 += __popc(bg);
                 e0 += __popc(be);
             }
@@ -217,54 +283,38 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Move a,
     }
 }
 
-// dst apart from src: 16 bytes of a kept row of k and of v at a time.
-constexpr int kMoveUnits = 2;
-__global__ void __launch_bounds__(256) evict_move_kernel(const Move a) {
+// dst apart from src: a block moves some whole rows of a sequence (all heads), 16 bytes of k and of v at a time.
+// (evict of 256 heads: two units a thread 64.6 us, four 67.5, one 62.7, one and 512 threads 63.5)
+constexpr int kMoveThreads = 256, kMoveUnits = 1;
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const Move a) {
     mq_grid_release();
     mq_grid_wait();
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-    if (i < a.n) {
-        const int L = min(max(a.len[i], 0), a.cap);
-        a.len_out[i] = min(L, a.keep);
-    }
-    const long long scores = (long long)a.n * a.heads * a.dst_cap;
-    if (a.score_out)
-        for (long long s = i; s < scores; s += (long long)gridDim.x * 256) {
-            const int at = a.index[s];
-            a.score_out[s] = at < 0 ? 0.0f : a.score[s / a.dst_cap * a.cap + at];
-        }
-    if (a.keep == 0) return;
-    // kAtOnce units a thread, a grid's width apart
-    constexpr int kAtOnce = kMoveUnits;
-    const long long units = (long long)a.n * a.keep * a.heads * a.chunks, width = (long long)gridDim.x * 256;
-    uint4 x[kAtOnce], y[kAtOnce];
-    long long to[kAtOnce];
+    const int b = a.by_blocks.of(blockIdx.x), j0 = (blockIdx.x - b * a.by_blocks.d) * a.rows;
+    const int kept = min(min(max(a.len[b], 0), a.cap), a.keep);   // the same after len_out is written over len
+    if (j0 == 0 && threadIdx.x == 0) a.len_out[b] = kept;
+    if (j0 >= kept) return;
+    const int units = min(a.rows, kept - j0) * a.by_row.d;
+    const int32_t* index = a.index + (long long)b * a.heads * a.dst_cap + j0;
+    for (int w0 = threadIdx.x; w0 < units; w0 += kMoveUnits * kMoveThreads) {
+        uint4 x[kMoveUnits], y[kMoveUnits];
+        long long to[kMoveUnits];
 #pragma unroll
-    for (int u = 0; u < kAtOnce; ++u) {
-        const long long w = i + u * width;
-        to[u] = -1;
-        if (w < units) {
-            long long r = w / a.chunks;
-            const int c = (int)(w - r * a.chunks);
-            const long long bj = r / a.heads;
-            const int h = (int)(r - bj * a.heads);
-            const long long b = bj / a.keep;
-            const int j = (int)(bj - b * a.keep);
-            const int at = a.index[(b * a.heads + h) * a.dst_cap + j];
-            if (at >= 0) {
-                const long long from = b * a.ss + at * a.sr + h * a.sh + c;
-                to[u] = b * a.ds + j * a.dr + h * a.dh + c;
-                x[u] = __ldcs(a.k + from);
-                y[u] = __ldcs(a.v + from);
+        for (int u = 0; u < kMoveUnits; ++u) {
+            const int w = w0 + u * kMoveThreads;
+            if (w >= units) continue;
+            const int j = a.by_row.of(w), r = w - j * a.by_row.d, h = a.by_chunks.of(r), c = r - h * a.by_chunks.d;
+            const long long from = b * a.ss + index[(long long)h * a.dst_cap + j] * a.sr + h * a.sh + c;
+            to[u] = b * a.ds + (j0 + j) * a.dr + h * a.dh + c;
+            x[u] = __ldcs(a.k + from);
+            y[u] = __ldcs(a.v + from);
+        }
+#pragma unroll
+        for (int u = 0; u < kMoveUnits; ++u)
+            if (w0 + u * kMoveThreads < units) {
+                __stcs(a.dk + to[u], x[u]);
+                __stcs(a.dv + to[u], y[u]);
             }
-        }
     }
-#pragma unroll
-    for (int u = 0; u < kAtOnce; ++u)
-        if (to[u] >= 0) {
-            __stcs(a.dk + to[u], x[u]);
-            __stcs(a.dv + to[u], y[u]);
-        }
 }
 
 // In place: rows only move down (index[j] >= j), so a block that takes one head's rows in order may
@@ -323,8 +373,9 @@ __global__ void __launch_bounds__(256) evict_len_kernel(const int32_t* len, int3
 
 int launch_select(const Move& a, int recent, int C, int held, int32_t* index, unsigned rows, size_t smem,
                   cudaStream_t stream) {
-    const bool brief = a.cap <= kBrief;
-    auto kern = brief ? evict_select_kernel<256> : evict_select_kernel<1024>;
+    // more rows than SMs: blocks of 512 threads, two of which an SM holds (of 1024 one: 256 heads 71 us, not 64)
+    const int threads = a.cap <= kBrief ? 256 : rows * C > (unsigned)mq::num_sms() ? 512 : 1024;
+    auto kern = threads == 256 ? evict_select_kernel<256> : threads == 512 ? evict_select_kernel<512> : evict_select_kernel<1024>;
     if (!mq::allow_smem(reinterpret_cast<const void*>(kern), kMaxKeys * (int)sizeof(uint32_t))) return MQ_ERR_LAUNCH;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -335,7 +386,7 @@ int launch_select(const Move& a, int recent, int C, int held, int32_t* index, un
     attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(rows * C);
-    cfg.blockDim = dim3(brief ? 256 : 1024);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = attr;
@@ -367,7 +418,7 @@ extern "C" int mq_kv_evict(const mq_kv* src, const int32_t* len, const float* sc
         !mq::aligned16(index))
         return MQ_ERR_ALIGN;
     const long long rows = (long long)src->n * src->heads;
-    if (rows > 0x7fffffffLL) return MQ_ERR_SHAPE;
+    if (rows > 0x7fffffffLL || (long long)src->heads * (src->dim / 8) > 0x3fffffffLL) return MQ_ERR_SHAPE;
     bool in_place = false;
     if (src->cap > 0 && dst->cap > 0) {
         in_place = src->k == dst->k && src->v == dst->v && src->cap == dst->cap && src->seq_stride == dst->seq_stride &&
@@ -405,8 +456,7 @@ extern "C" int mq_kv_evict(const mq_kv* src, const int32_t* len, const float* sc
     a.keep = keep;
     a.chunks = src->dim / 8;
     if (dst->cap > 0) {
-        // Scores that move in place, or beside rows that do, go through the ordered kernel.
-        const bool ordered_score = score_out && (in_place || score_out == score);
+        const bool ordered_score = score_out && score_out == score;   // they move down as rows in place do
         // a block for each 4096 scores of a head (measured: with fewer the rounds over them take longer, with more their
         // meetings), as long as the GPU holds them all at once
         int C = 1;
@@ -414,20 +464,24 @@ extern "C" int mq_kv_evict(const mq_kv* src, const int32_t* len, const float* sc
         const int per = (src->cap + C - 1) / C + 32;
         const int held = per < kMaxKeys ? per : kMaxKeys;
         const size_t smem = (size_t)held * sizeof(uint32_t);
+        if (ordered_score) a.score_out = nullptr;
         rc = launch_select(a, recent, C, held, index, (unsigned)rows, smem, stream);
         if (rc != MQ_OK) return rc;
+        a.score_out = score_out;
         if (!in_place) {
-            if (ordered_score) a.score_out = nullptr;
-            const long long units = (long long)a.n * keep * a.heads * a.chunks;
-            const long long each = (units + kMoveUnits - 1) / kMoveUnits;
-            const long long blocks = ((each > a.n ? each : a.n) + 255) / 256;
+            const int row = a.heads * a.chunks;
+            const long long full = keep < src->cap ? keep : src->cap;
+            a.rows = kMoveUnits * kMoveThreads / row > 0 ? kMoveUnits * kMoveThreads / row : 1;
+            const long long each = full > 0 ? (full + a.rows - 1) / a.rows : 1, blocks = each * a.n;   // (one for len_out)
             if (blocks > 0x7fffffffLL) return MQ_ERR_SHAPE;
-            rc = mq::launch_pdl(evict_move_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, a);
+            a.by_blocks = mq::div_by((int)each);
+            a.by_row = mq::div_by(row);
+            a.by_chunks = mq::div_by(a.chunks);
+            rc = mq::launch_pdl(evict_move_kernel, dim3((unsigned)blocks), dim3(kMoveThreads), 0, stream, a);
             if (rc != MQ_OK) return rc;
-            a.score_out = score_out;
         }
         if (in_place || ordered_score) {
-            const int what0 = in_place ? 0 : 2, count = (score_out ? 3 : 2) - what0;
+            const int what0 = in_place ? 0 : 2, count = (ordered_score ? 3 : 2) - what0;
             rc = mq::launch_pdl(evict_in_place_kernel, dim3((unsigned)rows, count), dim3(kInThreads), 0, stream, a,
                                 what0);
             if (rc != MQ_OK) return rc;

@@ -302,3 +302,26 @@ def test_evict_refuses():
                 dict(index=index[:1]), dict(src="cache"), dict(score=score[:1])):
         with pytest.raises((TypeError, ValueError)):
             mq.mq_kv_evict(**(ok | bad))
+
+
+@pytest.mark.parametrize("cap", [1500, 3000, 9000])
+@pytest.mark.parametrize("shared", [1, 2, 127, 128, 129, 300, 511, 512, 513, 1100])
+@pytest.mark.parametrize("digits", [8, 16, 24])
+def test_evict_scores_that_share_digits(cap, shared, digits):
+    """`shared` rows whose scores agree in their first `digits` bits, of which some are kept, among rows far above
+    and far below them: one block of 256 and of 1024 threads, and a cluster."""
+    g = torch.Generator().manual_seed(shared * 31 + digits)
+    above, keep = 100, 100 + (shared + 1) // 2
+    low = torch.randint(0, 1 << min(32 - digits, 20), (shared,), generator=g)
+    if shared > 4:
+        low[::5] = low[0]                               # ties across the border too
+    bits = torch.randint(1, 1000, (cap,), generator=g)                       # next to nothing
+    place = torch.randperm(cap, generator=g)
+    bits[place[:shared]] = 0x3F000000 + low
+    bits[place[shared:shared + above]] = 0x41000000 + torch.randint(0, 5000, (above,), generator=g)
+    score = bits.to(torch.int32).view(torch.float32).view(1, 1, cap)
+    src, dst = mq.KV(*(_rand((1, cap, 1, 8), i).half() for i in range(2))), mq.KV.empty(1, keep, 1, 8)
+    n = torch.tensor([cap], dtype=torch.int32, device="cuda")
+    index = torch.empty((1, 1, keep), dtype=torch.int32, device="cuda")
+    mq.mq_kv_evict(src, n, score.cuda(), keep, 0, dst, torch.empty_like(n), None, index)
+    assert index.view(-1).tolist() == R.evict(score.view(-1).tolist(), cap, keep, 0)
