@@ -9,9 +9,10 @@
 // descriptor of the transposed kind).
 //
 // The halves take turns: while one half's threads work on their tile, the tensor cores do the other half's
-// products. A segment of at most 128 rows gives both halves the same rows and every other tile. The maximum that the exponents are taken against is renewed only when a row passes it by 2^8
-// (the sums are the same in any scale, and 2^8 does not bring a 16-bit value near its end), so O in
-// tensor memory is hardly ever scaled again.
+// products (a tile of both halves and of D = 128 in 1.4 us, of which the products alone are 1.3; without the turns some
+// blocks stay in step and take up to 2.1). A segment of at most 128 rows gives both halves the same rows and every other
+// tile. The maximum that the exponents are taken against is renewed only when a row passes it by 2^8 (the sums are the
+// same in any scale, and 2^8 does not bring a 16-bit value near its end), so O in tensor memory is hardly ever scaled again.
 //
 // 384 threads, one block per SM: warps 0-3 and 4-7 the rows of the halves, warp 8 copies (TMA), warps 9 and 10 a
 // half's products each (one warp for both issued too slowly), warp 11 walks the block's run and hands its pieces
@@ -76,6 +77,7 @@ struct Bars {
     uint64_t full[8], empty[8];
     uint64_t q_full, q_free;
     uint64_t s_full[2], p_ready[2], pv_done[2];
+    uint64_t order[2];                     // the other half has issued its tile's products
     uint64_t twin_full[4], twin_free[4];   // per quarter: half 1's rows of a twin segment are there / were taken
     uint64_t piece_full[kPieces], piece_free[kPieces];
     uint64_t drained[2];
@@ -182,6 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::mbar_init(&bars.p_ready[h], 4);    // a warp each
             tc::mbar_init(&bars.pv_done[h], 1);
             tc::mbar_init(&bars.drained[h], 1);
+            tc::mbar_init(&bars.order[h], 1);
         }
         for (int i = 0; i < 4; ++i) {
             tc::mbar_init(&bars.twin_full[i], 1);
@@ -482,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t q_low = uniform(desc_low(tc::smem_u32(s_q), 16));
             const uint32_t k_low = uniform(desc_low(ring, 16)), v_low = uniform(desc_low(ring, C::kChunkBytes));
             int slot = 0;                        // ring slot of the piece's first K tile, and the phase there
-            uint32_t phase = 0, q_phase = 0, p_phase = 0;
+            uint32_t phase = 0, q_phase = 0, p_phase = 0, turn = h ^ 1;
             auto step_slots = [&](int n) {       // n < kRing slots on
                 slot += n;
                 if (slot >= C::kRing) {
@@ -538,6 +541,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     step_slots(g.twin ? 3 : 1);  // the half's next K
                     const bool more = t + step < g.n;
                     if (more && !(alive = wwait(bars, &bars.full[slot], phase))) break;
+                    // The halves issue by turns, a tile's PV and the next one's QK together: issued side by side they
+                    // would end side by side, and both halves' threads would wait for them at once, tile after tile.
+                    if (!(alive = wwait(bars, &bars.order[h], turn))) break;
+                    turn ^= 1;
                     if (!(alive = wwait(bars, &bars.p_ready[h], p_phase))) break;
                     p_phase ^= 1;
                     tc::tc_fence_after();
@@ -550,11 +557,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tc::mma_commit(&bars.empty[v_slot]);
                         if (g.twin) tc::mma_commit(&bars.empty[v_slot]);
                         if (more) qk(q_at, g.twin, t + 2 * step >= g.n);
+                        tc::mbar_arrive(&bars.order[h ^ 1]);
                     }
                     __syncwarp();
                     first = false;
                 }
                 if (!alive) break;
+                if (g.twin && h == 1 && (g.n & 1)) {   // half 0 has one tile more
+                    if (!(alive = wwait(bars, &bars.order[1], turn))) break;
+                    turn ^= 1;
+                    if (lane == 0) tc::mbar_arrive(&bars.order[0]);
+                }
                 // t stands at the half's first tile past the piece, `slot` at that tile's K: back to the piece's end
                 for (int n = 2 * (t - g.n); n > 0; --n)
                     if (--slot < 0) {
