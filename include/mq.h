@@ -4,7 +4,8 @@
  * The library computes the hot path of GGML-style quantized LLM inference:
  * activations quantized to int8 blocks of 32 (a "q8 plane"), produced either
  * standalone or fused into RMSNorm / SwiGLU, multiplied against q4_K / q6_K
- * weight super-blocks (prefill GEMM, decode GEMV).
+ * weight super-blocks (prefill GEMM, decode GEMV). Further down: what lies between a
+ * layer's attn_q|k|v and attn_o products (head norms, rotation, caches, attention).
  *
  * Sources (engineering write-ups of the "minfer" inference engine):
  *   [r60]  "64 · r60 — the coronation: flipping the verified gate set to default-on"
@@ -424,8 +425,10 @@ int mq_qk_norm_rope(const mq_qkv* x, void* q_out, const mq_kv* cache, const int3
  * the caches' type for the product with the values (2^-12 or 2^-9 relative, as the output's own
  * rounding is), sums in f32. An MQ_F32 output carries that rounding. Deterministic.
  * D: 64, 96, 128 or 256; Hq a multiple of Hkv. scale must be finite. ws: caller-owned device
- * memory of at least mq_attn_ws_bytes(...) bytes, 16-byte aligned, nothing kept in it between
- * calls; calls that run at the same time need one each. B == 0 or T == 0 is a no-op.
+ * memory of at least mq_attn_ws_bytes(this call's sizes) bytes (MQ_ERR_SCRATCH otherwise; the sizes choose
+ * the kernels, so a smaller call may need more), 16-byte aligned, nothing kept in it between
+ * calls; calls that run at the same time need one each. B == 0 or T == 0 is a no-op. A call is one to
+ * four launches, programmatic dependent ones as the producers; waits are bounded (mq_device_status).
  */
 size_t mq_attn_ws_bytes(int B, int T, int Hq, int Hkv, int D, int prefix_cap, int own_cap, int scores);
 int mq_attn_prefix(const void* q, long long q_stride, int B, int T, int Hq, const mq_kv* prefix, const mq_kv* own,
@@ -446,7 +449,7 @@ int mq_attn_prefix(const void* q, long long q_stride, int B, int T, int Hq, cons
  *   exactly src (same k, v, strides and cap: the rows move down in place); k or v ranges that
  *   overlap otherwise give MQ_ERR_SHAPE, as does score_out overlapping score unless it is score and
  *   the caps are equal. len_out may be len. Rows of dst past the kept ones are not written.
- * 0 <= recent <= keep, else MQ_ERR_SHAPE. n == 0 is a no-op.
+ * 0 <= recent <= keep, else MQ_ERR_SHAPE. n == 0 is a no-op. Programmatic dependent launches.
  */
 int mq_kv_evict(const mq_kv* src, const int32_t* len, const float* score, int keep, int recent, const mq_kv* dst,
                 int32_t* len_out, float* score_out, int32_t* index, cudaStream_t stream);

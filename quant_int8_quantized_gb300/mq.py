@@ -467,7 +467,8 @@ def mq_attn_ws_bytes(B: int, T: int, Hq: int, Hkv: int, D: int, prefix_cap: int,
 
 def attn_workspace(B: int, T: int, Hq: int, Hkv: int, D: int, prefix_cap: int, own_cap: int, scores: bool = False,
                    device="cuda") -> torch.Tensor:
-    """A workspace for mq_attn_prefix calls of up to these sizes on one stream."""
+    """A workspace for mq_attn_prefix calls of these sizes on one stream. (Sizes choose the kernels, so a
+    smaller call may need more; one that is too small is refused.)"""
     return torch.empty((max(16, mq_attn_ws_bytes(B, T, Hq, Hkv, D, prefix_cap, own_cap, scores)),), dtype=torch.uint8,
                        device=device)
 
