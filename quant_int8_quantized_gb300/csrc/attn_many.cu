@@ -266,11 +266,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int i = 1; i < 32; ++i) mx4[k] = fmaxf(mx4[k], __uint_as_float(s[k][i]));
                 }
                 const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * a.scale_log2;
-                const bool grew = mx > m + kGrow;          // true for the first key that a row sees
+                // (true for the first key that a row sees; lanes past the rows hold anything)
+                const bool grew = lane < n_rows && mx > m + kGrow;
                 if (j == j0) {
                     m = mx;
                 } else if (__any_sync(0xffffffffu, grew)) {
-                    const float now = fmaxf(m, mx);
+                    const float now = grew ? mx : m;   // a row's own matter: what its neighbours do must not show in it
                     const float f = now == -INFINITY ? 1.0f : exp2_fast(m - now);
                     m = now;
                     l *= f;

@@ -371,3 +371,24 @@ def test_scales_of_any_sign():
             mq.mq_attn_prefix(q, None, mq.KV(k, v), n, out, scale=scale)
             want, bound = R.attention(q, None, None, k, v, [77], scale, F16)
             _inside(out, want[0], bound[0], f"scale {scale}")
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(28, 4), (6, 2), (5, 1)])
+def test_results_do_not_depend_on_what_ran_before(Hq, Hkv):
+    """Row tiles that are not full (groups that do not divide 256): what other calls left in their places must not
+    show in the rows beside them, not in the last bit either."""
+    T, D, P, cap = 700, 128, 300, 700
+    q, k, v = _rand((1, T, Hq, D), BF16, 1), _rand((1, cap, Hkv, D), BF16, 2), _rand((1, cap, Hkv, D), BF16, 3)
+    pre = mq.KV(_rand((1, P, Hkv, D), BF16, 4), _rand((1, P, Hkv, D), BF16, 5))
+    n = torch.tensor([T], dtype=torch.int32, device="cuda")
+    own, results = mq.KV(k, v), []
+    for std in (0.0, 1.0, 30.0, 300.0):
+        full = _rand((1, 2048, 8, D), BF16, 6, std)          # eight heads to a key head: full tiles
+        other = mq.KV(_rand((1, 2048, 1, D), BF16, 7), _rand((1, 2048, 1, D), BF16, 8))
+        mq.mq_attn_prefix(full, None, other, torch.full((1,), 2048, dtype=torch.int32, device="cuda"),
+                          torch.empty_like(full))
+        out, lse = torch.empty((1, T, Hq, D), device="cuda"), torch.empty((1, T, Hq), device="cuda")
+        mq.mq_attn_prefix(q, pre, own, n, out, lse=lse)
+        results.append((out, lse))
+    for out, lse in results[1:]:
+        assert torch.equal(out, results[0][0]) and torch.equal(lse, results[0][1])
