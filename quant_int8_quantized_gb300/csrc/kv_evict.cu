@@ -28,23 +28,6 @@ __device__ __forceinline__ uint32_t order_key(float f) {
     return (b & 0x80000000u) ? ~b : b | 0x80000000u;
 }
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// A shared-memory word of block `rank` of the cluster, at this block's address p.
-__device__ __forceinline__ int remote(const int* p, uint32_t rank) {
-    uint32_t at;
-    int v;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at));
-    return v;
-}
-
 struct Move {
     const uint4 *k, *v;
     uint4 *dk, *dv;
@@ -76,7 +59,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Move a,
     mq_grid_release();
     mq_grid_wait();
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-    const int rank = C > 1 ? (int)cluster_rank() : 0, row = blockIdx.x / C;
+    const int rank = C > 1 ? (int)mq_cluster_rank() : 0, row = blockIdx.x / C;
     const int b = row / a.heads;
     const int n = min(max(a.len[b], 0), a.cap), keep = a.keep, dst_cap = a.dst_cap;
     const float* sc = a.score + (long long)row * a.cap;
@@ -146,11 +129,11 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Move a,
                     else s_all[tid] = t;
                 }
                 if (C > 1) {
-                    cluster_sync();
+                    mq_cluster_sync();
                     if (tid < 256) {
                         int t[kMaxCluster];
 #pragma unroll
-                        for (int r = 0; r < kMaxCluster; ++r) t[r] = r < C ? remote(tot + tid, r) : 0;
+                        for (int r = 0; r < kMaxCluster; ++r) t[r] = r < C ? mq_remote(tot + tid, r) : 0;
 #pragma unroll
                         for (int r = 1; r < kMaxCluster; ++r) t[0] += t[r];
                         s_all[tid] = t[0];
@@ -203,14 +186,14 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Move a,
                 }
                 const uint32_t* list = s_cand;
                 if (C > 1) {
-                    cluster_sync();
+                    mq_cluster_sync();
                     if (tid < in) {
                         int r = 0, at = tid;
-                        for (int c = remote(&s_n, 0); at >= c && r < C - 1; c = remote(&s_n, r)) {
+                        for (int c = mq_remote(&s_n, 0); at >= c && r < C - 1; c = mq_remote(&s_n, r)) {
                             at -= c;
                             ++r;
                         }
-                        s_list[tid] = (uint32_t)remote(reinterpret_cast<const int*>(s_cand) + at, r);
+                        s_list[tid] = (uint32_t)mq_remote(reinterpret_cast<const int*>(s_cand) + at, r);
                     }
                     list = s_list;
                 }
@@ -263,8 +246,8 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Move a,
                     s_cnt[0] = ag;
                     s_cnt[1] = ae;
                 }
-                cluster_sync();
-                const int bg = lane < rank ? remote(&s_cnt[0], lane) : 0, be = lane < rank ? remote(&s_cnt[1], lane) : 0;
+                mq_cluster_sync();
+                const int bg = lane < rank ? mq_remote(&s_cnt[0], lane) : 0, be = lane < rank ? mq_remote(&s_cnt[1], lane) : 0;
                 g0 += __reduce_add_sync(0xffffffffu, bg);
                 e0 += __reduce_add_sync(0xffffffffu, be);
             }
@@ -278,7 +261,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Move a,
                 g0 += __popc(bg);
                 e0 += __popc(be);
             }
-            if (C > 1) cluster_sync();           // the others are done with this block's counts
+            if (C > 1) mq_cluster_sync();           // the others are done with this block's counts
         }
     }
 }
@@ -377,22 +360,7 @@ int launch_select(const Move& a, int recent, int C, int held, int32_t* index, un
     const int threads = a.cap <= kBrief ? 256 : rows * C > (unsigned)mq::num_sms() ? 512 : 1024;
     auto kern = threads == 256 ? evict_select_kernel<256> : threads == 512 ? evict_select_kernel<512> : evict_select_kernel<1024>;
     if (!mq::allow_smem(reinterpret_cast<const void*>(kern), kMaxKeys * (int)sizeof(uint32_t))) return MQ_ERR_LAUNCH;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = C;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(rows * C);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = C > 1 ? 2 : 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, recent, C, held, index);
-    return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? MQ_OK : MQ_ERR_LAUNCH;
+    return mq::launch_cluster(kern, dim3(C), dim3(rows * C), dim3(threads), smem, stream, a, recent, C, held, index);
 }
 
 bool overlap(const void* a, size_t an, const void* b, size_t bn) {

@@ -392,3 +392,12 @@ def test_results_do_not_depend_on_what_ran_before(Hq, Hkv):
         results.append((out, lse))
     for out, lse in results[1:]:
         assert torch.equal(out, results[0][0]) and torch.equal(lse, results[0][1])
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,cap,lens", [(17, 3, 3, 200, [200, 5]), (33, 14, 2, 301, [300, 33]), (150, 7, 1, 404, [404, 20]),
+                                                (400, 16, 2, 640, [555, 0]), (5, 28, 4, 1000, [777, 1000])])
+def test_score_of_many_queries(T, Hq, Hkv, cap, lens):
+    """Weights of several queries' rows added up by one and by several blocks, lengths below and above T, caps that do
+    and do not leave every row's products on 16 bytes."""
+    _case(2, T, Hq, Hkv, 64, 40, cap, lens, F16, scores=True)
+    _case(2, T, Hq, Hkv, 128, 0, cap, lens, BF16, scores=True)
