@@ -8,6 +8,7 @@ library has not been built, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -123,6 +124,17 @@ def _stream(stream):
     if stream is None:
         return _current_stream()
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+
+
+def _on(stream, device):
+    """Allocations made inside belong to `stream` (None: the current one). The caching allocator hands what is freed
+    to the same stream's next allocation, so memory that lives no longer than a call has to come from the stream that the
+    call runs on."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=device)
+    return torch.cuda.stream(stream)
 
 
 def _current_stream():
@@ -478,7 +490,8 @@ def mq_attn_prefix(q: torch.Tensor, prefix, own, own_len, out: torch.Tensor, sca
     """Attention of q [B, T, Hq, D] over a shared prefix (KV of one sequence, or None) and each
     sequence's own cache (KV of B sequences, or None) of own_len rows (include/mq.h). out: [B, T,
     Hq, D] in q's type or f32; lse: f32 [B, T, Hq]; score, score_out: f32 [B, Hkv, own.cap];
-    scale: 1 / sqrt(D) if None; ws: attn_workspace(...), allocated for this call if None."""
+    scale: 1 / sqrt(D) if None; ws: attn_workspace(...), allocated on the call's stream for this call
+    if None."""
     any_kv = own if own is not None else prefix
     if any_kv is None:
         raise ValueError("a prefix, an own cache or both are needed")
@@ -522,8 +535,9 @@ def mq_attn_prefix(q: torch.Tensor, prefix, own, own_len, out: torch.Tensor, sca
             raise ValueError("score_out must be [B, Hkv, own.cap]")
         score_out_ptr = score_out.data_ptr()
     if ws is None:
-        ws = attn_workspace(B, T, Hq, any_kv.heads, D, prefix.cap if prefix is not None else 0,
-                            own.cap if own is not None else 0, score is not None, q.device)
+        with _on(stream, q.device):
+            ws = attn_workspace(B, T, Hq, any_kv.heads, D, prefix.cap if prefix is not None else 0,
+                                own.cap if own is not None else 0, score is not None, q.device)
     _check((_lib or lib()).mq_attn_prefix(q.data_ptr(), row, B, T, Hq, prefix._ref if prefix is not None else None,
                                           own_ref, len_ptr, D ** -0.5 if scale is None else scale, out.data_ptr(),
                                           _TYPES[out_type], lse_ptr, score_ptr, score_out_ptr,
