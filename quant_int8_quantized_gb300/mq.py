@@ -128,8 +128,8 @@ def _stream(stream):
 
 def _on(stream, device):
     """Allocations made inside belong to `stream` (None: the current one). The caching allocator hands what is freed
-    to the same stream's next allocation, so memory that lives no longer than a call has to come from the stream that the
-    call runs on."""
+    to the same stream's next allocation, so memory that a call allocates for itself has to come from the stream that it
+    runs on."""
     if stream is None:
         return contextlib.nullcontext()
     if not isinstance(stream, torch.cuda.Stream):
@@ -234,10 +234,12 @@ def mq_q6k_packed_row_bytes(K: int) -> int:
 
 
 def mq_prepack_q6k(w: torch.Tensor, N: int, K: int, out: torch.Tensor = None, stream=None) -> torch.Tensor:
-    """Raw q6_K rows [N, K/256*210] (uint8) -> the prepacked layout [N, K/256*224] the GEMM reads."""
+    """Raw q6_K rows [N, K/256*210] (uint8) -> the prepacked layout [N, K/256*224] the GEMM reads. out:
+    allocated on the call's stream if None."""
     _dev_tensor(w, torch.uint8, "w")
     if out is None:
-        out = torch.empty((N, mq_q6k_packed_row_bytes(K)), dtype=torch.uint8, device=w.device)
+        with _on(stream, w.device):
+            out = torch.empty((N, mq_q6k_packed_row_bytes(K)), dtype=torch.uint8, device=w.device)
     _dev_tensor(out, torch.uint8, "out")
     _check(lib().mq_prepack_q6k(_ptr(w), int(N), int(K), _ptr(out), _stream(stream)), "mq_prepack_q6k")
     return out

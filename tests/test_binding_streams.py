@@ -75,3 +75,12 @@ def test_a_workspace_of_the_caller_is_taken_as_it_is(notes):
     watch()
     mq.mq_attn_prefix(q, None, own, length, out, ws=ws, stream=Stream(5))
     assert n.calls == [("mq_attn_prefix", 5)] and n.made == []
+
+
+@pytest.mark.parametrize("stream,handle", [(Stream(77), 77), (None, 0)])
+def test_prepacked_rows(notes, stream, handle):
+    n, watch = notes
+    w = torch.empty((64, 210), dtype=torch.uint8, device="cuda")
+    watch()
+    mq.mq_prepack_q6k(w, 64, 256, stream=stream)
+    assert n.calls == [("mq_prepack_q6k", handle)] and n.made == [handle] and n.current == 0
