@@ -49,6 +49,11 @@ constexpr int kHalf = kManyHalf;
 constexpr int kKeys = kManyKeys;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kGrow = 8.0f;           // powers of two by which a row may pass its maximum
+// Maxima from which a row's products are scaled and rounded, as the maximum itself was, before it is taken off. Below, one
+// fused step does both, and what it keeps of a product past the maximum's last place is 2^-5 at most; from 2^28 that would be
+// powers of two by which the weights leave their type. (-infinity: no key seen yet.)
+constexpr float kLarge = 1048576.0f;
+__device__ __forceinline__ bool is_large(float m) { return fabsf(m) >= kLarge && m != -INFINITY; }
 
 template <int D>
 struct Cfg {
@@ -225,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint8_t* stage = s_stage + wid * C::kStageBytes;
         auto unit_of = [&](int r, int u) { return reinterpret_cast<uint4*>(stage + r * 128 + ((u ^ (r & 7)) << 4)); };
         const int my_unit = lane & 7, my_row = lane >> 3;         // on the way out 8 lanes take a row's 128 bytes
-        uint32_t s_phase = 0, pv_phase = 0, twin_phase = 0;
+        uint32_t phase = 0, twin_phase = 0;   // phase: of the next tile's s_full; its pv_done follows in step
         bool alive = true;
         Reader reader;
         Piece g;
@@ -235,13 +240,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int n_rows = g.rows - half0 - quarter * 32;     // rows of the warp that count
             const int own_sees = g.prefix ? g.see : g.see + q_in;
             float m = -INFINITY, l = 0.0f;                    // base 2, scaled
+            float limit = -INFINITY;                          // of a tile's maximum that needs no other m
             const int step = g.twin ? 2 : 1, j0 = g.twin ? h : 0;
             for (int j = j0; j < g.n; j += step) {
-                if (!(alive = wwait(bars, &bars.s_full[h], s_phase))) break;
-                s_phase ^= 1;
+                if (!(alive = wwait(bars, &bars.s_full[h], phase))) break;
+                phase ^= 1;
                 if (n_rows <= 0) {                             // none of the warp's rows counts
                     if (lane == 0) tc::mbar_arrive(&bars.p_ready[h]);
-                    pv_phase ^= 1;
                     continue;
                 }
                 tc::tc_fence_after();
@@ -268,42 +273,70 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int i = 1; i < 32; ++i) mx4[k] = fmaxf(mx4[k], __uint_as_float(s[k][i]));
                 }
                 const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * a.scale_log2;
-                // (true for the first key that a row sees; lanes past the rows hold anything)
-                const bool grew = lane < n_rows && mx > m + kGrow;
-                if (j == j0) {
-                    m = mx;
-                } else if (__any_sync(0xffffffffu, grew)) {
-                    const float now = grew ? mx : m;   // a row's own matter: what its neighbours do must not show in it
-                    const float f = now == -INFINITY ? 1.0f : exp2_fast(m - now);
-                    m = now;
-                    l *= f;
-                    // the product before this one must be done with O
-                    if (!(alive = wwait(bars, &bars.pv_done[h], pv_phase ^ 1))) break;
-                    tc::tc_fence_after();
+                float2 sum[2] = {};
+                bool weighed = false;
+                // (lanes past the rows hold anything)
+                if (__any_sync(0xffffffffu, lane < n_rows && mx > limit)) {   // the first key that a row sees, among others
+                    // a row's own matter: what its neighbours do must not show in it
+                    const bool grew = j == j0 || (lane < n_rows && mx - m > kGrow);
+                    if (__any_sync(0xffffffffu, grew)) {
+                        const float now = grew ? mx : m;
+                        const float f = now == -INFINITY ? 1.0f : exp2_fast(m - now);
+                        m = now;
+                        limit = is_large(m) ? -INFINITY : m + kGrow;
+                        l *= f;
+                        if (j > j0) {
+                            // the product before this one must be done with O
+                            if (!(alive = wwait(bars, &bars.pv_done[h], phase))) break;
+                            tc::tc_fence_after();
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        uint32_t o[16];
-                        tc::tmem_ld16(o_col + k * 16, o);
-                        tc::tmem_ld_wait();
+                            for (int k = 0; k < D / 16; ++k) {
+                                uint32_t o[16];
+                                tc::tmem_ld16(o_col + k * 16, o);
+                                tc::tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                        tc::tmem_st16(o_col + k * 16, o);
+                                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                                tc::tmem_st16(o_col + k * 16, o);
+                            }
+                        }
+                    }
+                    if (__any_sync(0xffffffffu, lane < n_rows && is_large(m))) {
+                        // the products again, 32 at a time (P's columns up to here lie before the products that are left)
+                        weighed = true;
+#pragma unroll 1
+                        for (int k = 0; k < 4; ++k) {
+                            uint32_t x[32], pr[16];
+                            tc::tmem_ld32(s_col + k * 32, x);
+                            tc::tmem_ld_wait();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) {
+                                const float y = __uint_as_float(x[i]), base = m == -INFINITY ? 0.0f : m;
+                                float e = exp2_fast(is_large(m) ? __fmul_rn(y, a.scale_log2) - base : fmaf(y, a.scale_log2, -base));
+                                if (k0 + k * 32 + i >= seen) e = 0.0f;
+                                (i & 1 ? sum[i >> 1 & 1].y : sum[i >> 1 & 1].x) += e;
+                                x[i] = __float_as_uint(e);
+                            }
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) pr[i] = mq_pack2<T>(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+                            tc::tmem_st16(s_col + k * 16, pr);
+                        }
                     }
                 }
-                const float base = m == -INFINITY ? 0.0f : m;
-                float2 sum[2] = {};
+                if (!weighed) {
+                    const float base = m == -INFINITY ? 0.0f : m;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    uint32_t pr[16];
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t pr[16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float2 x = f2_fma(make_float2(__uint_as_float(s[k][2 * i]), __uint_as_float(s[k][2 * i + 1])),
-                                                f2_dup(a.scale_log2), f2_dup(-base));
-                        const float2 e = make_float2(exp2_fast(x.x), exp2_fast(x.y));
-                        sum[i & 1] = f2_add(sum[i & 1], e);
-                        pr[i] = mq_pack2<T>(e.x, e.y);
+                        for (int i = 0; i < 16; ++i) {
+                            const float2 x = f2_fma(make_float2(__uint_as_float(s[k][2 * i]), __uint_as_float(s[k][2 * i + 1])),
+                                                    f2_dup(a.scale_log2), f2_dup(-base));
+                            const float2 e = make_float2(exp2_fast(x.x), exp2_fast(x.y));
+                            sum[i & 1] = f2_add(sum[i & 1], e);
+                            pr[i] = mq_pack2<T>(e.x, e.y);
+                        }
+                        tc::tmem_st16(s_col + k * 16, pr);
                     }
-                    tc::tmem_st16(s_col + k * 16, pr);
                 }
                 sum[0] = f2_add(sum[0], sum[1]);
                 l += sum[0].x + sum[0].y;
@@ -311,10 +344,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&bars.p_ready[h]);
-                pv_phase ^= 1;
             }
             if (!alive) break;
-            if (j0 < g.n && !(alive = wwait(bars, &bars.pv_done[h], pv_phase ^ 1))) break;
+            if (j0 < g.n && !(alive = wwait(bars, &bars.pv_done[h], phase ^ 1))) break;
             // A twin segment's rows are joined by half 0's threads, which reach the other half's output in the same
             // lanes of tensor memory: f scales the own one, f1 the other.
             float f = 1.0f, f1 = 0.0f;
