@@ -277,4 +277,16 @@ struct Out {
 
 constexpr float kLn2 = 0.6931471805599453f;
 
+// Maxima (base 2, scaled) whose last place is no longer small beside the exponents taken against them. (-infinity: no key seen.)
+constexpr float kLarge = 1048576.0f;
+__device__ __forceinline__ bool is_large(float m) { return fabsf(m) >= kLarge && m != -INFINITY; }
+
+// What a row's exponents are taken against for a maximum of mx: UP powers of two below it, so that f16 has room for weights
+// far below the maximum's (against the maximum itself those under 2^-25 would be lost, however many there are). Any such
+// reference gives the same sums but for rounding; it stands for the maximum in a piece's statistics.
+template <int UP>
+__device__ __forceinline__ float reference(float mx) {
+    return UP == 0 || fabsf(mx) >= kLarge ? mx : mx - UP;
+}
+
 }  // namespace attn

@@ -13,6 +13,8 @@
 // Measured: the own caches of 64 sequences (17 to 2048 rows, 8 key heads of 128, 268 MB) in 49 us, 5.4 TB/s; one sequence on a
 // prefix of 512 in 6.4 us, which is latency.
 
+#include <type_traits>
+
 #include "attn_few.cuh"
 #include "attn_maps.cuh"
 
@@ -87,6 +89,9 @@ __device__ __forceinline__ float exp2_fast(float x) {   // 2^x within 2 ulp; 2^-
 }
 
 constexpr float kNone = -INFINITY;
+// A row's reference follows its maximum, so its weights are at most 2^14 in f16.
+template <typename T>
+constexpr int kUp = std::is_same<T, __half>::value ? 14 : 0;
 
 template <typename T, int D, bool RAW>
 __global__ void __launch_bounds__(kThreads, 8)
@@ -205,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 8)
         float o[D / 8][4];
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
-        float m[2] = {kNone, kNone}, l[2] = {0.0f, 0.0f};
+        float m[2] = {kNone, kNone}, l[2] = {0.0f, 0.0f};   // references and sums
         float* const raw_row = RAW ? a.raw + (((long long)w.b * p.Hkv + w.head) * tg + w.r0) * p.own_cap : nullptr;
 
 #pragma unroll 1
@@ -239,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 8)
                 mma<T>(s[0], qf[k], kf[0], kf[1]);
                 mma<T>(s[1], qf[k], kf[2], kf[3]);
             }
-            float mx[2] = {m[0], m[1]};
+            float mx[2] = {kNone, kNone};
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -274,6 +279,7 @@ __global__ void __launch_bounds__(kThreads, 8)
             for (int u = 0; u < 2; ++u) {
                 mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], 1));
                 mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], 2));
+                mx[u] = fmaxf(m[u], reference<kUp<T>>(mx[u]));
                 grew |= mx[u] != m[u];
                 const float safe = mx[u] == kNone ? 0.0f : mx[u];
                 alpha[u] = exp2_fast(m[u] - safe);

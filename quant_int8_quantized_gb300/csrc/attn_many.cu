@@ -48,12 +48,13 @@ constexpr int kLaunchRegs = 168, kRowRegs = 208, kOtherRegs = 88;
 constexpr int kHalf = kManyHalf;
 constexpr int kKeys = kManyKeys;
 constexpr uint32_t kTmemCols = 512;
-constexpr float kGrow = 8.0f;           // powers of two by which a row may pass its maximum
-// Maxima from which a row's products are scaled and rounded, as the maximum itself was, before it is taken off. Below, one
-// fused step does both, and what it keeps of a product past the maximum's last place is 2^-5 at most; from 2^28 that would be
-// powers of two by which the weights leave their type. (-infinity: no key seen yet.)
-constexpr float kLarge = 1048576.0f;
-__device__ __forceinline__ bool is_large(float m) { return fabsf(m) >= kLarge && m != -INFINITY; }
+constexpr float kGrow = 8.0f;           // powers of two by which a row may pass the maximum that its reference comes from
+// f16 holds weights up to 2^15 and down to 2^-24: the row's reference lies 2^7 below that maximum.
+template <typename T>
+constexpr int kUp = std::is_same<T, __half>::value ? 7 : 0;
+// Of rows whose maxima are large (attn.cuh) the products are scaled and rounded, as the maximum itself was, before the
+// reference is taken off. Otherwise one fused step does both, and what it keeps of a product past the maximum's last place is
+// 2^-5 at most; from 2^28 that would be powers of two by which the weights leave their type.
 
 template <int D>
 struct Cfg {
@@ -239,8 +240,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int r = half0 + row, q_in = p.by_group.of(r);   // this thread's row; its query in the segment
             const int n_rows = g.rows - half0 - quarter * 32;     // rows of the warp that count
             const int own_sees = g.prefix ? g.see : g.see + q_in;
-            float m = -INFINITY, l = 0.0f;                    // base 2, scaled
-            float limit = -INFINITY;                          // of a tile's maximum that needs no other m
+            float m = -INFINITY, l = 0.0f;                    // reference (base 2, scaled) and sum
+            float limit = -INFINITY;                          // of a tile's maximum that needs no other reference
             const int step = g.twin ? 2 : 1, j0 = g.twin ? h : 0;
             for (int j = j0; j < g.n; j += step) {
                 if (!(alive = wwait(bars, &bars.s_full[h], phase))) break;
@@ -278,12 +279,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // (lanes past the rows hold anything)
                 if (__any_sync(0xffffffffu, lane < n_rows && mx > limit)) {   // the first key that a row sees, among others
                     // a row's own matter: what its neighbours do must not show in it
-                    const bool grew = j == j0 || (lane < n_rows && mx - m > kGrow);
+                    const bool grew = j == j0 || (lane < n_rows && mx - m > kGrow + kUp<T>);
                     if (__any_sync(0xffffffffu, grew)) {
-                        const float now = grew ? mx : m;
+                        const float now = grew ? reference<kUp<T>>(mx) : m;
                         const float f = now == -INFINITY ? 1.0f : exp2_fast(m - now);
                         m = now;
-                        limit = is_large(m) ? -INFINITY : m + kGrow;
+                        limit = is_large(m) ? -INFINITY : m + (kGrow + kUp<T>);
                         l *= f;
                         if (j > j0) {
                             // the product before this one must be done with O

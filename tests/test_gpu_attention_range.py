@@ -80,3 +80,36 @@ def test_a_later_tile_just_above_the_maximum():
         out = torch.empty((1, 30, 1, D), device="cuda")
         mq.mq_attn_prefix(q, None, mq.KV(k, v), n, out, scale=91.0 + 1.37 * i)
         assert bool(((out >= 1 - 2.0 ** -10) & (out <= 2 + 2.0 ** -9)).all()), i
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("T,P,cap", [(1, 0, 16), (1, 0, 700), (1, 40000, 10), (3, 33000, 200), (20, 5000, 300), (600, 40000, 1000),
+                                     (700, 0, 700)])
+def test_many_small_weights_beside_a_dominant_one(T, P, cap, dtype):
+    """The first key outweighs each of the others some 2^25.5 times, and its value is zero: the output is what the others
+    add up to, and none may be lost for being small beside the first. Off by a rounding of each weight (relative, or half of
+    f16's smallest number against a weight of 2^7 for the maximum), by 2^-15 for the exponentials of products up to 18, by 2^-16 for
+    the sums."""
+    D, Hq = 64, 8
+    g = torch.Generator(device="cuda")
+    g.manual_seed(P + cap)
+    q = torch.zeros((1, T, Hq, D), dtype=dtype, device="cuda")
+    q[..., 0] = 8.0                                        # times a scale of 1/8: products are the keys' first element
+    N = P + cap
+    keys, vals = (torch.zeros((N, 1, D), dtype=dtype, device="cuda") for _ in range(2))
+    keys[1:, 0, 0] = (-17.675 + 0.3 * torch.randn(N - 1, generator=g, device="cuda").clamp(-2, 2)).to(dtype)
+    vals[1:, 0] = (0.5 + 0.5 * torch.rand((N - 1, D), generator=g, device="cuda")).to(dtype)
+    pre = mq.KV(keys[None, :P], vals[None, :P]) if P else None
+    out = torch.empty((1, T, Hq, D), device="cuda")
+    mq.mq_attn_prefix(q, pre, mq.KV(keys[None, P:], vals[None, P:]), torch.full((1,), cap, dtype=torch.int32, device="cuda"), out)
+    torch.cuda.synchronize()
+    assert mq.mq_device_status() == mq.MQ_OK
+    p = keys[:, 0, 0].double().exp()
+    sees = (N - T + 1 + torch.arange(T, device="cuda")) - 1                       # last key that each query sees
+    total = p.cumsum(0)[sees][:, None]
+    want = (p[:, None] * vals[:, 0].double()).cumsum(0)[sees] / total
+    mass = vals[:, 0].double().cumsum(0)[sees] / total
+    bound = want * (R.U[dtype] + 2.0 ** -15 + 2.0 ** -16) + (2.0 ** -32 * mass if dtype is F16 else 0.0) + 2.0 ** -24 * want
+    bad = (out[0].double() - want[:, None]).abs() > bound[:, None]
+    assert not bad.any(), f"{int(bad.sum())} of {bad.numel()}; worst relative error " \
+        f"{float(((out[0].double() - want[:, None]).abs() / want[:, None]).max()):.3g}"
