@@ -2,6 +2,7 @@
 // that join the pieces (attn.cuh) into outputs and add up attention weights.
 
 #include <cmath>
+#include <limits>
 
 #include "attn_few.cuh"
 #include "attn_many.cuh"
@@ -599,8 +600,9 @@ extern "C" int mq_attn_prefix(const void* q, long long q_stride, int B, int T, i
         m.q = q;
         m.q_stride = q_stride;
         m.len = own_len;
-        // a scale of next to nothing keeps masked products (-infinity) masked where zero would not
-        m.scale_log2 = std::fmax(std::fabs(scale) * kLog2e, 1e-30f);
+        // the least scale above zero keeps masked products (-infinity) masked where zero would not, and moves no finite one
+        // (below 2^128) by more than 2^-21
+        m.scale_log2 = std::fmax(std::fabs(scale) * kLog2e, std::numeric_limits<float>::denorm_min());
         m.negative = scale < 0.0f;
         m.out = many;
         m.split = c.own_many ? reinterpret_cast<int4*>(base + c.split) : nullptr;

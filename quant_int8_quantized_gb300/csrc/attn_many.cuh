@@ -11,7 +11,7 @@ struct ManyArgs {
     const void* q;
     long long q_stride;
     const int32_t* len;
-    float scale_log2;     // |scale| log2 e, not below 1e-30
+    float scale_log2;     // |scale| log2 e, above zero
     int negative;         // scale < 0
     Pieces out;
     int4* split;          // [G]: segment that begins in the block and goes on in others (or -1), its last block,

@@ -113,3 +113,18 @@ def test_many_small_weights_beside_a_dominant_one(T, P, cap, dtype):
     bad = (out[0].double() - want[:, None]).abs() > bound[:, None]
     assert not bad.any(), f"{int(bad.sum())} of {bad.numel()}; worst relative error " \
         f"{float(((out[0].double() - want[:, None]).abs() / want[:, None]).max()):.3g}"
+
+
+@pytest.mark.parametrize("scale", [0.0, 1e-38, 3e-33, -3e-33])
+@pytest.mark.parametrize("T", [1, 50])
+def test_scales_of_next_to_nothing(T, scale):
+    """Products of some 1e32: a scale of zero weighs all keys alike, one of 3e-33 does not quite."""
+    B, Hq, Hkv, D, P, cap = 2, 4, 2, 64, 70, 200
+    q, k, v = (_rand((B, n, h, D), BF16, i, s) for i, (n, h, s) in enumerate(((T, Hq, 3e15), (cap, Hkv, 3e15), (cap, Hkv, 1.0))))
+    pk, pv = _rand((1, P, Hkv, D), BF16, 5, 3e15), _rand((1, P, Hkv, D), BF16, 6)
+    lens = [cap, T + 20]
+    out, lse = torch.empty((B, T, Hq, D), device="cuda"), torch.empty((B, T, Hq), device="cuda")
+    mq.mq_attn_prefix(q, mq.KV(pk, pv), mq.KV(k, v), torch.tensor(lens, dtype=torch.int32, device="cuda"), out, scale=scale, lse=lse)
+    want, bound = R.attention(q, pk[0], pv[0], k, v, lens, scale, F32)
+    assert bool(((out.double() - want[0]).abs() <= bound[0]).all())
+    assert bool(((lse.double() - want[1]).abs() <= bound[1]).all())
