@@ -579,7 +579,8 @@ extern "C" int mq_attn_prefix(const void* q, long long q_stride, int B, int T, i
         return MQ_ERR_ALIGN;
     const bool scores = score_out && cap > 0;
     Cut c = cut_of(B, T, Hq, Hkv, D, P, cap, scores);
-    if (!c.fits || all_segs(c.few) > 0x3fffffffLL || all_segs(c.many) > 0x3fffffffLL || (long long)B * Hkv > 65535) return MQ_ERR_SHAPE;
+    if (!c.fits || all_segs(c.few) > 0x3fffffffLL || all_segs(c.many) > 0x3fffffffLL) return MQ_ERR_SHAPE;
+    if (scores && (long long)B * Hkv > 65535) return MQ_ERR_SHAPE;   // a grid's y axis
     if (ws_bytes < c.bytes) return MQ_ERR_SCRATCH;
     rc = mq::check_arch();
     if (rc != MQ_OK) return rc;

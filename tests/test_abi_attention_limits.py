@@ -1,0 +1,34 @@
+"""Limits of mq_attn_prefix, without a GPU: calls that a limit does not concern are taken (they end at a workspace of
+no bytes, before any CUDA call), those past one are refused."""
+import ctypes
+
+import pytest
+
+from quant_int8_quantized_gb300 import build as B
+from quant_int8_quantized_gb300 import mq
+
+
+@pytest.fixture(scope="module")
+def L():
+    B.build()
+    return mq.lib()
+
+
+def _kv(n, cap, heads=2, dim=64, k=16, v=16, seq=None, row=None):
+    row = heads * dim if row is None else row
+    return mq.CKV(k, v, cap * row if seq is None else seq, row, dim, 0, n, cap, heads, dim)
+
+
+def _call(L, B, T, Hq, prefix=None, own=None, q=1 << 20, stride=None, out=1 << 30, out_type=0, score=None, score_out=None, size=0):
+    D = (own or prefix).dim
+    return L.mq_attn_prefix(q, Hq * D if stride is None else stride, B, T, Hq, ctypes.byref(prefix) if prefix else None,
+                            ctypes.byref(own) if own else None, 16 if own else None, 0.125, out, out_type, None, score,
+                            score_out, 16, size, None)
+
+
+@pytest.mark.parametrize("B,Hkv,T", [(8192, 8, 1), (70000, 1, 1), (8192, 9, 5)])
+def test_sequences_times_heads_are_limited_with_weights_only(L, B, Hkv, T):
+    own = _kv(B, 100, Hkv)
+    assert _call(L, B, T, 2 * Hkv, own=own) == mq.MQ_ERR_SCRATCH
+    assert _call(L, B, T, 2 * Hkv, own=own, prefix=_kv(1, 50, Hkv)) == mq.MQ_ERR_SCRATCH
+    assert _call(L, B, T, 2 * Hkv, own=own, score=16, score_out=16) == mq.MQ_ERR_SHAPE

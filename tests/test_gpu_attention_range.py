@@ -128,3 +128,19 @@ def test_scales_of_next_to_nothing(T, scale):
     want, bound = R.attention(q, pk[0], pv[0], k, v, lens, scale, F32)
     assert bool(((out.double() - want[0]).abs() <= bound[0]).all())
     assert bool(((lse.double() - want[1]).abs() <= bound[1]).all())
+
+
+@pytest.mark.parametrize("T", [1, 3])
+def test_more_sequences_and_heads_than_a_grid_axis(T):
+    """8200 sequences of 8 key heads, most of them short; sampled ones against the reference."""
+    B, H, D, P, cap = 8200, 8, 64, 20, 6
+    q, k, v = (_rand((B, n, H, D), F16, i) for i, n in enumerate((T, cap, cap)))
+    pk, pv = _rand((1, P, H, D), F16, 3), _rand((1, P, H, D), F16, 4)
+    lens = [(5 * b) % (cap + 1) for b in range(B)]
+    out = torch.empty((B, T, H, D), device="cuda")
+    mq.mq_attn_prefix(q, mq.KV(pk, pv), mq.KV(k, v), torch.tensor(lens, dtype=torch.int32, device="cuda"), out)
+    torch.cuda.synchronize()
+    assert mq.mq_device_status() == mq.MQ_OK
+    for b in (0, 1, 4099, 8190, 8191, 8192, 8199):
+        want, bound = R.attention(q[b:b + 1], pk[0], pv[0], k[b:b + 1], v[b:b + 1], lens[b:b + 1], D ** -0.5, F32)
+        assert bool(((out[b:b + 1].double() - want[0]).abs() <= bound[0]).all()), b
