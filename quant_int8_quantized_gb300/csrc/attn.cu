@@ -540,15 +540,21 @@ bool valid_heads(int Hq, int Hkv, int D) {
     return Hq > 0 && Hkv > 0 && Hq % Hkv == 0 && (D == 64 || D == 96 || D == 128 || D == 256);
 }
 
-// Rows, segments and places are counted in int32.
-bool valid_counts(long long B, long long T, long long Hq) { return B * T * Hq <= 0x3fffffffLL; }
+// Rows, segments and places are counted in int32, and so are keys up to the end of the last tile.
+bool valid_counts(long long B, long long T, int Hq, int prefix_cap, int own_cap) {
+    constexpr long long kMost = 0x3fffffff;
+    constexpr int kCapMost = 0x7fffffff - 255;
+    return B * T <= kMost && B * T * Hq <= kMost && prefix_cap <= kCapMost && own_cap <= kCapMost;
+}
 
 }  // namespace
 }  // namespace attn
 
 extern "C" size_t mq_attn_ws_bytes(int B, int T, int Hq, int Hkv, int D, int prefix_cap, int own_cap, int scores) {
     using namespace attn;
-    if (B <= 0 || T <= 0 || prefix_cap < 0 || own_cap < 0 || !valid_heads(Hq, Hkv, D) || !valid_counts(B, T, Hq)) return 0;
+    if (B <= 0 || T <= 0 || prefix_cap < 0 || own_cap < 0 || !valid_heads(Hq, Hkv, D) ||
+        !valid_counts(B, T, Hq, prefix_cap, own_cap))
+        return 0;
     return cut_of(B, T, Hq, Hkv, D, prefix_cap, own_cap, scores != 0).bytes;
 }
 
@@ -570,9 +576,9 @@ extern "C" int mq_attn_prefix(const void* q, long long q_stride, int B, int T, i
     if (out_type != type && out_type != MQ_F32) return MQ_ERR_TYPE;
     if (!valid_heads(Hq, Hkv, D) || (prefix && prefix->n != 1) || (own && own->n != B)) return MQ_ERR_SHAPE;
     if (B == 0 || T == 0) return MQ_OK;
-    if (!valid_counts(B, T, Hq) || q_stride < (long long)Hq * D || q_stride % 8 != 0 || !std::isfinite(scale))
-        return MQ_ERR_SHAPE;
     const int P = prefix ? prefix->cap : 0, cap = own ? own->cap : 0;
+    if (!valid_counts(B, T, Hq, P, cap) || q_stride < (long long)Hq * D || q_stride % 8 != 0 || !std::isfinite(scale))
+        return MQ_ERR_SHAPE;
     if (!q || !out || !ws || (own && !own_len) || (score == nullptr) != (score_out == nullptr)) return MQ_ERR_NULL;
     if (!mq::aligned16(q) || !mq::aligned16(out) || !mq::aligned16(ws) || !mq::aligned16(own_len) ||
         !mq::aligned16(lse) || !mq::aligned16(score) || !mq::aligned16(score_out))

@@ -32,3 +32,17 @@ def test_sequences_times_heads_are_limited_with_weights_only(L, B, Hkv, T):
     assert _call(L, B, T, 2 * Hkv, own=own) == mq.MQ_ERR_SCRATCH
     assert _call(L, B, T, 2 * Hkv, own=own, prefix=_kv(1, 50, Hkv)) == mq.MQ_ERR_SCRATCH
     assert _call(L, B, T, 2 * Hkv, own=own, score=16, score_out=16) == mq.MQ_ERR_SHAPE
+
+
+BIG = (1 << 31) - 1
+
+
+@pytest.mark.parametrize("B,T,Hq,prefix_cap", [(BIG, BIG, 4, 5), (BIG, 1 << 30, 2, 5), (1 << 16, 1 << 16, 1 << 16, 5), (1 << 30, 1, 2, 5),
+                                               (1, 1, 2, BIG), (1, 64, 8, BIG - 100)])
+def test_counts_past_32_bits_are_refused(L, B, T, Hq, prefix_cap):
+    assert _call(L, B, T, Hq, prefix=_kv(1, prefix_cap, 2 if Hq % 2 == 0 else 1)) == mq.MQ_ERR_SHAPE
+
+
+def test_a_cache_of_more_rows_than_can_be_counted_is_refused(L):
+    assert _call(L, 1, 1, 2, own=_kv(1, BIG, 1)) == mq.MQ_ERR_SHAPE
+    assert _call(L, 1, 64, 8, own=_kv(1, BIG - 100, 1)) == mq.MQ_ERR_SHAPE
