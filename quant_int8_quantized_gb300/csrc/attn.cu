@@ -547,6 +547,12 @@ bool valid_counts(long long B, long long T, int Hq, int prefix_cap, int own_cap)
     return B * T <= kMost && B * T * Hq <= kMost && prefix_cap <= kCapMost && own_cap <= kCapMost;
 }
 
+// Segments and costs fit int32; with weights, sequences times key heads a grid's y axis.
+bool valid_cut(const Cut& c, int B, int Hkv, bool scores) {
+    return c.fits && all_segs(c.few) <= 0x3fffffffLL && all_segs(c.many) <= 0x3fffffffLL &&
+           !(scores && (long long)B * Hkv > 65535);
+}
+
 }  // namespace
 }  // namespace attn
 
@@ -555,7 +561,8 @@ extern "C" size_t mq_attn_ws_bytes(int B, int T, int Hq, int Hkv, int D, int pre
     if (B <= 0 || T <= 0 || prefix_cap < 0 || own_cap < 0 || !valid_heads(Hq, Hkv, D) ||
         !valid_counts(B, T, Hq, prefix_cap, own_cap))
         return 0;
-    return cut_of(B, T, Hq, Hkv, D, prefix_cap, own_cap, scores != 0).bytes;
+    const Cut c = cut_of(B, T, Hq, Hkv, D, prefix_cap, own_cap, scores != 0);
+    return valid_cut(c, B, Hkv, scores && own_cap > 0) ? c.bytes : 0;
 }
 
 extern "C" int mq_attn_prefix(const void* q, long long q_stride, int B, int T, int Hq, const mq_kv* prefix,
@@ -585,8 +592,7 @@ extern "C" int mq_attn_prefix(const void* q, long long q_stride, int B, int T, i
         return MQ_ERR_ALIGN;
     const bool scores = score_out && cap > 0;
     Cut c = cut_of(B, T, Hq, Hkv, D, P, cap, scores);
-    if (!c.fits || all_segs(c.few) > 0x3fffffffLL || all_segs(c.many) > 0x3fffffffLL) return MQ_ERR_SHAPE;
-    if (scores && (long long)B * Hkv > 65535) return MQ_ERR_SHAPE;   // a grid's y axis
+    if (!valid_cut(c, B, Hkv, scores)) return MQ_ERR_SHAPE;
     if (ws_bytes < c.bytes) return MQ_ERR_SCRATCH;
     rc = mq::check_arch();
     if (rc != MQ_OK) return rc;

@@ -16,7 +16,7 @@ def L():
 
 def _kv(n, cap, heads=2, dim=64, k=16, v=16, seq=None, row=None):
     row = heads * dim if row is None else row
-    return mq.CKV(k, v, cap * row if seq is None else seq, row, dim, 0, n, cap, heads, dim)
+    return mq.CKV(k, v, max(cap, 1) * row if seq is None else seq, row, dim, 0, n, cap, heads, dim)
 
 
 def _call(L, B, T, Hq, prefix=None, own=None, q=1 << 20, stride=None, out=1 << 30, out_type=0, score=None, score_out=None, size=0):
@@ -46,3 +46,14 @@ def test_counts_past_32_bits_are_refused(L, B, T, Hq, prefix_cap):
 def test_a_cache_of_more_rows_than_can_be_counted_is_refused(L):
     assert _call(L, 1, 1, 2, own=_kv(1, BIG, 1)) == mq.MQ_ERR_SHAPE
     assert _call(L, 1, 64, 8, own=_kv(1, BIG - 100, 1)) == mq.MQ_ERR_SHAPE
+
+
+@pytest.mark.parametrize("B,T,Hq,Hkv,P,cap,scores", [(8192, 1, 64, 8, 0, 1 << 22, False), (64, 1 << 14, 40, 8, 0, 1 << 24, True),
+                                                     (1, 1 << 20, 64, 8, 1 << 24, 0, False), (8192, 1, 16, 8, 0, 100, True),
+                                                     (70000, 1, 2, 1, 30, 0, True), (70000, 1, 2, 1, 30, 5, True)])
+def test_sizes_that_a_call_refuses_have_no_workspace(L, B, T, Hq, Hkv, P, cap, scores):
+    """With weights, a cache of no rows has none to add up: such a call is taken."""
+    own, prefix = _kv(B, cap, Hkv, 64), _kv(1, P, Hkv, 64) if P else None
+    rc = _call(L, B, T, Hq, prefix=prefix, own=own, score=16 if scores else None, score_out=16 if scores else None)
+    assert rc == (mq.MQ_ERR_SCRATCH if cap == 0 and scores else mq.MQ_ERR_SHAPE)
+    assert (mq.mq_attn_ws_bytes(B, T, Hq, Hkv, 64, P, cap, scores) > 0) == (rc == mq.MQ_ERR_SCRATCH)
