@@ -426,8 +426,8 @@ int mq_qk_norm_rope(const mq_qkv* x, void* q_out, const mq_kv* cache, const int3
  * the caches' type for the product with the values (2^-12 or 2^-9 relative, as the output's own
  * rounding is), sums in f32. An MQ_F32 output carries that rounding. Deterministic.
  * D: 64, 96, 128 or 256; Hq a multiple of Hkv; at most 2^30 - 1 rows (B * T * Hq), 2^31 - 256 keys in a cache, and
- * some 2^31 tiles of 16 rows of a key head by 16 keys (256 by 128 where the call has that many rows) in all, else MQ_ERR_SHAPE;
- * mq_attn_ws_bytes gives 0 for such sizes. scale must be finite. ws: caller-owned device
+ * some 2^31 tiles of 16 rows of a key head by 16 keys (256 by 128 where the call has that many rows) in all, else MQ_ERR_SHAPE
+ * (mq_attn_ws_bytes gives 0 for such sizes), as for strides of 2^39 elements and more between rows. scale must be finite. ws: caller-owned device
  * memory of at least mq_attn_ws_bytes(this call's sizes) bytes (MQ_ERR_SCRATCH otherwise; the sizes choose
  * the kernels, so a smaller call may need more), 16-byte aligned, nothing kept in it between
  * calls; calls that run at the same time need one each. B == 0 or T == 0 is a no-op. A call is one to

@@ -6,6 +6,7 @@
 
 #include "attn_few.cuh"
 #include "attn_many.cuh"
+#include "attn_maps.cuh"
 
 namespace attn {
 namespace {
@@ -547,6 +548,11 @@ bool valid_counts(long long B, long long T, int Hq, int prefix_cap, int own_cap)
     return B * T <= kMost && B * T * Hq <= kMost && prefix_cap <= kCapMost && own_cap <= kCapMost;
 }
 
+bool valid_strides(const mq_kv* c) {
+    return !c || ((c->n <= 1 || c->seq_stride <= kStrideMost) && (c->cap <= 1 || c->row_stride <= kStrideMost) &&
+                  (c->heads <= 1 || c->head_stride <= kStrideMost));
+}
+
 // Segments and costs fit int32; with weights, sequences times key heads a grid's y axis.
 bool valid_cut(const Cut& c, int B, int Hkv, bool scores) {
     return c.fits && all_segs(c.few) <= 0x3fffffffLL && all_segs(c.many) <= 0x3fffffffLL &&
@@ -584,6 +590,7 @@ extern "C" int mq_attn_prefix(const void* q, long long q_stride, int B, int T, i
     if (!valid_heads(Hq, Hkv, D) || (prefix && prefix->n != 1) || (own && own->n != B)) return MQ_ERR_SHAPE;
     if (B == 0 || T == 0) return MQ_OK;
     const int P = prefix ? prefix->cap : 0, cap = own ? own->cap : 0;
+    if (!valid_strides(prefix) || !valid_strides(own) || ((long long)B * T > 1 && q_stride > kStrideMost)) return MQ_ERR_SHAPE;
     if (!valid_counts(B, T, Hq, P, cap) || q_stride < (long long)Hq * D || q_stride % 8 != 0 || !std::isfinite(scale))
         return MQ_ERR_SHAPE;
     if (!q || !out || !ws || (own && !own_len) || (score == nullptr) != (score_out == nullptr)) return MQ_ERR_NULL;

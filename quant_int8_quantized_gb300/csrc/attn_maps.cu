@@ -36,9 +36,10 @@ bool encode(CUtensorMap* map, int type, const void* base, int rank, const cuuint
 }  // namespace
 
 bool kv_map(CUtensorMap* map, const mq_kv* c, const void* base, int box_dims, int box_rows) {
-    auto stride = [](long long s) { return (cuuint64_t)(s > 0 ? s * 2 : 16); };   // an axis of one step may have none
+    // an axis of one step may have any stride: nothing steps along it
+    auto stride = [](long long s, int steps) { return (cuuint64_t)(steps > 1 ? s * 2 : 16); };
     const cuuint64_t dims[4] = {(cuuint64_t)c->dim, (cuuint64_t)c->heads, (cuuint64_t)c->cap, (cuuint64_t)c->n};
-    const cuuint64_t strides[3] = {stride(c->head_stride), stride(c->row_stride), stride(c->seq_stride)};
+    const cuuint64_t strides[3] = {stride(c->head_stride, c->heads), stride(c->row_stride, c->cap), stride(c->seq_stride, c->n)};
     const cuuint32_t box[4] = {(cuuint32_t)box_dims, 1, (cuuint32_t)box_rows, 1};
     return encode(map, c->type, base, 4, dims, strides, box);
 }
@@ -46,7 +47,7 @@ bool kv_map(CUtensorMap* map, const mq_kv* c, const void* base, int box_dims, in
 bool q_map(CUtensorMap* map, const void* q, long long q_stride, long long queries, int Hq, int D, int type, int group,
            int box_queries) {
     const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)Hq, (cuuint64_t)queries};
-    const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)q_stride * 2};
+    const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)(queries > 1 ? q_stride : (long long)Hq * D) * 2};
     const cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)box_queries};
     return encode(map, type, q, 3, dims, strides, box);
 }

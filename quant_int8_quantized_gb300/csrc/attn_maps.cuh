@@ -8,6 +8,9 @@
 
 namespace attn {
 
+// Elements between steps that a tensor map can hold (2^40 bytes it cannot).
+constexpr long long kStrideMost = (1LL << 39) - 8;
+
 // [n][cap][heads][dim] of k or v (`base`) as (dim, head, row, sequence): boxes of `dims` (64: 128-byte swizzle,
 // 32: 64-byte swizzle) by `rows` rows of one head; rows past the cap read as zeros.
 bool kv_map(CUtensorMap* map, const mq_kv* c, const void* base, int dims, int rows);

@@ -57,3 +57,23 @@ def test_sizes_that_a_call_refuses_have_no_workspace(L, B, T, Hq, Hkv, P, cap, s
     rc = _call(L, B, T, Hq, prefix=prefix, own=own, score=16 if scores else None, score_out=16 if scores else None)
     assert rc == (mq.MQ_ERR_SCRATCH if cap == 0 and scores else mq.MQ_ERR_SHAPE)
     assert (mq.mq_attn_ws_bytes(B, T, Hq, Hkv, 64, P, cap, scores) > 0) == (rc == mq.MQ_ERR_SCRATCH)
+
+
+@pytest.mark.parametrize("what", ["own sequences", "own rows", "prefix rows", "queries"])
+def test_strides_past_what_a_copy_can_step_are_refused(L, what):
+    """2^40 bytes and more between rows that both exist: no tensor map holds that."""
+    own, prefix, stride = _kv(2, 10), _kv(1, 10), None
+    if what == "own sequences":
+        own = _kv(2, 10, seq=1 << 39)
+    elif what == "own rows":
+        own = _kv(2, 10, row=1 << 39, seq=128)
+    elif what == "prefix rows":
+        prefix = _kv(1, 10, row=1 << 39, seq=0)
+    else:
+        stride = 1 << 39
+    assert _call(L, 2, 1, 4, prefix=prefix, own=own, stride=stride) == mq.MQ_ERR_SHAPE
+
+
+def test_a_stride_that_nothing_steps_along_does_not_matter(L):
+    own = _kv(1, 10, seq=1 << 40)
+    assert _call(L, 1, 1, 4, own=own, stride=1 << 40) == mq.MQ_ERR_SCRATCH
