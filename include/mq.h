@@ -419,6 +419,8 @@ int mq_qk_norm_rope(const mq_qkv* x, void* q_out, const mq_kv* cache, const int3
  *             score_out[b][g][j] = score[b][g][j] + the weights p_j of own row j, summed over the
  *             T queries and the group's heads, for j < own_len[b]; other entries are not touched.
  *             B * Hkv is then at most 65535 (MQ_ERR_SHAPE).
+ * The outputs overlap neither each other nor what the call reads, but that score_out may be score: an out over rows of q and a
+ * score_out over other entries of score are MQ_ERR_SHAPE.
  * A query that sees no key gives zeros and an lse of -infinity.
  * Rows that a query sees must be finite for that query's result to be; with T > 1 a value row that holds
  * infinities or NaN also reaches the queries of its sequence that come before it.

@@ -601,6 +601,10 @@ extern "C" int mq_attn_prefix(const void* q, long long q_stride, int B, int T, i
     Cut c = cut_of(B, T, Hq, Hkv, D, P, cap, scores);
     if (!valid_cut(c, B, Hkv, scores)) return MQ_ERR_SHAPE;
     if (ws_bytes < c.bytes) return MQ_ERR_SCRATCH;
+    const long long all_rows = (long long)B * T * Hq, score_bytes = scores ? 4LL * B * Hkv * cap : 0;
+    if (mq::rows_meet(q, (long long)B * T, 2 * q_stride, 2LL * Hq * D, out, all_rows * D * (out_type == MQ_F32 ? 4 : 2)) ||
+        (score != score_out && mq::rows_meet(score, 1, score_bytes, score_bytes, score_out, score_bytes)))
+        return MQ_ERR_SHAPE;   // read by some blocks while others write
     rc = mq::check_arch();
     if (rc != MQ_OK) return rc;
     uint8_t* base = static_cast<uint8_t*>(ws);

@@ -3,6 +3,7 @@ no bytes, before any CUDA call), those past one are refused."""
 import ctypes
 
 import pytest
+import torch
 
 from quant_int8_quantized_gb300 import build as B
 from quant_int8_quantized_gb300 import mq
@@ -77,3 +78,34 @@ def test_strides_past_what_a_copy_can_step_are_refused(L, what):
 def test_a_stride_that_nothing_steps_along_does_not_matter(L):
     own = _kv(1, 10, seq=1 << 40)
     assert _call(L, 1, 1, 4, own=own, stride=1 << 40) == mq.MQ_ERR_SCRATCH
+
+
+ENOUGH = 1 << 40      # bytes of workspace: what follows is looked at last, before the device
+
+
+@pytest.mark.parametrize("T,Hq,stride,out,out_type", [
+    (1, 4, 256, 0, 0), (600, 28, 28 * 64, 0, 0), (600, 28, 28 * 64, 0, 2), (600, 4, 1024, 512, 0),      # over q, over its gaps and rows
+    (600, 28, 28 * 64, 600 * 28 * 128 - 16, 0), (600, 28, 28 * 64, -(600 * 28 * 128) + 16, 0),          # over its end, over its start
+    (1, 4, 256, -1008, 2), (2, 4, 1 << 20, (1 << 21) - 16, 0)])
+def test_outputs_over_queries_are_refused(L, T, Hq, stride, out, out_type):
+    """Blocks that are done write rows of out while others still read q."""
+    q = 1 << 30
+    rc = _call(L, 1, T, Hq, own=_kv(1, 700, 2 if Hq == 4 else 4), q=q, stride=stride, out=q + out, out_type=out_type, size=ENOUGH)
+    assert rc == mq.MQ_ERR_SHAPE
+
+
+@pytest.mark.parametrize("at", [16, 16 * 70, -16])
+def test_weights_over_others_are_refused(L, at):
+    score = 1 << 29
+    rc = _call(L, 2, 1, 4, own=_kv(2, 100), q=1 << 20, out=1 << 30, score=score, score_out=score + at, size=ENOUGH)
+    assert rc == mq.MQ_ERR_SHAPE
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="addresses that are none: these calls get as far as the device")
+@pytest.mark.parametrize("T,stride,out", [(1, 256, 512), (1, 256, -512), (2, 1 << 20, 512), (2, 1 << 20, (1 << 21) - 1024), (2, 256, 1024)])
+def test_outputs_beside_queries_and_weights_in_place_are_taken(L, T, stride, out):
+    """Also between two rows of q that lie far apart."""
+    q, score = 1 << 30, 1 << 29
+    for at in (0, 2 * 2 * 100 * 4, -2 * 2 * 100 * 4):
+        rc = _call(L, 1, T, 4, own=_kv(1, 200), q=q, stride=stride, out=q + out, score=score, score_out=score + at, size=ENOUGH)
+        assert rc == mq.MQ_ERR_ARCH

@@ -45,3 +45,27 @@ def test_strides_that_nothing_steps_along():
     assert rc == mq.MQ_OK
     want, bound = R.attention(q, pk[0], pv[0], k, v, [77], D ** -0.5, F32)
     assert bool(((out.double() - want[0]).abs() <= bound[0]).all())
+
+
+@pytest.mark.parametrize("T", [1, 40, 600])
+def test_outputs_over_queries(T):
+    """Over the queries: refused, whichever kernel would run. Beside them in one allocation: right."""
+    Hq, Hkv, D, cap = 28, 4, 64, T + 100
+    both = _rand((1, T, 2 * Hq, D), F16, 1)
+    q, beside = both[:, :, :Hq].contiguous(), _rand((2, 1, T, Hq, D), F16, 1)
+    k, v = _rand((1, cap, Hkv, D), F16, 2), _rand((1, cap, Hkv, D), F16, 3)
+    n = torch.tensor([cap], dtype=torch.int32, device="cuda")
+    own = mq.KV(k, v)
+    over = [(q, q)]
+    if T > 1:                                          # rows of the other heads, between which the output has no place
+        over.append((both[:, :, Hq:], both.view(-1)[:T * Hq * D]))
+    for x, out in over:
+        before = x.clone()
+        with pytest.raises(mq.MQError) as e:
+            mq.mq_attn_prefix(x, None, own, n, out)
+        assert e.value.status == mq.MQ_ERR_SHAPE and torch.equal(x, before)
+    beside[0] = q
+    mq.mq_attn_prefix(beside[0], None, own, n, beside[1])
+    only = [0, T // 2, T - 1]
+    want, bound = R.attention(q, None, None, k, v, [cap], D ** -0.5, F16, only=only)
+    assert bool(((beside[1][:, only].double() - want[0][:, only]).abs() <= bound[0][:, only]).all())
