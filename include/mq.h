@@ -391,12 +391,12 @@ typedef struct mq_qkv {
  *     a' = a cos t - b sin t,  b' = a sin t + b cos t
  * rounded once to the cache's type. Sums and products are f32; t is reduced to one turn in
  * 64 bits, so large positions lose nothing. Values are only rounded.
- * q_out: [M][Hq][D]. Key and value of token m go to row slot[m] of the cache, counted over
- * all its sequences (sequence slot / cap, row slot % cap); slot NULL: row m. A slot outside
+ * q_out: [M][Hq][D]; it and the cache lie apart from q, k and v. Key and value of token m go to row slot[m] of the
+ * cache, counted over all its sequences (sequence slot / cap, row slot % cap); slot NULL: row m. A slot outside
  * [0, n * cap) is skipped (padding tokens). Two tokens must not have the same slot. The
  * cache's type, heads and dim say what is written; its k and v may be NULL where the input's
  * are. MQ_ERR_SHAPE: M < 0, n_pairs outside 0 .. D/2, n_axes outside 1 .. 8 (with pairs), strides
- * below the row's width or not a multiple of 4, M > n * cap with slot NULL. M == 0 is a no-op.
+ * below the row's width or not a multiple of 4, M > n * cap with slot NULL, q_out over q, k or v. M == 0 is a no-op.
  * A programmatic dependent launch, as the producers; wq and wk are read through the read-only path.
  */
 int mq_qk_norm_rope(const mq_qkv* x, void* q_out, const mq_kv* cache, const int32_t* slot, cudaStream_t stream);

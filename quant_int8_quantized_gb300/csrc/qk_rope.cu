@@ -217,6 +217,8 @@ extern "C" int mq_qk_norm_rope(const mq_qkv* x, void* q_out, const mq_kv* cache,
         !mq::aligned16(x->wk) || !mq::aligned16(x->inv_freq) || !mq::aligned16(x->axis) || !mq::aligned16(x->pos) ||
         !mq::aligned16(slot))
         return MQ_ERR_ALIGN;
+    for (int i = 0; i < 3; ++i)   // a block's output rows would lie over what others have yet to read
+        if (mq::rows_meet(src[i], x->M, 4 * st[i], 4LL * heads[i] * D, q_out, 2LL * x->M * heads[0] * D)) return MQ_ERR_SHAPE;
     rc = mq::check_arch();
     if (rc != MQ_OK) return rc;
     Args a;
