@@ -434,6 +434,8 @@ def mq_qk_norm_rope(q, k, v, q_out, cache: KV, slot=None, pos=None, inv_freq=Non
     first = q if q is not None else k if k is not None else v
     if first is None:
         raise ValueError("one of q, k and v is needed")
+    if not isinstance(first, torch.Tensor):
+        raise TypeError(f"{'q' if first is q else 'k' if first is k else 'v'} must be a torch.Tensor")
     M, D = first.shape[0], cache.dim
     q_ptr, q_stride, Hq = _heads(q, "q", M, D)
     k_ptr, k_stride, _ = _heads(k, "k", M, D, cache.heads)
@@ -514,6 +516,8 @@ def mq_attn_prefix(q: torch.Tensor, prefix, own, own_len, out: torch.Tensor, sca
     if rows and (st[3] != 1 or (Hq > 1 and st[2] != D) or (B > 1 and T > 1 and st[0] != T * st[1])):
         raise ValueError("q: a token's heads must be contiguous, and the tokens at one stride")
     row = st[1] if T > 1 else st[0] if B > 1 else Hq * D
+    if not isinstance(out, torch.Tensor):
+        raise TypeError("out must be a torch.Tensor")
     out_type = out.dtype
     if out_type is not dtype and out_type is not torch.float32:
         raise TypeError(f"out must be {dtype} or torch.float32, got {out_type}")
