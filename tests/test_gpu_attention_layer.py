@@ -69,3 +69,69 @@ def test_each_call_of_a_step_against_64_bits(example, monkeypatch):
     for t in range(40):
         layer.step(synth.normal((2, 512), 7, f"t{t}", device="cuda"))
     assert seen == {"attn": 40, "evict": 3}
+
+
+def test_lock_step_with_64_bits(example, monkeypatch):
+    """Prompt and 40 decode steps beside a layer of its own kind, which knows positions, rows, lengths, scores and
+    evictions by itself and computes in 64 bits from the products' f32 outputs. What the layer rounds to 16 bits or sums
+    up in f32 is checked and then taken over, so that both stay in step."""
+    B, Hq, Hkv, D, cap, keep, recent, T = 2, 4, 2, 64, 16, 8, 2, 33
+    layer = example.AttentionLayer(hidden=512, Hq=Hq, Hkv=Hkv, D=D, batch=B, prefix_cap=40, cap=cap, keep=keep, recent=recent, seed=11)
+    saw, rope, quant = {}, mq.mq_qk_norm_rope, mq.mq_quantize_q8
+
+    def watch_rope(q, k, v, q_out, *a, **kw):
+        saw.update(q=q.clone(), k=k.clone(), v=v.clone())
+        saw["q16"] = rope(q, k, v, q_out, *a, **kw)
+        return saw["q16"]
+
+    def watch_quant(x, plane):
+        saw["o"] = x.clone()
+        return quant(x, plane)
+
+    monkeypatch.setattr(example.mq, "mq_qk_norm_rope", watch_rope)
+    monkeypatch.setattr(example.mq, "mq_quantize_q8", watch_quant)
+
+    def inside(got, want, bound):
+        return bool(((got.double() - want).abs() <= bound).all())
+
+    def turned(positions):
+        pos = torch.tensor([positions], dtype=torch.int32, device="cuda")
+        return [R.rope(saw[x], w, 1e-6, pos, layer.freq, None, 1, False, layer.dtype) for x, w in (("q", layer.q_norm), ("k", layer.k_norm))]
+
+    layer.prompt(synth.normal((T, 512), 1, "lock.p", device="cuda"))
+    (wq, bq), (wk, bk) = turned(list(range(T)))
+    pk, pv = layer.prefix.k[0, :T].clone(), layer.prefix.v[0, :T].clone()
+    assert inside(saw["q16"], wq, bq) and inside(pk, wk, bk) and torch.equal(pv, saw["v"].to(layer.dtype))
+    (o, _, _), (bo, _, _) = R.attention(saw["q16"][None], None, None, pk[None], pv[None], [T], D ** -0.5, torch.float32)
+    assert inside(saw["o"].view(1, T, Hq, D), o, bo)
+
+    # caches, one head at a time: rows kept [rows, D] and their scores
+    ks = [[torch.empty((0, D), dtype=layer.dtype, device="cuda") for _ in range(Hkv)] for _ in range(B)]
+    vs = [[x.clone() for x in row] for row in ks]
+    sc = [[torch.empty((0,), device="cuda") for _ in range(Hkv)] for _ in range(B)]
+    evictions = 0
+    for t in range(40):
+        if len(ks[0][0]) == cap:
+            evictions += 1
+            for b in range(B):
+                for h in range(Hkv):
+                    rows = R.evict(sc[b][h].tolist(), cap, keep, recent)
+                    ks[b][h], vs[b][h], sc[b][h] = (x[b][h][rows] for x in (ks, vs, sc))
+        layer.step(synth.normal((B, 512), 2, f"lock.{t}", device="cuda"))
+        (wq, bq), (wk, bk) = turned([T + t] * B)
+        n = len(ks[0][0]) + 1
+        assert layer.length.tolist() == [n] * B and layer.position.tolist() == [T + t + 1] * B
+        assert inside(saw["q16"], wq, bq)
+        k, v = layer.own.k[:, :n].clone(), layer.own.v[:, :n].clone()
+        score = torch.zeros((B, Hkv, n), device="cuda")
+        for b in range(B):
+            for h in range(Hkv):
+                assert torch.equal(k[b, :n - 1, h], ks[b][h]) and torch.equal(v[b, :n - 1, h], vs[b][h]), (t, b, h)
+                assert inside(k[b, n - 1, h], wk[b, h], bk[b, h]) and torch.equal(v[b, n - 1, h], saw["v"][b, h].to(layer.dtype))
+                score[b, h, :n - 1] = sc[b][h]
+        (o, _, s), (bo, _, bs) = R.attention(saw["q16"].view(B, 1, Hq, D), pk, pv, k, v, [n] * B, D ** -0.5, torch.float32, score)
+        assert inside(saw["o"].view(B, 1, Hq, D), o, bo) and inside(layer.score[:, :, :n], s, bs)
+        for b in range(B):
+            for h in range(Hkv):
+                ks[b][h], vs[b][h], sc[b][h] = k[b, :, h], v[b, :, h], layer.score[b, h, :n].clone()
+    assert evictions == 3
