@@ -454,7 +454,7 @@ int mq_attn_prefix(const void* q, long long q_stride, int B, int T, int Hq, cons
  *   exactly src (same k, v, strides and cap: the rows move down in place); k or v ranges that
  *   overlap otherwise give MQ_ERR_SHAPE, as does score_out overlapping score unless it is score and
  *   the caps are equal. len_out may be len. Rows of dst past the kept ones are not written.
- * 0 <= recent <= keep, else MQ_ERR_SHAPE. n == 0 is a no-op. Programmatic dependent launches.
+ * 0 <= recent <= keep and caps of at most 2^31 - 2^16, else MQ_ERR_SHAPE. n == 0 is a no-op. Programmatic dependent launches.
  */
 int mq_kv_evict(const mq_kv* src, const int32_t* len, const float* score, int keep, int recent, const mq_kv* dst,
                 int32_t* len_out, float* score_out, int32_t* index, cudaStream_t stream);

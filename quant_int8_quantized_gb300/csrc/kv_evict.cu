@@ -21,6 +21,8 @@ constexpr int kMaxCluster = 8;
 constexpr int kBrief = 2048;             // scores of a head up to which a block has 256 threads, not 1024
 constexpr int kMaxKeys = 40 * 1024;      // of a block's stretch that shared memory holds; longer ones are read again
 
+constexpr int kMostRows = 0x7fffffff - 0xffff;   // loops over rows step past the last by at most 8 x 1024
+
 // Order of floats as unsigned integers; -0 equals +0, NaN is below everything.
 __device__ __forceinline__ uint32_t order_key(float f) {
     if (f != f) return 0u;
@@ -378,7 +380,7 @@ extern "C" int mq_kv_evict(const mq_kv* src, const int32_t* len, const float* sc
     if (rc != MQ_OK) return rc;
     if (src->type != dst->type) return MQ_ERR_TYPE;
     if (src->n != dst->n || src->heads != dst->heads || src->dim != dst->dim || recent < 0 || recent > keep ||
-        dst->cap < keep)
+        dst->cap < keep || src->cap > kMostRows || dst->cap > kMostRows)
         return MQ_ERR_SHAPE;
     if (src->n == 0) return MQ_OK;
     if (!len || !len_out || (src->cap > 0 && !score) || (dst->cap > 0 && !index)) return MQ_ERR_NULL;
