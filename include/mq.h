@@ -54,7 +54,8 @@ enum {
     MQ_ERR_SHAPE = 2,   /* K not a positive multiple of 256, negative M/N, plane dims mismatch, GEMV M outside [1, 8] */
     MQ_ERR_ALIGN = 3,   /* a pointer is not 16-byte aligned */
     MQ_ERR_ARCH = 4,    /* the current device is not a compute capability 10.3 (GB300) GPU */
-    MQ_ERR_LAUNCH = 5,  /* the CUDA launch (or tensor-map encoding) failed */
+    MQ_ERR_LAUNCH = 5,  /* the CUDA launch (or tensor-map encoding) failed, or the compiler gave mq_attn_prefix's
+                           tensor-core kernel other registers than it shares out among its warps */
     MQ_ERR_DEVICE = 6,  /* a kernel gave up on a bounded wait (reported by mq_device_status) */
     MQ_ERR_SCRATCH = 7, /* mq_gemm_q6k_static: the call needs more than its fixed scratch array holds;
                            mq_attn_prefix: ws_bytes is less than mq_attn_ws_bytes gives */
@@ -407,7 +408,9 @@ int mq_qk_norm_rope(const mq_qkv* x, void* q_out, const mq_kv* cache, const int3
  *     out[b][t][h] = sum_j p_j v_j,   p = softmax_j(scale * q[b][t][h] . k_j)
  * with j over every row of the prefix, then the rows j < own_len[b] - T + 1 + t of sequence b of `own`: the
  * last T of its own_len[b] rows belong to the T queries themselves, each of which sees the
- * keys up to its own. The prefix's keys and values are read once for the whole batch.
+ * keys up to its own. The prefix's keys and values are read once for a tile of query rows of a key head, 16 or up to 256 of
+ * them, which holds rows of the whole batch where own caches are short or queries few; sequences of 17 rows and more with large
+ * caches read it once each. What several tiles read comes from L2 as far as it fits there.
  *   q       : [B * T][Hq][D] in the caches' type, row stride q_stride (a multiple of 8, at least Hq * D).
  *   prefix  : one sequence (n == 1) whose rows 0 .. cap-1 are all seen; NULL or cap == 0: none.
  *   own     : n == B sequences; NULL: none (own_len is then not read). own_len: int32 [B] on
@@ -425,14 +428,16 @@ int mq_qk_norm_rope(const mq_qkv* x, void* q_out, const mq_kv* cache, const int3
  * Rows that a query sees must be finite for that query's result to be; with T > 1 a value row that holds
  * infinities or NaN also reaches the queries of its sequence that come before it.
  * Arithmetic: products in f32 from 16-bit operands, softmax in f32, probabilities rounded to
- * the caches' type for the product with the values (2^-12 or 2^-9 relative, as the output's own
- * rounding is), sums in f32. An MQ_F32 output carries that rounding. Deterministic.
+ * the caches' type for the product with the values, sums in f32. That rounding moves a weight by at most 2^-11 (MQ_F16) or
+ * 2^-8 (MQ_BF16) of itself, or, in f16, 2^-32 of its row's largest where that is more; so an output moves by as much of
+ * sum p_j |v_j| (plus 2^-32 of the largest p times sum |v_j|) at most, and an MQ_F32 output too. Deterministic.
  * D: 64, 96, 128 or 256; Hq a multiple of Hkv; at most 2^30 - 1 rows (B * T * Hq), 2^31 - 256 keys in a cache, and
  * some 2^31 tiles of 16 rows of a key head by 16 keys (256 by 128 where the call has that many rows) in all, else MQ_ERR_SHAPE
  * (mq_attn_ws_bytes gives 0 for such sizes), as for strides of 2^39 elements and more between rows. scale must be finite. ws: caller-owned device
  * memory of at least mq_attn_ws_bytes(this call's sizes) bytes (MQ_ERR_SCRATCH otherwise; the sizes choose
  * the kernels, so a smaller call may need more), 16-byte aligned, nothing kept in it between
- * calls; calls that run at the same time need one each. B == 0 or T == 0 is a no-op. A call is one to
+ * calls; calls that run at the same time need one each. With score it holds every product with an own row in f32: 4 bytes
+ * times B * T * Hq * own->cap, so a long prompt is better split into calls of fewer queries. B == 0 or T == 0 is a no-op. A call is one to
  * four launches, programmatic dependent ones as the producers; waits are bounded (mq_device_status).
  */
 size_t mq_attn_ws_bytes(int B, int T, int Hq, int Hkv, int D, int prefix_cap, int own_cap, int scores);

@@ -5,7 +5,8 @@
 // segments begin with the prefix's keys). Its keys come in tiles. All segments' tiles in a row, prefix
 // segments first, are cut into runs of equal cost, one per block, whatever the lengths on the device
 // are, so ragged batches stay balanced; a run may end inside a segment and go on in the next. What a block
-// computes of one segment is a *piece*: the unnormalised output, maximum and sum of its rows over its keys, left in
+// computes of one segment is a *piece*: the unnormalised output, reference (about the maximum) and sum of its rows over its
+// keys, left in
 // the workspace at place block + segment (both only grow along the row of tiles, so places differ). The
 // joining kernels add a row's pieces up in the order of their keys.
 #pragma once
@@ -264,7 +265,7 @@ __device__ __forceinline__ void advance(const Plan& p, const int32_t* len, Curso
 // the first; segments without tiles have no entry.
 struct Pieces {
     float* o;      // [place][rows][D]
-    float2* ml;    // [place][rows]: maximum (of the scaled products, base 2) and sum
+    float2* ml;    // [place][rows]: reference (of the scaled products, base 2) and sum of 2^(product - reference)
     int2* info;
 };
 

@@ -11,8 +11,9 @@
 // The halves take turns: while one half's threads work on their tile, the tensor cores do the other half's
 // products (a tile of both halves and of D = 128 in 1.4 us, of which the products alone are 1.3; without the turns some
 // blocks stay in step and take up to 2.1). A segment of at most 128 rows gives both halves the same rows and every other
-// tile. The maximum that the exponents are taken against is renewed only when a row passes it by 2^8 (the sums are the
-// same in any scale, and 2^8 does not bring a 16-bit value near its end), so O in tensor memory is hardly ever scaled again.
+// tile. The reference that the exponents are taken against is renewed only when a row passes the maximum behind it by 2^8
+// (the sums are the same in any scale, and 2^8 does not bring a 16-bit value near its end), so O in tensor memory is hardly
+// ever scaled again.
 //
 // 384 threads, one block per SM: warps 0-3 and 4-7 the rows of the halves, warp 8 copies (TMA), warps 9 and 10 a
 // half's products each (one warp for both issued too slowly), warp 11 walks the block's run and hands its pieces
@@ -20,8 +21,9 @@
 // out again to give a row's thread its 128 products. Shared memory at D = 128: Q (64 KB), a ring of four K and
 // V tiles (32 KB each), and 32 KB through which the rows' outputs go out whole. The next piece's Q is on its
 // way as soon as the last product with this one's is done, and its first products run beside the output.
-// Bound: the tensor cores. Measured: 2048 tokens of 32 heads of 128 behind 16384 keys in 356 us, 1.64 PFLOP/s; 3314 of 28 behind
-// 1000 in 112 us, 1.13 PFLOP/s, where the pieces' first tiles and outputs weigh more.
+// Bound: the tensor cores. Measured: 2048 tokens of 32 heads of 128 behind 16384 keys in 342 us, 1.71 PFLOP/s; 3314 of 28 behind
+// 1000 in 112 us, 1.12 PFLOP/s, where the pieces' first tiles and outputs weigh more; the same with heads of 64 in 87 us, 0.72
+// PFLOP/s: half the products for as many exponentials.
 // Waits are bounded; a wait that runs out is recorded (mq_device_status), the block drains its own copies
 // and products, frees tensor memory and returns.
 

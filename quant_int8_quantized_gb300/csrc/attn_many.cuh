@@ -25,7 +25,7 @@ constexpr int kManyKeys = 128;    // keys per tile
 
 // Costs: a tile of two halves, a tile of a segment that one half would hold (its tiles alternate between the
 // halves: measured at two thirds of the former), a segment's beginning and
-// end (8192 tokens of 32 heads: 7 355 us, 8 357, 10 359, 13 363; 3314 of 28: 112, 114, 112, 115).
+// end (8192 tokens of 32 heads: 7 364 us, 8 362, 10 365, 13 369; 3314 of 28: 112, 113, 112, 114).
 constexpr int kManyCost = 2, kManyWide = 3, kManyExtra = 7;
 
 // Whole queries only: a segment's rows are one box of the queries' tensor map.
