@@ -7,7 +7,8 @@ with copy on write, compaction).
 Rows of a page come in blocks of 16 rows of one head: the keys' 4-bit numbers, the values', the keys' scales, the
 values' (one byte per 32 dims). A number is n d with n = nibble - 8 and d = (8 + c % 8) 2^(c / 8 - 18) for a scale byte
 c >= 8, c 2^-17 below. The 8 dims 32 b + 8 t + 2 j + h of a key row are nibble j of half h of its 32-bit word
-4-wide (t, b); the dims 32 u + 4 g + i of a value row 8 p + 2 t + c are nibble i of half c of word (p, g, t, u).
+(row, t, b); the dims 32 u + 4 g + i of a value row 8 p + 2 t + c are nibble i of half c of word (p, g, t, u). The value
+scales of two neighbouring rows lie side by side.
 """
 import math
 import random
@@ -147,7 +148,7 @@ def _packed(k, v):
     vu = blocks((vn + 8).to(torch.uint8).flatten(-2)).unflatten(3, (2, 4, 2)).unflatten(-1, (b, 8, 2, 2))
     vu = vu.permute(0, 1, 2, 3, 7, 4, 6, 5, 8, 9)    # .., p, g, t, u, c, i / 2, i % 2
     parts = [(u[..., 0] | (u[..., 1] << 4)).flatten(3) for u in (ku, vu)]
-    parts += [blocks(c.to(torch.uint8)).flatten(3) for c in (kc, vc)]
+    parts += [blocks(kc.to(torch.uint8)).flatten(3), blocks(vc.to(torch.uint8)).unflatten(3, (8, 2)).transpose(4, 5).flatten(3)]
     return torch.cat(parts, -1).flatten(1)
 
 
@@ -165,8 +166,9 @@ def _unpacked(pages, R, H, D):
     v = v.permute(0, 1, 2, 3, 5, 7, 6, 4, 8, 9).flatten(7).flatten(3, 5)          # .., row, u, dims of a block
     k = k.flatten(4).unflatten(-1, (b, 32))
     out = []
-    for u, at in ((k, 2 * n), (v, 2 * n + 16 * b)):
-        d = _scale(x[..., at:at + 16 * b]).float().unflatten(-1, (16, b))
+    kc, vc = x[..., 2 * n:2 * n + 16 * b].unflatten(-1, (16, b)), x[..., 2 * n + 16 * b:]
+    for u, code in ((k, kc), (v, vc.unflatten(-1, (8, b, 2)).transpose(4, 5).flatten(3, 4))):
+        d = _scale(code).float()
         y = (u.float() - 8.0) * d[..., None]
         out.append(y.flatten(-2).flatten(2, 3).transpose(1, 2).reshape(*lead, R, H, D))
     return out
@@ -212,7 +214,7 @@ def prepare(case, seed):
         s["k"], s["v"] = kv[:, :Hkv], kv[:, Hkv:]
         s["wq"] = _normal(g, (D,), std=0.1).add_(1.0) if c["norm"] else None
         s["wk"] = _normal(g, (D,), std=0.1).add_(1.0) if c["norm"] else None
-        s["freq"], s["turn"] = _freq(c["rot"], c["factor"]), 0.1 * math.log(c["factor"]) + 1.0
+        s["freq"], s["turn"] = _freq(c["rot"], c["factor"]), float(torch.tensor(0.1 * math.log(c["factor"]) + 1.0))
         base = int(torch.randint(0, 100000, (1,), generator=g, device="cuda"))
         lens = [M // n + (b < M % n) for b in range(n)]
         cap = max(lens)
@@ -493,7 +495,7 @@ def _exact_attn(s):
     vb = 8 * D + (((r // 8 * 8 + g) * 4 + r % 8 // 2) * (D // 32) + b) * 4 + 2 * (r % 2) + i // 2
     vs = 4 * (i % 2)
     kc = 16 * D + r * (D // 32) + b
-    vc = kc + 16 * (D // 32)
+    vc = 16 * D + 16 * (D // 32) + (r // 2 * (D // 32) + b) * 2 + r % 2
     scales = [m * 2.0 ** -17 for m in range(8)] + [(8 + m) * 2.0 ** (e - 18) for e in range(1, 32) for m in range(8)]
     scales = torch.tensor(scales, dtype=torch.float64, device="cuda")
     for q in range(B):
