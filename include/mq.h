@@ -58,7 +58,7 @@ enum {
                            tensor-core kernel other registers than it shares out among its warps */
     MQ_ERR_DEVICE = 6,  /* a kernel gave up on a bounded wait (reported by mq_device_status) */
     MQ_ERR_SCRATCH = 7, /* mq_gemm_q6k_static: the call needs more than its fixed scratch array holds;
-                           mq_attn_prefix: ws_bytes is less than mq_attn_ws_bytes gives */
+                           mq_attn_prefix, mq_attn_kv4, mq_pages_*: ws_bytes is less than the call's ..._ws_bytes gives */
     MQ_ERR_TYPE = 8     /* an element type that the call does not take */
 };
 
@@ -463,6 +463,128 @@ int mq_attn_prefix(const void* q, long long q_stride, int B, int T, int Hq, cons
  */
 int mq_kv_evict(const mq_kv* src, const int32_t* len, const float* score, int keep, int recent, const mq_kv* dst,
                 int32_t* len_out, float* score_out, int32_t* index, cudaStream_t stream);
+
+/*
+ * Keys and values in 4 bits, on pages
+ * ------------------------------------
+ * A cache of n sequences whose rows lie on pages of a pool: row j of sequence i is row j % page_rows of page
+ * table[i * table_stride + j / page_rows]. A page holds the rows of all key heads, head by head, each as blocks of 16 rows:
+ *     8 dim bytes of key numbers, 8 dim of value numbers, dim / 2 of key scales, dim / 2 of value scales.
+ * Dims come in blocks of 32 that share a scale d; a number is n d with n = nibble - 8. With nb = dim / 32:
+ *     key    of row r, dim 32 b + 8 t + 2 j + h (t, j < 4; h < 2): bits 16 h + 4 j of 32-bit word (4 r + t) nb + b;
+ *     value  of row 8 p + 2 t + c, dim 32 u + 4 g + i (p, c < 2; t, i < 4; g < 8): bits 16 c + 4 i of word ((8 p + g) 4 + t) nb + u;
+ *     scales one byte c: (8 + c % 8) 2^(c / 8 - 18) for c >= 8, c 2^-17 below (c << 7 are the bits of d in binary16); the
+ *            keys' byte r nb + b, the values' byte (r / 2) 2 nb + 2 b + r % 2.
+ * That is 17/32 bytes a number. n d is exact in MQ_F16 and MQ_BF16. The writer below makes n = -7 .. 7 and c <= 191 (d <= 480);
+ * a cache made otherwise may have n = -8 and must keep c <= 191 in rows that are read.
+ * dim: 64, 96, 128 or 256; page_rows: a power of two, 16 .. 1024; page_stride: bytes from page to page, a multiple of 16 of
+ * at least mq_kv4_page_bytes; width: entries of a sequence's table, width * page_rows < 2^31 - 255. Sequences may share pages.
+ * An entry outside 0 .. n_pages - 1 is no page: rows there read as zeros, and writes to them are left out. The table lies on the device and is
+ * read when the kernels run. The struct lives in host memory. MQ_ERR_SHAPE otherwise; pages and table 16-byte aligned.
+ */
+typedef struct mq_kv4 {
+    void* pages;
+    long long page_stride;
+    const int32_t* table;
+    long long table_stride;
+    int n;
+    int width;
+    int n_pages;
+    int page_rows;
+    int heads;
+    int dim;
+} mq_kv4;
+
+/* page_rows / 16 * heads * 17 dim (0 for sizes that are refused). */
+size_t mq_kv4_page_bytes(int page_rows, int heads, int dim);
+
+/*
+ * mq_qk_norm_rope_kv4 — mq_qk_norm_rope with the keys and values rounded to 4 bits: token m's go to row row[m] of sequence
+ * seq[m] (seq NULL: sequence 0). Rotated pairs are multiplied by rot_scale (contexts scaled beyond the trained length want
+ * one above 1; 1 otherwise), queries and keys alike:
+ *     a' = rot_scale (a cos t - b sin t),  b' = rot_scale (a sin t + b cos t).
+ * q_out: [M][Hq][D] in `type` (MQ_F16, MQ_BF16), rounded once. For each block of 32 dims of a key or value y: d is the least
+ * scale with 7 d >= max |y| (480 where that is more than 3360), n = rint(y / d), ties to even, within -7 .. 7. Both are decided for
+ * y as the formula gives it (where 32 bits do not tell, in 64), so what is written does not depend on the order of 32-bit sums.
+ * A token whose sequence, row or page there is none is skipped (its queries are not). Two tokens must not have the same place.
+ * q_out, the pages and q, k, v lie apart (MQ_ERR_SHAPE). row is required with k or v. Otherwise as mq_qk_norm_rope.
+ */
+int mq_qk_norm_rope_kv4(const mq_qkv* x, int type, float rot_scale, void* q_out, const mq_kv4* cache, const int32_t* seq,
+                        const int32_t* row, cudaStream_t stream);
+
+/*
+ * mq_kv4_read — rows in 16 bits: rows 0 .. len[i] - 1 of each sequence (as far as dst->cap and the table go) to the same rows
+ * of dst, exactly. dst: same n, heads and dim; apart from the pages. Its other rows are not written. len: int32 [n] on the
+ * device. A programmatic dependent launch.
+ */
+int mq_kv4_read(const mq_kv4* src, const int32_t* len, const mq_kv* dst, cudaStream_t stream);
+
+/*
+ * mq_attn_kv4 — mq_attn_prefix without a prefix, over such a cache:
+ *     out[b][t][h] = sum_j p_j v_j,   p = softmax_j(scale * q[b][t][h] . k_j),   j < len[b] - T + 1 + t.
+ * q: [B * T][Hq][D] in `type` (MQ_F16, MQ_BF16), row stride q_stride (a multiple of 8, at least Hq * D); cache->n == B; len: int32 [B] on
+ * the device, taken as 0 below 0 and as width * page_rows above it; out: [B * T][Hq][D] in `type` or MQ_F32; lse: f32 [B * T][Hq] or
+ * NULL. Rows at or past len are never used, whatever they hold. A query that sees no key gives zeros and an lse of -infinity.
+ * Arithmetic as mq_attn_prefix's with `type` for the caches' type: keys and values are exact in it, products and softmax f32,
+ * probabilities rounded to `type` (by at most 2^-11 or 2^-8 of themselves, or, in MQ_F16, 2^-32 of their row's largest). Deterministic.
+ * out overlaps neither q nor the pages. ws: at least mq_attn_kv4_ws_bytes(B, T, Hq, Hkv, D, width * page_rows) bytes, 16-byte
+ * aligned, nothing kept in it between calls; calls that run at the same time need one each. Where many query rows share a key head
+ * (dim 64 and 128) it holds rows in 16 bits: up to 1 GB, or one sequence's width * page_rows rows where that is more, and the call takes the
+ * batch in parts; otherwise a call is two launches. Counts as mq_attn_prefix's. B == 0 or T == 0 is a no-op.
+ * Waits are bounded (mq_device_status).
+ */
+size_t mq_attn_kv4_ws_bytes(int B, int T, int Hq, int Hkv, int D, int cap);
+int mq_attn_kv4(const void* q, int type, long long q_stride, int B, int T, int Hq, const mq_kv4* cache, const int32_t* len,
+                float scale, void* out, int out_type, float* lse, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Pages of any kind, all layers' at once: page p of layer l is the page_bytes bytes (a multiple of 16, up to 2^30) at
+ *     data + l * layer_stride + p * page_stride.
+ * Strides are multiples of 16 that keep all pages apart. data: 16-byte aligned device memory. Lives in host memory. */
+typedef struct mq_pool {
+    void* data;
+    long long page_bytes;
+    long long page_stride;
+    long long layer_stride;
+    int layers;
+    int n_pages;      /* up to 2^28 */
+    int page_rows;
+} mq_pool;
+
+/*
+ * mq_pages_next — m sequences from n: new sequence b goes on from old sequence from[b] (outside 0 .. n - 1: from nothing; from NULL:
+ * from b, and m == n), of which it keeps the first L = min(len[from[b]], keep[b]) rows (keep NULL: all), and is given place for add[b] more
+ * (add NULL: none):
+ *     table_out[b] = the ceil(L / page_rows) first entries of the old table, then new pages up to row L + add[b], then -1,
+ *     len_out[b] = L + add[b].
+ * Several sequences may go on from one (a fork: they share its pages), none (its pages are free), with fewer rows (a trim).
+ * Nobody counts references beside the tables: a page is held if a new sequence's kept entries name it, else free. New pages are the lowest free
+ * ones, handed out in the order of sequences and rows. Where a sequence with add[b] > 0 goes on inside a page (L % page_rows != 0)
+ * that others hold, it gets a new page and a copy (all layers); if all that hold it go on inside it, the first of them
+ * keeps it. Kept entries that name no page stay as they are, and rows are not given a page in place of one.
+ *     status[0] = pages that were missing. If any were, no sequence is given rows (forks and trims stand; len_out[b] = L);
+ *     status[1] = pages that are free now;
+ *     status[2] = sequences whose L + add[b] rows are more than the table holds: they are given none.
+ * table: int32 [n][width], table_out: int32 [m][width], len, len_out: int32 [n], [m]; from, keep, add: int32 [m]; status: int32 [3]; all on
+ * the device, 16-byte aligned. table_out may be table and len_out may be len; they must not overlap otherwise (MQ_ERR_SHAPE). Lengths are
+ * taken as 0 below 0 and as width * page_rows above it, keep and add as 0 below 0. n * width and width * page_rows below 2^31.
+ * ws: at least mq_pages_ws_bytes(pool, max(n, m), width) bytes, for calls that do not run at the same time. Two
+ * launches, programmatic dependent ones.
+ */
+size_t mq_pages_ws_bytes(const mq_pool* pool, int n, int width);
+int mq_pages_next(const mq_pool* pool, const int32_t* table, const int32_t* len, int n, int width, const int32_t* from,
+                  const int32_t* keep, const int32_t* add, int32_t* table_out, int32_t* len_out, int m, int32_t* status,
+                  void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * mq_pages_compact — closes the pool up: the U pages that rows below len lie on become pages 0 .. U - 1. Those below U stay;
+ * the others, in order, move (all layers) to the free places below U, in order.
+ *     where[p] = the new number of page p, -1 where no sequence holds it (int32 [n_pages]),
+ *     table_out[i][j] = where[table[i][j]] for the entries of rows below len[i] (as they are if they name no page), -1 past them,
+ *     live[0] = U.
+ * table_out may be table (no other overlap). Other arguments as for mq_pages_next (ws: mq_pages_ws_bytes(pool, n, width)).
+ */
+int mq_pages_compact(const mq_pool* pool, const int32_t* table, const int32_t* len, int n, int width, int32_t* table_out,
+                     int32_t* where, int32_t* live, void* ws, size_t ws_bytes, cudaStream_t stream);
 
 /*
  * mq_device_status — synchronizes `stream`, then returns MQ_OK if no kernel of

@@ -6,6 +6,7 @@
 #include <tuple>
 #include <utility>
 
+#include "kv4_calls.cuh"
 #include "mq_internal.cuh"
 
 namespace mq {
@@ -116,10 +117,11 @@ extern "C" const char* mq_status_str(int status) {
 }
 
 extern "C" int mq_device_status(cudaStream_t stream) {
-    unsigned gemm = 0, gemv = 0, attn = 0;
+    unsigned gemm = 0, gemv = 0, attn = 0, kv4 = 0;
     int rc = mq::take_gemm_device_error(stream, &gemm);
     if (rc == MQ_OK) rc = mq::take_gemv_device_error(stream, &gemv);
     if (rc == MQ_OK) rc = mq::take_attn_device_error(stream, &attn);
+    if (rc == MQ_OK) rc = attn::take_kv4_error(&kv4);
     if (rc != MQ_OK) return rc;
-    return (gemm | gemv | attn) ? MQ_ERR_DEVICE : MQ_OK;
+    return (gemm | gemv | attn | kv4) ? MQ_ERR_DEVICE : MQ_OK;
 }

@@ -11,21 +11,6 @@
 namespace attn {
 namespace {
 
-// One part of the keys, as the joining kernels see it.
-struct Part {
-    Pieces p;
-    int rows;      // per segment; 0: no such part
-    Plan plan;
-};
-
-struct JoinArgs {
-    Part prefix, own;
-    const int32_t* len;
-    int B, T, Hq, Hkv, group, own_cap, seg0;   // seg0: the own part's first segment
-    Out fin;
-    float* lse2;    // base 2, or nullptr
-};
-
 // Pieces of a row: `count` of them, `stride` rows apart, the first at row `first` of the pieces.
 struct Run {
     const Pieces* p;
@@ -560,6 +545,25 @@ bool valid_cut(const Cut& c, int B, int Hkv, bool scores) {
 }
 
 }  // namespace
+
+int launch_join(const JoinArgs& j, int D, int out_type, cudaStream_t stream) {
+    const long long rows = (long long)j.B * j.T * j.Hq;
+    auto join = [&](auto o) {
+        using O = decltype(o);
+        // few rows: eight warps each shorten the way through a row's pieces; many: they fill the GPU by themselves, and a row's
+        // few pieces leave most of eight warps idle. Whole call, one warp a row / eight: 400 rows 20.7 / 18.2 us, 560: 27.6 /
+        // 25.4, 640: 28.0 / 26.8, 840 of D 64: 14.5 / 17.9, 1024: 33.0 / 35.6, 1600: 24.7 / 31.3
+        const bool wide = rows <= 4LL * mq::num_sms();
+        auto kern = wide ? (D == 64 ? attn_join_kernel<O, 64, 8> : D == 96 ? attn_join_kernel<O, 96, 8>
+                            : D == 128 ? attn_join_kernel<O, 128, 8> : attn_join_kernel<O, 256, 8>)
+                         : (D == 64 ? attn_join_kernel<O, 64, 1> : D == 96 ? attn_join_kernel<O, 96, 1>
+                            : D == 128 ? attn_join_kernel<O, 128, 1> : attn_join_kernel<O, 256, 1>);
+        if (!mq::allow_smem(reinterpret_cast<const void*>(kern), 0)) return (int)MQ_ERR_LAUNCH;
+        return mq::launch_pdl(kern, dim3((unsigned)rows), dim3(wide ? 256 : 32), 0, stream, j);
+    };
+    return out_type == MQ_F32 ? join(float()) : out_type == MQ_F16 ? join(__half()) : join(__nv_bfloat16());
+}
+
 }  // namespace attn
 
 extern "C" size_t mq_attn_ws_bytes(int B, int T, int Hq, int Hkv, int D, int prefix_cap, int own_cap, int scores) {
@@ -571,11 +575,11 @@ extern "C" size_t mq_attn_ws_bytes(int B, int T, int Hq, int Hkv, int D, int pre
     return valid_cut(c, B, Hkv, scores && own_cap > 0) ? c.bytes : 0;
 }
 
-extern "C" int mq_attn_prefix(const void* q, long long q_stride, int B, int T, int Hq, const mq_kv* prefix,
-                              const mq_kv* own, const int32_t* own_len, float scale, void* out, int out_type,
-                              float* lse, const float* score, float* score_out, void* ws, size_t ws_bytes,
-                              cudaStream_t stream) {
-    using namespace attn;
+namespace attn {
+
+int call(const void* q, long long q_stride, int B, int T, int Hq, const mq_kv* prefix, const mq_kv* own, const int32_t* own_len,
+         float scale, void* out, int out_type, float* lse, const float* score, float* score_out, void* ws, size_t ws_bytes,
+         cudaStream_t stream, bool part) {
     if (B < 0 || T < 0) return MQ_ERR_SHAPE;
     const mq_kv* any = own ? own : prefix;
     if (!any) return MQ_ERR_NULL;
@@ -594,8 +598,8 @@ extern "C" int mq_attn_prefix(const void* q, long long q_stride, int B, int T, i
     if (!valid_counts(B, T, Hq, P, cap) || q_stride < (long long)Hq * D || q_stride % 8 != 0 || !std::isfinite(scale))
         return MQ_ERR_SHAPE;
     if (!q || !out || !ws || (own && !own_len) || (score == nullptr) != (score_out == nullptr)) return MQ_ERR_NULL;
-    if (!mq::aligned16(q) || !mq::aligned16(out) || !mq::aligned16(ws) || !mq::aligned16(own_len) ||
-        !mq::aligned16(lse) || !mq::aligned16(score) || !mq::aligned16(score_out))
+    if (!mq::aligned16(q) || !mq::aligned16(out) || !mq::aligned16(ws) || !mq::aligned16(score) || !mq::aligned16(score_out) ||
+        (!part && (!mq::aligned16(own_len) || !mq::aligned16(lse))))
         return MQ_ERR_ALIGN;
     const bool scores = score_out && cap > 0;
     Cut c = cut_of(B, T, Hq, Hkv, D, P, cap, scores);
@@ -673,21 +677,7 @@ extern "C" int mq_attn_prefix(const void* q, long long q_stride, int B, int T, i
     j.seg0 = prefix_segs(c.few);
     j.fin = fin;
     j.lse2 = lse2;
-    const dim3 grid((unsigned)((long long)B * T * Hq));
-    auto join = [&](auto o) {
-        using O = decltype(o);
-        // few rows: eight warps each shorten the way through a row's pieces; many: they fill the GPU by themselves, and a row's
-        // few pieces leave most of eight warps idle. Whole call, one warp a row / eight: 400 rows 20.7 / 18.2 us, 560: 27.6 /
-        // 25.4, 640: 28.0 / 26.8, 840 of D 64: 14.5 / 17.9, 1024: 33.0 / 35.6, 1600: 24.7 / 31.3
-        const bool wide = (long long)B * T * Hq <= 4LL * mq::num_sms();
-        auto kern = wide ? (D == 64 ? attn_join_kernel<O, 64, 8> : D == 96 ? attn_join_kernel<O, 96, 8>
-                            : D == 128 ? attn_join_kernel<O, 128, 8> : attn_join_kernel<O, 256, 8>)
-                         : (D == 64 ? attn_join_kernel<O, 64, 1> : D == 96 ? attn_join_kernel<O, 96, 1>
-                            : D == 128 ? attn_join_kernel<O, 128, 1> : attn_join_kernel<O, 256, 1>);
-        if (!mq::allow_smem(reinterpret_cast<const void*>(kern), 0)) return (int)MQ_ERR_LAUNCH;
-        return mq::launch_pdl(kern, grid, dim3(wide ? 256 : 32), 0, stream, j);
-    };
-    rc = out_type == MQ_F32 ? join(float()) : out_type == MQ_F16 ? join(__half()) : join(__nv_bfloat16());
+    rc = launch_join(j, D, out_type, stream);
     if (rc != MQ_OK || !scores) return rc;
     const int rows = T * j.group;
     if (rows > kScoreRowsFrom) {
@@ -705,4 +695,14 @@ extern "C" int mq_attn_prefix(const void* q, long long q_stride, int B, int T, i
                               score, score_out, T, Hq, Hkv, cap);
     };
     return cap % 4 == 0 ? score_call(attn_score_kernel<4>, 512) : score_call(attn_score_kernel<1>, 128);
+}
+
+}  // namespace attn
+
+extern "C" int mq_attn_prefix(const void* q, long long q_stride, int B, int T, int Hq, const mq_kv* prefix,
+                              const mq_kv* own, const int32_t* own_len, float scale, void* out, int out_type,
+                              float* lse, const float* score, float* score_out, void* ws, size_t ws_bytes,
+                              cudaStream_t stream) {
+    return attn::call(q, q_stride, B, T, Hq, prefix, own, own_len, scale, out, out_type, lse, score, score_out, ws, ws_bytes,
+                      stream, false);
 }

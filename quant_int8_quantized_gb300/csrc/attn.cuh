@@ -276,6 +276,29 @@ struct Out {
     int f32;       // out holds f32, not the caches' type
 };
 
+// One part of the keys, as the joining kernels see it.
+struct Part {
+    Pieces p;
+    int rows;      // per segment; 0: no such part
+    Plan plan;
+};
+
+struct JoinArgs {
+    Part prefix, own;
+    const int32_t* len;
+    int B, T, Hq, Hkv, group, own_cap, seg0;   // seg0: the own part's first segment
+    Out fin;
+    float* lse2;    // base 2, or nullptr
+};
+
+// The rows' pieces added up, rows written (attn.cu).
+int launch_join(const JoinArgs& j, int D, int out_type, cudaStream_t stream);
+
+// mq_attn_prefix. part: of a batch, so own_len and lse may begin at any sequence's.
+int call(const void* q, long long q_stride, int B, int T, int Hq, const mq_kv* prefix, const mq_kv* own, const int32_t* own_len,
+         float scale, void* out, int out_type, float* lse, const float* score, float* score_out, void* ws, size_t ws_bytes,
+         cudaStream_t stream, bool part);
+
 constexpr float kLn2 = 0.6931471805599453f;
 
 // Maxima (base 2, scaled) whose last place is no longer small beside the exponents taken against them. (-infinity: no key seen.)

@@ -1,0 +1,537 @@
+// Rows of a 4-bit cache (kv4.cuh): head norms and rotation of a layer's projections with the keys and values rounded
+// to 4 bits in the same pass, and rows read back in 16 bits.
+//
+// Writing. As in qk_rope.cu a thread holds four pairs of a head, a head is D / 8 lanes of an aligned group of 8, 16 or 32, and
+// cos and sin come once per token out of shared memory. Keys and values then change hands through shared memory so that a
+// lane has the eight dims of one word of the page, four lanes a block of 32 dims: two shuffles find its largest
+// magnitude a, the scale is the least one with 7 d >= a, the numbers are rint(y / d).
+// That rounding is decided for y as the formula has it, not as 32 bits do: y is off by at most 2^-19 of the head's
+// largest magnitude (norm: 8 fused additions, 5 levels of shuffles, square root, division, two products, less than 11 units of
+// 2^-24; cos and sin less than 4, the rotation's products and sum and rot_scale 4; a pair is at most sqrt(2) times the
+// largest), and where a border lies within that of y or of a, the warp computes its heads again in 64 bits. So the
+// bytes do not depend on how 32-bit sums are ordered. One head in some sixty is near a border.
+// Values are the inputs themselves: their borders (k + 1/2) d are exact in 32 bits.
+// Bound: HBM, 4 bytes read an element, 2 written (q) or 17/32.
+
+#include <cmath>
+
+#include "kv4.cuh"
+
+namespace kv4 {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr float kOff = 1.9073486328125e-06f;      // 2^-19, see above
+
+struct FillArgs {
+    const float* x[3];          // q, k, v (NULL: left out)
+    long long stride[3];
+    const float* w[2];
+    const float* inv_freq;
+    const uint8_t* axis;
+    const int32_t* pos;
+    const int32_t* seq;
+    const int32_t* row;
+    void* q_out;
+    Cache c;
+    int M, D, n_pairs, n_axes;
+    int h0, h1, h2;             // rows of a token: [0, h0) q, [h0, h1) k, [h1, h2) v
+    float eps, rot_scale;
+};
+
+// cos and sin of pos * freq, times `by`; the turn is taken out in 64 bits (qk_rope.cu).
+__device__ __forceinline__ float2 turn(int pos, float freq, float by) {
+    const double t = (double)pos * (double)freq * 0.31830988618379067154;   // in half turns
+    float s, c;
+    sincospif((float)(t - 2.0 * rint(0.5 * t)), &s, &c);
+    return make_float2(c * by, s * by);
+}
+
+// The least code whose 7 d is `a` or more.
+__device__ __forceinline__ int code_of(float a) {
+    if (!(a < 3360.0f)) return kMostCode;
+    const float t = a * (1.0f / 7.0f);
+    int c = t < 6.103515625e-05f ? (int)ceilf(t * 131072.0f) : (int)((__float_as_uint(t) + 0xfffffu) >> 20) - 896;
+    if (c > 0 && 7.0f * scale_of(c - 1) >= a) --c;
+    else if (7.0f * scale_of(c) < a) ++c;
+    return c;
+}
+__device__ __forceinline__ int code_of(double a) {
+    if (!(a < 3360.0)) return kMostCode;
+    int c = code_of((float)a);
+    if (c > 0 && 7.0 * (double)scale_of(c - 1) >= a) --c;
+    else if (7.0 * (double)scale_of(c) < a && c < kMostCode) ++c;
+    return c;
+}
+
+// rint(y / d), ties to even, and the rest y - n d (exact: both have few bits, and it is no longer than y).
+__device__ __forceinline__ float nearest(float y, float d, float inv, float& rest) {
+    float k = rintf(y * inv);
+    k = fminf(fmaxf(k, -8.0f), 8.0f);
+    rest = fmaf(-k, d, y);
+    const float over = 2.0f * fabsf(rest);
+    if (over > d || (over == d && ((int)k & 1))) k += copysignf(1.0f, rest);
+    return fminf(fmaxf(k, -7.0f), 7.0f);
+}
+
+// LG lanes a head. VEC: pairs come in fours (n_pairs % 4 == 0); otherwise each of a thread's
+// four pairs or eight plain numbers is placed by itself.
+template <typename T, int LG, bool INTER, bool VEC>
+__global__ void __launch_bounds__(kThreads) fill_kernel(const FillArgs a) {
+    extern __shared__ float2 s_turn[];                 // [n_pairs]
+    __shared__ double s_row[kThreads / LG][LG * 8];    // a head's row on its way from pairs to words
+    mq_grid_release();
+    mq_grid_wait();
+    const int m = blockIdx.x;                          // the token
+    const int lane = threadIdx.x % LG, group = threadIdx.x / LG;
+    const int D = a.D, n = a.n_pairs;
+    const int rows = a.h2;
+    const int r_first = blockIdx.y * (kThreads / LG) + group, r_step = gridDim.y * (kThreads / LG);
+
+    struct Row {
+        int what, h, np;
+        float v[8];
+    };
+    // Where element i of this thread lies (VEC: 0 .. 3 from low(np) on, 4 .. 7 from high(np); see qk_rope.cu).
+    auto place = [&](int np, int i) {
+        const int p = lane * 4 + i / 2;
+        if (p >= np) return lane * 8 + i;
+        return INTER ? 2 * p + (i & 1) : p + (i & 1) * np;
+    };
+    auto low = [&](int np) { return INTER || lane * 4 >= np ? lane * 8 : lane * 4; };
+    auto high = [&](int np) { return INTER || lane * 4 >= np ? lane * 8 + 4 : np + lane * 4; };
+    auto at = [&](int np, int i) { return VEC ? (i < 4 ? low(np) + i : high(np) + i - 4) : place(np, i); };
+    auto fetch = [&](int r, Row& x) {
+        const bool live = r < rows && lane * 8 < D;
+        const int hr = live ? r : 0;
+        x.what = hr < a.h0 ? 0 : hr < a.h1 ? 1 : 2;
+        x.h = hr - (x.what == 0 ? 0 : x.what == 1 ? a.h0 : a.h1);
+        x.np = x.what == 2 ? 0 : n;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x.v[i] = 0.0f;
+        if (!live) return;
+        const float* p = a.x[x.what] + (long long)m * a.stride[x.what] + (long long)x.h * D;
+        if constexpr (VEC) {
+            const float4 u0 = __ldca(reinterpret_cast<const float4*>(p + low(x.np)));
+            const float4 u1 = __ldca(reinterpret_cast<const float4*>(p + high(x.np)));
+            x.v[0] = u0.x, x.v[1] = u0.y, x.v[2] = u0.z, x.v[3] = u0.w;
+            x.v[4] = u1.x, x.v[5] = u1.y, x.v[6] = u1.z, x.v[7] = u1.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x.v[i] = __ldca(p + place(x.np, i));
+        }
+    };
+    Row now;
+    fetch(r_first, now);             // on its way while the turns are computed
+
+    auto angle = [&](int p, float& freq) {
+        const int ax = a.axis ? min((int)a.axis[p], a.n_axes - 1) : 0;
+        freq = a.inv_freq[p];
+        return a.pos[(long long)ax * a.M + m];
+    };
+    for (int p = threadIdx.x; p < n; p += kThreads) {
+        float freq;
+        const int pos = angle(p, freq);
+        s_turn[p] = turn(pos, freq, a.rot_scale);
+    }
+    int page = -1, row = -1;
+    if (a.h2 > a.h0) {
+        const int seq = a.seq ? __ldca(a.seq + m) : 0;
+        row = __ldca(a.row + m);
+        if ((unsigned)seq < (unsigned)a.c.n && row >= 0 && row >> a.c.shift < a.c.width) page = a.c.page(seq, row);
+    }
+    __syncthreads();
+    for (int r = r_first; r - group < rows; r += r_step) {
+        Row next;
+        fetch(r + r_step, next);     // (past the last row: nothing)
+        const bool live = r < rows && lane * 8 < D;
+        const int what = r < rows ? now.what : 0, h = now.h, np = now.np;
+        const int lo = low(np), hi = high(np);
+        const bool rot = lane * 4 < np;
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = now.v[i];
+        now = next;
+        const float* w = what == 2 ? nullptr : a.w[what];
+        float ss = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
+#pragma unroll
+        for (int o = LG / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if (w && live) {
+            const float sc = 1.0f / sqrtf(ss / (float)D + a.eps);
+            if constexpr (VEC) {
+                const float4 w0 = __ldg(reinterpret_cast<const float4*>(w + lo));
+                const float4 w1 = __ldg(reinterpret_cast<const float4*>(w + hi));
+                v[0] *= sc * w0.x, v[1] *= sc * w0.y, v[2] *= sc * w0.z, v[3] *= sc * w0.w;
+                v[4] *= sc * w1.x, v[5] *= sc * w1.y, v[6] *= sc * w1.z, v[7] *= sc * w1.w;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] *= sc * __ldg(w + place(np, i));
+            }
+        }
+        auto rotate = [](float& p, float& q, float2 t) {
+            const float u = p * t.x - q * t.y;
+            q = p * t.y + q * t.x;
+            p = u;
+        };
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (lane * 4 + i < np) {
+                if constexpr (VEC && !INTER) rotate(v[i], v[4 + i], s_turn[lane * 4 + i]);
+                else rotate(v[2 * i], v[2 * i + 1], s_turn[lane * 4 + i]);
+            }
+        if (live && what == 0) {
+            T* y = reinterpret_cast<T*>(a.q_out) + ((long long)m * a.h0 + h) * D;
+            if constexpr (VEC) {
+                const uint2 y0 = make_uint2(mq_pack2<T>(v[0], v[1]), mq_pack2<T>(v[2], v[3]));
+                const uint2 y1 = make_uint2(mq_pack2<T>(v[4], v[5]), mq_pack2<T>(v[6], v[7]));
+                if (INTER || !rot) {
+                    *reinterpret_cast<uint4*>(y + lo) = make_uint4(y0.x, y0.y, y1.x, y1.y);
+                } else {
+                    *reinterpret_cast<uint2*>(y + lo) = y0;
+                    *reinterpret_cast<uint2*>(y + hi) = y1;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[place(np, i)] = T(v[i]);
+            }
+        }
+        if (__all_sync(0xffffffffu, what == 0) || page < 0) continue;      // (the page is the token's: the same for all)
+
+        // ------------------------------------------------------------ keys and values to words and scales
+        float* row32 = reinterpret_cast<float*>(s_row[group]);
+        if (live && what == 1) {
+            if constexpr (VEC) {
+                *reinterpret_cast<float4*>(row32 + lo) = make_float4(v[0], v[1], v[2], v[3]);
+                *reinterpret_cast<float4*>(row32 + hi) = make_float4(v[4], v[5], v[6], v[7]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) row32[place(np, i)] = v[i];
+            }
+        }
+        __syncwarp();
+        if (live && what == 1) {
+            const float4 u0 = *reinterpret_cast<const float4*>(row32 + lane * 8);
+            const float4 u1 = *reinterpret_cast<const float4*>(row32 + lane * 8 + 4);
+            v[0] = u0.x, v[1] = u0.y, v[2] = u0.z, v[3] = u0.w;
+            v[4] = u1.x, v[5] = u1.y, v[6] = u1.z, v[7] = u1.w;
+        }
+        __syncwarp();
+        float most = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(v[i]));
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));          // of the block of 32 dims
+        float all = most;
+#pragma unroll
+        for (int o = 4; o < LG; o <<= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, o));
+        const bool exact = what != 1 || (!w && np == 0);                    // v is what there is to round
+        const float off = exact ? 0.0f : all * kOff;
+        int code = code_of(most);
+        float d = scale_of(code);
+        const float inv = d > 0.0f ? 1.0f / d : 0.0f;
+        bool near = !exact && most - off <= 3360.0f &&
+                    (7.0f * d < most + off || (code > 0 && 7.0f * scale_of(code - 1) >= most - off));
+        float num[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float rest;
+            num[i] = nearest(v[i], d, inv, rest);
+            near |= !exact && fabsf(fabsf(rest) - 0.5f * d) <= off;
+        }
+        if (__any_sync(0xffffffffu, near && live)) {
+            Row x;
+            fetch(r, x);
+            double y[8], sum = 0.0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                y[i] = x.v[i];
+                sum += y[i] * y[i];
+            }
+#pragma unroll
+            for (int o = LG / 2; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            double* row64 = s_row[group];
+            if (live && what == 1) {
+                if (w) {
+                    const double sc = 1.0 / sqrt(sum / D + (double)a.eps);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) y[i] *= sc * (double)w[at(np, i)];
+                }
+#pragma unroll 1
+                for (int i = 0; i < 4; ++i) {
+                    const int p = lane * 4 + i;
+                    if (p >= np) break;
+                    float freq;
+                    const int pos = angle(p, freq);
+                    double sn, cs;
+                    sincos((double)pos * (double)freq, &sn, &cs);
+                    cs *= (double)a.rot_scale;
+                    sn *= (double)a.rot_scale;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)       // (constant places: y stays in registers)
+                        if (k == i) {
+                            double &p0 = VEC && !INTER ? y[k] : y[2 * k], &p1 = VEC && !INTER ? y[4 + k] : y[2 * k + 1];
+                            const double u = p0 * cs - p1 * sn;
+                            p1 = p0 * sn + p1 * cs;
+                            p0 = u;
+                        }
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) row64[at(np, i)] = y[i];
+            }
+            __syncwarp();
+            double top = 0.0;
+            if (live && what == 1)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    y[i] = row64[lane * 8 + i];
+                    top = fmax(top, fabs(y[i]));
+                }
+            __syncwarp();
+            top = fmax(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmax(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            if (live && what == 1) {
+                code = code_of(top);
+                d = scale_of(code);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) num[i] = d > 0.0f ? (float)fmin(fmax(rint(y[i] / (double)d), -7.0), 7.0) : 0.0f;
+            }
+        }
+        if (!live || what == 0) continue;
+        uint32_t nib[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) nib[i] = (uint32_t)((int)num[i] + 8);
+        const int nb = D / 32, b = lane / 4, t = lane % 4, in = row & (kBlockRows - 1);
+        uint8_t* block = a.c.block(page, h, row, block_bytes(D));
+        if (what == 1) {
+            uint32_t word = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) word |= nib[i] << (16 * (i & 1) + 4 * (i >> 1));
+            reinterpret_cast<uint32_t*>(block)[(4 * in + t) * nb + b] = word;
+        } else {
+            uint16_t* half = reinterpret_cast<uint16_t*>(block + value_at(D));
+            const int p = in >> 3, tt = (in >> 1) & 3, c = in & 1;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const uint32_t u = nib[4 * k] | nib[4 * k + 1] << 4 | nib[4 * k + 2] << 8 | nib[4 * k + 3] << 12;
+                half[2 * (((8 * p + 2 * t + k) * 4 + tt) * nb + b) + c] = (uint16_t)u;
+            }
+        }
+        if (t == 0) block[what == 1 ? key_scale_at(D) + in * nb + b : value_scale_at(D) + (in >> 1) * 2 * nb + 2 * b + (in & 1)] = (uint8_t)code;
+    }
+}
+
+template <typename T, int LG>
+int launch_fill(const FillArgs& a, bool inter, dim3 grid, size_t smem, cudaStream_t stream) {
+    const bool vec = a.n_pairs % 4 == 0;
+    auto kern = vec ? (inter ? fill_kernel<T, LG, true, true> : fill_kernel<T, LG, false, true>)
+                    : (inter ? fill_kernel<T, LG, true, false> : fill_kernel<T, LG, false, false>);
+    return mq::launch_pdl(kern, grid, dim3(kThreads), smem, stream, a);
+}
+
+// ---------------------------------------------------------------------------------------------- rows in 16 bits
+
+struct ReadArgs {
+    Cache c;
+    const int32_t* len;
+    void* k;
+    void* v;
+    long long seq_stride, row_stride, head_stride;
+    int cap, chunks;        // rows at most of a sequence; chunks of kChunk blocks of them
+    long long units;        // sequences x heads x chunks
+};
+constexpr int kChunk = 4, kReadWarps = 4;
+
+// A warp takes 64 rows of a head, 16 at a time: the words that a lane loads are those that the products' operands are
+// made of, so eight lanes' stores fill a row's 64 bytes.
+template <typename T, int D>
+__global__ void __launch_bounds__(32 * kReadWarps) read_kernel(const ReadArgs a) {
+    constexpr int nb = D / 32;
+    mq_grid_release();
+    mq_grid_wait();
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const long long warps = (long long)gridDim.x * kReadWarps;
+    for (long long unit = (long long)blockIdx.x * kReadWarps + (threadIdx.x >> 5); unit < a.units; unit += warps) {
+        const long long sh = unit / a.chunks;
+        const int chunk = (int)(unit - sh * a.chunks), seq = (int)(sh / a.c.heads), h = (int)(sh - (long long)seq * a.c.heads);
+        const int len = min(max(__ldca(a.len + seq), 0), a.cap);
+        T* k_to = reinterpret_cast<T*>(a.k) + seq * a.seq_stride + h * a.head_stride;
+        T* v_to = reinterpret_cast<T*>(a.v) + seq * a.seq_stride + h * a.head_stride;
+#pragma unroll 1
+        for (int i = 0; i < kChunk; ++i) {
+            const int row0 = (chunk * kChunk + i) * kBlockRows;
+            if (row0 >= len) break;
+            const int page = a.c.page(seq, row0);
+            uint32_t kw[2][nb], vw[2][nb], ks[2][(nb + 3) / 4], vs[2][nb / 2 + nb % 2];
+            if (page >= 0) {
+                const uint8_t* block = a.c.block(page, h, row0, block_bytes(D));
+                auto from = [](const uint8_t* p) {
+                    return [p](auto type, int i) { return __ldca(reinterpret_cast<const decltype(type)*>(p) + i); };
+                };
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    words<nb>(from(block + (p * 32 + lane) * nb * 4), kw[p]);
+                    words<nb>(from(block + value_at(D) + (p * 32 + lane) * nb * 4), vw[p]);
+                    bytes<nb>(from(block + key_scale_at(D) + (g + 8 * p) * nb), ks[p]);
+                    bytes<2 * nb>(from(block + value_scale_at(D) + (4 * p + t) * 2 * nb), vs[p]);
+                }
+            } else {
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+#pragma unroll
+                    for (int b = 0; b < nb; ++b) kw[p][b] = vw[p][b] = 0;
+#pragma unroll
+                    for (int b = 0; b < (nb + 3) / 4; ++b) ks[p][b] = 0;
+#pragma unroll
+                    for (int b = 0; b < nb / 2 + nb % 2; ++b) vs[p][b] = 0;
+                }
+            }
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const int kr = row0 + g + 8 * p, vr = row0 + 8 * p + 2 * t;
+#pragma unroll
+                for (int b = 0; b < nb; ++b) {
+                    uint32_t x[4];
+                    numbers(kw[p][b], Scale<T>::of(twice(ks[p], b)), x);
+                    if (kr < len)
+                        *reinterpret_cast<uint4*>(k_to + kr * a.row_stride + 32 * b + 8 * t) = make_uint4(x[0], x[1], x[2], x[3]);
+                    numbers(vw[p][b], Scale<T>::of(both(vs[p], b)), x);
+                    T* to = v_to + vr * a.row_stride + 32 * b + 4 * g;
+                    if (vr < len)
+                        *reinterpret_cast<uint2*>(to) = make_uint2(__byte_perm(x[0], x[1], 0x5410), __byte_perm(x[2], x[3], 0x5410));
+                    if (vr + 1 < len)
+                        *reinterpret_cast<uint2*>(to + a.row_stride) =
+                            make_uint2(__byte_perm(x[0], x[1], 0x7632), __byte_perm(x[2], x[3], 0x7632));
+                }
+            }
+        }
+    }
+}
+
+}  // namespace
+
+int launch_read(const mq_kv4* src, const int32_t* len, const mq_kv* dst, cudaStream_t stream) {
+    ReadArgs a;
+    a.c = cache_of(src);
+    a.len = len;
+    a.k = dst->k;
+    a.v = dst->v;
+    a.seq_stride = dst->seq_stride;
+    a.row_stride = dst->row_stride;
+    a.head_stride = dst->head_stride;
+    const int held = src->width * src->page_rows;
+    a.cap = dst->cap < held ? dst->cap : held;
+    a.chunks = (a.cap + kChunk * kBlockRows - 1) / (kChunk * kBlockRows);
+    a.units = (long long)src->n * src->heads * a.chunks;
+    if (a.units == 0) return MQ_OK;
+    const long long blocks = (a.units + kReadWarps - 1) / kReadWarps, most = 16LL * mq::num_sms();
+    const dim3 grid((unsigned)(blocks < most ? blocks : most));
+    auto go = [&](auto t) {
+        using T = decltype(t);
+        auto kern = src->dim == 64 ? read_kernel<T, 64> : src->dim == 96 ? read_kernel<T, 96>
+                    : src->dim == 128 ? read_kernel<T, 128> : read_kernel<T, 256>;
+        return mq::launch_pdl(kern, grid, dim3(32 * kReadWarps), 0, stream, a);
+    };
+    return dst->type == MQ_F16 ? go(__half()) : go(__nv_bfloat16());
+}
+
+}  // namespace kv4
+
+extern "C" size_t mq_kv4_page_bytes(int page_rows, int heads, int dim) {
+    if (!kv4::valid_rows(page_rows) || !kv4::valid_dim(dim) || heads < 1) return 0;
+    return (size_t)(page_rows / 16) * heads * kv4::block_bytes(dim);
+}
+
+extern "C" int mq_qk_norm_rope_kv4(const mq_qkv* x, int type, float rot_scale, void* q_out, const mq_kv4* cache,
+                                   const int32_t* seq, const int32_t* row, cudaStream_t stream) {
+    using namespace kv4;
+    if (!x) return MQ_ERR_NULL;
+    int rc = check(cache, false);
+    if (rc != MQ_OK) return rc;
+    if (type != MQ_F16 && type != MQ_BF16) return MQ_ERR_TYPE;
+    const int D = cache->dim, Hkv = cache->heads;
+    if (x->M < 0 || x->Hq < 0 || x->n_pairs < 0 || 2 * x->n_pairs > D || !std::isfinite(rot_scale)) return MQ_ERR_SHAPE;
+    if (x->n_pairs > 0 && (x->n_axes < 1 || x->n_axes > 8)) return MQ_ERR_SHAPE;
+    if (x->M == 0) return MQ_OK;
+    const bool cached = x->k || x->v;
+    const float* src[3] = {x->q, x->k, x->v};
+    const long long st[3] = {x->q_stride, x->k_stride, x->v_stride};
+    const int heads[3] = {x->q ? x->Hq : 0, x->k ? Hkv : 0, x->v ? Hkv : 0};
+    if ((long long)heads[0] + heads[1] + heads[2] > 0x7fffff) return MQ_ERR_SHAPE;
+    for (int i = 0; i < 3; ++i)
+        if (src[i]) {
+            if (st[i] < (long long)heads[i] * D || st[i] % 4 != 0) return MQ_ERR_SHAPE;
+            if (!mq::aligned16(src[i])) return MQ_ERR_ALIGN;
+        }
+    if (x->n_pairs > 0 && (!x->inv_freq || !x->pos)) return MQ_ERR_NULL;
+    if ((heads[0] > 0 && !q_out) || (cached && !row)) return MQ_ERR_NULL;
+    if (cached) {
+        rc = check(cache, true);
+        if (rc != MQ_OK) return rc;
+    }
+    if (!mq::aligned16(q_out) || !mq::aligned16(x->wq) || !mq::aligned16(x->wk) || !mq::aligned16(x->inv_freq) ||
+        !mq::aligned16(x->axis) || !mq::aligned16(x->pos) || !mq::aligned16(seq) || !mq::aligned16(row))
+        return MQ_ERR_ALIGN;
+    const long long pool = cached ? cache->page_stride * cache->n_pages : 0, q_bytes = 2LL * x->M * heads[0] * D;
+    for (int i = 0; i < 3; ++i)   // a block's output rows would lie over what others have yet to read
+        if (mq::rows_meet(src[i], x->M, 4 * st[i], 4LL * heads[i] * D, q_out, q_bytes) ||
+            mq::rows_meet(src[i], x->M, 4 * st[i], 4LL * heads[i] * D, cache->pages, pool))
+            return MQ_ERR_SHAPE;
+    if (mq::rows_meet(q_out, 1, q_bytes, q_bytes, cache->pages, pool)) return MQ_ERR_SHAPE;
+    rc = mq::check_arch();
+    if (rc != MQ_OK) return rc;
+    FillArgs a;
+    for (int i = 0; i < 3; ++i) {
+        a.x[i] = src[i];
+        a.stride[i] = st[i];
+    }
+    a.w[0] = x->wq;
+    a.w[1] = x->wk;
+    a.inv_freq = x->inv_freq;
+    a.axis = x->axis;
+    a.pos = x->pos;
+    a.seq = seq;
+    a.row = row;
+    a.q_out = q_out;
+    a.c = cache_of(cache);
+    a.M = x->M;
+    a.D = D;
+    a.n_pairs = x->n_pairs;
+    a.n_axes = x->n_axes;
+    a.h0 = heads[0];
+    a.h1 = a.h0 + heads[1];
+    a.h2 = a.h1 + heads[2];
+    a.eps = x->eps;
+    a.rot_scale = rot_scale;
+    if (a.h2 == 0) return MQ_OK;
+    const int lg = D <= 64 ? 8 : D <= 128 ? 16 : 32, per = kThreads / lg;
+    const int passes = (a.h2 + per - 1) / per;
+    const dim3 grid(x->M, x->M >= 2 * mq::num_sms() ? 1 : passes < 65535 ? passes : 65535);
+    const size_t smem = (size_t)a.n_pairs * sizeof(float2);
+    const bool inter = x->interleaved != 0;
+    auto go = [&](auto t) {
+        using T = decltype(t);
+        return lg == 8 ? launch_fill<T, 8>(a, inter, grid, smem, stream)
+               : lg == 16 ? launch_fill<T, 16>(a, inter, grid, smem, stream)
+                          : launch_fill<T, 32>(a, inter, grid, smem, stream);
+    };
+    return type == MQ_F16 ? go(__half()) : go(__nv_bfloat16());
+}
+
+extern "C" int mq_kv4_read(const mq_kv4* src, const int32_t* len, const mq_kv* dst, cudaStream_t stream) {
+    using namespace kv4;
+    int rc = check(src, true);
+    if (rc == MQ_OK) rc = mq::check_kv(dst, true);
+    if (rc != MQ_OK) return rc;
+    if (dst->n != src->n || dst->heads != src->heads || dst->dim != src->dim) return MQ_ERR_SHAPE;
+    if (src->n == 0 || src->width == 0 || dst->cap == 0) return MQ_OK;
+    if (!len) return MQ_ERR_NULL;
+    if (!mq::aligned16(len)) return MQ_ERR_ALIGN;
+    const long long span = 2 * mq::kv_span(dst), pool = src->page_stride * src->n_pages;
+    if (mq::rows_meet(dst->k, 1, span, span, src->pages, pool) || mq::rows_meet(dst->v, 1, span, span, src->pages, pool))
+        return MQ_ERR_SHAPE;
+    rc = mq::check_arch();
+    if (rc != MQ_OK) return rc;
+    return launch_read(src, len, dst, stream);
+}

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import math
 import os
 
 import torch
@@ -26,6 +27,8 @@ EXPORTED = ["mq_plane_bytes", "mq_q4k_row_bytes", "mq_q6k_row_bytes", "mq_q6k_pa
             "mq_q5k_row_bytes", "mq_q4_0_row_bytes", "mq_q4_1_row_bytes", "mq_gemv_q5k", "mq_gemv_q4_0",
             "mq_gemv_q4_1", "mq_gemm_q4_0", "mq_gemm_q4_1", "mq_gemv_q6k_packed", "mq_gemm_q6k_static", "mq_gemm_q4k_pair",
             "mq_qk_norm_rope", "mq_attn_ws_bytes", "mq_attn_prefix", "mq_kv_evict",
+            "mq_kv4_page_bytes", "mq_qk_norm_rope_kv4", "mq_kv4_read", "mq_attn_kv4_ws_bytes", "mq_attn_kv4",
+            "mq_pages_ws_bytes", "mq_pages_next", "mq_pages_compact",
             "mq_device_status", "mq_status_str"]
 
 
@@ -52,6 +55,18 @@ class CQKV(ctypes.Structure):
                [(n, ctypes.c_longlong) for n in ("q_stride", "k_stride", "v_stride")] + \
                [(n, ctypes.c_void_p) for n in ("wq", "wk", "inv_freq", "axis", "pos")] + \
                [(n, ctypes.c_int) for n in ("M", "Hq", "n_pairs", "n_axes", "interleaved")] + [("eps", ctypes.c_float)]
+
+
+class CKV4(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("page_stride", ctypes.c_longlong), ("table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_longlong)] + \
+               [(n, ctypes.c_int) for n in ("n", "width", "n_pages", "page_rows", "heads", "dim")]
+
+
+class CPool(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("page_bytes", ctypes.c_longlong), ("page_stride", ctypes.c_longlong),
+                ("layer_stride", ctypes.c_longlong), ("layers", ctypes.c_int), ("n_pages", ctypes.c_int),
+                ("page_rows", ctypes.c_int)]
 
 
 _lib = None
@@ -102,6 +117,14 @@ def _load(path: str) -> ctypes.CDLL:
         "mq_attn_prefix": (i, [vp, ctypes.c_longlong, i, i, i, ctypes.POINTER(CKV), ctypes.POINTER(CKV), vp, f, vp, i,
                                vp, vp, vp, vp, sz, vp]),
         "mq_kv_evict": (i, [ctypes.POINTER(CKV), vp, vp, i, i, ctypes.POINTER(CKV), vp, vp, vp, vp]),
+        "mq_kv4_page_bytes": (sz, [i, i, i]),
+        "mq_qk_norm_rope_kv4": (i, [ctypes.POINTER(CQKV), i, f, vp, ctypes.POINTER(CKV4), vp, vp, vp]),
+        "mq_kv4_read": (i, [ctypes.POINTER(CKV4), vp, ctypes.POINTER(CKV), vp]),
+        "mq_attn_kv4_ws_bytes": (sz, [i, i, i, i, i, i]),
+        "mq_attn_kv4": (i, [vp, i, ctypes.c_longlong, i, i, i, ctypes.POINTER(CKV4), vp, f, vp, i, vp, vp, sz, vp]),
+        "mq_pages_ws_bytes": (sz, [ctypes.POINTER(CPool), i, i]),
+        "mq_pages_next": (i, [ctypes.POINTER(CPool), vp, vp, i, i, vp, vp, vp, vp, vp, i, vp, vp, sz, vp]),
+        "mq_pages_compact": (i, [ctypes.POINTER(CPool), vp, vp, i, i, vp, vp, vp, vp, sz, vp]),
         "mq_device_status": (i, [vp]),
         "mq_status_str": (ctypes.c_char_p, [i]),
     }
@@ -423,26 +446,20 @@ def _heads(t, name, M, D, heads=None):
     return t.data_ptr(), (st[0] if M > 1 else s[1] * D), s[1]
 
 
-def mq_qk_norm_rope(q, k, v, q_out, cache: KV, slot=None, pos=None, inv_freq=None, axis=None, wq=None, wk=None,
-                    eps: float = 1e-6, interleaved: bool = False, stream=None):
-    """Head norms of q and k, rotation by position, q to 16 bits and k, v into the cache rows slot
-    (include/mq.h). q: f32 [M, Hq, D]; k, v: f32 [M, Hkv, D] (any may be None; a token's heads are
-    contiguous, tokens at any stride); q_out: [M, Hq, D] of the cache's type; slot: int32 [M];
-    pos: int32 [M] or [n_axes, M]; inv_freq: f32 [n_pairs]; axis: uint8 [n_pairs]."""
-    if not isinstance(cache, KV):
-        raise TypeError("cache must be a KV")
+def _qkv(q, k, v, q_out, dtype, D, heads, pos, inv_freq, axis, wq, wk, eps, interleaved):
+    """The projections' struct and q_out's pointer."""
     first = q if q is not None else k if k is not None else v
     if first is None:
         raise ValueError("one of q, k and v is needed")
     if not isinstance(first, torch.Tensor):
         raise TypeError(f"{'q' if first is q else 'k' if first is k else 'v'} must be a torch.Tensor")
-    M, D = first.shape[0], cache.dim
+    M = first.shape[0]
     q_ptr, q_stride, Hq = _heads(q, "q", M, D)
-    k_ptr, k_stride, _ = _heads(k, "k", M, D, cache.heads)
-    v_ptr, v_stride, _ = _heads(v, "v", M, D, cache.heads)
-    out_ptr = slot_ptr = wq_ptr = wk_ptr = freq_ptr = axis_ptr = pos_ptr = None
+    k_ptr, k_stride, _ = _heads(k, "k", M, D, heads)
+    v_ptr, v_stride, _ = _heads(v, "v", M, D, heads)
+    out_ptr = wq_ptr = wk_ptr = freq_ptr = axis_ptr = pos_ptr = None
     if q is not None:
-        if _dev_tensor(q_out, cache.dtype, "q_out").numel() < M * Hq * D:
+        if _dev_tensor(q_out, dtype, "q_out").numel() < M * Hq * D:
             raise ValueError(f"q_out holds {q_out.numel()} elements, needs {M * Hq * D}")
         out_ptr = q_out.data_ptr()
     if wq is not None:
@@ -465,12 +482,24 @@ def mq_qk_norm_rope(q, k, v, q_out, cache: KV, slot=None, pos=None, inv_freq=Non
                 raise ValueError(f"axis must hold {n_pairs} entries")
             axis_ptr = axis.data_ptr()
         freq_ptr, pos_ptr = inv_freq.data_ptr(), pos.data_ptr()
+    return M, out_ptr, CQKV(q_ptr, k_ptr, v_ptr, q_stride, k_stride, v_stride, wq_ptr, wk_ptr, freq_ptr, axis_ptr, pos_ptr,
+                            M, Hq, n_pairs, n_axes, 1 if interleaved else 0, eps)
+
+
+def mq_qk_norm_rope(q, k, v, q_out, cache: KV, slot=None, pos=None, inv_freq=None, axis=None, wq=None, wk=None,
+                    eps: float = 1e-6, interleaved: bool = False, stream=None):
+    """Head norms of q and k, rotation by position, q to 16 bits and k, v into the cache rows slot
+    (include/mq.h). q: f32 [M, Hq, D]; k, v: f32 [M, Hkv, D] (any may be None; a token's heads are
+    contiguous, tokens at any stride); q_out: [M, Hq, D] of the cache's type; slot: int32 [M];
+    pos: int32 [M] or [n_axes, M]; inv_freq: f32 [n_pairs]; axis: uint8 [n_pairs]."""
+    if not isinstance(cache, KV):
+        raise TypeError("cache must be a KV")
+    M, out_ptr, x = _qkv(q, k, v, q_out, cache.dtype, cache.dim, cache.heads, pos, inv_freq, axis, wq, wk, eps, interleaved)
+    slot_ptr = None
     if slot is not None:
         if _dev_tensor(slot, torch.int32, "slot").numel() != M:
             raise ValueError(f"slot must hold {M} entries")
         slot_ptr = slot.data_ptr()
-    x = CQKV(q_ptr, k_ptr, v_ptr, q_stride, k_stride, v_stride, wq_ptr, wk_ptr, freq_ptr, axis_ptr, pos_ptr, M, Hq,
-             n_pairs, n_axes, 1 if interleaved else 0, eps)
     _check((_lib or lib()).mq_qk_norm_rope(ctypes.byref(x), out_ptr, cache._ref, slot_ptr, _stream(stream)),
            "mq_qk_norm_rope")
     return q_out
@@ -578,6 +607,239 @@ def mq_kv_evict(src: KV, length: torch.Tensor, score: torch.Tensor, keep: int, r
                                        length_out.data_ptr(), score_out_ptr, index.data_ptr(), _stream(stream)),
            "mq_kv_evict")
     return dst
+
+
+# ---------------------------------------------------------------- keys and values in 4 bits, on pages
+
+class KV4:
+    """Keys and values of n sequences in 4 bits (include/mq.h, mq_kv4): pages uint8 [n_pages, page bytes] (a page's bytes
+    contiguous, at least mq_kv4_page_bytes), table int32 [n, width] (a row's entries contiguous), on the same device."""
+
+    def __init__(self, pages: torch.Tensor, table: torch.Tensor, page_rows: int, heads: int, dim: int):
+        for t, dtype, name in ((pages, torch.uint8, "pages"), (table, torch.int32, "table")):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{name} must be a torch.Tensor")
+            if t.device.type != "cuda":
+                raise ValueError(f"{name} must be a CUDA tensor")
+            if t.dtype is not dtype:
+                raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+            if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+                raise ValueError(f"{name} must have two axes, the last one contiguous")
+        if pages.device != table.device:
+            raise ValueError("pages and table must be on the same device")
+        need = mq_kv4_page_bytes(page_rows, heads, dim)
+        if need == 0:
+            raise ValueError(f"no page of {page_rows} rows of {heads} heads of {dim}")
+        if pages.shape[1] < need:
+            raise ValueError(f"a page holds {pages.shape[1]} bytes, needs {need}")
+        self.pages, self.table, self.page_rows, self.heads, self.dim = pages, table, int(page_rows), int(heads), int(dim)
+        self.n, self.width = (int(x) for x in table.shape)
+        self.n_pages, self.cap = int(pages.shape[0]), self.width * self.page_rows
+        # an axis of one step has no stride that matters
+        self._c = CKV4(pages.data_ptr(), pages.stride(0) if self.n_pages > 1 else (need + 15) // 16 * 16, table.data_ptr(),
+                       table.stride(0) if self.n > 1 else self.width, self.n, self.width, self.n_pages, self.page_rows,
+                       self.heads, self.dim)
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def empty(cls, n: int, width: int, n_pages: int, heads: int, dim: int, page_rows: int = 64, device="cuda") -> "KV4":
+        """A pool of n_pages pages and n empty table rows of `width` entries (-1: no page)."""
+        return cls(torch.empty((n_pages, mq_kv4_page_bytes(page_rows, heads, dim)), dtype=torch.uint8, device=device),
+                   torch.full((n, width), -1, dtype=torch.int32, device=device), page_rows, heads, dim)
+
+
+def mq_kv4_page_bytes(page_rows: int, heads: int, dim: int) -> int:
+    return int(lib().mq_kv4_page_bytes(page_rows, heads, dim))
+
+
+def rope_freq_scaled(n_pairs: int, base: float = 10000.0, factor: float = 1.0, trained: int = 32768, fast: float = 32.0,
+                     slow: float = 1.0, device="cuda"):
+    """(inv_freq, rot_scale) for contexts `factor` times the trained length: pairs that turn more than `fast` times over it keep
+    their frequency, those that turn less than `slow` times have it divided by factor, those between are blended by their number
+    of turns; rot_scale is 1 + log(factor) / 10."""
+    i = torch.arange(n_pairs, dtype=torch.float64)
+    freq, scale = float(base) ** (-i / n_pairs), 1.0
+    if factor > 1.0:
+        keep = ((trained * freq / (2 * math.pi) - slow) / (fast - slow)).clamp(0.0, 1.0)
+        freq, scale = freq * (keep + (1.0 - keep) / factor), 1.0 + 0.1 * math.log(factor)
+    return freq.to(torch.float32).to(device), scale
+
+
+def mq_qk_norm_rope_kv4(q, k, v, q_out, cache: KV4, seq=None, row=None, pos=None, inv_freq=None, axis=None, wq=None, wk=None,
+                        eps: float = 1e-6, interleaved: bool = False, rot_scale: float = 1.0, stream=None):
+    """mq_qk_norm_rope with k and v rounded to 4 bits, to row row[m] of sequence seq[m] of the cache (include/mq.h). q_out:
+    [M, Hq, D] float16 or bfloat16; seq (None: sequence 0), row: int32 [M]."""
+    if not isinstance(cache, KV4):
+        raise TypeError("cache must be a KV4")
+    if q is not None and not isinstance(q_out, torch.Tensor):
+        raise TypeError("q_out must be a torch.Tensor")
+    dtype = q_out.dtype if q is not None else torch.float16
+    if dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError(f"q_out must be float16 or bfloat16, got {dtype}")
+    M, out_ptr, x = _qkv(q, k, v, q_out, dtype, cache.dim, cache.heads, pos, inv_freq, axis, wq, wk, eps, interleaved)
+    seq_ptr = row_ptr = None
+    if seq is not None:
+        if _dev_tensor(seq, torch.int32, "seq").numel() != M:
+            raise ValueError(f"seq must hold {M} entries")
+        seq_ptr = seq.data_ptr()
+    if row is not None:
+        if _dev_tensor(row, torch.int32, "row").numel() != M:
+            raise ValueError(f"row must hold {M} entries")
+        row_ptr = row.data_ptr()
+    _check((_lib or lib()).mq_qk_norm_rope_kv4(ctypes.byref(x), _TYPES[dtype], rot_scale, out_ptr, cache._ref, seq_ptr, row_ptr,
+                                               _stream(stream)), "mq_qk_norm_rope_kv4")
+    return q_out
+
+
+def mq_kv4_read(src: KV4, length: torch.Tensor, dst: KV, stream=None) -> KV:
+    """Rows below length (int32 [n]) of each sequence of src to the same rows of dst, in 16 bits (include/mq.h)."""
+    if not isinstance(src, KV4):
+        raise TypeError("src must be a KV4")
+    if not isinstance(dst, KV):
+        raise TypeError("dst must be a KV")
+    if _dev_tensor(length, torch.int32, "length").numel() != src.n:
+        raise ValueError(f"length must hold {src.n} lengths")
+    _check((_lib or lib()).mq_kv4_read(src._ref, length.data_ptr(), dst._ref, _stream(stream)), "mq_kv4_read")
+    return dst
+
+
+def mq_attn_kv4_ws_bytes(B: int, T: int, Hq: int, Hkv: int, D: int, cap: int) -> int:
+    return int(lib().mq_attn_kv4_ws_bytes(B, T, Hq, Hkv, D, cap))
+
+
+def attn_kv4_workspace(B: int, T: int, Hq: int, Hkv: int, D: int, cap: int, device="cuda") -> torch.Tensor:
+    """A workspace for mq_attn_kv4 calls of these sizes on one stream (cap: width * page_rows)."""
+    return torch.empty((max(16, mq_attn_kv4_ws_bytes(B, T, Hq, Hkv, D, cap)),), dtype=torch.uint8, device=device)
+
+
+def mq_attn_kv4(q: torch.Tensor, cache: KV4, length: torch.Tensor, out: torch.Tensor, scale=None, lse=None, ws=None,
+                stream=None) -> torch.Tensor:
+    """Attention of q [B, T, Hq, D] over the first `length` (int32 [B]) rows of each sequence of a 4-bit cache, the last T of which
+    belong to the T queries (include/mq.h). out: [B, T, Hq, D] in q's type or f32; lse: f32 [B, T, Hq]; scale: 1 / sqrt(D) if
+    None; ws: attn_kv4_workspace(...), allocated on the call's stream for this call if None."""
+    if not isinstance(cache, KV4):
+        raise TypeError("cache must be a KV4")
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise TypeError("q must be a torch.Tensor [B, T, Hq, D]")
+    B, T, Hq, D = q.shape
+    dtype = q.dtype
+    if not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor")
+    if dtype is not torch.float16 and dtype is not torch.bfloat16:
+        raise TypeError(f"q must be float16 or bfloat16, got {dtype}")
+    if D != cache.dim:
+        raise ValueError(f"q's heads are {D} wide, the cache's {cache.dim}")
+    rows = B * T * Hq
+    st = q.stride()
+    if rows and (st[3] != 1 or (Hq > 1 and st[2] != D) or (B > 1 and T > 1 and st[0] != T * st[1])):
+        raise ValueError("q: a token's heads must be contiguous, and the tokens at one stride")
+    row = st[1] if T > 1 else st[0] if B > 1 else Hq * D
+    if not isinstance(out, torch.Tensor):
+        raise TypeError("out must be a torch.Tensor")
+    out_type = out.dtype
+    if out_type is not dtype and out_type is not torch.float32:
+        raise TypeError(f"out must be {dtype} or torch.float32, got {out_type}")
+    if _dev_tensor(out, out_type, "out").numel() < rows * D:
+        raise ValueError(f"out holds {out.numel()} elements, needs {rows * D}")
+    if _dev_tensor(length, torch.int32, "length").numel() != B:
+        raise ValueError(f"length must hold {B} lengths")
+    lse_ptr = None
+    if lse is not None:
+        if _dev_tensor(lse, torch.float32, "lse").numel() < rows:
+            raise ValueError(f"lse needs {rows} elements")
+        lse_ptr = lse.data_ptr()
+    if ws is None:
+        with _on(stream, q.device):
+            ws = attn_kv4_workspace(B, T, Hq, cache.heads, D, cache.cap, q.device)
+    _check((_lib or lib()).mq_attn_kv4(q.data_ptr(), _TYPES[dtype], row, B, T, Hq, cache._ref, length.data_ptr(),
+                                       D ** -0.5 if scale is None else scale, out.data_ptr(), _TYPES[out_type], lse_ptr,
+                                       _dev_tensor(ws, torch.uint8, "ws").data_ptr(), ws.numel(), _stream(stream)),
+           "mq_attn_kv4")
+    return out
+
+
+class Pool:
+    """Pages of all layers (include/mq.h, mq_pool): uint8 [layers, n_pages, page bytes] or [n_pages, page bytes], a page's bytes
+    contiguous. Pages of any kind: a KV4's are those of one layer."""
+
+    def __init__(self, data: torch.Tensor, page_rows: int):
+        if not isinstance(data, torch.Tensor):
+            raise TypeError("data must be a torch.Tensor")
+        if data.device.type != "cuda":
+            raise ValueError("data must be a CUDA tensor")
+        if data.dtype is not torch.uint8:
+            raise TypeError(f"data must be torch.uint8, got {data.dtype}")
+        if data.dim() not in (2, 3) or data.stride(-1) != 1:
+            raise ValueError("data must be [layers, n_pages, page bytes] or [n_pages, page bytes], pages contiguous")
+        self.data, self.page_rows = data, int(page_rows)
+        self.layers, self.n_pages = (1, int(data.shape[0])) if data.dim() == 2 else (int(data.shape[0]), int(data.shape[1]))
+        size = int(data.shape[-1])
+        self._c = CPool(data.data_ptr(), size, data.stride(-2) if self.n_pages > 1 else size,
+                        data.stride(0) if self.layers > 1 else 0, self.layers, self.n_pages, self.page_rows)
+        self._ref = ctypes.byref(self._c)
+
+
+def mq_pages_ws_bytes(pool: Pool, n: int, width: int) -> int:
+    return int(lib().mq_pages_ws_bytes(pool._ref, n, width))
+
+
+def pages_workspace(pool: Pool, n: int, width: int) -> torch.Tensor:
+    """A workspace for mq_pages_next and mq_pages_compact calls of up to n sequences (old or new) on one stream."""
+    return torch.empty((max(16, mq_pages_ws_bytes(pool, n, width)),), dtype=torch.uint8, device=pool.data.device)
+
+
+def _table(t, name):
+    if _dev_tensor(t, torch.int32, name).dim() != 2:
+        raise ValueError(f"{name} must be [sequences, width]")
+    return int(t.shape[0]), int(t.shape[1])
+
+
+def mq_pages_next(pool: Pool, table, length, table_out, length_out, status, frm=None, keep=None, add=None, ws=None, stream=None):
+    """New sequences from old ones: fork, trim, free, reserve with copy on write (include/mq.h). table, table_out: int32 [n, width],
+    [m, width]; length, length_out: int32 [n], [m]; frm (None: each from its own), keep (None: all rows), add (None: none): int32 [m];
+    status: int32 [3] (missing pages, free pages, sequences too long for the table). table_out and length_out may be table and
+    length."""
+    if not isinstance(pool, Pool):
+        raise TypeError("pool must be a Pool")
+    (n, width), (m, width_out) = _table(table, "table"), _table(table_out, "table_out")
+    if width_out != width:
+        raise ValueError(f"table_out has {width_out} entries a sequence, table {width}")
+    ptr = []
+    for t, name, size, needed in ((length, "length", n, True), (length_out, "length_out", m, True), (status, "status", 3, True),
+                                  (frm, "frm", m, False), (keep, "keep", m, False), (add, "add", m, False)):
+        if t is None and not needed:
+            ptr.append(None)
+            continue
+        if _dev_tensor(t, torch.int32, name).numel() != size:
+            raise ValueError(f"{name} must hold {size} entries")
+        ptr.append(t.data_ptr())
+    if ws is None:
+        with _on(stream, pool.data.device):
+            ws = pages_workspace(pool, max(n, m), width)
+    _check((_lib or lib()).mq_pages_next(pool._ref, table.data_ptr(), ptr[0], n, width, ptr[3], ptr[4], ptr[5],
+                                         table_out.data_ptr(), ptr[1], m, ptr[2], _dev_tensor(ws, torch.uint8, "ws").data_ptr(),
+                                         ws.numel(), _stream(stream)), "mq_pages_next")
+    return table_out
+
+
+def mq_pages_compact(pool: Pool, table, length, table_out, where, live, ws=None, stream=None):
+    """The pages in use to the front of the pool, in place (include/mq.h). table, table_out: int32 [n, width]; length: int32 [n];
+    where: int32 [n_pages], each page's new number or -1; live: int32 [1], the pages in use. table_out may be table."""
+    if not isinstance(pool, Pool):
+        raise TypeError("pool must be a Pool")
+    n, width = _table(table, "table")
+    if _table(table_out, "table_out") != (n, width):
+        raise ValueError("table_out must have table's shape")
+    for t, name, size in ((length, "length", n), (where, "where", pool.n_pages), (live, "live", 1)):
+        if _dev_tensor(t, torch.int32, name).numel() != size:
+            raise ValueError(f"{name} must hold {size} entries")
+    if ws is None:
+        with _on(stream, pool.data.device):
+            ws = pages_workspace(pool, n, width)
+    _check((_lib or lib()).mq_pages_compact(pool._ref, table.data_ptr(), length.data_ptr(), n, width, table_out.data_ptr(),
+                                            where.data_ptr(), live.data_ptr(), _dev_tensor(ws, torch.uint8, "ws").data_ptr(),
+                                            ws.numel(), _stream(stream)), "mq_pages_compact")
+    return table_out
 
 
 def mq_device_status(stream=None) -> int:
