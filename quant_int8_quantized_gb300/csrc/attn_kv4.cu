@@ -31,16 +31,20 @@ __device__ unsigned int g_kv4_error;   // bit 0: a bounded wait gave up
 __device__ int g_kv4_skip_tile;        // test builds only: block 0 leaves out its first tile
 #endif
 
-constexpr int kKeys = 32;              // of a tile
 constexpr int kTileExtra = 2;          // what beginning and ending a segment costs, in tiles
+
+constexpr int keys_of(int D) { return D <= 128 ? 64 : 32; }   // of a tile
+constexpr int kStep = 32;              // keys that are multiplied at once
 
 template <int D, int NT>
 struct Shape {
+    static constexpr int kKeys = keys_of(D);
     static constexpr int kTile = kKeys / kv4::kBlockRows * kv4::block_bytes(D);
-    static constexpr int kStages = D <= 64 ? 4 : D <= 128 ? 3 : 2;
-    static constexpr int kSmem = kStages * kTile;
+    static constexpr int kStages = D <= 64 ? 3 : 2;
+    static constexpr int kRing = kStages * kTile;
+    static constexpr int kSmem = kRing + kStep / 2 * (D / 32) * 8;   // stages; a step's value scales
     // warps an SM: registers (the outputs alone are D NT / 4 of a lane's)
-    static constexpr int kPerSm = D * NT <= 128 ? 16 : D * NT <= 256 ? 12 : 8;
+    static constexpr int kPerSm = D * NT <= 64 ? 14 : D * NT <= 128 ? 11 : 8;
 };
 
 struct Kv4Args {
@@ -97,11 +101,12 @@ struct Piece {
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(32, Shape<D, NT>::kPerSm) attn_kv4_kernel(const Kv4Args a) {
     using C = Shape<D, NT>;
-    constexpr int nb = D / 32, kBlock = kv4::block_bytes(D), kStages = C::kStages;
+    constexpr int nb = D / 32, kBlock = kv4::block_bytes(D), kStages = C::kStages, kKeys = C::kKeys;
     extern __shared__ __align__(128) uint8_t s_ring[];
     __shared__ Piece s_piece[kStages + 1];
     __shared__ uint64_t s_full[kStages];
-    __shared__ int s_bad[kStages];         // blocks of the tile that are on no page
+    __shared__ uint32_t s_bad[kStages];    // blocks of the tile that are on no page
+    uint2* const s_scale = reinterpret_cast<uint2*>(s_ring + C::kRing);   // [row pair of the step][nb]
     mq_grid_release();
     const int lane = threadIdx.x;
     if (lane == 0) {
@@ -119,6 +124,8 @@ __global__ void __launch_bounds__(32, Shape<D, NT>::kPerSm) attn_kv4_kernel(cons
     int left = 0, handed = 0, key = 0, in_slot = 0;    // tiles of the copied piece left, pieces handed over
     int head = 0, seq = 0, issued = 0;
     int pages_at = 0, pages = -1;                      // lane i: page pages_at + i of the sequence
+    // a tile lies on `parts` pages, `part` bytes on each
+    const int parts = max(1, kKeys >> a.c.shift), part = C::kTile / parts, part_shift = min(a.c.shift, kKeys == 64 ? 6 : 5);
     auto copy = [&] {
         bool fresh = false;
         if (left == 0) {
@@ -147,33 +154,30 @@ __global__ void __launch_bounds__(32, Shape<D, NT>::kPerSm) attn_kv4_kernel(cons
             if (++handed == kStages + 1) handed = 0;
         }
         if (left > 0) {
-            const int first = key >> a.c.shift, last = (key + kKeys - 1) >> a.c.shift;   // (one page, or two of 16 rows)
-            if (fresh || last - pages_at >= 32) {
+            const int first = key >> a.c.shift;
+            if (fresh || first + parts - pages_at > 32) {
                 pages_at = first;
                 const int i = first + lane;
                 const int e = i < a.c.width ? __ldca(a.c.table + seq * a.c.table_stride + i) : -1;
                 pages = (unsigned)e < (unsigned)a.c.n_pages ? e : -1;
             }
-            const int p0 = __shfl_sync(0xffffffffu, pages, first - pages_at);
-            const int p1 = __shfl_sync(0xffffffffu, pages, last - pages_at);
+            const int page = __shfl_sync(0xffffffffu, pages, first - pages_at + min(lane, parts - 1));
+            const bool there = lane < parts && page >= 0;
+            const uint32_t all = __ballot_sync(0xffffffffu, there);
 #ifdef MQ_TEST_INJECT
             const bool skip = g_kv4_skip_tile && blockIdx.x == 0 && issued == 0;
 #else
             constexpr bool skip = false;
 #endif
-            if (!skip && lane == 0) {
-                const uint32_t st = tc::smem_u32(s_ring) + in_slot * C::kTile;
+            if (!skip) {
                 uint64_t* bar = &s_full[in_slot];
-                if (first == last) {
-                    tc::mbar_arrive_expect_tx(bar, p0 >= 0 ? C::kTile : 0);
-                    if (p0 >= 0) bulk_load(st, a.c.block(p0, head, key, kBlock), C::kTile, bar);
-                    s_bad[in_slot] = p0 >= 0 ? 0 : 3;
-                } else {
-                    tc::mbar_arrive_expect_tx(bar, ((p0 >= 0) + (p1 >= 0)) * kBlock);
-                    if (p0 >= 0) bulk_load(st, a.c.block(p0, head, key, kBlock), kBlock, bar);
-                    if (p1 >= 0) bulk_load(st + kBlock, a.c.block(p1, head, key + kv4::kBlockRows, kBlock), kBlock, bar);
-                    s_bad[in_slot] = (p0 < 0) + 2 * (p1 < 0);
+                if (lane == 0) {
+                    tc::mbar_arrive_expect_tx(bar, __popc(all) * part);
+                    s_bad[in_slot] = ~all & ((1u << parts) - 1);
                 }
+                if (there)
+                    bulk_load(tc::smem_u32(s_ring) + in_slot * C::kTile + lane * part,
+                              a.c.block(page, head, key, kBlock), part, bar);
             }
             __syncwarp();
             ++issued;
@@ -186,6 +190,9 @@ __global__ void __launch_bounds__(32, Shape<D, NT>::kPerSm) attn_kv4_kernel(cons
     for (int i = 0; i < kStages - 1; ++i) copy();
 
     // ---------------------------------------------------------------- products
+    auto from = [](const uint8_t* q) {
+        return [q](auto type, int i) { return reinterpret_cast<const decltype(type)*>(q)[i]; };
+    };
     int taken = 0, slot = 0, taken_tiles = 0;
     uint32_t phase = 0;
     bool alive = true;
@@ -225,133 +232,170 @@ __global__ void __launch_bounds__(32, Shape<D, NT>::kPerSm) attn_kv4_kernel(cons
             if (!(alive = __all_sync(0xffffffffu, mbar_ready(&s_full[slot], phase) ||
                                                       tc::mbar_wait(&s_full[slot], phase, kWaitLimitNs))))
                 break;
-            uint8_t* const st = s_ring + slot * C::kTile;
-            const int k0 = w.key0 + ti * kKeys, bad = s_bad[slot];
-            if (bad || k0 + kKeys > w.len) {
-                // scales of rows that are on no page, and of values past the end: zero, whatever lies there
-                const int blk = lane >> 4, r = lane & 15;
-                uint8_t* s = st + blk * kBlock;
-                const bool none = bad >> blk & 1;
-                if (none || k0 + lane >= w.len)
-#pragma unroll
-                    for (int b = 0; b < nb; ++b) {
-                        s[kv4::value_scale_at(D) + (r >> 1) * 2 * nb + 2 * b + (r & 1)] = 0;
-                        if (none) s[kv4::key_scale_at(D) + r * nb + b] = 0;
-                    }
-                tc::fence_proxy_async_smem();
-                __syncwarp();
-            }
+            uint8_t* const tile = s_ring + slot * C::kTile;
+            const uint32_t bad = s_bad[slot];
             ++taken_tiles;
             if (++slot == kStages) {
                 slot = 0;
                 phase ^= 1;
             }
-            auto from = [](const uint8_t* q) {
-                return [q](auto type, int i) { return reinterpret_cast<const decltype(type)*>(q)[i]; };
-            };
-            float s[2][NT][4];
+#pragma unroll 1
+            for (int in = 0; in < kKeys; in += kStep) {
+                const int k0 = w.key0 + ti * kKeys + in;
+                if (k0 >= w.len) break;
+                uint8_t* const st = tile + in / kv4::kBlockRows * kBlock;
+                if (bad || k0 + kStep > w.len) {
+                    // scales of rows that are on no page, and of values past the end: zero, whatever lies there
+                    const int blk = lane >> 4, r = lane & 15;
+                    uint8_t* s = st + blk * kBlock;
+                    const bool none = bad >> ((in + lane) >> part_shift) & 1;
+                    if (none || k0 + lane >= w.len)
 #pragma unroll
-            for (int blk = 0; blk < 2; ++blk) {
-                const uint8_t* at = st + blk * kBlock;
-                uint32_t kw[2][nb], ks[2][(nb + 3) / 4];
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    kv4::words<nb>(from(at + (u * 32 + lane) * nb * 4), kw[u]);
-                    kv4::bytes<nb>(from(at + kv4::key_scale_at(D) + (g + 8 * u) * nb), ks[u]);
+                        for (int b = 0; b < nb; ++b) {
+                            s[kv4::value_scale_at(D) + (r >> 1) * 2 * nb + 2 * b + (r & 1)] = 0;
+                            if (none) s[kv4::key_scale_at(D) + r * nb + b] = 0;
+                        }
+                    tc::fence_proxy_async_smem();
+                    __syncwarp();
                 }
+                // the values' scales as the numbers need them, once for all lanes: nb / 2 pairs of rows a lane
+                {
+                    const uint8_t* at = st + (lane >> 4) * kBlock + kv4::value_scale_at(D) + (lane & 15) * nb;
+                    if constexpr (nb % 2 == 0) {
+                        uint32_t c[(nb + 3) / 4];
+                        kv4::bytes<nb>(from(at), c);
+                        uint32_t x[nb];
 #pragma unroll
-                for (int j = 0; j < NT; ++j) s[blk][j][0] = s[blk][j][1] = s[blk][j][2] = s[blk][j][3] = 0.0f;
+                        for (int i = 0; i < nb / 2; ++i) {
+                            const kv4::Scale<T> sc = kv4::Scale<T>::of(kv4::both(c, i));
+                            x[2 * i] = *reinterpret_cast<const uint32_t*>(&sc.mul);
+                            x[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&sc.off);
+                        }
+                        uint32_t* to = reinterpret_cast<uint32_t*>(s_scale) + lane * nb;
+                        if constexpr (nb == 2) *reinterpret_cast<uint2*>(to) = make_uint2(x[0], x[1]);
+                        else
 #pragma unroll
-                for (int b = 0; b < nb; ++b) {
-                    uint32_t x0[4], x1[4];
-                    kv4::numbers(kw[0][b], kv4::Scale<T>::of(kv4::twice(ks[0], b)), x0);
-                    kv4::numbers(kw[1][b], kv4::Scale<T>::of(kv4::twice(ks[1], b)), x1);
-#pragma unroll
-                    for (int j = 0; j < NT; ++j) {
-                        mma<T>(s[blk][j], x0[0], x1[0], x0[1], x1[1], qf[j][b][0], qf[j][b][1]);
-                        mma<T>(s[blk][j], x0[2], x1[2], x0[3], x1[3], qf[j][b][2], qf[j][b][3]);
+                            for (int i = 0; i < nb / 4; ++i)
+                                reinterpret_cast<uint4*>(to)[i] = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                    } else {
+                        for (int i = lane; i < kStep / 2 * nb; i += 32) {
+                            const int pair = i / nb, b = i - pair * nb;
+                            const uint8_t* q = st + (pair >> 3) * kBlock + kv4::value_scale_at(D) + (pair & 7) * 2 * nb + 2 * b;
+                            const kv4::Scale<T> sc = kv4::Scale<T>::of((uint32_t)q[0] << 8 | (uint32_t)q[1] << 24);
+                            s_scale[i] = make_uint2(*reinterpret_cast<const uint32_t*>(&sc.mul), *reinterpret_cast<const uint32_t*>(&sc.off));
+                        }
                     }
                 }
-            }
-            // row (key) 16 blk + g + 8 (e / 2), column (query) 8 j + 2 t + e % 2
-            float mx[NT][2];
-            bool grew = false;
+                float s[2][NT][4];
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
+                for (int blk = 0; blk < 2; ++blk) {
+                    const uint8_t* at = st + blk * kBlock;
+                    uint32_t kw[2][nb], ks[2][(nb + 3) / 4];
 #pragma unroll
-                for (int blk = 0; blk < 2; ++blk)
+                    for (int u = 0; u < 2; ++u) {
+                        kv4::words<nb>(from(at + (u * 32 + lane) * nb * 4), kw[u]);
+                        kv4::bytes<nb>(from(at + kv4::key_scale_at(D) + (g + 8 * u) * nb), ks[u]);
+                    }
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s[blk][j][e] *= a.scale_log2;
-                if (k0 + kKeys > all_see) {
+                    for (int j = 0; j < NT; ++j) s[blk][j][0] = s[blk][j][1] = s[blk][j][2] = s[blk][j][3] = 0.0f;
+#pragma unroll
+                    for (int b = 0; b < nb; b += 2) {
+                        const kv4::Scale<T> s0 = kv4::Scale<T>::of(kv4::both(ks[0], b / 2)), s1 = kv4::Scale<T>::of(kv4::both(ks[1], b / 2));
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            if (b + e < nb) {
+                                uint32_t x0[4], x1[4];
+                                kv4::numbers(kw[0][b + e], kv4::half_of(s0, e), x0);
+                                kv4::numbers(kw[1][b + e], kv4::half_of(s1, e), x1);
+#pragma unroll
+                                for (int j = 0; j < NT; ++j) {
+                                    mma<T>(s[blk][j], x0[0], x1[0], x0[1], x1[1], qf[j][b + e][0], qf[j][b + e][1]);
+                                    mma<T>(s[blk][j], x0[2], x1[2], x0[3], x1[3], qf[j][b + e][2], qf[j][b + e][3]);
+                                }
+                            }
+                    }
+                }
+                // row (key) 16 blk + g + 8 (e / 2), column (query) 8 j + 2 t + e % 2
+                float mx[NT][2];
+                bool grew = false;
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
 #pragma unroll
                     for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (k0 + 16 * blk + g + 8 * (e >> 1) >= seen[j][e & 1]) s[blk][j][e] = kNone;
-                }
+                        for (int e = 0; e < 4; ++e) s[blk][j][e] *= a.scale_log2;
+                    if (k0 + kStep > all_see) {
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    mx[j][e] = fmaxf(fmaxf(s[0][j][e], s[0][j][e + 2]), fmaxf(s[1][j][e], s[1][j][e + 2]));
-                    grew |= mx[j][e] > m[j][e] + (kUp<T> + kGrow);
-                }
-            }
-            if (__any_sync(0xffffffffu, grew)) {
+                        for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    float alpha[2];
+                            for (int e = 0; e < 4; ++e)
+                                if (k0 + 16 * blk + g + 8 * (e >> 1) >= seen[j][e & 1]) s[blk][j][e] = kNone;
+                    }
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-#pragma unroll
-                        for (int x = 4; x < 32; x <<= 1) mx[j][e] = fmaxf(mx[j][e], __shfl_xor_sync(0xffffffffu, mx[j][e], x));
-                        const float now = mx[j][e] > m[j][e] + (kUp<T> + kGrow) ? reference<kUp<T>>(mx[j][e]) : m[j][e];
-                        alpha[e] = now == m[j][e] ? 1.0f : exp2_fast(m[j][e] - now);
-                        m[j][e] = now;
-                        l[j][e] *= alpha[e];
-                    }
-#pragma unroll
-                    for (int i = 0; i < 2 * nb; ++i) {
-                        o[i][j][0] *= alpha[0], o[i][j][1] *= alpha[1];
-                        o[i][j][2] *= alpha[0], o[i][j][3] *= alpha[1];
+                        mx[j][e] = fmaxf(fmaxf(s[0][j][e], s[0][j][e + 2]), fmaxf(s[1][j][e], s[1][j][e + 2]));
+                        grew |= mx[j][e] > m[j][e] + (kUp<T> + kGrow);
                     }
                 }
-            }
-            uint32_t pf[2][NT][2];
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const float safe[2] = {m[j][0] == kNone ? 0.0f : m[j][0], m[j][1] == kNone ? 0.0f : m[j][1]};
-#pragma unroll
-                for (int blk = 0; blk < 2; ++blk) {
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const float e0 = exp2_fast(s[blk][j][2 * u] - safe[0]), e1 = exp2_fast(s[blk][j][2 * u + 1] - safe[1]);
-                        l[j][0] += e0;
-                        l[j][1] += e1;
-                        pf[blk][j][u] = transposed(mq_pack2<T>(e0, e1));
-                    }
-                }
-            }
-#pragma unroll
-            for (int blk = 0; blk < 2; ++blk) {
-                const uint8_t* at = st + blk * kBlock;
-                uint32_t vw[2][nb], vs[2][nb / 2 + nb % 2];
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    kv4::words<nb>(from(at + kv4::value_at(D) + (u * 32 + lane) * nb * 4), vw[u]);
-                    kv4::bytes<2 * nb>(from(at + kv4::value_scale_at(D) + (4 * u + t) * 2 * nb), vs[u]);
-                }
-#pragma unroll
-                for (int b = 0; b < nb; ++b) {
-                    uint32_t x0[4], x1[4];
-                    kv4::numbers(vw[0][b], kv4::Scale<T>::of(kv4::both(vs[0], b)), x0);
-                    kv4::numbers(vw[1][b], kv4::Scale<T>::of(kv4::both(vs[1], b)), x1);
+                if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
                     for (int j = 0; j < NT; ++j) {
-                        mma<T>(o[2 * b][j], x0[0], x0[1], x1[0], x1[1], pf[blk][j][0], pf[blk][j][1]);
-                        mma<T>(o[2 * b + 1][j], x0[2], x0[3], x1[2], x1[3], pf[blk][j][0], pf[blk][j][1]);
+                        float alpha[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                            for (int x = 4; x < 32; x <<= 1) mx[j][e] = fmaxf(mx[j][e], __shfl_xor_sync(0xffffffffu, mx[j][e], x));
+                            const float now = mx[j][e] > m[j][e] + (kUp<T> + kGrow) ? reference<kUp<T>>(mx[j][e]) : m[j][e];
+                            alpha[e] = now == m[j][e] ? 1.0f : exp2_fast(m[j][e] - now);
+                            m[j][e] = now;
+                            l[j][e] *= alpha[e];
+                        }
+#pragma unroll
+                        for (int i = 0; i < 2 * nb; ++i) {
+                            o[i][j][0] *= alpha[0], o[i][j][1] *= alpha[1];
+                            o[i][j][2] *= alpha[0], o[i][j][3] *= alpha[1];
+                        }
                     }
                 }
+                uint32_t pf[2][NT][2];
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    const float safe[2] = {m[j][0] == kNone ? 0.0f : m[j][0], m[j][1] == kNone ? 0.0f : m[j][1]};
+#pragma unroll
+                    for (int blk = 0; blk < 2; ++blk) {
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const float e0 = exp2_fast(s[blk][j][2 * u] - safe[0]), e1 = exp2_fast(s[blk][j][2 * u + 1] - safe[1]);
+                            l[j][0] += e0;
+                            l[j][1] += e1;
+                            pf[blk][j][u] = transposed(mq_pack2<T>(e0, e1));
+                        }
+                    }
+                }
+                __syncwarp();      // the scales are there
+#pragma unroll
+                for (int blk = 0; blk < 2; ++blk) {
+                    const uint8_t* at = st + blk * kBlock;
+                    uint32_t vw[2][nb], vs[2][2 * nb];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        kv4::words<nb>(from(at + kv4::value_at(D) + (u * 32 + lane) * nb * 4), vw[u]);
+                        kv4::words<2 * nb>(from(reinterpret_cast<const uint8_t*>(s_scale + (8 * blk + 4 * u + t) * nb)), vs[u]);
+                    }
+#pragma unroll
+                    for (int b = 0; b < nb; ++b) {
+                        uint32_t x0[4], x1[4];
+                        kv4::numbers(vw[0][b], kv4::Scale<T>::from(vs[0][2 * b], vs[0][2 * b + 1]), x0);
+                        kv4::numbers(vw[1][b], kv4::Scale<T>::from(vs[1][2 * b], vs[1][2 * b + 1]), x1);
+#pragma unroll
+                        for (int j = 0; j < NT; ++j) {
+                            mma<T>(o[2 * b][j], x0[0], x0[1], x1[0], x1[1], pf[blk][j][0], pf[blk][j][1]);
+                            mma<T>(o[2 * b + 1][j], x0[2], x0[3], x1[2], x1[3], pf[blk][j][0], pf[blk][j][1]);
+                        }
+                    }
+                }
+                __syncwarp();      // scales, and after the last step the stage, may be written again
             }
-            __syncwarp();   // the stage may be written again
         }
         if (!alive) break;
         const long long place = ((long long)blockIdx.x + w.seg) * p.rows;
@@ -464,14 +508,14 @@ Kv4Cut cut_kv4(int B, int T, int Hq, int Hkv, int D, int cap) {
     p.own_cap = cap;
     p.own = 1;
     p.rows = 8 * c.nt;
-    p.keys = kKeys;
+    p.keys = keys_of(D);
     p.wide = p.rows;
     p.cost = p.wide_cost = 1;
     p.extra = kTileExtra;
     p.lanes = 1;
     p.by_group = div_by(group);
     p.by_per_seq = div_by(own_tiles_of_rows(p));
-    const long long segs = all_segs(p), most = segs * ceil_div(cap, kKeys);
+    const long long segs = all_segs(p), most = segs * ceil_div(cap, p.keys);
     if (most + segs * p.extra > 0x7fffffffLL || segs > 0x3fffffffLL) c.fits = false;
     int per_sm = 1;
     with_kernel(D, MQ_F16, c.nt, [&](auto, int, int n) { return per_sm = n; });

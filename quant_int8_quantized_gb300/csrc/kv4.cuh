@@ -97,6 +97,9 @@ struct Scale<__half> {
         const __half2 d = *reinterpret_cast<const __half2*>(&h);
         return {__hmul2(d, __float2half2_rn(0.0625f)), __hmul2(d, __float2half2_rn(-72.0f))};
     }
+    __device__ __forceinline__ static Scale from(uint32_t mul, uint32_t off) {
+        return {*reinterpret_cast<const __half2*>(&mul), *reinterpret_cast<const __half2*>(&off)};
+    }
 };
 template <>
 struct Scale<__nv_bfloat16> {
@@ -106,7 +109,18 @@ struct Scale<__nv_bfloat16> {
         const __nv_bfloat162 d = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&h), __float2bfloat162_rn(5.192296858534828e33f));
         return {d, __hmul2(d, __float2bfloat162_rn(-136.0f))};
     }
+    __device__ __forceinline__ static Scale from(uint32_t mul, uint32_t off) {
+        return {*reinterpret_cast<const __nv_bfloat162*>(&mul), *reinterpret_cast<const __nv_bfloat162*>(&off)};
+    }
 };
+// One of a pair's two scales for both numbers (an operand's half: no instruction).
+__device__ __forceinline__ Scale<__half> half_of(const Scale<__half>& s, int e) {
+    return e ? Scale<__half>{__high2half2(s.mul), __high2half2(s.off)} : Scale<__half>{__low2half2(s.mul), __low2half2(s.off)};
+}
+__device__ __forceinline__ Scale<__nv_bfloat16> half_of(const Scale<__nv_bfloat16>& s, int e) {
+    return e ? Scale<__nv_bfloat16>{__high2bfloat162(s.mul), __high2bfloat162(s.off)}
+             : Scale<__nv_bfloat16>{__low2bfloat162(s.mul), __low2bfloat162(s.off)};
+}
 // nb consecutive words (or bytes), aligned as far as nb allows.
 template <int nb, typename P>
 __device__ __forceinline__ void words(P load, uint32_t (&w)[nb]) {
