@@ -33,18 +33,19 @@ __device__ int g_kv4_skip_tile;        // test builds only: block 0 leaves out i
 
 constexpr int kTileExtra = 2;          // what beginning and ending a segment costs, in tiles
 
-constexpr int keys_of(int D) { return D <= 128 ? 64 : 32; }   // of a tile
+constexpr int keys_of(int D) { return D <= 64 ? 64 : 32; }    // of a tile
 constexpr int kStep = 32;              // keys that are multiplied at once
 
 template <int D, int NT>
 struct Shape {
     static constexpr int kKeys = keys_of(D);
     static constexpr int kTile = kKeys / kv4::kBlockRows * kv4::block_bytes(D);
-    static constexpr int kStages = D <= 64 ? 3 : 2;
+    static constexpr int kStages = D <= 64 ? 2 : D <= 128 ? 3 : 2;
     static constexpr int kRing = kStages * kTile;
-    static constexpr int kSmem = kRing + kStep / 2 * (D / 32) * 8;   // stages; a step's value scales
-    // warps an SM: registers (the outputs alone are D NT / 4 of a lane's)
-    static constexpr int kPerSm = D * NT <= 64 ? 14 : D * NT <= 128 ? 11 : 8;
+    static constexpr int kSmem = kRing + kStep / 2 * (D / 32) * 16;   // stages; a step's scales
+    // warps an SM, as registers allow (the outputs alone are D NT / 4 of a lane's); the same number on each of its four parts: 14
+    // took 15 % longer than 12 or 16
+    static constexpr int kPerSm = D * NT <= 64 ? 16 : D * NT <= 128 ? 12 : 8;
 };
 
 struct Kv4Args {
@@ -78,10 +79,25 @@ __device__ __forceinline__ float exp2_fast(float x) {          // 2^x within 2 u
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ void bulk_load(uint32_t to, const void* from, uint32_t bytes, uint64_t* bar) {
+__device__ __forceinline__ void expect(uint32_t bar, uint32_t bytes) {
+    asm volatile("{ .reg .b64 st; mbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1; }" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_load(uint32_t to, const void* from, uint32_t bytes, uint32_t bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to), "l"(from),
-                 "r"(bytes), "r"(tc::smem_u32(bar))
+                 "r"(bytes), "r"(bar)
                  : "memory");
+}
+
+// n words to shared memory, aligned as far as n allows.
+template <int n>
+__device__ __forceinline__ void put(uint32_t* to, const uint32_t (&x)[n]) {
+    if constexpr (n % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < n / 4; ++i) reinterpret_cast<uint4*>(to)[i] = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+    } else {
+        static_assert(n == 2, "pairs and fours");
+        *reinterpret_cast<uint2*>(to) = make_uint2(x[0], x[1]);
+    }
 }
 
 constexpr float kNone = -INFINITY;
@@ -102,11 +118,14 @@ template <typename T, int D, int NT>
 __global__ void __launch_bounds__(32, Shape<D, NT>::kPerSm) attn_kv4_kernel(const Kv4Args a) {
     using C = Shape<D, NT>;
     constexpr int nb = D / 32, kBlock = kv4::block_bytes(D), kStages = C::kStages, kKeys = C::kKeys;
+    constexpr bool kHalf = std::is_same<T, __half>::value;
+    using Factor = typename std::conditional<kHalf, kv4::Eighth, kv4::Scale<T>>::type;
+    constexpr float kUnit = kHalf ? 8.0f : 1.0f;       // of the numbers that it makes
+    constexpr int KW = Factor::kWords;
     extern __shared__ __align__(128) uint8_t s_ring[];
     __shared__ Piece s_piece[kStages + 1];
     __shared__ uint64_t s_full[kStages];
-    __shared__ uint32_t s_bad[kStages];    // blocks of the tile that are on no page
-    uint2* const s_scale = reinterpret_cast<uint2*>(s_ring + C::kRing);   // [row pair of the step][nb]
+    uint32_t* const s_value = reinterpret_cast<uint32_t*>(s_ring + C::kRing);    // [block of dims][pair of rows][KW]
     mq_grid_release();
     const int lane = threadIdx.x;
     if (lane == 0) {
@@ -123,9 +142,13 @@ __global__ void __launch_bounds__(32, Shape<D, NT>::kPerSm) attn_kv4_kernel(cons
     advance(p, a.len, c, 0);
     int left = 0, handed = 0, key = 0, in_slot = 0;    // tiles of the copied piece left, pieces handed over
     int head = 0, seq = 0, issued = 0;
-    int pages_at = 0, pages = -1;                      // lane i: page pages_at + i of the sequence
-    // a tile lies on `parts` pages, `part` bytes on each
-    const int parts = max(1, kKeys >> a.c.shift), part = C::kTile / parts, part_shift = min(a.c.shift, kKeys == 64 ? 6 : 5);
+    // a tile lies on `parts` pages, `part` bytes on each; lane i holds the place of part i - at from the next one on
+    const int parts = max(1, kKeys >> a.c.shift), part = C::kTile / parts, part_rows = kKeys / parts;
+    int at = 0;
+    const uint8_t* src = nullptr;
+    uint32_t there = 0;                                // the parts that are on a page
+    uint32_t bad[kStages] = {};                        // parts on no page, of the tile that is multiplied next (0) and those behind it
+    const uint32_t ring = tc::smem_u32(s_ring), full = tc::smem_u32(s_full);
     auto copy = [&] {
         bool fresh = false;
         if (left == 0) {
@@ -154,31 +177,26 @@ __global__ void __launch_bounds__(32, Shape<D, NT>::kPerSm) attn_kv4_kernel(cons
             if (++handed == kStages + 1) handed = 0;
         }
         if (left > 0) {
-            const int first = key >> a.c.shift;
-            if (fresh || first + parts - pages_at > 32) {
-                pages_at = first;
-                const int i = first + lane;
-                const int e = i < a.c.width ? __ldca(a.c.table + seq * a.c.table_stride + i) : -1;
-                pages = (unsigned)e < (unsigned)a.c.n_pages ? e : -1;
+            if (fresh || at + parts > 32) {       // the next 32 parts' places, a lane each
+                at = 0;
+                const int row = key + lane * part_rows;
+                const int page = row >> a.c.shift < a.c.width ? a.c.page(seq, row) : -1;
+                src = page >= 0 ? a.c.block(page, head, row, kBlock) : nullptr;
+                there = __ballot_sync(0xffffffffu, src != nullptr);
             }
-            const int page = __shfl_sync(0xffffffffu, pages, first - pages_at + min(lane, parts - 1));
-            const bool there = lane < parts && page >= 0;
-            const uint32_t all = __ballot_sync(0xffffffffu, there);
+            const uint32_t mine = there >> at & ((1u << parts) - 1);
+            bad[kStages - 1] = mine ^ ((1u << parts) - 1);
 #ifdef MQ_TEST_INJECT
             const bool skip = g_kv4_skip_tile && blockIdx.x == 0 && issued == 0;
 #else
             constexpr bool skip = false;
 #endif
-            if (!skip) {
-                uint64_t* bar = &s_full[in_slot];
-                if (lane == 0) {
-                    tc::mbar_arrive_expect_tx(bar, __popc(all) * part);
-                    s_bad[in_slot] = ~all & ((1u << parts) - 1);
-                }
-                if (there)
-                    bulk_load(tc::smem_u32(s_ring) + in_slot * C::kTile + lane * part,
-                              a.c.block(page, head, key, kBlock), part, bar);
+            if (!skip && (unsigned)(lane - at) < (unsigned)parts) {
+                const uint32_t bar = full + in_slot * 8;
+                if (lane == at) expect(bar, __popc(mine) * part);
+                if (src) bulk_load(ring + in_slot * C::kTile + (lane - at) * part, src, part, bar);
             }
+            at += parts;
             __syncwarp();
             ++issued;
             key += kKeys;
@@ -187,12 +205,20 @@ __global__ void __launch_bounds__(32, Shape<D, NT>::kPerSm) attn_kv4_kernel(cons
         }
     };
 #pragma unroll 1
-    for (int i = 0; i < kStages - 1; ++i) copy();
+    for (int i = 0; i < kStages - 1; ++i) {
+        if (i > 0)
+#pragma unroll
+            for (int k = 1; k < kStages; ++k) bad[k - 1] = bad[k];
+        copy();
+    }
+#pragma unroll
+    for (int k = 1; k < kStages; ++k) bad[k - 1] = bad[k];
 
     // ---------------------------------------------------------------- products
     auto from = [](const uint8_t* q) {
         return [q](auto type, int i) { return reinterpret_cast<const decltype(type)*>(q)[i]; };
     };
+    const float scale = fminf(fmaxf(a.scale_log2 * kUnit, -3.4028234663852886e38f), 3.4028234663852886e38f);
     int taken = 0, slot = 0, taken_tiles = 0;
     uint32_t phase = 0;
     bool alive = true;
@@ -233,7 +259,9 @@ __global__ void __launch_bounds__(32, Shape<D, NT>::kPerSm) attn_kv4_kernel(cons
                                                       tc::mbar_wait(&s_full[slot], phase, kWaitLimitNs))))
                 break;
             uint8_t* const tile = s_ring + slot * C::kTile;
-            const uint32_t bad = s_bad[slot];
+            const uint32_t none_of = bad[0];
+#pragma unroll
+            for (int i = 1; i < kStages; ++i) bad[i - 1] = bad[i];
             ++taken_tiles;
             if (++slot == kStages) {
                 slot = 0;
@@ -244,76 +272,79 @@ __global__ void __launch_bounds__(32, Shape<D, NT>::kPerSm) attn_kv4_kernel(cons
                 const int k0 = w.key0 + ti * kKeys + in;
                 if (k0 >= w.len) break;
                 uint8_t* const st = tile + in / kv4::kBlockRows * kBlock;
-                if (bad || k0 + kStep > w.len) {
-                    // scales of rows that are on no page, and of values past the end: zero, whatever lies there
-                    const int blk = lane >> 4, r = lane & 15;
-                    uint8_t* s = st + blk * kBlock;
-                    const bool none = bad >> ((in + lane) >> part_shift) & 1;
-                    if (none || k0 + lane >= w.len)
-#pragma unroll
-                        for (int b = 0; b < nb; ++b) {
-                            s[kv4::value_scale_at(D) + (r >> 1) * 2 * nb + 2 * b + (r & 1)] = 0;
-                            if (none) s[kv4::key_scale_at(D) + r * nb + b] = 0;
-                        }
-                    tc::fence_proxy_async_smem();
-                    __syncwarp();
-                }
-                // the values' scales as the numbers need them, once for all lanes: nb / 2 pairs of rows a lane
+                // The values' scales as the numbers need them, once for all lanes: half a pair of rows each. Those of rows that
+                // are on no page or past the end are zero, whatever lies there.
                 {
-                    const uint8_t* at = st + (lane >> 4) * kBlock + kv4::value_scale_at(D) + (lane & 15) * nb;
+                    uint32_t vc[(nb + 3) / 4];
+                    if constexpr (nb % 2 == 0) kv4::bytes<nb>(from(st + (lane >> 4) * kBlock + kv4::value_scale_at(D) + (lane & 15) * nb), vc);
+                    const int pair = (lane >> 4) * 8 + ((lane & 15) >> 1);        // of the step's 16
+                    uint32_t keep = ~0u;
+                    if (none_of || k0 + kStep > w.len) {
+                        if (none_of >> ((in + lane) / part_rows) & 1) {       // (once in the stage: keys' scales are read row by row)
+#pragma unroll
+                            for (int b = 0; b < nb; ++b) st[(lane >> 4) * kBlock + kv4::key_scale_at(D) + (lane & 15) * nb + b] = 0;
+                            tc::fence_proxy_async_smem();
+                        }
+                        const bool gone = none_of >> ((in + 2 * pair) / part_rows) & 1;
+                        keep = (!gone && k0 + 2 * pair < w.len ? 0x00ff00ffu : 0u) | (!gone && k0 + 2 * pair + 1 < w.len ? 0xff00ff00u : 0u);
+                    }
                     if constexpr (nb % 2 == 0) {
-                        uint32_t c[(nb + 3) / 4];
-                        kv4::bytes<nb>(from(at), c);
-                        uint32_t x[nb];
+#pragma unroll
+                        for (int i = 0; i < (nb + 3) / 4; ++i) vc[i] &= keep;
 #pragma unroll
                         for (int i = 0; i < nb / 2; ++i) {
-                            const kv4::Scale<T> sc = kv4::Scale<T>::of(kv4::both(c, i));
-                            x[2 * i] = *reinterpret_cast<const uint32_t*>(&sc.mul);
-                            x[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&sc.off);
+                            uint32_t y[KW];
+                            Factor::of(kv4::both(vc, i)).to(y);
+                            put<KW>(s_value + (((lane & 1) * (nb / 2) + i) * 16 + pair) * KW, y);
                         }
-                        uint32_t* to = reinterpret_cast<uint32_t*>(s_scale) + lane * nb;
-                        if constexpr (nb == 2) *reinterpret_cast<uint2*>(to) = make_uint2(x[0], x[1]);
-                        else
-#pragma unroll
-                            for (int i = 0; i < nb / 4; ++i)
-                                reinterpret_cast<uint4*>(to)[i] = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
                     } else {
-                        for (int i = lane; i < kStep / 2 * nb; i += 32) {
-                            const int pair = i / nb, b = i - pair * nb;
-                            const uint8_t* q = st + (pair >> 3) * kBlock + kv4::value_scale_at(D) + (pair & 7) * 2 * nb + 2 * b;
-                            const kv4::Scale<T> sc = kv4::Scale<T>::of((uint32_t)q[0] << 8 | (uint32_t)q[1] << 24);
-                            s_scale[i] = make_uint2(*reinterpret_cast<const uint32_t*>(&sc.mul), *reinterpret_cast<const uint32_t*>(&sc.off));
+                        const uint8_t* q = st + (lane >> 4) * kBlock + kv4::value_scale_at(D) + (pair & 7) * 2 * nb;
+                        for (int b = lane & 1; b < nb; b += 2) {
+                            uint32_t y[KW];
+                            Factor::of((q[2 * b] & keep & 255) << 8 | (q[2 * b + 1] & keep >> 8 & 255) << 24).to(y);
+                            put<KW>(s_value + (b * 16 + pair) * KW, y);
                         }
                     }
+                    __syncwarp();
                 }
                 float s[2][NT][4];
+                uint32_t kw[2][2][nb], ks[2][2][(nb + 3) / 4];
 #pragma unroll
                 for (int blk = 0; blk < 2; ++blk) {
-                    const uint8_t* at = st + blk * kBlock;
-                    uint32_t kw[2][nb], ks[2][(nb + 3) / 4];
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
-                        kv4::words<nb>(from(at + (u * 32 + lane) * nb * 4), kw[u]);
-                        kv4::bytes<nb>(from(at + kv4::key_scale_at(D) + (g + 8 * u) * nb), ks[u]);
+                        kv4::words<nb>(from(st + blk * kBlock + (u * 32 + lane) * nb * 4), kw[blk][u]);
+                        kv4::bytes<nb>(from(st + blk * kBlock + kv4::key_scale_at(D) + (g + 8 * u) * nb), ks[blk][u]);
                     }
 #pragma unroll
                     for (int j = 0; j < NT; ++j) s[blk][j][0] = s[blk][j][1] = s[blk][j][2] = s[blk][j][3] = 0.0f;
+                }
+                // (blocks by turns: a product waits for the one before it in its sum)
 #pragma unroll
-                    for (int b = 0; b < nb; b += 2) {
-                        const kv4::Scale<T> s0 = kv4::Scale<T>::of(kv4::both(ks[0], b / 2)), s1 = kv4::Scale<T>::of(kv4::both(ks[1], b / 2));
+                for (int b = 0; b < nb; b += 2) {
+                    Factor f[2][2];
 #pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            if (b + e < nb) {
-                                uint32_t x0[4], x1[4];
-                                kv4::numbers(kw[0][b + e], kv4::half_of(s0, e), x0);
-                                kv4::numbers(kw[1][b + e], kv4::half_of(s1, e), x1);
+                    for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
-                                for (int j = 0; j < NT; ++j) {
-                                    mma<T>(s[blk][j], x0[0], x1[0], x0[1], x1[1], qf[j][b + e][0], qf[j][b + e][1]);
-                                    mma<T>(s[blk][j], x0[2], x1[2], x0[3], x1[3], qf[j][b + e][2], qf[j][b + e][3]);
-                                }
+                        for (int u = 0; u < 2; ++u) f[blk][u] = Factor::of(kv4::both(ks[blk][u], b / 2) );
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        if (b + e < nb) {
+                            uint32_t x0[2][4], x1[2][4];
+#pragma unroll
+                            for (int blk = 0; blk < 2; ++blk) {
+                                kv4::numbers(kw[blk][0][b + e], f[blk][0].half(e), x0[blk]);
+                                kv4::numbers(kw[blk][1][b + e], f[blk][1].half(e), x1[blk]);
                             }
-                    }
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                                for (int blk = 0; blk < 2; ++blk)
+#pragma unroll
+                                    for (int j = 0; j < NT; ++j)
+                                        mma<T>(s[blk][j], x0[blk][2 * h], x1[blk][2 * h], x0[blk][2 * h + 1], x1[blk][2 * h + 1],
+                                               qf[j][b + e][2 * h], qf[j][b + e][2 * h + 1]);
+                        }
                 }
                 // row (key) 16 blk + g + 8 (e / 2), column (query) 8 j + 2 t + e % 2
                 float mx[NT][2];
@@ -323,7 +354,7 @@ __global__ void __launch_bounds__(32, Shape<D, NT>::kPerSm) attn_kv4_kernel(cons
 #pragma unroll
                     for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) s[blk][j][e] *= a.scale_log2;
+                        for (int e = 0; e < 4; ++e) s[blk][j][e] *= scale;
                     if (k0 + kStep > all_see) {
 #pragma unroll
                         for (int blk = 0; blk < 2; ++blk)
@@ -372,21 +403,19 @@ __global__ void __launch_bounds__(32, Shape<D, NT>::kPerSm) attn_kv4_kernel(cons
                         }
                     }
                 }
-                __syncwarp();      // the scales are there
 #pragma unroll
                 for (int blk = 0; blk < 2; ++blk) {
                     const uint8_t* at = st + blk * kBlock;
-                    uint32_t vw[2][nb], vs[2][2 * nb];
+                    uint32_t vw[2][nb];
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        kv4::words<nb>(from(at + kv4::value_at(D) + (u * 32 + lane) * nb * 4), vw[u]);
-                        kv4::words<2 * nb>(from(reinterpret_cast<const uint8_t*>(s_scale + (8 * blk + 4 * u + t) * nb)), vs[u]);
-                    }
+                    for (int u = 0; u < 2; ++u) kv4::words<nb>(from(at + kv4::value_at(D) + (u * 32 + lane) * nb * 4), vw[u]);
 #pragma unroll
                     for (int b = 0; b < nb; ++b) {
-                        uint32_t x0[4], x1[4];
-                        kv4::numbers(vw[0][b], kv4::Scale<T>::from(vs[0][2 * b], vs[0][2 * b + 1]), x0);
-                        kv4::numbers(vw[1][b], kv4::Scale<T>::from(vs[1][2 * b], vs[1][2 * b + 1]), x1);
+                        uint32_t x0[4], x1[4], f[KW];
+                        kv4::words<KW>(from(reinterpret_cast<const uint8_t*>(s_value + (16 * b + 8 * blk + t) * KW)), f);
+                        kv4::numbers(vw[0][b], Factor::from(f), x0);
+                        kv4::words<KW>(from(reinterpret_cast<const uint8_t*>(s_value + (16 * b + 8 * blk + 4 + t) * KW)), f);
+                        kv4::numbers(vw[1][b], Factor::from(f), x1);
 #pragma unroll
                         for (int j = 0; j < NT; ++j) {
                             mma<T>(o[2 * b][j], x0[0], x0[1], x1[0], x1[1], pf[blk][j][0], pf[blk][j][1]);
@@ -412,7 +441,7 @@ __global__ void __launch_bounds__(32, Shape<D, NT>::kPerSm) attn_kv4_kernel(cons
 #pragma unroll
                     for (int b = 0; b < nb; ++b)
                         *reinterpret_cast<float4*>(to + 32 * b) =
-                            make_float4(o[2 * b][j][e], o[2 * b][j][e + 2], o[2 * b + 1][j][e], o[2 * b + 1][j][e + 2]);
+                            make_float4(o[2 * b][j][e] * kUnit, o[2 * b][j][e + 2] * kUnit, o[2 * b + 1][j][e] * kUnit, o[2 * b + 1][j][e + 2] * kUnit);
                 }
             }
     }

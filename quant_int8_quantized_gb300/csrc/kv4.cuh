@@ -84,43 +84,87 @@ inline Cache cache_of(const mq_kv4* c) {
 // place of binary32's exponent are off by 2^112, subnormal ones too.
 __device__ __forceinline__ float scale_of(int c) { return __uint_as_float((uint32_t)c << 20) * 5.192296858534828e33f; }
 
-// The four pairs of 16-bit numbers n d of a word of nibbles: out[i] has the nibbles i of both halves.
-// bf16: 0x4300 | nibble is 128 + nibble, times d less 136 d (17 d: four bits by five, exact in bfloat16's eight): n d, exact.
-// f16: 0x6400 | nibble << 4 is 16 (64 + nibble), times d / 16 less 72 d (9 d: exact; below 2^16 up to d = 909): n d, exact.
+__device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }
+__device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t x) { return *reinterpret_cast<const __nv_bfloat162*>(&x); }
+template <typename V>
+__device__ __forceinline__ uint32_t as_word(const V& v) { return *reinterpret_cast<const uint32_t*>(&v); }
+
+__device__ __forceinline__ uint32_t mask_or(uint32_t x, uint32_t mask, uint32_t bits) {   // (x & mask) | bits
+    uint32_t y;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(y) : "r"(x), "r"(mask), "r"(bits));
+    return y;
+}
+
+// A word's nibbles as four pairs of 16-bit numbers n d, exact: out[i] those of the nibbles i of both halves, with a
+// pair of scales that came as bytes in the upper halves of two 16-bit words. A bit operation puts a nibble under an exponent, a fused
+// multiply-add takes out what that added:
+// bf16: 0x4300 | nibble is 128 + nibble, times d less 136 d (17 d: four bits by five, exact in bfloat16's eight).
+// f16: 0x6400 | nibble << 4 is 16 (64 + nibble), times d / 16 less 72 d (9 d; below 2^16 up to d = 909).
 template <typename T>
-struct Scale;      // a pair of scales as the numbers need them
+struct Scale;
 template <>
 struct Scale<__half> {
     __half2 mul, off;
-    __device__ __forceinline__ static Scale of(uint32_t high_bytes) {   // the bytes in the upper halves of two 16-bit words
-        const uint32_t h = high_bytes >> 1;
-        const __half2 d = *reinterpret_cast<const __half2*>(&h);
+    __device__ __forceinline__ static Scale of(uint32_t high_bytes) {
+        const __half2 d = as_half2(high_bytes >> 1);
         return {__hmul2(d, __float2half2_rn(0.0625f)), __hmul2(d, __float2half2_rn(-72.0f))};
-    }
-    __device__ __forceinline__ static Scale from(uint32_t mul, uint32_t off) {
-        return {*reinterpret_cast<const __half2*>(&mul), *reinterpret_cast<const __half2*>(&off)};
     }
 };
 template <>
 struct Scale<__nv_bfloat16> {
+    static constexpr int kWords = 2;
     __nv_bfloat162 mul, off;
     __device__ __forceinline__ static Scale of(uint32_t high_bytes) {
-        const uint32_t h = high_bytes >> 4;
-        const __nv_bfloat162 d = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&h), __float2bfloat162_rn(5.192296858534828e33f));
+        const __nv_bfloat162 d = __hmul2(as_bf162(high_bytes >> 4), __float2bfloat162_rn(5.192296858534828e33f));
         return {d, __hmul2(d, __float2bfloat162_rn(-136.0f))};
     }
-    __device__ __forceinline__ static Scale from(uint32_t mul, uint32_t off) {
-        return {*reinterpret_cast<const __nv_bfloat162*>(&mul), *reinterpret_cast<const __nv_bfloat162*>(&off)};
+    __device__ __forceinline__ static Scale from(const uint32_t* w) { return {as_bf162(w[0]), as_bf162(w[1])}; }
+    __device__ __forceinline__ void to(uint32_t* w) const { w[0] = as_word(mul), w[1] = as_word(off); }
+    // One of the two scales for both numbers (an operand's half: no instruction).
+    __device__ __forceinline__ Scale half(int e) const {
+        return e ? Scale{__high2bfloat162(mul), __high2bfloat162(off)} : Scale{__low2bfloat162(mul), __low2bfloat162(off)};
     }
 };
-// One of a pair's two scales for both numbers (an operand's half: no instruction).
-__device__ __forceinline__ Scale<__half> half_of(const Scale<__half>& s, int e) {
-    return e ? Scale<__half>{__high2half2(s.mul), __high2half2(s.off)} : Scale<__half>{__low2half2(s.mul), __low2half2(s.off)};
+__device__ __forceinline__ void numbers(uint32_t w, const Scale<__half>& s, uint32_t (&out)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        out[i] = as_word(__hfma2(as_half2(mask_or(i == 0 ? w << 4 : w >> (4 * i - 4), 0x00f000f0u, 0x64006400u)), s.mul, s.off));
 }
-__device__ __forceinline__ Scale<__nv_bfloat16> half_of(const Scale<__nv_bfloat16>& s, int e) {
-    return e ? Scale<__nv_bfloat16>{__high2bfloat162(s.mul), __high2bfloat162(s.off)}
-             : Scale<__nv_bfloat16>{__low2bfloat162(s.mul), __low2bfloat162(s.off)};
+__device__ __forceinline__ void numbers(uint32_t w, const Scale<__nv_bfloat16>& s, uint32_t (&out)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        out[i] = as_word(__hfma2(as_bf162(mask_or(w >> (4 * i), 0x000f000fu, 0x43004300u)), s.mul, s.off));
 }
+
+// In f16, an eighth of them, with one shift instead of three for two more multiplications a scale: 0x6400 | nibble is 1024 + nibble, times
+// d / 8 less 129 d; as above, times d / 128 less 9 d. 129 d stays below 2^16 up to d = 508 and has eight bits by four, d / 128 of the
+// least scale is binary16's least number: all exact. (An eighth, because 1032 d would leave the range from d = 64 on.)
+struct Eighth {
+    static constexpr int kWords = 4;
+    __half2 mul0, off0, mul1, off1;
+    __device__ __forceinline__ static Eighth of(uint32_t high_bytes) {
+        const __half2 d = as_half2(high_bytes >> 1);
+        return {__hmul2(d, __float2half2_rn(0.125f)), __hmul2(d, __float2half2_rn(-129.0f)),
+                __hmul2(d, __float2half2_rn(0.0078125f)), __hmul2(d, __float2half2_rn(-9.0f))};
+    }
+    __device__ __forceinline__ static Eighth from(const uint32_t* w) { return {as_half2(w[0]), as_half2(w[1]), as_half2(w[2]), as_half2(w[3])}; }
+    __device__ __forceinline__ void to(uint32_t* w) const {
+        w[0] = as_word(mul0), w[1] = as_word(off0), w[2] = as_word(mul1), w[3] = as_word(off1);
+    }
+    __device__ __forceinline__ Eighth half(int e) const {
+        return e ? Eighth{__high2half2(mul0), __high2half2(off0), __high2half2(mul1), __high2half2(off1)}
+                 : Eighth{__low2half2(mul0), __low2half2(off0), __low2half2(mul1), __low2half2(off1)};
+    }
+};
+__device__ __forceinline__ void numbers(uint32_t w, const Eighth& s, uint32_t (&out)[4]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t x = i ? w >> 8 : w;
+        out[2 * i] = as_word(__hfma2(as_half2(mask_or(x, 0x000f000fu, 0x64006400u)), s.mul0, s.off0));
+        out[2 * i + 1] = as_word(__hfma2(as_half2(mask_or(x, 0x00f000f0u, 0x64006400u)), s.mul1, s.off1));
+    }
+}
+
 // nb consecutive words (or bytes), aligned as far as nb allows.
 template <int nb, typename P>
 __device__ __forceinline__ void words(P load, uint32_t (&w)[nb]) {
@@ -161,30 +205,6 @@ __device__ __forceinline__ uint32_t twice(const uint32_t (&w)[n], int i) {
 template <int n>
 __device__ __forceinline__ uint32_t both(const uint32_t (&w)[n], int i) {
     return __byte_perm(w[i / 2], 0, i % 2 ? 0x3424 : 0x1404);
-}
-
-__device__ __forceinline__ uint32_t mask_or(uint32_t x, uint32_t mask, uint32_t bits) {   // (x & mask) | bits
-    uint32_t y;
-    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(y) : "r"(x), "r"(mask), "r"(bits));
-    return y;
-}
-__device__ __forceinline__ void numbers(uint32_t w, const Scale<__half>& s, uint32_t (&out)[4]) {
-    const uint32_t x[4] = {w << 4, w, w >> 4, w >> 8};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t y = mask_or(x[i], 0x00f000f0u, 0x64006400u);
-        const __half2 z = __hfma2(*reinterpret_cast<const __half2*>(&y), s.mul, s.off);
-        out[i] = *reinterpret_cast<const uint32_t*>(&z);
-    }
-}
-__device__ __forceinline__ void numbers(uint32_t w, const Scale<__nv_bfloat16>& s, uint32_t (&out)[4]) {
-    const uint32_t x[4] = {w, w >> 4, w >> 8, w >> 12};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t y = mask_or(x[i], 0x000f000fu, 0x43004300u);
-        const __nv_bfloat162 z = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&y), s.mul, s.off);
-        out[i] = *reinterpret_cast<const uint32_t*>(&z);
-    }
 }
 
 }  // namespace kv4
