@@ -5,13 +5,16 @@
 // cos and sin come once per token out of shared memory. Keys and values then change hands through shared memory so that a
 // lane has the eight dims of one word of the page, four lanes a block of 32 dims: two shuffles find its largest
 // magnitude a, the scale is the least one with 7 d >= a, the numbers are rint(y / d).
-// That rounding is decided for y as the formula has it, not as 32 bits do: y is off by at most 2^-19 of the head's
-// largest magnitude (norm: 8 fused additions, 5 levels of shuffles, square root, division, two products, less than 11 units of
-// 2^-24; cos and sin less than 4, the rotation's products and sum and rot_scale 4; a pair is at most sqrt(2) times the
-// largest), and where a border lies within that of y or of a, the warp computes its heads again in 64 bits. So the
-// bytes do not depend on how 32-bit sums are ordered. One head in some sixty is near a border.
-// Values are the inputs themselves: their borders (k + 1/2) d are exact in 32 bits.
-// Bound: HBM, 4 bytes read an element, 2 written (q) or 17/32.
+// That rounding is decided for y as the formula has it, not as 32 bits do. In units of u = 2^-24: a cosine or sine is off by the angle's
+// rounding (1.6), the function's (1) and rot_scale's product (0.5); a pair's product with them by sqrt(2) 3.1 and its own two
+// roundings, 6.4 of the pair's length, which is sqrt(2) times the head's largest magnitude at most: 9.1 u of it. A norm's factor
+// is off by half of the sum's 9 (two roundings, two levels of additions, up to five of shuffles) and by six more roundings' 5: 9.5
+// of the pair's length besides, 22.5 u in all. Where a border lies within that of y or of the block's largest, the row
+// goes to a list, and the block computes those rows again in 64 bits at its end, a thread a pair (in the warps that met them, all
+// heads of a warp at once, they held up 16384 tokens for 60 us of 164). So the bytes do not depend on how 32-bit sums are ordered.
+// Values are the inputs themselves: 32 bits tell on which side of a border they lie.
+// Bound: HBM, 4 bytes read an element, 2 written (q) or 17/32. Measured: 16384 tokens of 40 + 8 heads of 128, 115 us, 5.4 TB/s; 3314 of
+// 28 + 4, 27 us; one token, 3 us.
 
 #include <cmath>
 
@@ -20,8 +23,8 @@
 namespace kv4 {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr float kOff = 1.9073486328125e-06f;      // 2^-19, see above
+constexpr int kThreads = 128, kList = 64;
+constexpr float kOffNorm = 24.5f * 5.9604644775390625e-08f, kOffTurn = 9.6f * 5.9604644775390625e-08f;   // see above
 
 struct FillArgs {
     const float* x[3];          // q, k, v (NULL: left out)
@@ -47,6 +50,33 @@ __device__ __forceinline__ float2 turn(int pos, float freq, float by) {
     return make_float2(c * by, s * by);
 }
 
+// sin and cos of pi t for |t| <= 1 by their power series, to 2^-52. (Few instructions: where this runs, its code is seldom at hand,
+// and fetching it takes longer than running it.)
+__device__ __forceinline__ void sincos_pi(double t, double& s, double& c) {
+    const double k = rint(2.0 * t), x = fma(-0.5, k, t) * 3.14159265358979323846, z = x * x;   // |x| <= pi / 4
+    double u = 1.0 / 1307674368000.0, v = 1.0 / 20922789888000.0;
+    u = fma(u, -z, 1.0 / 6227020800.0), v = fma(v, -z, 1.0 / 87178291200.0);
+    u = fma(u, -z, 1.0 / 39916800.0), v = fma(v, -z, 1.0 / 479001600.0);
+    u = fma(u, -z, 1.0 / 362880.0), v = fma(v, -z, 1.0 / 3628800.0);
+    u = fma(u, -z, 1.0 / 5040.0), v = fma(v, -z, 1.0 / 40320.0);
+    u = fma(u, -z, 1.0 / 120.0), v = fma(v, -z, 1.0 / 720.0);
+    u = fma(u, -z, 1.0 / 6.0), v = fma(v, -z, 1.0 / 24.0);
+    u = fma(u, -z, 1.0), v = fma(v, -z, 0.5);
+    u *= x, v = fma(v, -z, 1.0);
+    const int q = (int)k & 3;
+    s = q & 1 ? v : u;
+    c = q & 1 ? u : v;
+    if (q >= 2) s = -s;
+    if (q == 1 || q == 2) c = -c;
+}
+// 1 / sqrt(x) in 64 bits: two steps of Newton's from the 32-bit one.
+__device__ __forceinline__ double inv_sqrt(double x) {
+    double y = rsqrtf((float)x);
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) y = fma(fma(-x * y, y, 1.0), 0.5 * y, y);
+    return y;
+}
+
 // The least code whose 7 d is `a` or more.
 __device__ __forceinline__ int code_of(float a) {
     if (!(a < 3360.0f)) return kMostCode;
@@ -64,13 +94,12 @@ __device__ __forceinline__ int code_of(double a) {
     return c;
 }
 
-// rint(y / d), ties to even, and the rest y - n d (exact: both have few bits, and it is no longer than y).
-__device__ __forceinline__ float nearest(float y, float d, float inv, float& rest) {
-    float k = rintf(y * inv);
-    k = fminf(fmaxf(k, -8.0f), 8.0f);
-    rest = fmaf(-k, d, y);
-    const float over = 2.0f * fabsf(rest);
-    if (over > d || (over == d && ((int)k & 1))) k += copysignf(1.0f, rest);
+// rint(y / d) within -7 .. 7, ties to even, exactly (binary32: y - n d has few bits, and is no longer than y).
+template <typename F>
+__device__ __forceinline__ float nearest(F y, float d, float inv) {
+    float k = fminf(fmaxf(rintf((float)y * inv), -8.0f), 8.0f);
+    const F rest = fma(-(F)k, (F)d, y), over = 2 * fabs(rest);
+    if (over > d || (over == d && ((int)k & 1))) k += rest < 0 ? -1.0f : 1.0f;
     return fminf(fmaxf(k, -7.0f), 7.0f);
 }
 
@@ -79,7 +108,8 @@ __device__ __forceinline__ float nearest(float y, float d, float inv, float& res
 template <typename T, int LG, bool INTER, bool VEC>
 __global__ void __launch_bounds__(kThreads) fill_kernel(const FillArgs a) {
     extern __shared__ float2 s_turn[];                 // [n_pairs]
-    __shared__ double s_row[kThreads / LG][LG * 8];    // a head's row on its way from pairs to words
+    __shared__ float s_row[kThreads / LG][LG * 8 + 16]; // a head's row on its way from pairs to words (heads in other banks)
+    __shared__ int s_list[kList], s_n;                 // rows that want 64 bits
     mq_grid_release();
     mq_grid_wait();
     const int m = blockIdx.x;                          // the token
@@ -100,7 +130,6 @@ __global__ void __launch_bounds__(kThreads) fill_kernel(const FillArgs a) {
     };
     auto low = [&](int np) { return INTER || lane * 4 >= np ? lane * 8 : lane * 4; };
     auto high = [&](int np) { return INTER || lane * 4 >= np ? lane * 8 + 4 : np + lane * 4; };
-    auto at = [&](int np, int i) { return VEC ? (i < 4 ? low(np) + i : high(np) + i - 4) : place(np, i); };
     auto fetch = [&](int r, Row& x) {
         const bool live = r < rows && lane * 8 < D;
         const int hr = live ? r : 0;
@@ -140,6 +169,7 @@ __global__ void __launch_bounds__(kThreads) fill_kernel(const FillArgs a) {
         row = __ldca(a.row + m);
         if ((unsigned)seq < (unsigned)a.c.n && row >= 0 && row >> a.c.shift < a.c.width) page = a.c.page(seq, row);
     }
+    if (threadIdx.x == 0) s_n = 0;
     __syncthreads();
     for (int r = r_first; r - group < rows; r += r_step) {
         Row next;
@@ -154,10 +184,14 @@ __global__ void __launch_bounds__(kThreads) fill_kernel(const FillArgs a) {
         now = next;
         const float* w = what == 2 ? nullptr : a.w[what];
         float ss = 0.0f;
+        if (a.w[0] || a.w[1]) {
+            float pr[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
+            for (int i = 0; i < 4; ++i) pr[i] = fmaf(v[2 * i], v[2 * i], v[2 * i + 1] * v[2 * i + 1]);
+            ss = (pr[0] + pr[1]) + (pr[2] + pr[3]);
 #pragma unroll
-        for (int o = LG / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            for (int o = LG / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        }
         if (w && live) {
             const float sc = 1.0f / sqrtf(ss / (float)D + a.eps);
             if constexpr (VEC) {
@@ -200,24 +234,26 @@ __global__ void __launch_bounds__(kThreads) fill_kernel(const FillArgs a) {
         if (__all_sync(0xffffffffu, what == 0) || page < 0) continue;      // (the page is the token's: the same for all)
 
         // ------------------------------------------------------------ keys and values to words and scales
-        float* row32 = reinterpret_cast<float*>(s_row[group]);
-        if (live && what == 1) {
-            if constexpr (VEC) {
-                *reinterpret_cast<float4*>(row32 + lo) = make_float4(v[0], v[1], v[2], v[3]);
-                *reinterpret_cast<float4*>(row32 + hi) = make_float4(v[4], v[5], v[6], v[7]);
-            } else {
+        if constexpr (!(INTER && VEC)) {               // (neighbours and values lie as they will be packed)
+            float* row32 = s_row[group];
+            if (live && what == 1) {
+                if constexpr (VEC) {
+                    *reinterpret_cast<float4*>(row32 + lo) = make_float4(v[0], v[1], v[2], v[3]);
+                    *reinterpret_cast<float4*>(row32 + hi) = make_float4(v[4], v[5], v[6], v[7]);
+                } else {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) row32[place(np, i)] = v[i];
+                    for (int i = 0; i < 8; ++i) row32[place(np, i)] = v[i];
+                }
             }
+            __syncwarp();
+            if (live && what == 1) {
+                const float4 u0 = *reinterpret_cast<const float4*>(row32 + lane * 8);
+                const float4 u1 = *reinterpret_cast<const float4*>(row32 + lane * 8 + 4);
+                v[0] = u0.x, v[1] = u0.y, v[2] = u0.z, v[3] = u0.w;
+                v[4] = u1.x, v[5] = u1.y, v[6] = u1.z, v[7] = u1.w;
+            }
+            __syncwarp();
         }
-        __syncwarp();
-        if (live && what == 1) {
-            const float4 u0 = *reinterpret_cast<const float4*>(row32 + lane * 8);
-            const float4 u1 = *reinterpret_cast<const float4*>(row32 + lane * 8 + 4);
-            v[0] = u0.x, v[1] = u0.y, v[2] = u0.z, v[3] = u0.w;
-            v[4] = u1.x, v[5] = u1.y, v[6] = u1.z, v[7] = u1.w;
-        }
-        __syncwarp();
         float most = 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(v[i]));
@@ -226,99 +262,113 @@ __global__ void __launch_bounds__(kThreads) fill_kernel(const FillArgs a) {
         float all = most;
 #pragma unroll
         for (int o = 4; o < LG; o <<= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, o));
-        const bool exact = what != 1 || (!w && np == 0);                    // v is what there is to round
-        const float off = exact ? 0.0f : all * kOff;
+        const bool exact = what != 1 || (!w && n == 0);                     // v is what there is to round
+        const float off = exact ? 0.0f : all * (w ? kOffNorm : kOffTurn);
         int code = code_of(most);
-        float d = scale_of(code);
-        const float inv = d > 0.0f ? 1.0f / d : 0.0f;
-        bool near = !exact && most - off <= 3360.0f &&
-                    (7.0f * d < most + off || (code > 0 && 7.0f * scale_of(code - 1) >= most - off));
-        float num[8];
+        const float d = scale_of(code);
+        const float inv = d > 0.0f ? __frcp_rn(d) : 0.0f;
+        // rint(v / d) + 8 in the last bits of v / d + 1.5 2^23 + 8, ties to even. The quotient is the correctly rounded one (a step
+        // from the product with the rounded reciprocal by the exact rest), and that is a tie only where v / d is: d has four bits, so
+        // another v / d lies more than half a unit away.
+        float quot[8], far = 0.0f;
+        uint32_t num[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            float rest;
-            num[i] = nearest(v[i], d, inv, rest);
-            near |= !exact && fabsf(fabsf(rest) - 0.5f * d) <= off;
+            const float q = v[i] * inv;
+            quot[i] = fmaf(fmaf(-q, d, v[i]), inv, q);
         }
-        if (__any_sync(0xffffffffu, near && live)) {
-            Row x;
-            fetch(r, x);
-            double y[8], sum = 0.0;
+        if (__any_sync(0xffffffffu, !(most <= 3360.0f)))
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                y[i] = x.v[i];
-                sum += y[i] * y[i];
+            for (int i = 0; i < 8; ++i) quot[i] = fminf(fmaxf(quot[i], -7.0f), 7.0f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float m = quot[i] + 12582920.0f;
+            far = fmaxf(far, fabsf(quot[i] - (m - 12582920.0f)));
+            num[i] = __float_as_uint(m);
+        }
+        // (a rotated or normed v is off by `off`: what lies next to a border goes to the list)
+        const bool near = !exact && (!(far < 0.5f - 1e-6f - off * inv) || !(most < 3360.0f - off) ||
+                          (most > 0.0f && (7.0f * d < most + off || (code > 0 && 7.0f * scale_of(code - 1) >= most - off))));
+        const uint32_t again = __ballot_sync(0xffffffffu, near && live) >> (threadIdx.x & 31 & ~(LG - 1)) &
+                               (LG == 32 ? ~0u : (1u << (LG & 31)) - 1);
+        if (again) {                                   // (all of a head's lanes)
+            if (lane == 0) {
+                const int k = atomicAdd(&s_n, 1);
+                if (k < kList) s_list[k] = r;
             }
-#pragma unroll
-            for (int o = LG / 2; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            double* row64 = s_row[group];
-            if (live && what == 1) {
-                if (w) {
-                    const double sc = 1.0 / sqrt(sum / D + (double)a.eps);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) y[i] *= sc * (double)w[at(np, i)];
-                }
-#pragma unroll 1
-                for (int i = 0; i < 4; ++i) {
-                    const int p = lane * 4 + i;
-                    if (p >= np) break;
-                    float freq;
-                    const int pos = angle(p, freq);
-                    double sn, cs;
-                    sincos((double)pos * (double)freq, &sn, &cs);
-                    cs *= (double)a.rot_scale;
-                    sn *= (double)a.rot_scale;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)       // (constant places: y stays in registers)
-                        if (k == i) {
-                            double &p0 = VEC && !INTER ? y[k] : y[2 * k], &p1 = VEC && !INTER ? y[4 + k] : y[2 * k + 1];
-                            const double u = p0 * cs - p1 * sn;
-                            p1 = p0 * sn + p1 * cs;
-                            p0 = u;
-                        }
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) row64[at(np, i)] = y[i];
-            }
-            __syncwarp();
-            double top = 0.0;
-            if (live && what == 1)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    y[i] = row64[lane * 8 + i];
-                    top = fmax(top, fabs(y[i]));
-                }
-            __syncwarp();
-            top = fmax(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmax(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            if (live && what == 1) {
-                code = code_of(top);
-                d = scale_of(code);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) num[i] = d > 0.0f ? (float)fmin(fmax(rint(y[i] / (double)d), -7.0), 7.0) : 0.0f;
-            }
+            continue;
         }
         if (!live || what == 0) continue;
-        uint32_t nib[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) nib[i] = (uint32_t)((int)num[i] + 8);
+        // four numbers, and what lies above their four bits (a constant, or nothing), as one sum
+        auto four = [&](int i0, int step) { return num[i0] + 16u * num[i0 + step] + 256u * num[i0 + 2 * step] + 4096u * num[i0 + 3 * step]; };
         const int nb = D / 32, b = lane / 4, t = lane % 4, in = row & (kBlockRows - 1);
         uint8_t* block = a.c.block(page, h, row, block_bytes(D));
         if (what == 1) {
-            uint32_t word = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) word |= nib[i] << (16 * (i & 1) + 4 * (i >> 1));
-            reinterpret_cast<uint32_t*>(block)[(4 * in + t) * nb + b] = word;
+            reinterpret_cast<uint32_t*>(block)[(4 * in + t) * nb + b] = __byte_perm(four(0, 2), four(1, 2), 0x5410);
         } else {
             uint16_t* half = reinterpret_cast<uint16_t*>(block + value_at(D));
             const int p = in >> 3, tt = (in >> 1) & 3, c = in & 1;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const uint32_t u = nib[4 * k] | nib[4 * k + 1] << 4 | nib[4 * k + 2] << 8 | nib[4 * k + 3] << 12;
-                half[2 * (((8 * p + 2 * t + k) * 4 + tt) * nb + b) + c] = (uint16_t)u;
-            }
+            for (int k = 0; k < 2; ++k) half[2 * (((8 * p + 2 * t + k) * 4 + tt) * nb + b) + c] = (uint16_t)four(4 * k, 1);
         }
         if (t == 0) block[what == 1 ? key_scale_at(D) + in * nb + b : value_scale_at(D) + (in >> 1) * 2 * nb + 2 * b + (in & 1)] = (uint8_t)code;
+    }
+
+    // ---------------------------------------------------------------- rows next to a border, in 64 bits: a thread a pair
+    __syncthreads();
+    if (s_n == 0) return;
+    __shared__ double s_y[256], s_part[kThreads / 32];
+    const float* const w = a.w[1];
+    const int nb = D / 32, in = row & (kBlockRows - 1), tid = threadIdx.x, wl = tid & 31, wid = tid >> 5;
+    const bool every = s_n > kList;                    // more than the list holds: all keys of this block
+    const int k_first = every ? (int)blockIdx.y * (kThreads / LG) : 0, k_end = every ? a.h1 : s_n;
+    for (int k = k_first; k < k_end; ++k) {
+        int r = k;
+        if (!every) r = s_list[k];
+        else if (k < a.h0 || (k / (kThreads / LG)) % (int)gridDim.y != (int)blockIdx.y) continue;
+        const int h = r - a.h0;
+        const float* x = a.x[1] + (long long)m * a.stride[1] + (long long)h * D;
+        double by = 1.0;
+        if (w) {
+            double sum = 0.0;
+            for (int i = tid; i < D; i += kThreads) sum = fma((double)x[i], (double)x[i], sum);
+#pragma unroll 1
+            for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (wl == 0) s_part[wid] = sum;
+            __syncthreads();
+            by = inv_sqrt((s_part[0] + s_part[1] + s_part[2] + s_part[3]) * (1.0 / D) + (double)a.eps);
+        }
+        auto normed = [&](int i) { return w ? (double)x[i] * by * (double)w[i] : (double)x[i]; };
+        for (int p = tid; p < n; p += kThreads) {
+            float freq;
+            const int pos = angle(p, freq);
+            const double t = (double)pos * (double)freq * 0.31830988618379067154;
+            double sn, cs;
+            sincos_pi(t - 2.0 * rint(0.5 * t), sn, cs);
+            cs *= (double)a.rot_scale;
+            sn *= (double)a.rot_scale;
+            const int i0 = INTER ? 2 * p : p, i1 = INTER ? 2 * p + 1 : p + n;
+            const double u = normed(i0), q = normed(i1);
+            s_y[i0] = u * cs - q * sn;
+            s_y[i1] = u * sn + q * cs;
+        }
+        for (int i = 2 * n + tid; i < D; i += kThreads) s_y[i] = normed(i);
+        __syncthreads();
+        uint8_t* block = a.c.block(page, h, row, block_bytes(D));
+        for (int b = wid; b < nb; b += kThreads / 32) {
+            const double y = s_y[32 * b + wl];
+            long long top = __double_as_longlong(y) & 0x7fffffffffffffffLL;   // (numbers without their sign are in the order of their bits)
+#pragma unroll 1
+            for (int o = 16; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const int code = code_of(__longlong_as_double(top));
+            const float d = scale_of(code);
+            uint32_t word = (8u + (int)nearest(y, d, d > 0.0f ? 1.0f / d : 0.0f)) << (16 * (wl & 1) + 4 * ((wl & 7) >> 1));
+#pragma unroll
+            for (int o = 4; o >= 1; o >>= 1) word |= __shfl_xor_sync(0xffffffffu, word, o);
+            if ((wl & 7) == 0) reinterpret_cast<uint32_t*>(block)[(4 * in + (wl >> 3)) * nb + b] = word;
+            if (wl == 0) block[key_scale_at(D) + in * nb + b] = (uint8_t)code;
+        }
+        __syncthreads();
     }
 }
 

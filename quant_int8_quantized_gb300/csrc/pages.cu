@@ -15,7 +15,7 @@ namespace pages {
 namespace {
 
 constexpr int kThreads = 1024, kBlocks = 8, kAll = kThreads * kBlocks;
-constexpr int kChunk = 256;      // table entries of a row that a warp takes at once
+constexpr int kChunk = 128;      // table entries of a row that a warp takes at once, four a lane
 
 struct Space {                   // of the workspace
     int32_t* tmp;                // [m][width] kept entries
@@ -48,41 +48,47 @@ Space space_of(uint8_t* ws, long long m, long long width, long long P) {
     return s;
 }
 
-// Sums over the cluster, in thread order: `before` this thread's number, and all. Barriers of the whole cluster.
-struct Scan {
-    int before, all;
-};
-__device__ __forceinline__ Scan scan(int x, int* s_warp, int* s_block) {
+// Sums of n numbers a thread over the cluster, in thread order: x becomes this thread's sum before it, all the whole. Once in a kernel; a
+// barrier of the whole cluster has to follow before a block ends.
+template <int n>
+__device__ __forceinline__ void scan(int (&x)[n], int (&all)[n]) {
+    __shared__ int s_warp[n][32], s_block[n];
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    int upto = x;
+    int upto[n];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += y;
+    for (int k = 0; k < n; ++k) {
+        upto[k] = x[k];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, upto[k], o);
+            if (lane >= o) upto[k] += y;
+        }
+        if (lane == 31) s_warp[k][wid] = upto[k];
     }
-    if (lane == 31) s_warp[wid] = upto;
     __syncthreads();
-    if (wid == 0) {
-        int y = s_warp[lane];
+    if (wid < n) {
+        int y = s_warp[wid][lane];
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int z = __shfl_up_sync(0xffffffffu, y, o);
             if (lane >= o) y += z;
         }
-        s_warp[lane] = y;
-        if (lane == 31) *s_block = y;
+        s_warp[wid][lane] = y;
+        if (lane == 31) s_block[wid] = y;
     }
     mq_cluster_sync();
-    Scan r = {upto - x + (wid > 0 ? s_warp[wid - 1] : 0), 0};
     const int rank = (int)mq_cluster_rank();
 #pragma unroll
-    for (int i = 0; i < kBlocks; ++i) {
-        const int y = mq_remote(s_block, i);
-        if (i < rank) r.before += y;
-        r.all += y;
+    for (int k = 0; k < n; ++k) {
+        x[k] = upto[k] - x[k] + (wid > 0 ? s_warp[k][wid - 1] : 0);
+        all[k] = 0;
+#pragma unroll
+        for (int i = 0; i < kBlocks; ++i) {
+            const int y = mq_remote(s_block + k, i);
+            if (i < rank) x[k] += y;
+            all[k] += y;
+        }
     }
-    mq_cluster_sync();           // before anyone's sums change
-    return r;
 }
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return (int)(((long long)a + b - 1) / b); }
@@ -95,7 +101,6 @@ struct NextArgs {
 };
 
 __global__ void __launch_bounds__(kThreads) next_kernel(const NextArgs a) {
-    __shared__ int s_warp[32], s_block;
     mq_grid_release();
     mq_grid_wait();
     const int id = (int)mq_cluster_rank() * kThreads + threadIdx.x, lane = threadIdx.x & 31;
@@ -124,76 +129,92 @@ __global__ void __launch_bounds__(kThreads) next_kernel(const NextArgs a) {
         const int f = a.from ? __ldca(a.from + b) : b;
         const int2 x = __ldcg(reinterpret_cast<const int2*>(a.s.info) + 2 * b);
         const int kept = ceil_div(x.x, a.R);
-        for (int i = i0 + lane; i < min(i0 + kChunk, a.width); i += 32) {
-            int e = -1;
-            if (i < kept) {
-                e = __ldca(a.table + (long long)f * a.width + i);
-                if ((unsigned)e < (unsigned)a.P) {
-                    atomicAdd(a.s.held + e, 1);
-                    if (i == kept - 1 && x.y > 0 && x.x % a.R != 0) {
-                        atomicAdd(a.s.writers + e, 1);
-                        atomicMin(a.s.first + e, b);
-                    }
+        int e[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int i = i0 + 32 * k + lane;
+            e[k] = i < kept ? __ldca(a.table + (long long)f * a.width + i) : -1;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int i = i0 + 32 * k + lane;
+            if ((unsigned)e[k] < (unsigned)a.P) {
+                atomicAdd(a.s.held + e[k], 1);
+                if (i == kept - 1 && x.y > 0 && x.x % a.R != 0) {
+                    atomicAdd(a.s.writers + e[k], 1);
+                    atomicMin(a.s.first + e[k], b);
                 }
             }
-            a.s.tmp[(long long)b * a.width + i] = e;
+            if (i < a.width) a.s.tmp[(long long)b * a.width + i] = e[k];
         }
     }
     mq_cluster_sync();
     // pages wanted, in the sequences' order; pages that nobody holds, in theirs
     const int bs = ceil_div(a.m, kAll), b0 = min(id * (long long)bs, (long long)a.m), b1 = min(b0 + bs, a.m);
-    auto wants = [&](int b, int2 x, int& copy) {
+    int want = 0, none = 0;
+    for (int b = b0; b < b1; ++b) {
+        const int2 x = __ldcg(reinterpret_cast<const int2*>(a.s.info) + 2 * b);
         const int kept = ceil_div(x.x, a.R);
-        copy = 0;
+        int copy = 0;
         if (x.y > 0 && x.x % a.R != 0) {
             const int e = __ldcg(a.s.tmp + (long long)b * a.width + kept - 1);
             if ((unsigned)e < (unsigned)a.P) {
-                const int h = __ldcg(a.s.held + e);
-                copy = h > 1 && !(__ldcg(a.s.writers + e) == h && __ldcg(a.s.first + e) == b);
+                const int h = __ldcg(a.s.held + e), writers = __ldcg(a.s.writers + e), first = __ldcg(a.s.first + e);
+                copy = h > 1 && !(writers == h && first == b);
             }
         }
-        return copy + ceil_div(x.x + x.y, a.R) - kept;
-    };
-    int want = 0;
-    for (int b = b0; b < b1; ++b) {
-        int copy;
-        want += wants(b, __ldcg(reinterpret_cast<const int2*>(a.s.info) + 2 * b), copy);
+        const int n = copy + ceil_div(x.x + x.y, a.R) - kept;
+        reinterpret_cast<int2*>(a.s.info)[2 * b + 1] = make_int2(n, copy);
+        want += n;
     }
     const int ps = ceil_div(a.P, kAll), p0 = min(id * (long long)ps, (long long)a.P), p1 = min(p0 + ps, a.P);
-    int none = 0;
-    for (int p = p0; p < p1; ++p) none += __ldcg(a.s.held + p) == 0;
-    const Scan w = scan(want, s_warp, &s_block), z = scan(none, s_warp, &s_block), t = scan(longs, s_warp, &s_block);
-    const bool enough = w.all <= z.all;
-    int rank = w.before;
+    uint32_t empty = 0;                               // the first 32 of this thread's pages
+#pragma unroll 8
+    for (int p = p0; p < p1; ++p) {
+        const bool x = __ldcg(a.s.held + p) == 0;
+        none += x;
+        if (p - p0 < 32) empty |= (uint32_t)x << (p - p0);
+    }
+    int before[3] = {want, none, longs}, all[3];
+    scan(before, all);
+    const bool enough = all[0] <= all[1];
+    int rank = before[0];
     for (int b = b0; b < b1; ++b) {
-        const int2 x = __ldcg(reinterpret_cast<const int2*>(a.s.info) + 2 * b);
-        int copy;
-        const int n = wants(b, x, copy);
-        reinterpret_cast<int2*>(a.s.info)[2 * b + 1] = make_int2(rank, copy);
+        int4 x = __ldcg(reinterpret_cast<const int4*>(a.s.info) + b);
         a.len_out[b] = enough ? x.x + x.y : x.x;
+        const int n = x.z;
+        a.s.info[4 * b + 2] = rank;
         rank += n;
     }
-    rank = z.before;
-    for (int p = p0; p < p1; ++p)
-        if (__ldcg(a.s.held + p) == 0) a.s.free[rank++] = p;
+    rank = before[1];
+    if (none > 0)
+        for (int p = p0; p < p1; ++p)
+            if (p - p0 < 32 ? empty >> (p - p0) & 1 : __ldcg(a.s.held + p) == 0) a.s.free[rank++] = p;
     if (id == 0) {
-        a.status[0] = enough ? 0 : w.all - z.all;
-        a.status[1] = enough ? z.all - w.all : z.all;
-        a.status[2] = t.all;
+        a.status[0] = enough ? 0 : all[0] - all[1];
+        a.status[1] = enough ? all[1] - all[0] : all[1];
+        a.status[2] = all[2];
     }
     mq_cluster_sync();
     for (long long u = id >> 5; u < (long long)a.m * chunks; u += kAll / 32) {
         const int b = (int)(u / chunks), i0 = (int)(u - (long long)b * chunks) * kChunk;
         const int4 x = __ldcg(reinterpret_cast<const int4*>(a.s.info) + b);
         const int kept = ceil_div(x.x, a.R), first = kept - x.w, end = ceil_div(x.x + x.y, a.R);
-        for (int i = i0 + lane; i < min(i0 + kChunk, a.width); i += 32) {
-            int e = __ldcg(a.s.tmp + (long long)b * a.width + i);
+        int e[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int i = i0 + 32 * k + lane;
+            e[k] = i < a.width ? __ldcg(a.s.tmp + (long long)b * a.width + i) : -1;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int i = i0 + 32 * k + lane;
             if (enough && i >= first && i < end) {
                 const int to = __ldcg(a.s.free + x.z + i - first);
-                if (i < kept) a.s.copies[atomicAdd(a.s.count, 1)] = make_int2(e, to);
-                e = to;
+                if (i < kept) a.s.copies[atomicAdd(a.s.count, 1)] = make_int2(e[k], to);
+                e[k] = to;
             }
-            a.table_out[(long long)b * a.width + i] = e;
+            if (i < a.width) a.table_out[(long long)b * a.width + i] = e[k];
         }
     }
 }
@@ -206,33 +227,43 @@ struct CompactArgs {
 };
 
 __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactArgs a) {
-    __shared__ int s_warp[32], s_block;
     mq_grid_release();
     mq_grid_wait();
     const int id = (int)mq_cluster_rank() * kThreads + threadIdx.x, lane = threadIdx.x & 31;
     for (int p = id; p < a.P; p += kAll) a.s.held[p] = 0;
     mq_cluster_sync();
     const int chunks = ceil_div(a.width, kChunk);
-    auto rows = [&](auto f) {      // every entry: its place, and whether its sequence holds rows there
+    auto rows = [&](auto load, auto f) {     // every entry: its place, and what it is if its sequence holds rows there
         for (long long u = id >> 5; u < (long long)a.n * chunks; u += kAll / 32) {
             const int b = (int)(u / chunks), i0 = (int)(u - (long long)b * chunks) * kChunk;
             const int used = ceil_div(min(max(__ldca(a.len + b), 0), a.width * a.R), a.R);
-            for (int i = i0 + lane; i < min(i0 + kChunk, a.width); i += 32) f((long long)b * a.width + i, i < used);
+            int e[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int i = i0 + 32 * k + lane;
+                e[k] = i < used ? load((long long)b * a.width + i) : -1;
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int i = i0 + 32 * k + lane;
+                if (i < a.width) f((long long)b * a.width + i, e[k]);
+            }
         }
     };
-    rows([&](long long at, bool used) {
-        if (!used) return;
-        const int e = __ldca(a.table + at);
-        if ((unsigned)e < (unsigned)a.P) a.s.held[e] = 1;
-    });
+    rows([&](long long at) { return __ldca(a.table + at); },
+         [&](long long, int e) {
+             if ((unsigned)e < (unsigned)a.P) a.s.held[e] = 1;
+         });
     mq_cluster_sync();
     const int ps = ceil_div(a.P, kAll), p0 = min(id * (long long)ps, (long long)a.P), p1 = min(p0 + ps, a.P);
     int mine = 0;
+#pragma unroll 8
     for (int p = p0; p < p1; ++p) mine += __ldcg(a.s.held + p);
-    const Scan z = scan(mine, s_warp, &s_block);
-    const int U = z.all;
+    int first[1] = {mine}, all[1];
+    scan(first, all);
+    const int U = all[0];
     // places below U that are free, in order; live pages before page U
-    int before = z.before;
+    int before = first[0];
     for (int p = p0; p < p1; ++p) {
         if (p == U) a.s.count[1] = before;
         const int h = __ldcg(a.s.held + p);
@@ -246,7 +277,7 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactArgs a) 
     mq_cluster_sync();
     const int below = __ldcg(a.s.count + 1);
     if (id == 0) a.s.count[0] = U - below;
-    before = z.before;
+    before = first[0];
     for (int p = p0; p < p1; ++p) {
         const int h = __ldcg(a.s.held + p);
         int to = h ? p : -1;
@@ -258,14 +289,12 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactArgs a) 
         before += h;
     }
     mq_cluster_sync();
-    rows([&](long long at, bool used) {
-        int e = -1;
-        if (used) {
-            e = __ldca(a.table + at);
-            if ((unsigned)e < (unsigned)a.P) e = __ldcg(a.where + e);
-        }
-        a.table_out[at] = e;
-    });
+    rows(
+        [&](long long at) {
+            const int e = __ldca(a.table + at);
+            return (unsigned)e < (unsigned)a.P ? __ldcg(a.where + e) : e;
+        },
+        [&](long long at, int e) { a.table_out[at] = e; });
 }
 
 // ---------------------------------------------------------------------------------------------- copies
@@ -302,7 +331,9 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const CopyArgs a) {
     }
 }
 
-int launch_copies(const mq_pool* pool, const Space& s, long long most, cudaStream_t stream) {
+// per_sm: blocks an SM at most. Blocks that take turns on an SM leave it to the scheduler where there is room: 1.6 GB of pages moved
+// with 8 an SM (all resident) 266 us, 64: 247.
+int launch_copies(const mq_pool* pool, const Space& s, long long most, int per_sm, cudaStream_t stream) {
     CopyArgs a;
     a.data = static_cast<uint8_t*>(pool->data);
     a.page_stride = pool->page_stride;
@@ -312,7 +343,7 @@ int launch_copies(const mq_pool* pool, const Space& s, long long most, cudaStrea
     a.count = s.count;
     a.layers = pool->layers;
     a.parts = (int)((pool->page_bytes + kPart - 1) / kPart);
-    const long long units = most * pool->layers * a.parts, held = 8LL * mq::num_sms();
+    const long long units = most * pool->layers * a.parts, held = (long long)per_sm * mq::num_sms();
     if (units == 0) return MQ_OK;
     return mq::launch_pdl(copy_kernel, dim3((unsigned)(units < held ? units : held)), dim3(kCopyThreads), 0, stream, a);
 }
@@ -379,7 +410,7 @@ extern "C" int mq_pages_next(const mq_pool* pool, const int32_t* table, const in
     const Space s = space_of(static_cast<uint8_t*>(ws), m, width, pool->n_pages);
     const NextArgs a = {table, len, from, keep, add, table_out, len_out, status, s, n, m, width, pool->n_pages, pool->page_rows};
     rc = launch_tables(next_kernel, a, stream);
-    return rc != MQ_OK || !add ? rc : launch_copies(pool, s, m, stream);
+    return rc != MQ_OK || !add ? rc : launch_copies(pool, s, m, 16, stream);
 }
 
 extern "C" int mq_pages_compact(const mq_pool* pool, const int32_t* table, const int32_t* len, int n, int width, int32_t* table_out,
@@ -401,5 +432,5 @@ extern "C" int mq_pages_compact(const mq_pool* pool, const int32_t* table, const
     rc = launch_tables(compact_kernel, a, stream);
     if (rc != MQ_OK) return rc;
     const long long most = (long long)n * width < pool->n_pages ? (long long)n * width : pool->n_pages;
-    return launch_copies(pool, s, most, stream);
+    return launch_copies(pool, s, most, 64, stream);
 }
