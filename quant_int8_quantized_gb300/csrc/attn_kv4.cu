@@ -31,21 +31,24 @@ __device__ unsigned int g_kv4_error;   // bit 0: a bounded wait gave up
 __device__ int g_kv4_skip_tile;        // test builds only: block 0 leaves out its first tile
 #endif
 
-constexpr int kTileExtra = 2;          // what beginning and ending a segment costs, in tiles
 
-constexpr int keys_of(int D) { return D <= 64 ? 64 : 32; }    // of a tile
+constexpr int keys_of(int D, int NT) { return D <= 64 || (D <= 128 && NT == 2) ? 64 : 32; }    // of a tile (measured)
 constexpr int kStep = 32;              // keys that are multiplied at once
 
 template <int D, int NT>
 struct Shape {
-    static constexpr int kKeys = keys_of(D);
+    static constexpr int kKeys = keys_of(D, NT);
     static constexpr int kTile = kKeys / kv4::kBlockRows * kv4::block_bytes(D);
-    static constexpr int kStages = D <= 64 ? 2 : D <= 128 ? 3 : 2;
+    static constexpr int kStages = D <= 64 || D > 128 || NT > 1 ? 2 : 3;
     static constexpr int kRing = kStages * kTile;
-    static constexpr int kSmem = kRing + kStep / 2 * (D / 32) * 16;   // stages; a step's scales
+    static constexpr int kScales = kStep / 2 * (D / 32) * 16;        // a step's
+    // more than eight rows: their operands lie in shared memory, each lane's where it alone reads them (registers would do for 8
+    // warps an SM instead of 12)
+    static constexpr bool kQueries = NT > 1;
+    static constexpr int kSmem = kRing + kScales + (kQueries ? NT * (D / 32) * 512 : 0);
     // warps an SM, as registers allow (the outputs alone are D NT / 4 of a lane's); the same number on each of its four parts: 14
     // took 15 % longer than 12 or 16
-    static constexpr int kPerSm = D * NT <= 64 ? 16 : D * NT <= 128 ? 12 : 8;
+    static constexpr int kPerSm = D * NT <= 64 ? 16 : (D <= 96 && NT <= 2) || NT == 1 && D <= 128 ? 12 : 8;
 };
 
 struct Kv4Args {
@@ -126,6 +129,7 @@ __global__ void __launch_bounds__(32, Shape<D, NT>::kPerSm) attn_kv4_kernel(cons
     __shared__ Piece s_piece[kStages + 1];
     __shared__ uint64_t s_full[kStages];
     uint32_t* const s_value = reinterpret_cast<uint32_t*>(s_ring + C::kRing);    // [block of dims][pair of rows][KW]
+    uint4* const s_query = reinterpret_cast<uint4*>(s_ring + C::kRing + C::kScales);   // [eight rows][block of dims][lane]
     mq_grid_release();
     const int lane = threadIdx.x;
     if (lane == 0) {
@@ -227,7 +231,7 @@ __global__ void __launch_bounds__(32, Shape<D, NT>::kPerSm) attn_kv4_kernel(cons
         if (w.n == 0) break;
         if (++taken == kStages + 1) taken = 0;
         // query rows 8 j + g (zeros past the last) as right operands, eight consecutive dims for each block of 32
-        uint32_t qf[NT][nb][4];
+        uint4 qf[C::kQueries ? 1 : NT][C::kQueries ? 1 : nb];
         int seen[NT][2];               // keys that rows 8 j + 2 t, 8 j + 2 t + 1 see
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
@@ -237,7 +241,8 @@ __global__ void __launch_bounds__(32, Shape<D, NT>::kPerSm) attn_kv4_kernel(cons
 #pragma unroll
             for (int b = 0; b < nb; ++b) {
                 const uint4 v = in < w.rows ? __ldca(q + 4 * b) : make_uint4(0, 0, 0, 0);
-                qf[j][b][0] = v.x, qf[j][b][1] = v.y, qf[j][b][2] = v.z, qf[j][b][3] = v.w;
+                if constexpr (C::kQueries) s_query[(j * nb + b) * 32 + lane] = v;
+                else qf[j][b] = v;
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e) seen[j][e] = w.len - p.T + 1 + p.by_group.of(w.r0 + 8 * j + 2 * t + e);
@@ -308,43 +313,54 @@ __global__ void __launch_bounds__(32, Shape<D, NT>::kPerSm) attn_kv4_kernel(cons
                     __syncwarp();
                 }
                 float s[2][NT][4];
-                uint32_t kw[2][2][nb], ks[2][2][(nb + 3) / 4];
+                // Blocks of 16 keys by turns where there are few rows: a product waits for the one before it in its sum.
+                constexpr int kAtOnce = NT == 1 ? 2 : 1;
 #pragma unroll
-                for (int blk = 0; blk < 2; ++blk) {
+                for (int blk0 = 0; blk0 < 2; blk0 += kAtOnce) {
+                    uint32_t kw[kAtOnce][2][nb], ks[kAtOnce][2][(nb + 3) / 4];
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        kv4::words<nb>(from(st + blk * kBlock + (u * 32 + lane) * nb * 4), kw[blk][u]);
-                        kv4::bytes<nb>(from(st + blk * kBlock + kv4::key_scale_at(D) + (g + 8 * u) * nb), ks[blk][u]);
+                    for (int i = 0; i < kAtOnce; ++i) {
+                        const uint8_t* at = st + (blk0 + i) * kBlock;
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            kv4::words<nb>(from(at + (u * 32 + lane) * nb * 4), kw[i][u]);
+                            kv4::bytes<nb>(from(at + kv4::key_scale_at(D) + (g + 8 * u) * nb), ks[i][u]);
+                        }
+#pragma unroll
+                        for (int j = 0; j < NT; ++j)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) s[blk0 + i][j][e] = 0.0f;
                     }
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) s[blk][j][0] = s[blk][j][1] = s[blk][j][2] = s[blk][j][3] = 0.0f;
-                }
-                // (blocks by turns: a product waits for the one before it in its sum)
+                    for (int b = 0; b < nb; b += 2) {
+                        Factor f[kAtOnce][2];
 #pragma unroll
-                for (int b = 0; b < nb; b += 2) {
-                    Factor f[2][2];
+                        for (int i = 0; i < kAtOnce; ++i)
 #pragma unroll
-                    for (int blk = 0; blk < 2; ++blk)
+                            for (int u = 0; u < 2; ++u) f[i][u] = Factor::of(kv4::both(ks[i][u], b / 2));
 #pragma unroll
-                        for (int u = 0; u < 2; ++u) f[blk][u] = Factor::of(kv4::both(ks[blk][u], b / 2) );
+                        for (int e = 0; e < 2; ++e)
+                            if (b + e < nb) {
+                                uint32_t x0[kAtOnce][4], x1[kAtOnce][4];
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        if (b + e < nb) {
-                            uint32_t x0[2][4], x1[2][4];
+                                for (int i = 0; i < kAtOnce; ++i) {
+                                    kv4::numbers(kw[i][0][b + e], f[i][0].half(e), x0[i]);
+                                    kv4::numbers(kw[i][1][b + e], f[i][1].half(e), x1[i]);
+                                }
+                                uint4 q[NT];
 #pragma unroll
-                            for (int blk = 0; blk < 2; ++blk) {
-                                kv4::numbers(kw[blk][0][b + e], f[blk][0].half(e), x0[blk]);
-                                kv4::numbers(kw[blk][1][b + e], f[blk][1].half(e), x1[blk]);
+                                for (int j = 0; j < NT; ++j)
+                                    q[j] = C::kQueries ? s_query[(j * nb + b + e) * 32 + lane] : qf[C::kQueries ? 0 : j][C::kQueries ? 0 : b + e];
+#pragma unroll
+                                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                                    for (int i = 0; i < kAtOnce; ++i) mma<T>(s[blk0 + i][j], x0[i][0], x1[i][0], x0[i][1], x1[i][1], q[j].x, q[j].y);
+#pragma unroll
+                                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                                    for (int i = 0; i < kAtOnce; ++i) mma<T>(s[blk0 + i][j], x0[i][2], x1[i][2], x0[i][3], x1[i][3], q[j].z, q[j].w);
                             }
-#pragma unroll
-                            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                                for (int blk = 0; blk < 2; ++blk)
-#pragma unroll
-                                    for (int j = 0; j < NT; ++j)
-                                        mma<T>(s[blk][j], x0[blk][2 * h], x1[blk][2 * h], x0[blk][2 * h + 1], x1[blk][2 * h + 1],
-                                               qf[j][b + e][2 * h], qf[j][b + e][2 * h + 1]);
-                        }
+                    }
                 }
                 // row (key) 16 blk + g + 8 (e / 2), column (query) 8 j + 2 t + e % 2
                 float mx[NT][2];
@@ -460,7 +476,8 @@ __global__ void __launch_bounds__(32, Shape<D, NT>::kPerSm) attn_kv4_kernel(cons
 // Tiles of eight rows that a segment has for `rows` rows of a key head; what registers allow is 4 of 128 dims.
 int tiles_of_rows(long long rows, int D) {
     const int most = D <= 128 ? 4 : 2;
-    return rows >= 8LL * most ? most : (int)((rows + 7) / 8);
+    const long long eights = (rows + 7) / 8, tiles = (eights + most - 1) / most;
+    return (int)((eights + tiles - 1) / tiles);
 }
 
 template <typename F>
@@ -537,18 +554,20 @@ Kv4Cut cut_kv4(int B, int T, int Hq, int Hkv, int D, int cap) {
     p.own_cap = cap;
     p.own = 1;
     p.rows = 8 * c.nt;
-    p.keys = keys_of(D);
+    p.keys = keys_of(D, c.nt);
     p.wide = p.rows;
     p.cost = p.wide_cost = 1;
-    p.extra = kTileExtra;
     p.lanes = 1;
     p.by_group = div_by(group);
     p.by_per_seq = div_by(own_tiles_of_rows(p));
     const long long segs = all_segs(p), most = segs * ceil_div(cap, p.keys);
-    if (most + segs * p.extra > 0x7fffffffLL || segs > 0x3fffffffLL) c.fits = false;
     int per_sm = 1;
     with_kernel(D, MQ_F16, c.nt, [&](auto, int, int n) { return per_sm = n; });
     const long long held = (long long)mq::num_sms() * per_sm;
+    // Beginning and ending a segment costs about a tile; where each tile can have a warp of its own it has (one sequence of 1000
+    // rows: 8.8 us, with runs of two tiles and more 9.9, of three 11.0).
+    p.extra = most <= 2 * held ? 0 : 1;
+    if (most + segs * p.extra > 0x7fffffffLL || segs > 0x3fffffffLL) c.fits = false;
     p.G = (int)(most < held ? most : held);
     const size_t places = (size_t)p.G + (size_t)segs;
     c.o = 0;
