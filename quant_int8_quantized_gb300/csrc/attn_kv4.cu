@@ -505,17 +505,25 @@ int with_kernel(int D, int type, int nt, F f) {
 
 size_t up16(size_t n) { return (n + 15) & ~(size_t)15; }
 
-// From so many query rows per key head on the rows are read into 16 bits for the tensor-core kernel.
-#ifndef MQ_KV4_READ_FROM
-#define MQ_KV4_READ_FROM 129
-#endif
-constexpr int kReadFrom = MQ_KV4_READ_FROM;
 // Bytes of 16-bit rows at once, unless one sequence has more.
 #ifndef MQ_KV4_READ_BYTES
 #define MQ_KV4_READ_BYTES (1LL << 30)
 #endif
 constexpr long long kReadBytes = MQ_KV4_READ_BYTES;
 
+// Whether the rows in use are read into 16 bits for the tensor-core kernel: where that is expected to take less time than walking the
+// 4-bit rows once for each tile of query rows, if the caches are as long as the tables allow. Measured, in us (walked / read): 4
+// sequences of 8192 rows, 8 key heads of 128, 80 query rows a head 74 / 92, 120: 92 / 92, 160: 110 / 89, 480: 290 / 94; of 6000 rows, 4 heads of
+// 64, 224: 33 / 54, 448: 55 / 55; one of 1500, 4 heads of 128, 448: 28 / 42, 896: 30 / 42.
+bool worth_reading(int B, int at_once, long long rows, int Hkv, int D, int cap, int nt) {
+#ifdef MQ_KV4_READ_FROM    // (test builds)
+    return rows >= MQ_KV4_READ_FROM;
+#else
+    const double width = D / 128.0, keys = (double)B * Hkv * cap;
+    const double walk = keys / 32 * ((rows + 8 * nt - 1) / (8 * nt)) * width * (1.5e-3 + 0.33e-3 * nt);
+    return walk > 30.0 * ((B + at_once - 1) / at_once) + keys * D * 4 / 3.3e6 + keys * D * 4 * (double)rows / 1.2e9;
+#endif
+}
 // How a call is cut.
 struct Kv4Cut {
     bool read, fits;
@@ -529,11 +537,12 @@ Kv4Cut cut_kv4(int B, int T, int Hq, int Hkv, int D, int cap) {
     const int group = Hq / Hkv;
     const long long rows = (long long)T * group;
     c.fits = true;
-    c.read = cap > 0 && many_takes(D, group) && rows >= kReadFrom;
+    c.nt = tiles_of_rows(rows, D);
+    const long long one = 2LL * cap * Hkv * D;                 // bytes of a sequence's keys in 16 bits
+    const long long most_at_once = one > 0 ? kReadBytes / (2 * one) : B;
+    c.at_once = (int)(most_at_once < 1 ? 1 : most_at_once < B ? most_at_once : B);
+    c.read = cap > 0 && many_takes(D, group) && worth_reading(B, c.at_once, rows, Hkv, D, cap, c.nt);
     if (c.read) {
-        const long long one = 2LL * cap * Hkv * D;             // of a sequence's keys
-        const long long most = one > 0 ? kReadBytes / (2 * one) : B;
-        c.at_once = (int)(most < 1 ? 1 : most < B ? most : B);
         c.kv = up16((size_t)one * c.at_once);
         size_t ws = mq_attn_ws_bytes(c.at_once, T, Hq, Hkv, D, 0, cap, 0);
         c.fits = ws > 0;
@@ -544,7 +553,6 @@ Kv4Cut cut_kv4(int B, int T, int Hq, int Hkv, int D, int cap) {
         c.bytes = 2 * c.kv + ws;
         return c;
     }
-    c.nt = tiles_of_rows(rows, D);
     Plan& p = c.plan;
     p.B = B;
     p.T = T;
