@@ -566,7 +566,8 @@ typedef struct mq_pool {
  *     status[2] = sequences whose L + add[b] rows are more than the table holds: they are given none.
  * table: int32 [n][width], table_out: int32 [m][width], len, len_out: int32 [n], [m]; from, keep, add: int32 [m]; status: int32 [3]; all on
  * the device, 16-byte aligned. table_out may be table and len_out may be len; they must not overlap otherwise (MQ_ERR_SHAPE). Lengths are
- * taken as 0 below 0 and as width * page_rows above it, keep and add as 0 below 0. n * width and width * page_rows below 2^31.
+ * taken as 0 below 0 and as width * page_rows above it, keep and add as 0 below 0. n * (width + 1) and width * page_rows
+ * below 2^31.
  * ws: at least mq_pages_ws_bytes(pool, max(n, m), width) bytes, for calls that do not run at the same time. Two
  * launches, programmatic dependent ones.
  */

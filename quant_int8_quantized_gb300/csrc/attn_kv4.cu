@@ -524,6 +524,7 @@ bool worth_reading(int B, int at_once, long long rows, int Hkv, int D, int cap, 
     return walk > 30.0 * ((B + at_once - 1) / at_once) + keys * D * 4 / 3.3e6 + keys * D * 4 * (double)rows / 1.2e9;
 #endif
 }
+
 // How a call is cut.
 struct Kv4Cut {
     bool read, fits;

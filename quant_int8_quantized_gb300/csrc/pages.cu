@@ -369,7 +369,7 @@ int check_pool(const mq_pool* p, bool pointers) {
 }
 
 bool valid_table(long long n, long long width, int page_rows) {
-    return n >= 0 && width >= 0 && n * width <= 0x7fffffffLL && n <= (1 << 28) && width * page_rows <= 0x7fffffffLL;
+    return n >= 0 && width >= 0 && n * (width + 1) <= 0x7fffffffLL && n <= (1 << 28) && width * page_rows <= 0x7fffffffLL;
 }
 
 // b over a, unless it begins where a does (the new table goes through the workspace).

@@ -611,6 +611,14 @@ def mq_kv_evict(src: KV, length: torch.Tensor, score: torch.Tensor, keep: int, r
 
 # ---------------------------------------------------------------- keys and values in 4 bits, on pages
 
+def _here(where: str, *tensors):
+    """The calls below run on the current device, so what they are given has to be there."""
+    now = _device() if _device is not None else torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != now:
+            raise ValueError(f"{where}: tensors must be on the current device (cuda:{now}), got {t.device}")
+
+
 class KV4:
     """Keys and values of n sequences in 4 bits (include/mq.h, mq_kv4): pages uint8 [n_pages, page bytes] (a page's bytes
     contiguous, at least mq_kv4_page_bytes), table int32 [n, width] (a row's entries contiguous), on the same device."""
@@ -677,6 +685,7 @@ def mq_qk_norm_rope_kv4(q, k, v, q_out, cache: KV4, seq=None, row=None, pos=None
     if dtype not in (torch.float16, torch.bfloat16):
         raise TypeError(f"q_out must be float16 or bfloat16, got {dtype}")
     M, out_ptr, x = _qkv(q, k, v, q_out, dtype, cache.dim, cache.heads, pos, inv_freq, axis, wq, wk, eps, interleaved)
+    _here("mq_qk_norm_rope_kv4", cache.pages, q, k, v, q_out, seq, row, pos, inv_freq, axis, wq, wk)
     seq_ptr = row_ptr = None
     if seq is not None:
         if _dev_tensor(seq, torch.int32, "seq").numel() != M:
@@ -699,6 +708,7 @@ def mq_kv4_read(src: KV4, length: torch.Tensor, dst: KV, stream=None) -> KV:
         raise TypeError("dst must be a KV")
     if _dev_tensor(length, torch.int32, "length").numel() != src.n:
         raise ValueError(f"length must hold {src.n} lengths")
+    _here("mq_kv4_read", src.pages, length, dst.k, dst.v)
     _check((_lib or lib()).mq_kv4_read(src._ref, length.data_ptr(), dst._ref, _stream(stream)), "mq_kv4_read")
     return dst
 
@@ -748,6 +758,7 @@ def mq_attn_kv4(q: torch.Tensor, cache: KV4, length: torch.Tensor, out: torch.Te
         if _dev_tensor(lse, torch.float32, "lse").numel() < rows:
             raise ValueError(f"lse needs {rows} elements")
         lse_ptr = lse.data_ptr()
+    _here("mq_attn_kv4", q, cache.pages, length, out, lse, ws)
     if ws is None:
         with _on(stream, q.device):
             ws = attn_kv4_workspace(B, T, Hq, cache.heads, D, cache.cap, q.device)
@@ -813,6 +824,7 @@ def mq_pages_next(pool: Pool, table, length, table_out, length_out, status, frm=
         if _dev_tensor(t, torch.int32, name).numel() != size:
             raise ValueError(f"{name} must hold {size} entries")
         ptr.append(t.data_ptr())
+    _here("mq_pages_next", pool.data, table, length, table_out, length_out, status, frm, keep, add, ws)
     if ws is None:
         with _on(stream, pool.data.device):
             ws = pages_workspace(pool, max(n, m), width)
@@ -833,6 +845,7 @@ def mq_pages_compact(pool: Pool, table, length, table_out, where, live, ws=None,
     for t, name, size in ((length, "length", n), (where, "where", pool.n_pages), (live, "live", 1)):
         if _dev_tensor(t, torch.int32, name).numel() != size:
             raise ValueError(f"{name} must hold {size} entries")
+    _here("mq_pages_compact", pool.data, table, length, table_out, where, live, ws)
     if ws is None:
         with _on(stream, pool.data.device):
             ws = pages_workspace(pool, n, width)

@@ -206,3 +206,18 @@ def test_scaled_frequencies():
         assert abs(r - want) <= 2.0 ** -24 * 1.01
     same, one = mq.rope_freq_scaled(n, 10000.0, device="cpu")
     assert one == 1.0 and torch.equal(same, mq.rope_freq(n, device="cpu"))
+
+
+def test_other_devices_are_refused(monkeypatch):
+    """The calls run on the current device: tensors that say they are on another are not handed on."""
+    import types
+
+    import torch
+
+    def on(i):
+        return types.SimpleNamespace(device=torch.device("cuda", i), get_device=lambda: i)
+
+    monkeypatch.setattr(mq, "_device", lambda: 1)
+    mq._here("call", on(1), None, on(1))
+    with pytest.raises(ValueError, match="current device"):
+        mq._here("call", on(1), on(0))
