@@ -93,6 +93,51 @@ __device__ __forceinline__ void scan(int (&x)[n], int (&all)[n]) {
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return (int)(((long long)a + b - 1) / b); }
 
+// The pages of a warp: `steps` times 32 of them, in order.
+struct Pages {
+    int first, end, steps;
+    __device__ __forceinline__ Pages(int P, int id) {
+        steps = ceil_div(ceil_div(P, 32), kAll / 32);
+        const long long at = (long long)(id >> 5) * steps * 32;
+        first = (int)(at < P ? at : P);
+        end = (int)(at + steps * 32 < P ? at + steps * 32 : P);
+    }
+    // Which of them the test holds for: lane i has those of step i (of the first 32 steps); lane 0's count is the warp's.
+    template <typename F>
+    __device__ __forceinline__ uint32_t read(const int32_t* held, F test, int& count) const {
+        const int lane = threadIdx.x & 31;
+        uint32_t mine = 0;
+        int n = 0;
+        for (int k0 = 0; k0 < steps; k0 += 4) {
+            int x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int p = first + (k0 + k) * 32 + lane;
+                x[k] = k0 + k < steps && p < end ? __ldcg(held + p) : -1;
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t b = __ballot_sync(0xffffffffu, x[k] >= 0 && test(x[k]));
+                n += __popc(b);
+                if (lane == k0 + k) mine = b;
+            }
+        }
+        count = lane == 0 ? n : 0;
+        return mine;
+    }
+    // f(page, whether the test holds, how many before it do) for each.
+    template <typename F, typename G>
+    __device__ __forceinline__ void each(const int32_t* held, uint32_t mine, int before, F test, G f) const {
+        const int lane = threadIdx.x & 31;
+        for (int k = 0; k < steps; ++k) {
+            const int p = first + k * 32 + lane;
+            const uint32_t b = k < 32 ? __shfl_sync(0xffffffffu, mine, k) : __ballot_sync(0xffffffffu, p < end && test(__ldcg(held + p)));
+            if (p < end) f(p, b >> lane & 1, before + __popc(b & ((1u << lane) - 1)));
+            before += __popc(b);
+        }
+    }
+};
+
 struct NextArgs {
     const int32_t *table, *len, *from, *keep, *add;
     int32_t *table_out, *len_out, *status;
@@ -151,7 +196,7 @@ __global__ void __launch_bounds__(kThreads) next_kernel(const NextArgs a) {
     mq_cluster_sync();
     // pages wanted, in the sequences' order; pages that nobody holds, in theirs
     const int bs = ceil_div(a.m, kAll), b0 = min(id * (long long)bs, (long long)a.m), b1 = min(b0 + bs, a.m);
-    int want = 0, none = 0;
+    int want = 0, none;
     for (int b = b0; b < b1; ++b) {
         const int2 x = __ldcg(reinterpret_cast<const int2*>(a.s.info) + 2 * b);
         const int kept = ceil_div(x.x, a.R);
@@ -167,14 +212,8 @@ __global__ void __launch_bounds__(kThreads) next_kernel(const NextArgs a) {
         reinterpret_cast<int2*>(a.s.info)[2 * b + 1] = make_int2(n, copy);
         want += n;
     }
-    const int ps = ceil_div(a.P, kAll), p0 = min(id * (long long)ps, (long long)a.P), p1 = min(p0 + ps, a.P);
-    uint32_t empty = 0;                               // the first 32 of this thread's pages
-#pragma unroll 8
-    for (int p = p0; p < p1; ++p) {
-        const bool x = __ldcg(a.s.held + p) == 0;
-        none += x;
-        if (p - p0 < 32) empty |= (uint32_t)x << (p - p0);
-    }
+    const Pages of(a.P, id);
+    uint32_t empty = of.read(a.s.held, [&](int held) { return held == 0; }, none);
     int before[3] = {want, none, longs}, all[3];
     scan(before, all);
     const bool enough = all[0] <= all[1];
@@ -186,10 +225,10 @@ __global__ void __launch_bounds__(kThreads) next_kernel(const NextArgs a) {
         a.s.info[4 * b + 2] = rank;
         rank += n;
     }
-    rank = before[1];
-    if (none > 0)
-        for (int p = p0; p < p1; ++p)
-            if (p - p0 < 32 ? empty >> (p - p0) & 1 : __ldcg(a.s.held + p) == 0) a.s.free[rank++] = p;
+    of.each(a.s.held, empty, __shfl_sync(0xffffffffu, before[1], 0), [&](int held) { return held == 0; },
+            [&](int p, bool is, int at) {
+                if (is) a.s.free[at] = p;
+            });
     if (id == 0) {
         a.status[0] = enough ? 0 : all[0] - all[1];
         a.status[1] = enough ? all[1] - all[0] : all[1];
@@ -255,21 +294,17 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactArgs a) 
              if ((unsigned)e < (unsigned)a.P) a.s.held[e] = 1;
          });
     mq_cluster_sync();
-    const int ps = ceil_div(a.P, kAll), p0 = min(id * (long long)ps, (long long)a.P), p1 = min(p0 + ps, a.P);
-    int mine = 0;
-#pragma unroll 8
-    for (int p = p0; p < p1; ++p) mine += __ldcg(a.s.held + p);
-    int first[1] = {mine}, all[1];
+    const Pages of(a.P, id);
+    auto is_live = [](int held) { return held != 0; };
+    int first[1], all[1];
+    const uint32_t lives = of.read(a.s.held, is_live, first[0]);
     scan(first, all);
-    const int U = all[0];
+    const int U = all[0], before = __shfl_sync(0xffffffffu, first[0], 0);
     // places below U that are free, in order; live pages before page U
-    int before = first[0];
-    for (int p = p0; p < p1; ++p) {
-        if (p == U) a.s.count[1] = before;
-        const int h = __ldcg(a.s.held + p);
-        if (!h && p < U) a.s.free[p - before] = p;
-        before += h;
-    }
+    of.each(a.s.held, lives, before, is_live, [&](int p, bool is, int at) {
+        if (p == U) a.s.count[1] = at;
+        if (!is && p < U) a.s.free[p - at] = p;
+    });
     if (id == 0) {
         if (U == a.P) a.s.count[1] = U;
         a.live[0] = U;
@@ -277,17 +312,14 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactArgs a) 
     mq_cluster_sync();
     const int below = __ldcg(a.s.count + 1);
     if (id == 0) a.s.count[0] = U - below;
-    before = first[0];
-    for (int p = p0; p < p1; ++p) {
-        const int h = __ldcg(a.s.held + p);
-        int to = h ? p : -1;
-        if (h && p >= U) {
-            to = __ldcg(a.s.free + before - below);
-            a.s.copies[before - below] = make_int2(p, to);
+    of.each(a.s.held, lives, before, is_live, [&](int p, bool is, int at) {
+        int to = is ? p : -1;
+        if (is && p >= U) {
+            to = __ldcg(a.s.free + at - below);
+            a.s.copies[at - below] = make_int2(p, to);
         }
         a.where[p] = to;
-        before += h;
-    }
+    });
     mq_cluster_sync();
     rows(
         [&](long long at) {
