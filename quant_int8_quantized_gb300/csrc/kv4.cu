@@ -107,14 +107,14 @@ __device__ __forceinline__ float nearest(F y, float d, float inv) {
 // four pairs or eight plain numbers is placed by itself.
 template <typename T, int LG, bool INTER, bool VEC>
 __global__ void __launch_bounds__(kThreads) fill_kernel(const FillArgs a) {
-    extern __shared__ float2 s_turn[];                 // [n_pairs]
+    extern __shared__ float2 s_turn[];                 // [4][n_pairs / 4]: pair 4 i + k at [k][i], a thread's four in four rows of banks
     __shared__ float s_row[kThreads / LG][LG * 8 + 16]; // a head's row on its way from pairs to words (heads in other banks)
     __shared__ int s_list[kList], s_n;                 // rows that want 64 bits
     mq_grid_release();
     mq_grid_wait();
     const int m = blockIdx.x;                          // the token
     const int lane = threadIdx.x % LG, group = threadIdx.x / LG;
-    const int D = a.D, n = a.n_pairs;
+    const int D = a.D, n = a.n_pairs, quarter = (n + 3) / 4;
     const int rows = a.h2;
     const int r_first = blockIdx.y * (kThreads / LG) + group, r_step = gridDim.y * (kThreads / LG);
 
@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kThreads) fill_kernel(const FillArgs a) {
     for (int p = threadIdx.x; p < n; p += kThreads) {
         float freq;
         const int pos = angle(p, freq);
-        s_turn[p] = turn(pos, freq, a.rot_scale);
+        s_turn[(p & 3) * quarter + (p >> 2)] = turn(pos, freq, a.rot_scale);
     }
     int page = -1, row = -1;
     if (a.h2 > a.h0) {
@@ -212,8 +212,8 @@ __global__ void __launch_bounds__(kThreads) fill_kernel(const FillArgs a) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             if (lane * 4 + i < np) {
-                if constexpr (VEC && !INTER) rotate(v[i], v[4 + i], s_turn[lane * 4 + i]);
-                else rotate(v[2 * i], v[2 * i + 1], s_turn[lane * 4 + i]);
+                if constexpr (VEC && !INTER) rotate(v[i], v[4 + i], s_turn[i * quarter + lane]);
+                else rotate(v[2 * i], v[2 * i + 1], s_turn[i * quarter + lane]);
             }
         if (live && what == 0) {
             T* y = reinterpret_cast<T*>(a.q_out) + ((long long)m * a.h0 + h) * D;
@@ -391,9 +391,9 @@ struct ReadArgs {
     int cap, chunks;        // rows at most of a sequence; chunks of kChunk blocks of them
     long long units;        // sequences x heads x chunks
 };
-constexpr int kChunk = 4, kReadWarps = 4;
+constexpr int kChunk = 2, kReadWarps = 4;
 
-// A warp takes 64 rows of a head, 16 at a time: the words that a lane loads are those that the products' operands are
+// A warp takes 32 rows of a head, 16 at a time: the words that a lane loads are those that the products' operands are
 // made of, so eight lanes' stores fill a row's 64 bytes.
 template <typename T, int D>
 __global__ void __launch_bounds__(32 * kReadWarps) read_kernel(const ReadArgs a) {
@@ -558,7 +558,7 @@ extern "C" int mq_qk_norm_rope_kv4(const mq_qkv* x, int type, float rot_scale, v
     const int lg = D <= 64 ? 8 : D <= 128 ? 16 : 32, per = kThreads / lg;
     const int passes = (a.h2 + per - 1) / per;
     const dim3 grid(x->M, x->M >= 2 * mq::num_sms() ? 1 : passes < 65535 ? passes : 65535);
-    const size_t smem = (size_t)a.n_pairs * sizeof(float2);
+    const size_t smem = (size_t)((a.n_pairs + 3) / 4) * 4 * sizeof(float2);
     const bool inter = x->interleaved != 0;
     auto go = [&](auto t) {
         using T = decltype(t);
