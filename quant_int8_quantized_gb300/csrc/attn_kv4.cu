@@ -573,9 +573,10 @@ Kv4Cut cut_kv4(int B, int T, int Hq, int Hkv, int D, int cap) {
     int per_sm = 1;
     with_kernel(D, MQ_F16, c.nt, [&](auto, int, int n) { return per_sm = n; });
     const long long held = (long long)mq::num_sms() * per_sm;
-    // Beginning and ending a segment costs about a tile; where each tile can have a warp of its own it has (one sequence of 1000
-    // rows: 8.8 us, with runs of two tiles and more 9.9, of three 11.0).
-    p.extra = most <= 2 * held ? 0 : 1;
+    // Beginning and ending a segment costs about a tile. Where there are few tiles, and their pieces few bytes to join, each has a
+    // warp of its own (one sequence of 1000 rows: 8.8 us, with runs of two tiles and more 9.9, of three 11.0; 32 queries of 7 heads on
+    // 1500 rows, 22 MB of pieces: 27.9, 22.2, 26.4).
+    p.extra = most <= 2 * held && most * p.rows * D * 4 <= 12 << 20 ? 0 : 1;
     if (most + segs * p.extra > 0x7fffffffLL || segs > 0x3fffffffLL) c.fits = false;
     p.G = (int)(most < held ? most : held);
     const size_t places = (size_t)p.G + (size_t)segs;
