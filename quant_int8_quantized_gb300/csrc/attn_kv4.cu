@@ -12,6 +12,8 @@
 //    instruction) to become the right operand of O^T += V^T P^T.
 //  - The maximum that the exponents are taken against is renewed when a row passes it by 2^8 (each row by itself, so that
 //    no row's bits depend on its neighbours), which leaves one vote a tile.
+// Measured: 64 sequences of 9000 to 20000 rows, 40 query and 8 key heads of 128 (1 GB), 202 us, 5.0 TB/s (its copies alone 157); one of
+// 1000 rows, 8.8 us with the join, which is latency.
 // Many rows (a prompt): the rows in use are read once into 16 bits in the workspace and mq_attn_prefix's tensor-core kernel
 // takes them from there; n d being exact, both ways compute the same products.
 
