@@ -42,7 +42,8 @@ struct Shape {
     static constexpr int kKeys = keys_of(D, NT);
     static constexpr int kTile = kKeys / kv4::kBlockRows * kv4::block_bytes(D);
     static constexpr int kStages = D <= 64 || D > 128 || NT > 1 ? 2 : 3;
-    static constexpr int kRing = kStages * kTile;
+    static constexpr int kStage = kTile + 16;                        // a tile, its barrier
+    static constexpr int kRing = kStages * kStage;
     static constexpr int kScales = kStep / 2 * (D / 32) * 16;        // a step's
     // more than eight rows: their operands lie in shared memory, each lane's where it alone reads them (registers would do for 8
     // warps an SM instead of 12)
@@ -73,6 +74,26 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
         asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+template <typename T>                     // with nothing added
+__device__ __forceinline__ void first_mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    if constexpr (std::is_same<T, __half>::value)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                     : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                     : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+// Non-suspending test of a phase.
+__device__ __forceinline__ bool bar_ready(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                 : "=r"(ok)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+    return ok != 0;
 }
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {   // 8 x 8 16-bit numbers, row i in lanes 4 i ..
     uint32_t y;
@@ -129,13 +150,12 @@ __global__ void __launch_bounds__(32, Shape<D, NT>::kPerSm) attn_kv4_kernel(cons
     constexpr int KW = Factor::kWords;
     extern __shared__ __align__(128) uint8_t s_ring[];
     __shared__ Piece s_piece[kStages + 1];
-    __shared__ uint64_t s_full[kStages];
     uint32_t* const s_value = reinterpret_cast<uint32_t*>(s_ring + C::kRing);    // [block of dims][pair of rows][KW]
     uint4* const s_query = reinterpret_cast<uint4*>(s_ring + C::kRing + C::kScales);   // [eight rows][block of dims][lane]
     mq_grid_release();
     const int lane = threadIdx.x;
     if (lane == 0) {
-        for (int i = 0; i < kStages; ++i) tc::mbar_init(&s_full[i], 1);
+        for (int i = 0; i < kStages; ++i) tc::mbar_init(reinterpret_cast<uint64_t*>(s_ring + i * C::kStage + C::kTile), 1);
         tc::fence_mbar_init();
     }
     mq_grid_wait();
@@ -146,17 +166,17 @@ __global__ void __launch_bounds__(32, Shape<D, NT>::kPerSm) attn_kv4_kernel(cons
     // ---------------------------------------------------------------- copies, kStages - 1 tiles ahead
     Cursor c = find_run<32>(p, a.len);
     advance(p, a.len, c, 0);
-    int left = 0, handed = 0, key = 0, in_slot = 0;    // tiles of the copied piece left, pieces handed over
+    int left = 0, handed = 0, key = 0;                 // tiles of the copied piece left, pieces handed over
     int head = 0, seq = 0, issued = 0;
     // a tile lies on `parts` pages, `part` bytes on each; lane i holds the place of part i - at from the next one on
     const int parts = max(1, kKeys >> a.c.shift), part = C::kTile / parts, part_rows = kKeys / parts;
-    int at = 0;
+    const uint32_t all_parts = (1u << parts) - 1, ring = tc::smem_u32(s_ring);
+    int at = 32;
     const uint8_t* src = nullptr;
     uint32_t there = 0;                                // the parts that are on a page
     uint32_t bad[kStages] = {};                        // parts on no page, of the tile that is multiplied next (0) and those behind it
-    const uint32_t ring = tc::smem_u32(s_ring), full = tc::smem_u32(s_full);
-    auto copy = [&] {
-        bool fresh = false;
+    // Tiles that issue() may be called for, without another look: 0 where the run is over.
+    auto look = [&] {
         if (left == 0) {
             Piece q;
             q.n = 0;
@@ -174,58 +194,63 @@ __global__ void __launch_bounds__(32, Shape<D, NT>::kPerSm) attn_kv4_kernel(cons
                 seq = q.b;
                 key = q.key0;
                 left = q.n;
-                fresh = true;
+                at = 32;
                 advance(p, a.len, c, q.n);
             }
             __syncwarp();
             if (lane == 0) s_piece[handed] = q;
             __syncwarp();
             if (++handed == kStages + 1) handed = 0;
+            if (left == 0) return 0;
         }
-        if (left > 0) {
-            if (fresh || at + parts > 32) {       // the next 32 parts' places, a lane each
-                at = 0;
-                const int row = key + lane * part_rows;
-                const int page = row >> a.c.shift < a.c.width ? a.c.page(seq, row) : -1;
-                src = page >= 0 ? a.c.block(page, head, row, kBlock) : nullptr;
-                there = __ballot_sync(0xffffffffu, src != nullptr);
-            }
-            const uint32_t mine = there >> at & ((1u << parts) - 1);
-            bad[kStages - 1] = mine ^ ((1u << parts) - 1);
+        if (at + parts > 32) {                         // the next 32 parts' places, a lane each
+            at = 0;
+            const int row = key + lane * part_rows;
+            const int page = row >> a.c.shift < a.c.width ? a.c.page(seq, row) : -1;
+            src = page >= 0 ? a.c.block(page, head, row, kBlock) : nullptr;
+            there = __ballot_sync(0xffffffffu, src != nullptr);
+        }
+        return min(left, (32 - at) / parts);
+    };
+    auto issue = [&](int off) {                        // the next tile, to the stage at `off`
+        const uint32_t mine = there >> at & all_parts;
+        bad[kStages - 1] = mine ^ all_parts;
 #ifdef MQ_TEST_INJECT
-            const bool skip = g_kv4_skip_tile && blockIdx.x == 0 && issued == 0;
+        const bool skip = g_kv4_skip_tile && blockIdx.x == 0 && issued == 0;
 #else
-            constexpr bool skip = false;
+        constexpr bool skip = false;
 #endif
-            if (!skip && (unsigned)(lane - at) < (unsigned)parts) {
-                const uint32_t bar = full + in_slot * 8;
-                if (lane == at) expect(bar, __popc(mine) * part);
-                if (src) bulk_load(ring + in_slot * C::kTile + (lane - at) * part, src, part, bar);
-            }
-            at += parts;
-            __syncwarp();
-            ++issued;
-            key += kKeys;
-            --left;
-            if (++in_slot == kStages) in_slot = 0;
+        if (!skip && (unsigned)(lane - at) < (unsigned)parts) {
+            const uint32_t to = ring + off, bar = to + C::kTile;
+            if (lane == at) expect(bar, __popc(mine) * part);
+            if (src) bulk_load(to + (lane - at) * part, src, part, bar);
         }
+        at += parts;
+        ++issued;
+    };
+    auto passed = [&](int n) {                         // after n of them
+        left -= n;
+        key += n * kKeys;
+    };
+    auto shift = [&] {
+#pragma unroll
+        for (int k = 1; k < kStages; ++k) bad[k - 1] = bad[k];
     };
 #pragma unroll 1
     for (int i = 0; i < kStages - 1; ++i) {
-        if (i > 0)
-#pragma unroll
-            for (int k = 1; k < kStages; ++k) bad[k - 1] = bad[k];
-        copy();
+        if (look() > 0) {
+            issue(i * C::kStage);
+            passed(1);
+        }
+        shift();
     }
-#pragma unroll
-    for (int k = 1; k < kStages; ++k) bad[k - 1] = bad[k];
 
     // ---------------------------------------------------------------- products
     auto from = [](const uint8_t* q) {
         return [q](auto type, int i) { return reinterpret_cast<const decltype(type)*>(q)[i]; };
     };
     const float scale = fminf(fmaxf(a.scale_log2 * kUnit, -3.4028234663852886e38f), 3.4028234663852886e38f);
-    int taken = 0, slot = 0, taken_tiles = 0;
+    int taken = 0, taken_tiles = 0, off = 0, free_off = C::kRing - C::kStage;    // stages: of the next tile, and the one free
     uint32_t phase = 0;
     bool alive = true;
     while (alive) {
@@ -255,29 +280,52 @@ __global__ void __launch_bounds__(32, Shape<D, NT>::kPerSm) attn_kv4_kernel(cons
         for (int i = 0; i < 2 * nb; ++i)
 #pragma unroll
             for (int j = 0; j < NT; ++j) o[i][j][0] = o[i][j][1] = o[i][j][2] = o[i][j][3] = 0.0f;
-        float m[NT][2], l[NT][2];      // references and (this lane's) sums
+        // Rows' references, and (this lane's) sums. Where registers allow, what every step wants of a reference m is held instead of it:
+        // what is added to the products for the exponents (-m; 0: no key seen yet) and the product from which on m is renewed.
+        constexpr bool kHeld = NT <= 2;
+        float minus[NT][2], limit[kHeld ? NT : 1][2] = {};
+        float2 l[NT];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) m[j][0] = m[j][1] = kNone, l[j][0] = l[j][1] = 0.0f;
+        for (int j = 0; j < NT; ++j) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                minus[j][e] = kHeld ? 0.0f : INFINITY;
+                if constexpr (kHeld) limit[j][e] = kNone;
+            }
+            l[j] = make_float2(0.0f, 0.0f);
+        }
+        auto limit_of = [&](int j, int e) { return kHeld ? limit[kHeld ? j : 0][e] : (kUp<T> + kGrow) - minus[j][e]; };
+        auto less_of = [&](int j, int e) { return kHeld || minus[j][e] != INFINITY ? minus[j][e] : 0.0f; };
+        auto minus_of = [&](int j, int e) { return kHeld && limit[kHeld ? j : 0][e] == kNone ? INFINITY : minus[j][e]; };   // -m
 
+        int k0 = w.key0, ahead = 0;    // ahead: tiles to go before the copying side has to look
+        bool more = true;              // it has some
 #pragma unroll 1
-        for (int ti = 0; ti < w.n; ++ti) {
-            copy();
-            if (!(alive = __all_sync(0xffffffffu, mbar_ready(&s_full[slot], phase) ||
-                                                      tc::mbar_wait(&s_full[slot], phase, kWaitLimitNs))))
+        for (int ti = w.n; ti > 0; --ti) {
+            if (ahead == 0) {
+                const int n = look();
+                more = n > 0;
+                ahead = more ? min(n, ti) : ti;
+                passed(more ? ahead : 0);
+            }
+            --ahead;
+            if (more) issue(free_off);
+            if (!(alive = __all_sync(0xffffffffu, bar_ready(ring + off + C::kTile, phase) ||
+                                                      tc::mbar_wait(reinterpret_cast<uint64_t*>(s_ring + off + C::kTile), phase, kWaitLimitNs))))
                 break;
-            uint8_t* const tile = s_ring + slot * C::kTile;
+            uint8_t* const tile = s_ring + off;
             const uint32_t none_of = bad[0];
-#pragma unroll
-            for (int i = 1; i < kStages; ++i) bad[i - 1] = bad[i];
+            shift();
             ++taken_tiles;
-            if (++slot == kStages) {
-                slot = 0;
+            free_off = off;
+            off += C::kStage;
+            if (off == C::kRing) {
+                off = 0;
                 phase ^= 1;
             }
 #pragma unroll 1
-            for (int in = 0; in < kKeys; in += kStep) {
-                const int k0 = w.key0 + ti * kKeys + in;
-                if (k0 >= w.len) break;
+            for (int in = 0; in < kKeys; in += kStep, k0 += kStep) {
+                if (kKeys > kStep && k0 >= w.len) break;
                 uint8_t* const st = tile + in / kv4::kBlockRows * kBlock;
                 // The values' scales as the numbers need them, once for all lanes: half a pair of rows each. Those of rows that
                 // are on no page or past the end are zero, whatever lies there.
@@ -328,10 +376,6 @@ __global__ void __launch_bounds__(32, Shape<D, NT>::kPerSm) attn_kv4_kernel(cons
                             kv4::words<nb>(from(at + (u * 32 + lane) * nb * 4), kw[i][u]);
                             kv4::bytes<nb>(from(at + kv4::key_scale_at(D) + (g + 8 * u) * nb), ks[i][u]);
                         }
-#pragma unroll
-                        for (int j = 0; j < NT; ++j)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) s[blk0 + i][j][e] = 0.0f;
                     }
 #pragma unroll
                     for (int b = 0; b < nb; b += 2) {
@@ -356,7 +400,10 @@ __global__ void __launch_bounds__(32, Shape<D, NT>::kPerSm) attn_kv4_kernel(cons
 #pragma unroll
                                 for (int j = 0; j < NT; ++j)
 #pragma unroll
-                                    for (int i = 0; i < kAtOnce; ++i) mma<T>(s[blk0 + i][j], x0[i][0], x1[i][0], x0[i][1], x1[i][1], q[j].x, q[j].y);
+                                    for (int i = 0; i < kAtOnce; ++i) {
+                                        if (b + e == 0) first_mma<T>(s[blk0 + i][j], x0[i][0], x1[i][0], x0[i][1], x1[i][1], q[j].x, q[j].y);
+                                        else mma<T>(s[blk0 + i][j], x0[i][0], x1[i][0], x0[i][1], x1[i][1], q[j].x, q[j].y);
+                                    }
 #pragma unroll
                                 for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -372,7 +419,10 @@ __global__ void __launch_bounds__(32, Shape<D, NT>::kPerSm) attn_kv4_kernel(cons
 #pragma unroll
                     for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) s[blk][j][e] *= scale;
+                        for (int u = 0; u < 2; ++u) {
+                            const float2 x = f2_mul(make_float2(s[blk][j][2 * u], s[blk][j][2 * u + 1]), f2_dup(scale));
+                            s[blk][j][2 * u] = x.x, s[blk][j][2 * u + 1] = x.y;
+                        }
                     if (k0 + kStep > all_see) {
 #pragma unroll
                         for (int blk = 0; blk < 2; ++blk)
@@ -382,8 +432,8 @@ __global__ void __launch_bounds__(32, Shape<D, NT>::kPerSm) attn_kv4_kernel(cons
                     }
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        mx[j][e] = fmaxf(fmaxf(s[0][j][e], s[0][j][e + 2]), fmaxf(s[1][j][e], s[1][j][e + 2]));
-                        grew |= mx[j][e] > m[j][e] + (kUp<T> + kGrow);
+                        mx[j][e] = fmaxf(fmaxf(fmaxf(s[0][j][e], s[0][j][e + 2]), s[1][j][e]), s[1][j][e + 2]);
+                        grew |= mx[j][e] > limit_of(j, e);
                     }
                 }
                 if (__any_sync(0xffffffffu, grew)) {
@@ -394,11 +444,13 @@ __global__ void __launch_bounds__(32, Shape<D, NT>::kPerSm) attn_kv4_kernel(cons
                         for (int e = 0; e < 2; ++e) {
 #pragma unroll
                             for (int x = 4; x < 32; x <<= 1) mx[j][e] = fmaxf(mx[j][e], __shfl_xor_sync(0xffffffffu, mx[j][e], x));
-                            const float now = mx[j][e] > m[j][e] + (kUp<T> + kGrow) ? reference<kUp<T>>(mx[j][e]) : m[j][e];
-                            alpha[e] = now == m[j][e] ? 1.0f : exp2_fast(m[j][e] - now);
-                            m[j][e] = now;
-                            l[j][e] *= alpha[e];
+                            const bool up = mx[j][e] > limit_of(j, e);
+                            const float was = minus_of(j, e), now = up ? -reference<kUp<T>>(mx[j][e]) : was;
+                            alpha[e] = up ? exp2_fast(now - was) : 1.0f;
+                            minus[j][e] = kHeld && now == INFINITY ? 0.0f : now;
+                            if constexpr (kHeld) limit[j][e] = (kUp<T> + kGrow) - now;
                         }
+                        l[j] = f2_mul(l[j], make_float2(alpha[0], alpha[1]));
 #pragma unroll
                         for (int i = 0; i < 2 * nb; ++i) {
                             o[i][j][0] *= alpha[0], o[i][j][1] *= alpha[1];
@@ -409,15 +461,15 @@ __global__ void __launch_bounds__(32, Shape<D, NT>::kPerSm) attn_kv4_kernel(cons
                 uint32_t pf[2][NT][2];
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
-                    const float safe[2] = {m[j][0] == kNone ? 0.0f : m[j][0], m[j][1] == kNone ? 0.0f : m[j][1]};
+                    const float2 less = make_float2(less_of(j, 0), less_of(j, 1));
 #pragma unroll
                     for (int blk = 0; blk < 2; ++blk) {
 #pragma unroll
                         for (int u = 0; u < 2; ++u) {
-                            const float e0 = exp2_fast(s[blk][j][2 * u] - safe[0]), e1 = exp2_fast(s[blk][j][2 * u + 1] - safe[1]);
-                            l[j][0] += e0;
-                            l[j][1] += e1;
-                            pf[blk][j][u] = transposed(mq_pack2<T>(e0, e1));
+                            const float2 x = f2_add(make_float2(s[blk][j][2 * u], s[blk][j][2 * u + 1]), less);
+                            const float2 e = make_float2(exp2_fast(x.x), exp2_fast(x.y));
+                            l[j] = f2_add(l[j], e);
+                            pf[blk][j][u] = transposed(mq_pack2<T>(e.x, e.y));
                         }
                     }
                 }
@@ -450,11 +502,12 @@ __global__ void __launch_bounds__(32, Shape<D, NT>::kPerSm) attn_kv4_kernel(cons
         for (int j = 0; j < NT; ++j)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
+                float sum = e ? l[j].y : l[j].x;
 #pragma unroll
-                for (int x = 4; x < 32; x <<= 1) l[j][e] += __shfl_xor_sync(0xffffffffu, l[j][e], x);
+                for (int x = 4; x < 32; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
                 const int r = 8 * j + 2 * t + e;
                 if (r < w.rows) {
-                    if (g == 0) a.out.ml[place + r] = make_float2(m[j][e], l[j][e]);
+                    if (g == 0) a.out.ml[place + r] = make_float2(-minus_of(j, e), sum);
                     float* to = a.out.o + (place + r) * D + 4 * g;
 #pragma unroll
                     for (int b = 0; b < nb; ++b)
@@ -466,9 +519,10 @@ __global__ void __launch_bounds__(32, Shape<D, NT>::kPerSm) attn_kv4_kernel(cons
     if (!alive) {   // a copy never came: recorded; those still in flight must land before the block leaves
         if (lane == 0) atomicOr(&g_kv4_error, 1u);
         for (int i = taken_tiles; i < issued; ++i) {
-            tc::mbar_wait(&s_full[slot], phase, kWaitLimitNs);
-            if (++slot == kStages) {
-                slot = 0;
+            tc::mbar_wait(reinterpret_cast<uint64_t*>(s_ring + off + C::kTile), phase, kWaitLimitNs);
+            off += C::kStage;
+            if (off == C::kRing) {
+                off = 0;
                 phase ^= 1;
             }
         }
