@@ -127,9 +127,8 @@ __device__ __forceinline__ void put(uint32_t* to, const uint32_t (&x)[n]) {
 }
 
 constexpr float kNone = -INFINITY;
-// Weights reach 2^15 in f16 and 2^8 in bf16: the reference lies 2^7 (f16) below a maximum, which may grow by 2^8.
-template <typename T>
-constexpr int kUp = std::is_same<T, __half>::value ? 7 : 0;
+// Weights are rounded to f16 and reach 2^15: the reference lies 2^7 below a maximum, which may grow by 2^8.
+constexpr int kUp = 7;
 constexpr float kGrow = 8.0f;
 
 // A piece as the copying side hands it to the multiplying side. n == 0: the run is over.
@@ -145,8 +144,10 @@ __global__ void __launch_bounds__(32, Shape<D, NT>::kPerSm) attn_kv4_kernel(cons
     using C = Shape<D, NT>;
     constexpr int nb = D / 32, kBlock = kv4::block_bytes(D), kStages = C::kStages, kKeys = C::kKeys;
     constexpr bool kHalf = std::is_same<T, __half>::value;
-    using Factor = typename std::conditional<kHalf, kv4::Eighth, kv4::Scale<T>>::type;
-    constexpr float kUnit = kHalf ? 8.0f : 1.0f;       // of the numbers that it makes
+    // keys in the queries' type; values and weights in f16, which has room for both and more bits for the weights
+    using KeyFactor = typename std::conditional<kHalf, kv4::Eighth, kv4::Scale<T>>::type;
+    using Factor = kv4::Eighth;
+    constexpr float kKeyUnit = kHalf ? 8.0f : 1.0f, kUnit = 8.0f;      // of the numbers that they make
     constexpr int KW = Factor::kWords;
     extern __shared__ __align__(128) uint8_t s_ring[];
     __shared__ Piece s_piece[kStages + 1];
@@ -249,7 +250,7 @@ __global__ void __launch_bounds__(32, Shape<D, NT>::kPerSm) attn_kv4_kernel(cons
     auto from = [](const uint8_t* q) {
         return [q](auto type, int i) { return reinterpret_cast<const decltype(type)*>(q)[i]; };
     };
-    const float scale = fminf(fmaxf(a.scale_log2 * kUnit, -3.4028234663852886e38f), 3.4028234663852886e38f);
+    const float scale = fminf(fmaxf(a.scale_log2 * kKeyUnit, -3.4028234663852886e38f), 3.4028234663852886e38f);
     int taken = 0, taken_tiles = 0, off = 0, free_off = C::kRing - C::kStage;    // stages: of the next tile, and the one free
     uint32_t phase = 0;
     bool alive = true;
@@ -294,7 +295,7 @@ __global__ void __launch_bounds__(32, Shape<D, NT>::kPerSm) attn_kv4_kernel(cons
             }
             l[j] = make_float2(0.0f, 0.0f);
         }
-        auto limit_of = [&](int j, int e) { return kHeld ? limit[kHeld ? j : 0][e] : (kUp<T> + kGrow) - minus[j][e]; };
+        auto limit_of = [&](int j, int e) { return kHeld ? limit[kHeld ? j : 0][e] : (kUp + kGrow) - minus[j][e]; };
         auto less_of = [&](int j, int e) { return kHeld || minus[j][e] != INFINITY ? minus[j][e] : 0.0f; };
         auto minus_of = [&](int j, int e) { return kHeld && limit[kHeld ? j : 0][e] == kNone ? INFINITY : minus[j][e]; };   // -m
 
@@ -379,11 +380,11 @@ __global__ void __launch_bounds__(32, Shape<D, NT>::kPerSm) attn_kv4_kernel(cons
                     }
 #pragma unroll
                     for (int b = 0; b < nb; b += 2) {
-                        Factor f[kAtOnce][2];
+                        KeyFactor f[kAtOnce][2];
 #pragma unroll
                         for (int i = 0; i < kAtOnce; ++i)
 #pragma unroll
-                            for (int u = 0; u < 2; ++u) f[i][u] = Factor::of(kv4::both(ks[i][u], b / 2));
+                            for (int u = 0; u < 2; ++u) f[i][u] = KeyFactor::of(kv4::both(ks[i][u], b / 2));
 #pragma unroll
                         for (int e = 0; e < 2; ++e)
                             if (b + e < nb) {
@@ -445,10 +446,10 @@ __global__ void __launch_bounds__(32, Shape<D, NT>::kPerSm) attn_kv4_kernel(cons
 #pragma unroll
                             for (int x = 4; x < 32; x <<= 1) mx[j][e] = fmaxf(mx[j][e], __shfl_xor_sync(0xffffffffu, mx[j][e], x));
                             const bool up = mx[j][e] > limit_of(j, e);
-                            const float was = minus_of(j, e), now = up ? -reference<kUp<T>>(mx[j][e]) : was;
+                            const float was = minus_of(j, e), now = up ? -reference<kUp>(mx[j][e]) : was;
                             alpha[e] = up ? exp2_fast(now - was) : 1.0f;
                             minus[j][e] = kHeld && now == INFINITY ? 0.0f : now;
-                            if constexpr (kHeld) limit[j][e] = (kUp<T> + kGrow) - now;
+                            if constexpr (kHeld) limit[j][e] = (kUp + kGrow) - now;
                         }
                         l[j] = f2_mul(l[j], make_float2(alpha[0], alpha[1]));
 #pragma unroll
@@ -469,7 +470,7 @@ __global__ void __launch_bounds__(32, Shape<D, NT>::kPerSm) attn_kv4_kernel(cons
                             const float2 x = f2_add(make_float2(s[blk][j][2 * u], s[blk][j][2 * u + 1]), less);
                             const float2 e = make_float2(exp2_fast(x.x), exp2_fast(x.y));
                             l[j] = f2_add(l[j], e);
-                            pf[blk][j][u] = transposed(mq_pack2<T>(e.x, e.y));
+                            pf[blk][j][u] = transposed(mq_pack2<__half>(e.x, e.y));
                         }
                     }
                 }
@@ -488,8 +489,8 @@ __global__ void __launch_bounds__(32, Shape<D, NT>::kPerSm) attn_kv4_kernel(cons
                         kv4::numbers(vw[1][b], Factor::from(f), x1);
 #pragma unroll
                         for (int j = 0; j < NT; ++j) {
-                            mma<T>(o[2 * b][j], x0[0], x0[1], x1[0], x1[1], pf[blk][j][0], pf[blk][j][1]);
-                            mma<T>(o[2 * b + 1][j], x0[2], x0[3], x1[2], x1[3], pf[blk][j][0], pf[blk][j][1]);
+                            mma<__half>(o[2 * b][j], x0[0], x0[1], x1[0], x1[1], pf[blk][j][0], pf[blk][j][1]);
+                            mma<__half>(o[2 * b + 1][j], x0[2], x0[3], x1[2], x1[3], pf[blk][j][0], pf[blk][j][1]);
                         }
                     }
                 }
