@@ -20,6 +20,7 @@
 #include <cmath>
 #include <type_traits>
 
+#include "attn_join.cuh"
 #include "attn_many.cuh"
 #include "attn_maps.cuh"
 #include "kv4.cuh"
@@ -62,6 +63,9 @@ struct Kv4Args {
     const int32_t* len;
     float scale_log2;
     Pieces out;
+    int4* split;          // [G]: the segment that begins in the block and goes on in others (or -1), its last block, its row tile (sequence and
+                          // tile) and key head
+    Out fin;
 };
 
 template <typename T>
@@ -136,10 +140,12 @@ struct Piece {
     int n, key0;         // tiles, first key
     int seg, head;
     int b, r0;           // sequence, first row
-    int rows, len;
+    int rows, len;       // rows: with kWhole where it is all of its segment, to be finished
 };
+constexpr int kWhole = 256;
 
-template <typename T, int D, int NT>
+// FIN: blocks finish the segments that they hold.
+template <typename T, int D, int NT, bool FIN>
 __global__ void __launch_bounds__(32, Shape<D, NT>::kPerSm) attn_kv4_kernel(const Kv4Args a) {
     using C = Shape<D, NT>;
     constexpr int nb = D / 32, kBlock = kv4::block_bytes(D), kStages = C::kStages, kKeys = C::kKeys;
@@ -163,6 +169,8 @@ __global__ void __launch_bounds__(32, Shape<D, NT>::kPerSm) attn_kv4_kernel(cons
     const Plan& p = a.plan;
     const int tg = p.T * p.group, per_seq = own_tiles_of_rows(p);
     const int g = lane >> 2, t = lane & 3;
+
+    if (FIN && lane == 0) a.split[blockIdx.x] = make_int4(-1, -1, -1, -1);
 
     // ---------------------------------------------------------------- copies, kStages - 1 tiles ahead
     Cursor c = find_run<32>(p, a.len);
@@ -190,7 +198,13 @@ __global__ void __launch_bounds__(32, Shape<D, NT>::kPerSm) attn_kv4_kernel(cons
                 q.r0 = (c.unit - q.b * per_seq) * p.rows;
                 q.rows = min(p.rows, tg - q.r0);
                 q.len = own_len_of(p, a.len, q.b);
-                if (lane == 0 && c.in == 0) a.out.info[c.seg] = blocks_of(p, c);
+                const bool whole = FIN && c.in == 0 && q.n == c.tiles;
+                if (whole) q.rows += kWhole;
+                if (lane == 0 && c.in == 0) {
+                    const int2 blocks = blocks_of(p, c);
+                    if (!FIN) a.out.info[c.seg] = blocks;
+                    else if (!whole) a.split[blockIdx.x] = make_int4(c.seg, blocks.y, c.unit, c.head);
+                }
                 head = c.head;
                 seq = q.b;
                 key = q.key0;
@@ -255,8 +269,10 @@ __global__ void __launch_bounds__(32, Shape<D, NT>::kPerSm) attn_kv4_kernel(cons
     uint32_t phase = 0;
     bool alive = true;
     while (alive) {
-        const Piece w = s_piece[taken];
+        Piece w = s_piece[taken];
         if (w.n == 0) break;
+        const bool whole = FIN && w.rows > kWhole;
+        if (whole) w.rows -= kWhole;
         if (++taken == kStages + 1) taken = 0;
         // query rows 8 j + g (zeros past the last) as right operands, eight consecutive dims for each block of 32
         uint4 qf[C::kQueries ? 1 : NT][C::kQueries ? 1 : nb];
@@ -507,14 +523,27 @@ __global__ void __launch_bounds__(32, Shape<D, NT>::kPerSm) attn_kv4_kernel(cons
 #pragma unroll
                 for (int x = 4; x < 32; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
                 const int r = 8 * j + 2 * t + e;
-                if (r < w.rows) {
-                    if (g == 0) a.out.ml[place + r] = make_float2(-minus_of(j, e), sum);
-                    float* to = a.out.o + (place + r) * D + 4 * g;
+                if (r >= w.rows) continue;
+                if (FIN && whole) {
+                    const int ti = p.by_group.of(w.r0 + r);
+                    const long long row = ((long long)w.b * p.T + ti) * p.Hq + w.head * p.group + w.r0 + r - ti * p.group;
+                    const float by = sum == 0.0f ? 0.0f : kUnit / sum;       // no key seen (a NaN or infinite sum stays one)
+                    if (g == 0 && a.fin.lse) a.fin.lse[row] = sum == 0.0f ? kNone : -minus_of(j, e) * kLn2 + logf(sum);
 #pragma unroll
-                    for (int b = 0; b < nb; ++b)
-                        *reinterpret_cast<float4*>(to + 32 * b) =
-                            make_float4(o[2 * b][j][e] * kUnit, o[2 * b][j][e + 2] * kUnit, o[2 * b + 1][j][e] * kUnit, o[2 * b + 1][j][e + 2] * kUnit);
+                    for (int b = 0; b < nb; ++b) {
+                        const float y[4] = {o[2 * b][j][e] * by, o[2 * b][j][e + 2] * by, o[2 * b + 1][j][e] * by, o[2 * b + 1][j][e + 2] * by};
+                        const long long to = row * D + 32 * b + 4 * g;
+                        if (a.fin.f32) *reinterpret_cast<float4*>(static_cast<float*>(a.fin.out) + to) = make_float4(y[0], y[1], y[2], y[3]);
+                        else *reinterpret_cast<uint2*>(static_cast<T*>(a.fin.out) + to) = make_uint2(mq_pack2<T>(y[0], y[1]), mq_pack2<T>(y[2], y[3]));
+                    }
+                    continue;
                 }
+                if (g == 0) a.out.ml[place + r] = make_float2(-minus_of(j, e), sum);
+                float* to = a.out.o + (place + r) * D + 4 * g;
+#pragma unroll
+                for (int b = 0; b < nb; ++b)
+                    *reinterpret_cast<float4*>(to + 32 * b) =
+                        make_float4(o[2 * b][j][e] * kUnit, o[2 * b][j][e + 2] * kUnit, o[2 * b + 1][j][e] * kUnit, o[2 * b + 1][j][e + 2] * kUnit);
             }
     }
     if (!alive) {   // a copy never came: recorded; those still in flight must land before the block leaves
@@ -530,6 +559,24 @@ __global__ void __launch_bounds__(32, Shape<D, NT>::kPerSm) attn_kv4_kernel(cons
     }
 }
 
+// The rows of the segments that one block of the first kernel began and another ended: grid x that block, y rows.
+template <typename O, int D>
+__global__ void __launch_bounds__(32) join_split_kernel(const Kv4Args a) {
+    mq_grid_release();
+    mq_grid_wait();
+    const Plan& p = a.plan;
+    const int4 s = __ldca(a.split + blockIdx.x);
+    if (s.x < 0 || s.y < (int)blockIdx.x || s.y >= p.G) return;
+    const int per_seq = own_tiles_of_rows(p), b = p.by_per_seq.of(s.z), r0 = (s.z - b * per_seq) * p.rows;
+    const int rows = min(p.rows, p.T * p.group - r0);
+    for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+        const int ti = p.by_group.of(r0 + r);
+        const Run run = {&a.out, ((long long)blockIdx.x + s.x) * p.rows + r, p.rows, s.y - (int)blockIdx.x + 1};
+        write_row<O, D>(add_pieces<D, 8>(run, Run{}, 0, run.count), a.fin, nullptr,
+                        ((long long)b * p.T + ti) * p.Hq + s.w * p.group + r0 + r - ti * p.group);
+    }
+}
+
 // Tiles of eight rows that a segment has for `rows` rows of a key head; what registers allow is 4 of 128 dims.
 int tiles_of_rows(long long rows, int D) {
     const int most = D <= 128 ? 4 : 2;
@@ -537,18 +584,26 @@ int tiles_of_rows(long long rows, int D) {
     return (int)((eights + tiles - 1) / tiles);
 }
 
+constexpr int kFinMost = 2;     // tiles of eight rows in kernels that finish segments
+
 template <typename F>
-int with_kernel(int D, int type, int nt, F f) {
+int with_kernel(int D, int type, int nt, bool fin, F f) {
     auto go = [&](auto t) {
         using T = decltype(t);
         auto of = [&](auto d) {
             constexpr int W = decltype(d)::value;
-            if (nt == 1) return f(attn_kv4_kernel<T, W, 1>, Shape<W, 1>::kSmem, Shape<W, 1>::kPerSm);
+            auto with = [&](auto n) {
+                constexpr int NT = decltype(n)::value;
+                if constexpr (NT <= kFinMost)
+                    if (fin) return f(attn_kv4_kernel<T, W, NT, true>, Shape<W, NT>::kSmem, Shape<W, NT>::kPerSm);
+                return f(attn_kv4_kernel<T, W, NT, false>, Shape<W, NT>::kSmem, Shape<W, NT>::kPerSm);
+            };
+            if (nt == 1) return with(std::integral_constant<int, 1>());
             if constexpr (W <= 128) {
-                if (nt == 3) return f(attn_kv4_kernel<T, W, 3>, Shape<W, 3>::kSmem, Shape<W, 3>::kPerSm);
-                if (nt == 4) return f(attn_kv4_kernel<T, W, 4>, Shape<W, 4>::kSmem, Shape<W, 4>::kPerSm);
+                if (nt == 3) return with(std::integral_constant<int, 3>());
+                if (nt == 4) return with(std::integral_constant<int, 4>());
             }
-            return f(attn_kv4_kernel<T, W, 2>, Shape<W, 2>::kSmem, Shape<W, 2>::kPerSm);
+            return with(std::integral_constant<int, 2>());
         };
         switch (D) {
             case 64: return of(std::integral_constant<int, 64>());
@@ -582,11 +637,17 @@ bool worth_reading(int B, int at_once, long long rows, int Hkv, int D, int cap, 
 #endif
 }
 
+// Segments for each block, at least, for blocks to finish those that they hold.
+#ifndef MQ_KV4_SPLIT_FROM      // (test builds: 0)
+#define MQ_KV4_SPLIT_FROM 1
+#endif
+
 // How a call is cut.
 struct Kv4Cut {
     bool read, fits;
     int nt, at_once;               // read: sequences at once
     Plan plan;
+    bool split;                    // segments that one block holds are finished by it
     size_t kv, o, ml, info, bytes; // read: bytes of the 16-bit keys (and of the values)
 };
 
@@ -626,9 +687,9 @@ Kv4Cut cut_kv4(int B, int T, int Hq, int Hkv, int D, int cap) {
     p.lanes = 1;
     p.by_group = div_by(group);
     p.by_per_seq = div_by(own_tiles_of_rows(p));
-    const long long segs = all_segs(p), most = segs * ceil_div(cap, p.keys);
+    const long long segs = cap > 0 ? all_segs(p) : 0, most = segs * ceil_div(cap, p.keys);
     int per_sm = 1;
-    with_kernel(D, MQ_F16, c.nt, [&](auto, int, int n) { return per_sm = n; });
+    with_kernel(D, MQ_F16, c.nt, false, [&](auto, int, int n) { return per_sm = n; });
     const long long held = (long long)mq::num_sms() * per_sm;
     // Beginning and ending a segment costs about a tile. Where there are few tiles, and their pieces few bytes to join, each has a
     // warp of its own (one sequence of 1000 rows: 8.8 us, with runs of two tiles and more 9.9, of three 11.0; 32 queries of 7 heads on
@@ -636,11 +697,15 @@ Kv4Cut cut_kv4(int B, int T, int Hq, int Hkv, int D, int cap) {
     p.extra = most <= 2 * held && most * p.rows * D * 4 <= 12 << 20 ? 0 : 1;
     if (most + segs * p.extra > 0x7fffffffLL || segs > 0x3fffffffLL) c.fits = false;
     p.G = (int)(most < held ? most : held);
+    // Where there are fewer segments than blocks most lie in several, and each row has a warp to add its pieces up (attn_join_kernel);
+    // else most lie in one or two (512 sequences of up to 2000 rows: 144 us that way, 140 this; 2048 of up to 300: 201 and 135).
+    c.split = c.nt <= kFinMost && segs >= (long long)MQ_KV4_SPLIT_FROM * p.G;
+    p.own_least = c.split ? 1 : 0;
     const size_t places = (size_t)p.G + (size_t)segs;
     c.o = 0;
     c.ml = up16(places * p.rows * D * sizeof(float));
     c.info = c.ml + up16(places * p.rows * sizeof(float2));
-    c.bytes = c.info + up16((size_t)segs * sizeof(int2));
+    c.bytes = c.info + up16(c.split ? (size_t)p.G * sizeof(int4) : (size_t)segs * sizeof(int2));
     return c;
 }
 
@@ -727,11 +792,24 @@ extern "C" int mq_attn_kv4(const void* q, int type, long long q_stride, int B, i
         f.len = len;
         f.scale_log2 = scale * 1.4426950408889634f;
         f.out = pieces;
-        rc = with_kernel(D, type, c.nt, [&](auto kern, int smem, int) {
+        f.split = c.split ? reinterpret_cast<int4*>(base + c.info) : nullptr;
+        f.fin = {out, lse, out_type == MQ_F32};
+        rc = with_kernel(D, type, c.nt, c.split, [&](auto kern, int smem, int) {
             if (!mq::allow_smem(reinterpret_cast<const void*>(kern), smem)) return (int)MQ_ERR_LAUNCH;
             return mq::launch_pdl(kern, dim3(c.plan.G), dim3(32), smem, stream, f);
         });
         if (rc != MQ_OK) return rc;
+        if (c.split) {
+            auto join = [&](auto o) {
+                using O = decltype(o);
+                auto kern = D == 64 ? join_split_kernel<O, 64> : D == 96 ? join_split_kernel<O, 96>
+                            : D == 128 ? join_split_kernel<O, 128> : join_split_kernel<O, 256>;
+                if (!mq::allow_smem(reinterpret_cast<const void*>(kern), 0)) return (int)MQ_ERR_LAUNCH;
+                const int rows = T * (Hq / Hkv) < c.plan.rows ? T * (Hq / Hkv) : c.plan.rows;
+                return mq::launch_pdl(kern, dim3(c.plan.G, rows), dim3(32), 0, stream, f);
+            };
+            return out_type == MQ_F32 ? join(float()) : out_type == MQ_F16 ? join(__half()) : join(__nv_bfloat16());
+        }
     }
     JoinArgs j = {};
     j.own = {pieces, cap > 0 ? c.plan.rows : 0, c.plan};

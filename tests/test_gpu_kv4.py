@@ -254,6 +254,17 @@ def test_read_strides():
 
 # ------------------------------------------------------------------------------------------- attention
 
+@pytest.fixture(params=["as it is", "finished by blocks"])
+def finish(request):
+    """The library, and a test build that finishes segments in the blocks that hold them in calls of any size (the library: from
+    609 query rows on)."""
+    own = mq.lib()
+    if request.param != "as it is":
+        mq._lib = mq._load(B.build_variant("kv4_split", ["MQ_KV4_SPLIT_FROM=0", "MQ_TEST_INJECT", "MQ_WAIT_LIMIT_NS=50000000ull"]))
+    yield
+    mq._lib = own
+
+
 def _inside(got, want, bound, what):
     got = got.double()
     assert not torch.isnan(got).any(), f"{what}: NaN"
@@ -302,46 +313,53 @@ def _attn_case(T, Hq, Hkv, D, rows, lens, dtype=F16, out_dtype=None, seed=0, std
 @pytest.mark.parametrize("D", [64, 96, 128, 256])
 @pytest.mark.parametrize("dtype", [F16, BF16])
 @pytest.mark.parametrize("T", [1, 3])
-def test_attention_widths(D, dtype, T):
+def test_attention_widths(D, dtype, T, finish):
     _attn_case(T, 8, 2, D, 32, [1, 16, 31, 33, 64, 100, 0, 150], dtype, seed=D + T)
 
 
 @pytest.mark.parametrize("rows", [16, 32, 64, 128, 1024])
-def test_attention_pages(rows):
+def test_attention_pages(rows, finish):
     _attn_case(1, 7, 1, 128, rows, [5, 15, 17, 200, 129, 1000], BF16, seed=rows)
 
 
 @pytest.mark.parametrize("Hq,Hkv", [(1, 1), (3, 1), (8, 1), (9, 1), (17, 1), (25, 1), (33, 1), (28, 4), (64, 8), (70, 2)])
-def test_attention_groups(Hq, Hkv):
+def test_attention_groups(Hq, Hkv, finish):
     _attn_case(1, Hq, Hkv, 128, 64, [77, 1, 300], F16, seed=Hq)
 
 
 @pytest.mark.parametrize("T", [2, 5, 8, 16, 19])
 @pytest.mark.parametrize("D", [64, 128, 256])
-def test_attention_several_queries(T, D):
+def test_attention_several_queries(T, D, finish):
     """Fewer rows than queries, too: those queries see nothing."""
     _attn_case(T, 12, 3, D, 16, [T, T + 1, 40, 97, 1, 0, T - 1], BF16, seed=T)
 
 
 @pytest.mark.parametrize("out_dtype", [F16, BF16, F32])
-def test_attention_out_types(out_dtype):
+def test_attention_out_types(out_dtype, finish):
     _attn_case(1, 8, 2, 128, 64, [100, 31], BF16 if out_dtype == BF16 else F16, out_dtype, seed=1)
 
 
-def test_attention_long():
+def test_attention_long(finish):
     """Several blocks a sequence, ragged, with pieces joined."""
     _attn_case(1, 40, 8, 128, 64, [9000, 17, 20011, 1], F16, seed=2)
     _attn_case(4, 14, 2, 64, 32, [5000, 3, 12345], BF16, seed=3)
 
 
-def test_attention_holes():
+def test_attention_many_sequences():
+    """Enough rows that the library itself finishes segments in their blocks; some sequences are empty."""
+    lens = [(37 * i) % 150 for i in range(90)] + [0, 1, 2500]
+    _attn_case(1, 8, 2, 128, 32, lens, F16, seed=77)
+    _attn_case(2, 8, 2, 64, 16, lens[:60], BF16, F32, seed=78)
+
+
+def test_attention_holes(finish):
     """Entries that are no page read as zero rows."""
     _attn_case(1, 8, 2, 128, 16, [100, 64, 16], F16, seed=4, holes=[(0, 1, -1), (0, 4, 10 ** 9), (1, 3, (0, 2)), (2, 0, -7)])
     _attn_case(2, 8, 2, 64, 64, [200, 64], BF16, seed=5, holes=[(0, 1, -1), (1, 0, -2 ** 31)])
     _attn_case(60, 8, 2, 128, 64, [200, 130], F16, seed=6, holes=[(0, 1, -1), (1, 0, 5000)], only=[0, 31, 59])
 
 
-def test_attention_lengths_outside():
+def test_attention_lengths_outside(finish):
     """Negative lengths are empty, those past the table end at it."""
     cache, q, _, _, _ = _attn_case(1, 4, 2, 64, 16, [32, 48], F16, seed=7, width=3)
     out = torch.empty_like(q)
@@ -364,7 +382,7 @@ def test_attention_scales(scale):
 
 
 @pytest.mark.parametrize("dtype", [F16, BF16])
-def test_attention_large_products(dtype):
+def test_attention_large_products(dtype, finish):
     """Products of 2^20 and more, with the maximum growing from tile to tile."""
     _attn_case(1, 4, 1, 64, 32, [200], dtype, seed=9, std=300.0, k_std=60.0, scale=3.0)
 
@@ -384,7 +402,7 @@ def test_attention_strided_queries_and_stream():
     assert torch.equal(out, want)
 
 
-def test_attention_row_is_its_own():
+def test_attention_row_is_its_own(finish):
     """A row's bits do not depend on its neighbours' numbers."""
     n, Hq, Hkv, D = 2, 16, 2, 128
     cache = R.random_cache(n, 8, 64, Hkv, D, 13)
@@ -463,26 +481,25 @@ def test_offsets_past_2_31():
     assert torch.equal(pages[P - 2:], small.pages)
 
 
-def test_prompt_in_parts():
-    """A test build that reads a few sequences at a time gives the same bits as the call that reads all at once."""
-    n, T, Hq, Hkv, D = 5, 70, 8, 2, 128
+@pytest.mark.parametrize("n", [2, 5])
+def test_prompt_read_into_16_bits(n):
+    """A test build that reads the rows of calls of any size into 16 bits, those of two sequences at a time."""
+    T, Hq, Hkv, D = 70, 8, 2, 128
     cache = R.random_cache(n, 5, 64, Hkv, D, 51)
-    length = torch.tensor([320, 100, 0, 71, 255], dtype=torch.int32, device="cuda")
+    lens = [320, 100, 0, 71, 255][:n]
+    length = torch.tensor(lens, dtype=torch.int32, device="cuda")
     q = _rand((n, T, Hq, D), 52, 1.0, F16)
-    own, outs = mq.lib(), []
-    for name, defines in (("kv4_all", ["MQ_KV4_READ_FROM=1"]),
-                          ("kv4_parts", ["MQ_KV4_READ_FROM=1", "MQ_KV4_READ_BYTES=700000"])):
-        try:
-            mq._lib = mq._load(B.build_variant(name, defines))
-            out, lse = torch.zeros_like(q), torch.zeros((n, T, Hq), device="cuda")
-            mq.mq_attn_kv4(q, cache, length, out, lse=lse)
-            torch.cuda.synchronize()
-            assert mq.mq_device_status() == mq.MQ_OK
-            outs.append((out, lse))
-        finally:
-            mq._lib = own
-    k, v = R.gather(cache.pages, cache.table, 64, Hkv, D, length.tolist())
-    want, bound = A.attention(q, None, None, k, v, length.tolist(), D ** -0.5, F16, only=[0, 35, 69])
-    for out, lse in outs:
-        _inside(out[:, [0, 35, 69]], want[0][:, [0, 35, 69]], bound[0][:, [0, 35, 69]], "out")
-        _inside(lse[:, [0, 35, 69]], want[1][:, [0, 35, 69]], bound[1][:, [0, 35, 69]], "lse")
+    own = mq.lib()
+    try:
+        mq._lib = mq._load(B.build_variant("kv4_read", ["MQ_KV4_READ_FROM=1", "MQ_KV4_READ_BYTES=700000"]))
+        out, lse = torch.zeros_like(q), torch.zeros((n, T, Hq), device="cuda")
+        mq.mq_attn_kv4(q, cache, length, out, lse=lse)
+        torch.cuda.synchronize()
+        assert mq.mq_device_status() == mq.MQ_OK
+    finally:
+        mq._lib = own
+    k, v = R.gather(cache.pages, cache.table, 64, Hkv, D, lens)
+    some = [0, 35, 69]
+    want, bound = A.attention(q, None, None, k, v, lens, D ** -0.5, F16, only=some)
+    _inside(out[:, some], want[0][:, some], bound[0][:, some], "out")
+    _inside(lse[:, some], want[1][:, some], bound[1][:, some], "lse")

@@ -196,7 +196,7 @@ def test_wait_runs_out_is_reported_and_forgotten():
     """A test build (50 ms wait limit) whose first block leaves out a copy: the call returns, the status says so once, and the
     next call is right."""
     own = mq.lib()
-    L = mq._load(B.build_variant("kv4_inject", ["MQ_TEST_INJECT", "MQ_WAIT_LIMIT_NS=50000000ull"]))
+    L = mq._load(B.build_variant("kv4_split", ["MQ_KV4_SPLIT_FROM=0", "MQ_TEST_INJECT", "MQ_WAIT_LIMIT_NS=50000000ull"]))
     L.mq_test_inject_kv4.restype, L.mq_test_inject_kv4.argtypes = ctypes.c_int, [ctypes.c_int]
     mq._lib = L
     try:
