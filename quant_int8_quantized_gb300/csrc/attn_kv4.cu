@@ -12,8 +12,8 @@
 //    instruction) to become the right operand of O^T += V^T P^T.
 //  - The maximum that the exponents are taken against is renewed when a row passes it by 2^8 (each row by itself, so that
 //    no row's bits depend on its neighbours), which leaves one vote a tile.
-// Measured: 64 sequences of 9000 to 20000 rows, 40 query and 8 key heads of 128 (1 GB), 202 us, 5.0 TB/s (its copies alone 157); one of
-// 1000 rows, 8.8 us with the join, which is latency.
+// Measured: 64 sequences of 9000 to 20000 rows, 40 query and 8 key heads of 128 (1 GB), 191 us, 5.3 TB/s (its copies alone 157 to 166, all
+// but them 164); one of 1000 rows, 9 us with the join, which is latency.
 // Many rows (a prompt): the rows in use are read once into 16 bits in the workspace and mq_attn_prefix's tensor-core kernel
 // takes them from there; n d being exact, both ways compute the same products.
 
@@ -34,7 +34,6 @@ __device__ unsigned int g_kv4_error;   // bit 0: a bounded wait gave up
 __device__ int g_kv4_skip_tile;        // test builds only: block 0 leaves out its first tile
 #endif
 
-
 constexpr int keys_of(int D, int NT) { return D <= 64 || (D <= 128 && NT == 2) ? 64 : 32; }    // of a tile (measured)
 constexpr int kStep = 32;              // keys that are multiplied at once
 
@@ -42,12 +41,12 @@ template <int D, int NT>
 struct Shape {
     static constexpr int kKeys = keys_of(D, NT);
     static constexpr int kTile = kKeys / kv4::kBlockRows * kv4::block_bytes(D);
-    static constexpr int kStages = D <= 64 || D > 128 || NT > 1 ? 2 : 3;
+    static constexpr int kStages = D <= 64 || D > 128 || NT > 1 ? 2 : 3;   // (a third for 32 rows: no difference)
     static constexpr int kStage = kTile + 16;                        // a tile, its barrier
     static constexpr int kRing = kStages * kStage;
     static constexpr int kScales = kStep / 2 * (D / 32) * 16;        // a step's
-    // more than eight rows: their operands lie in shared memory, each lane's where it alone reads them (registers would do for 8
-    // warps an SM instead of 12)
+    // more than eight rows: their operands (D / 8 registers of a lane for each eight) lie in shared memory, where the lane alone
+    // reads them (24 rows: 46 us for 40 with them in registers, which spilled)
     static constexpr bool kQueries = NT > 1;
     static constexpr int kSmem = kRing + kScales + (kQueries ? NT * (D / 32) * 512 : 0);
     // warps an SM, as registers allow (the outputs alone are D NT / 4 of a lane's); the same number on each of its four parts: 14

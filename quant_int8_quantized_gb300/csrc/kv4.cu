@@ -50,8 +50,7 @@ __device__ __forceinline__ float2 turn(int pos, float freq, float by) {
     return make_float2(c * by, s * by);
 }
 
-// sin and cos of pi t for |t| <= 1 by their power series, to 2^-52. (Few instructions: where this runs, its code is seldom at hand,
-// and fetching it takes longer than running it.)
+// sin and cos of pi t for |t| <= 1 by their power series, to 2^-51.
 __device__ __forceinline__ void sincos_pi(double t, double& s, double& c) {
     const double k = rint(2.0 * t), x = fma(-0.5, k, t) * 3.14159265358979323846, z = x * x;   // |x| <= pi / 4
     double u = 1.0 / 1307674368000.0, v = 1.0 / 20922789888000.0;
@@ -69,14 +68,6 @@ __device__ __forceinline__ void sincos_pi(double t, double& s, double& c) {
     if (q >= 2) s = -s;
     if (q == 1 || q == 2) c = -c;
 }
-// 1 / sqrt(x) in 64 bits: two steps of Newton's from the 32-bit one.
-__device__ __forceinline__ double inv_sqrt(double x) {
-    double y = rsqrtf((float)x);
-#pragma unroll 1
-    for (int i = 0; i < 2; ++i) y = fma(fma(-x * y, y, 1.0), 0.5 * y, y);
-    return y;
-}
-
 // The least code whose 7 d is `a` or more.
 __device__ __forceinline__ int code_of(float a) {
     if (!(a < 3360.0f)) return kMostCode;
@@ -183,7 +174,7 @@ __global__ void __launch_bounds__(kThreads) fill_kernel(const FillArgs a) {
         for (int i = 0; i < 8; ++i) v[i] = now.v[i];
         now = next;
         const float* w = what == 2 ? nullptr : a.w[what];
-        float ss = 0.0f;
+        float ss = 0.0f, mean = 1.0f;
         if (a.w[0] || a.w[1]) {
             float pr[4];
 #pragma unroll
@@ -193,7 +184,8 @@ __global__ void __launch_bounds__(kThreads) fill_kernel(const FillArgs a) {
             for (int o = LG / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
         }
         if (w && live) {
-            const float sc = 1.0f / sqrtf(ss / (float)D + a.eps);
+            mean = ss / (float)D + a.eps;
+            const float sc = 1.0f / sqrtf(mean);
             if constexpr (VEC) {
                 const float4 w0 = __ldg(reinterpret_cast<const float4*>(w + lo));
                 const float4 w1 = __ldg(reinterpret_cast<const float4*>(w + hi));
@@ -286,8 +278,8 @@ __global__ void __launch_bounds__(kThreads) fill_kernel(const FillArgs a) {
             far = fmaxf(far, fabsf(quot[i] - (m - 12582920.0f)));
             num[i] = __float_as_uint(m);
         }
-        // (a rotated or normed v is off by `off`: what lies next to a border goes to the list)
-        const bool near = !exact && (!(far < 0.5f - 1e-6f - off * inv) || !(most < 3360.0f - off) ||
+        // (a rotated or normed v is off by `off`: what lies next to a border goes to the list, and what 32 bits have no room for)
+        const bool near = !exact && (!(mean > 1e-30f && mean < 3e38f) || !(far < 0.5f - 1e-6f - off * inv) || !(most < 3360.0f - off) ||
                           (most > 0.0f && (7.0f * d < most + off || (code > 0 && 7.0f * scale_of(code - 1) >= most - off))));
         const uint32_t again = __ballot_sync(0xffffffffu, near && live) >> (threadIdx.x & 31 & ~(LG - 1)) &
                                (LG == 32 ? ~0u : (1u << (LG & 31)) - 1);
@@ -336,7 +328,7 @@ __global__ void __launch_bounds__(kThreads) fill_kernel(const FillArgs a) {
             for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
             if (wl == 0) s_part[wid] = sum;
             __syncthreads();
-            by = inv_sqrt((s_part[0] + s_part[1] + s_part[2] + s_part[3]) * (1.0 / D) + (double)a.eps);
+            by = 1.0 / sqrt((s_part[0] + s_part[1] + s_part[2] + s_part[3]) / D + (double)a.eps);
         }
         auto normed = [&](int i) { return w ? (double)x[i] * by * (double)w[i] : (double)x[i]; };
         for (int p = tid; p < n; p += kThreads) {

@@ -135,6 +135,26 @@ def test_fill_scales(std):
     _fill_case(64, 2, 2, 128, 64, 1, 64, norm=False, seed=9, std=std)
 
 
+def test_fill_norm_of_any_size():
+    """Heads whose mean square 32 bits do not hold, and zeros, normed."""
+    M, H, D = 24, 2, 64
+    x = _rand((M, H, D), 91)
+    x *= (10.0 ** torch.linspace(-30, 30, M, device="cuda"))[:, None, None]
+    x[5, 0] = 0.0
+    cache = mq.KV4.empty(1, 2, 2, H, D, 16)
+    cache.table.copy_(torch.tensor([[1, 0]]))
+    cache.pages.zero_()
+    wk, row = _rand((D,), 92, 0.1) + 1, torch.arange(M, dtype=torch.int32, device="cuda")
+    freq, pos = mq.rope_freq(32, device="cuda"), row + 3
+    for eps in (1e-6, 0.0):
+        mq.mq_qk_norm_rope_kv4(None, x, None, None, cache, None, row, pos, freq, wk=wk, eps=eps)
+        y = _rope64(x, wk, float(torch.tensor(eps)), pos[None], freq, None, 1, False, 1.0)
+        want = R.value4(*R.round4(y))
+        got = R.unpack(cache.pages[[1, 0]], 16, H, D)[0].flatten(0, 1)[:M]
+        bad = ((got != want) & torch.isfinite(y)).nonzero()          # (zeros over zero have no value)
+        assert len(bad) == 0, (eps, len(bad), bad[:4].tolist(), [(float(y[tuple(b)]), float(got[tuple(b)])) for b in bad[:4].tolist()])
+
+
 def test_fill_ties_and_grid():
     """Rows whose numbers lie on borders, whose largest lies on a scale's, and zeros."""
     M, H, D = 96, 2, 128
