@@ -553,7 +553,7 @@ typedef struct mq_pool {
 
 /*
  * mq_pages_next — m sequences from n: new sequence b goes on from old sequence from[b] (outside 0 .. n - 1: from nothing; from NULL:
- * from b, and m == n), of which it keeps the first L = min(len[from[b]], keep[b]) rows (keep NULL: all), and is given place for add[b] more
+ * from b, and m == n or 0), of which it keeps the first L = min(len[from[b]], keep[b]) rows (keep NULL: all), and is given place for add[b] more
  * (add NULL: none):
  *     table_out[b] = the ceil(L / page_rows) first entries of the old table, then new pages up to row L + add[b], then -1,
  *     len_out[b] = L + add[b].

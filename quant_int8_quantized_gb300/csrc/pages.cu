@@ -7,6 +7,7 @@
 // writing where a launch each would take two or three times that; the tables of a whole pool of 80000 pages are
 // some hundred entries a thread. The second, as wide as the GPU, copies what the first has listed. A copy's
 // source is a page that stays, its target one that nobody holds, so copies in any order are right.
+// (4, 8 and 16 blocks: 16 beams 13.6, 14.7, 17.9 us; 256 sequences 25.2, 18.5, 18.7, whose counts are scattered.)
 // Bound: the tables' part by the latency of some six barriers, copies by HBM.
 
 #include "heads.cuh"
@@ -429,7 +430,8 @@ extern "C" int mq_pages_next(const mq_pool* pool, const int32_t* table, const in
     using namespace pages;
     int rc = check_pool(pool, true);
     if (rc != MQ_OK) return rc;
-    if (!valid_table(n, width, pool->page_rows) || !valid_table(m, width, pool->page_rows) || (!from && n != m)) return MQ_ERR_SHAPE;
+    if (!valid_table(n, width, pool->page_rows) || !valid_table(m, width, pool->page_rows) || (!from && m > 0 && n != m))
+        return MQ_ERR_SHAPE;
     if (!status || !ws) return MQ_ERR_NULL;
     if ((n > 0 && (!len || (width > 0 && !table))) || (m > 0 && (!len_out || (width > 0 && !table_out)))) return MQ_ERR_NULL;
     for (const void* p : {(const void*)table, (const void*)len, (const void*)from, (const void*)keep, (const void*)add,

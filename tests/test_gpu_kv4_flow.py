@@ -1,6 +1,7 @@
 """The 4-bit cache's calls together, as a serving loop makes them, in lock step with sequences kept as plain lists of rows;
 and around them: memory that the binding allocates, calls at the same time, a copy that never comes."""
 import ctypes
+import math
 
 import pytest
 import torch
@@ -221,3 +222,71 @@ def test_wait_runs_out_is_reported_and_forgotten():
     finally:
         L.mq_test_inject_kv4(0)
         mq._lib = own
+
+
+@pytest.mark.parametrize("T", [1, 5, 70])
+def test_tables_and_pools_of_nothing(T):
+    """Tables without entries, pools without pages: queries are there all the same."""
+    n, Hq, H, D, rows = 2, 8, 2, 64, 16
+    q = torch.randn((n, T, Hq, D), device="cuda").to(F16)
+    none = torch.empty((n, 0), dtype=I32, device="cuda")
+    holes = torch.full((n, 5), -1, dtype=I32, device="cuda")
+    size = mq.mq_kv4_page_bytes(rows, H, D)
+    some, empty = torch.zeros((3, size), dtype=torch.uint8, device="cuda"), torch.empty((0, size), dtype=torch.uint8, device="cuda")
+    length = torch.tensor([77, 80], dtype=I32, device="cuda")
+    for cache, seen in ((mq.KV4(some, none, rows, H, D), 0), (mq.KV4(empty, none, rows, H, D), 0), (mq.KV4(empty, holes, rows, H, D), 77)):
+        out, lse = torch.full_like(q, 3.0), torch.zeros((n, T, Hq), device="cuda")
+        mq.mq_attn_kv4(q, cache, length, out, lse=lse)
+        assert (out == 0).all()
+        for b in range(n):
+            for t in range(T):
+                k = max(0, min(int(length[b]), cache.cap) - T + 1 + t)       # all keys are zeros
+                want = math.log(k) if k else -math.inf       # (log(128 k) - 7 log 2, a rounding or two of 2^-24 of each)
+                assert all(x == want or abs(x - want) <= 2e-6 * abs(want) + 2e-6 for x in lse[b, t].tolist())
+        x, q_out = torch.randn((4, Hq, D), device="cuda"), torch.zeros((4, Hq, D), dtype=F16, device="cuda")
+        k = torch.randn((4, H, D), device="cuda")
+        row = torch.arange(4, dtype=I32, device="cuda")
+        mq.mq_qk_norm_rope_kv4(x, k, k, q_out, cache, None, row)
+        assert torch.equal(q_out, x.to(F16))
+        kv = mq.KV.empty(n, 96, H, D)
+        kv.k.fill_(7.0)
+        kv.v.fill_(7.0)
+        mq.mq_kv4_read(cache, length, kv)
+        for b in range(n):
+            m = min(int(length[b]), cache.cap)
+            for y in (kv.k[b], kv.v[b]):
+                assert (y[:m] == 0).all() and (y[m:] == 7).all()
+    assert (some == 0).all()
+    assert mq.mq_device_status() == mq.MQ_OK
+
+
+def test_pages_of_nothing():
+    status, live = torch.full((3,), 9, dtype=I32, device="cuda"), torch.full((1,), 9, dtype=I32, device="cuda")
+
+    def ints(*x):
+        return torch.tensor(x, dtype=I32, device="cuda")
+
+    def table(n, width):
+        return torch.full((n, width), 77, dtype=I32, device="cuda")
+
+    pool = mq.Pool(torch.zeros((2, 6, 32), dtype=torch.uint8, device="cuda"), 16)
+    # from no sequences
+    out, length = table(2, 3), ints(5, 5)
+    mq.mq_pages_next(pool, table(0, 3), ints(), out, length, status, ints(0, -1), None, ints(17, 0))
+    assert (out.tolist(), length.tolist(), status.tolist()) == ([[0, 1, -1], [-1, -1, -1]], [17, 0], [0, 4, 0])
+    # to none
+    mq.mq_pages_next(pool, out, length, table(0, 3), ints(), status, ints(), None, None)
+    assert status.tolist() == [0, 6, 0]
+    # tables without entries
+    mq.mq_pages_next(pool, table(2, 0), ints(4, 4), table(2, 0), length, status, None, None, ints(1, 0))
+    assert (length.tolist(), status.tolist()) == ([0, 0], [0, 6, 1])
+    # no pages
+    bare = mq.Pool(torch.zeros((2, 0, 32), dtype=torch.uint8, device="cuda"), 16)
+    out, length = table(2, 3), ints(0, 0)
+    mq.mq_pages_next(bare, table(2, 3), ints(0, 0), out, length, status, None, None, ints(1, 0))
+    assert (out.tolist(), length.tolist(), status.tolist()) == ([[-1] * 3] * 2, [0, 0], [1, 0, 0])
+    mq.mq_pages_compact(bare, out, length, out, ints(), live)
+    assert live.tolist() == [0]
+    where = torch.full((6,), 9, dtype=I32, device="cuda")
+    mq.mq_pages_compact(pool, table(0, 3), ints(), table(0, 3), where, live)
+    assert (where.tolist(), live.tolist()) == ([-1] * 6, [0])
