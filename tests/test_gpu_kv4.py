@@ -321,6 +321,12 @@ def _attn_case(T, Hq, Hkv, D, rows, lens, dtype=F16, out_dtype=None, seed=0, std
     torch.cuda.synchronize()
     assert mq.mq_device_status() == mq.MQ_OK
     want, bound = A.attention(q, None, None, k, v, lens, scale, out_dtype, only=only)
+    # Weights are in f16 for bf16 queries too: the largest of a row is 2^7 or more, half of f16's least step 2^-25, and the sum
+    # no less than the largest, so besides 2^-8 (2^-11) of itself a weight is off by at most 2^-32. Seen where the values of all
+    # heavier keys are zeros.
+    used = torch.arange(v.shape[1], device="cuda") < length[:, None]
+    floor = 2.0 ** -32 * (v.abs() * used[..., None, None]).sum(1).repeat_interleave(Hq // Hkv, 1)[:, None]
+    bound = (bound[0] + floor, bound[1])
     sel = slice(None) if only is None else only
     _inside(out.t[:, sel], want[0][:, sel], bound[0][:, sel], "out")
     _inside(lse.t[:, sel], want[1][:, sel], bound[1][:, sel], "lse")
@@ -363,6 +369,11 @@ def test_attention_long(finish):
     """Several blocks a sequence, ragged, with pieces joined."""
     _attn_case(1, 40, 8, 128, 64, [9000, 17, 20011, 1], F16, seed=2)
     _attn_case(4, 14, 2, 64, 32, [5000, 3, 12345], BF16, seed=3)
+
+
+def test_attention_light_weights(finish):
+    """Dims whose value is zero at all keys but the lightest, in full precision."""
+    _attn_case(1, 36, 3, 256, 1024, [3, 0, 1, 6, 6, 4, 1], BF16, out_dtype=F32, seed=267439, std=6.0)
 
 
 def test_attention_many_sequences():
