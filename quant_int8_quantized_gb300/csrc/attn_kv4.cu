@@ -219,9 +219,9 @@ __global__ void __launch_bounds__(32, Shape<D, NT>::kPerSm) attn_kv4_kernel(cons
         }
         if (at + parts > 32) {                         // the next 32 parts' places, a lane each
             at = 0;
-            const int row = key + lane * part_rows;
-            const int page = row >> a.c.shift < a.c.width ? a.c.page(seq, row) : -1;
-            src = page >= 0 ? a.c.block(page, head, row, kBlock) : nullptr;
+            const unsigned row = (unsigned)key + lane * part_rows;      // (up to 1984 past a cache's end: past 2^31, too)
+            const int page = row >> a.c.shift < (unsigned)a.c.width ? a.c.page(seq, (int)row) : -1;
+            src = page >= 0 ? a.c.block(page, head, (int)row, kBlock) : nullptr;
             there = __ballot_sync(0xffffffffu, src != nullptr);
         }
         return min(left, (32 - at) / parts);
