@@ -264,14 +264,14 @@ __global__ void __launch_bounds__(kThreads) fill_kernel(const FillArgs a) {
         // another v / d lies more than half a unit away.
         float quot[8], far = 0.0f;
         uint32_t num[8];
+        if (__any_sync(0xffffffffu, !(most <= 3360.0f)))   // past 7 d of the largest scale: as 7 d (an infinity has no rest)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = fminf(fmaxf(v[i], -3360.0f), 3360.0f);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float q = v[i] * inv;
             quot[i] = fmaf(fmaf(-q, d, v[i]), inv, q);
         }
-        if (__any_sync(0xffffffffu, !(most <= 3360.0f)))
-#pragma unroll
-            for (int i = 0; i < 8; ++i) quot[i] = fminf(fmaxf(quot[i], -7.0f), 7.0f);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float m = quot[i] + 12582920.0f;
