@@ -506,6 +506,7 @@ size_t mq_kv4_page_bytes(int page_rows, int heads, int dim);
  * q_out: [M][Hq][D] in `type` (MQ_F16, MQ_BF16), rounded once. For each block of 32 dims of a key or value y: d is the least
  * scale with 7 d >= max |y| (480 where that is more than 3360), n = rint(y / d), ties to even, within -7 .. 7. Both are decided for
  * y as the formula gives it (where 32 bits do not tell, in 64), so what is written does not depend on the order of 32-bit sums.
+ * An infinity is n = 7 or -7 (d = 480); a NaN is taken as 0, for the block's largest too.
  * A token whose sequence, row or page there is none is skipped (its queries are not). Two tokens must not have the same place.
  * q_out, the pages and q, k, v lie apart (MQ_ERR_SHAPE). row is required with k or v. Otherwise as mq_qk_norm_rope.
  */

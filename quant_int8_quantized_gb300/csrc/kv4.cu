@@ -68,6 +68,11 @@ __device__ __forceinline__ void sincos_pi(double t, double& s, double& c) {
     if (q >= 2) s = -s;
     if (q == 1 || q == 2) c = -c;
 }
+__device__ __forceinline__ float max_nan(float a, float b) {   // NaN if one of them is
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
 // The least code whose 7 d is `a` or more.
 __device__ __forceinline__ int code_of(float a) {
     if (!(a < 3360.0f)) return kMostCode;
@@ -246,14 +251,25 @@ __global__ void __launch_bounds__(kThreads) fill_kernel(const FillArgs a) {
             }
             __syncwarp();
         }
-        float most = 0.0f;
+        float most;                                                         // of the block of 32 dims; NaN where one of them is
+        auto find_most = [&] {
+            most = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(v[i]));
-        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
-        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));          // of the block of 32 dims
+            for (int i = 0; i < 8; ++i) most = max_nan(most, fabsf(v[i]));
+            most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, 1));
+            most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, 2));
+        };
+        find_most();
         float all = most;
 #pragma unroll
-        for (int o = 4; o < LG; o <<= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, o));
+        for (int o = 4; o < LG; o <<= 1) all = max_nan(all, __shfl_xor_sync(0xffffffffu, all, o));
+        if (__any_sync(0xffffffffu, !(most <= 3360.0f))) {
+            // past 7 d of the largest scale: as 7 d (an infinity has no rest); no number: 0. (A head that this changes, and that is not to be
+            // rounded as it is, goes to the list by `all`.)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = v[i] == v[i] ? fminf(fmaxf(v[i], -3360.0f), 3360.0f) : 0.0f;
+            find_most();
+        }
         const bool exact = what != 1 || (!w && n == 0);                     // v is what there is to round
         const float off = exact ? 0.0f : all * (w ? kOffNorm : kOffTurn);
         int code = code_of(most);
@@ -264,9 +280,6 @@ __global__ void __launch_bounds__(kThreads) fill_kernel(const FillArgs a) {
         // another v / d lies more than half a unit away.
         float quot[8], far = 0.0f;
         uint32_t num[8];
-        if (__any_sync(0xffffffffu, !(most <= 3360.0f)))   // past 7 d of the largest scale: as 7 d (an infinity has no rest)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = fminf(fmaxf(v[i], -3360.0f), 3360.0f);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float q = v[i] * inv;
@@ -279,7 +292,7 @@ __global__ void __launch_bounds__(kThreads) fill_kernel(const FillArgs a) {
             num[i] = __float_as_uint(m);
         }
         // (a rotated or normed v is off by `off`: what lies next to a border goes to the list, and what 32 bits have no room for)
-        const bool near = !exact && (!(mean > 1e-30f && mean < 3e38f) || !(far < 0.5f - 1e-6f - off * inv) || !(most < 3360.0f - off) ||
+        const bool near = !exact && (!(mean > 1e-30f && mean < 3e38f) || !(far < 0.5f - 1e-6f - off * inv) || !(all < 3360.0f - off) ||
                           (most > 0.0f && (7.0f * d < most + off || (code > 0 && 7.0f * scale_of(code - 1) >= most - off))));
         const uint32_t again = __ballot_sync(0xffffffffu, near && live) >> (threadIdx.x & 31 & ~(LG - 1)) &
                                (LG == 32 ? ~0u : (1u << (LG & 31)) - 1);
@@ -348,7 +361,8 @@ __global__ void __launch_bounds__(kThreads) fill_kernel(const FillArgs a) {
         __syncthreads();
         uint8_t* block = a.c.block(page, h, row, block_bytes(D));
         for (int b = wid; b < nb; b += kThreads / 32) {
-            const double y = s_y[32 * b + wl];
+            double y = s_y[32 * b + wl];
+            if (y != y) y = 0.0;
             long long top = __double_as_longlong(y) & 0x7fffffffffffffffLL;   // (numbers without their sign are in the order of their bits)
 #pragma unroll 1
             for (int o = 16; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
