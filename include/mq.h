@@ -567,9 +567,9 @@ typedef struct mq_pool {
  *     status[1] = pages that are free now;
  *     status[2] = sequences whose L + add[b] rows are more than the table holds: they are given none.
  * table: int32 [n][width], table_out: int32 [m][width], len, len_out: int32 [n], [m]; from, keep, add: int32 [m]; status: int32 [3]; all on
- * the device, 16-byte aligned. table_out may be table and len_out may be len; they must not overlap otherwise (MQ_ERR_SHAPE). Lengths are
- * taken as 0 below 0 and as width * page_rows above it, keep and add as 0 below 0. n * (width + 1) and width * page_rows
- * below 2^31.
+ * the device, 16-byte aligned. table_out may be table and len_out may be len; otherwise table_out, len_out, status and the workspace
+ * overlap neither each other nor what is read, and none of all these the pool's pages (MQ_ERR_SHAPE). Lengths are taken as 0 below 0
+ * and as width * page_rows above it, keep and add as 0 below 0. n * (width + 1) and width * page_rows below 2^31.
  * ws: at least mq_pages_ws_bytes(pool, max(n, m), width) bytes, for calls that do not run at the same time. Two
  * launches, programmatic dependent ones.
  */
@@ -584,7 +584,8 @@ int mq_pages_next(const mq_pool* pool, const int32_t* table, const int32_t* len,
  *     where[p] = the new number of page p, -1 where no sequence holds it (int32 [n_pages]),
  *     table_out[i][j] = where[table[i][j]] for the entries of rows below len[i] (as they are if they name no page), -1 past them,
  *     live[0] = U.
- * table_out may be table (no other overlap). Other arguments as for mq_pages_next (ws: mq_pages_ws_bytes(pool, n, width)).
+ * table_out may be table; otherwise table_out, where, live and the workspace overlap neither each other nor what is read, and none of
+ * all these the pool's pages (MQ_ERR_SHAPE). Other arguments as for mq_pages_next (ws: mq_pages_ws_bytes(pool, n, width)).
  */
 int mq_pages_compact(const mq_pool* pool, const int32_t* table, const int32_t* len, int n, int width, int32_t* table_out,
                      int32_t* where, int32_t* live, void* ws, size_t ws_bytes, cudaStream_t stream);

@@ -405,9 +405,35 @@ bool valid_table(long long n, long long width, int page_rows) {
     return n >= 0 && width >= 0 && n * (width + 1) <= 0x7fffffffLL && n <= (1 << 28) && width * page_rows <= 0x7fffffffLL;
 }
 
-// b over a, unless it begins where a does (the new table goes through the workspace).
-bool partly(const void* a, long long a_bytes, const void* b, long long b_bytes) {
-    return a != b && mq::rows_meet(a, 1, a_bytes, a_bytes, b, b_bytes);
+// A range of bytes that a call writes or reads.
+struct Bytes {
+    const void* p;
+    long long n;
+    bool meets(const Bytes& b) const { return mq::rows_meet(p, 1, n, n, b.p, b.n); }
+};
+bool meets_pool(const mq_pool* p, const Bytes& b) {
+    if (p->n_pages == 0) return false;
+    const long long step = p->n_pages > 1 ? p->page_stride : p->page_bytes, next = p->layers > 1 ? p->layer_stride : 0;
+    const uint8_t* data = static_cast<const uint8_t*>(p->data);
+    if (!b.meets({data, next * (p->layers - 1) + step * (p->n_pages - 1) + p->page_bytes})) return false;
+    for (int i = 0; i < p->layers; ++i)      // (between pages of one layer may lie other things)
+        if (mq::rows_meet(data + i * next, p->n_pages, step, p->page_bytes, b.p, b.n)) return true;
+    return false;
+}
+// What is written lies apart from all else and from the pool, but that written[i] may be read[i] for the first `in_place` of
+// them (the new tables go through the workspace, a sequence's old length is read before its new one is written).
+template <int W, int R>
+bool apart(const mq_pool* pool, const Bytes (&written)[W], const Bytes (&read)[R], int in_place) {
+    for (int i = 0; i < W; ++i) {
+        if (meets_pool(pool, written[i])) return false;
+        for (int j = 0; j < i; ++j)
+            if (written[i].meets(written[j])) return false;
+        for (int j = 0; j < R; ++j)
+            if (written[i].meets(read[j]) && !(i == j && i < in_place && written[i].p == read[j].p)) return false;
+    }
+    for (const Bytes& b : read)
+        if (meets_pool(pool, b)) return false;
+    return true;
 }
 
 template <typename Args>
@@ -437,8 +463,11 @@ extern "C" int mq_pages_next(const mq_pool* pool, const int32_t* table, const in
     for (const void* p : {(const void*)table, (const void*)len, (const void*)from, (const void*)keep, (const void*)add,
                           (const void*)table_out, (const void*)len_out, (const void*)status, (const void*)ws})
         if (!mq::aligned16(p)) return MQ_ERR_ALIGN;
-    if (ws_bytes < mq_pages_ws_bytes(pool, m, width)) return MQ_ERR_SCRATCH;
-    if (partly(table, 4LL * n * width, table_out, 4LL * m * width) || partly(len, 4LL * n, len_out, 4LL * m)) return MQ_ERR_SHAPE;
+    const long long used = (long long)mq_pages_ws_bytes(pool, m, width);
+    if (ws_bytes < (size_t)used) return MQ_ERR_SCRATCH;
+    const Bytes written[] = {{table_out, 4LL * m * width}, {len_out, 4LL * m}, {status, 12}, {ws, used}};
+    const Bytes read[] = {{table, 4LL * n * width}, {len, 4LL * n}, {from, 4LL * m}, {keep, 4LL * m}, {add, 4LL * m}};
+    if (!apart(pool, written, read, 2)) return MQ_ERR_SHAPE;
     rc = mq::check_arch();
     if (rc != MQ_OK) return rc;
     const Space s = space_of(static_cast<uint8_t*>(ws), m, width, pool->n_pages);
@@ -457,8 +486,11 @@ extern "C" int mq_pages_compact(const mq_pool* pool, const int32_t* table, const
     if (n > 0 && (!len || (width > 0 && (!table || !table_out)))) return MQ_ERR_NULL;
     for (const void* p : {(const void*)table, (const void*)len, (const void*)table_out, (const void*)where, (const void*)live, (const void*)ws})
         if (!mq::aligned16(p)) return MQ_ERR_ALIGN;
-    if (ws_bytes < mq_pages_ws_bytes(pool, n, width)) return MQ_ERR_SCRATCH;
-    if (partly(table, 4LL * n * width, table_out, 4LL * n * width)) return MQ_ERR_SHAPE;
+    const long long used = (long long)mq_pages_ws_bytes(pool, n, width);
+    if (ws_bytes < (size_t)used) return MQ_ERR_SCRATCH;
+    const Bytes written[] = {{table_out, 4LL * n * width}, {where, 4LL * pool->n_pages}, {live, 4}, {ws, used}};
+    const Bytes read[] = {{table, 4LL * n * width}, {len, 4LL * n}};
+    if (!apart(pool, written, read, 1)) return MQ_ERR_SHAPE;
     rc = mq::check_arch();
     if (rc != MQ_OK) return rc;
     const Space s = space_of(static_cast<uint8_t*>(ws), n, width, pool->n_pages);
