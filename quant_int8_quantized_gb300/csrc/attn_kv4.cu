@@ -758,7 +758,7 @@ extern "C" int mq_attn_kv4(const void* q, int type, long long q_stride, int B, i
     if (ws_bytes < c.bytes) return MQ_ERR_SCRATCH;
     const long long rows = (long long)B * T * Hq, out_bytes = rows * D * (out_type == MQ_F32 ? 4 : 2);
     if (mq::rows_meet(q, (long long)B * T, 2 * q_stride, 2LL * Hq * D, out, out_bytes) ||
-        mq::rows_meet(out, 1, out_bytes, out_bytes, cache->pages, cache->page_stride * cache->n_pages))
+        kv4::meets_pages(cache, out, out_bytes))
         return MQ_ERR_SHAPE;   // read by some blocks while others write
     rc = mq::check_arch();
     if (rc != MQ_OK) return rc;

@@ -529,12 +529,12 @@ extern "C" int mq_qk_norm_rope_kv4(const mq_qkv* x, int type, float rot_scale, v
     if (!mq::aligned16(q_out) || !mq::aligned16(x->wq) || !mq::aligned16(x->wk) || !mq::aligned16(x->inv_freq) ||
         !mq::aligned16(x->axis) || !mq::aligned16(x->pos) || !mq::aligned16(seq) || !mq::aligned16(row))
         return MQ_ERR_ALIGN;
-    const long long pool = cached ? cache->page_stride * cache->n_pages : 0, q_bytes = 2LL * x->M * heads[0] * D;
+    const long long q_bytes = 2LL * x->M * heads[0] * D;
     for (int i = 0; i < 3; ++i)   // a block's output rows would lie over what others have yet to read
         if (mq::rows_meet(src[i], x->M, 4 * st[i], 4LL * heads[i] * D, q_out, q_bytes) ||
-            mq::rows_meet(src[i], x->M, 4 * st[i], 4LL * heads[i] * D, cache->pages, pool))
+            (cached && mq::rows_meet(src[i], x->M, 4 * st[i], 4LL * heads[i] * D, cache->pages, pool_span(cache))))
             return MQ_ERR_SHAPE;
-    if (mq::rows_meet(q_out, 1, q_bytes, q_bytes, cache->pages, pool)) return MQ_ERR_SHAPE;
+    if (cached && meets_pages(cache, q_out, q_bytes)) return MQ_ERR_SHAPE;
     rc = mq::check_arch();
     if (rc != MQ_OK) return rc;
     FillArgs a;
@@ -584,9 +584,8 @@ extern "C" int mq_kv4_read(const mq_kv4* src, const int32_t* len, const mq_kv* d
     if (src->n == 0 || src->width == 0 || dst->cap == 0) return MQ_OK;
     if (!len) return MQ_ERR_NULL;
     if (!mq::aligned16(len)) return MQ_ERR_ALIGN;
-    const long long span = 2 * mq::kv_span(dst), pool = src->page_stride * src->n_pages;
-    if (mq::rows_meet(dst->k, 1, span, span, src->pages, pool) || mq::rows_meet(dst->v, 1, span, span, src->pages, pool))
-        return MQ_ERR_SHAPE;
+    const long long span = 2 * mq::kv_span(dst);
+    if (meets_pages(src, dst->k, span) || meets_pages(src, dst->v, span)) return MQ_ERR_SHAPE;
     rc = mq::check_arch();
     if (rc != MQ_OK) return rc;
     return launch_read(src, len, dst, stream);

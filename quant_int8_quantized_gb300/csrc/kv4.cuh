@@ -48,13 +48,20 @@ struct Cache {
 inline bool valid_dim(int D) { return D == 64 || D == 96 || D == 128 || D == 256; }
 inline bool valid_rows(int r) { return r >= 16 && r <= 1024 && (r & (r - 1)) == 0; }
 
+// Bytes of a page that are used; of the pool from its first page to the end of its last.
+inline long long page_used(const mq_kv4* c) { return (long long)c->page_rows / 16 * block_bytes(c->dim) * c->heads; }
+inline long long pool_span(const mq_kv4* c) { return c->n_pages > 0 ? c->page_stride * (c->n_pages - 1) + page_used(c) : 0; }
+// Whether a page and the `bytes` from b on have a byte in common (between pages may lie other things: other layers' pages).
+inline bool meets_pages(const mq_kv4* c, const void* b, long long bytes) {
+    return mq::rows_meet(c->pages, c->n_pages, c->page_stride, page_used(c), b, bytes);
+}
+
 // Sizes, then (with `pointers`) pointers.
 inline int check(const mq_kv4* c, bool pointers) {
     if (!c) return MQ_ERR_NULL;
     if (c->n < 0 || c->width < 0 || c->n_pages < 0 || c->heads < 1 || c->heads > 65535 || !valid_dim(c->dim) || !valid_rows(c->page_rows))
         return MQ_ERR_SHAPE;
-    const long long head = (long long)c->page_rows / 16 * block_bytes(c->dim);
-    if (c->page_stride < head * c->heads || c->page_stride % 16 != 0 || c->page_stride > (1LL << 40)) return MQ_ERR_SHAPE;
+    if (c->page_stride < page_used(c) || c->page_stride % 16 != 0 || c->page_stride > (1LL << 40)) return MQ_ERR_SHAPE;
     if ((long long)c->width * c->page_rows > 0x7fffffffLL - 255) return MQ_ERR_SHAPE;
     if (c->n > 1 && (c->table_stride < c->width || c->table_stride > (1LL << 40))) return MQ_ERR_SHAPE;
     if (pointers && c->n > 0 && c->width > 0) {
