@@ -188,8 +188,26 @@ __global__ void __launch_bounds__(kThreads) fill_kernel(const FillArgs a) {
 #pragma unroll
             for (int o = LG / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
         }
+        if (w && live) mean = ss / (float)D + a.eps;
+        const bool lost = !(mean > 1e-30f && mean < 3e38f);                 // a mean square that 32 bits do not hold
+        if (__any_sync(0xffffffffu, lost)) {                                // taken by a power of two that brings them next to 1
+            float top = sqrtf(a.eps);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[i]));
+#pragma unroll
+            for (int o = LG / 2; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const float by = lost ? __uint_as_float(max(1, 253 - (int)(__float_as_uint(top) >> 23)) << 23) : 1.0f;
+            ss = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                v[i] *= by;
+                ss = fmaf(v[i], v[i], ss);
+            }
+#pragma unroll
+            for (int o = LG / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            if (lost) mean = ss / (float)D + a.eps * by * by;
+        }
         if (w && live) {
-            mean = ss / (float)D + a.eps;
             const float sc = 1.0f / sqrtf(mean);
             if constexpr (VEC) {
                 const float4 w0 = __ldg(reinterpret_cast<const float4*>(w + lo));
@@ -292,7 +310,7 @@ __global__ void __launch_bounds__(kThreads) fill_kernel(const FillArgs a) {
             num[i] = __float_as_uint(m);
         }
         // (a rotated or normed v is off by `off`: what lies next to a border goes to the list, and what 32 bits have no room for)
-        const bool near = !exact && (!(mean > 1e-30f && mean < 3e38f) || !(far < 0.5f - 1e-6f - off * inv) || !(all < 3360.0f - off) ||
+        const bool near = !exact && (lost || !(far < 0.5f - 1e-6f - off * inv) || !(all < 3360.0f - off) ||
                           (most > 0.0f && (7.0f * d < most + off || (code > 0 && 7.0f * scale_of(code - 1) >= most - off))));
         const uint32_t again = __ballot_sync(0xffffffffu, near && live) >> (threadIdx.x & 31 & ~(LG - 1)) &
                                (LG == 32 ? ~0u : (1u << (LG & 31)) - 1);

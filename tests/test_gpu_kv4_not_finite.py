@@ -1,8 +1,10 @@
-"""Keys and values that are not finite, written to 4-bit caches: every byte (tests/test_gpu_kv4.py's plain form)."""
+"""Numbers at the ends of what 32 bits hold, and past them: keys and values that are not finite, written to 4-bit caches, byte for byte;
+norms of queries of any size."""
 import pytest
 import torch
 
 from quant_int8_quantized_gb300 import mq
+from tests import _attn_ref as A
 from tests import _kv4_ref as R
 from tests._gpu_util import require_gpu
 from tests.test_gpu_kv4 import _fill_case, _rand, _rope64
@@ -77,3 +79,27 @@ def test_nan_bits():
             bits[m, 0, (7 * m) % D] = (0x7f800001 + 131 * m) if m % 2 else -1 - 4097 * m
     got, want = _pages(k, v, D)
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("D,inter,n_pairs", [(64, False, 32), (128, False, 64), (128, True, 30), (96, False, 11), (256, True, 128)])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("eps", [1e-6, 0.0, 1e-33])
+def test_queries_normed_of_any_size(D, inter, n_pairs, dtype, eps):
+    """Queries whose mean square 32 bits do not hold, among ones whose it is, keys between them in a warp; an infinity and a NaN make no
+    number of their own head alone."""
+    M, Hq, Hkv = 26, 5, 2
+    size = (10.0 ** torch.linspace(-37, 38, M, device="cuda", dtype=torch.float64))[:, None, None]
+    q, k = ((_rand((M, h, D), 41 + h).double().clamp(-3.0, 3.0) * size.roll(h, 0)).float() for h in (Hq, Hkv))
+    q[1, 2], q[2, 3, 7], q[3, 0, 1] = 1.0, INF, NAN
+    wq = _rand((D,), 44, 0.1) + 1
+    cache, row = mq.KV4.empty(1, 2, 2, Hkv, D, 16), torch.arange(M, dtype=torch.int32, device="cuda")
+    cache.table.copy_(torch.tensor([[0, 1]]))
+    out, pos, freq = torch.zeros((M, Hq, D), dtype=dtype, device="cuda"), row + 5, mq.rope_freq(n_pairs, device="cuda")
+    mq.mq_qk_norm_rope_kv4(q, k, None, out, cache, None, row, pos, freq, wq=wq, wk=wq, eps=eps, interleaved=inter)
+    want = _rope64(q, wq, float(torch.tensor(eps)), pos[None], freq, None, 1, inter, 1.0)
+    bad = torch.isnan(want)
+    assert bad[2, 3].any() and torch.equal(torch.isnan(out), bad)
+    # as tests/test_gpu_kv4.py counts: 2^-20 of the pair's size for 32 bits, and the rounding to 16
+    got, want = out.double().nan_to_num(0.0), want.nan_to_num(0.0)
+    size_q = want.abs().amax(-1, keepdim=True) * 2 ** 0.5 + want.abs()
+    assert bool(((got - want).abs() <= A.U[dtype] * want.abs() * 1.01 + 2.0 ** -20 * size_q + A.TINY[dtype]).all())
