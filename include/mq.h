@@ -526,9 +526,8 @@ int mq_kv4_read(const mq_kv4* src, const int32_t* len, const mq_kv* dst, cudaStr
  * q: [B * T][Hq][D] in `type` (MQ_F16, MQ_BF16), row stride q_stride (a multiple of 8, at least Hq * D); cache->n == B; len: int32 [B] on
  * the device, taken as 0 below 0 and as width * page_rows above it; out: [B * T][Hq][D] in `type` or MQ_F32; lse: f32 [B * T][Hq] or
  * NULL. Rows at or past len are never used, whatever they hold. A query that sees no key gives zeros and an lse of -infinity.
- * Arithmetic: keys and values are exact in 16 bits, products and softmax f32, probabilities rounded to 16 bits for the product with
- * the values: by at most 2^-11 (MQ_F16) or 2^-8 (MQ_BF16) of themselves, or 2^-32 of their row's largest where that is more.
- * Deterministic.
+ * Arithmetic: keys and values are exact in 16 bits, products and softmax f32, probabilities rounded to f16 for the product with
+ * the values, whatever the type: by at most 2^-11 of themselves, or 2^-32 of their row's largest where that is more. Deterministic.
  * out overlaps neither q nor the pages. ws: at least mq_attn_kv4_ws_bytes(B, T, Hq, Hkv, D, width * page_rows) bytes, 16-byte
  * aligned, nothing kept in it between calls; calls that run at the same time need one each. Where many query rows share a key head
  * (dim 64 and 128) it holds rows in 16 bits: up to 1 GB, or one sequence's width * page_rows rows where that is more, and the call takes the

@@ -325,14 +325,14 @@ struct Cut {
     size_t few_o, few_ml, few_info, many_o, many_ml, many_info, split, lse2, raw, bytes;
 };
 
-Cut cut_of(int B, int T, int Hq, int Hkv, int D, int prefix_keys, int own_cap, bool scores) {
+Cut cut_of(int B, int T, int Hq, int Hkv, int D, int prefix_keys, int own_cap, bool scores, bool part) {
     Cut c;
     const int group = Hq / Hkv;
     // bytes that the kernel for few rows would read; the weights' raw products come from it
     const long long row_tiles = ceil_div((long long)T * group, kFewRows), key_bytes = 4LL * Hkv * D;
     const long long own_rows = (long long)T * group, prefix_rows = B * own_rows;
-    c.own_many = own_cap > 0 && many_takes(D, group) && !scores && own_rows >= kManyFrom &&
-                 B * row_tiles * own_cap * key_bytes > kFewBytes;
+    c.own_many = own_cap > 0 && many_takes(D, group) && !scores &&
+                 (part || (own_rows >= kManyFrom && B * row_tiles * own_cap * key_bytes > kFewBytes));
     c.prefix_many = prefix_keys > 0 && !c.own_many && many_takes(D, group) && prefix_rows >= kManyFrom &&
                     ceil_div(prefix_rows, kFewRows) * prefix_keys * key_bytes > kFewBytes;
     c.fits = true;
@@ -453,11 +453,17 @@ extern "C" size_t mq_attn_ws_bytes(int B, int T, int Hq, int Hkv, int D, int pre
     if (B <= 0 || T <= 0 || prefix_cap < 0 || own_cap < 0 || !valid_heads(Hq, Hkv, D) ||
         !valid_counts(B, T, Hq, prefix_cap, own_cap))
         return 0;
-    const Cut c = cut_of(B, T, Hq, Hkv, D, prefix_cap, own_cap, scores != 0);
+    const Cut c = cut_of(B, T, Hq, Hkv, D, prefix_cap, own_cap, scores != 0, false);
     return valid_cut(c, B, Hkv, scores && own_cap > 0) ? c.bytes : 0;
 }
 
 namespace attn {
+
+size_t part_ws_bytes(int B, int T, int Hq, int Hkv, int D, int cap) {
+    if (!valid_counts(B, T, Hq, 0, cap)) return 0;
+    const Cut c = cut_of(B, T, Hq, Hkv, D, 0, cap, false, true);
+    return valid_cut(c, B, Hkv, false) ? c.bytes : 0;
+}
 
 int call(const void* q, long long q_stride, int B, int T, int Hq, const mq_kv* prefix, const mq_kv* own, const int32_t* own_len,
          float scale, void* out, int out_type, float* lse, const float* score, float* score_out, void* ws, size_t ws_bytes,
@@ -484,7 +490,7 @@ int call(const void* q, long long q_stride, int B, int T, int Hq, const mq_kv* p
         (!part && (!mq::aligned16(own_len) || !mq::aligned16(lse))))
         return MQ_ERR_ALIGN;
     const bool scores = score_out && cap > 0;
-    Cut c = cut_of(B, T, Hq, Hkv, D, P, cap, scores);
+    Cut c = cut_of(B, T, Hq, Hkv, D, P, cap, scores, part);
     if (!valid_cut(c, B, Hkv, scores)) return MQ_ERR_SHAPE;
     if (ws_bytes < c.bytes) return MQ_ERR_SCRATCH;
     const long long all_rows = (long long)B * T * Hq, score_bytes = scores ? 4LL * B * Hkv * cap : 0;
@@ -517,7 +523,7 @@ int call(const void* q, long long q_stride, int B, int T, int Hq, const mq_kv* p
         m.out = many;
         m.split = c.own_many ? reinterpret_cast<int4*>(base + c.split) : nullptr;
         m.fin = fin;
-        rc = launch_many(m, P > 0 ? prefix : nullptr, c.own_many ? own : nullptr, D, type, stream);
+        rc = launch_many(m, P > 0 ? prefix : nullptr, c.own_many ? own : nullptr, D, type, part ? MQ_F16 : type, stream);
         if (rc != MQ_OK) return rc;
         if (c.own_many) {
             const SplitArgs s = {{many, c.many.rows, c.many}, m.split, c.many, fin};

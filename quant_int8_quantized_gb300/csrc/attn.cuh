@@ -294,7 +294,9 @@ struct JoinArgs {
 // The rows' pieces added up, rows written (attn.cu).
 int launch_join(const JoinArgs& j, int D, int out_type, cudaStream_t stream);
 
-// mq_attn_prefix. part: of a batch, so own_len and lse may begin at any sequence's.
+// mq_attn_prefix. part: of a batch, so own_len and lse may begin at any sequence's; its own rows are those of a 4-bit cache: values in
+// f16 whatever the type, which has more bits for the weights, and the tensor-core kernel, however few the rows. Workspace: part_ws_bytes.
+size_t part_ws_bytes(int B, int T, int Hq, int Hkv, int D, int cap);
 int call(const void* q, long long q_stride, int B, int T, int Hq, const mq_kv* prefix, const mq_kv* own, const int32_t* own_len,
          float scale, void* out, int out_type, float* lse, const float* score, float* score_out, void* ws, size_t ws_bytes,
          cudaStream_t stream, bool part);

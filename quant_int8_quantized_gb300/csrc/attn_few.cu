@@ -369,8 +369,8 @@ int launch_few(const FewArgs& a, const mq_kv* prefix, const mq_kv* own, int D, i
     const mq_kv* p = prefix ? prefix : own;   // a part that is not there is never read
     const mq_kv* o = own ? own : prefix;
     const int dims = D % 64 == 0 ? 64 : 32;
-    if (!kv_map(&pk, p, p->k, dims, kKeys) || !kv_map(&pv, p, p->v, dims, kKeys) || !kv_map(&ok, o, o->k, dims, kKeys) ||
-        !kv_map(&ov, o, o->v, dims, kKeys))
+    if (!kv_map(&pk, p, p->k, type, dims, kKeys) || !kv_map(&pv, p, p->v, type, dims, kKeys) || !kv_map(&ok, o, o->k, type, dims, kKeys) ||
+        !kv_map(&ov, o, o->v, type, dims, kKeys))
         return MQ_ERR_LAUNCH;
     return with_kernel(D, type, a.raw != nullptr, [&](auto kern, int smem) {
         if (!mq::allow_smem(reinterpret_cast<const void*>(kern), smem)) return (int)MQ_ERR_LAUNCH;

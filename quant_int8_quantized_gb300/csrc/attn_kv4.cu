@@ -15,7 +15,7 @@
 // Measured: 64 sequences of 9000 to 20000 rows, 40 query and 8 key heads of 128 (1 GB), 191 us, 5.3 TB/s (its copies alone 157 to 166, all
 // but them 164); one of 1000 rows, 9 us with the join, which is latency.
 // Many rows (a prompt): the rows in use are read once into 16 bits in the workspace and mq_attn_prefix's tensor-core kernel
-// takes them from there; n d being exact, both ways compute the same products.
+// takes them from there; n d being exact, both ways compute the same products, and both hold values and weights in f16.
 
 #include <cmath>
 #include <type_traits>
@@ -662,10 +662,10 @@ Kv4Cut cut_kv4(int B, int T, int Hq, int Hkv, int D, int cap) {
     c.read = cap > 0 && many_takes(D, group) && worth_reading(B, c.at_once, rows, Hkv, D, cap, c.nt);
     if (c.read) {
         c.kv = up16((size_t)one * c.at_once);
-        size_t ws = mq_attn_ws_bytes(c.at_once, T, Hq, Hkv, D, 0, cap, 0);
+        size_t ws = part_ws_bytes(c.at_once, T, Hq, Hkv, D, cap);
         c.fits = ws > 0;
         if (B % c.at_once) {
-            const size_t rest = mq_attn_ws_bytes(B % c.at_once, T, Hq, Hkv, D, 0, cap, 0);
+            const size_t rest = part_ws_bytes(B % c.at_once, T, Hq, Hkv, D, cap);
             if (rest > ws) ws = rest;
         }
         c.bytes = 2 * c.kv + ws;
@@ -770,7 +770,7 @@ extern "C" int mq_attn_kv4(const void* q, int type, long long q_stride, int B, i
             part.n = n;
             part.table += b * cache->table_stride;
             const mq_kv kv = {base, base + c.kv, (long long)cap * Hkv * D, (long long)Hkv * D, D, type, n, cap, Hkv, D};
-            rc = kv4::launch_read(&part, len + b, &kv, stream);
+            rc = kv4::launch_read(&part, len + b, &kv, MQ_F16, stream);
             if (rc != MQ_OK) return rc;
             const long long at = (long long)b * T;
             rc = call(static_cast<const uint16_t*>(q) + at * q_stride, q_stride, n, T, Hq, nullptr, &kv, len + b, scale,

@@ -167,7 +167,8 @@ struct Reader {
     }
 };
 
-template <typename T, int D>
+// T: of queries and keys (and of narrow outputs). V: of values, and of the weights for the product with them.
+template <typename T, typename V, int D>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_many_kernel(const ManyArgs a, const __grid_constant__ CUtensorMap qm, const __grid_constant__ CUtensorMap pk,
                      const __grid_constant__ CUtensorMap pv, const __grid_constant__ CUtensorMap ok,
@@ -281,12 +282,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // (lanes past the rows hold anything)
                 if (__any_sync(0xffffffffu, lane < n_rows && mx > limit)) {   // the first key that a row sees, among others
                     // a row's own matter: what its neighbours do must not show in it
-                    const bool grew = j == j0 || (lane < n_rows && mx - m > kGrow + kUp<T>);
+                    const bool grew = j == j0 || (lane < n_rows && mx - m > kGrow + kUp<V>);
                     if (__any_sync(0xffffffffu, grew)) {
-                        const float now = grew ? reference<kUp<T>>(mx) : m;
+                        const float now = grew ? reference<kUp<V>>(mx) : m;
                         const float f = now == -INFINITY ? 1.0f : exp2_fast(m - now);
                         m = now;
-                        limit = is_large(m) ? -INFINITY : m + (kGrow + kUp<T>);
+                        limit = is_large(m) ? -INFINITY : m + (kGrow + kUp<V>);
                         l *= f;
                         if (j > j0) {
                             // the product before this one must be done with O
@@ -320,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 x[i] = __float_as_uint(e);
                             }
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) pr[i] = mq_pack2<T>(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+                            for (int i = 0; i < 16; ++i) pr[i] = mq_pack2<V>(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
                             tc::tmem_st16(s_col + k * 16, pr);
                         }
                     }
@@ -336,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                     f2_dup(a.scale_log2), f2_dup(-base));
                             const float2 e = make_float2(exp2_fast(x.x), exp2_fast(x.y));
                             sum[i & 1] = f2_add(sum[i & 1], e);
-                            pr[i] = mq_pack2<T>(e.x, e.y);
+                            pr[i] = mq_pack2<V>(e.x, e.y);
                         }
                         tc::tmem_st16(s_col + k * 16, pr);
                     }
@@ -514,9 +515,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (wid < 11) {
             // ------------------------------------------------------------ products of half h
             const int h = wid - 9;
-            constexpr uint32_t fmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+            constexpr uint32_t fmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u, v_fmt = std::is_same<V, __nv_bfloat16>::value ? 1u : 0u;
             const uint32_t idesc_qk = tc::instr_desc(kHalf, kKeys, fmt) | (a.negative ? 1u << 13 : 0u);
-            const uint32_t idesc_pv = tc::instr_desc(kHalf, D, fmt) | 1u << 16;   // V: the N axis contiguous
+            const uint32_t idesc_pv = tc::instr_desc(kHalf, D, v_fmt) | 1u << 16;   // V: the N axis contiguous
             constexpr uint32_t kTileLow = C::kTileBytes >> 4;
             const uint32_t ring = tc::smem_u32(s_ring);
             const uint32_t s_tm = uniform(tmem + h * 128), o_tm = uniform(tmem + 256 + h * 128);
@@ -687,24 +688,27 @@ bool regs_as_planned(const void* kern) {
 
 }  // namespace
 
-int launch_many(const ManyArgs& a, const mq_kv* prefix, const mq_kv* own, int D, int type, cudaStream_t stream) {
+int launch_many(const ManyArgs& a, const mq_kv* prefix, const mq_kv* own, int D, int type, int v_type, cudaStream_t stream) {
     CUtensorMap qm, pk, pv, ok, ov;
     const mq_kv* p = prefix ? prefix : own;   // a part that is not there is never read
     const mq_kv* o = own ? own : prefix;
     if (!q_map(&qm, a.q, a.q_stride, (long long)a.plan.B * a.plan.T, a.plan.Hq, D, type, a.plan.group,
                a.plan.rows / a.plan.group) ||
-        !kv_map(&pk, p, p->k, 64, kManyKeys) || !kv_map(&pv, p, p->v, 64, kManyKeys) ||
-        !kv_map(&ok, o, o->k, 64, kManyKeys) || !kv_map(&ov, o, o->v, 64, kManyKeys))
+        !kv_map(&pk, p, p->k, type, 64, kManyKeys) || !kv_map(&pv, p, p->v, v_type, 64, kManyKeys) ||
+        !kv_map(&ok, o, o->k, type, 64, kManyKeys) || !kv_map(&ov, o, o->v, v_type, 64, kManyKeys))
         return MQ_ERR_LAUNCH;
     auto go = [&](auto kern, int smem) {
         if (!regs_as_planned(reinterpret_cast<const void*>(kern))) return (int)MQ_ERR_LAUNCH;
         if (!mq::allow_smem(reinterpret_cast<const void*>(kern), smem)) return (int)MQ_ERR_LAUNCH;
         return mq::launch_pdl(kern, dim3(a.plan.G), dim3(kThreads), smem, stream, a, qm, pk, pv, ok, ov);
     };
-    if (type == MQ_F16)
-        return D == 64 ? go(attn_many_kernel<__half, 64>, Cfg<64>::kSmem) : go(attn_many_kernel<__half, 128>, Cfg<128>::kSmem);
-    return D == 64 ? go(attn_many_kernel<__nv_bfloat16, 64>, Cfg<64>::kSmem)
-                   : go(attn_many_kernel<__nv_bfloat16, 128>, Cfg<128>::kSmem);
+    auto of = [&](auto t, auto v) {
+        using T = decltype(t);
+        using V = decltype(v);
+        return D == 64 ? go(attn_many_kernel<T, V, 64>, Cfg<64>::kSmem) : go(attn_many_kernel<T, V, 128>, Cfg<128>::kSmem);
+    };
+    if (type == MQ_F16) return of(__half(), __half());
+    return v_type == MQ_F16 ? of(__nv_bfloat16(), __half()) : of(__nv_bfloat16(), __nv_bfloat16());
 }
 
 }  // namespace attn

@@ -32,6 +32,7 @@ constexpr int kManyCost = 2, kManyWide = 3, kManyExtra = 7;
 inline int many_rows(int group) { return kManyRows / group * group; }
 
 inline bool many_takes(int D, int group) { return (D == 64 || D == 128) && group <= kManyRows; }
-int launch_many(const ManyArgs& a, const mq_kv* prefix, const mq_kv* own, int D, int type, cudaStream_t stream);
+// v_type: of the values, `type` or MQ_F16.
+int launch_many(const ManyArgs& a, const mq_kv* prefix, const mq_kv* own, int D, int type, int v_type, cudaStream_t stream);
 
 }  // namespace attn

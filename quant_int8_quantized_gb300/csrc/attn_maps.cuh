@@ -13,7 +13,7 @@ constexpr long long kStrideMost = (1LL << 39) - 8;
 
 // [n][cap][heads][dim] of k or v (`base`) as (dim, head, row, sequence): boxes of `dims` (64: 128-byte swizzle,
 // 32: 64-byte swizzle) by `rows` rows of one head; rows past the cap read as zeros.
-bool kv_map(CUtensorMap* map, const mq_kv* c, const void* base, int dims, int rows);
+bool kv_map(CUtensorMap* map, const mq_kv* c, const void* base, int type, int dims, int rows);
 
 // The queries [B T][Hq][D] as (dim, head, query): a box is 64 dims of `group` heads of `queries` queries.
 bool q_map(CUtensorMap* map, const void* q, long long q_stride, long long queries, int Hq, int D, int type, int group,

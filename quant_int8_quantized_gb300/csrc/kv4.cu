@@ -419,7 +419,7 @@ constexpr int kChunk = 2, kReadWarps = 4;
 
 // A warp takes 32 rows of a head, 16 at a time: the words that a lane loads are those that the products' operands are
 // made of, so eight lanes' stores fill a row's 64 bytes.
-template <typename T, int D>
+template <typename T, typename V, int D>
 __global__ void __launch_bounds__(32 * kReadWarps) read_kernel(const ReadArgs a) {
     constexpr int nb = D / 32;
     mq_grid_release();
@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(32 * kReadWarps) read_kernel(const ReadArgs a)
         const int chunk = (int)(unit - sh * a.chunks), seq = (int)(sh / a.c.heads), h = (int)(sh - (long long)seq * a.c.heads);
         const int len = min(max(__ldca(a.len + seq), 0), a.cap);
         T* k_to = reinterpret_cast<T*>(a.k) + seq * a.seq_stride + h * a.head_stride;
-        T* v_to = reinterpret_cast<T*>(a.v) + seq * a.seq_stride + h * a.head_stride;
+        V* v_to = reinterpret_cast<V*>(a.v) + seq * a.seq_stride + h * a.head_stride;
 #pragma unroll 1
         for (int i = 0; i < kChunk; ++i) {
             const int row0 = (chunk * kChunk + i) * kBlockRows;
@@ -470,8 +470,8 @@ __global__ void __launch_bounds__(32 * kReadWarps) read_kernel(const ReadArgs a)
                     numbers(kw[p][b], Scale<T>::of(twice(ks[p], b)), x);
                     if (kr < len)
                         *reinterpret_cast<uint4*>(k_to + kr * a.row_stride + 32 * b + 8 * t) = make_uint4(x[0], x[1], x[2], x[3]);
-                    numbers(vw[p][b], Scale<T>::of(both(vs[p], b)), x);
-                    T* to = v_to + vr * a.row_stride + 32 * b + 4 * g;
+                    numbers(vw[p][b], Scale<V>::of(both(vs[p], b)), x);
+                    V* to = v_to + vr * a.row_stride + 32 * b + 4 * g;
                     if (vr < len)
                         *reinterpret_cast<uint2*>(to) = make_uint2(__byte_perm(x[0], x[1], 0x5410), __byte_perm(x[2], x[3], 0x5410));
                     if (vr + 1 < len)
@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(32 * kReadWarps) read_kernel(const ReadArgs a)
 
 }  // namespace
 
-int launch_read(const mq_kv4* src, const int32_t* len, const mq_kv* dst, cudaStream_t stream) {
+int launch_read(const mq_kv4* src, const int32_t* len, const mq_kv* dst, int v_type, cudaStream_t stream) {
     ReadArgs a;
     a.c = cache_of(src);
     a.len = len;
@@ -501,13 +501,15 @@ int launch_read(const mq_kv4* src, const int32_t* len, const mq_kv* dst, cudaStr
     if (a.units == 0) return MQ_OK;
     const long long blocks = (a.units + kReadWarps - 1) / kReadWarps, most = 16LL * mq::num_sms();
     const dim3 grid((unsigned)(blocks < most ? blocks : most));
-    auto go = [&](auto t) {
+    auto go = [&](auto t, auto v) {
         using T = decltype(t);
-        auto kern = src->dim == 64 ? read_kernel<T, 64> : src->dim == 96 ? read_kernel<T, 96>
-                    : src->dim == 128 ? read_kernel<T, 128> : read_kernel<T, 256>;
+        using V = decltype(v);
+        auto kern = src->dim == 64 ? read_kernel<T, V, 64> : src->dim == 96 ? read_kernel<T, V, 96>
+                    : src->dim == 128 ? read_kernel<T, V, 128> : read_kernel<T, V, 256>;
         return mq::launch_pdl(kern, grid, dim3(32 * kReadWarps), 0, stream, a);
     };
-    return dst->type == MQ_F16 ? go(__half()) : go(__nv_bfloat16());
+    if (dst->type == MQ_F16) return go(__half(), __half());
+    return v_type == MQ_F16 ? go(__nv_bfloat16(), __half()) : go(__nv_bfloat16(), __nv_bfloat16());
 }
 
 }  // namespace kv4
@@ -606,5 +608,5 @@ extern "C" int mq_kv4_read(const mq_kv4* src, const int32_t* len, const mq_kv* d
     if (meets_pages(src, dst->k, span) || meets_pages(src, dst->v, span)) return MQ_ERR_SHAPE;
     rc = mq::check_arch();
     if (rc != MQ_OK) return rc;
-    return launch_read(src, len, dst, stream);
+    return launch_read(src, len, dst, dst->type, stream);
 }

@@ -4,7 +4,8 @@
 #include "mq_internal.cuh"
 
 namespace kv4 {
-int launch_read(const mq_kv4* src, const int32_t* len, const mq_kv* dst, cudaStream_t stream);   // mq_kv4_read, checked
+// mq_kv4_read, checked; values in v_type (dst's type or MQ_F16)
+int launch_read(const mq_kv4* src, const int32_t* len, const mq_kv* dst, int v_type, cudaStream_t stream);
 }  // namespace kv4
 
 namespace attn {
