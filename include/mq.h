@@ -429,8 +429,9 @@ int mq_qk_norm_rope(const mq_qkv* x, void* q_out, const mq_kv* cache, const int3
  * infinities or NaN also reaches the queries of its sequence that come before it.
  * Arithmetic: products in f32 from 16-bit operands, softmax in f32, probabilities rounded to
  * the caches' type for the product with the values, sums in f32. That rounding moves a weight by at most 2^-11 (MQ_F16) or
- * 2^-8 (MQ_BF16) of itself, or, in f16, 2^-32 of its row's largest where that is more; so an output moves by as much of
- * sum p_j |v_j| (plus 2^-32 of the largest p times sum |v_j|) at most, and an MQ_F32 output too. Deterministic.
+ * 2^-8 (MQ_BF16) of itself, or, in f16, 2^-32 of its row's largest where that is more (2^-25 where the
+ * row's largest product scale * q . k_j / ln 2 is 2^20 or more in magnitude); so an output moves by as much of
+ * sum p_j |v_j| (plus 2^-32 or 2^-25 of the largest p times sum |v_j|) at most, and an MQ_F32 output too. Deterministic.
  * D: 64, 96, 128 or 256; Hq a multiple of Hkv; at most 2^30 - 1 rows (B * T * Hq), 2^31 - 256 keys in a cache, and
  * some 2^31 tiles of 16 rows of a key head by 16 keys (256 by 128 where the call has that many rows) in all, else MQ_ERR_SHAPE
  * (mq_attn_ws_bytes gives 0 for such sizes), as for strides of 2^39 elements and more between rows. scale must be finite. ws: caller-owned device
@@ -527,7 +528,9 @@ int mq_kv4_read(const mq_kv4* src, const int32_t* len, const mq_kv* dst, cudaStr
  * the device, taken as 0 below 0 and as width * page_rows above it; out: [B * T][Hq][D] in `type` or MQ_F32; lse: f32 [B * T][Hq] or
  * NULL. Rows at or past len are never used, whatever they hold. A query that sees no key gives zeros and an lse of -infinity.
  * Arithmetic: keys and values are exact in 16 bits, products and softmax f32, probabilities rounded to f16 for the product with
- * the values, whatever the type: by at most 2^-11 of themselves, or 2^-32 of their row's largest where that is more. Deterministic.
+ * the values, whatever the type: by at most 2^-11 of themselves, or 2^-32 of their row's largest where that is more (2^-25 where the
+ * row's largest product scale * q . k_j / ln 2 is 2^20 or more in magnitude: products of that size are themselves off by 2^-4 and
+ * more). Deterministic.
  * out overlaps neither q nor the pages. ws: at least mq_attn_kv4_ws_bytes(B, T, Hq, Hkv, D, width * page_rows) bytes, 16-byte
  * aligned, nothing kept in it between calls; calls that run at the same time need one each. Where many query rows share a key head
  * (dim 64 and 128) it holds rows in 16 bits: up to 1 GB, or one sequence's width * page_rows rows where that is more, and the call takes the

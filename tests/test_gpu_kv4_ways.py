@@ -118,3 +118,41 @@ def test_blocks_finish_their_segments(n, T, Hq, Hkv, D, rows, dtype, out_dtype, 
     floor = 2.0 ** -32 * (v.abs() * used[..., None, None]).sum(1).repeat_interleave(Hq // Hkv, 1)[:, None]
     _inside(out.t[some], want[0], bound[0] + floor, "out")
     _inside(lse.t[some], want[1], bound[1], "lse")
+
+
+def _light_key(heavy, T, dtype, cap=64, scale=0.69314718):
+    """T queries whose products (base 2) are `heavy` with all keys but one, whose is less by 28; in dim 0 that key alone has a value.
+    All products are whole numbers that 32 bits hold, and scale / ln 2 is 1. (output of dim 0, its value at that key, heavy keys)"""
+    D, n = 64, cap - T + 1
+    kn, vn = torch.zeros((1, cap, 1, D)), torch.zeros((1, cap, 1, D))
+    kc, vc = torch.zeros((1, cap, 1, 2)), torch.zeros((1, cap, 1, 2))
+    one, big = R.SCALES.index(1.0), R.SCALES.index(256.0)
+    kn[..., 0], kc[..., 0], kc[..., 1], vc[...] = 4, big, one, one
+    kn[0, 5, 0, 32], vn[0, 5, 0, 0], vn[..., 32:] = -7, 7, 3
+    cache = mq.KV4(R.pack((kn, kc), (vn, vc)).cuda(), torch.zeros((1, 1), dtype=torch.int32, device="cuda"), cap, 1, D)
+    q = torch.zeros((1, T, 1, D), dtype=dtype, device="cuda")
+    q[..., 0], q[..., 32] = heavy / 1024, 4.0
+    assert float(torch.tensor(scale) * torch.tensor(1.4426950408889634)) == 1.0
+    out = torch.full((1, T, 1, D), float("nan"), device="cuda")
+    mq.mq_attn_kv4(q, cache, torch.tensor([cap], dtype=torch.int32, device="cuda"), out, scale=float(torch.tensor(scale)))
+    return out[0, 0, 0, 0].item(), 7.0, n - 1
+
+
+@pytest.mark.parametrize("T", [1, 5])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("read", [False, True])
+@pytest.mark.parametrize("heavy", [2 ** 12, 2 ** 18, -2 ** 18, 2 ** 21, -2 ** 22])
+def test_how_light_a_weight_may_be(heavy, T, dtype, read):
+    """A weight of 2^-28 of the row's largest is there, within 2^-11 of itself and 2^-32 of the largest; where products reach 2^20
+    (base 2) it may be off by 2^-25 of the largest, as include/mq.h says."""
+    own = mq.lib()
+    try:
+        if read:
+            mq._lib = mq._load(B.build_variant("kv4_read", ["MQ_KV4_READ_FROM=1", "MQ_KV4_READ_BYTES=700000"]))
+        got, v, n = _light_key(heavy, T, dtype)
+        torch.cuda.synchronize()
+    finally:
+        mq._lib = own
+    p = 1.0 / (n + 2.0 ** -28)                         # of a heavy key
+    floor = 2.0 ** -25 if abs(heavy) >= 2 ** 20 else 2.0 ** -32
+    assert abs(got - 2.0 ** -28 * p * v) <= v * p * (max(2.0 ** -11 * 2.0 ** -28, floor) + 2.0 ** -28 * 2.0 ** -16)
