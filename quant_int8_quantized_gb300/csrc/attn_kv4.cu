@@ -1,9 +1,10 @@
 // Attention over a 4-bit cache on pages (kv4.cuh).
 //
 // Few query rows per key head (a decode step, drafted tokens): a block is one warp with a run of its own of the row of key
-// tiles (attn.cuh), as in attn_few.cu. A tile is 32 keys of a head, one contiguous copy of 17 D bytes (two where pages have
-// 16 rows) into a ring of stages. HBM would give an SM some 23 bytes a clock, 43 numbers, and a warp's instruction serves
-// 32 lanes: what bounds is the number of instructions per number, so everything is laid out to spend few on it.
+// tiles (attn.cuh), as in attn_few.cu. A tile is 32 or 64 keys of a head (keys_of), one contiguous copy of 17 D bytes for each 16 of
+// them, or a copy a page where pages are smaller than that, into a ring of stages. HBM would give an SM some 23 bytes a clock, 43
+// numbers, and a warp's instruction serves 32 lanes: what bounds is the number of instructions per number, so everything is laid out
+// to spend few on it.
 //  - Keys and values are the left operands (16 x 16) of the warp-wide products, the queries the right ones (16 x 8): eight
 //    rows' products cost what sixteen would the other way round, and the numbers become operands once for all rows.
 //  - A lane's operands are consecutive bytes of the page (kv4.cuh): 16-byte loads without conflicts, then one or two
@@ -46,7 +47,8 @@ struct Shape {
     static constexpr int kRing = kStages * kStage;
     static constexpr int kScales = kStep / 2 * (D / 32) * 16;        // a step's
     // more than eight rows: their operands (D / 8 registers of a lane for each eight) lie in shared memory, where the lane alone
-    // reads them (24 rows: 46 us for 40 with them in registers, which spilled)
+    // reads them (24 rows: 46 us for 40 with them in registers, which spilled more). -Xptxas -v still shows spills, bytes stored / loaded:
+    // 128 dims, 25 to 32 rows 364 / 292 (bf16 260 / 196); 256 dims, 9 to 16 rows 172 / 156 (132 / 112); 96 dims, 9 to 16 rows 48 / 52
     static constexpr bool kQueries = NT > 1;
     static constexpr int kSmem = kRing + kScales + (kQueries ? NT * (D / 32) * 512 : 0);
     // warps an SM, as registers allow (the outputs alone are D NT / 4 of a lane's); the same number on each of its four parts: 14
@@ -117,17 +119,7 @@ __device__ __forceinline__ void bulk_load(uint32_t to, const void* from, uint32_
                  : "memory");
 }
 
-// n words to shared memory, aligned as far as n allows.
-template <int n>
-__device__ __forceinline__ void put(uint32_t* to, const uint32_t (&x)[n]) {
-    if constexpr (n % 4 == 0) {
-#pragma unroll
-        for (int i = 0; i < n / 4; ++i) reinterpret_cast<uint4*>(to)[i] = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-    } else {
-        static_assert(n == 2, "pairs and fours");
-        *reinterpret_cast<uint2*>(to) = make_uint2(x[0], x[1]);
-    }
-}
+__device__ __forceinline__ void put(uint32_t* to, const uint32_t (&x)[4]) { *reinterpret_cast<uint4*>(to) = make_uint4(x[0], x[1], x[2], x[3]); }
 
 constexpr float kNone = -INFINITY;
 // Weights are rounded to f16 and reach 2^15: the reference lies 2^7 below a maximum, which may grow by 2^8.
@@ -366,14 +358,14 @@ __global__ void __launch_bounds__(32, Shape<D, NT>::kPerSm) attn_kv4_kernel(cons
                         for (int i = 0; i < nb / 2; ++i) {
                             uint32_t y[KW];
                             Factor::of(kv4::both(vc, i)).to(y);
-                            put<KW>(s_value + (((lane & 1) * (nb / 2) + i) * 16 + pair) * KW, y);
+                            put(s_value + (((lane & 1) * (nb / 2) + i) * 16 + pair) * KW, y);
                         }
                     } else {
                         const uint8_t* q = st + (lane >> 4) * kBlock + kv4::value_scale_at(D) + (pair & 7) * 2 * nb;
                         for (int b = lane & 1; b < nb; b += 2) {
                             uint32_t y[KW];
                             Factor::of((q[2 * b] & keep & 255) << 8 | (q[2 * b + 1] & keep >> 8 & 255) << 24).to(y);
-                            put<KW>(s_value + (b * 16 + pair) * KW, y);
+                            put(s_value + (b * 16 + pair) * KW, y);
                         }
                     }
                     __syncwarp();

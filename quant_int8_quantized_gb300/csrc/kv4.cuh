@@ -119,14 +119,11 @@ struct Scale<__half> {
 };
 template <>
 struct Scale<__nv_bfloat16> {
-    static constexpr int kWords = 2;
     __nv_bfloat162 mul, off;
     __device__ __forceinline__ static Scale of(uint32_t high_bytes) {
         const __nv_bfloat162 d = __hmul2(as_bf162(high_bytes >> 4), __float2bfloat162_rn(5.192296858534828e33f));
         return {d, __hmul2(d, __float2bfloat162_rn(-136.0f))};
     }
-    __device__ __forceinline__ static Scale from(const uint32_t* w) { return {as_bf162(w[0]), as_bf162(w[1])}; }
-    __device__ __forceinline__ void to(uint32_t* w) const { w[0] = as_word(mul), w[1] = as_word(off); }
     // One of the two scales for both numbers (an operand's half: no instruction).
     __device__ __forceinline__ Scale half(int e) const {
         return e ? Scale{__high2bfloat162(mul), __high2bfloat162(off)} : Scale{__low2bfloat162(mul), __low2bfloat162(off)};
