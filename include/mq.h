@@ -534,7 +534,10 @@ int mq_kv4_read(const mq_kv4* src, const int32_t* len, const mq_kv* dst, cudaStr
  * out overlaps neither q nor the pages. ws: at least mq_attn_kv4_ws_bytes(B, T, Hq, Hkv, D, width * page_rows) bytes, 16-byte
  * aligned, nothing kept in it between calls; calls that run at the same time need one each. Where many query rows share a key head
  * (dim 64 and 128) it holds rows in 16 bits: up to 1 GB, or one sequence's width * page_rows rows where that is more, and the call takes the
- * batch in parts; otherwise a call is two launches. Counts as mq_attn_prefix's. B == 0 or T == 0 is a no-op.
+ * batch in parts; otherwise a call is two launches. Lengths being on the device, what is chosen and the workspace go by width * page_rows:
+ * a table much wider than its sequences (640 rows in one for 131072) makes a call of many rows read into 16 bits, and a single sequence's
+ * tiles share blocks, where a narrower one would not. Who knows a bound of the lengths gives it as a smaller width, with the same
+ * table and table_stride. Counts as mq_attn_prefix's. B == 0 or T == 0 is a no-op.
  * Waits are bounded (mq_device_status).
  */
 size_t mq_attn_kv4_ws_bytes(int B, int T, int Hq, int Hkv, int D, int cap);

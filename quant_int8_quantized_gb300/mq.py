@@ -621,7 +621,8 @@ def _here(where: str, *tensors):
 
 class KV4:
     """Keys and values of n sequences in 4 bits (include/mq.h, mq_kv4): pages uint8 [n_pages, page bytes] (a page's bytes
-    contiguous, at least mq_kv4_page_bytes), table int32 [n, width] (a row's entries contiguous), on the same device."""
+    contiguous, at least mq_kv4_page_bytes), table int32 [n, width] (a row's entries contiguous), on the same device. mq_attn_kv4
+    chooses its way and workspace by the width: table[:, :w] where no sequence is longer than w pages."""
 
     def __init__(self, pages: torch.Tensor, table: torch.Tensor, page_rows: int, heads: int, dim: int):
         for t, dtype, name in ((pages, torch.uint8, "pages"), (table, torch.int32, "table")):
@@ -664,7 +665,8 @@ def rope_freq_scaled(n_pairs: int, base: float = 10000.0, factor: float = 1.0, t
                      slow: float = 1.0, device="cuda"):
     """(inv_freq, rot_scale) for contexts `factor` times the trained length: pairs that turn more than `fast` times over it keep
     their frequency, those that turn less than `slow` times have it divided by factor, those between are blended by their number
-    of turns; rot_scale is 1 + log(factor) / 10."""
+    of turns; rot_scale is 1 + log(factor) / 10. Many released models blend by the pair's index between those two bounds instead, and have
+    other frequencies there: give mq_qk_norm_rope_kv4 an inv_freq made as the model's own configuration says."""
     i = torch.arange(n_pairs, dtype=torch.float64)
     freq, scale = float(base) ** (-i / n_pairs), 1.0
     if factor > 1.0:

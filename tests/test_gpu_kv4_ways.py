@@ -156,3 +156,28 @@ def test_how_light_a_weight_may_be(heavy, T, dtype, read):
     p = 1.0 / (n + 2.0 ** -28)                         # of a heavy key
     floor = 2.0 ** -25 if abs(heavy) >= 2 ** 20 else 2.0 ** -32
     assert abs(got - 2.0 ** -28 * p * v) <= v * p * (max(2.0 ** -11 * 2.0 ** -28, floor) + 2.0 ** -28 * 2.0 ** -16)
+
+
+@pytest.mark.parametrize("T", [1, 64])
+def test_a_wide_table_and_its_first_columns(T):
+    """640 rows in a table for 131072: right as it is, and the same bits and workspace as a table for 640 where only its first columns are
+    given."""
+    n, Hq, Hkv, D, rows, width = 2, 40, 8, 128, 64, 2048
+    cache = R.random_cache(n, 10, rows, Hkv, D, 61)
+    wide = torch.full((n, width), -1, dtype=torch.int32, device="cuda")
+    wide[:, :10] = cache.table
+    lens = [640, 577]
+    length = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    q = _rand((n, T, Hq, D), 62, 1.0, F16)
+    out = []
+    for table in (cache.table, wide[:, :10], wide):
+        c = mq.KV4(cache.pages, table, rows, Hkv, D)
+        out.append(torch.full((n, T, Hq, D), float("nan"), device="cuda"))
+        mq.mq_attn_kv4(q, c, length, out[-1], ws=mq.attn_kv4_workspace(n, T, Hq, Hkv, D, c.cap))
+    assert torch.equal(out[0], out[1])
+    assert mq.mq_attn_kv4_ws_bytes(n, T, Hq, Hkv, D, 640) < mq.mq_attn_kv4_ws_bytes(n, T, Hq, Hkv, D, width * rows)
+    k, v = R.gather(cache.pages, cache.table, rows, Hkv, D, lens)
+    some = sorted({0, T - 1})
+    want, bound = A.attention(q, None, None, k, v, lens, D ** -0.5, F32, only=some)
+    for o in out:
+        _inside(o[:, some], want[0][:, some], bound[0][:, some] + 2.0 ** -32 * v.abs().sum(), "out")
