@@ -397,7 +397,8 @@ typedef struct mq_qkv {
  * [0, n * cap) is skipped (padding tokens). Two tokens must not have the same slot. The
  * cache's type, heads and dim say what is written; its k and v may be NULL where the input's
  * are. MQ_ERR_SHAPE: M < 0, n_pairs outside 0 .. D/2, n_axes outside 1 .. 8 (with pairs), strides
- * below the row's width or not a multiple of 4, M > n * cap with slot NULL, q_out over q, k or v. M == 0 is a no-op.
+ * below the row's width, not a multiple of 4 or (M > 1) above 2^40, M > n * cap with slot NULL, q_out over q, k or v. M == 0 is a
+ * no-op.
  * A programmatic dependent launch, as the producers; wq and wk are read through the read-only path.
  */
 int mq_qk_norm_rope(const mq_qkv* x, void* q_out, const mq_kv* cache, const int32_t* slot, cudaStream_t stream);

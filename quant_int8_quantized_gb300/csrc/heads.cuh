@@ -52,10 +52,14 @@ inline long long kv_span(const mq_kv* c) {
     return c->seq_stride * (c->n - 1) + c->row_stride * (c->cap - 1) + c->head_stride * (c->heads - 1) + c->dim;
 }
 
-// Whether `rows` rows of `width` bytes, `stride` bytes apart (at least width) from a on, and the `bytes` from b on have a
-// byte in common.
+// Elements from token to token at most, where there are several: bytes of it still fit 64 bits.
+constexpr long long kTokenStrideMost = 1LL << 40;
+
+// Whether `rows` rows of `width` bytes, `stride` bytes apart (at least width; of one row: anything) from a on, and the `bytes` from b
+// on have a byte in common.
 inline bool rows_meet(const void* a, long long rows, long long stride, long long width, const void* b, long long bytes) {
     if (!a || !b || rows <= 0 || width <= 0 || bytes <= 0) return false;
+    if (rows == 1) stride = width;
     const long long at = (long long)(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a));
     const long long first = at < width ? 0 : (at - width) / stride + 1;   // row that ends behind b
     return first < rows && first * stride < at + bytes;

@@ -537,7 +537,7 @@ extern "C" int mq_qk_norm_rope_kv4(const mq_qkv* x, int type, float rot_scale, v
     if ((long long)heads[0] + heads[1] + heads[2] > 0x7fffff) return MQ_ERR_SHAPE;
     for (int i = 0; i < 3; ++i)
         if (src[i]) {
-            if (st[i] < (long long)heads[i] * D || st[i] % 4 != 0) return MQ_ERR_SHAPE;
+            if (st[i] < (long long)heads[i] * D || st[i] % 4 != 0 || (x->M > 1 && st[i] > mq::kTokenStrideMost)) return MQ_ERR_SHAPE;
             if (!mq::aligned16(src[i])) return MQ_ERR_ALIGN;
         }
     if (x->n_pairs > 0 && (!x->inv_freq || !x->pos)) return MQ_ERR_NULL;

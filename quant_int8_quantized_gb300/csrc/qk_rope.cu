@@ -207,7 +207,7 @@ extern "C" int mq_qk_norm_rope(const mq_qkv* x, void* q_out, const mq_kv* cache,
     const int heads[3] = {x->q ? x->Hq : 0, x->k ? Hkv : 0, x->v ? Hkv : 0};
     for (int i = 0; i < 3; ++i)
         if (src[i]) {
-            if (st[i] < (long long)heads[i] * D || st[i] % 4 != 0) return MQ_ERR_SHAPE;
+            if (st[i] < (long long)heads[i] * D || st[i] % 4 != 0 || (x->M > 1 && st[i] > mq::kTokenStrideMost)) return MQ_ERR_SHAPE;
             if (!mq::aligned16(src[i])) return MQ_ERR_ALIGN;
         }
     if (x->n_pairs > 0 && (!x->inv_freq || !x->pos)) return MQ_ERR_NULL;
