@@ -532,7 +532,7 @@ int mq_kv4_read(const mq_kv4* src, const int32_t* len, const mq_kv* dst, cudaStr
  * the values, whatever the type: by at most 2^-11 of themselves, or 2^-32 of their row's largest where that is more (2^-25 where the
  * row's largest product scale * q . k_j / ln 2 is 2^20 or more in magnitude: products of that size are themselves off by 2^-4 and
  * more). Deterministic.
- * out overlaps neither q nor the pages. ws: at least mq_attn_kv4_ws_bytes(B, T, Hq, Hkv, D, width * page_rows) bytes, 16-byte
+ * out overlaps neither q nor the pages (MQ_ERR_SHAPE); out, lse and ws overlap neither one another nor anything else that is read. ws: at least mq_attn_kv4_ws_bytes(B, T, Hq, Hkv, D, width * page_rows) bytes, 16-byte
  * aligned, nothing kept in it between calls; calls that run at the same time need one each. Where many query rows share a key head
  * (dim 64 and 128) it holds rows in 16 bits: up to 1 GB, or one sequence's width * page_rows rows where that is more, and the call takes the
  * batch in parts; otherwise a call is two launches. Lengths being on the device, what is chosen and the workspace go by width * page_rows:
